@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the computation runs in the library's CUDA
 kernels.  Tensors are torch CUDA tensors (used for device memory and streams); the
 C entry points receive their raw pointers.  The binding has the C ABI's names:
-``kv_quant_cache``, ``fp8_decode_attn``, ``fp8_prefill_attn`` and the size queries.
+``kv_quant_cache``, ``fp8_decode_attn``, ``fp8_prefill_attn`` and the size queries; the rotary
+cache writes ``kv_rope_cache`` and ``kv_block_cache``; ``fp8_block_decode_attn`` and
+``fp8_block_prefill_attn`` over block-scaled pools.
 
 The library must have been built (``python -m fp8_kv_cache_quant_gb300.build`` or
 ``__graft_entry__.build()``); importing the binding does not load it, calling an
@@ -26,13 +28,15 @@ OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR = 0, 1, 2, 3
 SCALE_PER_TENSOR, SCALE_PER_HEAD = 0, 1
 KV_E4M3, KV_E5M2 = 0, 1
 FAULT_BLOCK_ID, FAULT_SLOT, FAULT_CONTEXT, FAULT_TIMEOUT, FAULT_QLEN, FAULT_WORKSPACE = 1, 2, 4, 8, 16, 32
+FAULT_POSITION = 64
 
 # Entry points declared by include/fp8kv.h (checked by the tests).
 EXPORTS = (
     "fkv_status_string", "fkv_version", "kv_quant_cache", "fp8_decode_attn_workspace_size",
     "fp8_decode_attn_num_splits", "fp8_decode_attn", "fkv_prefill_block_n", "fp8_prefill_attn",
     "fp8_decode_attn_noalloc", "fp8_decode_attn_split_blocks", "fkv_decode_block_n", "kv_quant_cache_clips",
-    "fp8_decode_step", "fkv_set_decode_wait_limit_ns",
+    "fp8_decode_step", "fkv_set_decode_wait_limit_ns", "kv_rope_cache", "kv_block_cache",
+    "fp8_block_decode_attn", "fp8_block_prefill_attn",
 )
 NOALLOC_WORKSPACE_BYTES = 16 << 20
 
@@ -47,6 +51,17 @@ class _LayerCache(ctypes.Structure):
     _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("num_blocks", ctypes.c_int32),
                 ("block_size", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
                 ("kv_format", ctypes.c_int32)]
+
+
+class _BlockCache(ctypes.Structure):
+    _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Rope(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("max_positions", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32)]
 
 
 _lib = None
@@ -96,6 +111,19 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.fp8_prefill_attn.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, _LayerCache, c_vp, c_i32, c_vp, c_vp, c_vp,
                                      c_vp, ctypes.c_int, c_f, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
                                      c_vp]
+    c_i64 = ctypes.c_int64
+    lib.kv_rope_cache.restype = ctypes.c_int
+    lib.kv_rope_cache.argtypes = [c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i32, _Rope,
+                                  _LayerCache, c_vp, c_vp, ctypes.c_int, c_i32, c_vp, c_i32, c_vp, c_vp]
+    lib.kv_block_cache.restype = ctypes.c_int
+    lib.kv_block_cache.argtypes = [c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_i32,
+                                   _Rope, _BlockCache, c_vp, c_i32, c_vp, c_vp, c_vp]
+    lib.fp8_block_decode_attn.restype = ctypes.c_int
+    lib.fp8_block_decode_attn.argtypes = [c_vp, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f, c_i32, c_vp, c_vp,
+                                          c_sz, c_i32, c_vp, c_vp]
+    lib.fp8_block_prefill_attn.restype = ctypes.c_int
+    lib.fp8_block_prefill_attn.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f,
+                                           c_i32, c_i32, c_vp, c_vp, c_vp]
     if path is None:
         _lib = lib
     return lib
@@ -305,4 +333,214 @@ def fp8_prefill_attn(q, cu_seqlens_q, max_q_len, cache: LayerCache, block_table,
                               int(promote_every), int(layer), mp, nl, _ptr(out), _ptr(fault), _stream(stream))
     del keep
     _check("fp8_prefill_attn", st)
+    return out
+
+
+# ------------------------------------------------------------------ rotary cache writes, block-scaled cache
+
+@dataclasses.dataclass
+class Rope:
+    """A rotary position embedding: ``cos_sin`` float32 [max_positions][rot_dim], row p holding
+    rot_dim / 2 cosines, then rot_dim / 2 sines; ``interleaved`` pairs neighbours (2 i, 2 i + 1)
+    instead of the halves (i, i + rot_dim / 2)."""
+
+    cos_sin: torch.Tensor
+    interleaved: bool = False
+
+    def c(self) -> _Rope:
+        t = self.cos_sin
+        return _Rope(t.data_ptr(), t.shape[0], t.shape[1], int(self.interleaved))
+
+    @staticmethod
+    def table(max_positions, rot_dim, base=10000.0, device="cuda"):
+        """The table of angles p * base^(-2 i / rot_dim), evaluated in float64."""
+        inv = float(base) ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+        a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * inv
+        return torch.cat((a.cos(), a.sin()), 1).float()
+
+
+@dataclasses.dataclass
+class BlockCache:
+    """One layer's block-scaled pools: e4m3 codes (uint8) [num_blocks][Hkv][16][D] and the
+    float32 scales [num_blocks][Hkv] of every block and KV head, for K and for V."""
+
+    k_cache: torch.Tensor
+    v_cache: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def c(self) -> _BlockCache:
+        n, h, bs, d = self.k_cache.shape
+        return _BlockCache(self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.k_scale.data_ptr(),
+                           self.v_scale.data_ptr(), n, bs, h, d)
+
+    @staticmethod
+    def empty(num_blocks, num_kv_heads, head_dim, device="cuda", block_size=16):
+        shape = (num_blocks, num_kv_heads, block_size, head_dim)
+        return BlockCache(*(torch.empty(shape, dtype=torch.uint8, device=device) for _ in range(2)),
+                          *(torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
+
+
+def _need(ok, fn, what):
+    if not ok:
+        raise ValueError(f"{fn}: {what}")
+
+
+def _tensors(fn, device, **named):
+    """Each named (tensor, dtype, shape): on `device`, of that type and shape, contiguous.  A shape entry
+    None accepts any length; a tensor None is left out."""
+    for name, (t, dtype, shape) in named.items():
+        if t is None:
+            continue
+        _need(t.device == device, fn, f"{name} is on {t.device}, not {device}")
+        _need(t.dtype is dtype, fn, f"{name} is {t.dtype}, not {dtype}")
+        _need(t.dim() == len(shape) and all(w is None or w == n for n, w in zip(t.shape, shape)), fn,
+              f"{name} has shape {tuple(t.shape)}, not {shape}")
+        _need(t.is_contiguous(), fn, f"{name} is not contiguous")
+
+
+def _rows(fn, device, name, t, n, heads, d):
+    """The token stride of a bf16 tensor [n][heads][d] whose rows are consecutive (a slice of a wider
+    projection's output serves)."""
+    _need(t.device == device, fn, f"{name} is on {t.device}, not {device}")
+    _need(t.dtype is torch.bfloat16, fn, f"{name} is {t.dtype}, not torch.bfloat16")
+    _need(t.dim() == 3 and t.shape == (n, heads, d), fn, f"{name} has shape {tuple(t.shape)}, not {(n, heads, d)}")
+    if n == 0:
+        return heads * d
+    s = t.stride()
+    _need(s[2] == 1 and (heads == 1 or s[1] == d), fn, f"{name}'s rows of {heads} x {d} elements are not consecutive")
+    return s[0] if n > 1 else max(s[0], heads * d) // 8 * 8
+
+
+def _launch(fn, device, stream, *args):
+    """lib.fn(*args, stream) with the tensors' device current; stream None: that device's current stream."""
+    f = getattr(load_library(), fn)
+    if device.index == torch.cuda.current_device():
+        _check(fn, f(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn, f(*args, _stream(stream)))
+
+
+def _cuda(fn, t):
+    _need(t.is_cuda, fn, "the tensors are not on a CUDA device")
+    return t.device
+
+
+def _query_rows(fn, device, q, q_out, n, d):
+    """(q pointer, stride, q_out pointer, stride, heads, q_out) of an optional query tensor [n][Hq][d]."""
+    if q is None:
+        _need(q_out is None, fn, "q_out without q")
+        return None, 0, None, 0, 0, None
+    _need(q.dim() == 3, fn, f"q has shape {tuple(q.shape)}")
+    hq = q.shape[1]
+    if q_out is None:
+        q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=device)
+    return (q.data_ptr(), _rows(fn, device, "q", q, n, hq, d), q_out.data_ptr(),
+            _rows(fn, device, "q_out", q_out, n, hq, d), hq, q_out)
+
+
+def _check_rope(fn, device, rope):
+    _tensors(fn, device, cos_sin=(rope.cos_sin, torch.float32, (None, None)))
+    return rope.c()
+
+
+def kv_rope_cache(q, k, v, positions, slot_mapping, rope: Rope, cache: LayerCache, k_scale=None, v_scale=None,
+                  gran=SCALE_PER_TENSOR, layer=0, skip_layer_mask=None, q_out=None, fault=None, stream=None):
+    """kv_quant_cache of K turned for its positions and of V, and the turned queries (bf16, returned; rows of
+    skipped tokens are not written).  q, k, v: bf16 [n][heads][D], rows may be slices of a wider tensor; q may
+    be None, q_out may be q.  positions, slot_mapping: int64 [n]."""
+    fn = "kv_rope_cache"
+    device = _cuda(fn, k)
+    _need(k.dim() == 3, fn, f"k has shape {tuple(k.shape)}")
+    n, h, d = k.shape
+    ks, vs = _rows(fn, device, "k", k, n, h, d), _rows(fn, device, "v", v, n, h, d)
+    qa = _query_rows(fn, device, q, q_out, n, d)
+    mp, nl, keep = _mask_arg(skip_layer_mask)
+    skipped = keep is not None and 0 <= layer < nl and bool(keep[layer])
+    scales = (h,) if gran == SCALE_PER_HEAD else (1,)
+    pool = (cache.k_cache.shape[0], h, None, d)
+    _tensors(fn, device, positions=(positions, torch.int64, (n,)), slot_mapping=(slot_mapping, torch.int64, (n,)),
+             k_cache=(cache.k_cache, torch.bfloat16 if skipped else torch.uint8, pool),
+             v_cache=(cache.v_cache, torch.bfloat16 if skipped else torch.uint8, tuple(cache.k_cache.shape)),
+             k_scale=(k_scale, torch.float32, scales), v_scale=(v_scale, torch.float32, scales),
+             fault=(fault, torch.int32, (1,)))
+    _launch(fn, device, stream, qa[0], qa[1], qa[2], qa[3], qa[4], k.data_ptr(), ks, v.data_ptr(), vs,
+            positions.data_ptr(), slot_mapping.data_ptr(), n, _check_rope(fn, device, rope), cache.c(), _ptr(k_scale),
+            _ptr(v_scale), int(gran), int(layer), mp, nl, _ptr(fault))
+    del keep
+    return qa[5]
+
+
+def _check_block_cache(fn, device, cache, h, d):
+    nb = cache.k_cache.shape[0]
+    pool = (nb, h, None, d)
+    _tensors(fn, device, k_cache=(cache.k_cache, torch.uint8, pool), v_cache=(cache.v_cache, torch.uint8,
+             tuple(cache.k_cache.shape)), k_scale=(cache.k_scale, torch.float32, (nb, h)),
+             v_scale=(cache.v_scale, torch.float32, (nb, h)))
+    return cache.c()
+
+
+def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, context_lens, rope: Optional[Rope] = None,
+                   q=None, q_out=None, fault=None, stream=None):
+    """Append each sequence's new tokens (rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k, v and q, the last of
+    its context_lens[b] tokens) to a block-scaled cache, K and q turned for their positions when ``rope`` is
+    given; returns the turned queries (None without q)."""
+    fn = "kv_block_cache"
+    device = _cuda(fn, k)
+    _need(k.dim() == 3, fn, f"k has shape {tuple(k.shape)}")
+    n, h, d = k.shape
+    ks, vs = _rows(fn, device, "k", k, n, h, d), _rows(fn, device, "v", v, n, h, d)
+    qa = _query_rows(fn, device, q, q_out, n, d)
+    b = block_table.shape[0]
+    _tensors(fn, device, cu_seqlens=(cu_seqlens, torch.int32, (b + 1,)), block_table=(block_table, torch.int32, (b, None)),
+             context_lens=(context_lens, torch.int32, (b,)), fault=(fault, torch.int32, (1,)))
+    c = _check_block_cache(fn, device, cache, h, d)
+    r = _check_rope(fn, device, rope) if rope is not None else _Rope()
+    _launch(fn, device, stream, qa[0], qa[1], qa[2], qa[3], qa[4], k.data_ptr(), ks, v.data_ptr(), vs, n,
+            cu_seqlens.data_ptr(), b, int(max_q_len), r, c, block_table.data_ptr(), block_table.shape[1],
+            context_lens.data_ptr(), _ptr(fault))
+    return qa[5]
+
+
+def _attn_args(fn, q, rows, cache, block_table, context_lens, out, fault):
+    device = _cuda(fn, q)
+    _need(q.dim() == 3 and cache.k_cache.dim() == 4, fn, f"q has shape {tuple(q.shape)}, the pools {tuple(cache.k_cache.shape)}")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    b = block_table.shape[0]
+    _tensors(fn, device, q=(q, torch.bfloat16, (rows, None, cache.k_cache.shape[3])), out=(out, torch.bfloat16, tuple(q.shape)),
+             block_table=(block_table, torch.int32, (b, None)), context_lens=(context_lens, torch.int32, (b,)),
+             fault=(fault, torch.int32, (1,)))
+    return device, out, _check_block_cache(fn, device, cache, cache.k_cache.shape[1], q.shape[2])
+
+
+def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softmax_scale=0.0, window=0, out=None,
+                          workspace=None, num_splits=0, fault=None, stream=None):
+    """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.  The
+    workspace is fp8_decode_attn's (``decode_workspace`` makes one; zero-filled before its first call)."""
+    fn = "fp8_block_decode_attn"
+    b, mb = block_table.shape
+    device, out, c = _attn_args(fn, q, b, cache, block_table, context_lens, out, fault)
+    hq = q.shape[1]
+    if workspace is None:
+        n = fp8_decode_attn_workspace_size(b, hq, c.num_kv_heads, c.head_dim, mb, window, num_splits)
+        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    _need(workspace.device == device and workspace.is_contiguous(), fn, "workspace on another device or not contiguous")
+    _launch(fn, device, stream, q.data_ptr(), b, hq, c, block_table.data_ptr(), mb, context_lens.data_ptr(),
+            float(softmax_scale), int(window), out.data_ptr(), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), int(num_splits), _ptr(fault))
+    return out
+
+
+def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_table, context_lens, softmax_scale=0.0,
+                           causal=True, window=0, out=None, fault=None, stream=None):
+    """Ragged chunks of queries (rows cu_seqlens_q[b] .. of q bf16 [total][Hq][D]) over a block-scaled cache."""
+    fn = "fp8_block_prefill_attn"
+    b, mb = block_table.shape
+    device, out, c = _attn_args(fn, q, None, cache, block_table, context_lens, out, fault)
+    _tensors(fn, device, cu_seqlens_q=(cu_seqlens_q, torch.int32, (b + 1,)))
+    _launch(fn, device, stream, q.data_ptr(), cu_seqlens_q.data_ptr(), q.shape[0], b, q.shape[1], int(max_q_len), c,
+            block_table.data_ptr(), mb, context_lens.data_ptr(), float(softmax_scale), int(bool(causal)), int(window),
+            out.data_ptr(), _ptr(fault))
     return out

@@ -132,6 +132,36 @@ fkv_status cache_write(const void* k, const void* v, const int64_t* slot_mapping
                                               reinterpret_cast<cudaStream_t>(stream), current_num_sms(), clips));
 }
 
+// ---- the rotary cache writes and the block-scaled cache
+
+// A rotation of heads of head_dim elements.
+fkv_status check_rope(const fkv_rope& r, int32_t head_dim) {
+  if (!r.cos_sin || !aligned(r.cos_sin, 16) || r.max_positions <= 0 || r.rot_dim <= 0) return FKV_INVALID_ARG;
+  if (r.rot_dim > head_dim) return FKV_INVALID_ARG;
+  return r.rot_dim % 16 == 0 ? FKV_OK : FKV_UNSUPPORTED;
+}
+
+// Rows of `row` consecutive bf16 elements at `stride` elements.
+bool valid_rows(const void* p, int64_t stride, int64_t row) {
+  return p != nullptr && aligned(p, 16) && stride >= row && stride % 8 == 0;
+}
+
+fkv_status check_block_cache(const fkv_block_cache& c) {
+  if (c.block_size != 16) return c.block_size > 0 ? FKV_UNSUPPORTED : FKV_INVALID_ARG;
+  if (c.num_blocks <= 0 || c.num_kv_heads <= 0) return FKV_INVALID_ARG;
+  return supported_head_dim(c.head_dim) ? FKV_OK : FKV_UNSUPPORTED;
+}
+
+bool valid_block_pools(const fkv_block_cache& c) {
+  return c.k_cache && c.v_cache && c.k_scale && c.v_scale && aligned(c.k_cache, 16) && aligned(c.v_cache, 16) &&
+         aligned(c.k_scale, 4) && aligned(c.v_scale, 4);
+}
+
+float base2_scale(float softmax_scale, int32_t head_dim) {
+  const float tau = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
+  return tau * 1.4426950408889634f;
+}
+
 }  // namespace
 
 namespace fkv {
@@ -236,7 +266,7 @@ const char* fkv_status_string(fkv_status status) {
   return "unknown status";
 }
 
-int32_t fkv_version(void) { return 105; }
+int32_t fkv_version(void) { return 106; }
 
 void fkv_set_decode_wait_limit_ns(unsigned long long ns) { g_decode_wait_ns.store(ns, std::memory_order_relaxed); }
 
@@ -371,6 +401,207 @@ fkv_status fp8_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t 
   p.fault = fault;
   return from_cuda(fkv::launch_prefill(p, cache.head_dim, bf16, cache.k_cache, cache.v_cache,
                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* positions,
+                         const int64_t* slot_mapping, int32_t n_tokens, fkv_rope rope, fkv_layer_cache cache,
+                         const float* k_scale, const float* v_scale, fkv_scale_gran gran, int32_t layer,
+                         const uint8_t* skip_layer_mask, int32_t num_layers, int32_t* fault, fkv_stream_t stream) {
+  if (n_tokens < 0 || num_q_heads < 0) return FKV_INVALID_ARG;
+  if (cache.block_size != 16) return cache.block_size > 0 ? FKV_UNSUPPORTED : FKV_INVALID_ARG;
+  if (cache.num_blocks <= 0 || cache.num_kv_heads <= 0 || !valid_format(cache)) return FKV_INVALID_ARG;
+  if (!supported_head_dim(cache.head_dim)) return FKV_UNSUPPORTED;
+  if (num_q_heads > 65535 || cache.num_kv_heads > 65535) return FKV_UNSUPPORTED;
+  if (gran != FKV_SCALE_PER_TENSOR && gran != FKV_SCALE_PER_HEAD) return FKV_INVALID_ARG;
+  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
+  fkv_status st = FKV_OK;
+  const bool bf16 = layer_is_bf16(layer, skip_layer_mask, num_layers, &st);
+  if (st != FKV_OK) return st;
+  st = check_rope(rope, cache.head_dim);
+  if (st != FKV_OK) return st;
+  if (n_tokens == 0) return FKV_OK;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
+  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
+  if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
+  if (q && (!valid_rows(q, q_stride, q_row) || !valid_rows(q_out, q_out_stride, q_row))) return FKV_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return FKV_INVALID_ARG;
+  if (!positions || !slot_mapping || !aligned(positions, 8) || !aligned(slot_mapping, 8)) return FKV_INVALID_ARG;
+  if (!cache.k_cache || !cache.v_cache || !aligned(cache.k_cache, 16) || !aligned(cache.v_cache, 16))
+    return FKV_INVALID_ARG;
+  if (!bf16 && (!k_scale || !v_scale)) return FKV_INVALID_ARG;
+  fkv::RopeCacheParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_out_stride = q_out_stride;
+  p.cos_sin = rope.cos_sin;
+  p.max_pos = rope.max_positions;
+  p.rot = rope.rot_dim;
+  p.interleaved = rope.interleaved != 0;
+  p.positions = positions;
+  p.slots = slot_mapping;
+  p.n_tokens = n_tokens;
+  p.Hq = num_q_heads;
+  p.H = cache.num_kv_heads;
+  p.D = cache.head_dim;
+  p.kc = static_cast<uint8_t*>(cache.k_cache);
+  p.vc = static_cast<uint8_t*>(cache.v_cache);
+  p.capacity = static_cast<long long>(cache.num_blocks) * 16;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.per_head = gran == FKV_SCALE_PER_HEAD;
+  p.fault = fault;
+  const int pool = bf16 ? 2 : cache.kv_format == FKV_KV_E5M2 ? 1 : 0;
+  return from_cuda(fkv::launch_rope_cache(p, pool, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t n_tokens,
+                          const int32_t* cu_seqlens, int32_t batch, int32_t max_q_len, fkv_rope rope,
+                          fkv_block_cache cache, const int32_t* block_table, int32_t max_blocks,
+                          const int32_t* context_lens, int32_t* fault, fkv_stream_t stream) {
+  if (n_tokens < 0 || batch < 0 || max_q_len < 0 || max_blocks <= 0 || num_q_heads < 0) return FKV_INVALID_ARG;
+  fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (batch > 65535 || num_q_heads > 65535 || cache.num_kv_heads > 65535) return FKV_UNSUPPORTED;
+  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
+  const bool turned = rope.cos_sin != nullptr;
+  if (turned) {
+    st = check_rope(rope, cache.head_dim);
+    if (st != FKV_OK) return st;
+  } else if (q != nullptr || rope.rot_dim != 0) {
+    return FKV_INVALID_ARG;
+  }
+  if (n_tokens == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
+  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
+  if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
+  if (q && (!valid_rows(q, q_stride, q_row) || !valid_rows(q_out, q_out_stride, q_row))) return FKV_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return FKV_INVALID_ARG;
+  if (!valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!cu_seqlens || !block_table || !context_lens || !aligned(cu_seqlens, 4) || !aligned(block_table, 4) ||
+      !aligned(context_lens, 4))
+    return FKV_INVALID_ARG;
+  fkv::BlockCacheParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_out_stride = q_out_stride;
+  p.cos_sin = rope.cos_sin;
+  p.max_pos = rope.max_positions;
+  p.rot = turned ? rope.rot_dim : 0;
+  p.interleaved = rope.interleaved != 0;
+  p.cu = cu_seqlens;
+  p.ctx = context_lens;
+  p.block_table = block_table;
+  p.n_tokens = n_tokens;
+  p.B = batch;
+  p.max_q_len = max_q_len;
+  p.Hq = num_q_heads;
+  p.H = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.kc = static_cast<uint8_t*>(cache.k_cache);
+  p.vc = static_cast<uint8_t*>(cache.v_cache);
+  p.ks = cache.k_scale;
+  p.vs = cache.v_scale;
+  p.fault = fault;
+  return from_cuda(fkv::launch_block_cache(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
+                                 const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                 float softmax_scale, int32_t window, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t num_splits, int32_t* fault, fkv_stream_t stream) {
+  if (batch < 0 || num_q_heads <= 0 || max_blocks <= 0 || window < 0 || num_splits < 0) return FKV_INVALID_ARG;
+  const fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
+  const int G = num_q_heads / cache.num_kv_heads;
+  if (!supported_group(G, cache.head_dim)) return FKV_UNSUPPORTED;
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return FKV_INVALID_ARG;
+  if (batch > 65535 || num_q_heads > 65535) return FKV_UNSUPPORTED;
+  if (batch == 0) return FKV_OK;
+  if (!q || !out || !block_table || !context_lens || !valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4))
+    return FKV_INVALID_ARG;
+  DecodePlan plan;
+  if (!plan_decode(batch, num_q_heads, cache.num_kv_heads, cache.head_dim, max_blocks, window, num_splits, &plan))
+    return FKV_UNSUPPORTED;
+  const size_t need = plan.o_bytes + plan.lse_bytes + plan.cnt_bytes;
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FKV_INVALID_ARG;
+  fkv::BlockAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(cache.v_cache);
+  p.k_scale = cache.k_scale;
+  p.v_scale = cache.v_scale;
+  p.block_table = block_table;
+  p.ctx = context_lens;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.Hkv = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
+  p.window = window;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.fault = fault;
+  return from_cuda(fkv::launch_block_attn(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
+                                  int32_t num_q_heads, int32_t max_q_len, fkv_block_cache cache,
+                                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                  float softmax_scale, int32_t causal, int32_t window, void* out, int32_t* fault,
+                                  fkv_stream_t stream) {
+  if (total_q < 0 || batch < 0 || num_q_heads <= 0 || max_q_len < 0 || max_blocks <= 0) return FKV_INVALID_ARG;
+  const fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale) || window < 0) return FKV_INVALID_ARG;
+  if (window > 0 && !causal) return FKV_UNSUPPORTED;  // a window is causal
+  if (batch > 65535 || num_q_heads > 65535) return FKV_UNSUPPORTED;
+  if (total_q == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
+  if (!q || !cu_seqlens_q || !block_table || !context_lens || !out || !valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) ||
+      !aligned(cu_seqlens_q, 4))
+    return FKV_INVALID_ARG;
+  fkv::BlockAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(cache.v_cache);
+  p.k_scale = cache.k_scale;
+  p.v_scale = cache.v_scale;
+  p.block_table = block_table;
+  p.ctx = context_lens;
+  p.cu = cu_seqlens_q;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.Hkv = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.max_q_len = max_q_len;
+  p.total_q = total_q;
+  p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
+  p.causal = causal != 0;
+  p.window = window;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.fault = fault;
+  return from_cuda(fkv::launch_block_attn(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/fp8kv.h"
@@ -58,6 +59,62 @@ struct PrefillParams {
   __nv_bfloat16* out;           // [total_q][Hq][D]
   int32_t* fault;
 };
+
+struct RopeCacheParams {
+  const __nv_bfloat16 *q, *k, *v;             // token rows at the strides (in elements)
+  long long q_stride, k_stride, v_stride;
+  __nv_bfloat16* q_out;
+  long long q_out_stride;
+  const float* cos_sin;                       // [max_pos][rot]
+  int max_pos, rot;
+  int interleaved;
+  const int64_t* positions;                   // [n_tokens]
+  const int64_t* slots;                       // [n_tokens]
+  int n_tokens, Hq, H, D;                     // Hq 0: no queries
+  uint8_t *kc, *vc;
+  long long capacity;                         // slots of the pool
+  const float *ks, *vs;
+  int per_head;
+  int32_t* fault;
+};
+
+// pool: 0 e4m3, 1 e5m2, 2 bf16
+cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, cudaStream_t s);
+
+struct BlockCacheParams {
+  const __nv_bfloat16 *q, *k, *v;
+  long long q_stride, k_stride, v_stride;
+  __nv_bfloat16* q_out;
+  long long q_out_stride;
+  const float* cos_sin;                       // null: no rotation (rot 0)
+  int max_pos, rot;
+  int interleaved;
+  const int32_t* cu;                          // [B + 1]
+  const int32_t* ctx;                         // [B]
+  const int32_t* block_table;                 // [B][max_blocks]
+  int n_tokens, B, max_q_len, Hq, H, num_blocks, max_blocks;
+  uint8_t *kc, *vc;
+  float *ks, *vs;                             // [num_blocks][H]
+  int32_t* fault;
+};
+
+cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s);
+
+struct BlockAttnParams {
+  const __nv_bfloat16* q;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;             // [num_blocks][Hkv]
+  const int32_t* block_table;                 // [B][max_blocks]
+  const int32_t* ctx;                         // [B]
+  const int32_t* cu;                          // [B + 1]; null: decode (one row per sequence)
+  int B, Hq, Hkv, num_blocks, max_blocks, max_q_len, total_q;
+  float sm_scale_log2;                        // softmax_scale * log2(e)
+  int causal, window;
+  __nv_bfloat16* out;
+  int32_t* fault;
+};
+
+cudaError_t launch_block_attn(const BlockAttnParams& p, int D, cudaStream_t s);
 
 cudaError_t launch_prefill(const PrefillParams& p, int D, bool bf16_layer, void* k_cache, void* v_cache,
                            cudaStream_t s);

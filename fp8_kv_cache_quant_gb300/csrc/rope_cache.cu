@@ -1,0 +1,325 @@
+// The cache writes that apply the rotary position embedding on the way: kv_rope_cache
+// (slot-mapped, pools with per-tensor or per-head scales, or bf16) and kv_block_cache
+// (block-scaled e4m3 pools).
+//
+// A head's row is handled in units of 16 elements, two 16-byte chunks whose elements pair up
+// under the rotation, so that a pair's two halves meet in one thread: with the half split,
+// chunks u and u + rot_dim / 16 of the turned part; otherwise two neighbouring chunks.  In
+// both styles unit u of the turned part takes table entries 8 u .. 8 u + 7.
+// The products and the sum of a rotation are rounded one by one to float32 (no fused
+// multiply-add), as an elementwise evaluation rounds them, so that the codes are reproducible.
+#include "common.cuh"
+#include "kernels.h"
+
+namespace fkv {
+namespace {
+
+// The two chunks (indices of 8 elements) of unit u.
+FKV_DEV void unit_chunks(int u, int rot, bool interleaved, int& a, int& b) {
+  const int n = rot >> 4;  // turned units
+  if (!interleaved && u < n) {
+    a = u;
+    b = u + n;
+  } else {
+    a = 2 * u;
+    b = 2 * u + 1;
+  }
+}
+
+FKV_DEV void unpack8(const uint4 x, float (&f)[8]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = bf16x2_to_f2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+
+FKV_DEV uint4 pack8_bf16(const float (&f)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 y = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 8 values times inv, rounded to float32, as FP8 codes.
+template <bool kE5>
+FKV_DEV uint2 pack8_fp8(const float (&f)[8], float inv) {
+  uint32_t o[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float y0 = __fmul_rn(f[4 * k], inv), y1 = __fmul_rn(f[4 * k + 1], inv);
+    const float y2 = __fmul_rn(f[4 * k + 2], inv), y3 = __fmul_rn(f[4 * k + 3], inv);
+    const uint32_t lo = kE5 ? f32x2_to_e5m2x2(y0, y1) : f32x2_to_e4m3x2(y0, y1);
+    const uint32_t hi = kE5 ? f32x2_to_e5m2x2(y2, y3) : f32x2_to_e4m3x2(y2, y3);
+    o[k] = lo | (hi << 16);
+  }
+  return make_uint2(o[0], o[1]);
+}
+
+FKV_DEV void load8(const float* p, float (&f)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+FKV_DEV void turn(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+// Turn unit u (values a and b of its two chunks) by the table row at `cs`.
+FKV_DEV void turn_unit(float (&a)[8], float (&b)[8], const float* cs, int rot, int u, bool interleaved) {
+  float c[8], s[8];
+  load8(cs + 8 * u, c);
+  load8(cs + rot / 2 + 8 * u, s);
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn(a[2 * i], a[2 * i + 1], c[i], s[i]);
+      turn(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i], s[i]);
+  }
+}
+
+// ---------------------------------------------------------------- kv_rope_cache
+
+// Thread = one unit of one row (query heads, then K heads, then V heads) of one token; a CTA
+// holds whole tokens (tokens_per_cta, or one token in several rounds).
+// kPool: 0 e4m3, 1 e5m2, 2 bf16.
+template <int kPool>
+__global__ void __launch_bounds__(512) rope_cache_kernel(const RopeCacheParams p, int tokens_per_cta) {
+  const int U = p.D >> 4;
+  const int per_token = (p.Hq + 2 * p.H) * U;
+  for (int item = threadIdx.x; item < tokens_per_cta * per_token; item += blockDim.x) {
+    const int tl = item / per_token, rem = item - tl * per_token;
+    const long long t = static_cast<long long>(blockIdx.x) * tokens_per_cta + tl;
+    if (t >= p.n_tokens) return;
+    const int row = rem / U, u = rem - row * U;
+    const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.H;
+    const int h = is_q ? row : (is_v ? row - p.Hq - p.H : row - p.Hq);
+    const bool turned = !is_v && u < (p.rot >> 4);
+    int ca, cb;
+    unit_chunks(u, is_v ? 0 : p.rot, p.interleaved, ca, cb);
+    const __nv_bfloat16* src = (is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride) + h * p.D;
+    const uint4 xa = reinterpret_cast<const uint4*>(src)[ca], xb = reinterpret_cast<const uint4*>(src)[cb];
+    const long long slot = p.slots[t], pos = p.positions[t];
+    if (slot < 0) continue;
+    if (slot >= p.capacity) {
+      if (rem == 0) raise_fault(p.fault, FKV_FAULT_SLOT);
+      continue;
+    }
+    if (pos < 0 || pos >= p.max_pos) {
+      if (rem == 0) raise_fault(p.fault, FKV_FAULT_POSITION);
+      continue;
+    }
+    float a[8], b[8];
+    unpack8(xa, a);
+    unpack8(xb, b);
+    if (turned) turn_unit(a, b, p.cos_sin + pos * p.rot, p.rot, u, p.interleaved);
+    if (is_q) {
+      uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * p.D);
+      dst[ca] = pack8_bf16(a);
+      dst[cb] = pack8_bf16(b);
+    } else {
+      // chunk index of the row's first 8 elements in the pool
+      const long long at = ((((slot >> 4) * p.H + h) << 4) + (slot & 15)) * (p.D >> 3);
+      uint8_t* pool = is_v ? p.vc : p.kc;
+      if constexpr (kPool == 2) {
+        reinterpret_cast<uint4*>(pool)[at + ca] = pack8_bf16(a);
+        reinterpret_cast<uint4*>(pool)[at + cb] = pack8_bf16(b);
+      } else {
+        const float inv = __frcp_rn((is_v ? p.vs : p.ks)[p.per_head ? h : 0]);
+        reinterpret_cast<uint2*>(pool)[at + ca] = pack8_fp8<kPool == 1>(a, inv);
+        reinterpret_cast<uint2*>(pool)[at + cb] = pack8_fp8<kPool == 1>(b, inv);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- kv_block_cache
+
+constexpr int kBlockThreads = 256;
+constexpr int kQueryItems = 4 * kBlockThreads;  // units of the query rows per CTA
+
+// Four e4m3 codes times r, each product rounded to float32, as e4m3 codes.
+FKV_DEV uint32_t rescale4(uint32_t w, float r) {
+  uint32_t h01, h23;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"(static_cast<uint16_t>(w >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+  return static_cast<uint32_t>(f32x2_to_e4m3x2(__fmul_rn(a.x, r), __fmul_rn(a.y, r))) |
+         (static_cast<uint32_t>(f32x2_to_e4m3x2(__fmul_rn(b.x, r), __fmul_rn(b.y, r))) << 16);
+}
+
+// The smallest power of two s >= 2^-126 with amax <= 448 s, from amax's bits: 448 = 1.75 * 2^8.
+FKV_DEV float pow2_scale(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127;
+  const int k = e - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(max(k, -126) + 127) << 23);
+}
+
+// CTA z = 0: the K and V of one block (page blockIdx.x of sequence blockIdx.y's new tokens), a
+// warp per (KV head, K or V): its 16 rows stay in registers between the maximum and the
+// codes, so that each input byte is read once.  CTAs z >= 1: slices of the page's query rows.
+template <int D>
+__global__ void __launch_bounds__(kBlockThreads) block_cache_kernel(const BlockCacheParams p) {
+  constexpr int U = D / 16;       // units of a row
+  constexpr int TP = 32 / U;      // tokens of a page that a warp handles at once
+  constexpr int R = 16 / TP;      // rounds
+  const int b = blockIdx.y;
+  const int r0 = p.cu[b], L = p.cu[b + 1] - r0, T = p.ctx[b];
+  const bool first = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0;
+  if (L < 0 || L > p.max_q_len || r0 < 0 || r0 + static_cast<long long>(L) > p.n_tokens) {
+    if (first) raise_fault(p.fault, FKV_FAULT_QLEN);
+    return;
+  }
+  if (T < 0 || T > static_cast<long long>(p.max_blocks) * 16) {
+    if (first) raise_fault(p.fault, FKV_FAULT_CONTEXT);
+    return;
+  }
+  if (L > T) {
+    if (first) raise_fault(p.fault, FKV_FAULT_QLEN);
+    return;
+  }
+  if (p.cos_sin != nullptr && T > p.max_pos && L > 0) {
+    if (first) raise_fault(p.fault, FKV_FAULT_POSITION);
+    return;
+  }
+  const int page = ((T - L) >> 4) + blockIdx.x;
+  if (L == 0 || page > (T - 1) >> 4) return;
+  const int lo = max(T - L, page * 16), hi = min(T, page * 16 + 16);  // new positions in the page
+  const long long row0 = static_cast<long long>(r0) - (T - L);        // row of position x: row0 + x
+
+  if (blockIdx.z > 0) {
+    const int items = (hi - lo) * p.Hq * U;
+    const int i0 = (blockIdx.z - 1) * kQueryItems, i1 = min(items, i0 + kQueryItems);
+    for (int i = i0 + threadIdx.x; i < i1; i += kBlockThreads) {
+      const int u = i % U, h = (i / U) % p.Hq, pos = lo + i / (U * p.Hq);
+      int ca, cb;
+      unit_chunks(u, p.rot, p.interleaved, ca, cb);
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + (row0 + pos) * p.q_stride + h * D);
+      float a[8], c[8];
+      unpack8(src[ca], a);
+      unpack8(src[cb], c);
+      if (u < (p.rot >> 4)) turn_unit(a, c, p.cos_sin + static_cast<long long>(pos) * p.rot, p.rot, u, p.interleaved);
+      uint4* dst = reinterpret_cast<uint4*>(p.q_out + (row0 + pos) * p.q_out_stride + h * D);
+      dst[ca] = pack8_bf16(a);
+      dst[cb] = pack8_bf16(c);
+    }
+    return;
+  }
+
+  const int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + page];
+  if (id < 0 || id >= p.num_blocks) {
+    if (threadIdx.x == 0) raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+    return;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = lane % U;
+  for (int task = warp; task < 2 * p.H; task += kBlockThreads / 32) {
+    const int g = task >> 1;
+    const bool is_v = task & 1;
+    const int rot = is_v ? 0 : p.rot;
+    int ca, cb;
+    unit_chunks(u, rot, p.interleaved, ca, cb);
+    const __nv_bfloat16* src = is_v ? p.v : p.k;
+    const long long stride = is_v ? p.v_stride : p.k_stride;
+    uint4 xa[R], xb[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int pos = page * 16 + r * TP + lane / U;
+      xa[r] = xb[r] = make_uint4(0u, 0u, 0u, 0u);
+      if (pos >= lo && pos < hi) {
+        const uint4* s = reinterpret_cast<const uint4*>(src + (row0 + pos) * stride + g * D);
+        xa[r] = s[ca];
+        xb[r] = s[cb];
+      }
+    }
+    float a[R][8], c[R][8];
+    uint32_t amax = 0;  // bits of the largest finite magnitude (magnitudes order as their bits)
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int pos = page * 16 + r * TP + lane / U;
+      unpack8(xa[r], a[r]);
+      unpack8(xb[r], c[r]);
+      if (u < (rot >> 4) && pos >= lo && pos < hi)
+        turn_unit(a[r], c[r], p.cos_sin + static_cast<long long>(pos) * p.rot, p.rot, u, p.interleaved);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = __float_as_uint(a[r][i]) & 0x7FFFFFFFu, y = __float_as_uint(c[r][i]) & 0x7FFFFFFFu;
+        if (x < 0x7F800000u) amax = max(amax, x);
+        if (y < 0x7F800000u) amax = max(amax, y);
+      }
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    float* scale = (is_v ? p.vs : p.ks) + static_cast<size_t>(id) * p.H + g;
+    float s = pow2_scale(amax);
+    uint8_t* block = (is_v ? p.vc : p.kc) + (static_cast<size_t>(id) * p.H + g) * 16 * D;
+    const int kept = lo - page * 16;  // slots that already hold tokens
+    if (kept > 0) {
+      const float old = *scale;
+      const bool usable = old >= 1.17549435e-38f && old <= 3.402823466e+38f;  // a normal positive number
+      __syncwarp();  // every lane has read the old scale before lane 0 replaces it
+      if (usable && old >= s) {
+        s = old;
+      } else if (usable) {
+        const float r = __fdiv_rn(old, s);
+        for (int i = lane; i < kept * D / 16; i += 32) {
+          uint4* q4 = reinterpret_cast<uint4*>(block) + i;
+          uint4 w = *q4;
+          w.x = rescale4(w.x, r);
+          w.y = rescale4(w.y, r);
+          w.z = rescale4(w.z, r);
+          w.w = rescale4(w.w, r);
+          *q4 = w;
+        }
+      }
+    }
+    if (lane == 0) *scale = s;
+    const float inv = __frcp_rn(s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int slot = r * TP + lane / U;
+      const int pos = page * 16 + slot;
+      if (pos >= lo && pos < hi) {
+        uint2* dst = reinterpret_cast<uint2*>(block + slot * D);
+        dst[ca] = pack8_fp8<false>(a[r], inv);
+        dst[cb] = pack8_fp8<false>(c[r], inv);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, cudaStream_t s) {
+  const int per_token = (p.Hq + 2 * p.H) * (p.D >> 4);
+  const int tokens = per_token >= 256 ? 1 : 256 / per_token;  // whole tokens per CTA
+  const int threads = std::min(512, (tokens * per_token + 31) / 32 * 32);
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.n_tokens) + tokens - 1) / tokens);
+  auto kern = pool == 2 ? rope_cache_kernel<2> : pool == 1 ? rope_cache_kernel<1> : rope_cache_kernel<0>;
+  kern<<<blocks, threads, 0, s>>>(p, tokens);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s) {
+  // pages that max_q_len tokens can touch, wherever the first of them lies in its block
+  const unsigned pages = static_cast<unsigned>((static_cast<long long>(p.max_q_len) + 14) / 16 + 1);
+  const long long items = static_cast<long long>(std::min(16, p.max_q_len)) * p.Hq * (D / 16);
+  const dim3 grid(pages, p.B, static_cast<unsigned>(1 + (items + kQueryItems - 1) / kQueryItems));
+  auto kern = D == 64 ? block_cache_kernel<64> : D == 128 ? block_cache_kernel<128> : block_cache_kernel<256>;
+  kern<<<grid, kBlockThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace fkv

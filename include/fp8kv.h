@@ -32,6 +32,10 @@
  *             query scale num_q_heads values.
  *   GQA       query head h reads KV head h / (num_q_heads / num_kv_heads).
  *
+ *   block-scaled pools (fkv_block_cache)  e4m3 pools of the same layout in which every
+ *             (block, KV head) has its own float32 scale for K and one for V: no scale is
+ *             calibrated, the append (kv_block_cache) finds it from the block's tokens.
+ *
  * Launches.  The decode kernels are launched with programmatic stream serialisation: a
  * decode kernel may be scheduled while the kernel before it in the stream finishes, and
  * sets up its barriers and tensor memory then, but reads and writes no global memory
@@ -81,6 +85,7 @@ typedef enum {
 #define FKV_FAULT_QLEN 16    /* prefill: query length > context length: sequence skipped     */
 #define FKV_FAULT_WORKSPACE 32 /* decode: a split counter of the workspace was not zero when the
                                   call began (zero-fill a workspace before its first call)     */
+#define FKV_FAULT_POSITION 64 /* rotary position outside the table: token (kv_block_cache: sequence) skipped */
 
 /* FP8 format of a layer's pools (fkv_layer_cache.kv_format). */
 typedef enum {
@@ -101,6 +106,35 @@ typedef struct {
   int32_t head_dim;
   int32_t kv_format; /* fkv_kv_format */
 } fkv_layer_cache;
+
+/* One layer of a block-scaled paged cache.  k_cache / v_cache: device pools of e4m3 codes,
+ * 16-byte aligned, [num_blocks][num_kv_heads][block_size][head_dim] (block_size 16).
+ * k_scale / v_scale: device float32 [num_blocks][num_kv_heads], 4-byte aligned; the value of
+ * a code is code * scale.  Scales are finite and >= 0. */
+typedef struct {
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;
+  float* v_scale;
+  int32_t num_blocks;
+  int32_t block_size;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+} fkv_block_cache;
+
+/* A rotary position embedding.  cos_sin: device float32 [max_positions][rot_dim], 16-byte
+ * aligned; row p holds rot_dim / 2 cosines, then rot_dim / 2 sines, of position p's angles.
+ * The first rot_dim elements of a head are turned in pairs: interleaved == 0 pairs element i
+ * with i + rot_dim / 2, otherwise 2 i with 2 i + 1.  Pair i = (a, b) becomes
+ *   (fl(fl(a * cos_i) - fl(b * sin_i)), fl(fl(b * cos_i) + fl(a * sin_i))),  fl: float32,
+ * rounded once more to what stores it.  rot_dim: a multiple of 16, 16 <= rot_dim <= head_dim;
+ * the other elements keep their values. */
+typedef struct {
+  const float* cos_sin;
+  int32_t max_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+} fkv_rope;
 
 /* Human-readable name of a status code (static string). */
 const char* fkv_status_string(fkv_status status);
@@ -165,6 +199,73 @@ fkv_status kv_quant_cache_clips(const void* k, const void* v, const int64_t* slo
                                 const float* v_scale, fkv_scale_gran gran, int32_t layer,
                                 const uint8_t* skip_layer_mask, int32_t num_layers,
                                 unsigned long long* clip_counts, int32_t* fault, fkv_stream_t stream);
+
+/*
+ * kv_rope_cache — kv_quant_cache with the rotary position embedding applied on the way.
+ *
+ * Token t's K rows, turned for position positions[t] (see fkv_rope), and its V rows are
+ * written at slot_mapping[t] exactly as kv_quant_cache writes them (the turned K enters the
+ * quantisation in float32, without a rounding to bf16 in between; a bf16 pool rounds it
+ * once); its query rows are turned likewise and written to q_out as bf16.
+ *
+ *   q, k, v       device bf16, token t's row of num_q_heads (num_kv_heads) * head_dim
+ *                 consecutive elements at t * q_stride (k_stride, v_stride) elements:
+ *                 slices of one projection's output serve as they are.  Strides are
+ *                 multiples of 8 and no shorter than the row; pointers 16-byte aligned
+ *   q_out         device bf16, rows at t * q_out_stride; may be q itself with q's stride
+ *                 (otherwise the two must not overlap).  q NULL (num_q_heads 0): no queries
+ *   positions     device int64 [n_tokens]; outside [0, rope.max_positions) the token is
+ *                 skipped and FKV_FAULT_POSITION raised
+ *   slot_mapping  as for kv_quant_cache; a token with a negative slot is skipped whole
+ *                 (nothing of it is written, q_out neither), so is one beyond the pool.
+ *                 Two tokens of a call must not name the same slot
+ *   cache ... num_layers, fault  as for kv_quant_cache
+ */
+fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                         int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                         int64_t v_stride, const int64_t* positions, const int64_t* slot_mapping,
+                         int32_t n_tokens, fkv_rope rope, fkv_layer_cache cache, const float* k_scale,
+                         const float* v_scale, fkv_scale_gran gran, int32_t layer,
+                         const uint8_t* skip_layer_mask, int32_t num_layers, int32_t* fault,
+                         fkv_stream_t stream);
+
+/*
+ * kv_block_cache — append new tokens to a block-scaled cache, rotary embedding included.
+ *
+ * Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k, v (and q) are the last L_b tokens of
+ * sequence b's context_lens[b] = T_b, at positions T_b - L_b .. T_b - 1; position p lies in
+ * block block_table[b][p / 16], slot p % 16.  K (and q, to q_out) is turned for its position
+ * when rope.cos_sin is given.  For every block that receives tokens, every KV head, and K and
+ * V apart:
+ *   need = the smallest power of two s >= 2^-126 with amax <= 448 s, amax the largest finite
+ *          magnitude among the block's new tokens;
+ *   a block whose slot 0 is written takes scale s = need, whatever it held;
+ *   a block that already holds tokens of the sequence (its first new slot is j > 0) takes
+ *          s = max(old scale, need), and when that is larger than the old one, its codes c in
+ *          slots 0 .. j - 1 become e4m3(fl32(c * fl32(old / s))) — exact for powers of two,
+ *          save for what falls below the subnormal step.  (An old scale that is not a normal
+ *          positive number counts as 0: s = need, and the codes stay.)
+ *   new codes are e4m3(fl32(x * fl32(1 / s))), round-to-nearest-even, saturating (infinities
+ *          become +-448, NaN stays NaN).
+ * Slots behind T_b - 1, and every other block, keep their bytes and scales.  A block that a
+ * call appends to must belong to one sequence of the call.
+ *
+ *   q, q_out, k, v, strides  as for kv_rope_cache; q needs rope.cos_sin
+ *   n_tokens      rows of q, k and v
+ *   cu_seqlens    device int32 [batch + 1], non-decreasing, starting at 0
+ *   max_q_len     host upper bound of every L_b (sizes the grid)
+ *   rope          cos_sin NULL (rot_dim 0): no rotation
+ * A sequence with L_b < 0, > max_q_len or > T_b or rows outside [0, n_tokens) is skipped and
+ * FKV_FAULT_QLEN raised; one whose T_b is outside [0, max_blocks * 16] likewise with
+ * FKV_FAULT_CONTEXT, one with T_b > rope.max_positions with FKV_FAULT_POSITION; a block id
+ * out of range skips the block (FKV_FAULT_BLOCK_ID).
+ */
+fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                          int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, int32_t n_tokens, const int32_t* cu_seqlens, int32_t batch,
+                          int32_t max_q_len, fkv_rope rope, fkv_block_cache cache,
+                          const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                          int32_t* fault, fkv_stream_t stream);
 
 /*
  * Workspace bytes fp8_decode_attn needs for these sizes (same argument meaning as
@@ -320,6 +421,23 @@ fkv_status fp8_decode_attn_noalloc(const void* q, int32_t batch, int32_t num_q_h
                                    void* out, int32_t num_splits, int32_t* fault,
                                    fkv_stream_t stream);
 
+/*
+ * fp8_block_decode_attn — one decode step of GQA attention over a block-scaled cache.
+ *
+ * As fp8_decode_attn with the scales of each block and KV head g, and with neither the query
+ * nor P rounded to 8 bits:
+ *   s_j = q . (k8_j * k_scale[block(j)][g]) * softmax_scale,
+ *   out = sum_j softmax(s)_j * (v8_j * v_scale[block(j)][g])   (bf16).
+ * The bf16 query enters exactly, P with at least the precision of bf16 (relative to each
+ * tile's largest p * v_scale), every sum is FP32.  Arguments, split-K plan, workspace
+ * (fp8_decode_attn_workspace_size bytes, the same rules) and limits as for fp8_decode_attn.
+ */
+fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
+                                 const int32_t* block_table, int32_t max_blocks,
+                                 const int32_t* context_lens, float softmax_scale, int32_t window, void* out,
+                                 void* workspace, size_t workspace_bytes, int32_t num_splits, int32_t* fault,
+                                 fkv_stream_t stream);
+
 /* Keys per tile of fp8_prefill_attn (its online-softmax and P-rounding granularity). */
 int32_t fkv_prefill_block_n(int32_t head_dim);
 
@@ -365,6 +483,27 @@ fkv_status fp8_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t 
                             float softmax_scale, int32_t causal, int32_t window,
                             int32_t promote_every, int32_t layer, const uint8_t* skip_layer_mask,
                             int32_t num_layers, void* out, int32_t* fault, fkv_stream_t stream);
+
+/*
+ * fp8_block_prefill_attn — prefill (chunked) attention over a block-scaled cache.
+ *
+ * As fp8_prefill_attn (causal with or without a sliding window, or all keys) with the
+ * scales of each block and KV head; query and P precision as for fp8_block_decode_attn.
+ *   q             device bf16 [total_q][num_q_heads][head_dim]
+ *   cu_seqlens_q  device int32 [batch + 1], non-decreasing, starting at 0, at most total_q
+ *   max_q_len     host upper bound of every Lq_b (sizes the grid)
+ *   context_lens  T_b; with causal != 0, Lq_b <= T_b.  Without, any Lq_b (queries that are
+ *                 not part of the cached sequence); with T_b = 0 their rows are zero
+ *   out           device bf16 [total_q][num_q_heads][head_dim]; rows of no sequence keep
+ *                 their bytes
+ * A sequence with Lq_b < 0, > max_q_len, > T_b (causal) or rows outside [0, total_q) is skipped
+ * and FKV_FAULT_QLEN raised; T_b outside [0, max_blocks * 16] is clamped (FKV_FAULT_CONTEXT).
+ */
+fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
+                                  int32_t num_q_heads, int32_t max_q_len, fkv_block_cache cache,
+                                  const int32_t* block_table, int32_t max_blocks,
+                                  const int32_t* context_lens, float softmax_scale, int32_t causal,
+                                  int32_t window, void* out, int32_t* fault, fkv_stream_t stream);
 
 #ifdef __cplusplus
 }

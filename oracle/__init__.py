@@ -16,7 +16,10 @@ Modules and the passages they follow:
              kernel's tile walk, P rounded to e4m3 and two-level accumulation
              (blog "Kernel 与 vLLM 改进": Two-level accumulation)
 
+  blockcache the rotary position embedding and the block-scaled cache: append with
+             power-of-two scales per block and KV head, and the plain softmax over it
+
 Every function is pinned by tests in ``tests/test_oracle_*.py`` against closed forms,
 brute force, invariants or library routines; none is "parity unpinned".
 """
-from . import e4m3, kvcache, attention  # noqa: F401
+from . import e4m3, kvcache, attention, blockcache  # noqa: F401
