@@ -369,11 +369,6 @@ class BlockCache:
     k_scale: torch.Tensor
     v_scale: torch.Tensor
 
-    def c(self) -> _BlockCache:
-        n, h, bs, d = self.k_cache.shape
-        return _BlockCache(self.k_cache.data_ptr(), self.v_cache.data_ptr(), self.k_scale.data_ptr(),
-                           self.v_scale.data_ptr(), n, bs, h, d)
-
     @staticmethod
     def empty(num_blocks, num_kv_heads, head_dim, device="cuda", block_size=16):
         shape = (num_blocks, num_kv_heads, block_size, head_dim)
@@ -381,68 +376,68 @@ class BlockCache:
                           *(torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
 
 
-def _need(ok, fn, what):
-    if not ok:
-        raise ValueError(f"{fn}: {what}")
+# The checks below run before every launch, and a small call's time is host time: what passes costs a
+# few attribute reads, and messages are built only for what does not.
+
+def _refuse(fn, what):
+    raise ValueError(f"{fn}: {what}")
 
 
-def _tensors(fn, device, **named):
-    """Each named (tensor, dtype, shape): on `device`, of that type and shape, contiguous.  A shape entry
-    None accepts any length; a tensor None is left out."""
-    for name, (t, dtype, shape) in named.items():
-        if t is None:
-            continue
-        _need(t.device == device, fn, f"{name} is on {t.device}, not {device}")
-        _need(t.dtype is dtype, fn, f"{name} is {t.dtype}, not {dtype}")
-        _need(t.dim() == len(shape) and all(w is None or w == n for n, w in zip(t.shape, shape)), fn,
-              f"{name} has shape {tuple(t.shape)}, not {shape}")
-        _need(t.is_contiguous(), fn, f"{name} is not contiguous")
+def _check_tensors(fn, device, *wanted):
+    """Each (name, tensor or None, dtype, shape): contiguous, of that type and shape, on `device`."""
+    for name, t, dtype, shape in wanted:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+            _refuse(fn, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}; "
+                        f"wanted {dtype} {tuple(shape)} on {device}, contiguous")
 
 
 def _rows(fn, device, name, t, n, heads, d):
     """The token stride of a bf16 tensor [n][heads][d] whose rows are consecutive (a slice of a wider
     projection's output serves)."""
-    _need(t.device == device, fn, f"{name} is on {t.device}, not {device}")
-    _need(t.dtype is torch.bfloat16, fn, f"{name} is {t.dtype}, not torch.bfloat16")
-    _need(t.dim() == 3 and t.shape == (n, heads, d), fn, f"{name} has shape {tuple(t.shape)}, not {(n, heads, d)}")
+    if not (t.dtype is torch.bfloat16 and t.shape == (n, heads, d) and t.device == device):
+        _refuse(fn, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; wanted torch.bfloat16 {(n, heads, d)} on {device}")
     if n == 0:
         return heads * d
     s = t.stride()
-    _need(s[2] == 1 and (heads == 1 or s[1] == d), fn, f"{name}'s rows of {heads} x {d} elements are not consecutive")
-    return s[0] if n > 1 else max(s[0], heads * d) // 8 * 8
+    if s[2] != 1 or (heads > 1 and s[1] != d):
+        _refuse(fn, f"{name}'s rows of {heads} x {d} elements are not consecutive (strides {s})")
+    return s[0] if n > 1 else heads * d
 
 
 def _launch(fn, device, stream, *args):
-    """lib.fn(*args, stream) with the tensors' device current; stream None: that device's current stream."""
-    f = getattr(load_library(), fn)
-    if device.index == torch.cuda.current_device():
-        _check(fn, f(*args, _stream(stream)))
+    """The library's fn(*args, stream) with the tensors' device current; stream None: that device's current
+    stream."""
+    call = getattr(_lib or load_library(), fn)
+    index = device.index
+    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if index == torch._C._cuda_getDevice():
+        st = call(*args, s)
     else:
         with torch.cuda.device(device):
-            _check(fn, f(*args, _stream(stream)))
+            st = call(*args, s)
+    if st != OK:
+        _check(fn, st)
 
 
-def _cuda(fn, t):
-    _need(t.is_cuda, fn, "the tensors are not on a CUDA device")
+def _device(fn, t):
+    """The CUDA device of t, whose number of dimensions is 3."""
+    if not t.is_cuda or t.dim() != 3:
+        _refuse(fn, f"a tensor of shape {tuple(t.shape)} on {t.device}; wanted [n][heads][head_dim] on a CUDA device")
     return t.device
 
 
 def _query_rows(fn, device, q, q_out, n, d):
-    """(q pointer, stride, q_out pointer, stride, heads, q_out) of an optional query tensor [n][Hq][d]."""
+    """(q, its stride, q_out, its stride, heads) as the entry points take them, and the output tensor, of
+    an optional query tensor [n][Hq][d]."""
     if q is None:
-        _need(q_out is None, fn, "q_out without q")
-        return None, 0, None, 0, 0, None
-    _need(q.dim() == 3, fn, f"q has shape {tuple(q.shape)}")
-    hq = q.shape[1]
+        if q_out is not None:
+            _refuse(fn, "q_out without q")
+        return (None, 0, None, 0, 0), None
+    hq = q.shape[1] if q.dim() == 3 else -1
+    stride = _rows(fn, device, "q", q, n, hq, d)
     if q_out is None:
         q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=device)
-    return (q.data_ptr(), _rows(fn, device, "q", q, n, hq, d), q_out.data_ptr(),
-            _rows(fn, device, "q_out", q_out, n, hq, d), hq, q_out)
-
-
-def _check_rope(fn, device, rope):
-    _tensors(fn, device, cos_sin=(rope.cos_sin, torch.float32, (None, None)))
-    return rope.c()
+    return (q.data_ptr(), stride, q_out.data_ptr(), _rows(fn, device, "q_out", q_out, n, hq, d), hq), q_out
 
 
 def kv_rope_cache(q, k, v, positions, slot_mapping, rope: Rope, cache: LayerCache, k_scale=None, v_scale=None,
@@ -451,34 +446,34 @@ def kv_rope_cache(q, k, v, positions, slot_mapping, rope: Rope, cache: LayerCach
     skipped tokens are not written).  q, k, v: bf16 [n][heads][D], rows may be slices of a wider tensor; q may
     be None, q_out may be q.  positions, slot_mapping: int64 [n]."""
     fn = "kv_rope_cache"
-    device = _cuda(fn, k)
-    _need(k.dim() == 3, fn, f"k has shape {tuple(k.shape)}")
+    device = _device(fn, k)
     n, h, d = k.shape
     ks, vs = _rows(fn, device, "k", k, n, h, d), _rows(fn, device, "v", v, n, h, d)
-    qa = _query_rows(fn, device, q, q_out, n, d)
+    qa, q_out = _query_rows(fn, device, q, q_out, n, d)
     mp, nl, keep = _mask_arg(skip_layer_mask)
-    skipped = keep is not None and 0 <= layer < nl and bool(keep[layer])
-    scales = (h,) if gran == SCALE_PER_HEAD else (1,)
-    pool = (cache.k_cache.shape[0], h, None, d)
-    _tensors(fn, device, positions=(positions, torch.int64, (n,)), slot_mapping=(slot_mapping, torch.int64, (n,)),
-             k_cache=(cache.k_cache, torch.bfloat16 if skipped else torch.uint8, pool),
-             v_cache=(cache.v_cache, torch.bfloat16 if skipped else torch.uint8, tuple(cache.k_cache.shape)),
-             k_scale=(k_scale, torch.float32, scales), v_scale=(v_scale, torch.float32, scales),
-             fault=(fault, torch.int32, (1,)))
-    _launch(fn, device, stream, qa[0], qa[1], qa[2], qa[3], qa[4], k.data_ptr(), ks, v.data_ptr(), vs,
-            positions.data_ptr(), slot_mapping.data_ptr(), n, _check_rope(fn, device, rope), cache.c(), _ptr(k_scale),
-            _ptr(v_scale), int(gran), int(layer), mp, nl, _ptr(fault))
+    pool_t = torch.bfloat16 if keep is not None and 0 <= layer < nl and keep[layer] else torch.uint8
+    pool = (cache.k_cache.shape[0], h, cache.k_cache.shape[2] if cache.k_cache.dim() == 4 else 16, d)
+    scales = (h if gran == SCALE_PER_HEAD else 1,)
+    cs = rope.cos_sin
+    _check_tensors(fn, device, ("positions", positions, torch.int64, (n,)), ("slot_mapping", slot_mapping, torch.int64, (n,)),
+                   ("k_cache", cache.k_cache, pool_t, pool), ("v_cache", cache.v_cache, pool_t, pool),
+                   ("k_scale", k_scale, torch.float32, scales), ("v_scale", v_scale, torch.float32, scales),
+                   ("cos_sin", cs, torch.float32, cs.shape if cs.dim() == 2 else (0, 0)), ("fault", fault, torch.int32, (1,)))
+    _launch(fn, device, stream, *qa, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), n,
+            rope.c(), _LayerCache(cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), pool[0], pool[2], h, d, cache.kv_format),
+            _ptr(k_scale), _ptr(v_scale), gran, layer, mp, nl, _ptr(fault))
     del keep
-    return qa[5]
+    return q_out
 
 
-def _check_block_cache(fn, device, cache, h, d):
-    nb = cache.k_cache.shape[0]
-    pool = (nb, h, None, d)
-    _tensors(fn, device, k_cache=(cache.k_cache, torch.uint8, pool), v_cache=(cache.v_cache, torch.uint8,
-             tuple(cache.k_cache.shape)), k_scale=(cache.k_scale, torch.float32, (nb, h)),
-             v_scale=(cache.v_scale, torch.float32, (nb, h)))
-    return cache.c()
+def _block_cache(fn, device, cache, h, d):
+    """The C structure of a block-scaled cache of h KV heads and head_dim d."""
+    k = cache.k_cache
+    nb, bs = (k.shape[0], k.shape[2]) if k.dim() == 4 else (0, 16)
+    pool, scales = (nb, h, bs, d), (nb, h)
+    _check_tensors(fn, device, ("k_cache", k, torch.uint8, pool), ("v_cache", cache.v_cache, torch.uint8, pool),
+                   ("k_scale", cache.k_scale, torch.float32, scales), ("v_scale", cache.v_scale, torch.float32, scales))
+    return _BlockCache(k.data_ptr(), cache.v_cache.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), nb, bs, h, d)
 
 
 def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, context_lens, rope: Optional[Rope] = None,
@@ -487,32 +482,33 @@ def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, 
     its context_lens[b] tokens) to a block-scaled cache, K and q turned for their positions when ``rope`` is
     given; returns the turned queries (None without q)."""
     fn = "kv_block_cache"
-    device = _cuda(fn, k)
-    _need(k.dim() == 3, fn, f"k has shape {tuple(k.shape)}")
+    device = _device(fn, k)
     n, h, d = k.shape
     ks, vs = _rows(fn, device, "k", k, n, h, d), _rows(fn, device, "v", v, n, h, d)
-    qa = _query_rows(fn, device, q, q_out, n, d)
-    b = block_table.shape[0]
-    _tensors(fn, device, cu_seqlens=(cu_seqlens, torch.int32, (b + 1,)), block_table=(block_table, torch.int32, (b, None)),
-             context_lens=(context_lens, torch.int32, (b,)), fault=(fault, torch.int32, (1,)))
-    c = _check_block_cache(fn, device, cache, h, d)
-    r = _check_rope(fn, device, rope) if rope is not None else _Rope()
-    _launch(fn, device, stream, qa[0], qa[1], qa[2], qa[3], qa[4], k.data_ptr(), ks, v.data_ptr(), vs, n,
-            cu_seqlens.data_ptr(), b, int(max_q_len), r, c, block_table.data_ptr(), block_table.shape[1],
-            context_lens.data_ptr(), _ptr(fault))
-    return qa[5]
+    qa, q_out = _query_rows(fn, device, q, q_out, n, d)
+    b, mb = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    cs = None if rope is None else rope.cos_sin
+    _check_tensors(fn, device, ("cu_seqlens", cu_seqlens, torch.int32, (b + 1,)), ("block_table", block_table, torch.int32, (b, mb)),
+                   ("context_lens", context_lens, torch.int32, (b,)), ("fault", fault, torch.int32, (1,)),
+                   ("cos_sin", cs, torch.float32, cs.shape if cs is not None and cs.dim() == 2 else (0, 0)))
+    c = _block_cache(fn, device, cache, h, d)
+    _launch(fn, device, stream, *qa, k.data_ptr(), ks, v.data_ptr(), vs, n, cu_seqlens.data_ptr(), b, max_q_len,
+            _Rope() if rope is None else rope.c(), c, block_table.data_ptr(), mb, context_lens.data_ptr(), _ptr(fault))
+    return q_out
 
 
 def _attn_args(fn, q, rows, cache, block_table, context_lens, out, fault):
-    device = _cuda(fn, q)
-    _need(q.dim() == 3 and cache.k_cache.dim() == 4, fn, f"q has shape {tuple(q.shape)}, the pools {tuple(cache.k_cache.shape)}")
+    device = _device(fn, q)
+    n, hq, d = q.shape
+    k = cache.k_cache
+    b, mb = block_table.shape if block_table.dim() == 2 else (-1, 0)
+    want = (n if rows is None else b, hq, d)
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    b = block_table.shape[0]
-    _tensors(fn, device, q=(q, torch.bfloat16, (rows, None, cache.k_cache.shape[3])), out=(out, torch.bfloat16, tuple(q.shape)),
-             block_table=(block_table, torch.int32, (b, None)), context_lens=(context_lens, torch.int32, (b,)),
-             fault=(fault, torch.int32, (1,)))
-    return device, out, _check_block_cache(fn, device, cache, cache.k_cache.shape[1], q.shape[2])
+        out = torch.empty(want, dtype=torch.bfloat16, device=device)
+    _check_tensors(fn, device, ("q", q, torch.bfloat16, want), ("out", out, torch.bfloat16, want),
+                   ("block_table", block_table, torch.int32, (b, mb)), ("context_lens", context_lens, torch.int32, (b,)),
+                   ("fault", fault, torch.int32, (1,)))
+    return device, out, _block_cache(fn, device, cache, k.shape[1] if k.dim() == 4 else 0, d), n, hq, b, mb
 
 
 def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softmax_scale=0.0, window=0, out=None,
@@ -520,16 +516,14 @@ def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softm
     """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.  The
     workspace is fp8_decode_attn's (``decode_workspace`` makes one; zero-filled before its first call)."""
     fn = "fp8_block_decode_attn"
-    b, mb = block_table.shape
-    device, out, c = _attn_args(fn, q, b, cache, block_table, context_lens, out, fault)
-    hq = q.shape[1]
+    device, out, c, _, hq, b, mb = _attn_args(fn, q, "batch", cache, block_table, context_lens, out, fault)
     if workspace is None:
         n = fp8_decode_attn_workspace_size(b, hq, c.num_kv_heads, c.head_dim, mb, window, num_splits)
         workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
-    _need(workspace.device == device and workspace.is_contiguous(), fn, "workspace on another device or not contiguous")
-    _launch(fn, device, stream, q.data_ptr(), b, hq, c, block_table.data_ptr(), mb, context_lens.data_ptr(),
-            float(softmax_scale), int(window), out.data_ptr(), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), int(num_splits), _ptr(fault))
+    if workspace.device != device or not workspace.is_contiguous():
+        _refuse(fn, f"workspace on {workspace.device}; wanted contiguous on {device}")
+    _launch(fn, device, stream, q.data_ptr(), b, hq, c, block_table.data_ptr(), mb, context_lens.data_ptr(), softmax_scale,
+            window, out.data_ptr(), workspace.data_ptr(), workspace.nbytes, num_splits, _ptr(fault))
     return out
 
 
@@ -537,10 +531,8 @@ def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_
                            causal=True, window=0, out=None, fault=None, stream=None):
     """Ragged chunks of queries (rows cu_seqlens_q[b] .. of q bf16 [total][Hq][D]) over a block-scaled cache."""
     fn = "fp8_block_prefill_attn"
-    b, mb = block_table.shape
-    device, out, c = _attn_args(fn, q, None, cache, block_table, context_lens, out, fault)
-    _tensors(fn, device, cu_seqlens_q=(cu_seqlens_q, torch.int32, (b + 1,)))
-    _launch(fn, device, stream, q.data_ptr(), cu_seqlens_q.data_ptr(), q.shape[0], b, q.shape[1], int(max_q_len), c,
-            block_table.data_ptr(), mb, context_lens.data_ptr(), float(softmax_scale), int(bool(causal)), int(window),
-            out.data_ptr(), _ptr(fault))
+    device, out, c, n, hq, b, mb = _attn_args(fn, q, None, cache, block_table, context_lens, out, fault)
+    _check_tensors(fn, device, ("cu_seqlens_q", cu_seqlens_q, torch.int32, (b + 1,)))
+    _launch(fn, device, stream, q.data_ptr(), cu_seqlens_q.data_ptr(), n, b, hq, max_q_len, c, block_table.data_ptr(), mb,
+            context_lens.data_ptr(), softmax_scale, bool(causal), window, out.data_ptr(), _ptr(fault))
     return out

@@ -102,6 +102,17 @@ bool plan_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_bloc
   return true;
 }
 
+// The split plan and its workspace: the split-completion counters first (zero between calls), then
+// the splits' log-sum-exps and normalised outputs (written before they are read).
+void place_workspace(const DecodePlan& plan, void* workspace, DecodeParams* p) {
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  p->bps = plan.bps;
+  p->max_splits = plan.max_splits;
+  p->done = reinterpret_cast<int32_t*>(at);
+  p->lse_part = reinterpret_cast<float*>(at + plan.cnt_bytes);
+  p->o_part = reinterpret_cast<float*>(at + plan.cnt_bytes + plan.lse_bytes);
+}
+
 fkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FKV_OK : FKV_CUDA_ERROR; }
 
 // Bound of the tensor-core decode's pipeline waits set by fkv_set_decode_wait_limit_ns;
@@ -232,13 +243,7 @@ fkv_status decode_entry(const void* k_new, const void* v_new, const void* q, int
   const float tau = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(cache.head_dim));
   p.sm_scale_log2 = tau * 1.4426950408889634f;
   p.window = window;
-  p.bps = plan.bps;
-  p.max_splits = plan.max_splits;
-  // workspace: the split-completion counters first (zero between calls), then the
-  // splits' log-sum-exps and normalised outputs (written before they are read)
-  p.done = static_cast<int32_t*>(workspace);
-  p.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cnt_bytes);
-  p.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cnt_bytes + plan.lse_bytes);
+  place_workspace(plan, workspace, &p);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
@@ -541,15 +546,15 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
     return FKV_UNSUPPORTED;
   const size_t need = plan.o_bytes + plan.lse_bytes + plan.cnt_bytes;
   if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FKV_INVALID_ARG;
-  fkv::BlockAttnParams p;
+  DecodeParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
   p.v_cache = static_cast<const uint8_t*>(cache.v_cache);
+  p.block_table = block_table;
+  p.context_lens = context_lens;
   p.k_scale = cache.k_scale;
   p.v_scale = cache.v_scale;
-  p.block_table = block_table;
-  p.ctx = context_lens;
   p.B = batch;
   p.Hq = num_q_heads;
   p.Hkv = cache.num_kv_heads;
@@ -557,9 +562,11 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   p.max_blocks = max_blocks;
   p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
   p.window = window;
+  place_workspace(plan, workspace, &p);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
-  return from_cuda(fkv::launch_block_attn(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+  p.pipe_wait_ns = kDefaultPipeWaitNs;
+  return from_cuda(fkv::launch_block_decode(p, cache.head_dim, G, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
@@ -579,7 +586,7 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) ||
       !aligned(cu_seqlens_q, 4))
     return FKV_INVALID_ARG;
-  fkv::BlockAttnParams p;
+  fkv::BlockPrefillParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
@@ -601,7 +608,7 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   p.window = window;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
-  return from_cuda(fkv::launch_block_attn(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -22,7 +22,7 @@ FKV_DEV void decode_codes(const uint8_t* p, float (&f)[N]) {
 
 // One query row against keys [lo, hi) of sequence b.
 template <int D>
-FKV_DEV void attend_row(const BlockAttnParams& p, int b, int h, long long row, int lo, int hi) {
+FKV_DEV void attend_row(const BlockPrefillParams& p, int b, int h, long long row, int lo, int hi) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31, g = h / (p.Hq / p.Hkv);
   float q[E], acc[E];
@@ -64,23 +64,19 @@ FKV_DEV void attend_row(const BlockAttnParams& p, int b, int h, long long row, i
 }
 
 // Context length of sequence b, clamped to what the block table addresses.
-FKV_DEV int clamped_context(const BlockAttnParams& p, int b, bool report) {
+FKV_DEV int clamped_context(const BlockPrefillParams& p, int b, bool report) {
   const int T = p.ctx[b];
   if (T >= 0 && T <= static_cast<long long>(p.max_blocks) * 16) return T;
   if (report) raise_fault(p.fault, FKV_FAULT_CONTEXT);
   return T < 0 ? 0 : p.max_blocks * 16;
 }
 
-// grid (query rows / 4, Hq, B), 4 warps.  p.cu null: decode, one row per sequence.
+// grid (query rows / 4, Hq, B), 4 warps.
 template <int D>
-__global__ void __launch_bounds__(128) block_attn_kernel(const BlockAttnParams p) {
+__global__ void __launch_bounds__(128) block_prefill_kernel(const BlockPrefillParams p) {
   const int b = blockIdx.z, h = blockIdx.y, i = blockIdx.x * 4 + (threadIdx.x >> 5);
   const bool first = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
   const int T = clamped_context(p, b, first);
-  if (p.cu == nullptr) {
-    if (i == 0) attend_row<D>(p, b, h, b, p.window > 0 ? max(0, T - p.window) : 0, T);
-    return;
-  }
   const int r0 = p.cu[b], L = p.cu[b + 1] - r0;
   if (L < 0 || L > p.max_q_len || (p.causal && L > T) || r0 < 0 || r0 + static_cast<long long>(L) > p.total_q) {
     if (first) raise_fault(p.fault, FKV_FAULT_QLEN);
@@ -94,10 +90,10 @@ __global__ void __launch_bounds__(128) block_attn_kernel(const BlockAttnParams p
 
 }  // namespace
 
-cudaError_t launch_block_attn(const BlockAttnParams& p, int D, cudaStream_t s) {
-  const dim3 grid(p.cu ? (p.max_q_len + 3) / 4 : 1, p.Hq, p.B);
-  auto kern = D == 64 ? block_attn_kernel<64> : D == 128 ? block_attn_kernel<128> : block_attn_kernel<256>;
-  kern<<<grid, p.cu ? 128 : 32, 0, s>>>(p);
+cudaError_t launch_block_prefill(const BlockPrefillParams& p, int D, cudaStream_t s) {
+  const dim3 grid((p.max_q_len + 3) / 4, p.Hq, p.B);
+  auto kern = D == 64 ? block_prefill_kernel<64> : D == 128 ? block_prefill_kernel<128> : block_prefill_kernel<256>;
+  kern<<<grid, 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -100,13 +100,13 @@ struct BlockCacheParams {
 
 cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s);
 
-struct BlockAttnParams {
+struct BlockPrefillParams {
   const __nv_bfloat16* q;
   const uint8_t *k_cache, *v_cache;
   const float *k_scale, *v_scale;             // [num_blocks][Hkv]
   const int32_t* block_table;                 // [B][max_blocks]
   const int32_t* ctx;                         // [B]
-  const int32_t* cu;                          // [B + 1]; null: decode (one row per sequence)
+  const int32_t* cu;                          // [B + 1]
   int B, Hq, Hkv, num_blocks, max_blocks, max_q_len, total_q;
   float sm_scale_log2;                        // softmax_scale * log2(e)
   int causal, window;
@@ -114,7 +114,7 @@ struct BlockAttnParams {
   int32_t* fault;
 };
 
-cudaError_t launch_block_attn(const BlockAttnParams& p, int D, cudaStream_t s);
+cudaError_t launch_block_prefill(const BlockPrefillParams& p, int D, cudaStream_t s);
 
 cudaError_t launch_prefill(const PrefillParams& p, int D, bool bf16_layer, void* k_cache, void* v_cache,
                            cudaStream_t s);
@@ -149,6 +149,10 @@ cudaError_t launch_decode(const DecodeParams& p, int D, int elt, int G, cudaStre
 // tiles); bf16 and e5m2 layers on the CUDA cores (P exact).
 bool decode_uses_tensor_cores(int D, int elt);
 cudaError_t launch_decode_tc(const DecodeParams& p, int D, int G, cudaStream_t s);
+
+// The same kernel over a block-scaled cache: k_scale and v_scale are [num_blocks][Hkv], the query
+// stays bf16 (q_scale unused), k_new is null.
+cudaError_t launch_block_decode(const DecodeParams& p, int D, int G, cudaStream_t s);
 
 // Supplies the decode's workspace of `need` bytes when the caller passes none: sets *ws
 // (256-byte aligned) and *bytes, with its first `counter_bytes` (the split counters) zero

@@ -172,10 +172,10 @@ def test_binding_row_strides():
 def test_binding_tensor_checks():
     dev = torch.device("cpu")
     t = torch.zeros(4, 6, dtype=torch.int32)
-    f._tensors("f", dev, t=(t, torch.int32, (4, None)), u=(None, torch.int32, (1,)))
-    for bad in (t.long(), t[:3], t.T, t[:, ::2], t[0]):
-        with pytest.raises(ValueError):
-            f._tensors("f", dev, t=(bad, torch.int32, (4, None)))
+    f._check_tensors("f", dev, ("t", t, torch.int32, (4, 6)), ("u", None, torch.int32, (1,)))
+    for bad in (t.long(), t[:3], t.T, torch.zeros(4, 12, dtype=torch.int32)[:, ::2], t[0]):
+        with pytest.raises(ValueError, match="f: t is"):
+            f._check_tensors("f", dev, ("t", bad, torch.int32, (4, 6)))
 
 
 def test_rope_table():
