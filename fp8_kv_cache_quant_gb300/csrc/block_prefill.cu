@@ -1,100 +1,651 @@
-// Attention over a block-scaled e4m3 cache, one warp per (query row, query head): the lanes
-// share head_dim, the warp walks the visible keys one after another with the running maximum
-// and sum of the softmax in float32.
+// Prefill (chunked) attention over a block-scaled e4m3 cache on tcgen05 tensor cores: FP8 products
+// with the bf16 query and P each as two e4m3 terms, FP32 accumulation in tensor memory, each
+// tile's partial promoted into FP32 registers.
+//
+// Mathematics.  With q' = q 2^-k (k per row, so that the row's largest magnitude lies in [128, 256))
+// and q' = hi + lo, hi the leading 3 fraction bits, the scores of a tile of 128 keys are
+//   x_j = (hi . k8_j + lo . k8_j) * c * ks[block(j)],   c = 2^k softmax_scale log2(e);
+// a bf16 value has 8 significant bits and e4m3 4, so that hi + lo is q' down to 2^-18 of the row's
+// largest element.  With the tile's own row maximum M_t and its largest V scale vmax,
+//   P_j = 2^(x_j - M_t + lv[block(j)]),  lv = log2(256 vs / vmax),  P = hi + lo likewise,
+//   l_t = sum_blocks 2^-lv sum_j P_j,  O_t = sum_j (hi + lo)_j v8_j,
+// and the running state is m' = max(m, M_t), acc = acc 2^(m - m') + O_t vmax 2^(M_t - m'),
+// l = l 2^(m - m') + l_t 2^(M_t - m'); the output acc / (256 l).  P loses what lies below 2^-18 of
+// its tile's largest p vs, and is otherwise within 2^-8 of its value: the precision of a bf16 P.
+// hi and lo accumulate into the same S and O_t (two products of K = 32 instead of one), so that
+// K and V are used as they lie in the cache, without a pass that widens them to 16 bits.
+//
+// CTA = (up to 128 rows, KV head, sequence); a row is a (token, query head of the group) pair, so
+// that short chunks fill the 128 rows of the products and K / V tiles serve the whole group.
+// 16 warps:
+//   0-7   softmax: warp w owns rows 32 (w % 4) + 16 (w / 4) .. + 15, lanes l and l + 16 each half of
+//         a row's columns (16x32bx2 TMEM loads): the query's two terms (prologue); then per tile
+//         the maximum, P's two terms into shared memory, the row's factors of acc and O_t;
+//   8-11  correction: acc in registers (at head_dim 256 its second half in TMEM), epilogue;
+//   12    K copies (a block per lane) and the tile's scales: ks, lv, 2^-lv and vmax, read one tile
+//         ahead and staged in shared memory;
+//   13    allocates TMEM, issues S = q' K8^T;    14  issues O_t = P V8;    15  V copies.
+// TMEM: two S buffers and two O_t buffers up to head_dim 128; at head_dim 256 one S buffer, two
+// 128-column O_t buffers for the halves of head_dim, and the second half of acc.
+// Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
+// products drain and returns.
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "prefill_common.cuh"
+#include "tc.cuh"
 
 namespace fkv {
 namespace {
 
-// The float32 values of N e4m3 codes at p.
-template <int N>
-FKV_DEV void decode_codes(const uint8_t* p, float (&f)[N]) {
-#pragma unroll
-  for (int i = 0; i < N / 2; ++i) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(reinterpret_cast<const uint16_t*>(p)[i]));
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    f[2 * i] = x.x;
-    f[2 * i + 1] = x.y;
-  }
-}
-
-// One query row against keys [lo, hi) of sequence b.
 template <int D>
-FKV_DEV void attend_row(const BlockPrefillParams& p, int b, int h, long long row, int lo, int hi) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31, g = h / (p.Hq / p.Hkv);
-  float q[E], acc[E];
-  const __nv_bfloat16* src = p.q + (row * p.Hq + h) * D + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    q[i] = __bfloat162float(src[i]);
-    acc[i] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  for (int j = lo; j < hi; ++j) {
-    int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + (j >> 4)];
-    if (id < 0 || id >= p.num_blocks) {
-      if (lane == 0) raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
-      id = 0;
-    }
-    const size_t at = (static_cast<size_t>(id) * p.Hkv + g) * 16 * D + (j & 15) * D + lane * E;
-    const size_t sc = static_cast<size_t>(id) * p.Hkv + g;
-    float k[E], v[E], x = 0.f;
-    decode_codes(p.k_cache + at, k);
-    decode_codes(p.v_cache + at, v);
-#pragma unroll
-    for (int i = 0; i < E; ++i) x = fmaf(q[i], k[i], x);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-    x *= p.k_scale[sc] * p.sm_scale_log2;
-    const float mn = fmaxf(m, x);
-    const float alpha = m == -INFINITY ? 0.f : ex2(m - mn), w = ex2(x - mn);
-    m = mn;
-    l = fmaf(l, alpha, w);
-    const float wv = w * p.v_scale[sc];
-#pragma unroll
-    for (int i = 0; i < E; ++i) acc[i] = fmaf(acc[i], alpha, wv * v[i]);
-  }
-  const float inv = hi > lo ? 1.f / l : 0.f;
-  __nv_bfloat16* dst = p.out + (row * p.Hq + h) * D + lane * E;
-#pragma unroll
-  for (int i = 0; i < E; ++i) dst[i] = __float2bfloat16(acc[i] * inv);
+struct BlockPrefillCfg {
+  static constexpr int BM = 128, BN = 128;          // rows of a CTA, keys of a tile
+  static constexpr int NBLK = BN / 16;              // blocks of a tile
+  static constexpr int RB = D < 128 ? D : 128;      // bytes of one swizzled row
+  static constexpr int NSUB = D / RB;               // sub-tiles along head_dim
+  static constexpr int SWZ = RB == 128 ? 2 : 4;     // descriptor swizzle mode (128 B / 64 B)
+  static constexpr int SUB = 128 * RB;              // bytes of one 128-row sub-tile (Q, K or V)
+  static constexpr int TILE = 128 * D;              // bytes of a term of Q, or of a K or V tile
+  static constexpr int NS = D <= 128 ? 3 : 2;       // K / V stages
+  static constexpr int DN = D < 128 ? D : 128;      // columns of one P.V product
+  static constexpr int NH = D / DN;                 // P.V passes per tile
+  static constexpr int PTERM = BM * BN;             // bytes of one term of P
+  static constexpr int PBUF = D <= 128 ? 2 : 1;     // P buffers (two do not fit at head_dim 256)
+  static constexpr int SBUF = D <= 128 ? 2 : 1;     // S buffers in TMEM
+  static constexpr int HC = BN / 2;                 // columns of a softmax thread
+  static constexpr int SW = 8;                      // softmax warps
+  static constexpr int THREADS = 512;
+  static constexpr int TM_OT = 128 * SBUF, TM_OH = TM_OT + 2 * DN;  // O_t buffers; second half of acc
+  static constexpr int TM_COLS = 512;
+  // scales of a tile in a ring of slots: the K copies run at most SBUF + NS tiles ahead of the
+  // softmax (a stage is refilled once its S was computed, an S buffer once it was read)
+  static constexpr int SCN = D <= 128 ? 8 : 4;
+  static constexpr int SCF = 32;                    // floats per slot: ks [8], lv [8], 2^-lv [8], vmax
+  static_assert(SCN > SBUF + NS, "a slot is rewritten only after the softmax is done with it");
+  // registers per thread of the warpgroups (launch: 128 each): softmax, correction, copies and MMA
+  static constexpr int REG_LAUNCH = 128, REG_SOFT = 120, REG_CORR = D > 64 ? 232 : 144,
+                       REG_MISC = 4 * REG_LAUNCH - 2 * REG_SOFT - REG_CORR;
+  static_assert(REG_SOFT <= REG_LAUNCH && REG_CORR >= REG_LAUNCH && REG_MISC <= REG_LAUNCH && REG_MISC >= 24 &&
+                    REG_SOFT % 8 == 0 && REG_CORR % 8 == 0 && REG_MISC % 8 == 0,
+                "setmaxnreg budgets");
+  // shared memory (bytes)
+  static constexpr int OFF_Q = 0;                   // hi, lo
+  static constexpr int OFF_K = OFF_Q + 2 * TILE;
+  static constexpr int OFF_V = OFF_K + NS * TILE;
+  static constexpr int OFF_P = OFF_V + NS * TILE;   // per buffer: hi, lo
+  static constexpr int OFF_F = OFF_P + PBUF * 2 * PTERM;  // factors [2][128] float2 (acc, O_t); last: (l, -)
+  static constexpr int OFF_SC = OFF_F + 2 * BM * 8;
+  static constexpr int OFF_BAR = OFF_SC + SCN * SCF * 4;
+  static constexpr int NBAR = 18 + 4 * NS + SCN;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, BN, 0, 0);
+  static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(128, DN, 0, 1);
+  static_assert(SMEM <= 227 * 1024, "shared memory budget");
+  static_assert(TM_OH + D - DN <= 512, "TMEM budget");
+};
+
+// e4m3 codes of the two terms of four values: `hi` the leading 3 fraction bits, `lo` the rest.
+FKV_DEV void split4(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
+  auto lead = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); };
+  const float2 ha = make_float2(lead(a.x), lead(a.y)), hb = make_float2(lead(b.x), lead(b.y));
+  const float2 neg = make_float2(-1.f, -1.f);
+  const float2 la = __ffma2_rn(ha, neg, a), lb = __ffma2_rn(hb, neg, b);
+  hi = static_cast<uint32_t>(f32x2_to_e4m3x2(ha.x, ha.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(hb.x, hb.y)) << 16);
+  lo = static_cast<uint32_t>(f32x2_to_e4m3x2(la.x, la.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(lb.x, lb.y)) << 16);
 }
 
-// Context length of sequence b, clamped to what the block table addresses.
-FKV_DEV int clamped_context(const BlockPrefillParams& p, int b, bool report) {
-  const int T = p.ctx[b];
-  if (T >= 0 && T <= static_cast<long long>(p.max_blocks) * 16) return T;
-  if (report) raise_fault(p.fault, FKV_FAULT_CONTEXT);
-  return T < 0 ? 0 : p.max_blocks * 16;
-}
+template <int D, bool WIN>
+__global__ void __launch_bounds__(512, 1)
+    block_prefill_kernel(const __grid_constant__ BlockPrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                         const __grid_constant__ CUtensorMap tmv) {
+  using C = BlockPrefillCfg<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sP = smem + C::OFF_P;
+  float2* sF = reinterpret_cast<float2*>(smem + C::OFF_F);
+  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars + 0;
+  uint64_t* s_full = bars + 1;      // [2] S(t) in buffer t % SBUF
+  uint64_t* s_free = bars + 3;      // [2]
+  uint64_t* p_full = bars + 5;      // [2] P(t) in buffer t % PBUF
+  uint64_t* p_free = bars + 7;      // [2]
+  uint64_t* o_full = bars + 9;      // [2] P.V pass n in buffer n % 2
+  uint64_t* o_free = bars + 11;     // [2]
+  uint64_t* mma_done = bars + 13;
+  uint64_t* f_full = bars + 14;     // [2] factors of tile t in slot t % 2 (tile n_t: the rows' l)
+  uint64_t* f_free = bars + 16;     // [2]
+  uint64_t* k_full = bars + 18;
+  uint64_t* k_empty = k_full + C::NS;
+  uint64_t* v_full = k_empty + C::NS;
+  uint64_t* v_empty = v_full + C::NS;
+  uint64_t* sc_full = v_empty + C::NS;  // [SCN] scales of tile t in slot t % SCN
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
 
-// grid (query rows / 4, Hq, B), 4 warps.
-template <int D>
-__global__ void __launch_bounds__(128) block_prefill_kernel(const BlockPrefillParams p) {
-  const int b = blockIdx.z, h = blockIdx.y, i = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const bool first = blockIdx.x == 0 && h == 0 && threadIdx.x == 0;
-  const int T = clamped_context(p, b, first);
-  const int r0 = p.cu[b], L = p.cu[b + 1] - r0;
-  if (L < 0 || L > p.max_q_len || (p.causal && L > T) || r0 < 0 || r0 + static_cast<long long>(L) > p.total_q) {
-    if (first) raise_fault(p.fault, FKV_FAULT_QLEN);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.Hq / p.Hkv;
+  // query heads [h_first, h_first + GC) of KV head g: the whole group, or a part of it when it has
+  // more than 128 heads
+  const int g = blockIdx.y / p.head_parts, part = blockIdx.y - g * p.head_parts;
+  const int GC = p.part_heads, h_first = part * GC;
+  const int tok = 128 / GC;                   // tokens per CTA
+  const int b = blockIdx.z;
+  const int qt = gridDim.x - 1 - blockIdx.x;  // longest (latest) query tiles first
+
+  // ------------------------------------------------------------ sequence geometry
+  const bool first_cta = qt == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+  const int r0 = p.cu[b];
+  const int Lq = p.cu[b + 1] - r0;
+  int T = p.ctx[b];
+  if (T < 0 || T > static_cast<long long>(p.max_blocks) * 16) {
+    if (first_cta) raise_fault(p.fault, FKV_FAULT_CONTEXT);
+    T = T < 0 ? 0 : p.max_blocks * 16;
+  }
+  if (Lq < 0 || Lq > p.max_q_len || (p.causal && Lq > T) || r0 < 0 || r0 + static_cast<long long>(Lq) > p.total_q) {
+    if (first_cta) raise_fault(p.fault, FKV_FAULT_QLEN);
     return;
   }
-  if (i >= L) return;
-  const int pos = T - L + i;
-  attend_row<D>(p, b, h, r0 + static_cast<long long>(i), p.window > 0 ? max(0, pos - p.window + 1) : 0,
-                p.causal ? pos + 1 : T);
+  const int q0 = qt * tok;  // first token of the CTA
+  if (q0 >= Lq) return;
+  const int toks = min(tok, Lq - q0);
+  const int pos0 = T - Lq + q0;  // absolute position of the first token (may be negative when not causal)
+  const int kv_end = p.causal ? min(T, pos0 + toks) : T;  // keys [kv_lo, kv_end) matter
+  const int kv_lo = WIN ? max(0, pos0 - p.window + 1) : 0;
+  const int tb = kv_lo / C::BN;                           // first key tile
+  const int n_t = (kv_end + C::BN - 1) / C::BN - tb;      // tiles u = 0 .. n_t-1 are tb + u
+  const int nblk_seq = (T + 15) >> 4;
+
+  if (threadIdx.x == 0) {
+    // barriers signalled by the softmax or correction warps count warps (one arrival each)
+    mbar_init(q_full, C::SW);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], C::SW);
+      mbar_init(&p_full[i], C::SW);
+      mbar_init(&p_free[i], 1);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_free[i], 4);
+      mbar_init(&f_full[i], C::SW);
+      mbar_init(&f_free[i], 4);
+    }
+    mbar_init(mma_done, 2);  // one commit from each MMA warp
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&k_full[s], 1);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int s = 0; s < C::SCN; ++s) mbar_init(&sc_full[s], 1);
+    *abort_s = 0;
+    fence_mbar_init();
+  }
+  if (warp == 13) {
+    tmem_alloc(tmem_slot, C::TM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < C::SW) {
+    // ============================================================ softmax warps
+    regs_dec<C::REG_SOFT>();
+    const int hf = lane >> 4;                                  // column half
+    const int rb = (warp & 3) * 32 + (warp >> 2) * 16;         // first TMEM lane
+    const int i = rb + (lane & 15);                            // row (TMEM lane i)
+    const int it = i / GC, h = h_first + i - it * GC;          // its token and head of the group
+    const bool row_ok = it < toks && h < G;
+    const int pos = pos0 + it;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(rb) << 16);
+    const int c0 = hf * C::HC;                                 // first column of this thread's half
+    float cst;                                                 // c of the row
+    // ---- prologue: the row's two terms in the swizzled Q tiles, half of the row per thread
+    {
+      constexpr int NCH = D / 16;  // 16-byte chunks (8 elements) of half a row
+      uint4 w[NCH];
+      uint32_t amax = 0;
+      const uint4* src = reinterpret_cast<const uint4*>(
+          p.q + (static_cast<long long>(r0 + q0 + it) * p.Hq + g * G + h) * D) + hf * NCH;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) {
+        w[c] = row_ok ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t in[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) amax = max(amax, max((in[j] << 16) & 0x7FFF0000u, in[j] & 0x7FFF0000u));
+      }
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+      const int k = max(static_cast<int>(amax >> 23) - 127 - 7, -126);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      // a row with a NaN or an infinity makes its scores, and so its output, NaN
+      cst = amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k) << 23)
+                               : __uint_as_float(0x7FC00000u);
+#pragma unroll
+      for (int c = 0; c < NCH; c += 2) {  // 16 elements: 16 bytes of each term
+        const uint32_t in[8] = {w[c].x, w[c].y, w[c].z, w[c].w, w[c + 1].x, w[c + 1].y, w[c + 1].z, w[c + 1].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 x0 = bf16x2_to_f2(in[2 * j]), x1 = bf16x2_to_f2(in[2 * j + 1]);
+          x0.x *= down; x0.y *= down; x1.x *= down; x1.y *= down;
+          split4(x0, x1, hi[j], lo[j]);
+        }
+        const int byte = hf * (D / 2) + c * 8;
+        uint8_t* dst = sQ + (byte / C::RB) * C::SUB + swz(static_cast<uint32_t>(i * C::RB + byte % C::RB), C::RB);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + C::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(q_full);
+    }
+    const int lim_row = (p.causal && row_ok) ? min(T, pos + 1) : T;  // keys [lo_row, lim_row) visible
+    const int lo_row = (WIN && row_ok) ? max(0, pos - p.window + 1) : 0;
+    float m = -1e30f, l = 0.f;  // l: this thread's columns only
+    bool ok = true;
+    for (int t = 0; t < n_t; ++t) {
+      if ((t & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+      const int sb = t % C::SBUF, pb = t % C::PBUF;
+      if (!pf_wait_warp(&s_full[sb], (t / C::SBUF) & 1)) { ok = false; break; }
+      tc_fence_after();
+      const uint32_t sc = lane_base + 128 * sb;
+      float v[C::HC];
+#pragma unroll
+      for (int c = 0; c < C::HC / 32; ++c) tmem_ld32_16x2<C::HC>(sc + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
+      const bool p_ready = t < C::PBUF || mbar_test_wait(&p_free[pb], ((t / C::PBUF) - 1) & 1);
+      const bool f_ready = t < 2 || mbar_test_wait(&f_free[t & 1], ((t >> 1) - 1) & 1);
+      // this half's four blocks: ks, lv, 2^-lv
+      if (!pf_wait_warp(&sc_full[t % C::SCN], (t / C::SCN) & 1)) { ok = false; break; }
+      const float* scl = sSc + (t % C::SCN) * C::SCF + 4 * hf;
+      const float4 ks4 = *reinterpret_cast<const float4*>(scl), lv4 = *reinterpret_cast<const float4*>(scl + 8),
+                   iv4 = *reinterpret_cast<const float4*>(scl + 16);
+      const float vmax = sSc[(t % C::SCN) * C::SCF + 24];
+      const float cb[4] = {cst * ks4.x, cst * ks4.y, cst * ks4.z, cst * ks4.w};
+      const int kbase = (tb + t) * C::BN + c0;  // key of this thread's first column
+      const int lim = lim_row - kbase, lo = WIN ? lo_row - kbase : -(1 << 30);
+      const bool full = lim >= C::HC && (!WIN || lo <= 0);
+      const bool wfull = __all_sync(0xffffffffu, full);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive_warp(&s_free[sb]);
+      // hidden scores become -inf (2^(-inf) = 0 is the zero the mask asks for), under a test that
+      // the whole warp takes alike
+      if (!wfull) {
+#pragma unroll
+        for (int j = 0; j < C::HC; ++j)
+          if (j >= lim || j < lo) v[j] = -INFINITY;
+      }
+      float tmax = -1e30f;  // (finite, so that a row that sees nothing of the tile adds zeros)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmax = fmaxf(tmax, max_tree<16>(v + 16 * k) * cb[k]);
+      tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16));
+      // one of the two factors is 1, the other 2^-|m - tmax|
+      const float e = ex2(-fabsf(m - tmax));
+      const float alpha = m > tmax ? 1.f : e, corr = m > tmax ? e : 1.f;
+      m = fmaxf(m, tmax);
+      if (!__all_sync(0xffffffffu, p_ready) && !pf_wait_warp(&p_free[pb], ((t / C::PBUF) - 1) & 1)) { ok = false; break; }
+      uint8_t* P = sP + pb * 2 * C::PTERM;
+      const float nb[4] = {lv4.x - tmax, lv4.y - tmax, lv4.z - tmax, lv4.w - tmax};
+      const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+      float lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // block k: 16 columns, 16 bytes of each term
+        const float2 c2 = make_float2(cb[k], cb[k]), n2 = make_float2(nb[k], nb[k]);
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t hi[4], lw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 x0 = __ffma2_rn(make_float2(v[16 * k + 4 * j], v[16 * k + 4 * j + 1]), c2, n2);
+          float2 x1 = __ffma2_rn(make_float2(v[16 * k + 4 * j + 2], v[16 * k + 4 * j + 3]), c2, n2);
+          x0.x = ex2(x0.x); x0.y = ex2(x0.y); x1.x = ex2(x1.x); x1.y = ex2(x1.y);
+          sum = __fadd2_rn(sum, __fadd2_rn(x0, x1));
+          split4(x0, x1, hi[j], lw[j]);
+        }
+        lt = fmaf(sum.x + sum.y, iv[k], lt);
+        uint8_t* dst = P + swz(static_cast<uint32_t>(i * 128 + c0 + 16 * k), 128);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(dst + C::PTERM) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+      }
+      l = fmaf(l, alpha, corr * lt);
+      if (!__all_sync(0xffffffffu, f_ready) && !pf_wait_warp(&f_free[t & 1], ((t >> 1) - 1) & 1)) { ok = false; break; }
+      if (hf == 0) sF[(t & 1) * C::BM + i] = make_float2(alpha, corr * vmax);
+      mbar_arrive_warp(&f_full[t & 1]);
+      fence_proxy_async_smem();
+      mbar_arrive_warp(&p_full[pb]);
+    }
+    tmem_ld_wait();  // no load left in flight on an early exit
+    // ---- the rows' l takes the factor slot after the last tile's
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (ok && n_t >= 2) ok = pf_wait_warp(&f_free[n_t & 1], ((n_t >> 1) - 1) & 1);
+    if (ok) {
+      if (hf == 0) sF[(n_t & 1) * C::BM + i] = make_float2(l, 0.f);
+      mbar_arrive_warp(&f_full[n_t & 1]);
+    } else {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    }
+  } else if (warp < C::SW + 4) {
+    // ============================================================ correction warpgroup
+    regs_inc<C::REG_CORR>();
+    const int i = threadIdx.x - 32 * C::SW;    // row (TMEM lane i)
+    const int it = i / GC, h = h_first + i - it * GC;
+    const bool row_ok = it < toks && h < G;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp - C::SW) * 32) << 16);
+    bool ok = true;
+    float O[C::DN];  // acc, columns [0, DN)
+#pragma unroll
+    for (int j = 0; j < C::DN; ++j) O[j] = 0.f;
+    for (int t = 0; t < n_t; ++t) {
+      if ((t & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+      if (!pf_wait_warp(&f_full[t & 1], (t >> 1) & 1)) { ok = false; break; }
+      const float2 f = sF[(t & 1) * C::BM + i];
+      mbar_arrive_warp(&f_free[t & 1]);
+      const float2 a2 = make_float2(f.x, f.x), b2 = make_float2(f.y, f.y);
+#pragma unroll
+      for (int hn = 0; hn < C::NH; ++hn) {
+        const int n = C::NH * t + hn, ob = n & 1;
+        if (!pf_wait_warp(&o_full[ob], (n >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t src = lane_base + C::TM_OT + ob * C::DN;
+        if (hn == 0) {
+#pragma unroll
+          for (int c = 0; c < C::DN / 32; ++c) {
+            float o[32];
+            tmem_ld32(src + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 x = __fmul2_rn(make_float2(o[j], o[j + 1]), b2);
+              const float2 r = __ffma2_rn(make_float2(O[32 * c + j], O[32 * c + j + 1]), a2, x);
+              O[32 * c + j] = r.x;
+              O[32 * c + j + 1] = r.y;
+            }
+            pin32(O + 32 * c);
+          }
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < C::DN / 32; ++c) {
+            float o[32], acc[32];
+            const uint32_t dst = lane_base + C::TM_OH + 32 * c;
+            tmem_ld32(src + 32 * c, o);
+            if (t > 0) tmem_ld32(dst, acc);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 x = __fmul2_rn(make_float2(o[j], o[j + 1]), b2);
+              const float2 r = t > 0 ? __ffma2_rn(make_float2(acc[j], acc[j + 1]), a2, x) : x;
+              acc[j] = r.x;
+              acc[j + 1] = r.y;
+            }
+            tmem_st32(dst, acc);
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive_warp(&o_free[ob]);
+      }
+      if (!ok) break;
+    }
+    // ---- epilogue: acc / (256 l) as bf16 (every lane loads; rows past the chunk do not store)
+    if (ok) ok = pf_wait_warp(&f_full[n_t & 1], (n_t >> 1) & 1);
+    if (!ok) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    } else {
+      const float l = sF[(n_t & 1) * C::BM + i].x;
+      const float f = l == 0.f ? 0.f : 1.f / (256.f * l);  // (a row that sees no key: zero)
+      __nv_bfloat16* dst = p.out + (static_cast<long long>(r0 + q0 + it) * p.Hq + g * G + h) * D;
+      auto store32 = [&](int c, const float* x) {
+        if (!row_ok) return;
+        uint32_t w[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+          w[j] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        uint4* o4 = reinterpret_cast<uint4*>(dst + 32 * c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o4[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      };
+#pragma unroll
+      for (int c = 0; c < C::DN / 32; ++c) store32(c, O + 32 * c);
+      if constexpr (C::NH == 2) {
+#pragma unroll 1
+        for (int c = 0; c < C::DN / 32; ++c) {
+          float acc[32];
+          if (n_t > 0) {
+            tmem_ld32(lane_base + C::TM_OH + 32 * c, acc);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[j] = 0.f;
+          }
+          store32(C::DN / 32 + c, acc);
+        }
+      }
+    }
+  } else {
+    regs_dec<C::REG_MISC>();
+    if (warp == 12 || warp == 15) {
+      // ============================================================ copies: K (12), V (15)
+      // Lane j < 8 copies the tile's j-th block; block ids are read two tiles ahead, scales (K
+      // warp) one.
+      const bool is_k = warp == 12;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? k_empty : v_empty;
+      uint8_t* base = is_k ? sK : sV;
+      const CUtensorMap* map = is_k ? &tmk : &tmv;
+      const int* trow = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+      int last[C::NS];  // last use of each stage whose copies were issued
+#pragma unroll
+      for (int s = 0; s < C::NS; ++s) last[s] = -1;
+      // block id, -1 past the sequence (copied from block 0, its keys masked)
+      auto block_id = [&](int t) -> int {
+        const int lb = (tb + t) * C::NBLK + lane;
+        if (lane >= C::NBLK || t >= n_t || lb >= nblk_seq) return -1;
+        const int id = trow[lb];
+        if (id >= 0 && id < p.num_blocks) return id;
+        raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+        return 0;
+      };
+      float ks_n = 0.f, vs_n = 0.f;
+      auto read_scales = [&](int id) {
+        ks_n = vs_n = 0.f;
+        if (is_k && id >= 0) {
+          const size_t at = static_cast<size_t>(id) * p.Hkv + g;
+          ks_n = p.k_scale[at];
+          vs_n = p.v_scale[at];
+        }
+      };
+      int id = block_id(0), id_next = block_id(1);
+      read_scales(id);
+      for (int t = 0; t < n_t; ++t) {
+        if (abort_warp(abort_s)) break;
+        const float ks = ks_n, vs = vs_n;
+        const int id_t = max(id, 0);
+        read_scales(id_next);
+        id = id_next;
+        id_next = block_id(t + 2);
+        const int st = t % C::NS, use = t / C::NS;
+        bool ok = true;
+        if (lane == 0 && use > 0) ok = pf_wait(&empty[st], (use - 1) & 1);
+        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+          if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+          *abort_s = 1;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], C::TILE);
+        __syncwarp();
+        if (lane < C::NBLK) {
+          uint8_t* dst = base + st * C::TILE + lane * 16 * C::RB;
+#pragma unroll
+          for (int s = 0; s < C::NSUB; ++s) tma_load_4d(dst + s * C::SUB, map, s * C::RB, 0, g, id_t, &full[st]);
+        }
+        last[st] = use;
+        if (is_k) {
+          // the tile's scales.  lv is kept above -32 (a V scale 2^-40 of the tile's largest, zeros
+          // too, whose P falls below the terms' range), so that its inverse stays finite; ks above
+          // 2^-100, so that a hidden score of -inf stays one.
+          float vmax = vs;
+#pragma unroll
+          for (int off = 4; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+          const float lv = vs > 0.f ? fmaxf(lg2(__fdividef(vs, vmax)) + 8.f, -32.f) : -32.f;
+          float* slot = sSc + (t % C::SCN) * C::SCF;
+          if (lane < C::NBLK) {
+            slot[lane] = fmaxf(ks, 7.888609e-31f);
+            slot[8 + lane] = lv;
+            slot[16 + lane] = ex2(-lv);
+          }
+          if (lane == 0) slot[24] = vmax;
+          mbar_arrive_warp(&sc_full[t % C::SCN]);
+        }
+      }
+      // let every issued copy land before the CTA can exit
+      if (lane == 0)
+        for (int s = 0; s < C::NS; ++s)
+          if (last[s] >= 0) pf_wait(&full[s], last[s] & 1);
+      __syncwarp();
+    } else {
+      // ============================================================ MMA issuers: S (13), P.V (14)
+      const uint64_t dQ = smem_desc(smem_u32(sQ), 16, 8 * C::RB, C::SWZ);
+      const uint64_t dK = smem_desc(smem_u32(sK), 16, 8 * C::RB, C::SWZ);
+      const uint64_t dV = smem_desc(smem_u32(sV), 8 * C::RB, 8 * C::RB, C::SWZ);
+      const uint64_t dP = smem_desc(smem_u32(sP), 16, 1024, 2);
+      bool ok = true;
+      if (warp == 13) {
+        ok = pf_wait_warp(q_full, 0);
+        for (int t = 0; ok && t < n_t; ++t) {
+          if ((t & 7) == 7 && abort_warp(abort_s)) break;
+          const int st = t % C::NS, sb = t % C::SBUF;
+          ok = pf_wait_warp(&k_full[st], (t / C::NS) & 1);
+          if (ok && t >= C::SBUF) ok = pf_wait_warp(&s_free[sb], ((t / C::SBUF) - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (lane == 0) {
+            // S(t) = hi K8^T + lo K8^T
+#pragma unroll
+            for (int term = 0; term < 2; ++term)
+#pragma unroll
+              for (int kk = 0; kk < D / 32; ++kk) {
+                const int byte = kk * 32;
+                const uint32_t off = (byte / C::RB) * C::SUB + (byte % C::RB);
+                umma_f8(tmem + 128 * sb, desc_add(dQ, term * C::TILE + off), desc_add(dK, st * C::TILE + off), C::IDESC_QK,
+                        (term > 0 || kk > 0) ? 1u : 0u);
+              }
+            umma_commit(&s_full[sb]);
+            umma_commit(&k_empty[st]);
+          }
+          __syncwarp();
+        }
+      } else {
+        int n = 0;  // P.V passes issued
+        for (int t = 0; ok && t < n_t; ++t) {
+          if ((t & 7) == 7 && abort_warp(abort_s)) break;
+          const int st = t % C::NS, pb = t % C::PBUF;
+          ok = pf_wait_warp(&p_full[pb], (t / C::PBUF) & 1) && pf_wait_warp(&v_full[st], (t / C::NS) & 1);
+          if (!ok) break;
+          // keys past the context, and before a window, may hold any bytes (NaN codes): zero their V
+          // rows, since 0 * NaN would poison the product even though their P is 0
+          const int kbase = (tb + t) * C::BN;
+          const int keep_lo = max(kv_lo - kbase, 0), keep_hi = min(T - kbase, C::BN);
+          if (keep_lo > 0 || keep_hi < C::BN) {
+            constexpr int CPR = C::RB / 16;  // 16-byte chunks of a row
+            for (int x = lane; x < C::BN * C::NSUB * CPR; x += 32) {
+              const int c = x % CPR, s = (x / CPR) % C::NSUB, r = x / (CPR * C::NSUB);
+              if (r < keep_lo || r >= keep_hi)
+                *reinterpret_cast<uint4*>(sV + st * C::TILE + s * C::SUB + r * C::RB + c * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int hn = 0; hn < C::NH; ++hn, ++n) {
+            // O_t buffer n % 2 is free once the correction took pass n - 2
+            const int ob = n & 1;
+            if (n >= 2 && !pf_wait_warp(&o_free[ob], ((n >> 1) - 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            if (lane == 0) {
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+#pragma unroll
+                for (int kk = 0; kk < C::BN / 32; ++kk)
+                  umma_f8(tmem + C::TM_OT + ob * C::DN, desc_add(dP, pb * 2 * C::PTERM + term * C::PTERM + kk * 32),
+                          desc_add(dV, st * C::TILE + hn * C::SUB + kk * 32 * C::RB), C::IDESC_PV,
+                          (term > 0 || kk > 0) ? 1u : 0u);
+              umma_commit(&o_full[ob]);
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (lane == 0) {
+            umma_commit(&v_empty[st]);
+            umma_commit(&p_free[pb]);
+          }
+          __syncwarp();
+        }
+      }
+      if (!ok) {
+        if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+        *abort_s = 1;
+      }
+      // every product issued by either warp completes before TMEM is released
+      if (lane == 0) {
+        umma_commit(mma_done);
+        pf_wait(mma_done, 0);
+      }
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  if (warp == 13) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+template <int D, bool WIN>
+cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, cudaStream_t s) {
+  using C = BlockPrefillCfg<D>;
+  CUtensorMap tmk, tmv;
+  if (!make_pool_map(&tmk, const_cast<uint8_t*>(p.k_cache), D, p.Hkv, p.num_blocks, C::RB) ||
+      !make_pool_map(&tmv, const_cast<uint8_t*>(p.v_cache), D, p.Hkv, p.num_blocks, C::RB))
+    return cudaErrorInvalidValue;
+  auto kern = block_prefill_kernel<D, WIN>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  // the warpgroups' register budgets add up to the launch's 128 per thread: a kernel built with
+  // fewer would wait forever in setmaxnreg.inc, so it is never launched
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    regs.store(a.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != C::REG_LAUNCH) return cudaErrorInvalidKernelImage;
+  kern<<<grid, C::THREADS, C::SMEM, s>>>(p, tmk, tmv);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_block_prefill(const BlockPrefillParams& p, int D, cudaStream_t s) {
-  const dim3 grid((p.max_q_len + 3) / 4, p.Hq, p.B);
-  auto kern = D == 64 ? block_prefill_kernel<64> : D == 128 ? block_prefill_kernel<128> : block_prefill_kernel<256>;
-  kern<<<grid, 128, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_block_prefill(BlockPrefillParams p, int D, cudaStream_t s) {
+  // the group's heads in as few equal parts of at most 128 as there can be; whole tokens per CTA
+  const int G = p.Hq / p.Hkv;
+  p.head_parts = (G + 127) / 128;
+  p.part_heads = (G + p.head_parts - 1) / p.head_parts;
+  const int tok = 128 / p.part_heads;
+  const long long y = static_cast<long long>(p.Hkv) * p.head_parts;
+  if (y > 65535) return cudaErrorInvalidValue;
+  const dim3 grid((p.max_q_len + tok - 1) / tok, static_cast<unsigned>(y), p.B);
+  if (p.window > 0)
+    return D == 64 ? launch_t<64, true>(p, grid, s) : D == 128 ? launch_t<128, true>(p, grid, s) : launch_t<256, true>(p, grid, s);
+  return D == 64 ? launch_t<64, false>(p, grid, s) : D == 128 ? launch_t<128, false>(p, grid, s) : launch_t<256, false>(p, grid, s);
 }
 
 }  // namespace fkv

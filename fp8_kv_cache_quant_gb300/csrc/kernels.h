@@ -112,9 +112,10 @@ struct BlockPrefillParams {
   int causal, window;
   __nv_bfloat16* out;
   int32_t* fault;
+  int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads
 };
 
-cudaError_t launch_block_prefill(const BlockPrefillParams& p, int D, cudaStream_t s);
+cudaError_t launch_block_prefill(BlockPrefillParams p, int D, cudaStream_t s);
 
 cudaError_t launch_prefill(const PrefillParams& p, int D, bool bf16_layer, void* k_cache, void* v_cache,
                            cudaStream_t s);
