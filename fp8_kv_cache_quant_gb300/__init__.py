@@ -1,7 +1,7 @@
 """Python binding of libfp8kv.so (FP8 KV-cache quantisation and FP8 attention, sm_103a).
 
-Argument marshalling only: every step of the computation runs in the library's CUDA
-kernels.  Tensors are torch CUDA tensors (used for device memory and streams); the
+Argument marshalling only (part of it compiled, csrc/binding.cpp): every step of the
+computation runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (used for device memory and streams); the
 C entry points receive their raw pointers.  The binding has the C ABI's names:
 ``kv_quant_cache``, ``fp8_decode_attn``, ``fp8_prefill_attn`` and the size queries; the rotary
 cache writes ``kv_rope_cache`` and ``kv_block_cache``; ``fp8_block_decode_attn`` and
@@ -65,6 +65,7 @@ class _Rope(ctypes.Structure):
 
 
 _lib = None
+_compiled = None
 
 
 def load_library(path: Optional[str] = None) -> ctypes.CDLL:
@@ -347,10 +348,6 @@ class Rope:
     cos_sin: torch.Tensor
     interleaved: bool = False
 
-    def c(self) -> _Rope:
-        t = self.cos_sin
-        return _Rope(t.data_ptr(), t.shape[0], t.shape[1], int(self.interleaved))
-
     @staticmethod
     def table(max_positions, rot_dim, base=10000.0, device="cuda"):
         """The table of angles p * base^(-2 i / rot_dim), evaluated in float64."""
@@ -376,68 +373,36 @@ class BlockCache:
                           *(torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)))
 
 
-# The checks below run before every launch, and a small call's time is host time: what passes costs a
-# few attribute reads, and messages are built only for what does not.
-
-def _refuse(fn, what):
-    raise ValueError(f"{fn}: {what}")
-
-
-def _check_tensors(fn, device, *wanted):
-    """Each (name, tensor or None, dtype, shape): contiguous, of that type and shape, on `device`."""
-    for name, t, dtype, shape in wanted:
-        if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
-            _refuse(fn, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}; "
-                        f"wanted {dtype} {tuple(shape)} on {device}, contiguous")
-
-
-def _rows(fn, device, name, t, n, heads, d):
-    """The token stride of a bf16 tensor [n][heads][d] whose rows are consecutive (a slice of a wider
-    projection's output serves)."""
-    if not (t.dtype is torch.bfloat16 and t.shape == (n, heads, d) and t.device == device):
-        _refuse(fn, f"{name} is {t.dtype} {tuple(t.shape)} on {t.device}; wanted torch.bfloat16 {(n, heads, d)} on {device}")
-    if n == 0:
-        return heads * d
-    s = t.stride()
-    if s[2] != 1 or (heads > 1 and s[1] != d):
-        _refuse(fn, f"{name}'s rows of {heads} x {d} elements are not consecutive (strides {s})")
-    return s[0] if n > 1 else heads * d
+def load_binding():
+    """The compiled part of this binding (_binding.so): the checks and calls of the functions below, whose
+    small calls are bound by the host."""
+    global _compiled
+    if _compiled is None:
+        load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"_binding.so not built ({e}); run __graft_entry__.build()") from e
+        _compiled = _binding
+    return _compiled
 
 
-def _launch(fn, device, stream, *args):
-    """The library's fn(*args, stream) with the tensors' device current; stream None: that device's current
-    stream."""
-    call = getattr(_lib or load_library(), fn)
-    index = device.index
+def _call(fn, on, stream, *args):
+    """fn of the compiled binding, with the device of the tensor `on` current; stream None: that device's current
+    stream.  Returns its tensor."""
+    index = on.get_device()
+    if index < 0:
+        raise ValueError(f"{fn}: the tensors are not on a CUDA device")
+    call = getattr(_compiled or load_binding(), fn)
     s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
     if index == torch._C._cuda_getDevice():
-        st = call(*args, s)
+        st, out = call(s, *args)
     else:
-        with torch.cuda.device(device):
-            st = call(*args, s)
+        with torch.cuda.device(index):
+            st, out = call(s, *args)
     if st != OK:
         _check(fn, st)
-
-
-def _device(fn, t):
-    """The CUDA device of t, whose number of dimensions is 3."""
-    if not t.is_cuda or t.dim() != 3:
-        _refuse(fn, f"a tensor of shape {tuple(t.shape)} on {t.device}; wanted [n][heads][head_dim] on a CUDA device")
-    return t.device
-
-
-def _query_rows(fn, device, q, q_out, n, d):
-    """(q, its stride, q_out, its stride, heads) as the entry points take them, and the output tensor, of
-    an optional query tensor [n][Hq][d]."""
-    if q is None:
-        if q_out is not None:
-            _refuse(fn, "q_out without q")
-        return (None, 0, None, 0, 0), None
-    hq = q.shape[1] if q.dim() == 3 else -1
-    stride = _rows(fn, device, "q", q, n, hq, d)
-    if q_out is None:
-        q_out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=device)
-    return (q.data_ptr(), stride, q_out.data_ptr(), _rows(fn, device, "q_out", q_out, n, hq, d), hq), q_out
+    return out
 
 
 def kv_rope_cache(q, k, v, positions, slot_mapping, rope: Rope, cache: LayerCache, k_scale=None, v_scale=None,
@@ -445,35 +410,10 @@ def kv_rope_cache(q, k, v, positions, slot_mapping, rope: Rope, cache: LayerCach
     """kv_quant_cache of K turned for its positions and of V, and the turned queries (bf16, returned; rows of
     skipped tokens are not written).  q, k, v: bf16 [n][heads][D], rows may be slices of a wider tensor; q may
     be None, q_out may be q.  positions, slot_mapping: int64 [n]."""
-    fn = "kv_rope_cache"
-    device = _device(fn, k)
-    n, h, d = k.shape
-    ks, vs = _rows(fn, device, "k", k, n, h, d), _rows(fn, device, "v", v, n, h, d)
-    qa, q_out = _query_rows(fn, device, q, q_out, n, d)
     mp, nl, keep = _mask_arg(skip_layer_mask)
-    pool_t = torch.bfloat16 if keep is not None and 0 <= layer < nl and keep[layer] else torch.uint8
-    pool = (cache.k_cache.shape[0], h, cache.k_cache.shape[2] if cache.k_cache.dim() == 4 else 16, d)
-    scales = (h if gran == SCALE_PER_HEAD else 1,)
-    cs = rope.cos_sin
-    _check_tensors(fn, device, ("positions", positions, torch.int64, (n,)), ("slot_mapping", slot_mapping, torch.int64, (n,)),
-                   ("k_cache", cache.k_cache, pool_t, pool), ("v_cache", cache.v_cache, pool_t, pool),
-                   ("k_scale", k_scale, torch.float32, scales), ("v_scale", v_scale, torch.float32, scales),
-                   ("cos_sin", cs, torch.float32, cs.shape if cs.dim() == 2 else (0, 0)), ("fault", fault, torch.int32, (1,)))
-    _launch(fn, device, stream, *qa, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(), slot_mapping.data_ptr(), n,
-            rope.c(), _LayerCache(cache.k_cache.data_ptr(), cache.v_cache.data_ptr(), pool[0], pool[2], h, d, cache.kv_format),
-            _ptr(k_scale), _ptr(v_scale), gran, layer, mp, nl, _ptr(fault))
-    del keep
-    return q_out
-
-
-def _block_cache(fn, device, cache, h, d):
-    """The C structure of a block-scaled cache of h KV heads and head_dim d."""
-    k = cache.k_cache
-    nb, bs = (k.shape[0], k.shape[2]) if k.dim() == 4 else (0, 16)
-    pool, scales = (nb, h, bs, d), (nb, h)
-    _check_tensors(fn, device, ("k_cache", k, torch.uint8, pool), ("v_cache", cache.v_cache, torch.uint8, pool),
-                   ("k_scale", cache.k_scale, torch.float32, scales), ("v_scale", cache.v_scale, torch.float32, scales))
-    return _BlockCache(k.data_ptr(), cache.v_cache.data_ptr(), cache.k_scale.data_ptr(), cache.v_scale.data_ptr(), nb, bs, h, d)
+    skipped = keep is not None and 0 <= layer < nl and bool(keep[layer])
+    return _call("kv_rope_cache", k, stream, q, k, v, positions, slot_mapping, rope.cos_sin, rope.interleaved, cache.k_cache,
+                 cache.v_cache, cache.kv_format, k_scale, v_scale, gran, layer, mp, nl, skipped, q_out, fault)
 
 
 def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, context_lens, rope: Optional[Rope] = None,
@@ -481,58 +421,26 @@ def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, 
     """Append each sequence's new tokens (rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k, v and q, the last of
     its context_lens[b] tokens) to a block-scaled cache, K and q turned for their positions when ``rope`` is
     given; returns the turned queries (None without q)."""
-    fn = "kv_block_cache"
-    device = _device(fn, k)
-    n, h, d = k.shape
-    ks, vs = _rows(fn, device, "k", k, n, h, d), _rows(fn, device, "v", v, n, h, d)
-    qa, q_out = _query_rows(fn, device, q, q_out, n, d)
-    b, mb = block_table.shape if block_table.dim() == 2 else (-1, 0)
-    cs = None if rope is None else rope.cos_sin
-    _check_tensors(fn, device, ("cu_seqlens", cu_seqlens, torch.int32, (b + 1,)), ("block_table", block_table, torch.int32, (b, mb)),
-                   ("context_lens", context_lens, torch.int32, (b,)), ("fault", fault, torch.int32, (1,)),
-                   ("cos_sin", cs, torch.float32, cs.shape if cs is not None and cs.dim() == 2 else (0, 0)))
-    c = _block_cache(fn, device, cache, h, d)
-    _launch(fn, device, stream, *qa, k.data_ptr(), ks, v.data_ptr(), vs, n, cu_seqlens.data_ptr(), b, max_q_len,
-            _Rope() if rope is None else rope.c(), c, block_table.data_ptr(), mb, context_lens.data_ptr(), _ptr(fault))
-    return q_out
-
-
-def _attn_args(fn, q, rows, cache, block_table, context_lens, out, fault):
-    device = _device(fn, q)
-    n, hq, d = q.shape
-    k = cache.k_cache
-    b, mb = block_table.shape if block_table.dim() == 2 else (-1, 0)
-    want = (n if rows is None else b, hq, d)
-    if out is None:
-        out = torch.empty(want, dtype=torch.bfloat16, device=device)
-    _check_tensors(fn, device, ("q", q, torch.bfloat16, want), ("out", out, torch.bfloat16, want),
-                   ("block_table", block_table, torch.int32, (b, mb)), ("context_lens", context_lens, torch.int32, (b,)),
-                   ("fault", fault, torch.int32, (1,)))
-    return device, out, _block_cache(fn, device, cache, k.shape[1] if k.dim() == 4 else 0, d), n, hq, b, mb
+    return _call("kv_block_cache", k, stream, k, v, cu_seqlens, max_q_len, cache.k_cache, cache.v_cache, cache.k_scale,
+                 cache.v_scale, block_table, context_lens, None if rope is None else rope.cos_sin,
+                 rope is not None and rope.interleaved, q, q_out, fault)
 
 
 def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softmax_scale=0.0, window=0, out=None,
                           workspace=None, num_splits=0, fault=None, stream=None):
     """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.  The
     workspace is fp8_decode_attn's (``decode_workspace`` makes one; zero-filled before its first call)."""
-    fn = "fp8_block_decode_attn"
-    device, out, c, _, hq, b, mb = _attn_args(fn, q, "batch", cache, block_table, context_lens, out, fault)
     if workspace is None:
-        n = fp8_decode_attn_workspace_size(b, hq, c.num_kv_heads, c.head_dim, mb, window, num_splits)
-        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        _refuse(fn, f"workspace on {workspace.device}; wanted contiguous on {device}")
-    _launch(fn, device, stream, q.data_ptr(), b, hq, c, block_table.data_ptr(), mb, context_lens.data_ptr(), softmax_scale,
-            window, out.data_ptr(), workspace.data_ptr(), workspace.nbytes, num_splits, _ptr(fault))
-    return out
+        b, mb = block_table.shape
+        _, h, _, d = cache.k_cache.shape
+        n = fp8_decode_attn_workspace_size(b, q.shape[1], h, d, mb, window, num_splits)
+        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+    return _call("fp8_block_decode_attn", q, stream, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
+                 context_lens, softmax_scale, window, out, workspace, num_splits, fault)
 
 
 def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_table, context_lens, softmax_scale=0.0,
                            causal=True, window=0, out=None, fault=None, stream=None):
     """Ragged chunks of queries (rows cu_seqlens_q[b] .. of q bf16 [total][Hq][D]) over a block-scaled cache."""
-    fn = "fp8_block_prefill_attn"
-    device, out, c, n, hq, b, mb = _attn_args(fn, q, None, cache, block_table, context_lens, out, fault)
-    _check_tensors(fn, device, ("cu_seqlens_q", cu_seqlens_q, torch.int32, (b + 1,)))
-    _launch(fn, device, stream, q.data_ptr(), cu_seqlens_q.data_ptr(), n, b, hq, max_q_len, c, block_table.data_ptr(), mb,
-            context_lens.data_ptr(), softmax_scale, bool(causal), window, out.data_ptr(), _ptr(fault))
-    return out
+    return _call("fp8_block_prefill_attn", q, stream, q, cu_seqlens_q, max_q_len, cache.k_cache, cache.v_cache, cache.k_scale,
+                 cache.v_scale, block_table, context_lens, softmax_scale, causal, window, out, fault)

@@ -157,25 +157,71 @@ def test_binding_refuses_cpu_tensors():
         f.fp8_block_prefill_attn(k, i, 1, cache, table, i[:1])
 
 
-def test_binding_row_strides():
-    dev = torch.device("cpu")
-    wide = torch.zeros(5, 3 * 128, dtype=torch.bfloat16)
-    assert f._rows("f", dev, "k", wide[:, 128:256].view(5, 2, 64), 5, 2, 64) == 384
-    assert f._rows("f", dev, "k", wide[:1, :128].view(1, 2, 64), 1, 2, 64) >= 128
-    assert f._rows("f", dev, "k", wide[:0, :128].view(0, 2, 64), 0, 2, 64) == 128
-    for bad in (wide[:, ::2].unflatten(1, (3, 64))[:, :2], wide.view(5, 6, 64)[:, ::3], wide.float()[:, :128].view(5, 2, 64),
-                wide[:, :128].view(5, 2, 64)[:4]):
-        with pytest.raises(ValueError):
-            f._rows("f", dev, "k", bad, 5, 2, 64)
+def _bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
 
 
-def test_binding_tensor_checks():
-    dev = torch.device("cpu")
-    t = torch.zeros(4, 6, dtype=torch.int32)
-    f._check_tensors("f", dev, ("t", t, torch.int32, (4, 6)), ("u", None, torch.int32, (1,)))
-    for bad in (t.long(), t[:3], t.T, torch.zeros(4, 12, dtype=torch.int32)[:, ::2], t[0]):
-        with pytest.raises(ValueError, match="f: t is"):
-            f._check_tensors("f", dev, ("t", bad, torch.int32, (4, 6)))
+def _refused(fn, match, args, **change):
+    """The compiled binding refuses the arguments with `change` made (on the CPU: nothing is launched)."""
+    a = dict(args)
+    a.update(change)
+    with pytest.raises(ValueError, match=match):
+        getattr(f.load_binding(), fn)(0, *a.values())
+
+
+def test_compiled_binding_checks_of_the_writes(lib):
+    i64 = torch.zeros(5, dtype=torch.int64)
+    pool, s, t = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.ones(1), torch.zeros(9, 64)
+    wide = _bf(5, 3 * 128)
+    a = dict(q=_bf(5, 4, 64), k=wide[:, 128:256].view(5, 2, 64), v=_bf(5, 2, 64), pos=i64, slots=i64, cs=t, il=0, kc=pool, vc=pool,
+             fmt=0, ks=s, vs=s, gran=0, layer=0, mask=None, nl=0, skip=0, qo=None, fault=None)
+    for match, change in [
+        ("positions is Int", dict(pos=i64.int())), (r"positions is Long \[4\]", dict(pos=i64[:4])), ("slot_mapping", dict(slots=i64[:0])),
+        ("k's rows are not consecutive", dict(k=wide[:, ::2].unflatten(1, (3, 64))[:, :2])), ("v's rows", dict(v=wide.view(5, 6, 64)[:, ::3])),
+        ("k is Float", dict(k=torch.zeros(5, 2, 64))), ("v is BFloat16", dict(v=_bf(4, 2, 64))), ("q is BFloat16", dict(q=_bf(5, 4, 32))),
+        ("q is", dict(q=_bf(5, 256))), ("q_out without q", dict(q=None, qo=_bf(5, 4, 64))), ("q_out is", dict(qo=_bf(5, 4, 64).float())),
+        ("q_out's rows", dict(qo=_bf(5, 64, 4).transpose(1, 2))), ("k_cache is Byte", dict(skip=1)), ("v_cache", dict(vc=pool[:2])),
+        ("k_cache is Byte .*not contiguous", dict(kc=torch.zeros(3, 16, 2, 64, dtype=torch.uint8).transpose(1, 2))),
+        ("k_cache", dict(kc=pool[0])), (r"wanted Float \[2\]", dict(gran=1)), ("v_scale is Double", dict(vs=s.double())),
+        ("cos_sin", dict(cs=t.half())), ("cos_sin", dict(cs=t[0])), ("fault", dict(fault=i64)), ("not a tensor", dict(v=3)),
+        ("not a tensor", dict(v=None)), ("32 bits", dict(layer=1 << 40)),
+    ]:
+        _refused("kv_rope_cache", match, a, **change)
+    i32 = torch.zeros(3, dtype=torch.int32)
+    c = dict(k=_bf(5, 2, 64), v=_bf(5, 2, 64), cu=i32, mx=3, kc=pool, vc=pool, ks=torch.ones(3, 2), vs=torch.ones(3, 2),
+             tab=torch.zeros(2, 4, dtype=torch.int32), ctx=i32[:2], cs=t, il=0, q=None, qo=None, fault=None)
+    for match, change in [
+        ("cu_seqlens", dict(cu=i32[:2])), ("cu_seqlens is Long", dict(cu=i32.long())), ("block_table", dict(tab=i32)),
+        ("block_table is Int .*not contiguous", dict(tab=torch.zeros(4, 2, dtype=torch.int32).T)), ("context_lens", dict(ctx=i32)),
+        ("k_scale", dict(ks=torch.ones(3, 1))), ("v_scale", dict(vs=torch.ones(2, 2))), ("k_cache", dict(k=_bf(5, 3, 64), v=_bf(5, 3, 64))),
+        ("v_cache", dict(vc=pool.view(torch.int8))), ("fault", dict(fault=torch.zeros(2, dtype=torch.int32))), ("cos_sin", dict(cs=t.T)),
+        ("k is", dict(k=_bf(5, 128))),
+    ]:
+        _refused("kv_block_cache", match, c, **change)
+    with pytest.raises(TypeError):
+        f.load_binding().kv_block_cache(0, *dict(c, mx="3").values())
+    for n in (3, 20):
+        with pytest.raises(ValueError, match="arguments"):
+            f.load_binding().kv_block_cache(0, *(list(c.values()) * 2)[:n])
+
+
+def test_compiled_binding_checks_of_the_attention(lib):
+    pool, s, i32 = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.ones(3, 2), torch.zeros(3, dtype=torch.int32)
+    tab = torch.zeros(2, 4, dtype=torch.int32)
+    d = dict(q=_bf(2, 4, 64), kc=pool, vc=pool, ks=s, vs=s, tab=tab, ctx=i32[:2], sm=0.0, win=0, out=None,
+             ws=torch.zeros(1 << 16, dtype=torch.uint8), ns=0, fault=None)
+    for match, change in [
+        ("q is BFloat16 .3, 4, 64", dict(q=_bf(3, 4, 64))), ("q is Half", dict(q=_bf(2, 4, 64).half())), ("out is", dict(out=_bf(2, 4, 32))),
+        ("k_cache", dict(q=_bf(2, 4, 128))), ("q is", dict(q=_bf(4, 2, 64).transpose(0, 1))), ("workspace", dict(ws=torch.zeros(8, 8)[:, ::2])),
+        ("context_lens", dict(ctx=i32)), ("block_table", dict(tab=tab.long())), ("v_scale", dict(vs=s.T.contiguous())),
+    ]:
+        _refused("fp8_block_decode_attn", match, d, **change)
+    p = dict(q=_bf(5, 4, 64), cu=i32, mx=3, kc=pool, vc=pool, ks=s, vs=s, tab=tab, ctx=i32[:2], sm=0.0, causal=1, win=0, out=None, fault=None)
+    for match, change in [
+        ("q is", dict(q=_bf(4, 5, 64).transpose(0, 1))), ("cu_seqlens_q", dict(cu=i32[:2])), ("out is", dict(out=_bf(6, 4, 64))),
+        ("32 bits", dict(mx=1 << 31)), ("fault", dict(fault=i32)), ("not a tensor", dict(cu=None)),
+    ]:
+        _refused("fp8_block_prefill_attn", match, p, **change)
 
 
 def test_rope_table():
@@ -183,5 +229,3 @@ def test_rope_table():
     assert t.shape == (7, 32) and t.dtype is torch.float32
     assert torch.equal(t[0], torch.cat((torch.ones(16), torch.zeros(16))))
     assert abs(float(t[3, 1]) - torch.cos(torch.tensor(3.0 * 10000.0 ** (-2 / 32), dtype=torch.float64)).item()) < 2 ** -24
-    r = f.Rope(t, interleaved=True).c()
-    assert (r.max_positions, r.rot_dim, r.interleaved) == (7, 32, 1)
