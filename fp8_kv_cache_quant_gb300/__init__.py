@@ -36,7 +36,7 @@ EXPORTS = (
     "fp8_decode_attn_num_splits", "fp8_decode_attn", "fkv_prefill_block_n", "fp8_prefill_attn",
     "fp8_decode_attn_noalloc", "fp8_decode_attn_split_blocks", "fkv_decode_block_n", "kv_quant_cache_clips",
     "fp8_decode_step", "fkv_set_decode_wait_limit_ns", "kv_rope_cache", "kv_block_cache",
-    "fp8_block_decode_attn", "fp8_block_prefill_attn",
+    "fp8_block_decode_attn_workspace_size", "fp8_block_decode_attn", "fp8_block_prefill_attn",
 )
 NOALLOC_WORKSPACE_BYTES = 16 << 20
 
@@ -121,7 +121,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                                    _Rope, _BlockCache, c_vp, c_i32, c_vp, c_vp, c_vp]
     lib.fp8_block_decode_attn.restype = ctypes.c_int
     lib.fp8_block_decode_attn.argtypes = [c_vp, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f, c_i32, c_vp, c_vp,
-                                          c_sz, c_i32, c_vp, c_vp]
+                                          c_sz, c_vp, c_vp]
+    lib.fp8_block_decode_attn_workspace_size.restype = c_sz
+    lib.fp8_block_decode_attn_workspace_size.argtypes = [c_i32] * 4
     lib.fp8_block_prefill_attn.restype = ctypes.c_int
     lib.fp8_block_prefill_attn.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f,
                                            c_i32, c_i32, c_vp, c_vp, c_vp]
@@ -426,17 +428,28 @@ def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, 
                  rope is not None and rope.interleaved, q, q_out, fault)
 
 
+def fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim) -> int:
+    return int(load_library().fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim))
+
+
+def block_decode_workspace(batch, num_q_heads, cache: BlockCache):
+    """A zero-filled workspace of fp8_block_decode_attn (calls that may overlap on the GPU each need one)."""
+    if not cache.k_cache.is_cuda:
+        raise ValueError("fp8_block_decode_attn: the tensors are not on a CUDA device")
+    _, h, _, d = cache.k_cache.shape
+    with torch.cuda.device(cache.k_cache.device):
+        n = fp8_block_decode_attn_workspace_size(batch, num_q_heads, h, d)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k_cache.device)
+
+
 def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softmax_scale=0.0, window=0, out=None,
-                          workspace=None, num_splits=0, fault=None, stream=None):
-    """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.  The
-    workspace is fp8_decode_attn's (``decode_workspace`` makes one; zero-filled before its first call)."""
+                          workspace=None, fault=None, stream=None):
+    """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.
+    ``workspace``: of block_decode_workspace (one is made for the call when None)."""
     if workspace is None:
-        b, mb = block_table.shape
-        _, h, _, d = cache.k_cache.shape
-        n = fp8_decode_attn_workspace_size(b, q.shape[1], h, d, mb, window, num_splits)
-        workspace = torch.zeros(max(n, 256), dtype=torch.uint8, device=q.device)
+        workspace = block_decode_workspace(q.shape[0], q.shape[1], cache)
     return _call("fp8_block_decode_attn", q, stream, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
-                 context_lens, softmax_scale, window, out, workspace, num_splits, fault)
+                 context_lens, softmax_scale, window, out, workspace, fault)
 
 
 def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_table, context_lens, softmax_scale=0.0,

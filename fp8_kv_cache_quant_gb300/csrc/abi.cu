@@ -102,17 +102,6 @@ bool plan_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_bloc
   return true;
 }
 
-// The split plan and its workspace: the split-completion counters first (zero between calls), then
-// the splits' log-sum-exps and normalised outputs (written before they are read).
-void place_workspace(const DecodePlan& plan, void* workspace, DecodeParams* p) {
-  uint8_t* at = static_cast<uint8_t*>(workspace);
-  p->bps = plan.bps;
-  p->max_splits = plan.max_splits;
-  p->done = reinterpret_cast<int32_t*>(at);
-  p->lse_part = reinterpret_cast<float*>(at + plan.cnt_bytes);
-  p->o_part = reinterpret_cast<float*>(at + plan.cnt_bytes + plan.lse_bytes);
-}
-
 fkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FKV_OK : FKV_CUDA_ERROR; }
 
 // Bound of the tensor-core decode's pipeline waits set by fkv_set_decode_wait_limit_ns;
@@ -166,6 +155,26 @@ fkv_status check_block_cache(const fkv_block_cache& c) {
 bool valid_block_pools(const fkv_block_cache& c) {
   return c.k_cache && c.v_cache && c.k_scale && c.v_scale && aligned(c.k_cache, 16) && aligned(c.v_cache, 16) &&
          aligned(c.k_scale, 4) && aligned(c.v_scale, 4);
+}
+
+// The block-scaled decode: CTAs resident at once, of which a unit (sequence, KV head) is given at
+// most 160 (the merge of its pieces grows with them: 0.05 us each, a tile of its own 1.5 us), and the
+// workspace: piece counters, the pieces' log-sum-exps and outputs.
+struct BlockDecodePlan {
+  long long ctas = 0;
+  size_t cnt_bytes = 0, lse_bytes = 0, o_bytes = 0;
+};
+
+BlockDecodePlan plan_block_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
+  const int G = Hq / Hkv;
+  const long long units = static_cast<long long>(B) * Hkv;
+  BlockDecodePlan plan;
+  plan.ctas = std::min<long long>(static_cast<long long>(current_num_sms()) * fkv::block_decode_ctas_per_sm(D, G), 160 * units);
+  const size_t rows = static_cast<size_t>(plan.ctas + units) * G;
+  plan.cnt_bytes = align256(units * sizeof(int32_t));
+  plan.lse_bytes = align256(rows * sizeof(float));
+  plan.o_bytes = rows * D * sizeof(float);
+  return plan;
 }
 
 float base2_scale(float softmax_scale, int32_t head_dim) {
@@ -243,7 +252,13 @@ fkv_status decode_entry(const void* k_new, const void* v_new, const void* q, int
   const float tau = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(cache.head_dim));
   p.sm_scale_log2 = tau * 1.4426950408889634f;
   p.window = window;
-  place_workspace(plan, workspace, &p);
+  p.bps = plan.bps;
+  p.max_splits = plan.max_splits;
+  // workspace: the split-completion counters first (zero between calls), then the
+  // splits' log-sum-exps and normalised outputs (written before they are read)
+  p.done = static_cast<int32_t*>(workspace);
+  p.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cnt_bytes);
+  p.o_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan.cnt_bytes + plan.lse_bytes);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
@@ -525,11 +540,19 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
   return from_cuda(fkv::launch_block_cache(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t fp8_block_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim) {
+  if (batch <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads != 0) return 0;
+  if (!supported_head_dim(head_dim) || !supported_group(num_q_heads / num_kv_heads, head_dim)) return 0;
+  const BlockDecodePlan plan = plan_block_decode(batch, num_q_heads, num_kv_heads, head_dim);
+  return plan.cnt_bytes + plan.lse_bytes + plan.o_bytes;
+}
+
 fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
                                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
                                  float softmax_scale, int32_t window, void* out, void* workspace,
-                                 size_t workspace_bytes, int32_t num_splits, int32_t* fault, fkv_stream_t stream) {
-  if (batch < 0 || num_q_heads <= 0 || max_blocks <= 0 || window < 0 || num_splits < 0) return FKV_INVALID_ARG;
+                                 size_t workspace_bytes, int32_t* fault, fkv_stream_t stream) {
+  if (batch < 0 || num_q_heads <= 0 || max_blocks <= 0 || window < 0) return FKV_INVALID_ARG;
   const fkv_status st = check_block_cache(cache);
   if (st != FKV_OK) return st;
   if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
@@ -541,20 +564,18 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   if (!q || !out || !block_table || !context_lens || !valid_block_pools(cache)) return FKV_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4))
     return FKV_INVALID_ARG;
-  DecodePlan plan;
-  if (!plan_decode(batch, num_q_heads, cache.num_kv_heads, cache.head_dim, max_blocks, window, num_splits, &plan))
-    return FKV_UNSUPPORTED;
-  const size_t need = plan.o_bytes + plan.lse_bytes + plan.cnt_bytes;
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FKV_INVALID_ARG;
-  DecodeParams p;
+  const BlockDecodePlan plan = plan_block_decode(batch, num_q_heads, cache.num_kv_heads, cache.head_dim);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.cnt_bytes + plan.lse_bytes + plan.o_bytes)
+    return FKV_INVALID_ARG;
+  fkv::BlockDecodeParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
   p.v_cache = static_cast<const uint8_t*>(cache.v_cache);
-  p.block_table = block_table;
-  p.context_lens = context_lens;
   p.k_scale = cache.k_scale;
   p.v_scale = cache.v_scale;
+  p.block_table = block_table;
+  p.ctx = context_lens;
   p.B = batch;
   p.Hq = num_q_heads;
   p.Hkv = cache.num_kv_heads;
@@ -562,11 +583,18 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   p.max_blocks = max_blocks;
   p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
   p.window = window;
-  place_workspace(plan, workspace, &p);
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  p.done = reinterpret_cast<int32_t*>(at);
+  p.lse_part = reinterpret_cast<float*>(at + plan.cnt_bytes);
+  p.o_part = reinterpret_cast<float*>(at + plan.cnt_bytes + plan.lse_bytes);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
-  p.pipe_wait_ns = kDefaultPipeWaitNs;
-  return from_cuda(fkv::launch_block_decode(p, cache.head_dim, G, reinterpret_cast<cudaStream_t>(stream)));
+  // no more CTAs than there can be places (a unit's tiles and the blank one that leads them)
+  const long long blocks = window > 0 ? std::min<long long>(max_blocks, (window + 15LL) / 16 + 1) : max_blocks;
+  const int tpb = fkv::block_decode_tile_blocks(cache.head_dim);
+  const long long tiles = static_cast<long long>(batch) * cache.num_kv_heads * ((blocks + tpb - 1) / tpb + 1);
+  const int ctas = static_cast<int>(std::min(plan.ctas, tiles));
+  return from_cuda(fkv::launch_block_decode(p, cache.head_dim, ctas, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,

@@ -242,8 +242,7 @@ PyObject* kv_block_cache_(Args a) {
   return result(st, q.out);
 }
 
-// stream, q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, softmax_scale, window, out, workspace,
-// num_splits, fault
+// stream, q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, softmax_scale, window, out, workspace, fault
 PyObject* fp8_block_decode_attn_(Args a) {
   void* stream = a.pointer();
   const Tensor q = three_dims(a, "q");
@@ -254,7 +253,6 @@ PyObject* fp8_block_decode_attn_(Args a) {
   const int32_t window = a.i32();
   Tensor out = a.tensor("out", true);
   const Tensor workspace = a.tensor("workspace");
-  const int32_t num_splits = a.i32();
   const Tensor fault = a.tensor("fault", true);
   a.done();
   if (table.dim() != 2) refuse(a.fn, "block_table is " + text(table) + "; wanted [batch][blocks]");
@@ -266,7 +264,7 @@ PyObject* fp8_block_decode_attn_(Args a) {
       src, small(a.fn, b), small(a.fn, hq), c,
       fits<int32_t>(a.fn, "block_table", table, at::kInt, table.sizes(), dev), small(a.fn, table.size(1)),
       fits<int32_t>(a.fn, "context_lens", ctx, at::kInt, {b}, dev), softmax_scale, window,
-      fits(a.fn, "out", out, at::kBFloat16, {b, hq, d}, dev), workspace.data_ptr(), workspace.nbytes(), num_splits,
+      fits(a.fn, "out", out, at::kBFloat16, {b, hq, d}, dev), workspace.data_ptr(), workspace.nbytes(),
       fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev), static_cast<fkv_stream_t>(stream));
   return result(st, out);
 }

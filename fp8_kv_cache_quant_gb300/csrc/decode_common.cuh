@@ -106,7 +106,7 @@ FKV_DEV void merge_splits(const DecodeParams& p, int b, int g, int ns, float vs,
       // the weights summed pairwise in the order of a warp's butterfly over eight lanes,
       // as the general path below sums them
       const float W = ((w[0] + w[4]) + (w[2] + w[6])) + ((w[1] + w[5]) + (w[3] + w[7]));
-      const float inv = (W != 0.f) ? vs / W : 0.f;  // (a NaN weight stays one)
+      const float inv = (W > 0.f) ? vs / W : 0.f;
       __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + (static_cast<size_t>(b) * p.Hq + g * G + h) * D + d);
       dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
       dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
@@ -135,7 +135,7 @@ FKV_DEV void merge_splits(const DecodeParams& p, int b, int g, int ns, float vs,
     for (int off = 16; off > 0; off >>= 1) W += __shfl_xor_sync(0xffffffffu, W, off);
     if (lane == 0) {
       ms_s[h] = M;
-      inv_s[h] = (W != 0.f) ? vs / W : 0.f;
+      inv_s[h] = (W > 0.f) ? vs / W : 0.f;
     }
   }
   constexpr int U = 16;                              // split partials loaded before use

@@ -46,17 +46,12 @@
 namespace fkv {
 namespace {
 
-// BLK: a block-scaled cache (fp8_block_decode_attn); otherwise e4m3 layers with one scale per
-// tensor or head.
-template <int D, int G, bool BLK>
+template <int D, int G>
 struct DecodeTcCfg {
   static constexpr int BN = D == 64 ? 256 : 128;  // keys per tile (the P rounding's tile)
   static constexpr int TPB = BN / 16;             // pool blocks per tile
   static constexpr int NHALF = BN / 128;          // S^T products (M = 128 keys each) per tile
-  // query heads padded to the MMA's N; BLK: head h's leading term is row (column) h, its
-  // residual row LO + h
-  static constexpr int NP = BLK && G > 8 ? 32 : 16;
-  static constexpr int LO = NP / 2;
+  static constexpr int NP = 16;                // query heads padded to the MMA's N
   static constexpr int RB = D < 128 ? D : 128; // bytes of one swizzled row
   static constexpr int SWZ = RB == 128 ? 2 : 4;  // descriptor swizzle mode (128 / 64 bytes)
   static constexpr int NSUB = D / RB;          // column blocks of a K / V row
@@ -69,19 +64,19 @@ struct DecodeTcCfg {
   static constexpr int PTILE = NP * BN;        // bytes of one P8^T tile: NHALF sub-tiles [NP][128 keys]
   static constexpr int TM_S = 0;               // S^T buffers: TMEM columns [0, 2 * NHALF * NP)
   static constexpr int TM_O = 2 * NHALF * NP;  // O_tile^T buffers: [TM_O, TM_O + 2 * NSUB * NP)
-  static constexpr int SLD = BLK ? NP : (D == 64 && G <= 8) ? 8 : 16;  // S^T columns a softmax thread loads
+  static constexpr int SLD = (D == 64 && G <= 8) ? 8 : 16;  // S^T columns a softmax thread loads
   // block ids of the split staged in shared memory once (head_dim 128 and 256); at head_dim
   // 64, whose three CTAs per SM leave no room for them, each copying lane reads its block's
   // id one tile ahead of the copy
   static constexpr bool STAGE_IDS = D != 64;
-  static constexpr int TM_COLS = TM_O + 2 * NSUB * NP <= 64 ? 64 : TM_O + 2 * NSUB * NP <= 128 ? 128 : 256;
+  static constexpr int TM_COLS = TM_O + 2 * NSUB * NP <= 64 ? 64 : 128;
   // shared memory (bytes; tiles on 1024-byte boundaries for the 128-byte swizzle)
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + NS * KTILE;
   static constexpr int OFF_Q = OFF_V + NS * KTILE;
   static constexpr int OFF_P = OFF_Q + NSUB * QSUB;  // two P8^T tiles
   static constexpr int OFF_RED = OFF_P + 2 * PTILE;  // [2][4 warps][NP] floats
-  static constexpr int OFF_A = OFF_RED + 2 * 4 * NP * 4;  // alpha (BLK: and beta) [2][NP]; then m, l [2][NP]
+  static constexpr int OFF_A = OFF_RED + 2 * 4 * NP * 4;  // alpha [2][NP]; then m, l [2][NP]
   static constexpr int OFF_BAR = OFF_A + 4 * NP * 4;
   static constexpr int NBAR = 21 + 4 * NS;
   static constexpr int OFF_IDS = OFF_BAR + NBAR * 8;     // [MAX_BPS] block ids of the split (STAGE_IDS)
@@ -91,8 +86,7 @@ struct DecodeTcCfg {
   static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(MPV, NP, 1, 0);  // V8 MN-major, P8 K-major
   // merge scratch (in the K stages, free by then): 2 G + G * CH floats
   static constexpr int CH = (NS * KTILE / 4 - 2 * G) / G < 256 ? (NS * KTILE / 4 - 2 * G) / G : 256;
-  static_assert(G >= 1 && G <= (BLK ? LO : NP), "query heads per KV head");
-  static_assert(!BLK || G + 1 <= NP, "the tile's largest V scale rides with the heads' maxima");
+  static_assert(G >= 1 && G <= NP, "query heads per KV head");
   static_assert(D == 64 || D == 128 || D == 256, "head_dim");
   static_assert(MAX_BPS % TPB == 0 && TPB * NS <= 32, "whole tiles per split; the prologue's ids in one warp");
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
@@ -144,19 +138,11 @@ FKV_DEV float warp_max(float v) {
   return r;
 }
 
-// A float as two e4m3 terms: `hi` keeps the leading 3 fraction bits, `lo` is 16 times the rest, so
-// that hi + lo / 16 has 8 significant bits once both are rounded to e4m3.  Below e4m3's least
-// normal number everything goes to `lo`.  |x| <= 256, so that lo <= 448.
-FKV_DEV void two_terms(float x, float& hi, float& lo) {
-  hi = fabsf(x) >= 0.015625f ? __uint_as_float(__float_as_uint(x) & 0xFFF00000u) : 0.f;
-  lo = (x - hi) * 16.f;
-}
-
-template <int D, int G, bool BLK>
+template <int D, int G>
 __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1)
     decode_tc_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv) {
-  using C = DecodeTcCfg<D, G, BLK>;
+  using C = DecodeTcCfg<D, G>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem + C::OFF_K;
@@ -273,7 +259,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
   const int n0 = min(C::NS, n_t);  // tiles whose copies go out in the prologue
   // fp8_decode_step: the split holding position T - 1 (the last) writes the current token
   // into the pools before its first copy of that block (not when the context was clamped)
-  if (!BLK && warp == 8 && p.k_new != nullptr && sigma == r.nsplit - 1 && !r.clamped) write_current_token<D>(p, b, g, T, lane);
+  if (warp == 8 && p.k_new != nullptr && sigma == r.nsplit - 1 && !r.clamped) write_current_token<D>(p, b, g, T, lane);
   if (warp == 8) {
     __syncwarp();
     int id = 0;  // block `lane` of the split
@@ -309,78 +295,9 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
     // ============================================================ softmax warpgroup
     const int i = threadIdx.x;  // key i of a tile (TMEM lane i)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    float cst[G];  // log2(e) * softmax scale * the query's scale (* k_s[g] when it is one per head)
     // ---- prologue: the G query rows -> e4m3 codes in the swizzled Q8 tile (rows G..15
     // zero), and the padding rows of both P8^T tiles zeroed once
-    if constexpr (BLK) {
-      // Row h scaled by the power of two that brings its largest magnitude into [128, 256), in two
-      // terms: a bf16 value has 8 significant bits, so the terms hold it exactly down to 2^-20 of
-      // the row's largest.  A row with a NaN or an infinity makes its scores, and so its output, NaN.
-      constexpr int NCH = (D / 16 + 7) / 8;  // 16-element chunks per thread
-      const int row = i >> 3;
-      uint32_t in[NCH][8];
-      uint32_t amax = 0;
-#pragma unroll
-      for (int cc = 0; cc < NCH; ++cc) {
-        const int c = (i & 7) + 8 * cc;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
-        if (row < G && c < D / 16) {
-          const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(b) * p.Hq + g * G + row) * D) + 2 * c;
-          const uint4 a = src[0], a2 = src[1];
-          in[cc][0] = a.x; in[cc][1] = a.y; in[cc][2] = a.z; in[cc][3] = a.w;
-          in[cc][4] = a2.x; in[cc][5] = a2.y; in[cc][6] = a2.z; in[cc][7] = a2.w;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
-      }
-#pragma unroll
-      for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-      const int k = max(static_cast<int>(amax >> 23) - 127 - 7, -126);  // q = q' * 2^k
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      if ((i & 7) == 0 && row < G)
-        ml_s[row] = amax < 0x7F800000u ? __uint_as_float(static_cast<uint32_t>(127 + k) << 23) : __uint_as_float(0x7FC00000u);
-#pragma unroll
-      for (int cc = 0; cc < NCH; ++cc) {
-        const int c = (i & 7) + 8 * cc;
-        if (c >= D / 16) continue;
-        uint32_t wh[4], wl[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
-          float h0, h1, h2, h3, l0, l1, l2, l3;
-          two_terms(x0.x * down, h0, l0);
-          two_terms(x0.y * down, h1, l1);
-          two_terms(x1.x * down, h2, l2);
-          two_terms(x1.y * down, h3, l3);
-          wh[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(h0, h1)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(h2, h3)) << 16);
-          wl[j] = static_cast<uint32_t>(f32x2_to_e4m3x2(l0, l1)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(l2, l3)) << 16);
-        }
-        const int byte = c * 16;
-        uint8_t* sub = sQ + (byte / C::RB) * C::QSUB;
-        if (row < C::LO) {
-          *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>(row * C::RB + byte % C::RB), C::RB)) =
-              make_uint4(wh[0], wh[1], wh[2], wh[3]);
-          *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>((C::LO + row) * C::RB + byte % C::RB), C::RB)) =
-              make_uint4(wl[0], wl[1], wl[2], wl[3]);
-        }
-      }
-      if constexpr (G < C::LO) {
-        // rows G .. LO - 1 and LO + G .. NP - 1 of both P8^T tiles (every sub-tile)
-        constexpr int PAD = 2 * (C::LO - G) * 8;  // 16-byte chunks
-        for (int x = i; x < 2 * C::NHALF * PAD; x += 128) {
-          const int sub = x / PAD, rem = x % PAD;
-          const int r8 = rem / 8, prow = r8 < C::LO - G ? G + r8 : C::LO + G + (r8 - (C::LO - G));
-          *reinterpret_cast<uint4*>(sP + (sub / C::NHALF) * C::PTILE + (sub % C::NHALF) * (C::NP * 128) + prow * 128 +
-                                    (rem % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive_warp(q_full);
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // the rows' scales are in ml_s
-#pragma unroll
-      for (int h = 0; h < G; ++h) cst[h] = p.sm_scale_log2 * ml_s[h];
-    } else {
+    {
       const int row = i >> 3;
 #pragma unroll
       for (int c = i & 7; c < D / 16; c += 8) {
@@ -415,34 +332,10 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       fence_proxy_async_smem();
       mbar_arrive_warp(q_full);
     }
-    if constexpr (!BLK) {
+    float cst[G];  // log2(e) * softmax scale * q_s[h] * k_s[g]
 #pragma unroll
-      for (int h = 0; h < G; ++h)
-        cst[h] = p.sm_scale_log2 * p.q_scale[p.per_head ? g * G + h : 0] * p.k_scale[p.per_head ? g : 0];
-    }
-    // BLK: the scales of this thread's keys' blocks, read one tile ahead, and their block ids, two
-    // tiles ahead (blocks past the split: scale 0)
-    float ks_next[C::NHALF], vs_next[C::NHALF];
-    int id_next[C::NHALF] = {};
-    auto read_id = [&](int t, int hh) -> int {
-      const int j = TPB * t + 8 * hh + (i >> 4);
-      if (j >= be - bb) return -1;
-      const int id = C::STAGE_IDS ? ids_s[j] : p.block_table[static_cast<size_t>(b) * p.max_blocks + bb + j];
-      return id >= 0 && id < p.num_blocks ? id : 0;  // (reported where the block is copied)
-    };
-    auto read_scales = [&](int hh) {
-      const size_t at = static_cast<size_t>(max(id_next[hh], 0)) * p.Hkv + g;
-      ks_next[hh] = id_next[hh] >= 0 ? p.k_scale[at] : 0.f;
-      vs_next[hh] = id_next[hh] >= 0 ? p.v_scale[at] : 0.f;
-    };
-    if constexpr (BLK) {
-#pragma unroll
-      for (int hh = 0; hh < C::NHALF; ++hh) {
-        id_next[hh] = read_id(0, hh);
-        read_scales(hh);
-        id_next[hh] = read_id(1, hh);
-      }
-    }
+    for (int h = 0; h < G; ++h)
+      cst[h] = p.sm_scale_log2 * p.q_scale[p.per_head ? g * G + h : 0] * p.k_scale[p.per_head ? g : 0];
     float m[G], lsum[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) {
@@ -461,7 +354,6 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       for (int hh = 0; hh < NH2; ++hh) {
         const uint32_t col = lane_base + C::TM_S + (sb * NH2 + hh) * C::NP;
         if constexpr (C::SLD == 8) tmem_ld8(col, sv[hh]);
-        else if constexpr (C::SLD == 32) tmem_ld32(col, sv[hh]);
         else tmem_ld16(col, sv[hh]);
       }
       tmem_ld_wait();
@@ -469,16 +361,6 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       mbar_arrive_warp(&s_free[sb]);
       bool valid[NH2];
       float x[NH2][G], wm[G];
-      float ks[NH2], vs[NH2];  // BLK
-      if constexpr (BLK) {
-#pragma unroll
-        for (int hh = 0; hh < NH2; ++hh) {
-          ks[hh] = ks_next[hh];
-          vs[hh] = vs_next[hh];
-          read_scales(hh);
-          id_next[hh] = read_id(t + 2, hh);
-        }
-      }
 #pragma unroll
       for (int hh = 0; hh < NH2; ++hh) {
         const int key = (bb + TPB * t) * 16 + 128 * hh + i;
@@ -487,12 +369,7 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
 #pragma unroll
       for (int h = 0; h < G; ++h) {
 #pragma unroll
-        for (int hh = 0; hh < NH2; ++hh) {
-          if constexpr (BLK)
-            x[hh][h] = valid[hh] ? fmaf(sv[hh][C::LO + h], 0.0625f, sv[hh][h]) * (cst[h] * ks[hh]) : -INFINITY;
-          else
-            x[hh][h] = valid[hh] ? sv[hh][h] * cst[h] : -INFINITY;
-        }
+        for (int hh = 0; hh < NH2; ++hh) x[hh][h] = valid[hh] ? sv[hh][h] * cst[h] : -INFINITY;
         wm[h] = x[0][h];
 #pragma unroll
         for (int hh = 1; hh < NH2; ++hh) wm[h] = fmaxf(wm[h], x[hh][h]);
@@ -501,19 +378,12 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       // reduction per head), then across the 4
 #pragma unroll
       for (int h = 0; h < G; ++h) wm[h] = warp_max(wm[h]);
-      float vmax = 0.f;  // BLK: the largest V scale of the tile's visible keys
-      if constexpr (BLK) {
-#pragma unroll
-        for (int hh = 0; hh < NH2; ++hh) vmax = fmaxf(vmax, valid[hh] ? vs[hh] : 0.f);
-        vmax = warp_max(vmax);
-      }
       // reduction t uses slot t % 2 (its previous use, t - 2, was read by every warp
       // before that warp's arrival for t - 1)
       float* red = red_s + (t & 1) * 4 * C::NP;
       if (lane == 0) {
 #pragma unroll
         for (int h = 0; h < G; ++h) red[warp * C::NP + h] = wm[h];
-        if constexpr (BLK) red[warp * C::NP + G] = vmax;
         mbar_arrive(&red_full[t & 1]);
       }
       if (!wait_warp(&red_full[t & 1], (t >> 1) & 1, p.pipe_wait_ns)) { ok = false; break; }
@@ -522,39 +392,9 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       // the correction warpgroup read tile t-2's alpha
       if (t >= 2 && !wait_warp(&p_free[pb], ((t >> 1) - 1) & 1, p.pipe_wait_ns)) { ok = false; break; }
       if (t >= 2 && !wait_warp(&a_free[pb], ((t >> 1) - 1) & 1, p.pipe_wait_ns)) { ok = false; break; }
-      // BLK: V's scales enter through P.  The tile's P is taken against its own maximum, scaled so
-      // that the largest possible p * v_scale is 256 (the P.V partial then spans no more than the
-      // tile needs, whatever came before it); the correction brings the partial to the running
-      // maximum: beta = 2^(tile max - m) * the tile's largest v_scale.
-      float rv[NH2];
-      if constexpr (BLK) {
-        vmax = fmaxf(fmaxf(red[G], red[C::NP + G]), fmaxf(red[2 * C::NP + G], red[3 * C::NP + G]));
-#pragma unroll
-        for (int hh = 0; hh < NH2; ++hh) rv[hh] = vmax > 0.f ? __fdividef(vs[hh], vmax) * 256.f : 0.f;
-      }
       float pvs[NH2][G];
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        if constexpr (BLK) {
-          const float tmax = fmaxf(fmaxf(red[h], red[C::NP + h]), fmaxf(red[2 * C::NP + h], red[3 * C::NP + h]));
-          // one of the two factors is 1: the other is 2^-|m - tmax|
-          const float e = ex2(-fabsf(m[h] - tmax));
-          const float alpha = m[h] > tmax ? 1.f : e, corr = m[h] > tmax ? e : 1.f;
-          float psum = 0.f;
-#pragma unroll
-          for (int hh = 0; hh < NH2; ++hh) {
-            const float pv = valid[hh] ? ex2(x[hh][h] - tmax) : 0.f;
-            psum += pv;
-            pvs[hh][h] = pv * rv[hh];
-          }
-          lsum[h] = fmaf(lsum[h], alpha, psum * corr);
-          m[h] = fmaxf(m[h], tmax);
-          if (i == 0) {
-            alpha_s[pb * C::NP + h] = alpha;
-            alpha_s[pb * C::NP + C::LO + h] = corr * vmax;
-          }
-          continue;
-        }
         const float tmax = fmaxf(fmaxf(red[h], red[C::NP + h]), fmaxf(red[2 * C::NP + h], red[3 * C::NP + h]));
         const float mn = fmaxf(m[h], tmax);
         const float alpha = (m[h] == -INFINITY) ? 0.f : ex2(m[h] - mn);
@@ -574,21 +414,8 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       for (int hh = 0; hh < NH2; ++hh) {
 #pragma unroll
         for (int h = 0; h < G; h += 2) {
-          uint8_t* row = sP + pb * C::PTILE + hh * (C::NP * 128);
-          if constexpr (BLK) {
-            float h0, l0, h1 = 0.f, l1 = 0.f;
-            two_terms(pvs[hh][h], h0, l0);
-            if (h + 1 < G) two_terms(pvs[hh][h + 1], h1, l1);
-            const uint16_t hi2 = f32x2_to_e4m3x2(h0, h1), lo2 = f32x2_to_e4m3x2(l0, l1);
-            row[swz(static_cast<uint32_t>(h * 128 + i), 128)] = static_cast<uint8_t>(hi2 & 0xFF);
-            row[swz(static_cast<uint32_t>((C::LO + h) * 128 + i), 128)] = static_cast<uint8_t>(lo2 & 0xFF);
-            if (h + 1 < G) {
-              row[swz(static_cast<uint32_t>((h + 1) * 128 + i), 128)] = static_cast<uint8_t>(hi2 >> 8);
-              row[swz(static_cast<uint32_t>((C::LO + h + 1) * 128 + i), 128)] = static_cast<uint8_t>(lo2 >> 8);
-            }
-            continue;
-          }
           const uint16_t code2 = f32x2_to_e4m3x2(pvs[hh][h], h + 1 < G ? pvs[hh][h + 1] : 0.f);
+          uint8_t* row = sP + pb * C::PTILE + hh * (C::NP * 128);
           row[swz(static_cast<uint32_t>(h * 128 + i), 128)] = static_cast<uint8_t>(code2 & 0xFF);
           if (h + 1 < G) row[swz(static_cast<uint32_t>((h + 1) * 128 + i), 128)] = static_cast<uint8_t>(code2 >> 8);
         }
@@ -644,34 +471,23 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       if ((t & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
       const int ob = t & 1;
       if (!wait_warp(&a_full[ob], (t >> 1) & 1, p.pipe_wait_ns)) { ok = false; break; }
-      float alpha[G], beta[G];
+      float alpha[G];
 #pragma unroll
-      for (int h = 0; h < G; ++h) {
-        alpha[h] = alpha_s[ob * C::NP + h];
-        if constexpr (BLK) beta[h] = alpha_s[ob * C::NP + C::LO + h];
-      }
+      for (int h = 0; h < G; ++h) alpha[h] = alpha_s[ob * C::NP + h];
       mbar_arrive_warp(&a_free[ob]);
       // acc = acc * alpha + O_tile^T(t): the two-level accumulation of tile t
       if (!wait_warp(&o_full[ob], (t >> 1) & 1, p.pipe_wait_ns)) { ok = false; break; }
       tc_fence_after();
-      float o[C::NSUB][C::NP];
+      float o[C::NSUB][16];
 #pragma unroll
-      for (int s2 = 0; s2 < C::NSUB; ++s2) {
-        if constexpr (C::NP == 32) tmem_ld32(lane_base + C::TM_O + (ob * C::NSUB + s2) * C::NP, o[s2]);
-        else tmem_ld16(lane_base + C::TM_O + (ob * C::NSUB + s2) * C::NP, o[s2]);
-      }
+      for (int s2 = 0; s2 < C::NSUB; ++s2) tmem_ld16(lane_base + C::TM_O + (ob * C::NSUB + s2) * C::NP, o[s2]);
       tmem_ld_wait();
       tc_fence_before();
       mbar_arrive_warp(&o_free[ob]);
 #pragma unroll
       for (int s2 = 0; s2 < C::NSUB; ++s2)
 #pragma unroll
-        for (int h = 0; h < G; ++h) {
-          if constexpr (BLK)
-            acc[s2][h] = fmaf(acc[s2][h], alpha[h], beta[h] * fmaf(o[s2][C::LO + h], 0.0625f, o[s2][h]));
-          else
-            acc[s2][h] = fmaf(acc[s2][h], alpha[h], o[s2][h]);
-        }
+        for (int h = 0; h < G; ++h) acc[s2][h] = fmaf(acc[s2][h], alpha[h], o[s2][h]);
     }
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
@@ -683,14 +499,12 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
       for (int h = 0; h < G; ++h) {
         const float L = ml_s[C::NP + h];
         const size_t row = (static_cast<size_t>(b) * p.Hq + g * G + h) * p.max_splits + sigma;
-        // P8 carries the factor 448 (BLK: 256; there a NaN sum stays one)
-        const float inv = BLK ? 1.f / (256.f * L) : L > 0.f ? 1.f / (448.f * L) : 0.f;
+        const float inv = L > 0.f ? 1.f / (448.f * L) : 0.f;  // P8 carries the factor 448
         if (has_row) {
 #pragma unroll
           for (int s2 = 0; s2 < C::NSUB; ++s2) p.o_part[row * D + s2 * 128 + d] = acc[s2][h] * inv;
         }
-        // (a NaN sum's weight is infinite: the merge divides infinity by itself)
-        if (i == 0) p.lse_part[row] = L > 0.f ? ml_s[h] + lg2(L) : (BLK ? INFINITY : -INFINITY);
+        if (i == 0) p.lse_part[row] = L > 0.f ? ml_s[h] + lg2(L) : -INFINITY;
       }
     } else if (ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
@@ -809,18 +623,9 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
         // keys past the context may hold stale bytes (NaN codes) or were not loaded: zero
         // their V rows, since 0 * NaN would poison the product even though their P is 0
         const int kbase = (bb + TPB * tp) * 16;
-        constexpr int CPR = C::RB / 16;  // 16-byte chunks per row
-        if (BLK && kbase < klo) {
-          // so may the keys before a window
-          for (int it = lane; it < (klo - kbase) * C::NSUB * CPR; it += 32) {
-            const int c = it % CPR, s = (it / CPR) % C::NSUB, rr = (it / CPR) / C::NSUB;
-            *reinterpret_cast<uint4*>(sV + st * C::KTILE + s * C::KSUB + rr * C::RB + c * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
         if (kbase + C::BN > T) {
           const int first = max(T - kbase, 0);
+          constexpr int CPR = C::RB / 16;  // 16-byte chunks per row
           const int items = (C::BN - first) * C::NSUB * CPR;
           for (int it = lane; it < items; it += 32) {
             const int c = it % CPR;
@@ -886,45 +691,35 @@ __global__ void __launch_bounds__(kDecodeTcThreads, (D <= 128 && G <= 8) ? 3 : 1
   __syncthreads();
   if (!*last_s) return;
   __threadfence();
-  merge_splits<D, G, kDecodeTcThreads, C::CH>(p, b, g, r.nsplit, BLK ? 1.f : p.v_scale[p.per_head ? g : 0],
+  merge_splits<D, G, kDecodeTcThreads, C::CH>(p, b, g, r.nsplit, p.v_scale[p.per_head ? g : 0],
                                              reinterpret_cast<float*>(sK));
 }
 
-template <int D, int G, bool BLK>
+template <int D, int G>
 cudaError_t launch_decode_tc_t(const DecodeParams& p, cudaStream_t s) {
-  using C = DecodeTcCfg<D, G, BLK>;
+  using C = DecodeTcCfg<D, G>;
   if (p.bps > C::MAX_BPS || p.bps % C::TPB != 0) return cudaErrorInvalidValue;  // whole tiles
   CUtensorMap tmk, tmv;
   if (!make_pool_map(&tmk, const_cast<uint8_t*>(p.k_cache), D, p.Hkv, p.num_blocks, C::RB) ||
       !make_pool_map(&tmv, const_cast<uint8_t*>(p.v_cache), D, p.Hkv, p.num_blocks, C::RB))
     return cudaErrorInvalidValue;
-  auto kern = decode_tc_kernel<D, G, BLK>;
+  auto kern = decode_tc_kernel<D, G>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   dim3 grid(p.max_splits, p.Hkv, p.B);
   return launch_dependent(kern, grid, dim3(kDecodeTcThreads), C::SMEM, s, p, tmk, tmv);
 }
 
-template <int D, bool BLK>
+template <int D>
 cudaError_t launch_decode_tc_g(const DecodeParams& p, int G, cudaStream_t s) {
   switch (G) {
-    case 1: return launch_decode_tc_t<D, 1, BLK>(p, s);
-    case 2: return launch_decode_tc_t<D, 2, BLK>(p, s);
-    case 4: return launch_decode_tc_t<D, 4, BLK>(p, s);
-    case 8: return launch_decode_tc_t<D, 8, BLK>(p, s);
-    case 16:
-      if constexpr (!BLK || D <= 128) return launch_decode_tc_t<D, 16, BLK>(p, s);
-      else return cudaErrorInvalidValue;
+    case 1: return launch_decode_tc_t<D, 1>(p, s);
+    case 2: return launch_decode_tc_t<D, 2>(p, s);
+    case 4: return launch_decode_tc_t<D, 4>(p, s);
+    case 8: return launch_decode_tc_t<D, 8>(p, s);
+    case 16: return launch_decode_tc_t<D, 16>(p, s);
     default: return cudaErrorInvalidValue;
   }
-}
-
-template <bool BLK>
-cudaError_t launch_decode_tc_d(const DecodeParams& p, int D, int G, cudaStream_t s) {
-  if (D == 64) return launch_decode_tc_g<64, BLK>(p, G, s);
-  if (D == 128) return launch_decode_tc_g<128, BLK>(p, G, s);
-  if (D == 256) return launch_decode_tc_g<256, BLK>(p, G, s);
-  return cudaErrorInvalidValue;
 }
 
 }  // namespace
@@ -932,11 +727,10 @@ cudaError_t launch_decode_tc_d(const DecodeParams& p, int D, int G, cudaStream_t
 bool decode_uses_tensor_cores(int D, int elt) { return elt == 1 && (D == 64 || D == 128 || D == 256); }
 
 cudaError_t launch_decode_tc(const DecodeParams& p, int D, int G, cudaStream_t s) {
-  return launch_decode_tc_d<false>(p, D, G, s);
-}
-
-cudaError_t launch_block_decode(const DecodeParams& p, int D, int G, cudaStream_t s) {
-  return launch_decode_tc_d<true>(p, D, G, s);
+  if (D == 64) return launch_decode_tc_g<64>(p, G, s);
+  if (D == 128) return launch_decode_tc_g<128>(p, G, s);
+  if (D == 256) return launch_decode_tc_g<256>(p, G, s);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace fkv

@@ -151,9 +151,26 @@ cudaError_t launch_decode(const DecodeParams& p, int D, int elt, int G, cudaStre
 bool decode_uses_tensor_cores(int D, int elt);
 cudaError_t launch_decode_tc(const DecodeParams& p, int D, int G, cudaStream_t s);
 
-// The same kernel over a block-scaled cache: k_scale and v_scale are [num_blocks][Hkv], the query
-// stays bf16 (q_scale unused), k_new is null.
-cudaError_t launch_block_decode(const DecodeParams& p, int D, int G, cudaStream_t s);
+struct BlockDecodeParams {
+  const __nv_bfloat16* q;                     // [B][Hq][D]
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;             // [num_blocks][Hkv]
+  const int32_t* block_table;                 // [B][max_blocks]
+  const int32_t* ctx;                         // [B]
+  int B, Hq, Hkv, num_blocks, max_blocks;
+  float sm_scale_log2;                        // softmax_scale * log2(e)
+  int window;
+  int32_t* done;                              // [B * Hkv] pieces finished, zero between calls
+  float* lse_part;                            // [N + B * Hkv][G], base 2
+  float* o_part;                              // [N + B * Hkv][G][D]
+  __nv_bfloat16* out;                         // [B][Hq][D]
+  int32_t* fault;
+};
+
+// CTAs of the block-scaled decode that an SM holds, pool blocks of its tiles, and its launch on N CTAs.
+int block_decode_ctas_per_sm(int D, int G);
+int block_decode_tile_blocks(int D);
+cudaError_t launch_block_decode(const BlockDecodeParams& p, int D, int N, cudaStream_t s);
 
 // Supplies the decode's workspace of `need` bytes when the caller passes none: sets *ws
 // (256-byte aligned) and *bytes, with its first `counter_bytes` (the split counters) zero

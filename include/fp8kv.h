@@ -421,6 +421,11 @@ fkv_status fp8_decode_attn_noalloc(const void* q, int32_t batch, int32_t num_q_h
                                    void* out, int32_t num_splits, int32_t* fault,
                                    fkv_stream_t stream);
 
+/* Workspace bytes fp8_block_decode_attn needs for these sizes on the current device; 0 for
+ * sizes it does not take.  They do not depend on the context lengths. */
+size_t fp8_block_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                            int32_t head_dim);
+
 /*
  * fp8_block_decode_attn — one decode step of GQA attention over a block-scaled cache.
  *
@@ -428,15 +433,29 @@ fkv_status fp8_decode_attn_noalloc(const void* q, int32_t batch, int32_t num_q_h
  * nor P rounded to 8 bits:
  *   s_j = q . (k8_j * k_scale[block(j)][g]) * softmax_scale,
  *   out = sum_j softmax(s)_j * (v8_j * v_scale[block(j)][g])   (bf16).
- * The bf16 query enters exactly, P with at least the precision of bf16 (relative to each
- * tile's largest p * v_scale), every sum is FP32.  Arguments, split-K plan, workspace
- * (fp8_decode_attn_workspace_size bytes, the same rules) and limits as for fp8_decode_attn.
+ * The bf16 query enters exactly (down to 2^-18 of its head's largest element), P with at least
+ * the precision of bf16 (down to 2^-18 of a 128-key tile's largest p * v_scale; 256 keys at
+ * head_dim 64), every sum is FP32.  A query row that holds a NaN or an infinity gives a NaN
+ * row.  The cached tokens' codes are finite; what lies behind the last token of a sequence, and
+ * before a window, may be any bytes.
+ *
+ * The split of the contexts over the CTAs is made on the GPU from context_lens, evenly, so that a
+ * captured launch replays well with other lengths.
+ *
+ *   q, block_table, context_lens, softmax_scale, window, out  as for fp8_decode_attn
+ *   workspace     device, >= fp8_block_decode_attn_workspace_size(...) bytes, 256-byte aligned,
+ *                 zero-filled before its first call.  Its first 4 * batch * num_kv_heads bytes are
+ *                 counters that a call finds and leaves zero; the rest is scratch.  Calls that
+ *                 may overlap on the GPU (other streams, two captured graphs) each need their own;
+ *                 calls in one stream share one, with the same or a smaller batch * num_kv_heads
+ *                 (zero it again when that grows).  A counter found non-zero sets
+ *                 FKV_FAULT_WORKSPACE
+ * Limits as for fp8_decode_attn.  A sequence with no key gets a zero row.
  */
 fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
                                  const int32_t* block_table, int32_t max_blocks,
                                  const int32_t* context_lens, float softmax_scale, int32_t window, void* out,
-                                 void* workspace, size_t workspace_bytes, int32_t num_splits, int32_t* fault,
-                                 fkv_stream_t stream);
+                                 void* workspace, size_t workspace_bytes, int32_t* fault, fkv_stream_t stream);
 
 /* Keys per tile of fp8_prefill_attn (its online-softmax and P-rounding granularity). */
 int32_t fkv_prefill_block_n(int32_t head_dim);

@@ -94,13 +94,13 @@ def test_block_cache_unsupported(lib, kw):
 
 
 def _decode(lib, **kw):
-    a = dict(q=P, b=2, hq=8, cache=_block(), table=P, mb=9, ctx=P, sm=0.0, win=0, out=P, ws=P, wsb=1 << 30, ns=0)
+    a = dict(q=P, b=2, hq=8, cache=_block(), table=P, mb=9, ctx=P, sm=0.0, win=0, out=P, ws=P, wsb=1 << 30)
     a.update(kw)
     return lib.fp8_block_decode_attn(*a.values(), None, None)
 
 
 @pytest.mark.parametrize("kw", [
-    dict(b=-1), dict(hq=0), dict(hq=7), dict(mb=0), dict(win=-1), dict(ns=-1), dict(sm=-1.0), dict(sm=float("inf")),
+    dict(b=-1), dict(hq=0), dict(hq=7), dict(mb=0), dict(win=-1), dict(sm=-1.0), dict(sm=float("inf")),
     dict(sm=float("nan")), dict(q=None), dict(out=None), dict(table=None), dict(ctx=None), dict(ws=None), dict(wsb=64),
     dict(ws=P + 128), dict(q=P + 8), dict(out=P + 8), dict(cache=_block(vs=None)), dict(cache=_block(nb=-4)),
 ])
@@ -114,9 +114,13 @@ def test_block_decode_unsupported(lib, kw):
     assert _decode(lib, **kw) == f.UNSUPPORTED
 
 
-def test_block_decode_takes_the_decode_workspace(lib):
-    n = f.fp8_decode_attn_workspace_size(2, 8, 2, 128, 9)
+def test_block_decode_workspace(lib):
+    n = f.fp8_block_decode_attn_workspace_size(2, 8, 2, 128)
     assert n > 0 and _decode(lib, wsb=n - 1) == f.INVALID_ARG
+    # counters, and a row per CTA and unit
+    assert n >= 4 * 4 + 4 * (128 + 1) * 4 * (152 + 4)
+    for bad in ((0, 8, 2, 128), (2, 7, 2, 128), (2, 8, 2, 96), (2, 6, 2, 128), (2, 8, 0, 64), (2, 32, 2, 256)):
+        assert f.fp8_block_decode_attn_workspace_size(*bad) == 0
 
 
 def _prefill(lib, **kw):
@@ -209,7 +213,7 @@ def test_compiled_binding_checks_of_the_attention(lib):
     pool, s, i32 = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.ones(3, 2), torch.zeros(3, dtype=torch.int32)
     tab = torch.zeros(2, 4, dtype=torch.int32)
     d = dict(q=_bf(2, 4, 64), kc=pool, vc=pool, ks=s, vs=s, tab=tab, ctx=i32[:2], sm=0.0, win=0, out=None,
-             ws=torch.zeros(1 << 16, dtype=torch.uint8), ns=0, fault=None)
+             ws=torch.zeros(1 << 16, dtype=torch.uint8), fault=None)
     for match, change in [
         ("q is BFloat16 .3, 4, 64", dict(q=_bf(3, 4, 64))), ("q is Half", dict(q=_bf(2, 4, 64).half())), ("out is", dict(out=_bf(2, 4, 32))),
         ("k_cache", dict(q=_bf(2, 4, 128))), ("q is", dict(q=_bf(4, 2, 64).transpose(0, 1))), ("workspace", dict(ws=torch.zeros(8, 8)[:, ::2])),

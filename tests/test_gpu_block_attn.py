@@ -111,10 +111,39 @@ def test_decode_windows(d, window):
     _check(c.decode(window=window), c.exact(window=window))
 
 
-@pytest.mark.parametrize("splits", [1, 2, 5, 40])
-def test_decode_splits_and_softmax_scale(splits):
-    c = Case([2100, 40, 0], 8, 1, 128, seed=splits)
-    _check(c.decode(num_splits=splits, softmax_scale=0.2), c.exact(softmax_scale=0.2))
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("ctx,hq,h", [([2100, 40, 0], 8, 1), ([0, 0, 7, 0], 4, 4), ([9000], 2, 2),
+                                      ([33, 500, 0, 16, 128, 1000, 64] * 11, 8, 8), ([20] * 300, 2, 1), ([5000] + [1] * 70, 3, 3)])
+def test_decode_ranges_over_sequences(d, ctx, hq, h):
+    """Contexts whose tiles are dealt out over the CTAs: units in many pieces, in one, several units (and
+    sequences without keys between them) in one CTA's range."""
+    c = Case(ctx, hq, h, d, seed=len(ctx))
+    _check(c.decode(softmax_scale=0.2), c.exact(softmax_scale=0.2))
+
+
+def test_decode_range_of_many_short_units():
+    """More units than resident CTAs, each of a tile or two: every CTA walks several pieces."""
+    rng = np.random.default_rng(4)
+    ctx = [int(x) for x in rng.integers(0, 260, 230)]
+    c = Case(ctx, 12, 6, 64, seed=7)
+    _check(c.decode(), c.exact())
+
+
+def test_decode_replays_with_other_contexts():
+    """A captured launch with other context lengths than it was captured with."""
+    full = [700, 300, 1100]
+    c = Case(full, 8, 2, 128, seed=13)
+    q, cache, table = c.q.cuda(), c.cache(), _i32(c.table)
+    ctx, out = _i32([1, 1, 1]), torch.empty(3, 8, 128, dtype=torch.bfloat16, device="cuda")
+    ws = f.block_decode_workspace(3, 8, cache)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f.fp8_block_decode_attn(q, cache, table, ctx, out=out, workspace=ws)
+    for lens in (full, [0, 300, 17], [700, 0, 0], [5, 6, 1100], [0, 0, 0], full):
+        c.ctx = lens
+        ctx.copy_(_i32(lens))
+        graph.replay()
+        _check(out, c.exact())
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -174,7 +203,7 @@ def test_decode_long_context():
 def test_decode_reuses_its_workspace_and_two_streams_with_their_own():
     c = Case([900, 77, 1300], 8, 2, 128, seed=21)
     q, cache, table, ctx = c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx)
-    ws = [torch.zeros(f.fp8_decode_attn_workspace_size(3, 8, 2, 128, table.shape[1]), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ws = [f.block_decode_workspace(3, 8, cache) for _ in range(2)]
     first = f.fp8_block_decode_attn(q, cache, table, ctx, workspace=ws[0])
     torch.cuda.synchronize()
     outs = []
@@ -331,7 +360,7 @@ def test_serving_run(d, hq, h, style):
     # one graph, replayed with new inputs
     q, k, v = (t.clone() for t in draw(2))
     dctx, cu = _i32([1, 1]), _i32([0, 1, 2])
-    ws = torch.zeros(f.fp8_decode_attn_workspace_size(2, hq, h, d, 12), dtype=torch.uint8, device="cuda")
+    ws = f.block_decode_workspace(2, hq, cache)
     turned, out = torch.empty(2, hq, d, dtype=torch.bfloat16, device="cuda"), torch.empty(2, hq, d, dtype=torch.bfloat16, device="cuda")
     spare = f.BlockCache(*(t.clone() for t in (cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale)))
     graph = torch.cuda.CUDAGraph()
