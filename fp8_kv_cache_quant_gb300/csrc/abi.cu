@@ -432,7 +432,7 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
   if (cache.block_size != 16) return cache.block_size > 0 ? FKV_UNSUPPORTED : FKV_INVALID_ARG;
   if (cache.num_blocks <= 0 || cache.num_kv_heads <= 0 || !valid_format(cache)) return FKV_INVALID_ARG;
   if (!supported_head_dim(cache.head_dim)) return FKV_UNSUPPORTED;
-  if (num_q_heads > 65535 || cache.num_kv_heads > 65535) return FKV_UNSUPPORTED;
+  if (num_q_heads > 8192 || cache.num_kv_heads > 8192) return FKV_UNSUPPORTED;
   if (gran != FKV_SCALE_PER_TENSOR && gran != FKV_SCALE_PER_HEAD) return FKV_INVALID_ARG;
   if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   fkv_status st = FKV_OK;
@@ -478,7 +478,7 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
   p.per_head = gran == FKV_SCALE_PER_HEAD;
   p.fault = fault;
   const int pool = bf16 ? 2 : cache.kv_format == FKV_KV_E5M2 ? 1 : 0;
-  return from_cuda(fkv::launch_rope_cache(p, pool, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(fkv::launch_rope_cache(p, pool, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
@@ -489,7 +489,7 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
   if (n_tokens < 0 || batch < 0 || max_q_len < 0 || max_blocks <= 0 || num_q_heads < 0) return FKV_INVALID_ARG;
   fkv_status st = check_block_cache(cache);
   if (st != FKV_OK) return st;
-  if (batch > 65535 || num_q_heads > 65535 || cache.num_kv_heads > 65535) return FKV_UNSUPPORTED;
+  if (batch > 65535 || num_q_heads > 8192 || cache.num_kv_heads > 8192) return FKV_UNSUPPORTED;
   if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   const bool turned = rope.cos_sin != nullptr;
   if (turned) {

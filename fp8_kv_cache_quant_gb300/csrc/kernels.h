@@ -79,7 +79,7 @@ struct RopeCacheParams {
 };
 
 // pool: 0 e4m3, 1 e5m2, 2 bf16
-cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, cudaStream_t s);
+cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s);
 
 struct BlockCacheParams {
   const __nv_bfloat16 *q, *k, *v;

@@ -92,52 +92,64 @@ FKV_DEV void turn_unit(float (&a)[8], float (&b)[8], const float* cs, int rot, i
 
 // ---------------------------------------------------------------- kv_rope_cache
 
-// Thread = one unit of one row (query heads, then K heads, then V heads) of one token; a CTA
-// holds whole tokens (tokens_per_cta, or one token in several rounds).
+constexpr int kRopeThreads = 256;
+
+// Thread = one unit of one row (query heads, then K heads, then V heads), the same one of every
+// token that it handles: the grid's active threads are a multiple (t_step) of a token's units, so
+// that row and unit are found once and token t is followed by t + t_step.  HBM-bound: the next
+// token's elements, slot and position are loaded before the current token is turned and stored, so
+// that a thread has 32 bytes in flight all the time.
 // kPool: 0 e4m3, 1 e5m2, 2 bf16.
-template <int kPool>
-__global__ void __launch_bounds__(512) rope_cache_kernel(const RopeCacheParams p, int tokens_per_cta) {
-  const int U = p.D >> 4;
+template <int D, int kPool>
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_cache_kernel(const RopeCacheParams p, int t_step) {
+  constexpr int U = D / 16;
   const int per_token = (p.Hq + 2 * p.H) * U;
-  for (int item = threadIdx.x; item < tokens_per_cta * per_token; item += blockDim.x) {
-    const int tl = item / per_token, rem = item - tl * per_token;
-    const long long t = static_cast<long long>(blockIdx.x) * tokens_per_cta + tl;
-    if (t >= p.n_tokens) return;
-    const int row = rem / U, u = rem - row * U;
-    const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.H;
-    const int h = is_q ? row : (is_v ? row - p.Hq - p.H : row - p.Hq);
-    const bool turned = !is_v && u < (p.rot >> 4);
-    int ca, cb;
-    unit_chunks(u, is_v ? 0 : p.rot, p.interleaved, ca, cb);
-    const __nv_bfloat16* src = (is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride) + h * p.D;
-    const uint4 xa = reinterpret_cast<const uint4*>(src)[ca], xb = reinterpret_cast<const uint4*>(src)[cb];
-    const long long slot = p.slots[t], pos = p.positions[t];
-    if (slot < 0) continue;
-    if (slot >= p.capacity) {
-      if (rem == 0) raise_fault(p.fault, FKV_FAULT_SLOT);
-      continue;
-    }
-    if (pos < 0 || pos >= p.max_pos) {
-      if (rem == 0) raise_fault(p.fault, FKV_FAULT_POSITION);
-      continue;
-    }
+  const long long gid = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  if (gid >= static_cast<long long>(per_token) * t_step) return;
+  const int t0 = static_cast<int>(gid / per_token), rem = static_cast<int>(gid - static_cast<long long>(t0) * per_token);
+  const int row = rem / U, u = rem % U;
+  const bool is_q = row < p.Hq, is_v = row >= p.Hq + p.H;
+  const int h = is_q ? row : (is_v ? row - p.Hq - p.H : row - p.Hq);
+  const bool turned = !is_v && u < (p.rot >> 4);
+  int ca, cb;
+  unit_chunks(u, is_v ? 0 : p.rot, p.interleaved, ca, cb);
+  const long long stride = is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride;
+  const __nv_bfloat16* src = (is_q ? p.q : is_v ? p.v : p.k) + h * D;
+  uint8_t* pool = is_v ? p.vc : p.kc;
+  const float inv = is_q || kPool == 2 ? 1.f : __frcp_rn((is_v ? p.vs : p.ks)[p.per_head ? h : 0]);
+  uint4 xa, xb;
+  long long slot, pos;
+  auto fetch = [&](long long t) {
+    const uint4* x = reinterpret_cast<const uint4*>(src + t * stride);
+    xa = x[ca];
+    xb = x[cb];
+    slot = p.slots[t];
+    pos = p.positions[t];
+  };
+  if (t0 < p.n_tokens) fetch(t0);
+  for (long long t = t0; t < p.n_tokens; t += t_step) {
     float a[8], b[8];
     unpack8(xa, a);
     unpack8(xb, b);
-    if (turned) turn_unit(a, b, p.cos_sin + pos * p.rot, p.rot, u, p.interleaved);
+    const long long s = slot, x = pos;
+    if (t + t_step < p.n_tokens) fetch(t + t_step);
+    if (s < 0) continue;
+    if (s >= p.capacity || x < 0 || x >= p.max_pos) {
+      if (rem == 0) raise_fault(p.fault, s >= p.capacity ? FKV_FAULT_SLOT : FKV_FAULT_POSITION);
+      continue;
+    }
+    if (turned) turn_unit(a, b, p.cos_sin + x * p.rot, p.rot, u, p.interleaved);
     if (is_q) {
-      uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * p.D);
+      uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * D);
       dst[ca] = pack8_bf16(a);
       dst[cb] = pack8_bf16(b);
     } else {
       // chunk index of the row's first 8 elements in the pool
-      const long long at = ((((slot >> 4) * p.H + h) << 4) + (slot & 15)) * (p.D >> 3);
-      uint8_t* pool = is_v ? p.vc : p.kc;
+      const long long at = ((((s >> 4) * p.H + h) << 4) + (s & 15)) * (D >> 3);
       if constexpr (kPool == 2) {
         reinterpret_cast<uint4*>(pool)[at + ca] = pack8_bf16(a);
         reinterpret_cast<uint4*>(pool)[at + cb] = pack8_bf16(b);
       } else {
-        const float inv = __frcp_rn((is_v ? p.vs : p.ks)[p.per_head ? h : 0]);
         reinterpret_cast<uint2*>(pool)[at + ca] = pack8_fp8<kPool == 1>(a, inv);
         reinterpret_cast<uint2*>(pool)[at + cb] = pack8_fp8<kPool == 1>(b, inv);
       }
@@ -148,7 +160,9 @@ __global__ void __launch_bounds__(512) rope_cache_kernel(const RopeCacheParams p
 // ---------------------------------------------------------------- kv_block_cache
 
 constexpr int kBlockThreads = 256;
-constexpr int kQueryItems = 4 * kBlockThreads;  // units of the query rows per CTA
+constexpr int kBlockTasks = kBlockThreads / 64;  // (KV head, K or V) pairs per CTA, two warps each
+constexpr int kQueryLoads = 4;
+constexpr int kQueryItems = kQueryLoads * kBlockThreads;  // units of the query rows per CTA
 
 // Four e4m3 codes times r, each product rounded to float32, as e4m3 codes.
 FKV_DEV uint32_t rescale4(uint32_t w, float r) {
@@ -168,14 +182,17 @@ FKV_DEV float pow2_scale(uint32_t amax_bits) {
   return __uint_as_float(static_cast<uint32_t>(max(k, -126) + 127) << 23);
 }
 
-// CTA z = 0: the K and V of one block (page blockIdx.x of sequence blockIdx.y's new tokens), a
-// warp per (KV head, K or V): its 16 rows stay in registers between the maximum and the
-// codes, so that each input byte is read once.  CTAs z >= 1: slices of the page's query rows.
+// grid (pages of a sequence's new tokens, sequences, kv_parts + slices of the query rows).
+// CTAs z < kv_parts: K and V of one block, two warps per (KV head, K or V), 8 of its 16 rows each:
+// the rows stay in registers between the maximum and the codes, so that each input byte is read
+// once, and two warps rather than one keep them few enough for three CTAs per SM.  The others turn
+// query rows, four units per thread with all loads up front.
 template <int D>
-__global__ void __launch_bounds__(kBlockThreads) block_cache_kernel(const BlockCacheParams p) {
+__global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 3 : 2) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
   constexpr int U = D / 16;       // units of a row
-  constexpr int TP = 32 / U;      // tokens of a page that a warp handles at once
-  constexpr int R = 16 / TP;      // rounds
+  constexpr int TP = 32 / U;      // rows that a warp handles at once
+  constexpr int R = 8 / TP;       // rounds
+  __shared__ uint32_t amax_s[kBlockThreads / 32];
   const int b = blockIdx.y;
   const int r0 = p.cu[b], L = p.cu[b + 1] - r0, T = p.ctx[b];
   const bool first = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0;
@@ -200,125 +217,149 @@ __global__ void __launch_bounds__(kBlockThreads) block_cache_kernel(const BlockC
   const int lo = max(T - L, page * 16), hi = min(T, page * 16 + 16);  // new positions in the page
   const long long row0 = static_cast<long long>(r0) - (T - L);        // row of position x: row0 + x
 
-  if (blockIdx.z > 0) {
+  if (static_cast<int>(blockIdx.z) >= kv_parts) {
     const int items = (hi - lo) * p.Hq * U;
-    const int i0 = (blockIdx.z - 1) * kQueryItems, i1 = min(items, i0 + kQueryItems);
-    for (int i = i0 + threadIdx.x; i < i1; i += kBlockThreads) {
-      const int u = i % U, h = (i / U) % p.Hq, pos = lo + i / (U * p.Hq);
-      int ca, cb;
-      unit_chunks(u, p.rot, p.interleaved, ca, cb);
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (row0 + pos) * p.q_stride + h * D);
+    const int i0 = (blockIdx.z - kv_parts) * kQueryItems + threadIdx.x;
+    if (i0 >= items) return;
+    const int u = i0 % U;  // the same in every step: the CTA's threads are a multiple of U
+    int ca, cb;
+    unit_chunks(u, p.rot, p.interleaved, ca, cb);
+    uint4 xa[kQueryLoads], xb[kQueryLoads];
+    int pos[kQueryLoads], h[kQueryLoads];
+#pragma unroll
+    for (int j = 0; j < kQueryLoads; ++j) {
+      const int i = i0 + j * kBlockThreads;
+      const int th = i / U, tl = th / p.Hq;
+      pos[j] = lo + tl;
+      h[j] = th - tl * p.Hq;
+      if (i < items) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (row0 + pos[j]) * p.q_stride + h[j] * D);
+        xa[j] = src[ca];
+        xb[j] = src[cb];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kQueryLoads; ++j) {
+      if (i0 + j * kBlockThreads >= items) break;
       float a[8], c[8];
-      unpack8(src[ca], a);
-      unpack8(src[cb], c);
-      if (u < (p.rot >> 4)) turn_unit(a, c, p.cos_sin + static_cast<long long>(pos) * p.rot, p.rot, u, p.interleaved);
-      uint4* dst = reinterpret_cast<uint4*>(p.q_out + (row0 + pos) * p.q_out_stride + h * D);
+      unpack8(xa[j], a);
+      unpack8(xb[j], c);
+      if (u < (p.rot >> 4)) turn_unit(a, c, p.cos_sin + static_cast<long long>(pos[j]) * p.rot, p.rot, u, p.interleaved);
+      uint4* dst = reinterpret_cast<uint4*>(p.q_out + (row0 + pos[j]) * p.q_out_stride + h[j] * D);
       dst[ca] = pack8_bf16(a);
       dst[cb] = pack8_bf16(c);
     }
     return;
   }
 
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int task = blockIdx.z * kBlockTasks + (warp >> 1);
+  if (task >= 2 * p.H) return;  // both warps of the pair
+  const int g = task >> 1;
+  const bool is_v = task & 1;
+  const int u = lane % U, rot = is_v ? 0 : p.rot;
+  const int slot0 = 8 * (warp & 1) + lane / U;  // this lane's row in round 0
+  int ca, cb;
+  unit_chunks(u, rot, p.interleaved, ca, cb);
+  const __nv_bfloat16* src = is_v ? p.v : p.k;
+  const long long stride = is_v ? p.v_stride : p.k_stride;
+  uint4 xa[R], xb[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int pos = page * 16 + slot0 + r * TP;
+    xa[r] = xb[r] = make_uint4(0u, 0u, 0u, 0u);
+    if (pos >= lo && pos < hi) {
+      const uint4* s = reinterpret_cast<const uint4*>(src + (row0 + pos) * stride + g * D);
+      xa[r] = s[ca];
+      xb[r] = s[cb];
+    }
+  }
   const int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + page];
   if (id < 0 || id >= p.num_blocks) {
     if (threadIdx.x == 0) raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u = lane % U;
-  for (int task = warp; task < 2 * p.H; task += kBlockThreads / 32) {
-    const int g = task >> 1;
-    const bool is_v = task & 1;
-    const int rot = is_v ? 0 : p.rot;
-    int ca, cb;
-    unit_chunks(u, rot, p.interleaved, ca, cb);
-    const __nv_bfloat16* src = is_v ? p.v : p.k;
-    const long long stride = is_v ? p.v_stride : p.k_stride;
-    uint4 xa[R], xb[R];
+  float* scale = (is_v ? p.vs : p.ks) + static_cast<size_t>(id) * p.H + g;
+  const int kept = lo - page * 16;  // slots that already hold tokens
+  const float old = kept > 0 ? *scale : 0.f;
+  float a[R][8], c[R][8];
+  uint32_t amax = 0;  // bits of the largest finite magnitude (magnitudes order as their bits)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int pos = page * 16 + r * TP + lane / U;
-      xa[r] = xb[r] = make_uint4(0u, 0u, 0u, 0u);
-      if (pos >= lo && pos < hi) {
-        const uint4* s = reinterpret_cast<const uint4*>(src + (row0 + pos) * stride + g * D);
-        xa[r] = s[ca];
-        xb[r] = s[cb];
+  for (int r = 0; r < R; ++r) {
+    const int pos = page * 16 + slot0 + r * TP;
+    unpack8(xa[r], a[r]);
+    unpack8(xb[r], c[r]);
+    if (u < (rot >> 4) && pos >= lo && pos < hi)
+      turn_unit(a[r], c[r], p.cos_sin + static_cast<long long>(pos) * p.rot, p.rot, u, p.interleaved);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = __float_as_uint(a[r][i]) & 0x7FFFFFFFu, y = __float_as_uint(c[r][i]) & 0x7FFFFFFFu;
+      if (x < 0x7F800000u) amax = max(amax, x);
+      if (y < 0x7F800000u) amax = max(amax, y);
+    }
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (lane == 0) amax_s[warp] = amax;
+  // the pair's barrier; both warps have read the old scale before it is replaced below
+  asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+  float s = pow2_scale(max(amax, amax_s[warp ^ 1]));
+  uint8_t* block = (is_v ? p.vc : p.kc) + (static_cast<size_t>(id) * p.H + g) * 16 * D;
+  if (kept > 0 && old >= 1.17549435e-38f && old <= 3.402823466e+38f) {  // a normal positive number
+    if (old >= s) {
+      s = old;
+    } else {
+      const float r = __fdiv_rn(old, s);
+      for (int i = lane + 32 * (warp & 1); i < kept * D / 16; i += 64) {
+        uint4* q4 = reinterpret_cast<uint4*>(block) + i;
+        uint4 w = *q4;
+        w.x = rescale4(w.x, r);
+        w.y = rescale4(w.y, r);
+        w.z = rescale4(w.z, r);
+        w.w = rescale4(w.w, r);
+        *q4 = w;
       }
     }
-    float a[R][8], c[R][8];
-    uint32_t amax = 0;  // bits of the largest finite magnitude (magnitudes order as their bits)
+  }
+  if (lane == 0 && (warp & 1) == 0) *scale = s;
+  const float inv = __frcp_rn(s);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int pos = page * 16 + r * TP + lane / U;
-      unpack8(xa[r], a[r]);
-      unpack8(xb[r], c[r]);
-      if (u < (rot >> 4) && pos >= lo && pos < hi)
-        turn_unit(a[r], c[r], p.cos_sin + static_cast<long long>(pos) * p.rot, p.rot, u, p.interleaved);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t x = __float_as_uint(a[r][i]) & 0x7FFFFFFFu, y = __float_as_uint(c[r][i]) & 0x7FFFFFFFu;
-        if (x < 0x7F800000u) amax = max(amax, x);
-        if (y < 0x7F800000u) amax = max(amax, y);
-      }
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    float* scale = (is_v ? p.vs : p.ks) + static_cast<size_t>(id) * p.H + g;
-    float s = pow2_scale(amax);
-    uint8_t* block = (is_v ? p.vc : p.kc) + (static_cast<size_t>(id) * p.H + g) * 16 * D;
-    const int kept = lo - page * 16;  // slots that already hold tokens
-    if (kept > 0) {
-      const float old = *scale;
-      const bool usable = old >= 1.17549435e-38f && old <= 3.402823466e+38f;  // a normal positive number
-      __syncwarp();  // every lane has read the old scale before lane 0 replaces it
-      if (usable && old >= s) {
-        s = old;
-      } else if (usable) {
-        const float r = __fdiv_rn(old, s);
-        for (int i = lane; i < kept * D / 16; i += 32) {
-          uint4* q4 = reinterpret_cast<uint4*>(block) + i;
-          uint4 w = *q4;
-          w.x = rescale4(w.x, r);
-          w.y = rescale4(w.y, r);
-          w.z = rescale4(w.z, r);
-          w.w = rescale4(w.w, r);
-          *q4 = w;
-        }
-      }
-    }
-    if (lane == 0) *scale = s;
-    const float inv = __frcp_rn(s);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int slot = r * TP + lane / U;
-      const int pos = page * 16 + slot;
-      if (pos >= lo && pos < hi) {
-        uint2* dst = reinterpret_cast<uint2*>(block + slot * D);
-        dst[ca] = pack8_fp8<false>(a[r], inv);
-        dst[cb] = pack8_fp8<false>(c[r], inv);
-      }
+  for (int r = 0; r < R; ++r) {
+    const int slot = slot0 + r * TP, pos = page * 16 + slot;
+    if (pos >= lo && pos < hi) {
+      uint2* dst = reinterpret_cast<uint2*>(block + slot * D);
+      dst[ca] = pack8_fp8<false>(a[r], inv);
+      dst[cb] = pack8_fp8<false>(c[r], inv);
     }
   }
 }
 
+template <int D>
+cudaError_t launch_rope(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
+  const long long per_token = static_cast<long long>(p.Hq + 2 * p.H) * (D / 16);
+  // as many tokens at once as four CTAs per SM hold
+  const long long t_step = std::min<long long>(p.n_tokens, std::max<long long>(1, 4LL * num_sms * kRopeThreads / per_token));
+  const unsigned blocks = static_cast<unsigned>((per_token * t_step + kRopeThreads - 1) / kRopeThreads);
+  auto kern = pool == 2 ? rope_cache_kernel<D, 2> : pool == 1 ? rope_cache_kernel<D, 1> : rope_cache_kernel<D, 0>;
+  kern<<<blocks, kRopeThreads, 0, s>>>(p, static_cast<int>(t_step));
+  return cudaGetLastError();
+}
+
 }  // namespace
 
-cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, cudaStream_t s) {
-  const int per_token = (p.Hq + 2 * p.H) * (p.D >> 4);
-  const int tokens = per_token >= 256 ? 1 : 256 / per_token;  // whole tokens per CTA
-  const int threads = std::min(512, (tokens * per_token + 31) / 32 * 32);
-  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(p.n_tokens) + tokens - 1) / tokens);
-  auto kern = pool == 2 ? rope_cache_kernel<2> : pool == 1 ? rope_cache_kernel<1> : rope_cache_kernel<0>;
-  kern<<<blocks, threads, 0, s>>>(p, tokens);
-  return cudaGetLastError();
+cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
+  if (p.D == 64) return launch_rope<64>(p, pool, num_sms, s);
+  if (p.D == 128) return launch_rope<128>(p, pool, num_sms, s);
+  return launch_rope<256>(p, pool, num_sms, s);
 }
 
 cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s) {
   // pages that max_q_len tokens can touch, wherever the first of them lies in its block
   const unsigned pages = static_cast<unsigned>((static_cast<long long>(p.max_q_len) + 14) / 16 + 1);
   const long long items = static_cast<long long>(std::min(16, p.max_q_len)) * p.Hq * (D / 16);
-  const dim3 grid(pages, p.B, static_cast<unsigned>(1 + (items + kQueryItems - 1) / kQueryItems));
+  const int kv_parts = (2 * p.H + kBlockTasks - 1) / kBlockTasks;
+  const dim3 grid(pages, p.B, static_cast<unsigned>(kv_parts + (items + kQueryItems - 1) / kQueryItems));
   auto kern = D == 64 ? block_cache_kernel<64> : D == 128 ? block_cache_kernel<128> : block_cache_kernel<256>;
-  kern<<<grid, kBlockThreads, 0, s>>>(p);
+  kern<<<grid, kBlockThreads, 0, s>>>(p, kv_parts);
   return cudaGetLastError();
 }
 
