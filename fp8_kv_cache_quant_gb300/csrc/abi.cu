@@ -636,7 +636,7 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   p.window = window;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
-  return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -27,6 +27,9 @@
 //   13    allocates TMEM, issues S = q' K8^T;    14  issues O_t = P V8;    15  V copies.
 // TMEM: two S buffers and two O_t buffers up to head_dim 128; at head_dim 256 one S buffer, two
 // 128-column O_t buffers for the halves of head_dim, and the second half of acc.
+// Few rows (drafted tokens, short chunks) over a long context: a cluster of up to 8 CTAs shares
+// the rows' key tiles, and the partial results meet through distributed shared memory, where each
+// CTA merges its share of the rows (SPLIT).
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns.
 #include <atomic>
@@ -75,7 +78,7 @@ struct BlockPrefillCfg {
   static constexpr int OFF_K = OFF_Q + 2 * TILE;
   static constexpr int OFF_V = OFF_K + NS * TILE;
   static constexpr int OFF_P = OFF_V + NS * TILE;   // per buffer: hi, lo
-  static constexpr int OFF_F = OFF_P + PBUF * 2 * PTERM;  // factors [2][128] float2 (acc, O_t); last: (l, -)
+  static constexpr int OFF_F = OFF_P + PBUF * 2 * PTERM;  // factors [2][128] float2 (acc, O_t); last: (l, m)
   static constexpr int OFF_SC = OFF_F + 2 * BM * 8;
   static constexpr int OFF_BAR = OFF_SC + SCN * SCF * 4;
   static constexpr int NBAR = 18 + 4 * NS + SCN;
@@ -97,7 +100,38 @@ FKV_DEV void split4(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
   lo = static_cast<uint32_t>(f32x2_to_e4m3x2(la.x, la.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(lb.x, lb.y)) << 16);
 }
 
-template <int D, bool WIN>
+FKV_DEV uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+FKV_DEV uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every CTA of the cluster: earlier writes of all are visible behind it.
+FKV_DEV void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of this CTA's shared location `p` in CTA `rank` of the cluster, and loads from there.
+FKV_DEV uint32_t peer_address(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+FKV_DEV float2 peer_ld2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+FKV_DEV float4 peer_ld4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
+
+template <int D, bool WIN, bool SPLIT>
 __global__ void __launch_bounds__(512, 1)
     block_prefill_kernel(const __grid_constant__ BlockPrefillParams p, const __grid_constant__ CUtensorMap tmk,
                          const __grid_constant__ CUtensorMap tmv) {
@@ -136,10 +170,12 @@ __global__ void __launch_bounds__(512, 1)
   const int GC = p.part_heads, h_first = part * GC;
   const int tok = 128 / GC;                   // tokens per CTA
   const int b = blockIdx.z;
-  const int qt = gridDim.x - 1 - blockIdx.x;  // longest (latest) query tiles first
+  // longest (latest) query tiles first; SPLIT: a cluster per query tile
+  const int share = SPLIT ? static_cast<int>(cluster_rank()) : 0, shares = SPLIT ? static_cast<int>(cluster_size()) : 1;
+  const int qt = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) / shares;
 
   // ------------------------------------------------------------ sequence geometry
-  const bool first_cta = qt == 0 && blockIdx.y == 0 && threadIdx.x == 0;
+  const bool first_cta = qt == 0 && share == 0 && blockIdx.y == 0 && threadIdx.x == 0;
   const int r0 = p.cu[b];
   const int Lq = p.cu[b + 1] - r0;
   int T = p.ctx[b];
@@ -157,8 +193,10 @@ __global__ void __launch_bounds__(512, 1)
   const int pos0 = T - Lq + q0;  // absolute position of the first token (may be negative when not causal)
   const int kv_end = p.causal ? min(T, pos0 + toks) : T;  // keys [kv_lo, kv_end) matter
   const int kv_lo = WIN ? max(0, pos0 - p.window + 1) : 0;
-  const int tb = kv_lo / C::BN;                           // first key tile
-  const int n_t = (kv_end + C::BN - 1) / C::BN - tb;      // tiles u = 0 .. n_t-1 are tb + u
+  // tiles u = 0 .. n_t-1 are tb + u; SPLIT: this CTA's share of them
+  const int tb0 = kv_lo / C::BN, n_all = (kv_end + C::BN - 1) / C::BN - tb0;
+  const int tb = tb0 + share * n_all / shares;
+  const int n_t = tb0 + (share + 1) * n_all / shares - tb;
   const int nblk_seq = (T + 15) >> 4;
 
   if (threadIdx.x == 0) {
@@ -202,6 +240,7 @@ __global__ void __launch_bounds__(512, 1)
     const int i = rb + (lane & 15);                            // row (TMEM lane i)
     const int it = i / GC, h = h_first + i - it * GC;          // its token and head of the group
     const bool row_ok = it < toks && h < G;
+    const bool live = __any_sync(0xffffffffu, row_ok);         // the warp has a row to work on
     const int pos = pos0 + it;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(rb) << 16);
     const int c0 = hf * C::HC;                                 // first column of this thread's half
@@ -253,6 +292,16 @@ __global__ void __launch_bounds__(512, 1)
       const int sb = t % C::SBUF, pb = t % C::PBUF;
       if (!pf_wait_warp(&s_full[sb], (t / C::SBUF) & 1)) { ok = false; break; }
       tc_fence_after();
+      if (!live) {
+        // a warp without rows takes part in the barriers only (what its rows of P hold reaches no
+        // other row)
+        mbar_arrive_warp(&s_free[sb]);
+        if (t >= C::PBUF && !pf_wait_warp(&p_free[pb], ((t / C::PBUF) - 1) & 1)) { ok = false; break; }
+        if (t >= 2 && !pf_wait_warp(&f_free[t & 1], ((t >> 1) - 1) & 1)) { ok = false; break; }
+        mbar_arrive_warp(&f_full[t & 1]);
+        mbar_arrive_warp(&p_full[pb]);
+        continue;
+      }
       const uint32_t sc = lane_base + 128 * sb;
       float v[C::HC];
 #pragma unroll
@@ -319,11 +368,11 @@ __global__ void __launch_bounds__(512, 1)
       mbar_arrive_warp(&p_full[pb]);
     }
     tmem_ld_wait();  // no load left in flight on an early exit
-    // ---- the rows' l takes the factor slot after the last tile's
+    // ---- the rows' l and m take the factor slot after the last tile's
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     if (ok && n_t >= 2) ok = pf_wait_warp(&f_free[n_t & 1], ((n_t >> 1) - 1) & 1);
     if (ok) {
-      if (hf == 0) sF[(n_t & 1) * C::BM + i] = make_float2(l, 0.f);
+      if (hf == 0) sF[(n_t & 1) * C::BM + i] = make_float2(l, m);
       mbar_arrive_warp(&f_full[n_t & 1]);
     } else {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
@@ -335,6 +384,7 @@ __global__ void __launch_bounds__(512, 1)
     const int i = threadIdx.x - 32 * C::SW;    // row (TMEM lane i)
     const int it = i / GC, h = h_first + i - it * GC;
     const bool row_ok = it < toks && h < G;
+    const bool live = __any_sync(0xffffffffu, row_ok);
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp - C::SW) * 32) << 16);
     bool ok = true;
     float O[C::DN];  // acc, columns [0, DN)
@@ -352,7 +402,9 @@ __global__ void __launch_bounds__(512, 1)
         if (!pf_wait_warp(&o_full[ob], (n >> 1) & 1)) { ok = false; break; }
         tc_fence_after();
         const uint32_t src = lane_base + C::TM_OT + ob * C::DN;
-        if (hn == 0) {
+        if (!live) {
+          // no rows
+        } else if (hn == 0) {
 #pragma unroll
           for (int c = 0; c < C::DN / 32; ++c) {
             float o[32];
@@ -391,7 +443,9 @@ __global__ void __launch_bounds__(512, 1)
       }
       if (!ok) break;
     }
-    // ---- epilogue: acc / (256 l) as bf16 (every lane loads; rows past the chunk do not store)
+    // ---- epilogue (every lane loads; rows past the chunk do not store): acc / (256 l) as bf16, or
+    // with SPLIT acc as it is, into shared memory over the K and V stages, whose copies and products are
+    // all done: four columns of a row at [column / 4][row]
     if (ok) ok = pf_wait_warp(&f_full[n_t & 1], (n_t >> 1) & 1);
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
@@ -400,17 +454,23 @@ __global__ void __launch_bounds__(512, 1)
       const float l = sF[(n_t & 1) * C::BM + i].x;
       const float f = l == 0.f ? 0.f : 1.f / (256.f * l);  // (a row that sees no key: zero)
       __nv_bfloat16* dst = p.out + (static_cast<long long>(r0 + q0 + it) * p.Hq + g * G + h) * D;
+      float4* part = reinterpret_cast<float4*>(sK);
       auto store32 = [&](int c, const float* x) {
         if (!row_ok) return;
-        uint32_t w[16];
+        if constexpr (SPLIT) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
-          w[j] = *reinterpret_cast<const uint32_t*>(&y);
+          for (int j = 0; j < 8; ++j) part[(8 * c + j) * C::BM + i] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+            w[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          uint4* o4 = reinterpret_cast<uint4*>(dst + 32 * c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o4[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         }
-        uint4* o4 = reinterpret_cast<uint4*>(dst + 32 * c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o4[j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
       };
 #pragma unroll
       for (int c = 0; c < C::DN / 32; ++c) store32(c, O + 32 * c);
@@ -606,16 +666,47 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
+  if constexpr (SPLIT) {
+    // the shares (acc, l, m)_r of every row: M = max m_r, out = sum 2^(m_r - M) acc_r / (256 sum 2^(m_r - M) l_r),
+    // by the softmax warps, whose register budget holds it
+    cluster_sync();
+    const int rows = toks * GC;
+    constexpr int kMergers = 32 * C::SW;
+    for (int e = warp < C::SW ? share * kMergers + threadIdx.x : rows * D; e < rows * (D / 4); e += kMergers * shares) {
+      const int c = e / rows, i = e - c * rows;
+      const int it = i / GC, h = h_first + i - it * GC;
+      if (h >= G) continue;
+      float M = -1e30f, L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < shares; ++r) {
+        const int n_r = (r + 1) * n_all / shares - r * n_all / shares;  // where CTA r left its (l, m)
+        const float2 lm = peer_ld2(peer_address(sF + (n_r & 1) * C::BM + i, r));
+        const float4 x = peer_ld4(peer_address(reinterpret_cast<float4*>(sK) + c * C::BM + i, r));
+        const float mx = fmaxf(M, lm.y), a = ex2(M - mx), w = ex2(lm.y - mx);
+        M = mx;
+        L = fmaf(L, a, w * lm.x);
+        o.x = fmaf(o.x, a, w * x.x);
+        o.y = fmaf(o.y, a, w * x.y);
+        o.z = fmaf(o.z, a, w * x.z);
+        o.w = fmaf(o.w, a, w * x.w);
+      }
+      const float f = L == 0.f ? 0.f : 1.f / (256.f * L);
+      __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + (static_cast<long long>(r0 + q0 + it) * p.Hq + g * G + h) * D + 4 * c);
+      dst[0] = __floats2bfloat162_rn(o.x * f, o.y * f);
+      dst[1] = __floats2bfloat162_rn(o.z * f, o.w * f);
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
 }
 
-template <int D, bool WIN>
-cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, cudaStream_t s) {
+template <int D, bool WIN, bool SPLIT>
+cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, int shares, cudaStream_t s) {
   using C = BlockPrefillCfg<D>;
   CUtensorMap tmk, tmv;
   if (!make_pool_map(&tmk, const_cast<uint8_t*>(p.k_cache), D, p.Hkv, p.num_blocks, C::RB) ||
       !make_pool_map(&tmv, const_cast<uint8_t*>(p.v_cache), D, p.Hkv, p.num_blocks, C::RB))
     return cudaErrorInvalidValue;
-  auto kern = block_prefill_kernel<D, WIN>;
+  auto kern = block_prefill_kernel<D, WIN, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // the warpgroups' register budgets add up to the launch's 128 per thread: a kernel built with
@@ -628,13 +719,32 @@ cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, cudaStream_t s) {
     regs.store(a.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != C::REG_LAUNCH) return cudaErrorInvalidKernelImage;
-  kern<<<grid, C::THREADS, C::SMEM, s>>>(p, tmk, tmv);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute cluster[1];
+  cluster[0].id = cudaLaunchAttributeClusterDimension;
+  cluster[0].val.clusterDim.x = shares;
+  cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
+  cfg.attrs = cluster;
+  cfg.numAttrs = SPLIT ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
+}
+
+template <int D>
+cudaError_t launch_d(const BlockPrefillParams& p, dim3 grid, int shares, cudaStream_t s) {
+  if (shares > 1) {
+    grid.x *= shares;
+    return p.window > 0 ? launch_t<D, true, true>(p, grid, shares, s) : launch_t<D, false, true>(p, grid, shares, s);
+  }
+  return p.window > 0 ? launch_t<D, true, false>(p, grid, 1, s) : launch_t<D, false, false>(p, grid, 1, s);
 }
 
 }  // namespace
 
-cudaError_t launch_block_prefill(BlockPrefillParams p, int D, cudaStream_t s) {
+cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaStream_t s) {
   // the group's heads in as few equal parts of at most 128 as there can be; whole tokens per CTA
   const int G = p.Hq / p.Hkv;
   p.head_parts = (G + 127) / 128;
@@ -643,9 +753,14 @@ cudaError_t launch_block_prefill(BlockPrefillParams p, int D, cudaStream_t s) {
   const long long y = static_cast<long long>(p.Hkv) * p.head_parts;
   if (y > 65535) return cudaErrorInvalidValue;
   const dim3 grid((p.max_q_len + tok - 1) / tok, static_cast<unsigned>(y), p.B);
-  if (p.window > 0)
-    return D == 64 ? launch_t<64, true>(p, grid, s) : D == 128 ? launch_t<128, true>(p, grid, s) : launch_t<256, true>(p, grid, s);
-  return D == 64 ? launch_t<64, false>(p, grid, s) : D == 128 ? launch_t<128, false>(p, grid, s) : launch_t<256, false>(p, grid, s);
+  // CTAs that would leave SMs idle share their key tiles, two at least each
+  const long long ctas = y * grid.x * p.B;
+  const long long keys = p.window > 0 ? std::min<long long>(p.max_blocks * 16LL, static_cast<long long>(p.window) + tok + 128) : p.max_blocks * 16LL;
+  int shares = 1;
+  while (shares < 8 && ctas * shares * 2 <= num_sms && keys >= 128LL * 4 * shares) shares *= 2;
+  if (D == 64) return launch_d<64>(p, grid, shares, s);
+  if (D == 128) return launch_d<128>(p, grid, shares, s);
+  return launch_d<256>(p, grid, shares, s);
 }
 
 }  // namespace fkv

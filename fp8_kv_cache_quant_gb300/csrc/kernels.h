@@ -115,7 +115,7 @@ struct BlockPrefillParams {
   int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads
 };
 
-cudaError_t launch_block_prefill(BlockPrefillParams p, int D, cudaStream_t s);
+cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaStream_t s);
 
 cudaError_t launch_prefill(const PrefillParams& p, int D, bool bf16_layer, void* k_cache, void* v_cache,
                            cudaStream_t s);

@@ -265,6 +265,23 @@ def test_prefill_scales_far_apart(d):
     _check(c.prefill(), c.exact())
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("ctx,new,hq,h,kw", [
+    ([2050], [9], 8, 2, {}), ([1300, 5000, 70], [1, 4, 70], 4, 1, {}), ([3000], [20], 3, 1, dict(window=700)),
+    ([700, 2600], [7, 130], 2, 2, dict(causal=False)), ([4097, 129], [1, 2], 16, 1, dict(softmax_scale=0.3)),
+])
+def test_prefill_few_rows_over_long_contexts(d, ctx, new, hq, h, kw):
+    """Key tiles shared by the CTAs of a cluster, some of which may have none."""
+    c = Case(ctx, hq, h, d, new=new, seed=d + sum(new))
+    _check(c.prefill(**kw), c.exact(**kw))
+
+
+@pytest.mark.parametrize("hq", [130, 200])
+def test_prefill_groups_beyond_128_heads(hq):
+    c = Case([40, 300], hq, 1, 64, new=[3, 2], seed=hq)
+    _check(c.prefill(), c.exact())
+
+
 def test_prefill_leaves_other_rows_and_reports_bad_sequences():
     c = Case([40, 50, 60], 4, 2, 128, new=[10, 20, 30], seed=4)
     q = torch.cat((c.q, c.q[:7])).cuda()
