@@ -96,8 +96,8 @@ FKV_DEV void split4(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
   const float2 ha = make_float2(lead(a.x), lead(a.y)), hb = make_float2(lead(b.x), lead(b.y));
   const float2 neg = make_float2(-1.f, -1.f);
   const float2 la = __ffma2_rn(ha, neg, a), lb = __ffma2_rn(hb, neg, b);
-  hi = static_cast<uint32_t>(f32x2_to_e4m3x2(ha.x, ha.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(hb.x, hb.y)) << 16);
-  lo = static_cast<uint32_t>(f32x2_to_e4m3x2(la.x, la.y)) | (static_cast<uint32_t>(f32x2_to_e4m3x2(lb.x, lb.y)) << 16);
+  hi = f32x4_to_e4m3x4(ha, hb);
+  lo = f32x4_to_e4m3x4(la, lb);
 }
 
 FKV_DEV uint32_t cluster_rank() {
