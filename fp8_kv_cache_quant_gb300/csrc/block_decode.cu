@@ -334,7 +334,6 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // barriers and tensor memory need no input: they are set up before waiting for the kernels
   // before this one
-  griddep_launch_dependents();
   if (warp == 8 && lane == 0) {
     // barriers signalled by the softmax or correction warps count warps (one arrival each)
     mbar_init(q_full, 4);
@@ -423,6 +422,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // the next kernel may take its place on the SMs from here on (not before this CTA has its tensor memory)
+  griddep_launch_dependents();
 
   // sequences without keys: zero rows, spread over the CTAs
   for (int b = k; b < p.B; b += gridDim.x) {

@@ -174,6 +174,11 @@ __global__ void __launch_bounds__(512, 1)
   const int share = SPLIT ? static_cast<int>(cluster_rank()) : 0, shares = SPLIT ? static_cast<int>(cluster_size()) : 1;
   const int qt = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) / shares;
 
+  // SPLIT, whose few CTAs find free SMs while the kernel before ends, is launched with programmatic stream
+  // serialisation.  Its tensor memory, all of an SM's, is allocated after this wait: taken before, it
+  // could be what a CTA of the kernel before still needs to go on.
+  if constexpr (SPLIT) griddep_wait();
+
   // ------------------------------------------------------------ sequence geometry
   const bool first_cta = qt == 0 && share == 0 && blockIdx.y == 0 && threadIdx.x == 0;
   const int r0 = p.cu[b];
@@ -231,6 +236,7 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (SPLIT) griddep_launch_dependents();
 
   if (warp < C::SW) {
     // ============================================================ softmax warps
@@ -724,12 +730,14 @@ cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, int shares, cudaStr
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute cluster[1];
-  cluster[0].id = cudaLaunchAttributeClusterDimension;
-  cluster[0].val.clusterDim.x = shares;
-  cluster[0].val.clusterDim.y = cluster[0].val.clusterDim.z = 1;
-  cfg.attrs = cluster;
-  cfg.numAttrs = SPLIT ? 1 : 0;
+  cudaLaunchAttribute split[2];
+  split[0].id = cudaLaunchAttributeClusterDimension;
+  split[0].val.clusterDim.x = shares;
+  split[0].val.clusterDim.y = split[0].val.clusterDim.z = 1;
+  split[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  split[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = split;
+  cfg.numAttrs = SPLIT ? 2 : 0;
   return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
 }
 
