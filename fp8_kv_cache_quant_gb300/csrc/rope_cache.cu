@@ -98,10 +98,11 @@ constexpr int kRopeThreads = 256;
 // token that it handles: the grid's active threads are a multiple (t_step) of a token's units, so
 // that row and unit are found once and token t is followed by t + t_step.  HBM-bound: the next
 // token's elements, slot and position are loaded before the current token is turned and stored, so
-// that a thread has 32 bytes in flight all the time.
+// that a thread has 32 bytes in flight all the time.  Three CTAs per SM (four spill registers, five more):
+// 65,536 tokens of 32/8 heads at head_dim 128 take 257 us, 5.9 TB/s (280 and 321 us).
 // kPool: 0 e4m3, 1 e5m2, 2 bf16.
 template <int D, int kPool>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_cache_kernel(const RopeCacheParams p, int t_step) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeCacheParams p, int t_step) {
   constexpr int U = D / 16;
   const int per_token = (p.Hq + 2 * p.H) * U;
   const long long gid = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -185,10 +186,11 @@ FKV_DEV float pow2_scale(uint32_t amax_bits) {
 // grid (pages of a sequence's new tokens, sequences, kv_parts + slices of the query rows).
 // CTAs z < kv_parts: K and V of one block, two warps per (KV head, K or V), 8 of its 16 rows each:
 // the rows stay in registers between the maximum and the codes, so that each input byte is read
-// once, and two warps rather than one keep them few enough for three CTAs per SM.  The others turn
-// query rows, four units per thread with all loads up front.
+// once, and two warps rather than one keep them few enough for four CTAs per SM.  The others turn
+// query rows, four units per thread with all loads up front.  HBM-bound: 4 x 16,384 tokens of 32/8
+// heads at head_dim 128 take 275 us, 5.5 TB/s (three CTAs per SM 289 us; six units per thread 323 us).
 template <int D>
-__global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 3 : 2) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
+__global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 2) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
   constexpr int U = D / 16;       // units of a row
   constexpr int TP = 32 / U;      // rows that a warp handles at once
   constexpr int R = 8 / TP;       // rounds
@@ -336,8 +338,8 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 3 : 2) block_cache_k
 template <int D>
 cudaError_t launch_rope(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
   const long long per_token = static_cast<long long>(p.Hq + 2 * p.H) * (D / 16);
-  // as many tokens at once as four CTAs per SM hold
-  const long long t_step = std::min<long long>(p.n_tokens, std::max<long long>(1, 4LL * num_sms * kRopeThreads / per_token));
+  // as many tokens at once as three CTAs per SM hold
+  const long long t_step = std::min<long long>(p.n_tokens, std::max<long long>(1, 3LL * num_sms * kRopeThreads / per_token));
   const unsigned blocks = static_cast<unsigned>((per_token * t_step + kRopeThreads - 1) / kRopeThreads);
   auto kern = pool == 2 ? rope_cache_kernel<D, 2> : pool == 1 ? rope_cache_kernel<D, 1> : rope_cache_kernel<D, 0>;
   kern<<<blocks, kRopeThreads, 0, s>>>(p, static_cast<int>(t_step));
