@@ -510,10 +510,11 @@ __global__ void __launch_bounds__(512, 1)
       int last[C::NS];  // last use of each stage whose copies were issued
 #pragma unroll
       for (int s = 0; s < C::NS; ++s) last[s] = -1;
-      // block id, -1 past the sequence (copied from block 0, its keys masked)
+      // block id, -1 past the sequence and before the first visible key's block, whose table entry may
+      // name a block no longer (copied from block 0, its keys masked)
       auto block_id = [&](int t) -> int {
         const int lb = (tb + t) * C::NBLK + lane;
-        if (lane >= C::NBLK || t >= n_t || lb >= nblk_seq) return -1;
+        if (lane >= C::NBLK || t >= n_t || lb >= nblk_seq || lb < kv_lo >> 4) return -1;
         const int id = trow[lb];
         if (id >= 0 && id < p.num_blocks) return id;
         raise_fault(p.fault, FKV_FAULT_BLOCK_ID);

@@ -515,6 +515,10 @@ fkv_status fp8_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t 
  *                 not part of the cached sequence); with T_b = 0 their rows are zero
  *   out           device bf16 [total_q][num_q_heads][head_dim]; rows of no sequence keep
  *                 their bytes
+ * The codes of the keys that a chunk sees are finite (a NaN one reaches the rows beside those that
+ * see it); behind the last token, and before the chunk's window, there may be any bytes, and table
+ * entries of blocks wholly before it are not read.  A query row that holds a NaN or an infinity
+ * gives a NaN row.
  * A sequence with Lq_b < 0, > max_q_len, > T_b (causal) or rows outside [0, total_q) is skipped
  * and FKV_FAULT_QLEN raised; T_b outside [0, max_blocks * 16] is clamped (FKV_FAULT_CONTEXT).
  */

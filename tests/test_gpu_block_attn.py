@@ -282,6 +282,71 @@ def test_prefill_groups_beyond_128_heads(hq):
     _check(c.prefill(), c.exact())
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_windows_over_evicted_blocks(d):
+    """What lies before the window is gone: blocks taken out of the table, their slots in the window's
+    first block overwritten with NaN codes."""
+    ctx, new, w = [900, 140], [3, 20], 100
+    c = Case(ctx, 4, 2, d, new=new, seed=d)
+    exact = c.exact(window=w)
+    dec = Case(ctx, 4, 2, d, seed=d)
+    dec_exact = dec.exact(window=w)
+    for case, first in ((c, [t - n + 1 - w for t, n in zip(ctx, new)]), (dec, [t - w for t in ctx])):
+        for b, lo in enumerate(first):
+            for p in case.pools:
+                p[case.table[b, lo // 16], :, :lo % 16] = 0x7F
+            case.table[b, :lo // 16] = -1
+    _check(c.prefill(window=w), exact)
+    _check(dec.decode(window=w), dec_exact)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_query_rows_that_are_not_finite_give_nan_and_leave_the_others(d, bad):
+    for new, ctx in ((None, [300, 5000]), ([5, 2], [300, 5000])):
+        c = Case(ctx, 4, 2, d, new=new, seed=d)
+        ref = c.decode() if new is None else c.prefill()
+        c.q[1, 2, 7] = bad
+        out = c.decode() if new is None else c.prefill()
+        assert bool(torch.isnan(out[1, 2]).all())
+        out[1, 2] = ref[1, 2]
+        assert torch.equal(out, ref)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first call of each entry point is a captured one."""
+    code = """
+import torch, fp8_kv_cache_quant_gb300 as f
+f.load_binding()
+i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+k = torch.randn(3, 2, 64, device="cuda").to(torch.bfloat16)
+q = torch.randn(3, 4, 64, device="cuda").to(torch.bfloat16)
+c = f.BlockCache.empty(4, 2, 64)
+tab, ctx, cu = i32(1, 2).view(1, 2), i32(3), i32(0, 3)
+rope = f.Rope(f.Rope.table(40, 64))
+lc, s = f.LayerCache.empty(4, 2, 64), torch.ones(1, device="cuda")
+pos = torch.arange(3, device="cuda")
+ws = f.block_decode_workspace(1, 4, c)
+outs = [torch.empty_like(q) for _ in range(3)]
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    f.kv_rope_cache(None, k, k, pos, pos, rope, lc, s, s)
+    f.kv_block_cache(k, k, cu, 3, c, tab, ctx, rope=rope, q=q, q_out=outs[0])
+    f.fp8_block_prefill_attn(outs[0], cu, 3, c, tab, ctx, out=outs[1])
+    f.fp8_block_decode_attn(outs[0][2:], c, tab, ctx, out=outs[2][:1], workspace=ws)
+g.replay()
+torch.cuda.synchronize()
+assert torch.isfinite(outs[1]).all() and (outs[1][2] - outs[2][0]).float().abs().max() <= 2.0 ** -6 * outs[1][2].float().abs().max()
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_prefill_leaves_other_rows_and_reports_bad_sequences():
     c = Case([40, 50, 60], 4, 2, 128, new=[10, 20, 30], seed=4)
     q = torch.cat((c.q, c.q[:7])).cuda()
