@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(512, 1)
       }
     }
   } else {
-    regs_dec<C::REG_MISC>();
+    if constexpr (C::REG_MISC < C::REG_LAUNCH) regs_dec<C::REG_MISC>();
     if (warp == 12 || warp == 15) {
       // ============================================================ copies: K (12), V (15)
       // Lane j < 8 copies the tile's j-th block; block ids are read two tiles ahead, scales (K
