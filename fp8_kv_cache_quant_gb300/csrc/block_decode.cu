@@ -59,8 +59,10 @@ struct BlockDecodeCfg {
   static constexpr int MPV = D < 128 ? D : 128;   // M of one P.V product
   static constexpr int NS = G == 8 && D <= 128 ? 3 : 2;  // K / V stages
   static constexpr int QSUB = NP * RB;          // bytes of one column block of the query tile
-  static constexpr int PSUB = NP * 128;         // bytes of 128 keys of P^T
-  static constexpr int PTILE = NHALF * PSUB;
+  // P is stored key by key, MN-major: a key's 16 bytes (8 heads' hi, 8 heads' lo; for G = 16 two such
+  // columns, hi and lo) are one store of the thread that owns the key
+  static constexpr int PCOL = BN * 16;            // bytes of a 16-byte column over the tile's keys
+  static constexpr int PTILE = (NP / 16) * PCOL;
   static constexpr int TM_S = 0;                  // S^T buffers: columns [0, 2 NHALF NP)
   static constexpr int TM_O = 2 * NHALF * NP;     // O_t^T buffers
   static constexpr int TM_COLS = TM_O + 2 * NSUB * NP <= 64 ? 64 : TM_O + 2 * NSUB * NP <= 128 ? 128 : 256;
@@ -83,7 +85,7 @@ struct BlockDecodeCfg {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 40;
   static constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, NP, 0, 0);  // K and query K-major
-  static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(MPV, NP, 1, 0);  // V MN-major, P K-major
+  static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(MPV, NP, 1, 1);  // V and P MN-major
   static constexpr int CTAS = D > 128 || G > 8 ? 1 : G == 8 ? 2 : 3;              // per SM
   static_assert(OFF_K % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "tile alignment of the swizzles");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of the resident CTAs");
@@ -205,11 +207,12 @@ FKV_DEV float warp_max_f(float v) {
   return r;
 }
 
-// Two values as e4m3 terms: hi keeps the leading 3 fraction bits, lo the rest.
-FKV_DEV void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const float ha = __uint_as_float(__float_as_uint(a) & 0xFFF00000u), hb = __uint_as_float(__float_as_uint(b) & 0xFFF00000u);
-  hi = f32x2_to_e4m3x2(ha, hb);
-  lo = f32x2_to_e4m3x2(a - ha, b - hb);
+// Four values as e4m3 terms: hi keeps the leading 3 fraction bits, lo the rest.
+FKV_DEV void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
+  auto lead = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); };
+  const float ha = lead(a), hb = lead(b), hc = lead(c), hd = lead(d);
+  hi = f32x4_to_e4m3x4(make_float2(ha, hb), make_float2(hc, hd));
+  lo = f32x4_to_e4m3x4(make_float2(a - ha, b - hb), make_float2(c - hc, d - hd));
 }
 
 // The merge of a unit's pieces, rows row0 .. row0 + ns - 1 of the workspace, by the whole CTA:
@@ -480,11 +483,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
-            uint32_t h0, h1, l0, l1;
-            split2(x0.x * down, x0.y * down, h0, l0);
-            split2(x1.x * down, x1.y * down, h1, l1);
-            wh[j] = h0 | (h1 << 16);
-            wl[j] = l0 | (l1 << 16);
+            split4(x0.x * down, x0.y * down, x1.x * down, x1.y * down, wh[j], wl[j]);
           }
           const int byte = c * 16;
           uint8_t* sub = sQ + (byte / C::RB) * C::QSUB;
@@ -510,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       if (!wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       float x[C::NHALF][G];  // the scores of key i + 128 hh of the tile
+      uint32_t whi[C::NHALF][(G + 3) / 4 < 2 ? 2 : (G + 3) / 4], wlo[C::NHALF][(G + 3) / 4 < 2 ? 2 : (G + 3) / 4];  // P's codes
       float sv[C::NP];
       auto load_s = [&](int hh) {
         const uint32_t col = lane_base + C::TM_S + (sb * C::NHALF + hh) * C::NP;
@@ -559,43 +559,66 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       const int pb = u & 1;
       if (u >= 2 && !wait_warp(&p_free[pb], ((u >> 1) - 1) & 1)) { ok = false; break; }
       if (u >= 2 && !wait_warp(&f_free[pb], ((u >> 1) - 1) & 1)) { ok = false; break; }
+      // four heads at a time (a word of codes): maxima, P's terms, factors
 #pragma unroll
-      for (int h = 0; h < G; h += 2) {
-        constexpr int TWO = G > 1 ? 2 : 1;
-        float pv[C::NHALF][2];
+      for (int h4 = 0; h4 < G; h4 += 4) {
+        constexpr int HN = G < 4 ? G : 4;
+        float tm[4];
+        {
+          const float4 r0 = *reinterpret_cast<const float4*>(red + h4), r1 = *reinterpret_cast<const float4*>(red + LO + h4);
+          const float4 r2 = *reinterpret_cast<const float4*>(red + 2 * LO + h4), r3 = *reinterpret_cast<const float4*>(red + 3 * LO + h4);
+          tm[0] = fmaxf(fmaxf(r0.x, r1.x), fmaxf(r2.x, r3.x));
+          tm[1] = fmaxf(fmaxf(r0.y, r1.y), fmaxf(r2.y, r3.y));
+          tm[2] = fmaxf(fmaxf(r0.z, r1.z), fmaxf(r2.z, r3.z));
+          tm[3] = fmaxf(fmaxf(r0.w, r1.w), fmaxf(r2.w, r3.w));
+        }
+        float pv[C::NHALF][4], al[4], be[4];
 #pragma unroll
-        for (int j = 0; j < TWO; ++j) {
-          const float tmax = fmaxf(fmaxf(red[h + j], red[LO + h + j]), fmaxf(red[2 * LO + h + j], red[3 * LO + h + j]));
+        for (int j = 0; j < 4; ++j) {
+          al[j] = be[j] = 0.f;
+          if (j >= HN) {
+#pragma unroll
+            for (int hh = 0; hh < C::NHALF; ++hh) pv[hh][j] = 0.f;
+            continue;
+          }
+          const int h = h4 + j;
           // one of the two factors is 1, the other 2^-|m - tmax|
-          const float e = ex2(-fabsf(m[h + j] - tmax));
-          const float alpha = m[h + j] > tmax ? 1.f : e, corr = m[h + j] > tmax ? e : 1.f;
+          const float e = ex2(-fabsf(m[h] - tm[j]));
+          const float alpha = m[h] > tm[j] ? 1.f : e, corr = m[h] > tm[j] ? e : 1.f;
           float psum = 0.f;
 #pragma unroll
           for (int hh = 0; hh < C::NHALF; ++hh) {
-            const float w = valid[hh] ? ex2(x[hh][h + j] - tmax) : 0.f;
+            const float w = valid[hh] ? ex2(x[hh][h] - tm[j]) : 0.f;
             psum += w;
             pv[hh][j] = w * rv[hh];
           }
-          lsum[h + j] = fmaf(lsum[h + j], alpha, psum * corr);
-          m[h + j] = fmaxf(m[h + j], tmax);
-          if (i == 0) {
-            f_s[pb * 2 * LO + h + j] = alpha;
-            f_s[pb * 2 * LO + LO + h + j] = corr * vmax;
-          }
+          lsum[h] = fmaf(lsum[h], alpha, psum * corr);
+          m[h] = fmaxf(m[h], tm[j]);
+          al[j] = alpha;
+          be[j] = corr * vmax;
         }
+        if (i == 0) {
+          *reinterpret_cast<float4*>(f_s + pb * 2 * LO + h4) = make_float4(al[0], al[1], al[2], al[3]);
+          *reinterpret_cast<float4*>(f_s + pb * 2 * LO + LO + h4) = make_float4(be[0], be[1], be[2], be[3]);
+        }
+        // the codes of heads h4 .. h4 + 3: words h4 / 4 (hi) and LO / 4 + h4 / 4 (lo) of the key's bytes
 #pragma unroll
         for (int hh = 0; hh < C::NHALF; ++hh) {
           uint32_t hi, lo;
-          split2(pv[hh][0], TWO == 2 ? pv[hh][1] : 0.f, hi, lo);
-          uint8_t* row = sP + pb * C::PTILE + hh * C::PSUB;
-          row[swz(static_cast<uint32_t>(h * 128 + i), 128)] = static_cast<uint8_t>(hi & 0xFF);
-          row[swz(static_cast<uint32_t>((LO + h) * 128 + i), 128)] = static_cast<uint8_t>(lo & 0xFF);
-          if constexpr (TWO == 2) {
-            row[swz(static_cast<uint32_t>((h + 1) * 128 + i), 128)] = static_cast<uint8_t>(hi >> 8);
-            row[swz(static_cast<uint32_t>((LO + h + 1) * 128 + i), 128)] = static_cast<uint8_t>(lo >> 8);
-          }
+          split4(pv[hh][0], pv[hh][1], pv[hh][2], pv[hh][3], hi, lo);
+          whi[hh][h4 / 4] = hi;
+          wlo[hh][h4 / 4] = lo;
         }
-        if constexpr (G >= 8) asm volatile("" ::: "memory");  // two heads at a time: 64 registers
+      }
+#pragma unroll
+      for (int hh = 0; hh < C::NHALF; ++hh) {
+        uint8_t* key = sP + pb * C::PTILE + (128 * hh + i) * 16;
+        if constexpr (G <= 8) {
+          *reinterpret_cast<uint4*>(key) = make_uint4(whi[hh][0], G > 4 ? whi[hh][1] : 0u, wlo[hh][0], G > 4 ? wlo[hh][1] : 0u);
+        } else {
+          *reinterpret_cast<uint4*>(key) = make_uint4(whi[hh][0], whi[hh][1], whi[hh][2], whi[hh][3]);
+          *reinterpret_cast<uint4*>(key + C::PCOL) = make_uint4(wlo[hh][0], wlo[hh][1], wlo[hh][2], wlo[hh][3]);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(&p_full[pb]);
@@ -861,7 +884,9 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
             for (int kk = 0; kk < C::BN / 32; ++kk) {
               const uint64_t ad = smem_desc(sVa + st * C::KTILE + s * C::KSUB + kk * 32 * C::RB, 8 * C::RB, 8 * C::RB, C::SWZ);
-              const uint64_t bd = smem_desc(sPa + pb * C::PTILE + (kk / 4) * C::PSUB + (kk % 4) * 32, 16, 1024, 2);
+              // no swizzle: 8 keys of 16 bytes per 128-byte core matrix, the next 8 keys 128 bytes on, the next
+              // 16 heads PCOL on
+              const uint64_t bd = smem_desc(sPa + pb * C::PTILE + kk * 32 * 16, 128, G > 8 ? C::PCOL : 128, 0);
               umma_f8(tmem + C::TM_O + (pb * C::NSUB + s) * C::NP, ad, bd, C::IDESC_PV, kk > 0 ? 1u : 0u);
             }
           umma_commit(&o_full[pb]);
