@@ -593,6 +593,7 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   const long long blocks = window > 0 ? std::min<long long>(max_blocks, (window + 15LL) / 16 + 1) : max_blocks;
   const int tpb = fkv::block_decode_tile_blocks(cache.head_dim);
   const long long tiles = static_cast<long long>(batch) * cache.num_kv_heads * ((blocks + tpb - 1) / tpb + 1);
+  if (tiles > INT32_MAX) return FKV_UNSUPPORTED;  // the kernel counts them in 32 bits
   const int ctas = static_cast<int>(std::min(plan.ctas, tiles));
   return from_cuda(fkv::launch_block_decode(p, cache.head_dim, ctas, reinterpret_cast<cudaStream_t>(stream)));
 }

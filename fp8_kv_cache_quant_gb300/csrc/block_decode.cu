@@ -135,50 +135,51 @@ struct Cursor {
   FKV_DEV int blocks() const { return min(TPB, ((s.T + 15) >> 4) - block0()); }      // and how many it has
 };
 
-// The range of CTA k: its first tile and their number, the place w0 of that tile, W (places in all) and N,
-// the CTAs that have places.  Every lane of a warp takes part.
+// The range of CTA k: its first tile and their number, the place w0 of that tile, W (places in all, below
+// 2^31) and N, the CTAs that have places.  Every lane of a warp takes part.
 template <int TPB>
-FKV_DEV Cursor<TPB> first_tile(const BlockDecodeParams& p, int k, int& N, long long& w0, long long& W, bool report) {
+FKV_DEV Cursor<TPB> first_tile(const BlockDecodeParams& p, int k, int& N, int& w0, int& W, bool report) {
   const int lane = threadIdx.x & 31;
   auto places = [](int n) { return n > 0 ? n + 1 : 0; };
-  long long total = 0;
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    int n = b0 + lane < p.B ? places(seq_of<TPB>(p, b0 + lane, report).n) : 0;
-    total += __reduce_add_sync(0xffffffffu, n);
-  }
+  auto seq = [&](int b0, bool rep) { return b0 + lane < p.B ? seq_of<TPB>(p, b0 + lane, rep) : Seq{0, 0, 0}; };
+  const Seq s0 = seq(0, report);
+  int total = __reduce_add_sync(0xffffffffu, places(s0.n));
+  for (int b0 = 32; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, places(seq(b0, report).n));
   W = total * p.Hkv;
-  N = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
-  w0 = k < N ? k * W / N : 0;
-  const long long w1 = k < N ? (k + 1) * W / N : 0;
+  N = min(static_cast<int>(gridDim.x), W);
   Cursor<TPB> c;
   c.left = c.b = c.g = c.t = c.piece = 0;
   c.s = Seq{0, 0, 0};
-  if (w1 == w0) return c;
-  long long base = 0;  // places of the sequences before b0
+  w0 = 0;
+  if (k >= N) return c;
+  const int each = W / N, rest = W - each * N;  // floor(k W / N) = k each + floor(k rest / N)
+  w0 = k * each + k * rest / N;
+  const int w1 = (k + 1) * each + (k + 1) * rest / N;
+  int base = 0;  // places of the sequences before b0
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const Seq s = b0 + lane < p.B ? seq_of<TPB>(p, b0 + lane, false) : Seq{0, 0, 0};
+    const Seq s = b0 == 0 ? s0 : seq(b0, false);
     int before = places(s.n);  // inclusive sums over the lanes
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, before, off);
       if (lane >= off) before += x;
     }
-    const unsigned past = __ballot_sync(0xffffffffu, base + static_cast<long long>(before) * p.Hkv > w0);
+    const unsigned past = __ballot_sync(0xffffffffu, base + before * p.Hkv > w0);
     if (past != 0) {
       const int j = __ffs(past) - 1;  // the first sequence that ends behind w0
       c.b = b0 + j;
       c.s.T = __shfl_sync(0xffffffffu, s.T, j);
       c.s.lo = __shfl_sync(0xffffffffu, s.lo, j);
       c.s.n = __shfl_sync(0xffffffffu, s.n, j);
-      const long long rem = w0 - base - static_cast<long long>(__shfl_sync(0xffffffffu, before - places(s.n), j)) * p.Hkv;
-      c.g = static_cast<int>(rem / (c.s.n + 1));
-      c.t = static_cast<int>(rem - static_cast<long long>(c.g) * (c.s.n + 1)) - 1;
+      const int rem = w0 - base - __shfl_sync(0xffffffffu, before - places(s.n), j) * p.Hkv;
+      c.g = rem / (c.s.n + 1);
+      c.t = rem - c.g * (c.s.n + 1) - 1;
       if (c.t < 0) {  // a blank place: its unit's first tile is next
         c.t = 0;
         ++w0;
       }
       // the tiles among places w0 .. w1 - 1: blanks lie at the units' first places
-      long long at = w0 - c.t - 1, blanks = 0;  // the blank place of the current unit
+      int at = w0 - c.t - 1, blanks = 0;  // the blank place of the current unit
       int b = c.b, g = c.g, n = c.s.n;
       for (;;) {
         at += n + 1;
@@ -190,16 +191,27 @@ FKV_DEV Cursor<TPB> first_tile(const BlockDecodeParams& p, int k, int& N, long l
           while (n == 0 && b < p.B);
         }
       }
-      c.left = static_cast<int>(w1 - w0 - blanks);
+      c.left = w1 - w0 - blanks;
       return c;
     }
-    base += static_cast<long long>(__shfl_sync(0xffffffffu, before, 31)) * p.Hkv;
+    base += __shfl_sync(0xffffffffu, before, 31) * p.Hkv;
   }
   return c;
 }
 
-// The CTA whose range holds place w.
-FKV_DEV int cta_of(long long w, long long W, int N) { return static_cast<int>(((w + 1) * N - 1) / W); }
+// The CTA whose range holds place w: floor(((w + 1) N - 1) / W).
+FKV_DEV int cta_of(int w, int W, int N) {
+  const unsigned long long x = static_cast<unsigned long long>(w + 1) * N - 1;
+  return static_cast<int>(x >> 32 ? x / W : static_cast<uint32_t>(x) / static_cast<uint32_t>(W));
+}
+
+// Add 1 to a counter with release and acquire semantics at GPU scope: what this CTA wrote before the
+// barrier in front of it is visible to whom the sum orders behind it.
+FKV_DEV int count_acq_rel(int32_t* p) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
 
 FKV_DEV float warp_max_f(float v) {
   float r;
@@ -371,8 +383,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     tc_fence_before();
   }
   griddep_wait();
-  int N;
-  long long w0, W;
+  int N, w0, W;
   Place at = first_tile<TPB>(p, k, N, w0, W, k == 0 && warp == 0);
   const int n = at.left;  // tiles of this CTA
   // the table's entry of block `lane` of a tile, read ahead of its use and looked at only there (a
@@ -397,29 +408,35 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       for (int s = 0; s < C::NSUB; ++s) tma_load_4d(dst + s * C::KSUB + lane * 16 * C::RB, map, s * C::RB, 0, c.g, id, full);
     }
   };
-  // The producer warps start before the CTA's barrier: the barriers that they use are initialised by
-  // warp 8 itself, and warp 9 waits for the CTA's barrier.
-  const int n0 = min(C::NS, n);
-  int id = 0;
+  // The loads that the first tile waits for go out before the CTA's barrier and before the first copies of K
+  // and V, which fill the memory system's queues for some microseconds: the query rows (softmax
+  // warps, 8 threads per row), the first tiles' block ids (warp 8).
+  constexpr int NCH = (D / 16 + 7) / 8;  // 16-element chunks of a query row per thread
+  uint32_t in[NCH][8];
+  auto load_query = [&](const Place& c) {
+    const int row = threadIdx.x >> 3;
+#pragma unroll
+    for (int cc = 0; cc < NCH; ++cc) {
+      const int ch = (threadIdx.x & 7) + 8 * cc;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
+      if (row < G && ch < D / 16) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(c.b) * p.Hq + c.g * G + row) * D) + 2 * ch;
+        const uint4 a = src[0], a2 = src[1];
+        in[cc][0] = a.x; in[cc][1] = a.y; in[cc][2] = a.z; in[cc][3] = a.w;
+        in[cc][4] = a2.x; in[cc][5] = a2.y; in[cc][6] = a2.z; in[cc][7] = a2.w;
+      }
+    }
+  };
+  if (warp < 4 && n > 0) load_query(at);
+  const int n0 = min(C::NS, n);  // tiles whose copies warp 8 issues first, K and V
+  int ids[C::NS];
   if (warp == 8 && n > 0) {
-    __syncwarp();
-    // the first tiles' K and V, so that the first latency overlaps the rest of the prologue
     Place c = at;
-    int ids[C::NS];
 #pragma unroll
     for (int j = 0; j < C::NS; ++j) {
       ids[j] = block_id(c);
       if (j + 1 < C::NS) c.advance(p);
-    }
-    c = at;
-#pragma unroll
-    for (int j = 0; j < C::NS; ++j) {
-      if (j >= n0) break;
-      const int x = checked(ids[j]);
-      if (j == 0) id = x;
-      copy_tile(&tmk, sK + j * C::KTILE, c, x, &k_full[j]);
-      copy_tile(&tmv, sV + j * C::KTILE, c, x, &v_full[j]);
-      c.advance(p);
     }
   }
   __syncthreads();
@@ -429,11 +446,12 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   griddep_launch_dependents();
 
   // sequences without keys: zero rows, spread over the CTAs
-  for (int b = k; b < p.B; b += gridDim.x) {
-    if (seq_of<TPB>(p, b, false).n != 0) continue;
-    for (int x = threadIdx.x; x < p.Hq * D / 8; x += kThreads)
-      reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.Hq * D)[x] = make_uint4(0u, 0u, 0u, 0u);
-  }
+  if (warp >= 4 && warp < 8)
+    for (int b = k; b < p.B; b += gridDim.x) {
+      if (seq_of<TPB>(p, b, false).n != 0) continue;
+      for (int x = threadIdx.x - 128; x < p.Hq * D / 8; x += 128)
+        reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.Hq * D)[x] = make_uint4(0u, 0u, 0u, 0u);
+    }
 
   if (n == 0) {
     // more CTAs than tiles
@@ -450,24 +468,13 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         // last piece's query are done: their S was read).  8 threads per row.  A row with a NaN or
         // an infinity makes its scores, and so its output, NaN.
         fresh = false;
-        constexpr int NCH = (D / 16 + 7) / 8;  // 16-element chunks per thread
         const int row = i >> 3;
+        if (at.piece > 0) load_query(at);
         uint32_t amax = 0;
-        uint32_t in[NCH][8];
 #pragma unroll
-        for (int cc = 0; cc < NCH; ++cc) {
-          const int c = (i & 7) + 8 * cc;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
-          if (row < G && c < D / 16) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<size_t>(at.b) * p.Hq + at.g * G + row) * D) + 2 * c;
-            const uint4 a = src[0], a2 = src[1];
-            in[cc][0] = a.x; in[cc][1] = a.y; in[cc][2] = a.z; in[cc][3] = a.w;
-            in[cc][4] = a2.x; in[cc][5] = a2.y; in[cc][6] = a2.z; in[cc][7] = a2.w;
-          }
+        for (int cc = 0; cc < NCH; ++cc)
 #pragma unroll
           for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
-        }
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
         const int e = max(static_cast<int>(amax >> 23) - 127 - 7, -126);  // q = q' * 2^e
@@ -667,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
       for (int s2 = 0; s2 < C::NSUB; ++s2) acc[s2][h] = 0.f;
     bool ok = true;
-    long long w = w0;  // the tile's place
+    int w = w0;  // the tile's place
     for (int u = 0; u < n; ++u) {
       if ((u & 7) == 7 && abort_warp(abort_s)) ok = false;
       const int ob = u & 1;
@@ -703,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         // ---- the piece's result: o = acc / (256 l), lse = m + log2 l
         const int r = at.piece;
         const int unit = at.b * p.Hkv + at.g;
-        const long long u0 = w - at.t;  // the place of the unit's first tile
+        const int u0 = w - at.t;  // the place of the unit's first tile
         const int k0 = cta_of(u0, W, N), ns = cta_of(u0 + at.s.n - 1, W, N) - k0 + 1;
         if (ok) ok = wait_warp(&l_full[r & 1], (r >> 1) & 1);
         if (ok) {
@@ -748,8 +755,21 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     }
   } else if (warp == 8) {
     // ============================================================ K copies and scales
-    // K(u) into stage u % NS once the S^T of tile u - NS has read it (the first NS went out in the
-    // prologue); the scales of tile u into their slot.
+    // K(u) into stage u % NS once the S^T of tile u - NS has read it, the first NS with their V at
+    // once; the scales of tile u into their slot.
+    int id = 0;
+    {
+      Place c = at;
+#pragma unroll
+      for (int j = 0; j < C::NS; ++j) {
+        if (j >= n0) break;
+        const int x = checked(ids[j]);
+        if (j == 0) id = x;
+        copy_tile(&tmk, sK + j * C::KTILE, c, x, &k_full[j]);
+        copy_tile(&tmv, sV + j * C::KTILE, c, x, &v_full[j]);
+        c.advance(p);
+      }
+    }
     Place nx = at;
     nx.advance(p);
     int id_next = block_id(nx);
@@ -807,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     // Lane 0 polls the pipeline's barriers without blocking and issues, in whatever order they
     // become possible, the V loads, the S^T products and the P.V products.
     const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV), sPa = smem_u32(sP);
-    int tq = 0, tp = 0, tv = n0;  // next S^T, P.V and V load (the first n0 V loads: prologue)
+  int tq = 0, tp = 0, tv = n0;  // next S^T, P.V and V load (the first n0 V loads: warp 8)
     Place vat = at, qat = at, pat = at;
     for (int j = 0; j < n0; ++j) vat.advance(p);
     bool q_ready = false;  // the query of tile tq's piece is in place
@@ -919,7 +939,6 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     }
     __syncwarp();
   }
-  __threadfence();  // the pieces, before they are counted
   __syncthreads();
   if (warp == 9) {
     tc_fence_after();
@@ -930,14 +949,13 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     const int unit = pend_s[3 * j], k0 = pend_s[3 * j + 1], ns = pend_s[3 * j + 2];
     if (ns == 0) continue;
     if (threadIdx.x == 0) {
-      const int old = atomicAdd(&p.done[unit], 1);
+      const int old = count_acq_rel(&p.done[unit]);
       if (old >= ns) raise_fault(p.fault, FKV_FAULT_WORKSPACE);
       if (old == ns - 1) p.done[unit] = 0;
       *last_s = old == ns - 1;
     }
     __syncthreads();
     if (*last_s) {
-      __threadfence();
       merge_pieces<D, G>(p, unit, static_cast<long long>(k0) + unit, ns, reinterpret_cast<float*>(sK));
     }
     __syncthreads();
