@@ -161,7 +161,9 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
 // ---------------------------------------------------------------- kv_block_cache
 
 constexpr int kBlockThreads = 256;
-constexpr int kBlockTasks = kBlockThreads / 64;  // (KV head, K or V) pairs per CTA, two warps each
+// warps per (KV head, K or V) of a block, and how many of those a CTA takes
+constexpr int block_warps(int D) { return D <= 128 ? 2 : 4; }
+constexpr int block_tasks(int D) { return kBlockThreads / 32 / block_warps(D); }
 constexpr int kQueryLoads = 4;
 constexpr int kQueryItems = kQueryLoads * kBlockThreads;  // units of the query rows per CTA
 
@@ -184,16 +186,17 @@ FKV_DEV float pow2_scale(uint32_t amax_bits) {
 }
 
 // grid (pages of a sequence's new tokens, sequences, kv_parts + slices of the query rows).
-// CTAs z < kv_parts: K and V of one block, two warps per (KV head, K or V), 8 of its 16 rows each:
-// the rows stay in registers between the maximum and the codes, so that each input byte is read
-// once, and two warps rather than one keep them few enough for four CTAs per SM.  The others turn
+// CTAs z < kv_parts: K and V of one block, two (head_dim 256: four) warps per (KV head, K or V), which
+// share its 16 rows: the rows stay in registers between the maximum and the codes, so that each
+// input byte is read once, and several warps keep them few enough for four CTAs per SM.  The others turn
 // query rows, four units per thread with all loads up front.  HBM-bound: 4 x 16,384 tokens of 32/8
 // heads at head_dim 128 take 275 us, 5.5 TB/s (three CTAs per SM 289 us; six units per thread 323 us).
 template <int D>
-__global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 2) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
+__global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
   constexpr int U = D / 16;       // units of a row
   constexpr int TP = 32 / U;      // rows that a warp handles at once
-  constexpr int R = 8 / TP;       // rounds
+  constexpr int WT = block_warps(D);
+  constexpr int R = 16 / WT / TP; // rounds
   __shared__ uint32_t amax_s[kBlockThreads / 32];
   const int b = blockIdx.y;
   const int r0 = p.cu[b], L = p.cu[b + 1] - r0, T = p.ctx[b];
@@ -255,12 +258,12 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 2) block_cache_k
   }
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int task = blockIdx.z * kBlockTasks + (warp >> 1);
-  if (task >= 2 * p.H) return;  // both warps of the pair
+  const int task = blockIdx.z * block_tasks(D) + warp / WT, part = warp % WT;
+  if (task >= 2 * p.H) return;  // all warps of the task
   const int g = task >> 1;
   const bool is_v = task & 1;
   const int u = lane % U, rot = is_v ? 0 : p.rot;
-  const int slot0 = 8 * (warp & 1) + lane / U;  // this lane's row in round 0
+  const int slot0 = (16 / WT) * part + lane / U;  // this lane's row in round 0
   int ca, cb;
   unit_chunks(u, rot, p.interleaved, ca, cb);
   const __nv_bfloat16* src = is_v ? p.v : p.k;
@@ -302,16 +305,18 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 2) block_cache_k
   }
   amax = __reduce_max_sync(0xffffffffu, amax);
   if (lane == 0) amax_s[warp] = amax;
-  // the pair's barrier; both warps have read the old scale before it is replaced below
-  asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-  float s = pow2_scale(max(amax, amax_s[warp ^ 1]));
+  // the task's barrier; its warps have read the old scale before it is replaced below
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WT), "n"(32 * WT) : "memory");
+#pragma unroll
+  for (int w = 0; w < WT; ++w) amax = max(amax, amax_s[warp - part + w]);
+  float s = pow2_scale(amax);
   uint8_t* block = (is_v ? p.vc : p.kc) + (static_cast<size_t>(id) * p.H + g) * 16 * D;
   if (kept > 0 && old >= 1.17549435e-38f && old <= 3.402823466e+38f) {  // a normal positive number
     if (old >= s) {
       s = old;
     } else {
       const float r = __fdiv_rn(old, s);
-      for (int i = lane + 32 * (warp & 1); i < kept * D / 16; i += 64) {
+      for (int i = lane + 32 * part; i < kept * D / 16; i += 32 * WT) {
         uint4* q4 = reinterpret_cast<uint4*>(block) + i;
         uint4 w = *q4;
         w.x = rescale4(w.x, r);
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 2) block_cache_k
       }
     }
   }
-  if (lane == 0 && (warp & 1) == 0) *scale = s;
+  if (lane == 0 && part == 0) *scale = s;
   const float inv = __frcp_rn(s);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -358,7 +363,7 @@ cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s)
   // pages that max_q_len tokens can touch, wherever the first of them lies in its block
   const unsigned pages = static_cast<unsigned>((static_cast<long long>(p.max_q_len) + 14) / 16 + 1);
   const long long items = static_cast<long long>(std::min(16, p.max_q_len)) * p.Hq * (D / 16);
-  const int kv_parts = (2 * p.H + kBlockTasks - 1) / kBlockTasks;
+  const int kv_parts = (2 * p.H + block_tasks(D) - 1) / block_tasks(D);
   const dim3 grid(pages, p.B, static_cast<unsigned>(kv_parts + (items + kQueryItems - 1) / kQueryItems));
   auto kern = D == 64 ? block_cache_kernel<64> : D == 128 ? block_cache_kernel<128> : block_cache_kernel<256>;
   kern<<<grid, kBlockThreads, 0, s>>>(p, kv_parts);
