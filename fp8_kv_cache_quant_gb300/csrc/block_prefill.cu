@@ -320,7 +320,10 @@ __global__ void __launch_bounds__(512, 1)
       const float4 ks4 = *reinterpret_cast<const float4*>(scl), lv4 = *reinterpret_cast<const float4*>(scl + 8),
                    iv4 = *reinterpret_cast<const float4*>(scl + 16);
       const float vmax = sSc[(t % C::SCN) * C::SCF + 24];
-      const float cb[4] = {cst * ks4.x, cst * ks4.y, cst * ks4.z, cst * ks4.w};
+      // (plus 2^-126, so that a hidden score of -inf stays one where the product is zero: a row of zeros, a
+      // K scale of zero; |S| < 2^26, so that this adds less than 2^-100 to a score)
+      constexpr float kLeast = 1.17549435e-38f;
+      const float cb[4] = {fmaf(cst, ks4.x, kLeast), fmaf(cst, ks4.y, kLeast), fmaf(cst, ks4.z, kLeast), fmaf(cst, ks4.w, kLeast)};
       const int kbase = (tb + t) * C::BN + c0;  // key of this thread's first column
       const int lim = lim_row - kbase, lo = WIN ? lo_row - kbase : -(1 << 30);
       const bool full = lim >= C::HC && (!WIN || lo <= 0);
@@ -556,15 +559,14 @@ __global__ void __launch_bounds__(512, 1)
         last[st] = use;
         if (is_k) {
           // the tile's scales.  lv is kept above -32 (a V scale 2^-40 of the tile's largest, zeros
-          // too, whose P falls below the terms' range), so that its inverse stays finite; ks above
-          // 2^-100, so that a hidden score of -inf stays one.
+          // too, whose P falls below the terms' range), so that its inverse stays finite.
           float vmax = vs;
 #pragma unroll
           for (int off = 4; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
           const float lv = vs > 0.f ? fmaxf(lg2(__fdividef(vs, vmax)) + 8.f, -32.f) : -32.f;
           float* slot = sSc + (t % C::SCN) * C::SCF;
           if (lane < C::NBLK) {
-            slot[lane] = fmaxf(ks, 7.888609e-31f);
+            slot[lane] = ks;
             slot[8 + lane] = lv;
             slot[16 + lane] = ex2(-lv);
           }

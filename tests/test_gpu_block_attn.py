@@ -276,6 +276,43 @@ def test_prefill_few_rows_over_long_contexts(d, ctx, new, hq, h, kw):
     _check(c.prefill(**kw), c.exact(**kw))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_and_blocks_of_zeros(d):
+    """Query rows of zeros (and tiny ones) over blocks of zero keys, whose scale the append sets to 2^-126, and
+    blocks of scale zero: the keys they see weigh alike, the masked ones nothing."""
+    for new in (None, [200, 77, 1]):
+        for window in (0, 40):
+            c = Case([500, 77, 130], 4, 2, d, new=new, seed=d)
+            c.q[:, 1] = 0
+            c.q[::3] = 0
+            c.q[1::5] *= 2.0 ** -120
+            zero = c.table[0, 1:31:2]
+            c.pools[0][zero] = 0
+            c.scales[0][zero] = 2.0 ** -126
+            c.scales[0][c.table[0, 2:31:4]] = 0.0
+            c.pools[0][c.table[2]] = np.where(c.pools[0][c.table[2]] & 0x7F == 0x7F, 0x7F, 0)
+            c.scales[0][c.table[2]] = 2.0 ** -126
+            _check(c.decode(window=window) if new is None else c.prefill(window=window), c.exact(window=window), (new, window))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_subnormal_value_scales(d):
+    """Scales on both sides of the smallest normal number (outputs are normal bf16 numbers, whose step at
+    2^-126 is within the tolerance's 2^-10 V)."""
+    for new in (None, [200, 77]):
+        c = Case([500, 77], 4, 2, d, new=new, seed=d)
+        c.scales[1] = (c.scales[1].astype(np.float64) * 2.0 ** -119).astype(np.float32)
+        c.scales[1][c.table[1]] = 2.0 ** -128
+        _check(c.decode() if new is None else c.prefill(), c.exact(), new)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_last_wave_in_clusters(d):
+    """More CTAs than SMs over a long context, in clusters of two; one sequence of few queries among them."""
+    c = Case([8230, 8300], 32, 4, d, new=[317, 5], seed=d)
+    _check(c.prefill(), c.exact())
+
+
 @pytest.mark.parametrize("hq", [130, 200])
 def test_prefill_groups_beyond_128_heads(hq):
     c = Case([40, 300], hq, 1, 64, new=[3, 2], seed=hq)
