@@ -165,13 +165,17 @@ struct BlockDecodePlan {
   size_t cnt_bytes = 0, lse_bytes = 0, o_bytes = 0;
 };
 
+// Places that the counters have at least, so that the scratch of one call never lies where a call of
+// another batch counts.
+constexpr long long kBlockDecodeCounters = 16384;
+
 BlockDecodePlan plan_block_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
   const int G = Hq / Hkv;
   const long long units = static_cast<long long>(B) * Hkv;
   BlockDecodePlan plan;
   plan.ctas = std::min<long long>(static_cast<long long>(current_num_sms()) * fkv::block_decode_ctas_per_sm(D, G), 160 * units);
   const size_t rows = static_cast<size_t>(plan.ctas + units) * G;
-  plan.cnt_bytes = align256(units * sizeof(int32_t));
+  plan.cnt_bytes = align256(std::max(units, kBlockDecodeCounters) * sizeof(int32_t));
   plan.lse_bytes = align256(rows * sizeof(float));
   plan.o_bytes = rows * D * sizeof(float);
   return plan;

@@ -129,6 +129,16 @@ def test_decode_range_of_many_short_units():
     _check(c.decode(), c.exact())
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_workspace_serves_other_batches(d):
+    """A batch that shrinks and grows again, and other heads, over one workspace that is never cleared."""
+    cases = [Case([700] * 90, 8, 2, d, seed=1), Case([4000, 10], 8, 2, d, seed=2), Case([2500], 2, 2, 64, seed=3)]
+    fresh = [c.decode() for c in cases]
+    ws = f.block_decode_workspace(90, 8, cases[0].cache())
+    for i in (0, 1, 0, 2, 1, 2, 0):
+        assert torch.equal(cases[i].decode(workspace=ws), fresh[i]), i
+
+
 def test_decode_replays_with_other_contexts():
     """A captured launch with other context lengths than it was captured with."""
     full = [700, 300, 1100]
