@@ -389,18 +389,24 @@ def load_binding():
     return _compiled
 
 
+def _current(stream, index):
+    """A context in which the raw stream of device `index` is the current one."""
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index))
+
+
 def _call(fn, on, stream, *args):
-    """fn of the compiled binding, with the device of the tensor `on` current; stream None: that device's current
-    stream.  Returns its tensor."""
+    """fn of the compiled binding, with the device of the tensor `on` and the stream current (what the call
+    allocates belongs to that stream); stream None: that device's current stream.  Returns its tensor."""
     index = on.get_device()
     if index < 0:
         raise ValueError(f"{fn}: the tensors are not on a CUDA device")
     call = getattr(_compiled or load_binding(), fn)
-    s = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-    if index == torch._C._cuda_getDevice():
+    current = torch._C._cuda_getCurrentRawStream(index)
+    s = current if stream is None else _stream(stream)
+    if s == current and index == torch._C._cuda_getDevice():
         st, out = call(s, *args)
     else:
-        with torch.cuda.device(index):
+        with _current(s, index):
             st, out = call(s, *args)
     if st != OK:
         _check(fn, st)
@@ -432,14 +438,16 @@ def fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_
     return int(load_library().fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim))
 
 
-def block_decode_workspace(batch, num_q_heads, cache: BlockCache):
-    """A zero-filled workspace of fp8_block_decode_attn (calls that may overlap on the GPU each need one)."""
-    if not cache.k_cache.is_cuda:
+def block_decode_workspace(batch, num_q_heads, cache: BlockCache, stream=None):
+    """A workspace of fp8_block_decode_attn, zero-filled on the stream (calls that may overlap on the GPU each
+    need one)."""
+    index = cache.k_cache.get_device()
+    if index < 0:
         raise ValueError("fp8_block_decode_attn: the tensors are not on a CUDA device")
     _, h, _, d = cache.k_cache.shape
-    with torch.cuda.device(cache.k_cache.device):
+    with torch.cuda.device(index) if stream is None else _current(_stream(stream), index):
         n = fp8_block_decode_attn_workspace_size(batch, num_q_heads, h, d)
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k_cache.device)
+        return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k_cache.device)
 
 
 def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softmax_scale=0.0, window=0, out=None,
@@ -447,7 +455,7 @@ def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softm
     """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.
     ``workspace``: of block_decode_workspace (one is made for the call when None)."""
     if workspace is None:
-        workspace = block_decode_workspace(q.shape[0], q.shape[1], cache)
+        workspace = block_decode_workspace(q.shape[0], q.shape[1], cache, stream)
     return _call("fp8_block_decode_attn", q, stream, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
                  context_lens, softmax_scale, window, out, workspace, fault)
 

@@ -139,6 +139,30 @@ def test_decode_workspace_serves_other_batches(d):
         assert torch.equal(cases[i].decode(workspace=ws), fresh[i]), i
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_call_on_another_stream_makes_its_tensors_there(raw):
+    """The workspace and the output that a call makes belong to the stream it is given, also while the
+    current stream is busy and free memory holds other bytes."""
+    c = Case([3000, 40], 8, 2, 128, seed=5)
+    p = Case([300, 40], 8, 2, 128, new=[20, 3], seed=6)
+    ref, pref = c.decode(), p.prefill()
+    fault = torch.zeros(1, dtype=torch.int32, device="cuda")
+    args = (c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx))
+    pargs = (p.q.cuda(), _i32(p.cu), p.max_new, p.cache(), _i32(p.table), _i32(p.ctx))
+    dirty = f.block_decode_workspace(2, 8, args[1]).fill_(255)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del dirty
+    torch.cuda._sleep(100_000_000)
+    given = s.cuda_stream if raw else s
+    out = f.fp8_block_decode_attn(*args, fault=fault, stream=given)
+    pout = f.fp8_block_prefill_attn(*pargs, fault=fault, stream=given)
+    with torch.cuda.stream(s):
+        got, pgot, bits = out.cpu(), pout.cpu(), fault.cpu()
+    assert int(bits) == 0
+    assert torch.equal(got, ref.cpu()) and torch.equal(pgot, pref.cpu())
+
+
 def test_decode_replays_with_other_contexts():
     """A captured launch with other context lengths than it was captured with."""
     full = [700, 300, 1100]
