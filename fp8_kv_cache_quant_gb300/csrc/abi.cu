@@ -157,6 +157,9 @@ bool valid_block_pools(const fkv_block_cache& c) {
          aligned(c.k_scale, 4) && aligned(c.v_scale, 4);
 }
 
+// Columns of a block table whose positions (and a tile more) the kernels count in 32 bits.
+constexpr int32_t kMaxTableBlocks = (1 << 27) - 64;
+
 // The block-scaled decode: CTAs resident at once, of which a unit (sequence, KV head) is given at
 // most 160 (the merge of its pieces grows with them: 0.05 us each, a tile of its own 1.5 us), and the
 // workspace: piece counters, the pieces' log-sum-exps and outputs.
@@ -493,7 +496,7 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
   if (n_tokens < 0 || batch < 0 || max_q_len < 0 || max_blocks <= 0 || num_q_heads < 0) return FKV_INVALID_ARG;
   fkv_status st = check_block_cache(cache);
   if (st != FKV_OK) return st;
-  if (batch > 65535 || num_q_heads > 8192 || cache.num_kv_heads > 8192) return FKV_UNSUPPORTED;
+  if (batch > 65535 || num_q_heads > 8192 || cache.num_kv_heads > 8192 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
   if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   const bool turned = rope.cos_sin != nullptr;
   if (turned) {
@@ -531,7 +534,7 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
   p.block_table = block_table;
   p.n_tokens = n_tokens;
   p.B = batch;
-  p.max_q_len = max_q_len;
+  p.max_q_len = std::min(max_q_len, n_tokens);  // (longer ones have rows beyond n_tokens)
   p.Hq = num_q_heads;
   p.H = cache.num_kv_heads;
   p.num_blocks = cache.num_blocks;
@@ -563,7 +566,7 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   const int G = num_q_heads / cache.num_kv_heads;
   if (!supported_group(G, cache.head_dim)) return FKV_UNSUPPORTED;
   if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return FKV_INVALID_ARG;
-  if (batch > 65535 || num_q_heads > 65535) return FKV_UNSUPPORTED;
+  if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
   if (batch == 0) return FKV_OK;
   if (!q || !out || !block_table || !context_lens || !valid_block_pools(cache)) return FKV_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4))
@@ -613,7 +616,7 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
   if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale) || window < 0) return FKV_INVALID_ARG;
   if (window > 0 && !causal) return FKV_UNSUPPORTED;  // a window is causal
-  if (batch > 65535 || num_q_heads > 65535) return FKV_UNSUPPORTED;
+  if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
   if (total_q == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
   if (!q || !cu_seqlens_q || !block_table || !context_lens || !out || !valid_block_pools(cache)) return FKV_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) ||
@@ -634,7 +637,7 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   p.Hkv = cache.num_kv_heads;
   p.num_blocks = cache.num_blocks;
   p.max_blocks = max_blocks;
-  p.max_q_len = max_q_len;
+  p.max_q_len = std::min(max_q_len, total_q);  // (longer ones have rows beyond total_q)
   p.total_q = total_q;
   p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
   p.causal = causal != 0;

@@ -763,7 +763,7 @@ cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaS
   const int tok = 128 / p.part_heads;
   const long long y = static_cast<long long>(p.Hkv) * p.head_parts;
   if (y > 65535) return cudaErrorInvalidValue;
-  const dim3 grid((p.max_q_len + tok - 1) / tok, static_cast<unsigned>(y), p.B);
+  const dim3 grid(static_cast<unsigned>((p.max_q_len - 1LL) / tok + 1), static_cast<unsigned>(y), p.B);
   // CTAs that would leave SMs idle share their key tiles, two at least each
   const long long ctas = y * grid.x * p.B;
   const long long keys = p.window > 0 ? std::min<long long>(p.max_blocks * 16LL, static_cast<long long>(p.window) + tok + 128) : p.max_blocks * 16LL;

@@ -253,7 +253,8 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
  *   q, q_out, k, v, strides  as for kv_rope_cache; q needs rope.cos_sin
  *   n_tokens      rows of q, k and v
  *   cu_seqlens    device int32 [batch + 1], non-decreasing, starting at 0
- *   max_q_len     host upper bound of every L_b (sizes the grid)
+ *   max_q_len     host upper bound of every L_b (sizes the grid; any above n_tokens serves as n_tokens)
+ *   max_blocks    columns of block_table, below 2^27 - 63 here and in the attention over these pools
  *   rope          cos_sin NULL (rot_dim 0): no rotation
  * A sequence with L_b < 0, > max_q_len or > T_b or rows outside [0, n_tokens) is skipped and
  * FKV_FAULT_QLEN raised; one whose T_b is outside [0, max_blocks * 16] likewise with
@@ -510,7 +511,7 @@ fkv_status fp8_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t 
  * scales of each block and KV head; query and P precision as for fp8_block_decode_attn.
  *   q             device bf16 [total_q][num_q_heads][head_dim]
  *   cu_seqlens_q  device int32 [batch + 1], non-decreasing, starting at 0, at most total_q
- *   max_q_len     host upper bound of every Lq_b (sizes the grid)
+ *   max_q_len     host upper bound of every Lq_b (sizes the grid; any above total_q serves as total_q)
  *   context_lens  T_b; with causal != 0, Lq_b <= T_b.  Without, any Lq_b (queries that are
  *                 not part of the cached sequence); with T_b = 0 their rows are zero
  *   out           device bf16 [total_q][num_q_heads][head_dim]; rows of no sequence keep

@@ -88,7 +88,7 @@ def test_block_cache_invalid(lib, kw):
     assert _block_cache(lib, **kw) == f.INVALID_ARG
 
 
-@pytest.mark.parametrize("kw", [dict(cache=_block(bs=32)), dict(cache=_block(D=80)), dict(b=65536), dict(rope=_rope(rot=8))])
+@pytest.mark.parametrize("kw", [dict(cache=_block(bs=32)), dict(cache=_block(D=80)), dict(b=65536), dict(mb=2 ** 27), dict(rope=_rope(rot=8))])
 def test_block_cache_unsupported(lib, kw):
     assert _block_cache(lib, **kw) == f.UNSUPPORTED
 
@@ -109,7 +109,7 @@ def test_block_decode_invalid(lib, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(hq=6), dict(hq=64), dict(hq=32, cache=_block(D=256)), dict(cache=_block(D=32)), dict(cache=_block(bs=1)),
-                                dict(b=65536)])
+                                dict(b=65536), dict(mb=2 ** 27)])
 def test_block_decode_unsupported(lib, kw):
     assert _decode(lib, **kw) == f.UNSUPPORTED
 
@@ -138,7 +138,7 @@ def test_block_prefill_invalid(lib, kw):
     assert _prefill(lib, **kw) == f.INVALID_ARG
 
 
-@pytest.mark.parametrize("kw", [dict(win=3, causal=0), dict(cache=_block(D=48)), dict(b=65536), dict(hq=65536 * 2)])
+@pytest.mark.parametrize("kw", [dict(win=3, causal=0), dict(cache=_block(D=48)), dict(b=65536), dict(mb=2 ** 27), dict(hq=65536 * 2)])
 def test_block_prefill_unsupported(lib, kw):
     assert _prefill(lib, **kw) == f.UNSUPPORTED
 

@@ -347,6 +347,21 @@ def test_prefill_last_wave_in_clusters(d):
     _check(c.prefill(), c.exact())
 
 
+def test_lengths_bounded_by_the_largest_integer():
+    """max_q_len may be any upper bound."""
+    c = Case([300, 40], 4, 2, 128, new=[20, 3], seed=6)
+    ref = c.prefill()
+    c.max_new = 2 ** 31 - 1
+    assert torch.equal(c.prefill(), ref)
+    k = torch.randn(23, 2, 128, device="cuda").to(torch.bfloat16)
+    pools = []
+    for most in (20, 2 ** 31 - 1):
+        cache = c.cache()
+        f.kv_block_cache(k, k, _i32(c.cu), most, cache, _i32(c.table), _i32(c.ctx))
+        pools.append(cache)
+    assert torch.equal(pools[0].k_cache, pools[1].k_cache) and torch.equal(pools[0].v_scale, pools[1].v_scale)
+
+
 @pytest.mark.parametrize("hq", [130, 200])
 def test_prefill_groups_beyond_128_heads(hq):
     c = Case([40, 300], hq, 1, 64, new=[3, 2], seed=hq)
