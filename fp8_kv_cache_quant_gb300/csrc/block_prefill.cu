@@ -744,13 +744,54 @@ cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, int shares, cudaStr
   return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
 }
 
+// Clusters of that many CTAs that the current device holds at once: fewer than its SMs over the size, since
+// a cluster stays within a group of SMs.  Asked once per device and size.
+template <int D, bool WIN>
+int clusters_at_once(int shares) {
+  using C = BlockPrefillCfg<D>;
+  constexpr int kDevices = 16;
+  static std::atomic<int> known[kDevices][9];  // the number plus 1
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kDevices && (n = known[dev][shares].load(std::memory_order_relaxed)) != 0) return n - 1;
+  auto kern = block_prefill_kernel<D, WIN, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(shares);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeClusterDimension;
+  a[0].val.clusterDim.x = shares;
+  a[0].val.clusterDim.y = a[0].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  if (dev < kDevices) known[dev][shares].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+template <int D, bool WIN>
+cudaError_t launch_w(const BlockPrefillParams& p, dim3 grid, int num_sms, cudaStream_t s) {
+  const long long ctas = static_cast<long long>(grid.x) * grid.y * grid.z;
+  const long long keys = WIN ? std::min<long long>(p.max_blocks * 16LL, static_cast<long long>(p.window) + 256) : p.max_blocks * 16LL;
+  // CTAs that would leave SMs idle share their key tiles, two at least each, in clusters as large as can
+  // all be there at once
+  int shares = static_cast<int>(std::max<long long>(1, std::min<long long>(std::min<long long>(8, num_sms / ctas), keys / 256)));
+  while (shares > 1 && ctas > clusters_at_once<D, WIN>(shares)) --shares;
+  // Clusters of two also even out the last wave of a chunk over a long context, whose CTAs are all alike,
+  // where that saves more than the 8 % that sharing costs: 1,500 queries over 32,768 keys (32/8 heads,
+  // head_dim 128: 375 CTAs) 818 us against 895, 2,048 1,127 against 1,174; not 1,024 (654 against 607).
+  const long long waves = (ctas + num_sms - 1) / num_sms, half_waves = (2 * ctas + num_sms - 1) / num_sms;
+  if (D <= 128 && waves > 1 && keys >= 4LL * p.max_q_len && keys >= 128LL * 64 && half_waves * 108 < waves * 200) shares = 2;
+  if (shares == 1) return launch_t<D, WIN, false>(p, grid, 1, s);
+  grid.x *= shares;
+  return launch_t<D, WIN, true>(p, grid, shares, s);
+}
+
 template <int D>
-cudaError_t launch_d(const BlockPrefillParams& p, dim3 grid, int shares, cudaStream_t s) {
-  if (shares > 1) {
-    grid.x *= shares;
-    return p.window > 0 ? launch_t<D, true, true>(p, grid, shares, s) : launch_t<D, false, true>(p, grid, shares, s);
-  }
-  return p.window > 0 ? launch_t<D, true, false>(p, grid, 1, s) : launch_t<D, false, false>(p, grid, 1, s);
+cudaError_t launch_d(const BlockPrefillParams& p, dim3 grid, int num_sms, cudaStream_t s) {
+  return p.window > 0 ? launch_w<D, true>(p, grid, num_sms, s) : launch_w<D, false>(p, grid, num_sms, s);
 }
 
 }  // namespace
@@ -764,20 +805,9 @@ cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaS
   const long long y = static_cast<long long>(p.Hkv) * p.head_parts;
   if (y > 65535) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((p.max_q_len - 1LL) / tok + 1), static_cast<unsigned>(y), p.B);
-  // CTAs that would leave SMs idle share their key tiles, two at least each
-  const long long ctas = y * grid.x * p.B;
-  const long long keys = p.window > 0 ? std::min<long long>(p.max_blocks * 16LL, static_cast<long long>(p.window) + tok + 128) : p.max_blocks * 16LL;
-  int shares = 1;
-  while (shares < 8 && ctas * shares * 2 <= num_sms && keys >= 128LL * 4 * shares) shares *= 2;
-  // Clusters of two also even out the last wave of a chunk over a long context, whose CTAs are all alike,
-  // where that saves more than the 8 % that sharing costs: 1,500 queries over 32,768 keys (32/8 heads,
-  // head_dim 128: 375 CTAs) 818 us against 895, 2,048 1,127 against 1,174; not 1,024 (654 against 607).
-  const long long waves = (ctas + num_sms - 1) / num_sms, half_waves = (2 * ctas + num_sms - 1) / num_sms;
-  if (D <= 128 && shares == 1 && waves > 1 && keys >= 4LL * p.max_q_len && keys >= 128LL * 64 && half_waves * 108 < waves * 200)
-    shares = 2;
-  if (D == 64) return launch_d<64>(p, grid, shares, s);
-  if (D == 128) return launch_d<128>(p, grid, shares, s);
-  return launch_d<256>(p, grid, shares, s);
+  if (D == 64) return launch_d<64>(p, grid, num_sms, s);
+  if (D == 128) return launch_d<128>(p, grid, num_sms, s);
+  return launch_d<256>(p, grid, num_sms, s);
 }
 
 }  // namespace fkv

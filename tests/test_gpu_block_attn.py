@@ -340,6 +340,16 @@ def test_subnormal_value_scales(d):
         _check(c.decode() if new is None else c.prefill(), c.exact(), new)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("batch,h", [(1, 2), (2, 8), (5, 4), (3, 8), (7, 4), (5, 8), (9, 7)])
+def test_prefill_clusters_of_any_size(d, batch, h):
+    """Few rows on 2 to 63 CTAs: clusters of 8 down to 2, also of sizes that are no power of two, over key tiles
+    that do not divide among them."""
+    ctx = [2000 - 37 * b for b in range(batch)]
+    c = Case(ctx, 2 * h, h, d, new=[3 + b for b in range(batch)], seed=d + batch)
+    _check(c.prefill(), c.exact())
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_prefill_last_wave_in_clusters(d):
     """More CTAs than SMs over a long context, in clusters of two; one sequence of few queries among them."""
