@@ -14,6 +14,14 @@
 namespace fkv {
 namespace {
 
+// The kernels are launched while the one before in the stream finishes; their CTAs wait here, before they
+// touch global memory, and only then let the next such kernel's in, so that what that one finds
+// running are CTAs of this kernel alone.  4,133 tokens of 64/8 heads at head_dim 64 18.5 -> 16.9 us per call.
+FKV_DEV void after_previous() {
+  griddep_wait();
+  griddep_launch_dependents();
+}
+
 // The two chunks (indices of 8 elements) of unit u.
 FKV_DEV void unit_chunks(int u, int rot, bool interleaved, int& a, int& b) {
   const int n = rot >> 4;  // turned units
@@ -99,10 +107,11 @@ constexpr int kRopeThreads = 256;
 // that row and unit are found once and token t is followed by t + t_step.  HBM-bound: the next
 // token's elements, slot and position are loaded before the current token is turned and stored, so
 // that a thread has 32 bytes in flight all the time.  Three CTAs per SM (four spill registers, five more):
-// 65,536 tokens of 32/8 heads at head_dim 128 take 257 us, 5.9 TB/s (280 and 321 us).
+// 65,536 tokens of 32/8 heads at head_dim 128 take 255 us, 5.9 TB/s (280 and 321 us).
 // kPool: 0 e4m3, 1 e5m2, 2 bf16.
 template <int D, int kPool>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeCacheParams p, int t_step) {
+  after_previous();
   constexpr int U = D / 16;
   const int per_token = (p.Hq + 2 * p.H) * U;
   const long long gid = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
@@ -190,7 +199,7 @@ FKV_DEV float pow2_scale(uint32_t amax_bits) {
 // share its 16 rows: the rows stay in registers between the maximum and the codes, so that each
 // input byte is read once, and several warps keep them few enough for four CTAs per SM.  The others turn
 // query rows, four units per thread with all loads up front.  HBM-bound: 4 x 16,384 tokens of 32/8
-// heads at head_dim 128 take 275 us, 5.5 TB/s (three CTAs per SM 289 us; six units per thread 323 us).
+// heads at head_dim 128 take 273 us, 5.5 TB/s (three CTAs per SM 289 us; six units per thread 323 us).
 template <int D>
 __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
   constexpr int U = D / 16;       // units of a row
@@ -198,6 +207,7 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
   constexpr int WT = block_warps(D);
   constexpr int R = 16 / WT / TP; // rounds
   __shared__ uint32_t amax_s[kBlockThreads / 32];
+  after_previous();
   const int b = blockIdx.y;
   const int r0 = p.cu[b], L = p.cu[b + 1] - r0, T = p.ctx[b];
   const bool first = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0;
@@ -347,8 +357,7 @@ cudaError_t launch_rope(const RopeCacheParams& p, int pool, int num_sms, cudaStr
   const long long t_step = std::min<long long>(p.n_tokens, std::max<long long>(1, 3LL * num_sms * kRopeThreads / per_token));
   const unsigned blocks = static_cast<unsigned>((per_token * t_step + kRopeThreads - 1) / kRopeThreads);
   auto kern = pool == 2 ? rope_cache_kernel<D, 2> : pool == 1 ? rope_cache_kernel<D, 1> : rope_cache_kernel<D, 0>;
-  kern<<<blocks, kRopeThreads, 0, s>>>(p, static_cast<int>(t_step));
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3(blocks), dim3(kRopeThreads), 0, s, p, static_cast<int>(t_step));
 }
 
 }  // namespace
@@ -366,8 +375,7 @@ cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s)
   const int kv_parts = (2 * p.H + block_tasks(D) - 1) / block_tasks(D);
   const dim3 grid(pages, p.B, static_cast<unsigned>(kv_parts + (items + kQueryItems - 1) / kQueryItems));
   auto kern = D == 64 ? block_cache_kernel<64> : D == 128 ? block_cache_kernel<128> : block_cache_kernel<256>;
-  kern<<<grid, kBlockThreads, 0, s>>>(p, kv_parts);
-  return cudaGetLastError();
+  return launch_dependent(kern, grid, dim3(kBlockThreads), 0, s, p, kv_parts);
 }
 
 }  // namespace fkv

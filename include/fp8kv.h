@@ -36,10 +36,11 @@
  *             (block, KV head) has its own float32 scale for K and one for V: no scale is
  *             calibrated, the append (kv_block_cache) finds it from the block's tokens.
  *
- * Launches.  The decode kernels are launched with programmatic stream serialisation: a
- * decode kernel may be scheduled while the kernel before it in the stream finishes, and
- * sets up its barriers and tensor memory then, but reads and writes no global memory
- * until that kernel has completed, so the stream's ordering is kept.
+ * Launches.  The decode kernels, the rotary and block-scaled cache writes and the block-scaled
+ * prefill of few rows are launched with programmatic stream serialisation: such a kernel may
+ * be scheduled while the kernel before it in the stream finishes, and a decode kernel sets up
+ * its barriers and tensor memory then, but it reads and writes no global memory until that
+ * kernel has completed, so the stream's ordering is kept.
  *
  * Errors.  Argument checks run on the host before anything is enqueued and return
  * FKV_INVALID_ARG or FKV_UNSUPPORTED; a failed launch returns FKV_CUDA_ERROR.  Data
@@ -213,7 +214,8 @@ fkv_status kv_quant_cache_clips(const void* k, const void* v, const int64_t* slo
  *                 slices of one projection's output serve as they are.  Strides are
  *                 multiples of 8 and no shorter than the row; pointers 16-byte aligned
  *   q_out         device bf16, rows at t * q_out_stride; may be q itself with q's stride
- *                 (otherwise the two must not overlap).  q NULL (num_q_heads 0): no queries
+ *                 (otherwise the two must not overlap, and it overlaps neither k nor v).
+ *                 q NULL (num_q_heads 0): no queries
  *   positions     device int64 [n_tokens]; outside [0, rope.max_positions) the token is
  *                 skipped and FKV_FAULT_POSITION raised
  *   slot_mapping  as for kv_quant_cache; a token with a negative slot is skipped whole

@@ -280,6 +280,34 @@ def test_writes_past_four_gigabytes():
     assert torch.equal(big.k_cache[ids[0]], small.k_cache[1]) and torch.equal(big.v_cache[ids[1], :, :4], small.v_cache[0, :, :4])
 
 
+def test_writes_follow_one_another():
+    """Calls in a row, each of which reads what the one before wrote: queries turned in place, and a block that grows
+    token by token, against the same calls with a wait after each."""
+    rng = np.random.default_rng(12)
+    n, h, d = 700, 4, 128
+    rope = f.Rope(f.Rope.table(900, d))
+    pos = torch.arange(n, device="cuda")
+    k, q0 = _bf16(rng, n, h, d).cuda(), _bf16(rng, n, 2 * h, d).cuda()
+    growing = _bf16(rng, 48, h, d).cuda() * torch.logspace(-3, 2, 48, device="cuda", dtype=torch.bfloat16)[:, None, None]
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    ctx = [torch.tensor([t + 1], dtype=torch.int32, device="cuda") for t in range(48)]
+    results = []
+    for wait in (True, False):
+        q, cache, blocks = q0.clone(), f.LayerCache.empty(n // 16 + 1, h, d), f.BlockCache.empty(3, h, d)
+        one = torch.ones(1, device="cuda")
+        for t in range(48):
+            f.kv_rope_cache(q, k, k, pos, pos, rope, cache, one, one, q_out=q)
+            if wait:
+                torch.cuda.synchronize()
+            f.kv_block_cache(growing[t:t + 1], q[t:t + 1, :h], cu, 1, blocks, table, ctx[t], rope=rope)
+            if wait:
+                torch.cuda.synchronize()
+        results.append((q, cache.k_cache.view(-1, h, 16, d)[:n // 16], blocks.k_cache, blocks.v_cache, blocks.k_scale, blocks.v_scale))
+    for x, y in zip(*results):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def test_writes_captured_and_on_another_stream():
     rng = np.random.default_rng(12)
     h, hq, d = 2, 4, 128
