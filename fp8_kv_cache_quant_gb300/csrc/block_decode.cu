@@ -32,9 +32,10 @@
 // CTA = 10 warps:
 //   0-3   softmax: the query's terms; per tile thread i owns key i (and 128 + i): score, mask, the
 //         heads' tile maxima, P's terms, the factors of acc and O_t;
-//   4-7   correction: thread i owns head_dim row i (and 128 + i): acc, then the piece, the merge;
+//   4-7   correction: thread i owns head_dim row i (and 128 + i): acc, then the piece, the merge; and a
+//         quarter each of V's copies, whose stage is free when O_t has come;
 //   8     K copies (a block per lane) and the tile's scales, read a tile ahead and staged;
-//   9     TMEM; polls the barriers and issues V copies, S^T and P.V products as they become possible.
+//   9     TMEM; polls the barriers and issues S^T and P.V products as they become possible.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns (its pieces are then undefined, its units still counted).
 #include "common.cuh"
@@ -81,7 +82,7 @@ struct BlockDecodeCfg {
   static constexpr int OFF_QS = OFF_ML + 2 * 2 * LO * 4;  // c of the query rows [LO]
   static constexpr int OFF_SC = OFF_QS + LO * 4;
   static constexpr int OFF_BAR = OFF_SC + SCN * SCF * 4;
-  static constexpr int NBAR = 24 + 4 * NS + SCN;
+  static constexpr int NBAR = 24 + 3 * NS + SCN;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 40;
   static constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, NP, 0, 0);  // K and query K-major
@@ -338,8 +339,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   uint64_t* k_full = bars + 24;
   uint64_t* k_empty = k_full + C::NS;
   uint64_t* v_full = k_empty + C::NS;
-  uint64_t* v_empty = v_full + C::NS;
-  uint64_t* sc_full = v_empty + C::NS;  // [SCN] scales of tile u in slot u % SCN
+  uint64_t* sc_full = v_full + C::NS;  // [SCN] scales of tile u in slot u % SCN
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* last_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
@@ -369,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     for (int s = 0; s < C::NS; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_full[s], 4);
     }
     for (int s = 0; s < C::SCN; ++s) mbar_init(&sc_full[s], 1);
     *abort_s = 0;
@@ -673,6 +672,29 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     for (int h = 0; h < G; ++h)
 #pragma unroll
       for (int s2 = 0; s2 < C::NSUB; ++s2) acc[s2][h] = 0.f;
+    // V's copies: blocks v0 .. v0 + VB - 1 of a tile, a block per lane, its id read a tile ahead
+    constexpr int VB = TPB / 4;
+    const int v0 = (warp - 4) * VB;
+    Place vat = at;
+    for (int j = 0; j < n0; ++j) vat.advance(p);
+    auto v_id = [&]() -> int {
+      if (vat.left <= 0 || lane >= VB || v0 + lane >= vat.blocks()) return 0;
+      return p.block_table[static_cast<size_t>(vat.b) * p.max_blocks + vat.block0() + v0 + lane];
+    };
+    int tv = n0, vid = v_id();  // the next tile to copy
+    auto copy_v = [&]() {
+      const int st = tv % C::NS, nblk = min(max(vat.blocks() - v0, 0), VB), id = checked(vid);
+      if (lane == 0) mbar_arrive_expect_tx(&v_full[st], nblk * 16 * D);
+      __syncwarp();
+      if (lane < nblk) {
+#pragma unroll
+        for (int s = 0; s < C::NSUB; ++s)
+          tma_load_4d(sV + st * C::KTILE + s * C::KSUB + (v0 + lane) * 16 * C::RB, &tmv, s * C::RB, 0, vat.g, id, &v_full[st]);
+      }
+      ++tv;
+      vat.advance(p);
+      vid = v_id();
+    };
     bool ok = true;
     int w = w0;  // the tile's place
     for (int u = 0; u < n; ++u) {
@@ -698,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
           if constexpr (C::NP == 16) tmem_ld16(col, o[s2]);
           else tmem_ld32(col, o[s2]);
         }
+        if (tv < n) copy_v();  // the P.V of tile u = tv - NS is done with its stage
         tmem_ld_wait();
         tc_fence_before();
         mbar_arrive_warp(&o_free[ob]);
@@ -752,6 +775,11 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
+      // let the copies land before the CTA can exit (on the way to here without a fault, P.V read them all)
+      if (lane == 0)
+        for (int s = 0; s < C::NS; ++s)
+          if (tv > s) wait_ns(&v_full[s], ((tv - 1 - s) / C::NS) & 1);
+      __syncwarp();
     }
   } else if (warp == 8) {
     // ============================================================ K copies and scales
@@ -766,6 +794,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         const int x = checked(ids[j]);
         if (j == 0) id = x;
         copy_tile(&tmk, sK + j * C::KTILE, c, x, &k_full[j]);
+        if (lane > 0 && lane < 4) mbar_arrive(&v_full[j]);  // (a phase has four arrivals)
         copy_tile(&tmv, sV + j * C::KTILE, c, x, &v_full[j]);
         c.advance(p);
       }
@@ -815,38 +844,31 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       if (lane == 0) slot[2 * TPB] = vmax;
       mbar_arrive_warp(&sc_full[u % C::SCN]);
     }
-    // let every issued copy land before the CTA can exit
+    // let every copy issued here land before the CTA can exit
     if (lane == 0) {
       used = max(used, n0);
       for (int s = 0; s < C::NS; ++s)
         if (used > s) wait_ns(&k_full[s], ((used - 1 - s) / C::NS) & 1);
+      for (int s = 0; s < n0; ++s)
+        if (*abort_s) wait_ns(&v_full[s], 0);
     }
     __syncwarp();
   } else {
-    // ============================================================ MMA issuer and V copies (warp 9)
+    // ============================================================ MMA issuer (warp 9)
     // Lane 0 polls the pipeline's barriers without blocking and issues, in whatever order they
-    // become possible, the V loads, the S^T products and the P.V products.
-    const uint32_t sQa = smem_u32(sQ), sKa = smem_u32(sK), sVa = smem_u32(sV), sPa = smem_u32(sP);
-  int tq = 0, tp = 0, tv = n0;  // next S^T, P.V and V load (the first n0 V loads: warp 8)
-    Place vat = at, qat = at, pat = at;
-    for (int j = 0; j < n0; ++j) vat.advance(p);
+    // become possible, the S^T and the P.V products.
+    const uint64_t dK = smem_desc(smem_u32(sK), 16, 8 * C::RB, C::SWZ), dQ = smem_desc(smem_u32(sQ), 16, 8 * C::RB, C::SWZ);
+    const uint64_t dV = smem_desc(smem_u32(sV), 8 * C::RB, 8 * C::RB, C::SWZ);
+    // P without swizzle: 8 keys of 16 bytes per 128-byte core matrix, the next 8 keys 128 bytes on, the next
+    // 16 heads PCOL on
+    const uint64_t dP = smem_desc(smem_u32(sP), 128, G > 8 ? C::PCOL : 128, 0);
+    int tq = 0, tp = 0;  // next S^T and P.V
+    Place qat = at, pat = at;
     bool q_ready = false;  // the query of tile tq's piece is in place
-    int vid = block_id(vat);
     bool ok = true;
-    uint64_t t_progress = globaltimer_ns();
+    uint64_t t_idle = 0;
     while (ok && tp < n) {
-      if (abort_warp(abort_s)) break;
-      int events = 0;  // bit 0: progress; bit 1: P.V of tile tp ready; bit 2: S^T issued
-      int vgo = 0;
-      if (lane == 0) vgo = tv < n && mbar_test_wait(&v_empty[tv % C::NS], ((tv / C::NS) - 1) & 1);
-      if (__shfl_sync(0xffffffffu, vgo, 0)) {
-        const int st = tv % C::NS;
-        copy_tile(&tmv, sV + st * C::KTILE, vat, checked(vid), &v_full[st]);
-        ++tv;
-        vat.advance(p);
-        vid = block_id(vat);  // the next tile's, read ahead
-        events |= 1;
-      }
+      int events = 0;  // bit 1: P.V of tile tp ready; bit 2: S^T issued
       if (lane == 0) {
         // S^T(tq) = K8(tq) q^T into buffer tq % 2: K landed, the buffer's previous S read
         if (tq < n && (q_ready || mbar_test_wait(q_full, qat.piece & 1)) &&
@@ -859,14 +881,13 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk) {
               const int byte = kk * 32;
-              const uint64_t ad = smem_desc(sKa + st * C::KTILE + (byte / C::RB) * C::KSUB + hh * 128 * C::RB + byte % C::RB,
-                                            16, 8 * C::RB, C::SWZ);
-              const uint64_t bd = smem_desc(sQa + (byte / C::RB) * C::QSUB + byte % C::RB, 16, 8 * C::RB, C::SWZ);
-              umma_f8(tmem + C::TM_S + (sb * C::NHALF + hh) * C::NP, ad, bd, C::IDESC_QK, kk > 0 ? 1u : 0u);
+              umma_f8(tmem + C::TM_S + (sb * C::NHALF + hh) * C::NP,
+                      desc_add(dK, st * C::KTILE + (byte / C::RB) * C::KSUB + hh * 128 * C::RB + byte % C::RB),
+                      desc_add(dQ, (byte / C::RB) * C::QSUB + byte % C::RB), C::IDESC_QK, kk > 0 ? 1u : 0u);
             }
           umma_commit(&s_full[sb]);
           umma_commit(&k_empty[st]);
-          events |= 5;
+          events |= 4;
         }
         // P.V of tile tp: P written, V landed, the O_t buffer promoted (tile tp - 2)
         if (tp < tq + ((events >> 2) & 1) && mbar_test_wait(&p_full[tp & 1], (tp >> 1) & 1) &&
@@ -902,15 +923,10 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
           for (int s = 0; s < C::NSUB; ++s)
 #pragma unroll
-            for (int kk = 0; kk < C::BN / 32; ++kk) {
-              const uint64_t ad = smem_desc(sVa + st * C::KTILE + s * C::KSUB + kk * 32 * C::RB, 8 * C::RB, 8 * C::RB, C::SWZ);
-              // no swizzle: 8 keys of 16 bytes per 128-byte core matrix, the next 8 keys 128 bytes on, the next
-              // 16 heads PCOL on
-              const uint64_t bd = smem_desc(sPa + pb * C::PTILE + kk * 32 * 16, 128, G > 8 ? C::PCOL : 128, 0);
-              umma_f8(tmem + C::TM_O + (pb * C::NSUB + s) * C::NP, ad, bd, C::IDESC_PV, kk > 0 ? 1u : 0u);
-            }
+            for (int kk = 0; kk < C::BN / 32; ++kk)
+              umma_f8(tmem + C::TM_O + (pb * C::NSUB + s) * C::NP, desc_add(dV, st * C::KTILE + s * C::KSUB + kk * 32 * C::RB),
+                      desc_add(dP, pb * C::PTILE + kk * 32 * 16), C::IDESC_PV, kk > 0 ? 1u : 0u);
           umma_commit(&o_full[pb]);
-          umma_commit(&v_empty[st]);
           umma_commit(&p_free[pb]);
         }
         __syncwarp();
@@ -918,24 +934,23 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         pat.advance(p);
       }
       if (events != 0) {
-        t_progress = globaltimer_ns();
-      } else if (globaltimer_ns() - t_progress > kPipeWaitNs) {
-        ok = false;
-      } else {
-        __nanosleep(32);  // leave the issue slots to the softmax warp sharing this SM quarter
+        t_idle = 0;
+        continue;
       }
+      if (abort_warp(abort_s)) break;
+      const uint64_t now = globaltimer_ns();
+      if (t_idle == 0) t_idle = now;
+      if (__any_sync(0xffffffffu, now - t_idle > kPipeWaitNs)) ok = false;
+      __nanosleep(32);  // leave the issue slots to the softmax warp sharing this SM quarter
     }
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
-    // every product issued by this warp completes before TMEM is released, and every V copy
-    // lands before the CTA can exit
+    // every product issued by this warp completes before TMEM is released
     if (lane == 0) {
       umma_commit(mma_done);
       wait_ns(mma_done, 0);
-      for (int s = 0; s < C::NS; ++s)
-        if (tv > s) wait_ns(&v_full[s], ((tv - 1 - s) / C::NS) & 1);
     }
     __syncwarp();
   }
