@@ -165,6 +165,7 @@ constexpr int32_t kMaxTableBlocks = (1 << 27) - 64;
 // workspace: piece counters, the pieces' log-sum-exps and outputs.
 struct BlockDecodePlan {
   long long ctas = 0;
+  int halves = 0;  // 1: a group of 16 heads is two units of 8
   size_t cnt_bytes = 0, lse_bytes = 0, o_bytes = 0;
 };
 
@@ -173,10 +174,11 @@ struct BlockDecodePlan {
 constexpr long long kBlockDecodeCounters = 16384;
 
 BlockDecodePlan plan_block_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
-  const int G = Hq / Hkv;
-  const long long units = static_cast<long long>(B) * Hkv;
   BlockDecodePlan plan;
-  plan.ctas = std::min<long long>(static_cast<long long>(current_num_sms()) * fkv::block_decode_ctas_per_sm(D, G), 160 * units);
+  plan.halves = Hq / Hkv == 16 ? 1 : 0;
+  const int G = (Hq / Hkv) >> plan.halves;
+  const long long units = static_cast<long long>(B) * Hkv << plan.halves;
+  plan.ctas = std::min<long long>(static_cast<long long>(current_num_sms()) * fkv::block_decode_ctas_per_sm(D), 160 * units);
   const size_t rows = static_cast<size_t>(plan.ctas + units) * G;
   plan.cnt_bytes = align256(std::max(units, kBlockDecodeCounters) * sizeof(int32_t));
   plan.lse_bytes = align256(rows * sizeof(float));
@@ -585,7 +587,8 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   p.ctx = context_lens;
   p.B = batch;
   p.Hq = num_q_heads;
-  p.Hkv = cache.num_kv_heads;
+  p.Hkv = cache.num_kv_heads << plan.halves;
+  p.halves = plan.halves;
   p.num_blocks = cache.num_blocks;
   p.max_blocks = max_blocks;
   p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
@@ -599,7 +602,7 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   // no more CTAs than there can be places (a unit's tiles and the blank one that leads them)
   const long long blocks = window > 0 ? std::min<long long>(max_blocks, (window + 15LL) / 16 + 1) : max_blocks;
   const int tpb = fkv::block_decode_tile_blocks(cache.head_dim);
-  const long long tiles = static_cast<long long>(batch) * cache.num_kv_heads * ((blocks + tpb - 1) / tpb + 1);
+  const long long tiles = static_cast<long long>(batch) * p.Hkv * ((blocks + tpb - 1) / tpb + 1);
   if (tiles > INT32_MAX) return FKV_UNSUPPORTED;  // the kernel counts them in 32 bits
   const int ctas = static_cast<int>(std::min(plan.ctas, tiles));
   return from_cuda(fkv::launch_block_decode(p, cache.head_dim, ctas, reinterpret_cast<cudaStream_t>(stream)));

@@ -13,11 +13,12 @@
 // below 2^-18 of its tile's largest p vs, and is otherwise within 2^-8 of its value.
 //
 // The products are taken transposed, keys and head_dim on the MMA's M side, the G query heads on N:
-//   S^T [128 keys][2 LO] = K8 . (hi | lo)^T,   O^T [128 d][2 LO] = V8^T . (hi | lo)^T
-// so that the cache tiles are the A operands as TMA lands them; LO = 8 (16 for G = 16), and the
-// threads that read S^T and O^T add column LO + h to column h.  (hi and lo accumulating into the
-// same columns instead takes twice the products: 68 against 59 us for the layer of 8 x 16k-24k
-// tokens.)  head_dim 64: tiles of 256 keys (two S^T products), an M = 64 P.V product whose row r
+//   S^T [128 keys][16] = K8 . (hi | lo)^T,   O^T [128 d][16] = V8^T . (hi | lo)^T
+// so that the cache tiles are the A operands as TMA lands them; the threads that read S^T and O^T
+// add column 8 + h to column h.  A group of 16 heads is two units of 8 that read the same K and V, the
+// second time from L2.  (hi and lo accumulating into the
+// same columns instead takes twice the products: 68 against 63 us for the layer of 8 x 16k-24k
+// tokens, 32/8 heads, head_dim 128, when it was tried.)  head_dim 64: tiles of 256 keys (two S^T products), an M = 64 P.V product whose row r
 // sits in TMEM lane 32 (r / 16) + r % 16; otherwise tiles of 128 keys.
 //
 // Work.  The decode reads every cached byte once, so the CTAs should all read the same number.  The
@@ -36,6 +37,11 @@
 //         quarter each of V's copies, whose stage is free when O_t has come;
 //   8     K copies (a block per lane) and the tile's scales, read a tile ahead and staged;
 //   9     TMEM; polls the barriers and issues S^T and P.V products as they become possible.
+// What bounds it: HBM, around a fixed 12-15 us of ramp, last pieces and merge (178 MB of head_dim 64 take
+// 39 us, 356 MB of head_dim 128 63, groups of one head: 7.3 TB/s on what the second adds).  8 x 16k-24k tokens, 32/8
+// heads, head_dim 128: 63 us, 5.4 TB/s; 8 x 8k-32k, 64/8 heads, head_dim 64: 44 us (49.7 when warp 9 copied V: it
+// was then busy all the time); one sequence of 4,096: 10.4 us.  Two CTAs per SM with three stages of K and V;
+// three with two stages were within 1.5 % either way at 64 registers.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns (its pieces are then undefined, its units still counted).
 #include "common.cuh"
@@ -50,20 +56,20 @@ struct BlockDecodeCfg {
   static constexpr int BN = D == 64 ? 256 : 128;  // keys per tile
   static constexpr int TPB = BN / 16;             // pool blocks per tile
   static constexpr int NHALF = BN / 128;          // S^T products (M = 128 keys) per tile
-  static constexpr int LO = G <= 8 ? 8 : 16;      // first row (column) of the residual terms
+  static constexpr int LO = 8;                    // first row (column) of the residual terms
   static constexpr int NP = 2 * LO;               // the MMA's N
+  static constexpr int NL = G <= 4 ? 4 : LO;      // columns of a term that are read back
   static constexpr int RB = D < 128 ? D : 128;    // bytes of one swizzled row
   static constexpr int SWZ = RB == 128 ? 2 : 4;   // descriptor swizzle mode (128 / 64 bytes)
   static constexpr int NSUB = D / RB;             // column blocks of a K / V row
   static constexpr int KSUB = BN * RB;            // bytes of one column block of a K / V tile
   static constexpr int KTILE = BN * D;            // bytes of a K or V tile
   static constexpr int MPV = D < 128 ? D : 128;   // M of one P.V product
-  static constexpr int NS = G == 8 && D <= 128 ? 3 : 2;  // K / V stages
+  static constexpr int NS = D <= 128 ? 3 : 2;  // K / V stages
   static constexpr int QSUB = NP * RB;          // bytes of one column block of the query tile
-  // P is stored key by key, MN-major: a key's 16 bytes (8 heads' hi, 8 heads' lo; for G = 16 two such
-  // columns, hi and lo) are one store of the thread that owns the key
-  static constexpr int PCOL = BN * 16;            // bytes of a 16-byte column over the tile's keys
-  static constexpr int PTILE = (NP / 16) * PCOL;
+  // P is stored key by key, MN-major: a key's 16 bytes (8 heads' hi, 8 heads' lo) are one store of the
+  // thread that owns the key
+  static constexpr int PTILE = BN * 16;
   static constexpr int TM_S = 0;                  // S^T buffers: columns [0, 2 NHALF NP)
   static constexpr int TM_O = 2 * NHALF * NP;     // O_t^T buffers
   static constexpr int TM_COLS = TM_O + 2 * NSUB * NP <= 64 ? 64 : TM_O + 2 * NSUB * NP <= 128 ? 128 : 256;
@@ -87,7 +93,7 @@ struct BlockDecodeCfg {
   static constexpr int SMEM = OFF_MISC + 40;
   static constexpr uint32_t IDESC_QK = idesc_e4m3_f32(128, NP, 0, 0);  // K and query K-major
   static constexpr uint32_t IDESC_PV = idesc_e4m3_f32(MPV, NP, 1, 1);  // V and P MN-major
-  static constexpr int CTAS = D > 128 || G > 8 ? 1 : G == 8 ? 2 : 3;              // per SM
+  static constexpr int CTAS = D <= 128 ? 2 : 1;   // per SM
   static_assert(OFF_K % 1024 == 0 && OFF_P % 1024 == 0 && OFF_BAR % 8 == 0, "tile alignment of the swizzles");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of the resident CTAs");
 };
@@ -214,6 +220,27 @@ FKV_DEV int count_acq_rel(int32_t* p) {
   return old;
 }
 
+FKV_DEV void tmem_ld4(uint32_t addr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr));
+}
+
+// The heads' columns of both terms: NL of hi, NL of lo.
+template <typename C>
+FKV_DEV void load_terms(uint32_t col, float (&v)[2 * C::NL]) {
+  if constexpr (C::NL == 4) {
+    tmem_ld4(col, v);
+    tmem_ld4(col + C::LO, v + 4);
+  } else {
+    tmem_ld16(col, v);
+  }
+}
+
+FKV_DEV void prefetch_tensormap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 FKV_DEV float warp_max_f(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -231,8 +258,8 @@ FKV_DEV void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& 
 // The merge of a unit's pieces, rows row0 .. row0 + ns - 1 of the workspace, by the whole CTA:
 // o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M) in FP32.  First the heads' weights (a warp per head)
 // into shared memory; then groups of threads, one thread per four outputs, take a share of the
-// pieces each, eight at a time so that a round trip to L2 serves eight, and the groups' sums are
-// added.  A piece whose sums are NaN has lse +inf, so that the output is NaN.
+// pieces each, eight at a time so that a round trip to L2 serves eight (the first eight are requested
+// before the weights), and the groups' sums are added.  A piece whose sums are NaN has lse +inf, so that the output is NaN.
 template <int D, int G>
 FKV_DEV void merge_pieces(const BlockDecodeParams& p, int unit, long long row0, int ns, float* scratch) {
   constexpr int QUADS = G * D / 4, PARTS = QUADS <= kThreads ? kThreads / QUADS : 1, U = 8;
@@ -240,6 +267,16 @@ FKV_DEV void merge_pieces(const BlockDecodeParams& p, int unit, long long row0, 
   float4* o_s = reinterpret_cast<float4*>(scratch + 16);  // [PARTS][QUADS]
   float* w_s = scratch + 16 + 4 * PARTS * QUADS;          // [G][ns]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int part = threadIdx.x / QUADS, q0 = PARTS > 1 ? threadIdx.x - part * QUADS : threadIdx.x;
+  const int sb = PARTS > 1 ? part * ns / PARTS : 0, se = PARTS > 1 ? (part + 1) * ns / PARTS : ns;
+  // pieces s .. s + U - 1 (the last one again behind it) of quad qd
+  auto load = [&](float4 (&x)[U], int qd, int s, int s1) {
+    const float* src = p.o_part + row0 * G * D + 4 * qd;
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(min(s + u, s1 - 1)) * G * D));
+  };
+  float4 first[U];  // this thread's first pieces, on their way while the weights are made
+  if (PARTS == 1 ? q0 < QUADS : part < PARTS && sb < se) load(first, q0, sb, se);
   for (int h = warp; h < G; h += kThreads / 32) {
     const float* lse = p.lse_part + row0 * G + h;
     float M = -INFINITY;
@@ -263,12 +300,15 @@ FKV_DEV void merge_pieces(const BlockDecodeParams& p, int unit, long long row0, 
   __nv_bfloat16* out = p.out + static_cast<size_t>(unit) * G * D;  // (b * Hkv + g) * G rows of D
   auto sum = [&](int qd, int s0, int s1) -> float4 {
     const float* w = w_s + (qd / (D / 4)) * ns;
-    const float* src = p.o_part + row0 * G * D + 4 * qd;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = s0; s < s1; s += U) {
       float4 x[U];
+      if (qd == q0 && s == s0) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(min(s + u, s1 - 1)) * G * D));
+        for (int u = 0; u < U; ++u) x[u] = first[u];
+      } else {
+        load(x, qd, s, s1);
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const float wu = s + u < s1 ? w[s + u] : 0.f;
@@ -289,8 +329,8 @@ FKV_DEV void merge_pieces(const BlockDecodeParams& p, int unit, long long row0, 
   if constexpr (PARTS == 1) {
     for (int qd = threadIdx.x; qd < QUADS; qd += kThreads) store(qd, sum(qd, 0, ns));
   } else {
-    const int part = threadIdx.x / QUADS, qd = threadIdx.x - part * QUADS;
-    if (part < PARTS) o_s[part * QUADS + qd] = sum(qd, part * ns / PARTS, (part + 1) * ns / PARTS);
+    const int qd = q0;
+    if (part < PARTS) o_s[part * QUADS + qd] = sum(qd, sb, se);
     __syncthreads();
     if (part == 0) {
       float4 o = o_s[qd];
@@ -375,6 +415,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     *abort_s = 0;
     pend_s[2] = pend_s[5] = 0;
     fence_mbar_init();
+    prefetch_tensormap(&tmk);
+    prefetch_tensormap(&tmv);
   }
   if (warp == 9) {
     tmem_alloc(tmem_slot, C::TM_COLS);
@@ -404,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     __syncwarp();
     if (lane < nblk) {
 #pragma unroll
-      for (int s = 0; s < C::NSUB; ++s) tma_load_4d(dst + s * C::KSUB + lane * 16 * C::RB, map, s * C::RB, 0, c.g, id, full);
+      for (int s = 0; s < C::NSUB; ++s) tma_load_4d(dst + s * C::KSUB + lane * 16 * C::RB, map, s * C::RB, 0, c.g >> p.halves, id, full);
     }
   };
   // The loads that the first tile waits for go out before the CTA's barrier and before the first copies of K
@@ -515,12 +557,11 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       if (!wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
       tc_fence_after();
       float x[C::NHALF][G];  // the scores of key i + 128 hh of the tile
-      uint32_t whi[C::NHALF][(G + 3) / 4 < 2 ? 2 : (G + 3) / 4], wlo[C::NHALF][(G + 3) / 4 < 2 ? 2 : (G + 3) / 4];  // P's codes
-      float sv[C::NP];
+      uint32_t whi[C::NHALF][2], wlo[C::NHALF][2];  // P's codes
+      float sv[2 * C::NL];
       auto load_s = [&](int hh) {
         const uint32_t col = lane_base + C::TM_S + (sb * C::NHALF + hh) * C::NP;
-        if constexpr (C::NP == 16) tmem_ld16(col, sv);
-        else tmem_ld32(col, sv);
+        load_terms<C>(col, sv);
       };
       load_s(0);
       if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1)) { ok = false; break; }
@@ -539,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       for (int hh = 0; hh < C::NHALF; ++hh) {
         tmem_ld_wait();
 #pragma unroll
-        for (int h = 0; h < G; ++h) x[hh][h] = sv[h] + sv[LO + h];
+        for (int h = 0; h < G; ++h) x[hh][h] = sv[h] + sv[C::NL + h];
         if (hh + 1 < C::NHALF) load_s(hh + 1);
       }
       tc_fence_before();
@@ -619,12 +660,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
       for (int hh = 0; hh < C::NHALF; ++hh) {
         uint8_t* key = sP + pb * C::PTILE + (128 * hh + i) * 16;
-        if constexpr (G <= 8) {
-          *reinterpret_cast<uint4*>(key) = make_uint4(whi[hh][0], G > 4 ? whi[hh][1] : 0u, wlo[hh][0], G > 4 ? wlo[hh][1] : 0u);
-        } else {
-          *reinterpret_cast<uint4*>(key) = make_uint4(whi[hh][0], whi[hh][1], whi[hh][2], whi[hh][3]);
-          *reinterpret_cast<uint4*>(key + C::PCOL) = make_uint4(wlo[hh][0], wlo[hh][1], wlo[hh][2], wlo[hh][3]);
-        }
+        *reinterpret_cast<uint4*>(key) = make_uint4(whi[hh][0], G > 4 ? whi[hh][1] : 0u, wlo[hh][0], G > 4 ? wlo[hh][1] : 0u);
       }
       fence_proxy_async_smem();
       mbar_arrive_warp(&p_full[pb]);
@@ -689,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       if (lane < nblk) {
 #pragma unroll
         for (int s = 0; s < C::NSUB; ++s)
-          tma_load_4d(sV + st * C::KTILE + s * C::KSUB + (v0 + lane) * 16 * C::RB, &tmv, s * C::RB, 0, vat.g, id, &v_full[st]);
+          tma_load_4d(sV + st * C::KTILE + s * C::KSUB + (v0 + lane) * 16 * C::RB, &tmv, s * C::RB, 0, vat.g >> p.halves, id, &v_full[st]);
       }
       ++tv;
       vat.advance(p);
@@ -713,12 +749,11 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       }
       if (ok) {
         tc_fence_after();
-        float o[C::NSUB][C::NP];
+        float o[C::NSUB][2 * C::NL];
 #pragma unroll
         for (int s2 = 0; s2 < C::NSUB; ++s2) {
           const uint32_t col = lane_base + C::TM_O + (ob * C::NSUB + s2) * C::NP;
-          if constexpr (C::NP == 16) tmem_ld16(col, o[s2]);
-          else tmem_ld32(col, o[s2]);
+          load_terms<C>(col, o[s2]);
         }
         if (tv < n) copy_v();  // the P.V of tile u = tv - NS is done with its stage
         tmem_ld_wait();
@@ -727,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
         for (int s2 = 0; s2 < C::NSUB; ++s2)
 #pragma unroll
-          for (int h = 0; h < G; ++h) acc[s2][h] = fmaf(acc[s2][h], alpha[h], beta[h] * (o[s2][h] + o[s2][LO + h]));
+          for (int h = 0; h < G; ++h) acc[s2][h] = fmaf(acc[s2][h], alpha[h], beta[h] * (o[s2][h] + o[s2][C::NL + h]));
       }
       if (at.piece_ends()) {
         // ---- the piece's result: o = acc / (256 l), lse = m + log2 l
@@ -806,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     auto read_scales = [&](const Place& c, int j) {
       ks_n = vs_n = 0.f;
       if (c.left > 0 && lane < c.blocks()) {
-        const size_t x = static_cast<size_t>(j) * p.Hkv + c.g;
+        const size_t x = static_cast<size_t>(j) * (p.Hkv >> p.halves) + (c.g >> p.halves);
         ks_n = p.k_scale[x];
         vs_n = p.v_scale[x];
       }
@@ -859,9 +894,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     // become possible, the S^T and the P.V products.
     const uint64_t dK = smem_desc(smem_u32(sK), 16, 8 * C::RB, C::SWZ), dQ = smem_desc(smem_u32(sQ), 16, 8 * C::RB, C::SWZ);
     const uint64_t dV = smem_desc(smem_u32(sV), 8 * C::RB, 8 * C::RB, C::SWZ);
-    // P without swizzle: 8 keys of 16 bytes per 128-byte core matrix, the next 8 keys 128 bytes on, the next
-    // 16 heads PCOL on
-    const uint64_t dP = smem_desc(smem_u32(sP), 128, G > 8 ? C::PCOL : 128, 0);
+    // P without swizzle: 8 keys of 16 bytes per 128-byte core matrix, the next 8 keys 128 bytes on
+    const uint64_t dP = smem_desc(smem_u32(sP), 128, 128, 0);
     int tq = 0, tp = 0;  // next S^T and P.V
     Place qat = at, pat = at;
     bool q_ready = false;  // the query of tile tq's piece is in place
@@ -981,8 +1015,8 @@ template <int D, int G>
 cudaError_t launch_t(const BlockDecodeParams& p, int N, cudaStream_t s) {
   using C = BlockDecodeCfg<D, G>;
   CUtensorMap tmk, tmv;
-  if (!make_pool_map(&tmk, const_cast<uint8_t*>(p.k_cache), D, p.Hkv, p.num_blocks, C::RB) ||
-      !make_pool_map(&tmv, const_cast<uint8_t*>(p.v_cache), D, p.Hkv, p.num_blocks, C::RB))
+  if (!make_pool_map(&tmk, const_cast<uint8_t*>(p.k_cache), D, p.Hkv >> p.halves, p.num_blocks, C::RB) ||
+      !make_pool_map(&tmv, const_cast<uint8_t*>(p.v_cache), D, p.Hkv >> p.halves, p.num_blocks, C::RB))
     return cudaErrorInvalidValue;
   auto kern = block_decode_kernel<D, G>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -997,16 +1031,13 @@ cudaError_t launch_g(const BlockDecodeParams& p, int G, int N, cudaStream_t s) {
     case 2: return launch_t<D, 2>(p, N, s);
     case 4: return launch_t<D, 4>(p, N, s);
     case 8: return launch_t<D, 8>(p, N, s);
-    case 16:
-      if constexpr (D <= 128) return launch_t<D, 16>(p, N, s);
-      else return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-int block_decode_ctas_per_sm(int D, int G) { return D > 128 || G > 8 ? 1 : G == 8 ? 2 : 3; }
+int block_decode_ctas_per_sm(int D) { return D <= 128 ? 2 : 1; }
 
 int block_decode_tile_blocks(int D) { return D == 64 ? 16 : 8; }
 

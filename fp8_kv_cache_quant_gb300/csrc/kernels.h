@@ -154,10 +154,11 @@ cudaError_t launch_decode_tc(const DecodeParams& p, int D, int G, cudaStream_t s
 struct BlockDecodeParams {
   const __nv_bfloat16* q;                     // [B][Hq][D]
   const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;             // [num_blocks][Hkv]
+  const float *k_scale, *v_scale;             // [num_blocks][Hkv >> halves]
   const int32_t* block_table;                 // [B][max_blocks]
   const int32_t* ctx;                         // [B]
-  int B, Hq, Hkv, num_blocks, max_blocks;
+  int B, Hq, Hkv, num_blocks, max_blocks;     // Hkv: units of a sequence, Hq / Hkv query heads each
+  int halves;                                 // 1: units 2 g and 2 g + 1 share KV head g
   float sm_scale_log2;                        // softmax_scale * log2(e)
   int window;
   int32_t* done;                              // [B * Hkv] pieces finished, zero between calls
@@ -168,7 +169,7 @@ struct BlockDecodeParams {
 };
 
 // CTAs of the block-scaled decode that an SM holds, pool blocks of its tiles, and its launch on N CTAs.
-int block_decode_ctas_per_sm(int D, int G);
+int block_decode_ctas_per_sm(int D);
 int block_decode_tile_blocks(int D);
 cudaError_t launch_block_decode(const BlockDecodeParams& p, int D, int N, cudaStream_t s);
 
