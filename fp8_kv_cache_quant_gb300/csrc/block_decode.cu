@@ -15,20 +15,21 @@
 // The products are taken transposed, keys and head_dim on the MMA's M side, the G query heads on N:
 //   S^T [128 keys][16] = K8 . (hi | lo)^T,   O^T [128 d][16] = V8^T . (hi | lo)^T
 // so that the cache tiles are the A operands as TMA lands them; the threads that read S^T and O^T
-// add column 8 + h to column h.  A group of 16 heads is two units of 8 that read the same K and V, the
-// second time from L2.  (hi and lo accumulating into the
-// same columns instead takes twice the products: 68 against 63 us for the layer of 8 x 16k-24k
-// tokens, 32/8 heads, head_dim 128, when it was tried.)  head_dim 64: tiles of 256 keys (two S^T products), an M = 64 P.V product whose row r
-// sits in TMEM lane 32 (r / 16) + r % 16; otherwise tiles of 128 keys.
+// add column 8 + h to column h.  (hi and lo accumulating into the same columns instead takes twice
+// the products: 68 against 63 us for the layer of 8 x 16k-24k tokens, 32/8 heads, head_dim 128, when it was
+// tried.)  head_dim 64: tiles of 256 keys (two S^T products), an M = 64 P.V product whose row r sits
+// in TMEM lane 32 (r / 16) + r % 16; otherwise tiles of 128 keys.  A group of 16 heads is two units of
+// 8 that read the same K and V.
 //
 // Work.  The decode reads every cached byte once, so the CTAs should all read the same number.  The
 // context lengths are known on the GPU alone (a captured graph replays with others), so the
 // split is made there: the tiles of all (sequence, KV head) units in a row, each unit's led by a blank
 // one that stands for the time its beginning takes, W places in all; CTA k of N takes places
 // floor(k W / N) .. floor((k + 1) W / N) - 1, N the CTAs that are resident at once (or W).  A range that
-// spans several units is walked as one pipeline (the copies run ahead across the border).  A unit in one piece is written by its CTA; the others' pieces go to the workspace as
-// (o / l, log2-sum-exp), piece (k, unit u) at row k + u, and the CTA that completes a unit merges it
-// once it is through with its own range (all end at the same time).
+// spans several units is walked as one pipeline (the copies run ahead across the border).  A unit in
+// one piece is written by its CTA; the others' pieces go to the workspace as (o / l, log2-sum-exp),
+// piece (k, unit u) at row k + u, and the CTA that completes a unit merges it once it is through with
+// its own range (all end at the same time).
 //
 // CTA = 10 warps:
 //   0-3   softmax: the query's terms; per tile thread i owns key i (and 128 + i): score, mask, the
@@ -37,11 +38,12 @@
 //         quarter each of V's copies, whose stage is free when O_t has come;
 //   8     K copies (a block per lane) and the tile's scales, read a tile ahead and staged;
 //   9     TMEM; polls the barriers and issues S^T and P.V products as they become possible.
-// What bounds it: HBM, around a fixed 12-15 us of ramp, last pieces and merge (178 MB of head_dim 64 take
-// 39 us, 356 MB of head_dim 128 63, groups of one head: 7.3 TB/s on what the second adds).  8 x 16k-24k tokens, 32/8
-// heads, head_dim 128: 63 us, 5.4 TB/s; 8 x 8k-32k, 64/8 heads, head_dim 64: 44 us (49.7 when warp 9 copied V: it
-// was then busy all the time); one sequence of 4,096: 10.4 us.  Two CTAs per SM with three stages of K and V;
-// three with two stages were within 1.5 % either way at 64 registers.
+//
+// What bounds it: HBM, around a fixed 12-15 us of ramp, last pieces and merge (groups of one head: 178 MB of
+// head_dim 64 take 39 us, 356 MB of head_dim 128 63, 7.3 TB/s on the difference).  8 x 16k-24k tokens, 32/8
+// heads, head_dim 128: 63 us, 5.4 TB/s; 8 x 8k-32k, 64/8 heads, head_dim 64: 44 us (49.7 when warp 9 copied V
+// as well and was busy all the time); one sequence of 4,096: 10.4 us.  Two CTAs per SM with three stages
+// of K and V; three CTAs with two stages, at 64 registers, are within 1.5 % of it either way.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns (its pieces are then undefined, its units still counted).
 #include "common.cuh"
