@@ -5,8 +5,7 @@
 #include <cstdint>
 #include <cstring>
 
-#include "common.cuh"
-#include "kernels.h"
+#include "block_common.cuh"
 
 namespace {
 

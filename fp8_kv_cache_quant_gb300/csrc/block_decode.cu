@@ -46,8 +46,7 @@
 // of K and V; three CTAs with two stages, at 64 registers, are within 1.5 % of it either way.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns (its pieces are then undefined, its units still counted).
-#include "common.cuh"
-#include "kernels.h"
+#include "block_common.cuh"
 #include "tc.cuh"
 
 namespace fkv {

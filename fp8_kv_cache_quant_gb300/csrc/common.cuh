@@ -39,19 +39,6 @@ FKV_DEV uint16_t f32x2_to_e4m3x2(float lo, float hi) {
   return r;
 }
 
-// Four float32 values -> four e4m3 codes in a word, a's first, in one statement: joined from two
-// 16-bit results in C++, the halves are widened, shifted and merged instead.
-FKV_DEV uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-      "mov.b32 %0, {lo, hi};\n\t}"
-      : "=r"(r)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
 // Two float32 values -> two e5m2 codes, round-to-nearest-even, saturating to +-57344
 // (PTX cvt.rn.satfinite.e5m2x2.f32).  Returns (code(hi) << 8) | code(lo).
 FKV_DEV uint16_t f32x2_to_e5m2x2(float lo, float hi) {

@@ -2,7 +2,6 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <algorithm>
 #include <cstdint>
 
 #include "../../include/fp8kv.h"
@@ -60,63 +59,6 @@ struct PrefillParams {
   int32_t* fault;
 };
 
-struct RopeCacheParams {
-  const __nv_bfloat16 *q, *k, *v;             // token rows at the strides (in elements)
-  long long q_stride, k_stride, v_stride;
-  __nv_bfloat16* q_out;
-  long long q_out_stride;
-  const float* cos_sin;                       // [max_pos][rot]
-  int max_pos, rot;
-  int interleaved;
-  const int64_t* positions;                   // [n_tokens]
-  const int64_t* slots;                       // [n_tokens]
-  int n_tokens, Hq, H, D;                     // Hq 0: no queries
-  uint8_t *kc, *vc;
-  long long capacity;                         // slots of the pool
-  const float *ks, *vs;
-  int per_head;
-  int32_t* fault;
-};
-
-// pool: 0 e4m3, 1 e5m2, 2 bf16
-cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s);
-
-struct BlockCacheParams {
-  const __nv_bfloat16 *q, *k, *v;
-  long long q_stride, k_stride, v_stride;
-  __nv_bfloat16* q_out;
-  long long q_out_stride;
-  const float* cos_sin;                       // null: no rotation (rot 0)
-  int max_pos, rot;
-  int interleaved;
-  const int32_t* cu;                          // [B + 1]
-  const int32_t* ctx;                         // [B]
-  const int32_t* block_table;                 // [B][max_blocks]
-  int n_tokens, B, max_q_len, Hq, H, num_blocks, max_blocks;
-  uint8_t *kc, *vc;
-  float *ks, *vs;                             // [num_blocks][H]
-  int32_t* fault;
-};
-
-cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s);
-
-struct BlockPrefillParams {
-  const __nv_bfloat16* q;
-  const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;             // [num_blocks][Hkv]
-  const int32_t* block_table;                 // [B][max_blocks]
-  const int32_t* ctx;                         // [B]
-  const int32_t* cu;                          // [B + 1]
-  int B, Hq, Hkv, num_blocks, max_blocks, max_q_len, total_q;
-  float sm_scale_log2;                        // softmax_scale * log2(e)
-  int causal, window;
-  __nv_bfloat16* out;
-  int32_t* fault;
-  int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads
-};
-
-cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaStream_t s);
-
 cudaError_t launch_prefill(const PrefillParams& p, int D, bool bf16_layer, void* k_cache, void* v_cache,
                            cudaStream_t s);
 
@@ -150,28 +92,6 @@ cudaError_t launch_decode(const DecodeParams& p, int D, int elt, int G, cudaStre
 // tiles); bf16 and e5m2 layers on the CUDA cores (P exact).
 bool decode_uses_tensor_cores(int D, int elt);
 cudaError_t launch_decode_tc(const DecodeParams& p, int D, int G, cudaStream_t s);
-
-struct BlockDecodeParams {
-  const __nv_bfloat16* q;                     // [B][Hq][D]
-  const uint8_t *k_cache, *v_cache;
-  const float *k_scale, *v_scale;             // [num_blocks][Hkv >> halves]
-  const int32_t* block_table;                 // [B][max_blocks]
-  const int32_t* ctx;                         // [B]
-  int B, Hq, Hkv, num_blocks, max_blocks;     // Hkv: units of a sequence, Hq / Hkv query heads each
-  int halves;                                 // 1: units 2 g and 2 g + 1 share KV head g
-  float sm_scale_log2;                        // softmax_scale * log2(e)
-  int window;
-  int32_t* done;                              // [B * Hkv] pieces finished, zero between calls
-  float* lse_part;                            // [N + B * Hkv][G], base 2
-  float* o_part;                              // [N + B * Hkv][G][D]
-  __nv_bfloat16* out;                         // [B][Hq][D]
-  int32_t* fault;
-};
-
-// CTAs of the block-scaled decode that an SM holds, pool blocks of its tiles, and its launch on N CTAs.
-int block_decode_ctas_per_sm(int D);
-int block_decode_tile_blocks(int D);
-cudaError_t launch_block_decode(const BlockDecodeParams& p, int D, int N, cudaStream_t s);
 
 // Supplies the decode's workspace of `need` bytes when the caller passes none: sets *ws
 // (256-byte aligned) and *bytes, with its first `counter_bytes` (the split counters) zero

@@ -8,8 +8,7 @@
 // both styles unit u of the turned part takes table entries 8 u .. 8 u + 7.
 // The products and the sum of a rotation are rounded one by one to float32 (no fused
 // multiply-add), as an elementwise evaluation rounds them, so that the codes are reproducible.
-#include "common.cuh"
-#include "kernels.h"
+#include "block_common.cuh"
 
 namespace fkv {
 namespace {
