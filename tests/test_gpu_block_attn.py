@@ -443,6 +443,55 @@ assert torch.isfinite(outs[1]).all() and (outs[1][2] - outs[2][0]).float().abs()
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+def test_captured_behind_copies_fills_and_joined_streams():
+    """One graph in which the calls follow a copy, a fill, kernels of torch and a second stream, replayed with other
+    inputs, against the same calls made eagerly."""
+    d, hq, h = 128, 8, 2
+    rng = np.random.default_rng(3)
+    rope = f.Rope(f.Rope.table(300, d))
+    table, cu = _i32([[1, 3], [0, 2]]), _i32([0, 5, 25])
+    ctx, pos = _i32([5, 20]), torch.arange(25, device="cuda")
+    one = torch.ones(1, device="cuda")
+
+    def draw():
+        return torch.from_numpy(rng.standard_normal((25, hq + 2 * h, d)).astype(np.float32)).to(torch.bfloat16).cuda()
+
+    x, source = draw(), draw()
+    side = torch.cuda.Stream()
+    slots, blocks, more = f.LayerCache.empty(2, h, d), f.BlockCache.empty(4, h, d), f.BlockCache.empty(4, h, d)
+
+    def calls():
+        x.copy_(source)
+        slots.k_cache.zero_()
+        q1 = f.kv_rope_cache(x[:, :hq], x[:, hq:hq + h], x[:, hq + h:], pos, pos, rope, slots, one, one)
+        more.k_scale.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y = x + x
+            q2 = f.kv_block_cache(y[:, hq:hq + h], y[:, hq + h:], cu, 20, more, table, ctx, rope=rope, q=y[:, :hq])
+            o2 = f.fp8_block_decode_attn(q2[3:5], more, table, ctx)
+        q3 = f.kv_block_cache(x[:, hq:hq + h], x[:, hq + h:], cu, 20, blocks, table, ctx, rope=rope, q=x[:, :hq])
+        o3 = f.fp8_block_prefill_attn(q3, cu, 20, blocks, table, ctx)
+        torch.cuda.current_stream().wait_stream(side)
+        o4 = f.fp8_block_decode_attn(q3[:2], more, table, ctx)
+        return [q1, q2, o2, q3, o3, o4, slots.k_cache[:1], more.k_scale, blocks.v_scale]
+
+    calls()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = calls()
+    for _ in range(3):
+        source.copy_(draw())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        want = calls()
+        torch.cuda.synchronize()
+        for i, (a, b) in enumerate(zip(got, want)):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8)), i
+
+
 def test_prefill_leaves_other_rows_and_reports_bad_sequences():
     c = Case([40, 50, 60], 4, 2, 128, new=[10, 20, 30], seed=4)
     q = torch.cat((c.q, c.q[:7])).cuda()
