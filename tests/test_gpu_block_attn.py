@@ -129,6 +129,25 @@ def test_decode_range_of_many_short_units():
     _check(c.decode(), c.exact())
 
 
+def test_decode_of_very_many_sequences():
+    """More (sequence, KV head) pairs than the workspace's least number of counters, after a call with a smaller batch
+    over the same workspace."""
+    rng = np.random.default_rng(9)
+    c = Case([int(x) for x in rng.integers(0, 24, 9000)] + [6000], 4, 2, 64, seed=9)
+    small = Case([300, 6000], 4, 2, 64, seed=1)
+    ws = f.block_decode_workspace(len(c.ctx), 4, c.cache())
+    _check(c.decode(workspace=ws), c.exact())
+    _check(small.decode(workspace=ws), small.exact())
+
+
+@pytest.mark.parametrize("d,hq,h", [(64, 96, 96), (128, 160, 40), (256, 72, 9)])
+def test_attention_of_many_heads(d, hq, h):
+    dec = Case([70, 300, 1], hq, h, d, seed=d)
+    _check(dec.decode(), dec.exact())
+    pre = Case([70, 300, 1], hq, h, d, new=[7, 2, 1], seed=d)
+    _check(pre.prefill(), pre.exact())
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_decode_workspace_serves_other_batches(d):
     """A batch that shrinks and grows again, and other heads, over one workspace that is never cleared."""
