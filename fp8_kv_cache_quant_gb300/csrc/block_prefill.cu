@@ -204,10 +204,9 @@ __global__ void __launch_bounds__(512, 1)
   const int share = SPLIT ? static_cast<int>(cluster_rank()) : 0, shares = SPLIT ? static_cast<int>(cluster_size()) : 1;
   const int qt = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) / shares;
 
-  // SPLIT, whose few CTAs find free SMs while the kernel before ends, is launched with programmatic stream
-  // serialisation.  Its tensor memory, all of an SM's, is allocated after this wait: taken before, it
-  // could be what a CTA of the kernel before still needs to go on.
-  if constexpr (SPLIT) griddep_wait();
+  // Launched with programmatic stream serialisation.  The tensor memory, all of an SM's, is allocated
+  // after this wait: taken before, it could be what a CTA of the kernel before still needs to go on.
+  griddep_wait();
 
   // ------------------------------------------------------------ sequence geometry
   const bool first_cta = qt == 0 && share == 0 && blockIdx.y == 0 && threadIdx.x == 0;
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(512, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if constexpr (SPLIT) griddep_launch_dependents();
+  griddep_launch_dependents();
 
   if (warp < C::SW) {
     // ============================================================ softmax warps
@@ -763,14 +762,14 @@ cudaError_t launch_t(const BlockPrefillParams& p, dim3 grid, int shares, cudaStr
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
-  cudaLaunchAttribute split[2];
-  split[0].id = cudaLaunchAttributeClusterDimension;
-  split[0].val.clusterDim.x = shares;
-  split[0].val.clusterDim.y = split[0].val.clusterDim.z = 1;
-  split[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  split[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = split;
-  cfg.numAttrs = SPLIT ? 2 : 0;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = shares;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = SPLIT ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, p, tmk, tmv);
 }
 

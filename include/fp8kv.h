@@ -37,7 +37,7 @@
  *             calibrated, the append (kv_block_cache) finds it from the block's tokens.
  *
  * Launches.  The decode kernels, the rotary and block-scaled cache writes and the block-scaled
- * prefill of few rows are launched with programmatic stream serialisation: such a kernel may
+ * prefill are launched with programmatic stream serialisation: such a kernel may
  * be scheduled while the kernel before it in the stream finishes, and a decode kernel sets up
  * its barriers and tensor memory then, but it reads and writes no global memory until that
  * kernel has completed, so the stream's ordering is kept.
