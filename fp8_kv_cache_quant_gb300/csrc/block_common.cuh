@@ -9,6 +9,13 @@
 
 namespace fkv {
 
+// ex2 whose results below 2^-126 are not flushed.
+FKV_DEV float ex2_subnormal(float x) {
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Four float32 values -> four e4m3 codes in a word, a's first, in one statement: joined from two
 // 16-bit results in C++, the halves are widened, shifted and merged instead.
 FKV_DEV uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
@@ -20,6 +27,60 @@ FKV_DEV uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
       : "=r"(r)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
+}
+
+constexpr float kLog2E4m3Max = 8.807354922057604f;  // log2(448)
+
+// 2^n of a whole number -126 <= n <= 127.
+FKV_DEV float pow2i(float n) { return __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23); }
+
+constexpr float kFloatMax = 3.402823466e+38f;
+
+// V scales in the exponent.  P_j = 2^(x_j + L_j - R) carries its block's scale vs = 2^L; the softmax's sum takes
+// it out again, l = sum P_j 2^(o - L_j).  A scale 2^100 and more below the largest of its tile, zero among them,
+// counts as zero: its keys enter l as if it were 2^-100 of the largest, so that their P stays a normal
+// float32 number, and are left out of the product (their factor is given as -2^(o - L)).  The whole number o keeps
+// l within float32: its factors are at most 2^80 for L >= o - 80, its largest term is above 2^-120 for L <= o + 118.
+// It begins at 0, which serves scales from 2^-80 to 2^118, and follows smaller ones down and larger ones up (of
+// scales 2^198 and more apart in one sequence the small ones count as zero as well).
+struct ScaleRange {
+  float o = 0.f, top = -INFINITY, low = INFINITY;  // the offset, the largest and the smallest L so far
+};
+struct BlockScale {
+  float lv, iv;  // L and 2^(o - L), the latter negative where the scale counts as zero
+  // 0 as a rule.  Where o changed, a scale counts as zero or the scales so far lie so far apart that 2^-|r - R_t| may
+  // underflow though the keys' weights are alike: 2^(new o - old o), by which l so far is multiplied
+  // (up to the largest float) before it is joined by join_sums
+  float rare;
+};
+
+// A tile's scales, a block per lane (`in`: the lane has one that a query sees).  Every lane of the warp takes part.
+FKV_DEV BlockScale block_scales(ScaleRange& range, float vs, bool in) {
+  const bool some = in && vs > 0.f;
+  const float L = some ? lg2(vs) : 0.f;
+  float least, most;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(most) : "f"(some ? L : -INFINITY));
+  const float bottom = most > -INFINITY ? most - 100.f : -100.f;
+  bool zero = in && !(some && L > bottom);
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(least) : "f"(zero ? bottom : some ? L : INFINITY));
+  range.top = fmaxf(range.top, most);
+  range.low = fminf(range.low, least);
+  const float o = fmaxf(fmaxf(fminf(range.o, floorf(least) + 80.f), ceilf(range.top) - 118.f), -120.f);
+  zero = zero || (some && L < o - 80.f);
+  BlockScale r;
+  const bool rare = __any_sync(0xffffffffu, zero) || o != range.o || range.top - range.low > 100.f;
+  r.rare = rare ? pow2i(o - range.o) : 0.f;
+  range.o = o;
+  r.lv = zero ? fmaxf(bottom, o - 80.f) : L;
+  r.iv = in ? ex2_subnormal(o - r.lv) : 1.f;
+  if (zero) r.iv = -r.iv;
+  return r;
+}
+
+// l 2^(r - r') + lt 2^(R - r') with r' = max(r, R) and d = r - R, the factor in two halves.
+FKV_DEV float join_sums(float l, float lt, float d) {
+  const float h = ex2(-0.5f * fabsf(d));
+  return d > 0.f ? fmaf(lt * h, h, l) : fmaf(l * h, h, lt);
 }
 
 struct RopeCacheParams {

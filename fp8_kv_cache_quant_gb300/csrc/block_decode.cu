@@ -6,11 +6,13 @@
 // and q' = hi + lo, hi the leading 3 fraction bits, the score of key j is
 //   x_j = (hi . k8_j + lo . k8_j) * ks[block(j)] * c,   c = 2^k softmax_scale log2(e);
 // a bf16 value has 8 significant bits and e4m3 4, so that hi + lo is q' down to 2^-18 of the row's
-// largest element.  Per tile, with its own maximum M_t and its largest V scale vmax,
-//   P_j = 2^(x_j - M_t) * 256 vs[block(j)] / vmax = hi + lo likewise,   O_t = sum_j (hi + lo)_j v8_j,
-// and the running state is m' = max(m, M_t), acc = acc 2^(m - m') + O_t vmax 2^(M_t - m'),
-// l = l 2^(m - m') + 2^(M_t - m') sum_j 2^(x_j - M_t); the output acc / (256 l).  P loses what lies
-// below 2^-18 of its tile's largest p vs, and is otherwise within 2^-8 of its value.
+// largest element.  Per tile, with y_j = x_j + L[block(j)], L = log2 vs, and the tile's maximum R_t of y,
+//   P_j = 2^(y_j - R_t) * 448 = hi + lo likewise,   O_t = sum_j (hi + lo)_j v8_j,
+// and the running state is r' = max(r, R_t), acc = acc 2^(r - r') + O_t 2^(R_t - r'),
+// l = l 2^(r - r') + 2^(R_t - r') sum_j P_j / 448 * 2^(o - L[block(j)]); the output 2^o acc / (448 l).  P is taken against the
+// largest p vs of the tile's visible keys, whichever key has it: it loses what lies below 2^-17 of
+// that, and is otherwise within 2^-8 of its value.  o keeps l within float32's range: block_scales in
+// block_common.cuh.
 //
 // The products are taken transposed, keys and head_dim on the MMA's M side, the G query heads on N:
 //   S^T [128 keys][16] = K8 . (hi | lo)^T,   O^T [128 d][16] = V8^T . (hi | lo)^T
@@ -46,6 +48,8 @@
 // of K and V; three CTAs with two stages, at 64 registers, are within 1.5 % of it either way.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns (its pieces are then undefined, its units still counted).
+#include <type_traits>
+
 #include "block_common.cuh"
 #include "tc.cuh"
 
@@ -77,7 +81,7 @@ struct BlockDecodeCfg {
   // scales of a tile, ring of slots: the K copies run at most NS + 2 tiles ahead of the softmax's
   // release of an S buffer, which follows its reading of the scales
   static constexpr int SCN = NS + 2;
-  static constexpr int SCF = 2 * TPB + 4;         // ks [TPB], 256 vs / vmax [TPB], vmax
+  static constexpr int SCF = 3 * TPB + 4;         // ks [TPB], L [TPB], 2^(o - L) [TPB], o, BlockScale's rare
   // shared memory (bytes)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = OFF_Q + NSUB * QSUB;
@@ -85,8 +89,9 @@ struct BlockDecodeCfg {
   static constexpr int OFF_V = OFF_K + NS * KTILE;
   static constexpr int OFF_RED = OFF_V + NS * KTILE;  // [2][4 warps][LO] floats
   static constexpr int OFF_F = OFF_RED + 2 * 4 * LO * 4;  // factors of acc and O_t [2][2][LO]
-  static constexpr int OFF_ML = OFF_F + 2 * 2 * LO * 4;   // m and l of a piece [2][2][LO]
-  static constexpr int OFF_QS = OFF_ML + 2 * 2 * LO * 4;  // c of the query rows [LO]
+  static constexpr int MLF = 2 * LO + 4;                  // r, l [LO] and o of a piece
+  static constexpr int OFF_ML = OFF_F + 2 * 2 * LO * 4;   // [2][MLF]
+  static constexpr int OFF_QS = OFF_ML + 2 * MLF * 4;     // c of the query rows [LO]
   static constexpr int OFF_SC = OFF_QS + LO * 4;
   static constexpr int OFF_BAR = OFF_SC + SCN * SCF * 4;
   static constexpr int NBAR = 24 + 3 * NS + SCN;
@@ -375,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   uint64_t* red_full = bars + 14;  // [2] the 4 warps' values of reduction r in slot r % 2
   uint64_t* f_full = bars + 16;    // [2] factors of tile u in slot u % 2
   uint64_t* f_free = bars + 18;    // [2]
-  uint64_t* l_full = bars + 20;    // [2] m and l of piece r in slot r % 2 ...
+  uint64_t* l_full = bars + 20;    // [2] r, l and o of piece r in slot r % 2 ...
   uint64_t* l_free = bars + 22;    // [2] ... and taken
   uint64_t* k_full = bars + 24;
   uint64_t* k_empty = k_full + C::NS;
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     // ============================================================ softmax warpgroup
     const int i = threadIdx.x;  // key i of a tile (TMEM lane i)
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-    float m[G], lsum[G];
+    float m[G], lsum[G];  // r and (this thread's keys only) l
     bool ok = true;
     bool fresh = true;  // the next tile begins a piece
     for (int u = 0; ok && u < n; ++u) {
@@ -567,16 +572,18 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       load_s(0);
       if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1)) { ok = false; break; }
       const float* slot = sc_s + (u % C::SCN) * C::SCF;
-      float ks[C::NHALF], rv[C::NHALF];
+      float ks[C::NHALF], lv[C::NHALF], iv[C::NHALF], pmax[C::NHALF];
       bool valid[C::NHALF];
 #pragma unroll
       for (int hh = 0; hh < C::NHALF; ++hh) {
         ks[hh] = slot[8 * hh + (i >> 4)];
-        rv[hh] = slot[TPB + 8 * hh + (i >> 4)];
+        lv[hh] = slot[TPB + 8 * hh + (i >> 4)];
+        iv[hh] = slot[2 * TPB + 8 * hh + (i >> 4)];
+        pmax[hh] = iv[hh] > 0.f ? 448.f : 0.f;  // (0: a scale that counts as zero)
         const int key = at.block0() * 16 + 128 * hh + i;
         valid[hh] = key >= at.s.lo && key < at.s.T;
       }
-      const float vmax = slot[2 * TPB];
+      const float o = slot[3 * TPB], rare = slot[3 * TPB + 1];
 #pragma unroll
       for (int hh = 0; hh < C::NHALF; ++hh) {
         tmem_ld_wait();
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       }
       tc_fence_before();
       mbar_arrive_warp(&s_free[sb]);
-      // the heads' maxima over the tile's keys: within the warp, then across the 4
+      // the heads' maxima of y over the tile's keys: within the warp, then across the 4
       const int rr = u + at.piece;  // reductions before this one (each piece ended with one of its own)
       float* red = red_s + (rr & 1) * 4 * LO;
 #pragma unroll
@@ -594,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         float wm = -INFINITY;
 #pragma unroll
         for (int hh = 0; hh < C::NHALF; ++hh) {
-          x[hh][h] = valid[hh] ? x[hh][h] * (qs_s[h] * ks[hh]) : -INFINITY;  // (c in shared memory: registers)
+          x[hh][h] = valid[hh] ? fmaf(x[hh][h], qs_s[h] * ks[hh], lv[hh]) : -INFINITY;  // (c in shared memory: registers)
           wm = hh == 0 ? x[hh][h] : fmaxf(wm, x[hh][h]);
         }
         wm = warp_max_f(wm);
@@ -608,56 +615,60 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       if (u >= 2 && !wait_warp(&p_free[pb], ((u >> 1) - 1) & 1)) { ok = false; break; }
       if (u >= 2 && !wait_warp(&f_free[pb], ((u >> 1) - 1) & 1)) { ok = false; break; }
       // four heads at a time (a word of codes): maxima, P's terms, factors
+      auto heads = [&](auto rarely) {
 #pragma unroll
-      for (int h4 = 0; h4 < G; h4 += 4) {
-        constexpr int HN = G < 4 ? G : 4;
-        float tm[4];
-        {
-          const float4 r0 = *reinterpret_cast<const float4*>(red + h4), r1 = *reinterpret_cast<const float4*>(red + LO + h4);
-          const float4 r2 = *reinterpret_cast<const float4*>(red + 2 * LO + h4), r3 = *reinterpret_cast<const float4*>(red + 3 * LO + h4);
-          tm[0] = fmaxf(fmaxf(r0.x, r1.x), fmaxf(r2.x, r3.x));
-          tm[1] = fmaxf(fmaxf(r0.y, r1.y), fmaxf(r2.y, r3.y));
-          tm[2] = fmaxf(fmaxf(r0.z, r1.z), fmaxf(r2.z, r3.z));
-          tm[3] = fmaxf(fmaxf(r0.w, r1.w), fmaxf(r2.w, r3.w));
-        }
-        float pv[C::NHALF][4], al[4], be[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          al[j] = be[j] = 0.f;
-          if (j >= HN) {
-#pragma unroll
-            for (int hh = 0; hh < C::NHALF; ++hh) pv[hh][j] = 0.f;
-            continue;
+        for (int h4 = 0; h4 < G; h4 += 4) {
+          constexpr int HN = G < 4 ? G : 4;
+          float tm[4];
+          {
+            const float4 r0 = *reinterpret_cast<const float4*>(red + h4), r1 = *reinterpret_cast<const float4*>(red + LO + h4);
+            const float4 r2 = *reinterpret_cast<const float4*>(red + 2 * LO + h4), r3 = *reinterpret_cast<const float4*>(red + 3 * LO + h4);
+            tm[0] = fmaxf(fmaxf(r0.x, r1.x), fmaxf(r2.x, r3.x));
+            tm[1] = fmaxf(fmaxf(r0.y, r1.y), fmaxf(r2.y, r3.y));
+            tm[2] = fmaxf(fmaxf(r0.z, r1.z), fmaxf(r2.z, r3.z));
+            tm[3] = fmaxf(fmaxf(r0.w, r1.w), fmaxf(r2.w, r3.w));
           }
-          const int h = h4 + j;
-          // one of the two factors is 1, the other 2^-|m - tmax|
-          const float e = ex2(-fabsf(m[h] - tm[j]));
-          const float alpha = m[h] > tm[j] ? 1.f : e, corr = m[h] > tm[j] ? e : 1.f;
-          float psum = 0.f;
+          float pv[C::NHALF][4], al[4], be[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            al[j] = be[j] = 0.f;
+            if (j >= HN) {
+#pragma unroll
+              for (int hh = 0; hh < C::NHALF; ++hh) pv[hh][j] = 0.f;
+              continue;
+            }
+            const int h = h4 + j;
+            // one of the two factors is 1, the other 2^-|m - tmax|
+            const float dm = m[h] - tm[j], e = ex2(-fabsf(dm));
+            const float alpha = m[h] > tm[j] ? 1.f : e, corr = m[h] > tm[j] ? e : 1.f;
+            float psum = 0.f;
+#pragma unroll
+            for (int hh = 0; hh < C::NHALF; ++hh) {
+              const float w = valid[hh] ? ex2(x[hh][h] - tm[j]) : 0.f;
+              psum = fmaf(w, fabsf(iv[hh]), psum);
+              pv[hh][j] = w * pmax[hh];
+            }
+            lsum[h] = decltype(rarely)::value ? join_sums(fminf(lsum[h] * rare, kFloatMax), psum, dm) : fmaf(lsum[h], alpha, psum * corr);
+            m[h] = fmaxf(m[h], tm[j]);
+            al[j] = alpha;
+            be[j] = corr;
+          }
+          if (i == 0) {
+            *reinterpret_cast<float4*>(f_s + pb * 2 * LO + h4) = make_float4(al[0], al[1], al[2], al[3]);
+            *reinterpret_cast<float4*>(f_s + pb * 2 * LO + LO + h4) = make_float4(be[0], be[1], be[2], be[3]);
+          }
+          // the codes of heads h4 .. h4 + 3: words h4 / 4 (hi) and LO / 4 + h4 / 4 (lo) of the key's bytes
 #pragma unroll
           for (int hh = 0; hh < C::NHALF; ++hh) {
-            const float w = valid[hh] ? ex2(x[hh][h] - tm[j]) : 0.f;
-            psum += w;
-            pv[hh][j] = w * rv[hh];
+            uint32_t hi, lo;
+            split4(pv[hh][0], pv[hh][1], pv[hh][2], pv[hh][3], hi, lo);
+            whi[hh][h4 / 4] = hi;
+            wlo[hh][h4 / 4] = lo;
           }
-          lsum[h] = fmaf(lsum[h], alpha, psum * corr);
-          m[h] = fmaxf(m[h], tm[j]);
-          al[j] = alpha;
-          be[j] = corr * vmax;
         }
-        if (i == 0) {
-          *reinterpret_cast<float4*>(f_s + pb * 2 * LO + h4) = make_float4(al[0], al[1], al[2], al[3]);
-          *reinterpret_cast<float4*>(f_s + pb * 2 * LO + LO + h4) = make_float4(be[0], be[1], be[2], be[3]);
-        }
-        // the codes of heads h4 .. h4 + 3: words h4 / 4 (hi) and LO / 4 + h4 / 4 (lo) of the key's bytes
-#pragma unroll
-        for (int hh = 0; hh < C::NHALF; ++hh) {
-          uint32_t hi, lo;
-          split4(pv[hh][0], pv[hh][1], pv[hh][2], pv[hh][3], hi, lo);
-          whi[hh][h4 / 4] = hi;
-          wlo[hh][h4 / 4] = lo;
-        }
-      }
+      };
+      if (rare == 0.f) heads(std::false_type());
+      else heads(std::true_type());
 #pragma unroll
       for (int hh = 0; hh < C::NHALF; ++hh) {
         uint8_t* key = sP + pb * C::PTILE + (128 * hh + i) * 16;
@@ -667,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       mbar_arrive_warp(&p_full[pb]);
       mbar_arrive_warp(&f_full[pb]);
       if (at.piece_ends()) {
-        // ---- the piece's m and l (the latter summed over the 128 key threads) for the correction
+        // ---- the piece's r, l (summed over the 128 key threads) and o for the correction
         const int r = at.piece, re = rr + 1;
 #pragma unroll
         for (int h = 0; h < G; ++h) {
@@ -683,9 +694,10 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
           const float* red2 = red_s + (re & 1) * 4 * LO;
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            ml_s[(r & 1) * 2 * LO + h] = m[h];
-            ml_s[(r & 1) * 2 * LO + LO + h] = (red2[h] + red2[LO + h]) + (red2[2 * LO + h] + red2[3 * LO + h]);
+            ml_s[(r & 1) * C::MLF + h] = m[h];
+            ml_s[(r & 1) * C::MLF + LO + h] = (red2[h] + red2[LO + h]) + (red2[2 * LO + h] + red2[3 * LO + h]);
           }
+          ml_s[(r & 1) * C::MLF + 2 * LO] = o;
         }
         mbar_arrive_warp(&l_full[r & 1]);
         fresh = true;
@@ -766,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
           for (int h = 0; h < G; ++h) acc[s2][h] = fmaf(acc[s2][h], alpha[h], beta[h] * (o[s2][h] + o[s2][C::NL + h]));
       }
       if (at.piece_ends()) {
-        // ---- the piece's result: o = acc / (256 l), lse = m + log2 l
+        // ---- the piece's result: 2^o acc / (448 l), and its log2-sum-exp r - o + log2 l
         const int r = at.piece;
         const int unit = at.b * p.Hkv + at.g;
         const int u0 = w - at.t;  // the place of the unit's first tile
@@ -774,22 +786,24 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         if (ok) ok = wait_warp(&l_full[r & 1], (r >> 1) & 1);
         if (ok) {
           const long long row = static_cast<long long>(k) + unit;
+          const float* ml = ml_s + (r & 1) * C::MLF;
+          const float o = ml[2 * LO], so = pow2i(o);
 #pragma unroll
           for (int h = 0; h < G; ++h) {
-            const float mh = ml_s[(r & 1) * 2 * LO + h], L = ml_s[(r & 1) * 2 * LO + LO + h];
-            const float inv = 1.f / (256.f * L);
+            const float mh = ml[h], L = ml[LO + h];
+            const float inv = 1.f / (448.f * L);
             if (ns == 1) {
               if (has_row) {
 #pragma unroll
                 for (int s2 = 0; s2 < C::NSUB; ++s2)
-                  p.out[(static_cast<size_t>(at.b) * p.Hq + at.g * G + h) * D + s2 * 128 + d] = __float2bfloat16(acc[s2][h] * inv);
+                  p.out[(static_cast<size_t>(at.b) * p.Hq + at.g * G + h) * D + s2 * 128 + d] = __float2bfloat16(acc[s2][h] * inv * so);
               }
             } else {
               if (has_row) {
 #pragma unroll
-                for (int s2 = 0; s2 < C::NSUB; ++s2) p.o_part[(row * G + h) * D + s2 * 128 + d] = acc[s2][h] * inv;
+                for (int s2 = 0; s2 < C::NSUB; ++s2) p.o_part[(row * G + h) * D + s2 * 128 + d] = acc[s2][h] * inv * so;
               }
-              if (i == 0) p.lse_part[row * G + h] = L > 0.f ? mh + lg2(L) : INFINITY;
+              if (i == 0) p.lse_part[row * G + h] = L > 0.f ? mh - o + lg2(L) : INFINITY;
             }
 #pragma unroll
             for (int s2 = 0; s2 < C::NSUB; ++s2) acc[s2][h] = 0.f;
@@ -848,6 +862,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       }
     };
     read_scales(at, id);
+    ScaleRange range;
     int used = 0;  // tiles whose K copy was issued
     for (int u = 0; u < n; ++u) {
       if (abort_warp(abort_s)) break;
@@ -869,15 +884,18 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         copy_tile(&tmk, sK + st * C::KTILE, here, id_u, &k_full[st]);
       }
       used = u + 1;
-      float vmax = vs;  // (lanes past the tile's blocks: 0)
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
+      if (here.t == 0) range = ScaleRange();  // another piece
+      const BlockScale sc = block_scales(range, vs, lane < here.blocks());
       float* slot = sc_s + (u % C::SCN) * C::SCF;
       if (lane < TPB) {
         slot[lane] = ks;
-        slot[TPB + lane] = vmax > 0.f ? __fdividef(vs, vmax) * 256.f : 0.f;
+        slot[TPB + lane] = sc.lv;
+        slot[2 * TPB + lane] = sc.iv;
       }
-      if (lane == 0) slot[2 * TPB] = vmax;
+      if (lane == 0) {
+        slot[3 * TPB] = range.o;
+        slot[3 * TPB + 1] = sc.rare;
+      }
       mbar_arrive_warp(&sc_full[u % C::SCN]);
     }
     // let every copy issued here land before the CTA can exit

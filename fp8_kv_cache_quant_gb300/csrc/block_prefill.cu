@@ -6,12 +6,14 @@
 // and q' = hi + lo, hi the leading 3 fraction bits, the scores of a tile of 128 keys are
 //   x_j = (hi . k8_j + lo . k8_j) * c * ks[block(j)],   c = 2^k softmax_scale log2(e);
 // a bf16 value has 8 significant bits and e4m3 4, so that hi + lo is q' down to 2^-18 of the row's
-// largest element.  With the tile's own row maximum M_t and its largest V scale vmax,
-//   P_j = 2^(x_j - M_t + lv[block(j)]),  lv = log2(256 vs / vmax),  P = hi + lo likewise,
-//   l_t = sum_blocks 2^-lv sum_j P_j,  O_t = sum_j (hi + lo)_j v8_j,
-// and the running state is m' = max(m, M_t), acc = acc 2^(m - m') + O_t vmax 2^(M_t - m'),
-// l = l 2^(m - m') + l_t 2^(M_t - m'); the output acc / (256 l).  P loses what lies below 2^-18 of
-// its tile's largest p vs, and is otherwise within 2^-8 of its value: the precision of a bf16 P.
+// largest element.  With y_j = x_j + L[block(j)], L = log2 vs, and the row's maximum R_t of y over the tile,
+//   P_j = 448 * 2^(y_j - R_t),  P = hi + lo likewise,
+//   l_t = sum_blocks 2^(o - L) sum_j P_j,  O_t = sum_j (hi + lo)_j v8_j,
+// and the running state is r' = max(r, R_t), acc = acc 2^(r - r') + O_t 2^(R_t - r'),
+// l = l 2^(r - r') + l_t 2^(R_t - r'); the output 2^o acc / l.  P is taken against the largest p vs of
+// the keys that the row sees in the tile, so that no other key's scale enters its arithmetic: it loses what lies
+// below 2^-17 of that, and is otherwise within 2^-8 of its value, the precision of a bf16 P.  o keeps l within
+// float32's range: block_scales in block_common.cuh.
 // hi and lo accumulate into the same S and O_t (two products of K = 32 instead of one), so that
 // K and V are used as they lie in the cache, without a pass that widens them to 16 bits.
 //
@@ -22,7 +24,7 @@
 //         a row's columns (16x32bx2 TMEM loads): the query's two terms (prologue); then per tile
 //         the maximum, P's two terms into shared memory, the row's factors of acc and O_t;
 //   8-11  correction: acc in registers (at head_dim 256 its second half in TMEM), epilogue;
-//   12    K copies (a block per lane) and the tile's scales: ks, lv, 2^-lv and vmax, read one tile
+//   12    K copies (a block per lane) and the tile's scales: ks, L, 2^(o - L) and o, read one tile
 //         ahead and staged in shared memory;
 //   13    allocates TMEM, issues S = q' K8^T;    14  issues O_t = P V8;    15  V copies.
 // TMEM: two S buffers and two O_t buffers up to head_dim 128; at head_dim 256 one S buffer, two
@@ -72,6 +74,8 @@ FKV_DEV void pin32(float* v) {
   asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
 }
 
+constexpr float kHuge = 3e38f;  // minus this: the maximum of no scores
+
 template <int D>
 struct BlockPrefillCfg {
   static constexpr int BM = 128, BN = 128;          // rows of a CTA, keys of a tile
@@ -95,10 +99,11 @@ struct BlockPrefillCfg {
   // scales of a tile in a ring of slots: the K copies run at most SBUF + NS tiles ahead of the
   // softmax (a stage is refilled once its S was computed, an S buffer once it was read)
   static constexpr int SCN = D <= 128 ? 8 : 4;
-  static constexpr int SCF = 32;                    // floats per slot: ks [8], lv [8], 2^-lv [8], vmax
+  static constexpr int SCF = 32;                    // floats per slot: ks [8], L [8], 2^(o - L) [8], o, BlockScale's rare
   static_assert(SCN > SBUF + NS, "a slot is rewritten only after the softmax is done with it");
-  // registers per thread of the warpgroups (launch: 128 each): softmax, correction, copies and MMA
-  static constexpr int REG_LAUNCH = 128, REG_SOFT = 120, REG_CORR = D > 64 ? 232 : 144,
+  // registers per thread of the warpgroups (launch: 128 each): softmax, correction, copies and MMA (head_dim 64
+  // spills at 120: 485 against 481 us for 2,048 queries over 8,192 keys, 64/8 heads)
+  static constexpr int REG_LAUNCH = 128, REG_SOFT = D > 64 ? 120 : 128, REG_CORR = D > 64 ? 232 : 144,
                        REG_MISC = 4 * REG_LAUNCH - 2 * REG_SOFT - REG_CORR;
   static_assert(REG_SOFT <= REG_LAUNCH && REG_CORR >= REG_LAUNCH && REG_MISC <= REG_LAUNCH && REG_MISC >= 24 &&
                     REG_SOFT % 8 == 0 && REG_CORR % 8 == 0 && REG_MISC % 8 == 0,
@@ -108,7 +113,7 @@ struct BlockPrefillCfg {
   static constexpr int OFF_K = OFF_Q + 2 * TILE;
   static constexpr int OFF_V = OFF_K + NS * TILE;
   static constexpr int OFF_P = OFF_V + NS * TILE;   // per buffer: hi, lo
-  static constexpr int OFF_F = OFF_P + PBUF * 2 * PTERM;  // factors [2][128] float2 (acc, O_t); last: (l, m)
+  static constexpr int OFF_F = OFF_P + PBUF * 2 * PTERM;  // factors [2][128] float2 (acc, O_t); last: (1 / l, 2^o)
   static constexpr int OFF_SC = OFF_F + 2 * BM * 8;
   static constexpr int OFF_BAR = OFF_SC + SCN * SCF * 4;
   static constexpr int NBAR = 18 + 4 * NS + SCN;
@@ -150,9 +155,9 @@ FKV_DEV uint32_t peer_address(const void* p, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
   return r;
 }
-FKV_DEV float2 peer_ld2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+FKV_DEV float peer_ld(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
   return v;
 }
 FKV_DEV float4 peer_ld4(uint32_t a) {
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(512, 1)
 
   if (warp < C::SW) {
     // ============================================================ softmax warps
-    regs_dec<C::REG_SOFT>();
+    if constexpr (C::REG_SOFT < C::REG_LAUNCH) regs_dec<C::REG_SOFT>();
     const int hf = lane >> 4;                                  // column half
     const int rb = (warp & 3) * 32 + (warp >> 2) * 16;         // first TMEM lane
     const int i = rb + (lane & 15);                            // row (TMEM lane i)
@@ -320,7 +325,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     const int lim_row = (p.causal && row_ok) ? min(T, pos + 1) : T;  // keys [lo_row, lim_row) visible
     const int lo_row = (WIN && row_ok) ? max(0, pos - p.window + 1) : 0;
-    float m = -1e30f, l = 0.f;  // l: this thread's columns only
+    float m = -kHuge, l = 0.f;  // r, and l of this thread's columns only
     bool ok = true;
     for (int t = 0; t < n_t; ++t) {
       if ((t & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
@@ -343,12 +348,12 @@ __global__ void __launch_bounds__(512, 1)
       for (int c = 0; c < C::HC / 32; ++c) tmem_ld32_16x2<C::HC>(sc + 32 * c, *reinterpret_cast<float(*)[32]>(v + 32 * c));
       const bool p_ready = t < C::PBUF || mbar_test_wait(&p_free[pb], ((t / C::PBUF) - 1) & 1);
       const bool f_ready = t < 2 || mbar_test_wait(&f_free[t & 1], ((t >> 1) - 1) & 1);
-      // this half's four blocks: ks, lv, 2^-lv
+      // this half's four blocks: ks, L, 2^(o - L)
       if (!pf_wait_warp(&sc_full[t % C::SCN], (t / C::SCN) & 1)) { ok = false; break; }
       const float* scl = sSc + (t % C::SCN) * C::SCF + 4 * hf;
       const float4 ks4 = *reinterpret_cast<const float4*>(scl), lv4 = *reinterpret_cast<const float4*>(scl + 8),
                    iv4 = *reinterpret_cast<const float4*>(scl + 16);
-      const float vmax = sSc[(t % C::SCN) * C::SCF + 24];
+      const float rare = sSc[(t % C::SCN) * C::SCF + 25];
       // (plus 2^-126, so that a hidden score of -inf stays one where the product is zero: a row of zeros, a
       // K scale of zero; |S| < 2^26, so that this adds less than 2^-100 to a score)
       constexpr float kLeast = 1.17549435e-38f;
@@ -367,19 +372,32 @@ __global__ void __launch_bounds__(512, 1)
         for (int j = 0; j < C::HC; ++j)
           if (j >= lim || j < lo) v[j] = -INFINITY;
       }
-      float tmax = -1e30f;  // (finite, so that a row that sees nothing of the tile adds zeros)
+      const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
+      float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+      float tmax = -kHuge;  // (finite, so that a row that sees nothing of the tile adds zeros)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) tmax = fmaxf(tmax, max_tree<16>(v + 16 * k) * cb[k]);
+      for (int k = 0; k < 4; ++k) tmax = fmaxf(tmax, fmaf(max_tree<16>(v + 16 * k), cb[k], lv[k]));
       tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16));
       // one of the two factors is 1, the other 2^-|m - tmax|
       const float e = ex2(-fabsf(m - tmax));
       const float alpha = m > tmax ? 1.f : e, corr = m > tmax ? e : 1.f;
+      // the sum's own factors: in a rare tile (block_scales; the same in every thread) in two halves, 2^-|r - R_t|
+      // itself may underflow
+      if (rare == 0.f) {
+        l *= alpha;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) iv[k] *= corr;
+      } else {
+        const float half = ex2(-0.5f * fabsf(m - tmax)), la = m > tmax ? 1.f : half, lc = m > tmax ? half : 1.f;
+        l = fminf(l * rare, kFloatMax) * la * la;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) iv[k] = iv[k] * lc * lc;
+      }
       m = fmaxf(m, tmax);
       if (!__all_sync(0xffffffffu, p_ready) && !pf_wait_warp(&p_free[pb], ((t / C::PBUF) - 1) & 1)) { ok = false; break; }
       uint8_t* P = sP + pb * 2 * C::PTERM;
-      const float nb[4] = {lv4.x - tmax, lv4.y - tmax, lv4.z - tmax, lv4.w - tmax};
-      const float iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
-      float lt = 0.f;
+      const float top = tmax - kLog2E4m3Max;
+      const float nb[4] = {lv[0] - top, lv[1] - top, lv[2] - top, lv[3] - top};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // block k: 16 columns, 16 bytes of each term
         const float2 c2 = make_float2(cb[k], cb[k]), n2 = make_float2(nb[k], nb[k]);
@@ -393,24 +411,40 @@ __global__ void __launch_bounds__(512, 1)
           sum = __fadd2_rn(sum, __fadd2_rn(x0, x1));
           split4(x0, x1, hi[j], lw[j]);
         }
-        lt = fmaf(sum.x + sum.y, iv[k], lt);
+        l = fmaf(sum.x + sum.y, fabsf(iv[k]), l);
         uint8_t* dst = P + swz(static_cast<uint32_t>(i * 128 + c0 + 16 * k), 128);
         *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(dst + C::PTERM) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
       }
-      l = fmaf(l, alpha, corr * lt);
+      if (rare != 0.f) {  // a scale that counts as zero has no P (unrolled here: 1,098 us on 2,048 queries over 32,768 keys
+                          // at head_dim 128, rolled 1,141, behind the factors 1,118)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (iv[k] > 0.f) continue;
+          uint8_t* dst = P + swz(static_cast<uint32_t>(i * 128 + c0 + 16 * k), 128);
+          *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4*>(dst + C::PTERM) = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
       if (!__all_sync(0xffffffffu, f_ready) && !pf_wait_warp(&f_free[t & 1], ((t >> 1) - 1) & 1)) { ok = false; break; }
-      if (hf == 0) sF[(t & 1) * C::BM + i] = make_float2(alpha, corr * vmax);
+      if (hf == 0) sF[(t & 1) * C::BM + i] = make_float2(alpha, corr);
       mbar_arrive_warp(&f_full[t & 1]);
       fence_proxy_async_smem();
       mbar_arrive_warp(&p_full[pb]);
     }
     tmem_ld_wait();  // no load left in flight on an early exit
-    // ---- the rows' l and m take the factor slot after the last tile's
+    // ---- the rows' 1 / l and 2^o take the factor slot after the last tile's; SPLIT: the log2-sum-exp
+    // (log2 448 too large in every share; -kHuge for a row that sees nothing) lies over the query, whose
+    // products are done (without a tile: which every warp has written)
     l += __shfl_xor_sync(0xffffffffu, l, 16);
+    const float o = n_t > 0 ? sSc[((n_t - 1) % C::SCN) * C::SCF + 24] : 0.f;
     if (ok && n_t >= 2) ok = pf_wait_warp(&f_free[n_t & 1], ((n_t >> 1) - 1) & 1);
+    if (SPLIT && ok && n_t == 0) ok = pf_wait_warp(q_full, 0);
     if (ok) {
-      if (hf == 0) sF[(n_t & 1) * C::BM + i] = make_float2(l, m);
+      if (hf == 0) {
+        sF[(n_t & 1) * C::BM + i] = make_float2(l == 0.f ? 0.f : 1.f / l, pow2i(o));  // (a row that sees no key: zero)
+        if constexpr (SPLIT) reinterpret_cast<float*>(sQ)[i] = l == 0.f ? -kHuge : m - o + lg2(l);
+      }
       mbar_arrive_warp(&f_full[n_t & 1]);
     } else {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
@@ -481,28 +515,29 @@ __global__ void __launch_bounds__(512, 1)
       }
       if (!ok) break;
     }
-    // ---- epilogue (every lane loads; rows past the chunk do not store): acc / (256 l) as bf16, or
-    // with SPLIT acc as it is, into shared memory over the K and V stages, whose copies and products are
+    // ---- epilogue (every lane loads; rows past the chunk do not store): 2^o acc / l as bf16, or
+    // with SPLIT in float32, into shared memory over the K and V stages, whose copies and products are
     // all done: four columns of a row at [column / 4][row]
     if (ok) ok = pf_wait_warp(&f_full[n_t & 1], (n_t >> 1) & 1);
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     } else {
-      const float l = sF[(n_t & 1) * C::BM + i].x;
-      const float f = l == 0.f ? 0.f : 1.f / (256.f * l);  // (a row that sees no key: zero)
+      const float2 f = sF[(n_t & 1) * C::BM + i];
       __nv_bfloat16* dst = p.out + (static_cast<long long>(r0 + q0 + it) * p.Hq + g * G + h) * D;
       float4* part = reinterpret_cast<float4*>(sK);
       auto store32 = [&](int c, const float* x) {
         if (!row_ok) return;
         if constexpr (SPLIT) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) part[(8 * c + j) * C::BM + i] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+          for (int j = 0; j < 8; ++j)
+            part[(8 * c + j) * C::BM + i] =
+                make_float4(x[4 * j] * f.x * f.y, x[4 * j + 1] * f.x * f.y, x[4 * j + 2] * f.x * f.y, x[4 * j + 3] * f.x * f.y);
         } else {
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j] * f, x[2 * j + 1] * f);
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[2 * j] * f.x * f.y, x[2 * j + 1] * f.x * f.y);
             w[j] = *reinterpret_cast<const uint32_t*>(&y);
           }
           uint4* o4 = reinterpret_cast<uint4*>(dst + 32 * c);
@@ -552,6 +587,7 @@ __global__ void __launch_bounds__(512, 1)
         raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
         return 0;
       };
+      ScaleRange range;
       float ks_n = 0.f, vs_n = 0.f;
       auto read_scales = [&](int id) {
         ks_n = vs_n = 0.f;
@@ -587,19 +623,19 @@ __global__ void __launch_bounds__(512, 1)
         }
         last[st] = use;
         if (is_k) {
-          // the tile's scales.  lv is kept above -32 (a V scale 2^-40 of the tile's largest, zeros
-          // too, whose P falls below the terms' range), so that its inverse stays finite.
-          float vmax = vs;
-#pragma unroll
-          for (int off = 4; off > 0; off >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-          const float lv = vs > 0.f ? fmaxf(lg2(__fdividef(vs, vmax)) + 8.f, -32.f) : -32.f;
+          // the tile's scales, those of blocks that no row of this CTA sees left out
+          const int lb = (tb + t) * C::NBLK + lane;
+          const BlockScale sc = block_scales(range, vs, lane < C::NBLK && lb >= kv_lo >> 4 && lb < (kv_end + 15) >> 4);
           float* slot = sSc + (t % C::SCN) * C::SCF;
           if (lane < C::NBLK) {
             slot[lane] = ks;
-            slot[8 + lane] = lv;
-            slot[16 + lane] = ex2(-lv);
+            slot[8 + lane] = sc.lv;
+            slot[16 + lane] = sc.iv;
           }
-          if (lane == 0) slot[24] = vmax;
+          if (lane == 0) {
+            slot[24] = range.o;
+            slot[25] = sc.rare;
+          }
           mbar_arrive_warp(&sc_full[t % C::SCN]);
         }
       }
@@ -705,8 +741,8 @@ __global__ void __launch_bounds__(512, 1)
     tmem_dealloc(tmem, C::TM_COLS);
   }
   if constexpr (SPLIT) {
-    // the shares (acc, l, m)_r of every row: M = max m_r, out = sum 2^(m_r - M) acc_r / (256 sum 2^(m_r - M) l_r),
-    // by the softmax warps, whose register budget holds it
+    // the shares (o, lse)_r of every row: M = max lse_r, out = sum 2^(lse_r - M) o_r / sum 2^(lse_r - M), by the
+    // softmax warps, whose register budget holds it
     cluster_sync();
     const int rows = toks * GC;
     constexpr int kMergers = 32 * C::SW;
@@ -714,21 +750,20 @@ __global__ void __launch_bounds__(512, 1)
       const int c = e / rows, i = e - c * rows;
       const int it = i / GC, h = h_first + i - it * GC;
       if (h >= G) continue;
-      float M = -1e30f, L = 0.f;
+      float M = -kHuge, L = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int r = 0; r < shares; ++r) {
-        const int n_r = (r + 1) * n_all / shares - r * n_all / shares;  // where CTA r left its (l, m)
-        const float2 lm = peer_ld2(peer_address(sF + (n_r & 1) * C::BM + i, r));
+        const float lse = peer_ld(peer_address(reinterpret_cast<float*>(sQ) + i, r));
         const float4 x = peer_ld4(peer_address(reinterpret_cast<float4*>(sK) + c * C::BM + i, r));
-        const float mx = fmaxf(M, lm.y), a = ex2(M - mx), w = ex2(lm.y - mx);
+        const float mx = fmaxf(M, lse), a = ex2(M - mx), w = ex2(lse - mx);
         M = mx;
-        L = fmaf(L, a, w * lm.x);
+        L = fmaf(L, a, w);
         o.x = fmaf(o.x, a, w * x.x);
         o.y = fmaf(o.y, a, w * x.y);
         o.z = fmaf(o.z, a, w * x.z);
         o.w = fmaf(o.w, a, w * x.w);
       }
-      const float f = L == 0.f ? 0.f : 1.f / (256.f * L);
+      const float f = 1.f / L;
       __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + (static_cast<long long>(r0 + q0 + it) * p.Hq + g * G + h) * D + 4 * c);
       dst[0] = __floats2bfloat162_rn(o.x * f, o.y * f);
       dst[1] = __floats2bfloat162_rn(o.z * f, o.w * f);
