@@ -29,6 +29,25 @@ FKV_DEV uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
   return r;
 }
 
+// A query row enters the products scaled by 2^-k, its largest magnitude (float32 bits `amax`, finite) in (224, 448], as
+// two e4m3 terms.
+FKV_DEV int query_exponent(uint32_t amax) {
+  return max(static_cast<int>(amax >> 23) - 127 - 8 + ((amax & 0x7FFFFFu) > 0x600000u ? 1 : 0), -126);  // 448 = 1.75 * 2^8
+}
+
+// Four scaled query elements as two terms: hi the nearest code, lo that of what hi leaves.  A bf16 element
+// has 8 significant bits, 4 of them (the nearest, so that the rest has at most 4) in hi: exact down to 1/4, below that
+// within 2^-10, half a step of e4m3's subnormals, which is less than 2^-17 of the row's largest element.
+FKV_DEV void split4_query(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
+  hi = f32x4_to_e4m3x4(a, b);
+  uint32_t h01, h23;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"(static_cast<uint16_t>(hi & 0xFFFFu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"(static_cast<uint16_t>(hi >> 16)));
+  const float2 ha = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+  const float2 hb = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+  lo = f32x4_to_e4m3x4(make_float2(a.x - ha.x, a.y - ha.y), make_float2(b.x - hb.x, b.y - hb.y));
+}
+
 constexpr float kLog2E4m3Max = 8.807354922057604f;  // log2(448)
 
 // 2^n of a whole number -126 <= n <= 127.

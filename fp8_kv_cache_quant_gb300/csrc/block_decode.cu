@@ -2,12 +2,11 @@
 // with the bf16 query and P each as two e4m3 terms, FP32 accumulation in tensor memory, each
 // tile's partial promoted into FP32 registers, the context split evenly over the CTAs.
 //
-// Mathematics.  With q' = q 2^-k (k per head, so that the row's largest magnitude lies in [128, 256))
-// and q' = hi + lo, hi the leading 3 fraction bits, the score of key j is
+// Mathematics.  With q' = q 2^-k (k per head, so that the row's largest magnitude lies in (224, 448])
+// and q' = hi + lo, hi the nearest e4m3 value, the score of key j is
 //   x_j = (hi . k8_j + lo . k8_j) * ks[block(j)] * c,   c = 2^k softmax_scale log2(e);
-// a bf16 value has 8 significant bits and e4m3 4, so that hi + lo is q' down to 2^-18 of the row's
-// largest element.  Per tile, with y_j = x_j + L[block(j)], L = log2 vs, and the tile's maximum R_t of y,
-//   P_j = 2^(y_j - R_t) * 448 = hi + lo likewise,   O_t = sum_j (hi + lo)_j v8_j,
+// hi + lo is q' down to 2^-17 of the row's largest element (split4_query).  Per tile, with y_j = x_j + L[block(j)], L = log2 vs, and the tile's maximum R_t of y,
+//   P_j = 2^(y_j - R_t) * 448 = hi + lo, hi its leading 3 fraction bits,   O_t = sum_j (hi + lo)_j v8_j,
 // and the running state is r' = max(r, R_t), acc = acc 2^(r - r') + O_t 2^(R_t - r'),
 // l = l 2^(r - r') + 2^(R_t - r') sum_j P_j / 448 * 2^(o - L[block(j)]); the output 2^o acc / (448 l).  P is taken against the
 // largest p vs of the tile's visible keys, whichever key has it: it loses what lies below 2^-17 of
@@ -511,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     bool fresh = true;  // the next tile begins a piece
     for (int u = 0; ok && u < n; ++u) {
       if (fresh) {
-        // ---- the piece's query: head h's row scaled to [128, 256), as two terms (the products with the
+        // ---- the piece's query: head h's row scaled to (224, 448], as two terms (the products with the
         // last piece's query are done: their S was read).  8 threads per row.  A row with a NaN or
         // an infinity makes its scores, and so its output, NaN.
         fresh = false;
@@ -524,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
           for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
 #pragma unroll
         for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const int e = max(static_cast<int>(amax >> 23) - 127 - 7, -126);  // q = q' * 2^e
+        const int e = query_exponent(amax);  // q = q' * 2^e
         const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
         if ((i & 7) == 0 && row < G)
           qs_s[row] = amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23)
@@ -537,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
-            split4(x0.x * down, x0.y * down, x1.x * down, x1.y * down, wh[j], wl[j]);
+            split4_query(make_float2(x0.x * down, x0.y * down), make_float2(x1.x * down, x1.y * down), wh[j], wl[j]);
           }
           const int byte = c * 16;
           uint8_t* sub = sQ + (byte / C::RB) * C::QSUB;

@@ -2,12 +2,11 @@
 // with the bf16 query and P each as two e4m3 terms, FP32 accumulation in tensor memory, each
 // tile's partial promoted into FP32 registers.
 //
-// Mathematics.  With q' = q 2^-k (k per row, so that the row's largest magnitude lies in [128, 256))
-// and q' = hi + lo, hi the leading 3 fraction bits, the scores of a tile of 128 keys are
+// Mathematics.  With q' = q 2^-k (k per row, so that the row's largest magnitude lies in (224, 448])
+// and q' = hi + lo, hi the nearest e4m3 value, the scores of a tile of 128 keys are
 //   x_j = (hi . k8_j + lo . k8_j) * c * ks[block(j)],   c = 2^k softmax_scale log2(e);
-// a bf16 value has 8 significant bits and e4m3 4, so that hi + lo is q' down to 2^-18 of the row's
-// largest element.  With y_j = x_j + L[block(j)], L = log2 vs, and the row's maximum R_t of y over the tile,
-//   P_j = 448 * 2^(y_j - R_t),  P = hi + lo likewise,
+// hi + lo is q' down to 2^-17 of the row's largest element (split4_query).  With y_j = x_j + L[block(j)], L = log2 vs, and the row's maximum R_t of y over the tile,
+//   P_j = 448 * 2^(y_j - R_t),  P = hi + lo, hi its leading 3 fraction bits,
 //   l_t = sum_blocks 2^(o - L) sum_j P_j,  O_t = sum_j (hi + lo)_j v8_j,
 // and the running state is r' = max(r, R_t), acc = acc 2^(r - r') + O_t 2^(R_t - r'),
 // l = l 2^(r - r') + l_t 2^(R_t - r'); the output 2^o acc / l.  P is taken against the largest p vs of
@@ -300,7 +299,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int j = 0; j < 4; ++j) amax = max(amax, max((in[j] << 16) & 0x7FFF0000u, in[j] & 0x7FFF0000u));
       }
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
-      const int k = max(static_cast<int>(amax >> 23) - 127 - 7, -126);
+      const int k = query_exponent(amax);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
       // a row with a NaN or an infinity makes its scores, and so its output, NaN
       cst = amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k) << 23)
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(512, 1)
         for (int j = 0; j < 4; ++j) {
           float2 x0 = bf16x2_to_f2(in[2 * j]), x1 = bf16x2_to_f2(in[2 * j + 1]);
           x0.x *= down; x0.y *= down; x1.x *= down; x1.y *= down;
-          split4(x0, x1, hi[j], lo[j]);
+          split4_query(x0, x1, hi[j], lo[j]);
         }
         const int byte = hf * (D / 2) + c * 8;
         uint8_t* dst = sQ + (byte / C::RB) * C::SUB + swz(static_cast<uint32_t>(i * C::RB + byte % C::RB), C::RB);

@@ -436,7 +436,7 @@ size_t fp8_block_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, 
  * nor P rounded to 8 bits:
  *   s_j = q . (k8_j * k_scale[block(j)][g]) * softmax_scale,
  *   out = sum_j softmax(s)_j * (v8_j * v_scale[block(j)][g])   (bf16).
- * The bf16 query enters exactly (down to 2^-18 of its head's largest element), P with at least
+ * The bf16 query enters exactly (down to 2^-17 of its head's largest element), P with at least
  * the precision of bf16 (down to 2^-17 of the largest p * v_scale among the visible keys of its
  * 128-key tile; 256 keys at head_dim 64), every sum is FP32.  A V scale that is 2^-100
  * of the largest of its tile or less (2^-198 of its sequence's) counts as zero.  A query row that holds a NaN or an infinity gives a NaN

@@ -9,6 +9,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import blockcache
 from test_gpu_block_attn import Case
 
 f = pytest.importorskip("fp8_kv_cache_quant_gb300")
@@ -104,3 +105,41 @@ def test_value_scales_at_the_ends_of_float32(d, top):
         live = c.pools[1][c.table[0]]
         c.pools[1][c.table[0]] = np.where((live & 0x7F) > 0x38, (live & 0x80) | 0x38, live)
         _rows(c.decode() if new is None else c.prefill(), c.exact()[0], new)
+
+
+# ------------------------------------------------------------------ queries
+
+def _terms(x):
+    """The worst distance of a bf16 element from its two e4m3 terms when the leading one is truncated to 3 fraction
+    bits and each is then rounded by itself (x scaled so that the row's largest element is 128)."""
+    lead = (x.view(torch.int32) & -(1 << 20)).view(torch.float32)
+    e4 = lambda y: y.to(torch.float8_e4m3fn).float()  # noqa: E731
+    return e4(lead) + e4(x - lead) - x
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_queries_with_an_outlier_channel(d):
+    """One element 2^13 times the others, whose keys are zero there: the scores are made by the small ones alone.  With
+    its row's largest element brought to above 224, the remainder of a leading term is off by at most 2^-10, half a
+    step of e4m3's subnormals.  With |k| = 1 in d - 1 channels the scores are then off by at most
+    s = tau (d - 1) |q|max 2^-10 / 224, and the output by (e^2s - 1) sum p |v|, besides the rounding of P (2^-8) and
+    of the output (2^-9)."""
+    small = torch.arange(0x3C00, 0x3D80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).float()   # 2^-7 .. 2^-4
+    worst = float(small[int(_terms(small).abs().argmax())])
+    assert abs(_terms(torch.tensor([worst])).item()) > 2.0 ** -9.6
+    for new in (None, [5], [200]):
+        c = Case([300], 4, 1, d, new=new, seed=d, spread=0)
+        c.q[:] = worst / 128.0
+        c.q[..., 3] = 1.0
+        sign = np.random.default_rng(d).integers(0, 2, c.pools[0].shape[:3])[..., None]
+        c.pools[0] = np.broadcast_to(np.where(sign, 0x38, 0xB8), c.pools[0].shape).astype(np.uint8).copy()
+        c.pools[1] = c.pools[0].copy()                          # values +-1, along the scores
+        c.pools[0][..., 3] = 0
+        c.scales[0][:], c.scales[1][:] = 1.0, 1.0
+        tau = 2.0 ** 12 / d
+        ref, mag = c.exact(softmax_scale=tau)[0], blockcache.p_bound(
+            c.q.float().numpy().astype(np.float64), c.pools[0], c.pools[1], c.scales[0], c.scales[1], c.table, c.ctx, c.cu, softmax_scale=tau)
+        s = tau * (d - 1) * 2.0 ** -10 / 224.0
+        out = (c.decode(softmax_scale=tau) if new is None else c.prefill(softmax_scale=tau)).float().cpu().numpy().astype(np.float64)
+        tol = (np.expm1(2.0 * s) + 2.0 ** -8) * mag + 2.0 ** -9 * np.abs(ref)
+        assert np.all(np.abs(out - ref) <= tol), (new, float((np.abs(out - ref) / tol).max()))
