@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
   for (int w = 0; w < WT; ++w) amax = max(amax, amax_s[warp - part + w]);
   float s = pow2_scale(amax);
   uint8_t* block = (is_v ? p.vc : p.kc) + (static_cast<size_t>(id) * p.H + g) * 16 * D;
-  if (kept > 0 && old >= 1.17549435e-38f && old <= 3.402823466e+38f) {  // a normal positive number
+  if (kept > 0 && old >= 0.f && old <= 3.402823466e+38f) {  // (0 and subnormal numbers are below every s)
     if (old >= s) {
       s = old;
     } else {

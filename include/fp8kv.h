@@ -245,8 +245,9 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
  *   a block that already holds tokens of the sequence (its first new slot is j > 0) takes
  *          s = max(old scale, need), and when that is larger than the old one, its codes c in
  *          slots 0 .. j - 1 become e4m3(fl32(c * fl32(old / s))) — exact for powers of two,
- *          save for what falls below the subnormal step.  (An old scale that is not a normal
- *          positive number counts as 0: s = need, and the codes stay.)
+ *          save for what falls below the subnormal step.  (So the codes of a block of scale 0
+ *          become zeros.  A block whose scale is negative, infinite or NaN holds no values: it
+ *          takes s = need, and its codes stay.)
  *   new codes are e4m3(fl32(x * fl32(1 / s))), round-to-nearest-even, saturating (infinities
  *          become +-448, NaN stays NaN).
  * Slots behind T_b - 1, and every other block, keep their bytes and scales.  A block that a

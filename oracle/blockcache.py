@@ -60,7 +60,7 @@ def append(x, start, ids, pool, scale):
             s = scale_for(y)
             if kept:
                 old = float(scale[blk, h])
-                if math.isfinite(old) and old >= 2.0 ** -126:
+                if math.isfinite(old) and old >= 0.0:
                     if old >= s:
                         s = old
                     else:

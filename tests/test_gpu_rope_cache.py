@@ -327,3 +327,28 @@ def test_writes_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert _same(out, ref) and torch.equal(got.k_cache, want.k_cache) and torch.equal(got.v_scale, want.v_scale)
+
+
+def test_block_cache_continues_a_block_of_zero_or_subnormal_scale():
+    """Tokens of a block whose scale is 0 (or below 2^-126) are worth code * scale before and after the block takes
+    a larger scale, down to half of that scale's subnormal step 2^-9; in the oracle's bytes."""
+    rng = np.random.default_rng(21)
+    h, d = 2, 64
+    for old in (0.0, 2.0 ** -130, 2.0 ** -149, 1.5 * 2.0 ** -128):
+        for size in (1.0, 2.0 ** -123):
+            cache = _pools(rng, 2, h, d)
+            for p in (cache.k_cache, cache.v_cache):
+                p.copy_(torch.where((p & 0x7F) == 0x7F, 0x7E, p))
+            cache.k_scale.fill_(old), cache.v_scale.fill_(old)
+            k = _bf16(rng, 3, h, d, scale=size)
+            before = _snapshot(cache)
+            f.kv_block_cache(k.cuda(), k.cuda(), torch.tensor([0, 3], dtype=torch.int32).cuda(), 3, cache,
+                             torch.ones(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([11], dtype=torch.int32).cuda())
+            after = _snapshot(cache)
+            for a, b, s0, s1 in ((before[0], after[0], before[2], after[2]), (before[1], after[1], before[3], after[3])):
+                was, now = (e4m3.decode(x[1, :, :8]) * s[1].astype(np.float64)[:, None, None] for x, s in ((a, s0), (b, s1)))
+                assert np.all(np.abs(now - was) <= 2.0 ** -4 * np.abs(was) + 2.0 ** -10 * s1[1].astype(np.float64)[:, None, None]), old
+                assert np.array_equal(a[0], b[0]) and np.array_equal(a[1, :, 11:], b[1, :, 11:])
+            want = _oracle_append(before, k, k, [3], [11], np.ones((1, 1), int), None, False)
+            for got, ref in zip(after, want):
+                assert np.array_equal(got, ref), old

@@ -94,3 +94,18 @@ def test_attend_is_torch_softmax(causal, window):
             if window:
                 w[key <= pos - window] = -math.inf
             assert np.allclose(got[cu[b]:cu[b + 1], h], (torch.softmax(w, 1) @ V).numpy(), rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.parametrize("old", [0.0, 2.0 ** -130, 2.0 ** -149, 1.5 * 2.0 ** -128])
+def test_append_continues_a_block_of_zero_or_subnormal_scale(old):
+    """A value is code * scale whatever the scale >= 0: kept tokens are worth what they were, down to half of the
+    subnormal step 2^-9 of the block's new scale."""
+    for x in (1.0, 2.0 ** -125):
+        pool = np.full((1, 1, 16, 8), 0x7E, np.uint8)
+        pool[0, 0, 1] = 0xB8
+        scale = np.full((1, 1), old, np.float32)
+        before = e4m3.decode(pool[0, 0, :3]) * float(scale[0, 0])
+        blockcache.append(np.full((1, 1, 8), x), 3, [0], pool, scale)
+        assert scale[0, 0] == blockcache.scale_for([x])
+        after = e4m3.decode(pool[0, 0, :3]) * float(scale[0, 0])
+        assert np.all(np.abs(after - before) <= 2.0 ** -4 * np.abs(before) + float(scale[0, 0]) * 2.0 ** -10)
