@@ -442,13 +442,13 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
   if (!supported_head_dim(cache.head_dim)) return FKV_UNSUPPORTED;
   if (num_q_heads > 8192 || cache.num_kv_heads > 8192) return FKV_UNSUPPORTED;
   if (gran != FKV_SCALE_PER_TENSOR && gran != FKV_SCALE_PER_HEAD) return FKV_INVALID_ARG;
-  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   fkv_status st = FKV_OK;
   const bool bf16 = layer_is_bf16(layer, skip_layer_mask, num_layers, &st);
   if (st != FKV_OK) return st;
   st = check_rope(rope, cache.head_dim);
   if (st != FKV_OK) return st;
   if (n_tokens == 0) return FKV_OK;
+  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
   const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
   if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
@@ -498,15 +498,15 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
   fkv_status st = check_block_cache(cache);
   if (st != FKV_OK) return st;
   if (batch > 65535 || num_q_heads > 8192 || cache.num_kv_heads > 8192 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
-  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   const bool turned = rope.cos_sin != nullptr;
   if (turned) {
     st = check_rope(rope, cache.head_dim);
     if (st != FKV_OK) return st;
-  } else if (q != nullptr || rope.rot_dim != 0) {
+  } else if (num_q_heads > 0 || rope.rot_dim != 0) {
     return FKV_INVALID_ARG;
   }
   if (n_tokens == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
+  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
   const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
   const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
   if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;

@@ -233,3 +233,20 @@ def test_rope_table():
     assert t.shape == (7, 32) and t.dtype is torch.float32
     assert torch.equal(t[0], torch.cat((torch.ones(16), torch.zeros(16))))
     assert abs(float(t[3, 1]) - torch.cos(torch.tensor(3.0 * 10000.0 ** (-2 / 32), dtype=torch.float64)).item()) < 2 ** -24
+
+
+def test_empty_tensors_do_nothing(lib):
+    """No tokens, with and without queries, through the binding's own tensors (whose addresses are null)."""
+    e = lambda *s: torch.empty(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32, i64 = (lambda *s: torch.zeros(*s, dtype=torch.int32)), torch.zeros(0, dtype=torch.int64)
+    pool, s, t = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.ones(3, 2), torch.zeros(9, 64)
+    b = f.load_binding()
+    for q, out in ((None, None), (e(0, 4, 64), None), (e(0, 4, 64), e(0, 4, 64)), (e(9, 4, 64)[:0], None)):
+        st, got = b.kv_rope_cache(0, q, e(0, 2, 64), e(0, 2, 64), i64, i64, t, 0, pool, pool, 0, s[0, :1], s[0, :1], 0, 0, None, 0, 0, out, None)
+        assert st == f.OK and (got is None if q is None else got.shape == (0, 4, 64))
+        for n, batch in ((0, 2), (0, 0)):
+            st, got = b.kv_block_cache(0, e(n, 2, 64), e(n, 2, 64), i32(batch + 1), 3, pool, pool, s, s, i32(batch, 4), i32(batch), t, 0, q, out, None)
+            assert st == f.OK and (got is None if q is None else got.shape == (0, 4, 64))
+    assert b.fp8_block_prefill_attn(0, e(0, 4, 64), i32(3), 3, pool, pool, s, s, i32(2, 4), i32(2), 0.0, 1, 0, None, None)[0] == f.OK
+    ws = torch.zeros(256, dtype=torch.uint8)
+    assert b.fp8_block_decode_attn(0, e(0, 4, 64), pool, pool, s, s, i32(0, 4), i32(0), 0.0, 0, None, ws, None)[0] == f.OK
