@@ -168,8 +168,9 @@ struct BlockDecodePlan {
   size_t cnt_bytes = 0, lse_bytes = 0, o_bytes = 0;
 };
 
-// Places that the counters have at least, so that the scratch of one call never lies where a call of
-// another batch counts.
+// Piece counters, one per CTA: a unit of several pieces counts at the CTA of its first, which can be that of
+// one such unit only.  Their number is the same for every call, so that the scratch of one never lies
+// where another counts.
 constexpr long long kBlockDecodeCounters = 16384;
 
 BlockDecodePlan plan_block_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D) {
@@ -177,9 +178,9 @@ BlockDecodePlan plan_block_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D)
   plan.halves = Hq / Hkv == 16 ? 1 : 0;
   const int G = (Hq / Hkv) >> plan.halves;
   const long long units = static_cast<long long>(B) * Hkv << plan.halves;
-  plan.ctas = std::min<long long>(static_cast<long long>(current_num_sms()) * fkv::block_decode_ctas_per_sm(D), 160 * units);
+  plan.ctas = std::min({static_cast<long long>(current_num_sms()) * fkv::block_decode_ctas_per_sm(D), 160 * units, kBlockDecodeCounters});
   const size_t rows = static_cast<size_t>(plan.ctas + units) * G;
-  plan.cnt_bytes = align256(std::max(units, kBlockDecodeCounters) * sizeof(int32_t));
+  plan.cnt_bytes = kBlockDecodeCounters * sizeof(int32_t);
   plan.lse_bytes = align256(rows * sizeof(float));
   plan.o_bytes = rows * D * sizeof(float);
   return plan;

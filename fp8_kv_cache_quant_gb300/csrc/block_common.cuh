@@ -169,7 +169,7 @@ struct BlockDecodeParams {
   int halves;                                 // 1: units 2 g and 2 g + 1 share KV head g
   float sm_scale_log2;                        // softmax_scale * log2(e)
   int window;
-  int32_t* done;                              // [B * Hkv] pieces finished, zero between calls
+  int32_t* done;                              // [N] pieces finished of the unit that CTA k begins, zero between calls
   float* lse_part;                            // [N + B * Hkv][G], base 2
   float* o_part;                              // [N + B * Hkv][G][D]
   __nv_bfloat16* out;                         // [B][Hq][D]

@@ -1016,9 +1016,9 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     const int unit = pend_s[3 * j], k0 = pend_s[3 * j + 1], ns = pend_s[3 * j + 2];
     if (ns == 0) continue;
     if (threadIdx.x == 0) {
-      const int old = count_acq_rel(&p.done[unit]);
+      const int old = count_acq_rel(&p.done[k0]);  // (CTA k0 begins no other unit that goes on behind its range)
       if (old >= ns) raise_fault(p.fault, FKV_FAULT_WORKSPACE);
-      if (old == ns - 1) p.done[unit] = 0;
+      if (old == ns - 1) p.done[k0] = 0;
       *last_s = old == ns - 1;
     }
     __syncthreads();

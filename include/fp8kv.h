@@ -449,12 +449,10 @@ size_t fp8_block_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, 
  *
  *   q, block_table, context_lens, softmax_scale, window, out  as for fp8_decode_attn
  *   workspace     device, >= fp8_block_decode_attn_workspace_size(...) bytes, 256-byte aligned,
- *                 zero-filled before its first call.  Its first 4 * max(n, 16384) bytes are counters
- *                 that a call finds and leaves zero, n = batch * num_kv_heads (twice that for groups of
- *                 16 heads); the rest is scratch.  Calls that may overlap on the GPU (other streams,
- *                 two captured graphs) each need their own; calls in one stream share one, of any
- *                 batch, heads and head_dim that it is large enough for (where n passes 16384: zero it
- *                 again when n grows).  A counter found non-zero sets FKV_FAULT_WORKSPACE
+ *                 zero-filled before its first call.  Its first 65,536 bytes are counters that a call
+ *                 finds and leaves zero; the rest is scratch.  Calls that may overlap on the GPU (other
+ *                 streams, two captured graphs) each need their own; calls in one stream share one, of any
+ *                 batch, heads and head_dim that it is large enough for.  A counter found non-zero sets FKV_FAULT_WORKSPACE
  * Limits as for fp8_decode_attn.  A sequence with no key gets a zero row.
  */
 fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,

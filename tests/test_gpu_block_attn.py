@@ -626,3 +626,15 @@ def test_serving_run(d, hq, h, style):
             got = blockcache.sequence(cache.k_cache.cpu().numpy(), cache.k_scale.cpu().numpy(), table[b], ctx[b], g)
             s = np.repeat(cache.k_scale.cpu().numpy()[table[b], g], 16)[:ctx[b], None]
             assert np.all(np.abs(got - keys[b][:, g]) <= 2.0 ** -4 * np.abs(keys[b][:, g]) + 4 * s * 2.0 ** -10)
+
+
+def test_decode_of_very_many_sequences_after_smaller_calls():
+    """A batch of more (sequence, KV head) pairs than the workspace's counters, after calls of fewer over the same
+    workspace, whose scratch they have left in it: none of it is where the large batch counts."""
+    rng = np.random.default_rng(19)
+    big = Case([int(x) for x in rng.integers(0, 24, 9000)] + [60000], 4, 2, 64, seed=9)
+    exact = big.exact()
+    ws = f.block_decode_workspace(len(big.ctx), 4, big.cache())
+    for small in (Case([300, 6000], 4, 2, 64, seed=1), Case([9000] * 3, 16, 2, 256, seed=2), Case([700] * 90, 8, 2, 128, seed=3)):
+        _check(small.decode(workspace=ws), small.exact())
+        _check(big.decode(workspace=ws), exact)
