@@ -103,10 +103,15 @@ bool plan_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_bloc
 
 fkv_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FKV_OK : FKV_CUDA_ERROR; }
 
-// Bound of the tensor-core decode's pipeline waits set by fkv_set_decode_wait_limit_ns;
-// 0 = the default (kPipeWaitNs).
+// Bound of the pipeline waits of the tensor-core decode, and of the copies' waits of the block-scaled attention,
+// set by fkv_set_decode_wait_limit_ns; 0 = the default (kPipeWaitNs).
 std::atomic<unsigned long long> g_decode_wait_ns{0};
 constexpr unsigned long long kDefaultPipeWaitNs = 200000000ull;  // 200 ms, as kPipeWaitNs in tc.cuh
+
+unsigned long long pipe_wait_ns() {
+  const unsigned long long ns = g_decode_wait_ns.load(std::memory_order_relaxed);
+  return ns != 0 ? ns : kDefaultPipeWaitNs;
+}
 
 fkv_status cache_write(const void* k, const void* v, const int64_t* slot_mapping, int32_t n_tokens,
                        fkv_layer_cache cache, const float* k_scale, const float* v_scale, fkv_scale_gran gran,
@@ -272,8 +277,7 @@ fkv_status decode_entry(const void* k_new, const void* v_new, const void* q, int
   p.fault = fault;
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
   p.v_new = static_cast<const __nv_bfloat16*>(v_new);
-  const unsigned long long wait_ns = g_decode_wait_ns.load(std::memory_order_relaxed);
-  p.pipe_wait_ns = wait_ns != 0 ? wait_ns : kDefaultPipeWaitNs;
+  p.pipe_wait_ns = pipe_wait_ns();
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (fkv::decode_uses_tensor_cores(cache.head_dim, elt)) return from_cuda(fkv::launch_decode_tc(p, cache.head_dim, G, s));
   return from_cuda(fkv::launch_decode(p, cache.head_dim, elt, G, s));
@@ -599,6 +603,7 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
   p.o_part = reinterpret_cast<float*>(at + plan.cnt_bytes + plan.lse_bytes);
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
+  p.stage_wait_ns = pipe_wait_ns();
   // no more CTAs than there can be places (a unit's tiles and the blank one that leads them)
   const long long blocks = window > 0 ? std::min<long long>(max_blocks, (window + 15LL) / 16 + 1) : max_blocks;
   const int tpb = fkv::block_decode_tile_blocks(cache.head_dim);
@@ -647,6 +652,7 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   p.window = window;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.fault = fault;
+  p.stage_wait_ns = pipe_wait_ns();
   return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 

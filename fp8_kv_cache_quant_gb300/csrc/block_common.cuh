@@ -154,6 +154,7 @@ struct BlockPrefillParams {
   int causal, window;
   __nv_bfloat16* out;
   int32_t* fault;
+  uint64_t stage_wait_ns;                     // bound of the copies' wait for a free stage (the others': kPipeWaitNs)
   int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads
 };
 
@@ -174,6 +175,7 @@ struct BlockDecodeParams {
   float* o_part;                              // [N + B * Hkv][G][D]
   __nv_bfloat16* out;                         // [B][Hq][D]
   int32_t* fault;
+  uint64_t stage_wait_ns;                     // bound of the copies' wait for a free stage (the others': kPipeWaitNs)
 };
 
 // CTAs of the block-scaled decode that an SM holds, pool blocks of its tiles, and its launch on N CTAs.

@@ -703,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       }
       at.advance(p);
     }
+    tmem_ld_wait();  // no load left in flight on an early exit: the tensor memory is freed below
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
@@ -875,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       id_next = block_id(nx);
       const int st = u % C::NS, use = u / C::NS;
       if (u >= n0) {
-        if (!wait_warp(&k_empty[st], (use - 1) & 1)) {
+        if (!wait_warp(&k_empty[st], (use - 1) & 1, p.stage_wait_ns)) {
           if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
           *abort_s = 1;
           break;

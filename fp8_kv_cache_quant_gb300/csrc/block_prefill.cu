@@ -63,7 +63,7 @@ FKV_DEV float max_tree(const float* v) {
 
 // The waits take their timed path inline: the warpgroups run under different register budgets, which
 // one out-of-line function cannot serve.
-FKV_DEV bool pf_wait(uint64_t* bar, uint32_t parity) { return wait_ns<true>(bar, parity); }
+FKV_DEV bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kPipeWaitNs) { return wait_ns<true>(bar, parity, limit_ns); }
 FKV_DEV bool pf_wait_warp(uint64_t* bar, uint32_t parity) { return wait_warp<true>(bar, parity); }
 
 // An empty statement that "uses and redefines" 32 values: placed after the arithmetic on them,
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(512, 1)
         id_next = block_id(t + 2);
         const int st = t % C::NS, use = t / C::NS;
         bool ok = true;
-        if (lane == 0 && use > 0) ok = pf_wait(&empty[st], (use - 1) & 1);
+        if (lane == 0 && use > 0) ok = pf_wait(&empty[st], (use - 1) & 1, p.stage_wait_ns);
         if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
           if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
           *abort_s = 1;

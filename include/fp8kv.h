@@ -144,7 +144,8 @@ const char* fkv_status_string(fkv_status status);
 int32_t fkv_version(void);
 
 /*
- * fkv_set_decode_wait_limit_ns — test hook for the timeout path of the tensor-core decode.
+ * fkv_set_decode_wait_limit_ns — test hook for the timeout path of the tensor-core decode and
+ * of the block-scaled attention.
  *
  * Sets, for fp8_decode_attn / fp8_decode_step / fp8_decode_attn_noalloc launches on e4m3
  * layers made after the call (process-wide), the wall-clock bound of each in-kernel
@@ -153,7 +154,10 @@ int32_t fkv_version(void);
  * recovery that follows can be exercised without a stalled GPU: the CTA stops, lets
  * every copy and product it issued complete (those waits keep the 200 ms bound), frees
  * its tensor memory and returns; the output of such a launch is undefined (the split
- * merge reads whatever the workspace held).  Not for production use.
+ * merge reads whatever the workspace held).  For fp8_block_decode_attn and
+ * fp8_block_prefill_attn launches it bounds the wait of the copies for a stage that the
+ * products have read: they stop there, and the rest of such a CTA (one with more tiles than
+ * stages) runs into its own bounds of 200 ms.  Not for production use.
  */
 void fkv_set_decode_wait_limit_ns(unsigned long long ns);
 
