@@ -155,7 +155,8 @@ struct BlockPrefillParams {
   __nv_bfloat16* out;
   int32_t* fault;
   uint64_t stage_wait_ns;                     // bound of the copies' wait for a free stage (the others': kPipeWaitNs)
-  int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads
+  int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads;
+  int even_waves;                             // clusters are there to even out the last wave
 };
 
 cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaStream_t s);

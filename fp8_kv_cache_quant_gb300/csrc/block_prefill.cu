@@ -165,10 +165,14 @@ FKV_DEV float4 peer_ld4(uint32_t a) {
   return v;
 }
 
+// Whether a sequence's query tiles gain from sharing their key tiles in clusters of two where that evens out the last
+// wave: a chunk over a long context, whose CTAs are all alike.
+__host__ __device__ constexpr bool sharing_pays(long long keys, long long queries) { return keys >= 4 * queries && keys >= 8192; }
+
+// Query tile qt of sequence b and KV head blockIdx.y; SPLIT: a cluster's CTAs, `shares` of them at most, share its keys.
 template <int D, bool WIN, bool SPLIT>
-__global__ void __launch_bounds__(512, 1)
-    block_prefill_kernel(const __grid_constant__ BlockPrefillParams p, const __grid_constant__ CUtensorMap tmk,
-                         const __grid_constant__ CUtensorMap tmv) {
+FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, const CUtensorMap& tmv, int r0, int Lq, int T, int qt,
+                         int share, int shares) {
   using C = BlockPrefillCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem + C::OFF_Q;
@@ -204,27 +208,6 @@ __global__ void __launch_bounds__(512, 1)
   const int GC = p.part_heads, h_first = part * GC;
   const int tok = 128 / GC;                   // tokens per CTA
   const int b = blockIdx.z;
-  // longest (latest) query tiles first; SPLIT: a cluster per query tile
-  const int share = SPLIT ? static_cast<int>(cluster_rank()) : 0, shares = SPLIT ? static_cast<int>(cluster_size()) : 1;
-  const int qt = (static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x)) / shares;
-
-  // Launched with programmatic stream serialisation.  The tensor memory, all of an SM's, is allocated
-  // after this wait: taken before, it could be what a CTA of the kernel before still needs to go on.
-  griddep_wait();
-
-  // ------------------------------------------------------------ sequence geometry
-  const bool first_cta = qt == 0 && share == 0 && blockIdx.y == 0 && threadIdx.x == 0;
-  const int r0 = p.cu[b];
-  const int Lq = p.cu[b + 1] - r0;
-  int T = p.ctx[b];
-  if (T < 0 || T > static_cast<long long>(p.max_blocks) * 16) {
-    if (first_cta) raise_fault(p.fault, FKV_FAULT_CONTEXT);
-    T = T < 0 ? 0 : p.max_blocks * 16;
-  }
-  if (Lq < 0 || Lq > p.max_q_len || (p.causal && Lq > T) || r0 < 0 || r0 + static_cast<long long>(Lq) > p.total_q) {
-    if (first_cta) raise_fault(p.fault, FKV_FAULT_QLEN);
-    return;
-  }
   const int q0 = qt * tok;  // first token of the CTA
   if (q0 >= Lq) return;
   const int toks = min(tok, Lq - q0);
@@ -233,6 +216,18 @@ __global__ void __launch_bounds__(512, 1)
   const int kv_lo = WIN ? max(0, pos0 - p.window + 1) : 0;
   // tiles u = 0 .. n_t-1 are tb + u; SPLIT: this CTA's share of them
   const int tb0 = kv_lo / C::BN, n_all = (kv_end + C::BN - 1) / C::BN - tb0;
+  if constexpr (SPLIT) {
+    // two tiles at least for each that shares; the others of the cluster have no part
+    if (!p.even_waves) shares = max(1, min(shares, n_all / 2));
+    if (share >= shares) {
+      griddep_launch_dependents();
+      if (shares > 1) {
+        cluster_sync();
+        cluster_sync();
+      }
+      return;
+    }
+  }
   const int tb = tb0 + share * n_all / shares;
   const int n_t = tb0 + (share + 1) * n_all / shares - tb;
   const int nblk_seq = (T + 15) >> 4;
@@ -527,7 +522,7 @@ __global__ void __launch_bounds__(512, 1)
       float4* part = reinterpret_cast<float4*>(sK);
       auto store32 = [&](int c, const float* x) {
         if (!row_ok) return;
-        if constexpr (SPLIT) {
+        if (SPLIT && shares > 1) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             part[(8 * c + j) * C::BM + i] =
@@ -739,7 +734,7 @@ __global__ void __launch_bounds__(512, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
-  if constexpr (SPLIT) {
+  if (SPLIT && shares > 1) {
     // the shares (o, lse)_r of every row: M = max lse_r, out = sum 2^(lse_r - M) o_r / sum 2^(lse_r - M), by the
     // softmax warps, whose register budget holds it
     cluster_sync();
@@ -768,6 +763,45 @@ __global__ void __launch_bounds__(512, 1)
       dst[1] = __floats2bfloat162_rn(o.z * f, o.w * f);
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
+  }
+}
+
+template <int D, bool WIN, bool SPLIT>
+__global__ void __launch_bounds__(512, 1)
+    block_prefill_kernel(const __grid_constant__ BlockPrefillParams p, const __grid_constant__ CUtensorMap tmk,
+                         const __grid_constant__ CUtensorMap tmv) {
+  const int b = blockIdx.z;
+  // Launched with programmatic stream serialisation.  The tensor memory, all of an SM's, is allocated
+  // after this wait: taken before, it could be what a CTA of the kernel before still needs to go on.
+  griddep_wait();
+
+  // ------------------------------------------------------------ sequence geometry
+  const bool first_cta = blockIdx.x == gridDim.x - 1 && blockIdx.y == 0 && threadIdx.x == 0;
+  const int r0 = p.cu[b];
+  const int Lq = p.cu[b + 1] - r0;
+  int T = p.ctx[b];
+  if (T < 0 || T > static_cast<long long>(p.max_blocks) * 16) {
+    if (first_cta) raise_fault(p.fault, FKV_FAULT_CONTEXT);
+    T = T < 0 ? 0 : p.max_blocks * 16;
+  }
+  if (Lq < 0 || Lq > p.max_q_len || (p.causal && Lq > T) || r0 < 0 || r0 + static_cast<long long>(Lq) > p.total_q) {
+    if (first_cta) raise_fault(p.fault, FKV_FAULT_QLEN);
+    return;
+  }
+  // longest (latest) query tiles first
+  const int at = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
+  if constexpr (!SPLIT) {
+    attend_tile<D, WIN, false>(p, tmk, tmv, r0, Lq, T, at, 0, 1);
+  } else {
+    // a cluster per query tile, or, where clusters are there for the last wave's sake, a CTA per query tile for the
+    // sequences that do not gain from sharing
+    const int size = static_cast<int>(cluster_size());
+    if (D > 128 || !p.even_waves || sharing_pays(WIN ? min(static_cast<long long>(T), p.window + 256LL) : T, Lq)) {
+      attend_tile<D, WIN, true>(p, tmk, tmv, r0, Lq, T, at / size, static_cast<int>(cluster_rank()), size);
+    } else {
+      const int qt = at - static_cast<int>(gridDim.x) + static_cast<int>(gridDim.x) / size;
+      if (qt >= 0) attend_tile<D, WIN, false>(p, tmk, tmv, r0, Lq, T, qt, 0, 1);
+    }
   }
 }
 
@@ -835,26 +869,27 @@ int clusters_at_once(int shares) {
 }
 
 template <int D, bool WIN>
-cudaError_t launch_w(const BlockPrefillParams& p, dim3 grid, int num_sms, cudaStream_t s) {
-  const long long ctas = static_cast<long long>(grid.x) * grid.y * grid.z;
+cudaError_t launch_w(BlockPrefillParams p, dim3 grid, long long ctas, int num_sms, cudaStream_t s) {
+  // the table's width bounds the contexts from above; the kernel knows them, and shares no more than they are worth
   const long long keys = WIN ? std::min<long long>(p.max_blocks * 16LL, static_cast<long long>(p.window) + 256) : p.max_blocks * 16LL;
   // CTAs that would leave SMs idle share their key tiles, two at least each, in clusters as large as can
   // all be there at once
   int shares = static_cast<int>(std::max<long long>(1, std::min<long long>(std::min<long long>(8, num_sms / ctas), keys / 256)));
   while (shares > 1 && ctas > clusters_at_once<D, WIN>(shares)) --shares;
-  // Clusters of two also even out the last wave of a chunk over a long context, whose CTAs are all alike,
-  // where that saves more than the 8 % that sharing costs: 1,500 queries over 32,768 keys (32/8 heads,
-  // head_dim 128: 375 CTAs) 818 us against 895, 2,048 1,127 against 1,174; not 1,024 (654 against 607).
+  // Clusters of two also even out the last wave of a chunk over a long context, where that saves more than
+  // sharing costs: over 32,768 keys (32/8 heads, head_dim 128) 1,500 queries take 822 us against 956, 2,048
+  // 1,133 against 1,255; not 1,024 (657 against 648) or 3,000 (1,602 against 1,569).
   const long long waves = (ctas + num_sms - 1) / num_sms, half_waves = (2 * ctas + num_sms - 1) / num_sms;
-  if (D <= 128 && waves > 1 && keys >= 4LL * p.max_q_len && keys >= 128LL * 64 && half_waves * 108 < waves * 200) shares = 2;
+  p.even_waves = D <= 128 && waves > 1 && sharing_pays(keys, p.max_q_len) && half_waves * 108 < waves * 200;
+  if (p.even_waves) shares = 2;
   if (shares == 1) return launch_t<D, WIN, false>(p, grid, 1, s);
   grid.x *= shares;
   return launch_t<D, WIN, true>(p, grid, shares, s);
 }
 
 template <int D>
-cudaError_t launch_d(const BlockPrefillParams& p, dim3 grid, int num_sms, cudaStream_t s) {
-  return p.window > 0 ? launch_w<D, true>(p, grid, num_sms, s) : launch_w<D, false>(p, grid, num_sms, s);
+cudaError_t launch_d(const BlockPrefillParams& p, dim3 grid, long long ctas, int num_sms, cudaStream_t s) {
+  return p.window > 0 ? launch_w<D, true>(p, grid, ctas, num_sms, s) : launch_w<D, false>(p, grid, ctas, num_sms, s);
 }
 
 }  // namespace
@@ -868,9 +903,11 @@ cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaS
   const long long y = static_cast<long long>(p.Hkv) * p.head_parts;
   if (y > 65535) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((p.max_q_len - 1LL) / tok + 1), static_cast<unsigned>(y), p.B);
-  if (D == 64) return launch_d<64>(p, grid, num_sms, s);
-  if (D == 128) return launch_d<128>(p, grid, num_sms, s);
-  return launch_d<256>(p, grid, num_sms, s);
+  // CTAs that have rows, at most: of a ragged batch, far fewer than the grid's
+  const long long ctas = std::min<long long>(static_cast<long long>(grid.x) * p.B, static_cast<long long>(p.total_q) / tok + p.B) * y;
+  if (D == 64) return launch_d<64>(p, grid, ctas, num_sms, s);
+  if (D == 128) return launch_d<128>(p, grid, ctas, num_sms, s);
+  return launch_d<256>(p, grid, ctas, num_sms, s);
 }
 
 }  // namespace fkv

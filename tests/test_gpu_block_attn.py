@@ -638,3 +638,18 @@ def test_decode_of_very_many_sequences_after_smaller_calls():
     for small in (Case([300, 6000], 4, 2, 64, seed=1), Case([9000] * 3, 16, 2, 256, seed=2), Case([700] * 90, 8, 2, 128, seed=3)):
         _check(small.decode(workspace=ws), small.exact())
         _check(big.decode(workspace=ws), exact)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("ctx,new,hq,h,kw", [
+    ([200, 190, 180], [4, 3, 4], 8, 2, {}), ([300, 2000, 16], [2, 9, 1], 8, 2, {}), ([2000, 300], [5, 1], 4, 1, dict(window=150)),
+    ([700, 8300, 0, 3], [700, 40, 0, 3], 32, 4, {}), ([833], [833], 32, 4, {}), ([9000, 700], [300, 700], 32, 4, dict(window=8500)),
+    ([500, 9000], [400, 300], 32, 4, dict(causal=False)), ([2048] + [500] * 20, [600] + [1] * 20, 8, 2, {}),
+])
+def test_prefill_with_tables_wider_than_the_contexts(d, ctx, new, hq, h, kw):
+    """Tables as wide as a model's longest context: the plan, made from that width, must serve short contexts too
+    (query tiles that share their keys in clusters, some sequences of a batch and others not)."""
+    c = Case(ctx, hq, h, d, new=new, seed=d + len(ctx))
+    c.table = np.concatenate((c.table, np.full((len(ctx), 8192 - c.table.shape[1]), -1, np.int32)), 1)
+    exact = c.exact(**kw)
+    _check(c.prefill(**kw), exact)
