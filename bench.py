@@ -72,13 +72,13 @@ def _local_includes(csrc: str, name: str, seen=None) -> set:
 
 def kernel_source_sha(kernel_file: str) -> str:
     """First 16 hex digits of the sha256 of the code (comments removed) of a kernel's .cu
-    file followed by those of the shared headers common.cuh, tc.cuh, decode_common.cuh and
-    kernels.h (in that order) that it includes: a profile summary stays valid only while
+    file followed by those of the shared headers common.cuh, tc.cuh, decode_common.cuh,
+    kernels.h and prefill_common.cuh (in that order) that it includes: a profile summary stays valid only while
     none of them has changed."""
     csrc = os.path.join(ROOT, "fp8_kv_cache_quant_gb300", "csrc")
     used = _local_includes(csrc, kernel_file)
     h = hashlib.sha256()
-    for name in (kernel_file, "common.cuh", "tc.cuh", "decode_common.cuh", "kernels.h"):
+    for name in (kernel_file, "common.cuh", "tc.cuh", "decode_common.cuh", "kernels.h", "prefill_common.cuh"):
         if name in used:
             h.update(_code_only(open(os.path.join(csrc, name), encoding="utf-8").read()).encode())
     return h.hexdigest()[:16]

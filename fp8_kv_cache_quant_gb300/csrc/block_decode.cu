@@ -252,14 +252,6 @@ FKV_DEV float warp_max_f(float v) {
   return r;
 }
 
-// Four values as e4m3 terms: hi keeps the leading 3 fraction bits, lo the rest.
-FKV_DEV void split4(float a, float b, float c, float d, uint32_t& hi, uint32_t& lo) {
-  auto lead = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); };
-  const float ha = lead(a), hb = lead(b), hc = lead(c), hd = lead(d);
-  hi = f32x4_to_e4m3x4(make_float2(ha, hb), make_float2(hc, hd));
-  lo = f32x4_to_e4m3x4(make_float2(a - ha, b - hb), make_float2(c - hc, d - hd));
-}
-
 // The merge of a unit's pieces, rows row0 .. row0 + ns - 1 of the workspace, by the whole CTA:
 // o = sum_s 2^(lse_s - M) o_s / sum_s 2^(lse_s - M) in FP32.  First the heads' weights (a warp per head)
 // into shared memory; then groups of threads, one thread per four outputs, take a share of the
@@ -660,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
 #pragma unroll
           for (int hh = 0; hh < C::NHALF; ++hh) {
             uint32_t hi, lo;
-            split4(pv[hh][0], pv[hh][1], pv[hh][2], pv[hh][3], hi, lo);
+            split4<false>(make_float2(pv[hh][0], pv[hh][1]), make_float2(pv[hh][2], pv[hh][3]), hi, lo);
             whi[hh][h4 / 4] = hi;
             wlo[hh][h4 / 4] = lo;
           }

@@ -36,42 +36,11 @@
 #include <atomic>
 
 #include "block_common.cuh"
+#include "prefill_common.cuh"
 #include "tc.cuh"
 
 namespace fkv {
 namespace {
-
-FKV_DEV float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// Maximum of N values as a tree of three-input maxima (depth log3 N, rather than a chain
-// of N / 2 dependent operations).
-template <int N>
-FKV_DEV float max_tree(const float* v) {
-  if constexpr (N == 1) {
-    return v[0];
-  } else if constexpr (N == 2) {
-    return fmaxf(v[0], v[1]);
-  } else {
-    constexpr int A = (N + 2) / 3, B = (N - A + 1) / 2;
-    return fmax3(max_tree<A>(v), max_tree<B>(v + A), max_tree<N - A - B>(v + A + B));
-  }
-}
-
-// The waits take their timed path inline: the warpgroups run under different register budgets, which
-// one out-of-line function cannot serve.
-FKV_DEV bool pf_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kPipeWaitNs) { return wait_ns<true>(bar, parity, limit_ns); }
-FKV_DEV bool pf_wait_warp(uint64_t* bar, uint32_t parity) { return wait_warp<true>(bar, parity); }
-
-// An empty statement that "uses and redefines" 32 values: placed after the arithmetic on them,
-// it keeps the compiler from moving that arithmetic below the next TMEM load (which would
-// keep every chunk's loaded values live at once).
-FKV_DEV void pin32(float* v) {
-  asm volatile("" : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31]));
-}
 
 constexpr float kHuge = 3e38f;  // minus this: the maximum of no scores
 
@@ -123,16 +92,6 @@ struct BlockPrefillCfg {
   static_assert(SMEM <= 227 * 1024, "shared memory budget");
   static_assert(TM_OH + D - DN <= 512, "TMEM budget");
 };
-
-// e4m3 codes of the two terms of four values: `hi` the leading 3 fraction bits, `lo` the rest.
-FKV_DEV void split4(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
-  auto lead = [](float x) { return __uint_as_float(__float_as_uint(x) & 0xFFF00000u); };
-  const float2 ha = make_float2(lead(a.x), lead(a.y)), hb = make_float2(lead(b.x), lead(b.y));
-  const float2 neg = make_float2(-1.f, -1.f);
-  const float2 la = __ffma2_rn(ha, neg, a), lb = __ffma2_rn(hb, neg, b);
-  hi = f32x4_to_e4m3x4(ha, hb);
-  lo = f32x4_to_e4m3x4(la, lb);
-}
 
 FKV_DEV uint32_t cluster_rank() {
   uint32_t r;
@@ -403,7 +362,7 @@ FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, co
           float2 x1 = __ffma2_rn(make_float2(v[16 * k + 4 * j + 2], v[16 * k + 4 * j + 3]), c2, n2);
           x0.x = ex2(x0.x); x0.y = ex2(x0.y); x1.x = ex2(x1.x); x1.y = ex2(x1.y);
           sum = __fadd2_rn(sum, __fadd2_rn(x0, x1));
-          split4(x0, x1, hi[j], lw[j]);
+          split4<true>(x0, x1, hi[j], lw[j]);
         }
         l = fmaf(sum.x + sum.y, fabsf(iv[k]), l);
         uint8_t* dst = P + swz(static_cast<uint32_t>(i * 128 + c0 + 16 * k), 128);
