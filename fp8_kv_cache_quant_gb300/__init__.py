@@ -376,16 +376,21 @@ class BlockCache:
 
 
 def load_binding():
-    """The compiled part of this binding (_binding.so): the checks and calls of the functions below, whose
-    small calls are bound by the host."""
+    """The compiled part of this binding (built for this Python and this torch): the checks and calls of the functions
+    below, whose small calls are bound by the host."""
     global _compiled
     if _compiled is None:
+        import importlib.util
+
+        from .build import binding_path
         load_library()
-        try:
-            from . import _binding
-        except ImportError as e:
-            raise RuntimeError(f"_binding.so not built ({e}); run __graft_entry__.build()") from e
-        _compiled = _binding
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} not built; run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location(__name__ + "._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _compiled = module
     return _compiled
 
 

@@ -1,5 +1,6 @@
 """Build libfp8kv.so in-tree with nvcc for sm_103a (no cmake, one -gencode), and the binding's
-compiled part, _binding.so, with the host compiler against torch's headers.
+compiled part, binding_path(), with the host compiler against Python's and torch's headers.  The
+library needs neither of them: it is in place before the binding is built, and by itself with --library.
 
 Each CUDA translation unit is compiled in parallel, then linked into
 ``fp8_kv_cache_quant_gb300/libfp8kv.so``.  The CUDA runtime is linked statically;
@@ -18,7 +19,6 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libfp8kv.so")
-BINDING = os.path.join(PKG, "_binding.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -35,12 +35,20 @@ def _nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _stale(srcs, out) -> bool:
+def _stale(out, sources) -> bool:
     if not os.path.exists(out):
         return True
     t = os.path.getmtime(out)
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "fp8kv.h"), __file__]
+    deps = [os.path.join(CSRC, f) for f in sources] + [os.path.join(ROOT, "include", "fp8kv.h"), __file__]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def binding_path() -> str:
+    """The compiled binding of this Python and this torch, whose C++ interfaces it is built against."""
+    import sysconfig
+
+    import torch
+    return os.path.join(PKG, f"_binding-torch-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _compile_binding(obj: str):
@@ -61,21 +69,22 @@ def _link_binding(obj: str):
     """Against libfp8kv.so beside it and torch's libraries (those that torch has loaded already)."""
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING + ".tmp"
+    out = binding_path()
+    tmp = out + ".tmp"
     cmd = [os.environ.get("CXX") or "g++", "-shared", "-o", tmp, obj, "-L" + PKG, "-l:libfp8kv.so", "-L" + lib, "-lc10",
            "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"linking _binding.so failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+        raise RuntimeError(f"linking the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
 
 
-def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
+def build(verbose: bool = False, force: bool = False, extra_flags=(), library_only: bool = False) -> str:
     srcs = [s for s in SOURCES if os.path.exists(os.path.join(CSRC, s))]
-    if not force and not _stale(srcs, OUT) and not _stale(srcs, BINDING):
-        return OUT
+    library = force or _stale(OUT, [f for f in os.listdir(CSRC) if f != "binding.cpp"])
+    binding = not library_only and (force or _stale(binding_path(), ["binding.cpp"]))
     os.makedirs(BUILD_DIR, exist_ok=True)
-    nvcc = _nvcc()
+    nvcc = _nvcc() if library else None
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, src.replace(".cu", ".o"))
@@ -89,20 +98,25 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
 
     binding_obj = os.path.join(BUILD_DIR, "binding.o")
     with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        binding = ex.submit(_compile_binding, binding_obj)
-        objs = list(ex.map(compile_one, srcs))
-        binding.result()
-    tmp = OUT + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, OUT)
-    _link_binding(binding_obj)
+        compiled = ex.submit(_compile_binding, binding_obj) if binding else None
+        if library:
+            objs = list(ex.map(compile_one, srcs))
+            tmp = OUT + ".tmp"
+            cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(tmp, OUT)
+        if binding:
+            try:
+                compiled.result()
+                _link_binding(binding_obj)
+            except RuntimeError as e:
+                raise RuntimeError(f"{OUT} is built, the compiled binding is not: {e}") from e
     return OUT
 
 
 if __name__ == "__main__":
     v = "-v" in sys.argv
     extra = ["-Xptxas", "-v"] if "--ptxas" in sys.argv else []
-    print(build(verbose=v or bool(extra), force=True, extra_flags=extra))
+    print(build(verbose=v or bool(extra), force=True, extra_flags=extra, library_only="--library" in sys.argv))
