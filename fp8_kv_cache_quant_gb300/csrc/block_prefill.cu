@@ -125,8 +125,9 @@ FKV_DEV float4 peer_ld4(uint32_t a) {
 }
 
 // Whether a sequence's query tiles gain from sharing their key tiles in clusters of two where that evens out the last
-// wave: a chunk over a long context, whose CTAs are all alike.
-__host__ __device__ constexpr bool sharing_pays(long long keys, long long queries) { return keys >= 4 * queries && keys >= 8192; }
+// wave: a chunk over a context long enough for its CTAs to be alike (2,048 queries, 32/8 heads, head_dim 128, us shared and
+// not: over 8,192 keys 334 and 307, over 12,288 467 and 463, over 16,384 600 and 622).
+__host__ __device__ constexpr bool sharing_pays(long long keys, long long queries) { return keys >= 6 * queries && keys >= 8192; }
 
 // Query tile qt of sequence b and KV head blockIdx.y; SPLIT: a cluster's CTAs, `shares` of them at most, share its keys.
 template <int D, bool WIN, bool SPLIT>
