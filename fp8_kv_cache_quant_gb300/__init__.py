@@ -458,7 +458,7 @@ def block_decode_workspace(batch, num_q_heads, cache: BlockCache, stream=None):
 def fp8_block_decode_attn(q, cache: BlockCache, block_table, context_lens, softmax_scale=0.0, window=0, out=None,
                           workspace=None, fault=None, stream=None):
     """One decode step over a block-scaled cache: q bf16 [batch][Hq][D] (not rounded further), out bf16.
-    ``workspace``: of block_decode_workspace (one is made for the call when None)."""
+    ``workspace``: of block_decode_workspace (when None, one is made and cleared for the call: a loop keeps its own)."""
     if workspace is None:
         workspace = block_decode_workspace(q.shape[0], q.shape[1], cache, stream)
     return _call("fp8_block_decode_attn", q, stream, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,

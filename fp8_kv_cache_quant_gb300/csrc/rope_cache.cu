@@ -196,7 +196,8 @@ FKV_DEV float pow2_scale(uint32_t amax_bits) {
 // grid (pages of a sequence's new tokens, sequences, kv_parts + slices of the query rows).
 // CTAs z < kv_parts: K and V of one block, two (head_dim 256: four) warps per (KV head, K or V), which
 // share its 16 rows: the rows stay in registers between the maximum and the codes, so that each
-// input byte is read once, and several warps keep them few enough for four CTAs per SM.  The others turn
+// input byte is read once, and several warps keep them few enough for four CTAs per SM (at head_dim 64 and 128 with
+// 44 bytes of spills; head_dim 256 has three).  The others turn
 // query rows, four units per thread with all loads up front.  HBM-bound: 4 x 16,384 tokens of 32/8
 // heads at head_dim 128 take 273 us, 5.5 TB/s (three CTAs per SM 289 us; six units per thread 323 us).
 template <int D>
