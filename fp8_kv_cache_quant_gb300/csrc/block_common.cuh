@@ -172,7 +172,7 @@ struct BlockPrefillParams {
   __nv_bfloat16* out;
   int32_t* fault;
   uint64_t stage_wait_ns;                     // bound of the copies' wait for a free stage (the others': kPipeWaitNs)
-  int head_parts, part_heads;                 // set by the launch: a group in parts of part_heads heads;
+  int head_parts, part_heads, part_tokens;    // set by the launch: a group in parts of part_heads heads, a CTA's tokens;
   int even_waves;                             // clusters are there to even out the last wave
 };
 

@@ -166,10 +166,9 @@ FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, co
   // more than 128 heads
   const int g = blockIdx.y / p.head_parts, part = blockIdx.y - g * p.head_parts;
   const int GC = p.part_heads, h_first = part * GC;
-  const int tok = 128 / GC;                   // tokens per CTA
+  const int tok = p.part_tokens;              // tokens per CTA
   const int b = blockIdx.z;
   const int q0 = qt * tok;  // first token of the CTA
-  if (q0 >= Lq) return;
   const int toks = min(tok, Lq - q0);
   const int pos0 = T - Lq + q0;  // absolute position of the first token (may be negative when not causal)
   const int kv_end = p.causal ? min(T, pos0 + toks) : T;  // keys [kv_lo, kv_end) matter
@@ -751,16 +750,17 @@ __global__ void __launch_bounds__(512, 1)
   // longest (latest) query tiles first
   const int at = static_cast<int>(gridDim.x) - 1 - static_cast<int>(blockIdx.x);
   if constexpr (!SPLIT) {
-    attend_tile<D, WIN, false>(p, tmk, tmv, r0, Lq, T, at, 0, 1);
+    if (at * p.part_tokens < Lq) attend_tile<D, WIN, false>(p, tmk, tmv, r0, Lq, T, at, 0, 1);
   } else {
     // a cluster per query tile, or, where clusters are there for the last wave's sake, a CTA per query tile for the
     // sequences that do not gain from sharing
     const int size = static_cast<int>(cluster_size());
     if (D > 128 || !p.even_waves || sharing_pays(WIN ? min(static_cast<long long>(T), p.window + 256LL) : T, Lq)) {
-      attend_tile<D, WIN, true>(p, tmk, tmv, r0, Lq, T, at / size, static_cast<int>(cluster_rank()), size);
+      const int qt = at / size;
+      if (qt * p.part_tokens < Lq) attend_tile<D, WIN, true>(p, tmk, tmv, r0, Lq, T, qt, static_cast<int>(cluster_rank()), size);
     } else {
       const int qt = at - static_cast<int>(gridDim.x) + static_cast<int>(gridDim.x) / size;
-      if (qt >= 0) attend_tile<D, WIN, false>(p, tmk, tmv, r0, Lq, T, qt, 0, 1);
+      if (qt >= 0 && qt * p.part_tokens < Lq) attend_tile<D, WIN, false>(p, tmk, tmv, r0, Lq, T, qt, 0, 1);
     }
   }
 }
@@ -859,7 +859,8 @@ cudaError_t launch_block_prefill(BlockPrefillParams p, int D, int num_sms, cudaS
   const int G = p.Hq / p.Hkv;
   p.head_parts = (G + 127) / 128;
   p.part_heads = (G + p.head_parts - 1) / p.head_parts;
-  const int tok = 128 / p.part_heads;
+  p.part_tokens = 128 / p.part_heads;
+  const int tok = p.part_tokens;
   const long long y = static_cast<long long>(p.Hkv) * p.head_parts;
   if (y > 65535) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>((p.max_q_len - 1LL) / tok + 1), static_cast<unsigned>(y), p.B);
