@@ -70,8 +70,6 @@ FKV_DEV void split4(float2 a, float2 b, uint32_t& hi, uint32_t& lo) {
 // 2^n of a whole number -126 <= n <= 127.
 FKV_DEV float pow2i(float n) { return __uint_as_float(static_cast<uint32_t>(static_cast<int>(n) + 127) << 23); }
 
-constexpr float kFloatMax = 3.402823466e+38f;
-
 // V scales in the exponent.  P_j = 2^(x_j + L_j - R) carries its block's scale vs = 2^L; the softmax's sum takes
 // it out again, l = sum P_j 2^(o - L_j).  A scale 2^100 and more below the largest of its tile, zero among them,
 // counts as zero: its keys enter l as if it were 2^-100 of the largest, so that their P stays a normal
@@ -84,10 +82,10 @@ struct ScaleRange {
 };
 struct BlockScale {
   float lv, iv;  // L and 2^(o - L), the latter negative where the scale counts as zero
-  // 0 as a rule.  Where o changed, a scale counts as zero or the scales so far lie so far apart that 2^-|r - R_t| may
-  // underflow though the keys' weights are alike: 2^(new o - old o), by which l so far is multiplied
-  // (up to the largest float) before it is joined by join_sums
-  float rare;
+  // Not as a rule: o changed, a scale counts as zero, or the scales so far lie so far apart that 2^-|r - R_t| may
+  // underflow though the keys' weights are alike: the sums are joined by join_sums.
+  bool rare;
+  float change;  // new o - old o
 };
 
 // A tile's scales, a block per lane (`in`: the lane has one that a query sees).  Every lane of the warp takes part.
@@ -104,8 +102,8 @@ FKV_DEV BlockScale block_scales(ScaleRange& range, float vs, bool in) {
   const float o = fmaxf(fmaxf(fminf(range.o, floorf(least) + 80.f), ceilf(range.top) - 118.f), -120.f);
   zero = zero || (some && L < o - 80.f);
   BlockScale r;
-  const bool rare = __any_sync(0xffffffffu, zero) || o != range.o || range.top - range.low > 100.f;
-  r.rare = rare ? pow2i(o - range.o) : 0.f;
+  r.rare = __any_sync(0xffffffffu, zero) || o != range.o || range.top - range.low > 100.f;
+  r.change = o - range.o;
   range.o = o;
   r.lv = zero ? fmaxf(bottom, o - 80.f) : L;
   r.iv = in ? ex2_subnormal(o - r.lv) : 1.f;
@@ -113,10 +111,24 @@ FKV_DEV BlockScale block_scales(ScaleRange& range, float vs, bool in) {
   return r;
 }
 
-// l 2^(r - r') + lt 2^(R - r') with r' = max(r, R) and d = r - R, the factor in two halves.
-FKV_DEV float join_sums(float l, float lt, float d) {
-  const float h = ex2(-0.5f * fabsf(d));
-  return d > 0.f ? fmaf(lt * h, h, l) : fmaf(l * h, h, lt);
+// A row's state (r, l) joined by a rare tile's (R, lt), and the factors of acc and O_t.  Where o went down by n, l goes
+// with it; where it went up, r does instead, and l, whose keys may be worth 2^-198 of the new ones, stays
+// what it is (acc loses what is worth nothing beside them).  2^-|r - R| enters l in three equal factors: scales at the
+// two ends of float32 make it 2^-254 and less where the keys' weights are alike.
+struct RareFactors {
+  float l, lt;          // l and lt are to be multiplied by these three times
+  float alpha, beta;    // of acc and O_t
+};
+FKV_DEV RareFactors rare_factors(float& r, float& l, float R, float change) {
+  const float up = r + fmaxf(change, 0.f), next = fmaxf(up, R);
+  l *= ex2(fminf(change, 0.f));
+  RareFactors f;
+  f.l = ex2(0.33333334f * (up - next));
+  f.lt = ex2(0.33333334f * (R - next));
+  f.alpha = ex2(r - next);
+  f.beta = ex2(R - next);
+  r = next;
+  return f;
 }
 
 struct RopeCacheParams {

@@ -80,7 +80,7 @@ struct BlockDecodeCfg {
   // scales of a tile, ring of slots: the K copies run at most NS + 2 tiles ahead of the softmax's
   // release of an S buffer, which follows its reading of the scales
   static constexpr int SCN = NS + 2;
-  static constexpr int SCF = 3 * TPB + 4;         // ks [TPB], L [TPB], 2^(o - L) [TPB], o, BlockScale's rare
+  static constexpr int SCF = 3 * TPB + 4;         // ks [TPB], L [TPB], 2^(o - L) [TPB], o, BlockScale's rare and change
   // shared memory (bytes)
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_P = OFF_Q + NSUB * QSUB;
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         const int key = at.block0() * 16 + 128 * hh + i;
         valid[hh] = key >= at.s.lo && key < at.s.T;
       }
-      const float o = slot[3 * TPB], rare = slot[3 * TPB + 1];
+      const float o = slot[3 * TPB], rare = slot[3 * TPB + 1], change = slot[3 * TPB + 2];
 #pragma unroll
       for (int hh = 0; hh < C::NHALF; ++hh) {
         tmem_ld_wait();
@@ -630,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
             }
             const int h = h4 + j;
             // one of the two factors is 1, the other 2^-|m - tmax|
-            const float dm = m[h] - tm[j], e = ex2(-fabsf(dm));
+            const float e = ex2(-fabsf(m[h] - tm[j]));
             const float alpha = m[h] > tm[j] ? 1.f : e, corr = m[h] > tm[j] ? e : 1.f;
             float psum = 0.f;
 #pragma unroll
@@ -639,10 +639,17 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
               psum = fmaf(w, fabsf(iv[hh]), psum);
               pv[hh][j] = w * pmax[hh];
             }
-            lsum[h] = decltype(rarely)::value ? join_sums(fminf(lsum[h] * rare, kFloatMax), psum, dm) : fmaf(lsum[h], alpha, psum * corr);
-            m[h] = fmaxf(m[h], tm[j]);
-            al[j] = alpha;
-            be[j] = corr;
+            if constexpr (decltype(rarely)::value) {
+              const RareFactors f = rare_factors(m[h], lsum[h], tm[j], change);
+              lsum[h] = lsum[h] * f.l * f.l * f.l + psum * f.lt * f.lt * f.lt;
+              al[j] = f.alpha;
+              be[j] = f.beta;
+            } else {
+              lsum[h] = fmaf(lsum[h], alpha, psum * corr);
+              m[h] = fmaxf(m[h], tm[j]);
+              al[j] = alpha;
+              be[j] = corr;
+            }
           }
           if (i == 0) {
             *reinterpret_cast<float4*>(f_s + pb * 2 * LO + h4) = make_float4(al[0], al[1], al[2], al[3]);
@@ -886,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       }
       if (lane == 0) {
         slot[3 * TPB] = range.o;
-        slot[3 * TPB + 1] = sc.rare;
+        slot[3 * TPB + 1] = sc.rare ? 1.f : 0.f;
+        slot[3 * TPB + 2] = sc.change;
       }
       mbar_arrive_warp(&sc_full[u % C::SCN]);
     }

@@ -67,7 +67,7 @@ struct BlockPrefillCfg {
   // scales of a tile in a ring of slots: the K copies run at most SBUF + NS tiles ahead of the
   // softmax (a stage is refilled once its S was computed, an S buffer once it was read)
   static constexpr int SCN = D <= 128 ? 8 : 4;
-  static constexpr int SCF = 32;                    // floats per slot: ks [8], L [8], 2^(o - L) [8], o, BlockScale's rare
+  static constexpr int SCF = 32;                    // floats per slot: ks [8], L [8], 2^(o - L) [8], o, BlockScale's rare, change
   static_assert(SCN > SBUF + NS, "a slot is rewritten only after the softmax is done with it");
   // registers per thread of the warpgroups (launch: 128 each): softmax, correction, copies and MMA (head_dim 64
   // spills at 120: 485 against 481 us for 2,048 queries over 8,192 keys, 64/8 heads)
@@ -333,20 +333,21 @@ FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, co
       tmax = fmaxf(tmax, __shfl_xor_sync(0xffffffffu, tmax, 16));
       // one of the two factors is 1, the other 2^-|m - tmax|
       const float e = ex2(-fabsf(m - tmax));
-      const float alpha = m > tmax ? 1.f : e, corr = m > tmax ? e : 1.f;
-      // the sum's own factors: in a rare tile (block_scales; the same in every thread) in two halves, 2^-|r - R_t|
-      // itself may underflow
+      float alpha = m > tmax ? 1.f : e, corr = m > tmax ? e : 1.f;
+      // the sum's factors: the same, but in a rare tile (block_scales; the same in every thread)
       if (rare == 0.f) {
         l *= alpha;
 #pragma unroll
         for (int k = 0; k < 4; ++k) iv[k] *= corr;
+        m = fmaxf(m, tmax);
       } else {
-        const float half = ex2(-0.5f * fabsf(m - tmax)), la = m > tmax ? 1.f : half, lc = m > tmax ? half : 1.f;
-        l = fminf(l * rare, kFloatMax) * la * la;
+        const RareFactors f = rare_factors(m, l, tmax, sSc[(t % C::SCN) * C::SCF + 26]);
+        l = l * f.l * f.l * f.l;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) iv[k] = iv[k] * lc * lc;
+        for (int k = 0; k < 4; ++k) iv[k] = iv[k] * f.lt * f.lt * f.lt;
+        alpha = f.alpha;
+        corr = f.beta;
       }
-      m = fmaxf(m, tmax);
       if (!__all_sync(0xffffffffu, p_ready) && !pf_wait_warp(&p_free[pb], ((t / C::PBUF) - 1) & 1)) { ok = false; break; }
       uint8_t* P = sP + pb * 2 * C::PTERM;
       const float top = tmax - kLog2E4m3Max;
@@ -587,7 +588,8 @@ FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, co
           }
           if (lane == 0) {
             slot[24] = range.o;
-            slot[25] = sc.rare;
+            slot[25] = sc.rare ? 1.f : 0.f;
+            slot[26] = sc.change;
           }
           mbar_arrive_warp(&sc_full[t % C::SCN]);
         }

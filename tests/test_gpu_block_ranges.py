@@ -107,6 +107,20 @@ def test_value_scales_at_the_ends_of_float32(d, top):
         _rows(c.decode() if new is None else c.prefill(), c.exact()[0], new)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("first,then", [(2.0 ** -126, 2.0 ** 120), (2.0 ** 120, 2.0 ** -126), (2.0 ** -126, 2.0 ** 127), (2.0 ** -60, 2.0 ** 70)])
+def test_tiles_of_tiny_and_of_huge_value_scales(d, first, then):
+    """Whole tiles of scales at one end of float32, with zeros among them, before tiles at the other: every key's
+    weight counts, whatever its value is worth (codes of at most 1)."""
+    for new in (None, [300], [7]):
+        c = Case([900], 4, 1, d, new=new, seed=d, spread=0, q_size=0.3)
+        live = c.pools[1][c.table[0]]
+        c.pools[1][c.table[0]] = np.where((live & 0x7F) > 0x38, (live & 0x80) | 0x38, live)
+        for page, blk in enumerate(c.table[0]):
+            c.scales[1][blk] = np.float32(0.0 if page % 16 == 3 else first if page < 16 or 32 <= page < 48 else then)
+        _rows(c.decode() if new is None else c.prefill(), c.exact()[0], new)
+
+
 # ------------------------------------------------------------------ queries
 
 def _terms(x):
