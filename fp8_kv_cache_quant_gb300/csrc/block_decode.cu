@@ -41,9 +41,9 @@
 //   9     TMEM; polls the barriers and issues S^T and P.V products as they become possible.
 //
 // What bounds it: HBM, around a fixed 12-15 us of ramp, last pieces and merge (groups of one head: 178 MB of
-// head_dim 64 take 39 us, 356 MB of head_dim 128 63, 7.3 TB/s on the difference).  8 x 16k-24k tokens, 32/8
-// heads, head_dim 128: 63 us, 5.4 TB/s; 8 x 8k-32k, 64/8 heads, head_dim 64: 44 us (49.7 when warp 9 copied V
-// as well and was busy all the time); one sequence of 4,096: 10.4 us.  Two CTAs per SM with three stages
+// head_dim 64 take 40 us, 356 MB of head_dim 128 63, 7.3 TB/s on the difference).  8 x 16k-24k tokens, 32/8
+// heads, head_dim 128: 63 us, 5.4 TB/s; 8 x 8k-32k, 64/8 heads, head_dim 64: 47 us (six more when warp 9 copied
+// V as well and was busy all the time); one sequence of 4,096: 10.6 us.  Two CTAs per SM with three stages
 // of K and V; three CTAs with two stages, at 64 registers, are within 1.5 % of it either way.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and
 // products drain and returns (its pieces are then undefined, its units still counted).
