@@ -83,7 +83,7 @@ struct ScaleRange {
 struct BlockScale {
   float lv, iv;  // L and 2^(o - L), the latter negative where the scale counts as zero
   // Not as a rule: o changed, a scale counts as zero, or the scales so far lie so far apart that 2^-|r - R_t| may
-  // underflow though the keys' weights are alike: the sums are joined by join_sums.
+  // underflow though the keys' weights are alike: the sums are joined by rare_factors.
   bool rare;
   float change;  // new o - old o
 };

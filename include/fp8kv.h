@@ -255,7 +255,7 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
  *   new codes are e4m3(fl32(x * fl32(1 / s))), round-to-nearest-even, saturating (infinities
  *          become +-448, NaN stays NaN).
  * Slots behind T_b - 1, and every other block, keep their bytes and scales.  A block that a
- * call appends to must belong to one sequence of the call.
+ * call appends to must belong to one sequence of the call, and be one page of it.
  *
  *   q, q_out, k, v, strides  as for kv_rope_cache; q needs rope.cos_sin
  *   n_tokens      rows of q, k and v
