@@ -16,7 +16,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
-from typing import Optional
+from typing import Optional, Sequence
 
 import numpy as np
 import torch
@@ -36,6 +36,7 @@ EXPORTS = (
     "fp8_decode_attn_num_splits", "fp8_decode_attn", "fkv_prefill_block_n", "fp8_prefill_attn",
     "fp8_decode_attn_noalloc", "fp8_decode_attn_split_blocks", "fkv_decode_block_n", "kv_quant_cache_clips",
     "fp8_decode_step", "fkv_set_decode_wait_limit_ns", "kv_rope_cache", "kv_block_cache",
+    "kv_rope_cache_axes", "kv_block_cache_axes",
     "fp8_block_decode_attn_workspace_size", "fp8_block_decode_attn", "fp8_block_prefill_attn",
 )
 NOALLOC_WORKSPACE_BYTES = 16 << 20
@@ -57,6 +58,11 @@ class _BlockCache(ctypes.Structure):
     _fields_ = [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
                 ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Axes(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("axis_stride", ctypes.c_int64), ("num_axes", ctypes.c_int32),
+                ("pair_axis", ctypes.c_void_p)]
 
 
 class _Rope(ctypes.Structure):
@@ -119,6 +125,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kv_block_cache.restype = ctypes.c_int
     lib.kv_block_cache.argtypes = [c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i64, c_vp, c_i64, c_i32, c_vp, c_i32, c_i32,
                                    _Rope, _BlockCache, c_vp, c_i32, c_vp, c_vp, c_vp]
+    lib.kv_rope_cache_axes.restype = ctypes.c_int
+    lib.kv_rope_cache_axes.argtypes = [_Axes if i == 9 else t for i, t in enumerate(lib.kv_rope_cache.argtypes)]
+    lib.kv_block_cache_axes.restype = ctypes.c_int
+    lib.kv_block_cache_axes.argtypes = lib.kv_block_cache.argtypes[:10] + [_Axes] + lib.kv_block_cache.argtypes[10:]
     lib.fp8_block_decode_attn.restype = ctypes.c_int
     lib.fp8_block_decode_attn.argtypes = [c_vp, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f, c_i32, c_vp, c_vp,
                                           c_sz, c_vp, c_vp]
@@ -345,10 +355,26 @@ def fp8_prefill_attn(q, cu_seqlens_q, max_q_len, cache: LayerCache, block_table,
 class Rope:
     """A rotary position embedding: ``cos_sin`` float32 [max_positions][rot_dim], row p holding
     rot_dim / 2 cosines, then rot_dim / 2 sines; ``interleaved`` pairs neighbours (2 i, 2 i + 1)
-    instead of the halves (i, i + rot_dim / 2)."""
+    instead of the halves (i, i + rot_dim / 2).  ``axes``: for positions of several axes (time, height, width),
+    the axis, 0 to 3, of each of the rot_dim / 2 pairs; positions are then int64 [axes][n]."""
 
     cos_sin: torch.Tensor
     interleaved: bool = False
+    axes: Optional[Sequence[int]] = None
+
+    def __post_init__(self):
+        self.pair_axis, self.pair_args = None, (None, 0)   # bytes kept alive here, and what the calls take
+        if self.axes is not None:
+            x = np.asarray(self.axes)
+            if x.ndim != 1 or 2 * x.size != self.cos_sin.shape[1] or x.dtype.kind not in "iu" or x.min() < 0 or x.max() > 3:
+                raise ValueError(f"Rope: axes names an axis from 0 to 3 for each of the {self.cos_sin.shape[1] // 2} pairs")
+            self.pair_axis = np.ascontiguousarray(x, np.uint8)
+            self.pair_args = (self.pair_axis.ctypes.data, self.pair_axis.size)
+
+    @staticmethod
+    def sections(*pairs):
+        """``axes`` of consecutive sections: pairs[0] pairs of axis 0, then pairs[1] of axis 1, ..."""
+        return [a for a, n in enumerate(pairs) for _ in range(n)]
 
     @staticmethod
     def table(max_positions, rot_dim, base=10000.0, device="cuda"):
@@ -422,21 +448,29 @@ def kv_rope_cache(q, k, v, positions, slot_mapping, rope: Rope, cache: LayerCach
                   gran=SCALE_PER_TENSOR, layer=0, skip_layer_mask=None, q_out=None, fault=None, stream=None):
     """kv_quant_cache of K turned for its positions and of V, and the turned queries (bf16, returned; rows of
     skipped tokens are not written).  q, k, v: bf16 [n][heads][D], rows may be slices of a wider tensor; q may
-    be None, q_out may be q.  positions, slot_mapping: int64 [n]."""
+    be None, q_out may be q.  positions, slot_mapping: int64 [n]; with ``rope.axes`` positions is int64 [axes][n]."""
     mp, nl, keep = _mask_arg(skip_layer_mask)
     skipped = keep is not None and 0 <= layer < nl and bool(keep[layer])
-    return _call("kv_rope_cache", k, stream, q, k, v, positions, slot_mapping, rope.cos_sin, rope.interleaved, cache.k_cache,
-                 cache.v_cache, cache.kv_format, k_scale, v_scale, gran, layer, mp, nl, skipped, q_out, fault)
+    several = rope.pair_axis is not None
+    return _call("kv_rope_cache_axes" if several else "kv_rope_cache", k, stream, q, k, v, positions, slot_mapping, rope.cos_sin,
+                 rope.interleaved, *(rope.pair_args if several else ()), cache.k_cache, cache.v_cache, cache.kv_format, k_scale,
+                 v_scale, gran, layer, mp, nl, skipped, q_out, fault)
 
 
 def kv_block_cache(k, v, cu_seqlens, max_q_len, cache: BlockCache, block_table, context_lens, rope: Optional[Rope] = None,
-                   q=None, q_out=None, fault=None, stream=None):
+                   q=None, q_out=None, fault=None, stream=None, positions=None):
     """Append each sequence's new tokens (rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k, v and q, the last of
     its context_lens[b] tokens) to a block-scaled cache, K and q turned for their positions when ``rope`` is
-    given; returns the turned queries (None without q)."""
-    return _call("kv_block_cache", k, stream, k, v, cu_seqlens, max_q_len, cache.k_cache, cache.v_cache, cache.k_scale,
-                 cache.v_scale, block_table, context_lens, None if rope is None else rope.cos_sin,
-                 rope is not None and rope.interleaved, q, q_out, fault)
+    given; returns the turned queries (None without q).  ``positions``: int64 [n], or [axes][n] with ``rope.axes``,
+    what the rows are turned for (None: their places in the cache)."""
+    given = ()
+    if positions is not None:
+        given = (*((None, 0) if rope is None else rope.pair_args), positions)
+    elif rope is not None and rope.pair_axis is not None:
+        raise ValueError("kv_block_cache: a rope of several axes takes positions")
+    return _call("kv_block_cache_axes" if given else "kv_block_cache", k, stream, k, v, cu_seqlens, max_q_len, cache.k_cache,
+                 cache.v_cache, cache.k_scale, cache.v_scale, block_table, context_lens, None if rope is None else rope.cos_sin,
+                 rope is not None and rope.interleaved, *given, q, q_out, fault)
 
 
 def fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim) -> int:

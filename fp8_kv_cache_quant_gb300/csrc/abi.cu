@@ -191,6 +191,139 @@ BlockDecodePlan plan_block_decode(int32_t B, int32_t Hq, int32_t Hkv, int32_t D)
   return plan;
 }
 
+// The axes of the pairs in the kernels' form; false if there are none such.
+bool pair_axes(const fkv_axes& a, int32_t rot_dim, fkv::PairAxes* out) {
+  if (a.num_axes < 1 || a.num_axes > 4 || a.axis_stride < 0) return false;
+  out->count = a.num_axes;
+  out->stride = a.axis_stride;
+  for (int32_t i = 0; a.pair_axis && i < rot_dim / 2; ++i) {
+    if (a.pair_axis[i] >= a.num_axes) return false;
+    out->axis[i / 16] |= static_cast<uint32_t>(a.pair_axis[i]) << (2 * (i % 16));
+  }
+  return true;
+}
+
+fkv_status rope_cache_entry(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                         const void* k, int64_t k_stride, const void* v, int64_t v_stride, const fkv_axes& axes,
+                         const int64_t* slot_mapping, int32_t n_tokens, fkv_rope rope, fkv_layer_cache cache,
+                         const float* k_scale, const float* v_scale, fkv_scale_gran gran, int32_t layer,
+                         const uint8_t* skip_layer_mask, int32_t num_layers, int32_t* fault, fkv_stream_t stream) {
+  if (n_tokens < 0 || num_q_heads < 0) return FKV_INVALID_ARG;
+  if (cache.block_size != 16) return cache.block_size > 0 ? FKV_UNSUPPORTED : FKV_INVALID_ARG;
+  if (cache.num_blocks <= 0 || cache.num_kv_heads <= 0 || !valid_format(cache)) return FKV_INVALID_ARG;
+  if (!supported_head_dim(cache.head_dim)) return FKV_UNSUPPORTED;
+  if (num_q_heads > 8192 || cache.num_kv_heads > 8192) return FKV_UNSUPPORTED;
+  if (gran != FKV_SCALE_PER_TENSOR && gran != FKV_SCALE_PER_HEAD) return FKV_INVALID_ARG;
+  fkv_status st = FKV_OK;
+  const bool bf16 = layer_is_bf16(layer, skip_layer_mask, num_layers, &st);
+  if (st != FKV_OK) return st;
+  st = check_rope(rope, cache.head_dim);
+  if (st != FKV_OK) return st;
+  fkv::RopeCacheParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (!pair_axes(axes, rope.rot_dim, &p.axes)) return FKV_INVALID_ARG;
+  if (n_tokens == 0) return FKV_OK;
+  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
+  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
+  if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
+  if (q && (!valid_rows(q, q_stride, q_row) || !valid_rows(q_out, q_out_stride, q_row))) return FKV_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return FKV_INVALID_ARG;
+  if (!axes.positions || !slot_mapping || !aligned(axes.positions, 8) || !aligned(slot_mapping, 8)) return FKV_INVALID_ARG;
+  if (!cache.k_cache || !cache.v_cache || !aligned(cache.k_cache, 16) || !aligned(cache.v_cache, 16))
+    return FKV_INVALID_ARG;
+  if (!bf16 && (!k_scale || !v_scale)) return FKV_INVALID_ARG;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_out_stride = q_out_stride;
+  p.cos_sin = rope.cos_sin;
+  p.max_pos = rope.max_positions;
+  p.rot = rope.rot_dim;
+  p.interleaved = rope.interleaved != 0;
+  p.positions = axes.positions;
+  p.slots = slot_mapping;
+  p.n_tokens = n_tokens;
+  p.Hq = num_q_heads;
+  p.H = cache.num_kv_heads;
+  p.D = cache.head_dim;
+  p.kc = static_cast<uint8_t*>(cache.k_cache);
+  p.vc = static_cast<uint8_t*>(cache.v_cache);
+  p.capacity = static_cast<long long>(cache.num_blocks) * 16;
+  p.ks = k_scale;
+  p.vs = v_scale;
+  p.per_head = gran == FKV_SCALE_PER_HEAD;
+  p.fault = fault;
+  const int pool = bf16 ? 2 : cache.kv_format == FKV_KV_E5M2 ? 1 : 0;
+  return from_cuda(fkv::launch_rope_cache(p, pool, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
+fkv_status block_cache_entry(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                          const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t n_tokens,
+                          const fkv_axes* axes, const int32_t* cu_seqlens, int32_t batch, int32_t max_q_len, fkv_rope rope,
+                          fkv_block_cache cache, const int32_t* block_table, int32_t max_blocks,
+                          const int32_t* context_lens, int32_t* fault, fkv_stream_t stream) {
+  if (n_tokens < 0 || batch < 0 || max_q_len < 0 || max_blocks <= 0 || num_q_heads < 0) return FKV_INVALID_ARG;
+  fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (batch > 65535 || num_q_heads > 8192 || cache.num_kv_heads > 8192 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
+  const bool turned = rope.cos_sin != nullptr;
+  if (turned) {
+    st = check_rope(rope, cache.head_dim);
+    if (st != FKV_OK) return st;
+  } else if (num_q_heads > 0 || rope.rot_dim != 0) {
+    return FKV_INVALID_ARG;
+  }
+  fkv::BlockCacheParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (axes && (!turned || !pair_axes(*axes, rope.rot_dim, &p.axes))) return FKV_INVALID_ARG;
+  if (n_tokens == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
+  if (axes && (!axes->positions || !aligned(axes->positions, 8))) return FKV_INVALID_ARG;
+  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
+  const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
+  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
+  if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
+  if (q && (!valid_rows(q, q_stride, q_row) || !valid_rows(q_out, q_out_stride, q_row))) return FKV_INVALID_ARG;
+  if (q && q == q_out && q_stride != q_out_stride) return FKV_INVALID_ARG;
+  if (!valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!cu_seqlens || !block_table || !context_lens || !aligned(cu_seqlens, 4) || !aligned(block_table, 4) ||
+      !aligned(context_lens, 4))
+    return FKV_INVALID_ARG;
+  p.positions = axes ? axes->positions : nullptr;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_out_stride = q_out_stride;
+  p.cos_sin = rope.cos_sin;
+  p.max_pos = rope.max_positions;
+  p.rot = turned ? rope.rot_dim : 0;
+  p.interleaved = rope.interleaved != 0;
+  p.cu = cu_seqlens;
+  p.ctx = context_lens;
+  p.block_table = block_table;
+  p.n_tokens = n_tokens;
+  p.B = batch;
+  p.max_q_len = std::min(max_q_len, n_tokens);  // (longer ones have rows beyond n_tokens)
+  p.Hq = num_q_heads;
+  p.H = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.kc = static_cast<uint8_t*>(cache.k_cache);
+  p.vc = static_cast<uint8_t*>(cache.v_cache);
+  p.ks = cache.k_scale;
+  p.vs = cache.v_scale;
+  p.fault = fault;
+  return from_cuda(fkv::launch_block_cache(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 float base2_scale(float softmax_scale, int32_t head_dim) {
   const float tau = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(static_cast<float>(head_dim));
   return tau * 1.4426950408889634f;
@@ -299,7 +432,7 @@ const char* fkv_status_string(fkv_status status) {
   return "unknown status";
 }
 
-int32_t fkv_version(void) { return 106; }
+int32_t fkv_version(void) { return 107; }
 
 void fkv_set_decode_wait_limit_ns(unsigned long long ns) { g_decode_wait_ns.store(ns, std::memory_order_relaxed); }
 
@@ -441,57 +574,18 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
                          const int64_t* slot_mapping, int32_t n_tokens, fkv_rope rope, fkv_layer_cache cache,
                          const float* k_scale, const float* v_scale, fkv_scale_gran gran, int32_t layer,
                          const uint8_t* skip_layer_mask, int32_t num_layers, int32_t* fault, fkv_stream_t stream) {
-  if (n_tokens < 0 || num_q_heads < 0) return FKV_INVALID_ARG;
-  if (cache.block_size != 16) return cache.block_size > 0 ? FKV_UNSUPPORTED : FKV_INVALID_ARG;
-  if (cache.num_blocks <= 0 || cache.num_kv_heads <= 0 || !valid_format(cache)) return FKV_INVALID_ARG;
-  if (!supported_head_dim(cache.head_dim)) return FKV_UNSUPPORTED;
-  if (num_q_heads > 8192 || cache.num_kv_heads > 8192) return FKV_UNSUPPORTED;
-  if (gran != FKV_SCALE_PER_TENSOR && gran != FKV_SCALE_PER_HEAD) return FKV_INVALID_ARG;
-  fkv_status st = FKV_OK;
-  const bool bf16 = layer_is_bf16(layer, skip_layer_mask, num_layers, &st);
-  if (st != FKV_OK) return st;
-  st = check_rope(rope, cache.head_dim);
-  if (st != FKV_OK) return st;
-  if (n_tokens == 0) return FKV_OK;
-  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
-  const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
-  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
-  if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
-  if (q && (!valid_rows(q, q_stride, q_row) || !valid_rows(q_out, q_out_stride, q_row))) return FKV_INVALID_ARG;
-  if (q && q == q_out && q_stride != q_out_stride) return FKV_INVALID_ARG;
-  if (!positions || !slot_mapping || !aligned(positions, 8) || !aligned(slot_mapping, 8)) return FKV_INVALID_ARG;
-  if (!cache.k_cache || !cache.v_cache || !aligned(cache.k_cache, 16) || !aligned(cache.v_cache, 16))
-    return FKV_INVALID_ARG;
-  if (!bf16 && (!k_scale || !v_scale)) return FKV_INVALID_ARG;
-  fkv::RopeCacheParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v);
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.q_out = static_cast<__nv_bfloat16*>(q_out);
-  p.q_out_stride = q_out_stride;
-  p.cos_sin = rope.cos_sin;
-  p.max_pos = rope.max_positions;
-  p.rot = rope.rot_dim;
-  p.interleaved = rope.interleaved != 0;
-  p.positions = positions;
-  p.slots = slot_mapping;
-  p.n_tokens = n_tokens;
-  p.Hq = num_q_heads;
-  p.H = cache.num_kv_heads;
-  p.D = cache.head_dim;
-  p.kc = static_cast<uint8_t*>(cache.k_cache);
-  p.vc = static_cast<uint8_t*>(cache.v_cache);
-  p.capacity = static_cast<long long>(cache.num_blocks) * 16;
-  p.ks = k_scale;
-  p.vs = v_scale;
-  p.per_head = gran == FKV_SCALE_PER_HEAD;
-  p.fault = fault;
-  const int pool = bf16 ? 2 : cache.kv_format == FKV_KV_E5M2 ? 1 : 0;
-  return from_cuda(fkv::launch_rope_cache(p, pool, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+  const fkv_axes one = {positions, 0, 1, nullptr};
+  return rope_cache_entry(q, q_stride, q_out, q_out_stride, num_q_heads, k, k_stride, v, v_stride, one, slot_mapping, n_tokens,
+                          rope, cache, k_scale, v_scale, gran, layer, skip_layer_mask, num_layers, fault, stream);
+}
+
+fkv_status kv_rope_cache_axes(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                              const void* k, int64_t k_stride, const void* v, int64_t v_stride, fkv_axes axes,
+                              const int64_t* slot_mapping, int32_t n_tokens, fkv_rope rope, fkv_layer_cache cache,
+                              const float* k_scale, const float* v_scale, fkv_scale_gran gran, int32_t layer,
+                              const uint8_t* skip_layer_mask, int32_t num_layers, int32_t* fault, fkv_stream_t stream) {
+  return rope_cache_entry(q, q_stride, q_out, q_out_stride, num_q_heads, k, k_stride, v, v_stride, axes, slot_mapping, n_tokens,
+                          rope, cache, k_scale, v_scale, gran, layer, skip_layer_mask, num_layers, fault, stream);
 }
 
 fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
@@ -499,58 +593,17 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
                           const int32_t* cu_seqlens, int32_t batch, int32_t max_q_len, fkv_rope rope,
                           fkv_block_cache cache, const int32_t* block_table, int32_t max_blocks,
                           const int32_t* context_lens, int32_t* fault, fkv_stream_t stream) {
-  if (n_tokens < 0 || batch < 0 || max_q_len < 0 || max_blocks <= 0 || num_q_heads < 0) return FKV_INVALID_ARG;
-  fkv_status st = check_block_cache(cache);
-  if (st != FKV_OK) return st;
-  if (batch > 65535 || num_q_heads > 8192 || cache.num_kv_heads > 8192 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
-  const bool turned = rope.cos_sin != nullptr;
-  if (turned) {
-    st = check_rope(rope, cache.head_dim);
-    if (st != FKV_OK) return st;
-  } else if (num_q_heads > 0 || rope.rot_dim != 0) {
-    return FKV_INVALID_ARG;
-  }
-  if (n_tokens == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
-  if ((q != nullptr) != (num_q_heads > 0) || (q_out != nullptr) != (num_q_heads > 0)) return FKV_INVALID_ARG;
-  const int64_t q_row = static_cast<int64_t>(num_q_heads) * cache.head_dim;
-  const int64_t kv_row = static_cast<int64_t>(cache.num_kv_heads) * cache.head_dim;
-  if (!valid_rows(k, k_stride, kv_row) || !valid_rows(v, v_stride, kv_row)) return FKV_INVALID_ARG;
-  if (q && (!valid_rows(q, q_stride, q_row) || !valid_rows(q_out, q_out_stride, q_row))) return FKV_INVALID_ARG;
-  if (q && q == q_out && q_stride != q_out_stride) return FKV_INVALID_ARG;
-  if (!valid_block_pools(cache)) return FKV_INVALID_ARG;
-  if (!cu_seqlens || !block_table || !context_lens || !aligned(cu_seqlens, 4) || !aligned(block_table, 4) ||
-      !aligned(context_lens, 4))
-    return FKV_INVALID_ARG;
-  fkv::BlockCacheParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k = static_cast<const __nv_bfloat16*>(k);
-  p.v = static_cast<const __nv_bfloat16*>(v);
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
-  p.v_stride = v_stride;
-  p.q_out = static_cast<__nv_bfloat16*>(q_out);
-  p.q_out_stride = q_out_stride;
-  p.cos_sin = rope.cos_sin;
-  p.max_pos = rope.max_positions;
-  p.rot = turned ? rope.rot_dim : 0;
-  p.interleaved = rope.interleaved != 0;
-  p.cu = cu_seqlens;
-  p.ctx = context_lens;
-  p.block_table = block_table;
-  p.n_tokens = n_tokens;
-  p.B = batch;
-  p.max_q_len = std::min(max_q_len, n_tokens);  // (longer ones have rows beyond n_tokens)
-  p.Hq = num_q_heads;
-  p.H = cache.num_kv_heads;
-  p.num_blocks = cache.num_blocks;
-  p.max_blocks = max_blocks;
-  p.kc = static_cast<uint8_t*>(cache.k_cache);
-  p.vc = static_cast<uint8_t*>(cache.v_cache);
-  p.ks = cache.k_scale;
-  p.vs = cache.v_scale;
-  p.fault = fault;
-  return from_cuda(fkv::launch_block_cache(p, cache.head_dim, reinterpret_cast<cudaStream_t>(stream)));
+  return block_cache_entry(q, q_stride, q_out, q_out_stride, num_q_heads, k, k_stride, v, v_stride, n_tokens, nullptr, cu_seqlens,
+                           batch, max_q_len, rope, cache, block_table, max_blocks, context_lens, fault, stream);
+}
+
+fkv_status kv_block_cache_axes(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int32_t num_q_heads,
+                               const void* k, int64_t k_stride, const void* v, int64_t v_stride, int32_t n_tokens,
+                               fkv_axes axes, const int32_t* cu_seqlens, int32_t batch, int32_t max_q_len, fkv_rope rope,
+                               fkv_block_cache cache, const int32_t* block_table, int32_t max_blocks,
+                               const int32_t* context_lens, int32_t* fault, fkv_stream_t stream) {
+  return block_cache_entry(q, q_stride, q_out, q_out_stride, num_q_heads, k, k_stride, v, v_stride, n_tokens, &axes, cu_seqlens,
+                           batch, max_q_len, rope, cache, block_table, max_blocks, context_lens, fault, stream);
 }
 
 size_t fp8_block_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,

@@ -149,6 +149,29 @@ fkv_rope rope_of(const char* fn, const Tensor& cos_sin, bool interleaved, at::De
   return r;
 }
 
+// The axes of a rope's pairs, two arguments (the address of their bytes, null for none, and their number), and the
+// positions of n tokens that go with them: int64 [n], or [axes][n] whose rows may be slices.
+struct Axes {
+  const uint8_t* pair;
+  int64_t pairs;
+
+  Axes(Args& a, bool given) : pair(given ? static_cast<const uint8_t*>(a.pointer()) : nullptr), pairs(given ? a.integer() : 0) {}
+  fkv_axes of(const char* fn, const Tensor& pos, int64_t n, const fkv_rope& rope, at::Device device) const {
+    fkv_axes x = {nullptr, 0, 1, pair};
+    if (pair && pairs != rope.rot_dim / 2) refuse(fn, "the rope names the axes of " + std::to_string(pairs) + " pairs; its table has " + std::to_string(rope.rot_dim / 2));
+    if (!pair) {
+      x.positions = fits<int64_t>(fn, "positions", pos, at::kLong, {n}, device);
+      return x;
+    }
+    if (pos.scalar_type() != at::kLong || pos.dim() != 2 || pos.size(1) != n || pos.device() != device || (n > 1 && pos.stride(1) != 1))
+      refuse(fn, "positions is " + text(pos) + "; wanted Long [axes, " + std::to_string(n) + "] on " + device.str() + " with consecutive rows");
+    x.positions = static_cast<const int64_t*>(pos.data_ptr());
+    x.num_axes = small(fn, pos.size(0));
+    x.axis_stride = pos.stride(0);
+    return x;
+  }
+};
+
 // The next four arguments, a block-scaled cache whose heads are `heads` (-1: any) by d.
 fkv_block_cache block_cache(Args& a, int64_t heads, int64_t d, at::Device device) {
   const Tensor k = a.tensor("k_cache"), v = a.tensor("v_cache"), ks = a.tensor("k_scale"), vs = a.tensor("v_scale");
@@ -171,15 +194,17 @@ PyObject* result(fkv_status st, const Tensor& t) {
   return Py_BuildValue("iN", static_cast<int>(st), o);
 }
 
-// stream, q, k, v, positions, slot_mapping, cos_sin, interleaved, k_cache, v_cache, kv_format,
+// stream, q, k, v, positions, slot_mapping, cos_sin, interleaved, kAxes: the pairs' axes (see Axes), k_cache, v_cache, kv_format,
 // k_scale, v_scale, gran, layer, mask address, its length, whether the layer is skipped, q_out, fault
-PyObject* kv_rope_cache_(Args a) {
+template <bool kAxes>
+PyObject* rope_cache(Args a) {
   void* stream = a.pointer();
   Queries q;
   q.q = a.tensor("q", true);
   const Tensor k = three_dims(a, "k"), v = a.tensor("v"), pos = a.tensor("positions"), slots = a.tensor("slot_mapping"),
                cs = a.tensor("cos_sin");
   const bool interleaved = a.integer() != 0;
+  const Axes axes(a, kAxes);
   const Tensor kc = a.tensor("k_cache"), vc = a.tensor("v_cache");
   fkv_layer_cache c;
   c.kv_format = a.i32();
@@ -203,10 +228,11 @@ PyObject* kv_rope_cache_(Args a) {
   c.block_size = small(a.fn, bs);
   c.num_kv_heads = small(a.fn, h);
   c.head_dim = small(a.fn, d);
-  const fkv_status st = kv_rope_cache(
+  const fkv_rope rope = rope_of(a.fn, cs, interleaved, dev);
+  const fkv_status st = kv_rope_cache_axes(
       q.src, q.stride, q.dst, q.out_stride, q.heads, k.data_ptr(), k_stride, v.data_ptr(), v_stride,
-      fits<int64_t>(a.fn, "positions", pos, at::kLong, {n}, dev), fits<int64_t>(a.fn, "slot_mapping", slots, at::kLong, {n}, dev),
-      small(a.fn, n), rope_of(a.fn, cs, interleaved, dev), c, fits<float>(a.fn, "k_scale", ks, at::kFloat, {scales}, dev),
+      axes.of(a.fn, pos, n, rope, dev), fits<int64_t>(a.fn, "slot_mapping", slots, at::kLong, {n}, dev),
+      small(a.fn, n), rope, c, fits<float>(a.fn, "k_scale", ks, at::kFloat, {scales}, dev),
       fits<float>(a.fn, "v_scale", vs, at::kFloat, {scales}, dev), static_cast<fkv_scale_gran>(gran), layer,
       static_cast<const uint8_t*>(mask), layers, fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev),
       static_cast<fkv_stream_t>(stream));
@@ -214,8 +240,9 @@ PyObject* kv_rope_cache_(Args a) {
 }
 
 // stream, k, v, cu_seqlens, max_q_len, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, cos_sin,
-// interleaved, q, q_out, fault
-PyObject* kv_block_cache_(Args a) {
+// interleaved, kAxes: the pairs' axes (see Axes) and positions, q, q_out, fault
+template <bool kAxes>
+PyObject* block_cache_append(Args a) {
   void* stream = a.pointer();
   const Tensor k = three_dims(a, "k"), v = a.tensor("v"), cu = a.tensor("cu_seqlens");
   const int32_t max_q_len = a.i32();
@@ -224,6 +251,8 @@ PyObject* kv_block_cache_(Args a) {
   const fkv_block_cache c = block_cache(a, h, d, dev);
   const Tensor table = a.tensor("block_table"), ctx = a.tensor("context_lens"), cs = a.tensor("cos_sin", true);
   const bool interleaved = a.integer() != 0;
+  const Axes axes(a, kAxes);
+  const Tensor pos = kAxes ? a.tensor("positions") : Tensor();
   Queries q;
   q.q = a.tensor("q", true);
   q.out = a.tensor("q_out", true);
@@ -233,13 +262,19 @@ PyObject* kv_block_cache_(Args a) {
   q.check(a.fn, n, d, dev);
   if (table.dim() != 2) refuse(a.fn, "block_table is " + text(table) + "; wanted [batch][blocks]");
   const int64_t b = table.size(0);
-  const fkv_status st = kv_block_cache(
-      q.src, q.stride, q.dst, q.out_stride, q.heads, k.data_ptr(), k_stride, v.data_ptr(), v_stride, small(a.fn, n),
-      fits<int32_t>(a.fn, "cu_seqlens", cu, at::kInt, {b + 1}, dev), small(a.fn, b), max_q_len,
-      rope_of(a.fn, cs, interleaved, dev), c, fits<int32_t>(a.fn, "block_table", table, at::kInt, table.sizes(), dev),
-      small(a.fn, table.size(1)), fits<int32_t>(a.fn, "context_lens", ctx, at::kInt, {b}, dev),
-      fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev), static_cast<fkv_stream_t>(stream));
-  return result(st, q.out);
+  const fkv_rope rope = rope_of(a.fn, cs, interleaved, dev);
+  const int32_t *starts = fits<int32_t>(a.fn, "cu_seqlens", cu, at::kInt, {b + 1}, dev),
+                *blocks = fits<int32_t>(a.fn, "block_table", table, at::kInt, table.sizes(), dev),
+                *lens = fits<int32_t>(a.fn, "context_lens", ctx, at::kInt, {b}, dev);
+  int32_t* const flt = fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev);
+  const auto call = [&](auto entry, auto... positions) {
+    return entry(q.src, q.stride, q.dst, q.out_stride, q.heads, k.data_ptr(), k_stride, v.data_ptr(), v_stride, small(a.fn, n),
+                 positions..., starts, small(a.fn, b), max_q_len, rope, c, blocks, small(a.fn, table.size(1)), lens, flt,
+                 static_cast<fkv_stream_t>(stream));
+  };
+  if (!kAxes) return result(call(kv_block_cache), q.out);
+  if (!cs.defined()) refuse(a.fn, "positions without a rope");
+  return result(call(kv_block_cache_axes, axes.of(a.fn, pos, n, rope, dev)), q.out);
 }
 
 // stream, q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, softmax_scale, window, out, workspace, fault
@@ -297,6 +332,11 @@ PyObject* fp8_block_prefill_attn_(Args a) {
   return result(st, out);
 }
 
+PyObject* kv_rope_cache_(Args a) { return rope_cache<false>(a); }
+PyObject* kv_rope_cache_axes_(Args a) { return rope_cache<true>(a); }
+PyObject* kv_block_cache_(Args a) { return block_cache_append<false>(a); }
+PyObject* kv_block_cache_axes_(Args a) { return block_cache_append<true>(a); }
+
 // No C++ exception leaves a call: what torch throws becomes a RuntimeError.
 template <PyObject* (*kBody)(Args)>
 PyObject* entry(const char* fn, PyObject* const* args, Py_ssize_t n) {
@@ -315,12 +355,15 @@ PyObject* entry(const char* fn, PyObject* const* args, Py_ssize_t n) {
   PyObject* name##_py(PyObject*, PyObject* const* args, Py_ssize_t n) { return entry<name##_>(#name, args, n); }
 FKV_ENTRY(kv_rope_cache)
 FKV_ENTRY(kv_block_cache)
+FKV_ENTRY(kv_rope_cache_axes)
+FKV_ENTRY(kv_block_cache_axes)
 FKV_ENTRY(fp8_block_decode_attn)
 FKV_ENTRY(fp8_block_prefill_attn)
 #undef FKV_ENTRY
 
 #define FKV_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name##_py)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FKV_METHOD(kv_rope_cache), FKV_METHOD(kv_block_cache), FKV_METHOD(fp8_block_decode_attn),
+PyMethodDef methods[] = {FKV_METHOD(kv_rope_cache), FKV_METHOD(kv_block_cache), FKV_METHOD(kv_rope_cache_axes),
+                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(fp8_block_decode_attn),
                          FKV_METHOD(fp8_block_prefill_attn), {nullptr, nullptr, 0, nullptr}};
 #undef FKV_METHOD
 

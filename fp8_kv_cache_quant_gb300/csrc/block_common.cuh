@@ -131,6 +131,14 @@ FKV_DEV RareFactors rare_factors(float& r, float& l, float R, float change) {
   return f;
 }
 
+// The axes of a head's pairs, two bits each, and the positions' strides; count 0: one position per token, or
+// (kv_block_cache) the token's place.
+struct PairAxes {
+  int count;
+  long long stride;                           // between the axes' positions
+  uint32_t axis[8];                           // pair i: bits 2 i % 32 of word i / 16
+};
+
 struct RopeCacheParams {
   const __nv_bfloat16 *q, *k, *v;             // token rows at the strides (in elements)
   long long q_stride, k_stride, v_stride;
@@ -139,7 +147,8 @@ struct RopeCacheParams {
   const float* cos_sin;                       // [max_pos][rot]
   int max_pos, rot;
   int interleaved;
-  const int64_t* positions;                   // [n_tokens]
+  PairAxes axes;
+  const int64_t* positions;                   // [n_tokens], of axis a at a * axes.stride
   const int64_t* slots;                       // [n_tokens]
   int n_tokens, Hq, H, D;                     // Hq 0: no queries
   uint8_t *kc, *vc;
@@ -160,6 +169,8 @@ struct BlockCacheParams {
   const float* cos_sin;                       // null: no rotation (rot 0)
   int max_pos, rot;
   int interleaved;
+  PairAxes axes;
+  const int64_t* positions;                   // null: the tokens' places
   const int32_t* cu;                          // [B + 1]
   const int32_t* ctx;                         // [B]
   const int32_t* block_table;                 // [B][max_blocks]

@@ -97,6 +97,42 @@ FKV_DEV void turn_unit(float (&a)[8], float (&b)[8], const float* cs, int rot, i
   }
 }
 
+// The axes of the 8 pairs of unit u, two bits each.
+FKV_DEV uint32_t unit_axes(const PairAxes& x, int u) { return (x.axis[u >> 1] >> (16 * (u & 1))) & 0xFFFFu; }
+
+FKV_DEV int pick(const int (&pos)[4], uint32_t axis) {
+  const int lo = axis & 1 ? pos[1] : pos[0], hi = axis & 1 ? pos[3] : pos[2];
+  return axis & 2 ? hi : lo;
+}
+
+// turn_unit with the pairs' own positions: a unit whose pairs are all of one axis (sections) reads that
+// position's table row eight entries at a time, another one entry by entry.
+FKV_DEV void turn_unit_axes(float (&a)[8], float (&b)[8], const float* table, const int (&pos)[4], uint32_t axes, int rot, int u,
+                            bool interleaved) {
+  const uint32_t first = axes & 3;
+  if (axes == first * 0x5555u) {
+    turn_unit(a, b, table + static_cast<long long>(pick(pos, first)) * rot, rot, u, interleaved);
+    return;
+  }
+  float c[8], s[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float* cs = table + static_cast<long long>(pick(pos, axes >> (2 * i) & 3)) * rot + 8 * u + i;
+    c[i] = __ldg(cs);
+    s[i] = __ldg(cs + rot / 2);
+  }
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn(a[2 * i], a[2 * i + 1], c[i], s[i]);
+      turn(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i], s[i]);
+  }
+}
+
 // ---------------------------------------------------------------- kv_rope_cache
 
 constexpr int kRopeThreads = 256;
@@ -107,8 +143,8 @@ constexpr int kRopeThreads = 256;
 // token's elements, slot and position are loaded before the current token is turned and stored, so
 // that a thread has 32 bytes in flight all the time.  Three CTAs per SM (four spill registers, five more):
 // 65,536 tokens of 32/8 heads at head_dim 128 take 255 us, 5.9 TB/s (280 and 321 us).
-// kPool: 0 e4m3, 1 e5m2, 2 bf16.
-template <int D, int kPool>
+// kPool: 0 e4m3, 1 e5m2, 2 bf16.  kAxes: positions of several axes.
+template <int D, int kPool, bool kAxes>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeCacheParams p, int t_step) {
   after_previous();
   constexpr int U = D / 16;
@@ -126,14 +162,19 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
   const __nv_bfloat16* src = (is_q ? p.q : is_v ? p.v : p.k) + h * D;
   uint8_t* pool = is_v ? p.vc : p.kc;
   const float inv = is_q || kPool == 2 ? 1.f : __frcp_rn((is_v ? p.vs : p.ks)[p.per_head ? h : 0]);
+  const uint32_t axes = kAxes && turned ? unit_axes(p.axes, u) : 0u;
   uint4 xa, xb;
-  long long slot, pos;
+  long long slot, pos, more[3];  // more: of axes 1 .. 3
   auto fetch = [&](long long t) {
     const uint4* x = reinterpret_cast<const uint4*>(src + t * stride);
     xa = x[ca];
     xb = x[cb];
     slot = p.slots[t];
     pos = p.positions[t];
+    if constexpr (kAxes) {
+#pragma unroll
+      for (int x = 0; x < 3; ++x) more[x] = x + 1 < p.axes.count ? p.positions[(x + 1) * p.axes.stride + t] : 0;
+    }
   };
   if (t0 < p.n_tokens) fetch(t0);
   for (long long t = t0; t < p.n_tokens; t += t_step) {
@@ -141,13 +182,26 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
     unpack8(xa, a);
     unpack8(xb, b);
     const long long s = slot, x = pos;
+    bool in_table = x >= 0 && x < p.max_pos;
+    int at_axis[4] = {static_cast<int>(x), 0, 0, 0};
+    if constexpr (kAxes) {
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        in_table = in_table && more[i] >= 0 && more[i] < p.max_pos;
+        at_axis[i + 1] = static_cast<int>(more[i]);
+      }
+    }
     if (t + t_step < p.n_tokens) fetch(t + t_step);
     if (s < 0) continue;
-    if (s >= p.capacity || x < 0 || x >= p.max_pos) {
+    if (s >= p.capacity || !in_table) {
       if (rem == 0) raise_fault(p.fault, s >= p.capacity ? FKV_FAULT_SLOT : FKV_FAULT_POSITION);
       continue;
     }
-    if (turned) turn_unit(a, b, p.cos_sin + x * p.rot, p.rot, u, p.interleaved);
+    if constexpr (kAxes) {
+      if (turned) turn_unit_axes(a, b, p.cos_sin, at_axis, axes, p.rot, u, p.interleaved);
+    } else {
+      if (turned) turn_unit(a, b, p.cos_sin + x * p.rot, p.rot, u, p.interleaved);
+    }
     if (is_q) {
       uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * D);
       dst[ca] = pack8_bf16(a);
@@ -200,7 +254,8 @@ FKV_DEV float pow2_scale(uint32_t amax_bits) {
 // 44 bytes of spills; head_dim 256 has three).  The others turn
 // query rows, four units per thread with all loads up front.  HBM-bound: 4 x 16,384 tokens of 32/8
 // heads at head_dim 128 take 273 us, 5.5 TB/s (three CTAs per SM 289 us; six units per thread 323 us).
-template <int D>
+// kAxes: turned for given positions, of one axis or several, instead of the tokens' places.
+template <int D, bool kAxes>
 __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_kernel(const BlockCacheParams p, int kv_parts) {
   constexpr int U = D / 16;       // units of a row
   constexpr int TP = 32 / U;      // rows that a warp handles at once
@@ -223,7 +278,7 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
     if (first) raise_fault(p.fault, FKV_FAULT_QLEN);
     return;
   }
-  if (p.cos_sin != nullptr && T > p.max_pos && L > 0) {
+  if (!kAxes && p.cos_sin != nullptr && T > p.max_pos && L > 0) {
     if (first) raise_fault(p.fault, FKV_FAULT_POSITION);
     return;
   }
@@ -231,6 +286,21 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
   if (L == 0 || page > (T - 1) >> 4) return;
   const int lo = max(T - L, page * 16), hi = min(T, page * 16 + 16);  // new positions in the page
   const long long row0 = static_cast<long long>(r0) - (T - L);        // row of position x: row0 + x
+  // unit u (values a and b) of the token at place x, turned for its position or positions
+  auto turn_at = [&](float (&a)[8], float (&b)[8], int x, int u) {
+    if constexpr (kAxes) {
+      int pos[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long y = i < p.axes.count ? p.positions[i * p.axes.stride + row0 + x] : 0;
+        pos[i] = static_cast<int>(min(max(y, 0ll), p.max_pos - 1ll));
+        if (y != pos[i]) raise_fault(p.fault, FKV_FAULT_POSITION);
+      }
+      turn_unit_axes(a, b, p.cos_sin, pos, unit_axes(p.axes, u), p.rot, u, p.interleaved);
+    } else {
+      turn_unit(a, b, p.cos_sin + static_cast<long long>(x) * p.rot, p.rot, u, p.interleaved);
+    }
+  };
 
   if (static_cast<int>(blockIdx.z) >= kv_parts) {
     const int items = (hi - lo) * p.Hq * U;
@@ -259,7 +329,7 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
       float a[8], c[8];
       unpack8(xa[j], a);
       unpack8(xb[j], c);
-      if (u < (p.rot >> 4)) turn_unit(a, c, p.cos_sin + static_cast<long long>(pos[j]) * p.rot, p.rot, u, p.interleaved);
+      if (u < (p.rot >> 4)) turn_at(a, c, pos[j], u);
       uint4* dst = reinterpret_cast<uint4*>(p.q_out + (row0 + pos[j]) * p.q_out_stride + h[j] * D);
       dst[ca] = pack8_bf16(a);
       dst[cb] = pack8_bf16(c);
@@ -304,8 +374,7 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
     const int pos = page * 16 + slot0 + r * TP;
     unpack8(xa[r], a[r]);
     unpack8(xb[r], c[r]);
-    if (u < (rot >> 4) && pos >= lo && pos < hi)
-      turn_unit(a[r], c[r], p.cos_sin + static_cast<long long>(pos) * p.rot, p.rot, u, p.interleaved);
+    if (u < (rot >> 4) && pos >= lo && pos < hi) turn_at(a[r], c[r], pos, u);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t x = __float_as_uint(a[r][i]) & 0x7FFFFFFFu, y = __float_as_uint(c[r][i]) & 0x7FFFFFFFu;
@@ -350,22 +419,22 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
   }
 }
 
-template <int D>
+template <int D, bool kAxes>
 cudaError_t launch_rope(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
   const long long per_token = static_cast<long long>(p.Hq + 2 * p.H) * (D / 16);
   // as many tokens at once as three CTAs per SM hold
   const long long t_step = std::min<long long>(p.n_tokens, std::max<long long>(1, 3LL * num_sms * kRopeThreads / per_token));
   const unsigned blocks = static_cast<unsigned>((per_token * t_step + kRopeThreads - 1) / kRopeThreads);
-  auto kern = pool == 2 ? rope_cache_kernel<D, 2> : pool == 1 ? rope_cache_kernel<D, 1> : rope_cache_kernel<D, 0>;
+  auto kern = pool == 2 ? rope_cache_kernel<D, 2, kAxes> : pool == 1 ? rope_cache_kernel<D, 1, kAxes> : rope_cache_kernel<D, 0, kAxes>;
   return launch_dependent(kern, dim3(blocks), dim3(kRopeThreads), 0, s, p, static_cast<int>(t_step));
 }
 
 }  // namespace
 
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
-  if (p.D == 64) return launch_rope<64>(p, pool, num_sms, s);
-  if (p.D == 128) return launch_rope<128>(p, pool, num_sms, s);
-  return launch_rope<256>(p, pool, num_sms, s);
+  auto launch = p.axes.count > 1 ? (p.D == 64 ? launch_rope<64, true> : p.D == 128 ? launch_rope<128, true> : launch_rope<256, true>)
+                                 : (p.D == 64 ? launch_rope<64, false> : p.D == 128 ? launch_rope<128, false> : launch_rope<256, false>);
+  return launch(p, pool, num_sms, s);
 }
 
 cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s) {
@@ -374,7 +443,8 @@ cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s)
   const long long items = static_cast<long long>(std::min(16, p.max_q_len)) * p.Hq * (D / 16);
   const int kv_parts = (2 * p.H + block_tasks(D) - 1) / block_tasks(D);
   const dim3 grid(pages, p.B, static_cast<unsigned>(kv_parts + (items + kQueryItems - 1) / kQueryItems));
-  auto kern = D == 64 ? block_cache_kernel<64> : D == 128 ? block_cache_kernel<128> : block_cache_kernel<256>;
+  auto kern = p.positions ? (D == 64 ? block_cache_kernel<64, true> : D == 128 ? block_cache_kernel<128, true> : block_cache_kernel<256, true>)
+                          : (D == 64 ? block_cache_kernel<64, false> : D == 128 ? block_cache_kernel<128, false> : block_cache_kernel<256, false>);
   return launch_dependent(kern, grid, dim3(kBlockThreads), 0, s, p, kv_parts);
 }
 

@@ -137,6 +137,19 @@ typedef struct {
   int32_t interleaved;
 } fkv_rope;
 
+/* Rotary positions of several axes (time, height and width of image and video tokens), token by token.
+ * positions: device int64, axis a's position of token t at a * axis_stride + t.  Pair i of a head is
+ * turned by the table's entry i at the position of axis pair_axis[i] (host uint8 [rot_dim / 2], each below
+ * num_axes; NULL: axis 0 for all), so that sections of the pairs, pairs dealt out in turns, or any
+ * other assignment serve; frequencies that start anew with every axis are the table's own matter.
+ * 1 <= num_axes <= 4; axis_stride >= 0 (0: every axis the same positions). */
+typedef struct {
+  const int64_t* positions;
+  int64_t axis_stride;
+  int32_t num_axes;
+  const uint8_t* pair_axis; /* host */
+} fkv_axes;
+
 /* Human-readable name of a status code (static string). */
 const char* fkv_status_string(fkv_status status);
 
@@ -236,6 +249,20 @@ fkv_status kv_rope_cache(const void* q, int64_t q_stride, void* q_out, int64_t q
                          fkv_stream_t stream);
 
 /*
+ * kv_rope_cache_axes — kv_rope_cache with positions of several axes.
+ *
+ * As kv_rope_cache, every pair turned for the position of its own axis (see fkv_axes).  A token with a
+ * position outside [0, rope.max_positions) on any axis is skipped and FKV_FAULT_POSITION raised.
+ */
+fkv_status kv_rope_cache_axes(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                              int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, fkv_axes axes, const int64_t* slot_mapping,
+                              int32_t n_tokens, fkv_rope rope, fkv_layer_cache cache, const float* k_scale,
+                              const float* v_scale, fkv_scale_gran gran, int32_t layer,
+                              const uint8_t* skip_layer_mask, int32_t num_layers, int32_t* fault,
+                              fkv_stream_t stream);
+
+/*
  * kv_block_cache — append new tokens to a block-scaled cache, rotary embedding included.
  *
  * Rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of k, v (and q) are the last L_b tokens of
@@ -274,6 +301,22 @@ fkv_status kv_block_cache(const void* q, int64_t q_stride, void* q_out, int64_t 
                           int32_t max_q_len, fkv_rope rope, fkv_block_cache cache,
                           const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
                           int32_t* fault, fkv_stream_t stream);
+
+/*
+ * kv_block_cache_axes — kv_block_cache at positions that the caller names.
+ *
+ * As kv_block_cache with a rotation (rope.cos_sin is not NULL), but row t of k and q is turned for
+ * axes.positions (of one axis or several, see fkv_axes) instead of its place in the cache: tokens of
+ * images, and tokens behind a cache that lost some (kv_block_evict).  Where the tokens are stored goes by
+ * context_lens as before.  A position outside [0, rope.max_positions) is brought to its nearer end and
+ * FKV_FAULT_POSITION raised; T_b is not held against rope.max_positions.
+ */
+fkv_status kv_block_cache_axes(const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                               int32_t num_q_heads, const void* k, int64_t k_stride, const void* v,
+                               int64_t v_stride, int32_t n_tokens, fkv_axes axes, const int32_t* cu_seqlens,
+                               int32_t batch, int32_t max_q_len, fkv_rope rope, fkv_block_cache cache,
+                               const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                               int32_t* fault, fkv_stream_t stream);
 
 /*
  * Workspace bytes fp8_decode_attn needs for these sizes (same argument meaning as

@@ -1,0 +1,119 @@
+"""What the operators for long and shared contexts refuse on the host (no GPU needed): the C entry points before
+anything is enqueued, and the binding."""
+import ctypes
+import os
+
+import numpy as np
+import pytest
+import torch
+
+f = pytest.importorskip("fp8_kv_cache_quant_gb300")
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(f.LIB_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
+    return f.load_library()
+
+
+P = 1 << 20  # an aligned address that no refused call reads
+
+
+def _layer(**kw):
+    a = dict(k=P, v=P, nb=4, bs=16, H=2, D=128, fmt=0)
+    a.update(kw)
+    return f._LayerCache(a["k"], a["v"], a["nb"], a["bs"], a["H"], a["D"], a["fmt"])
+
+
+def _block(**kw):
+    a = dict(k=P, v=P, ks=P, vs=P, nb=4, bs=16, H=2, D=128)
+    a.update(kw)
+    return f._BlockCache(a["k"], a["v"], a["ks"], a["vs"], a["nb"], a["bs"], a["H"], a["D"])
+
+
+def _rope(**kw):
+    a = dict(t=P, n=100, rot=128, il=0)
+    a.update(kw)
+    return f._Rope(a["t"], a["n"], a["rot"], a["il"])
+
+
+_PAIRS = (ctypes.c_uint8 * 64)(*([0] * 32 + [2] * 32))
+
+
+def _pos(**kw):
+    a = dict(pos=P, stride=64, n=3, pair=ctypes.addressof(_PAIRS))
+    a.update(kw)
+    return f._Axes(a["pos"], a["stride"], a["n"], a["pair"])
+
+
+BAD_AXES = [dict(n=0), dict(n=5), dict(n=2), dict(stride=-1), dict(pos=None), dict(pos=P + 4)]
+
+
+def _rope_axes(lib, **kw):
+    a = dict(q=P, qs=1024, qo=2 * P, qos=1024, hq=8, k=P, ks=256, v=P, vs=256, axes=_pos(), slot=P, n=4, rope=_rope(),
+             cache=_layer(), ksc=P, vsc=P, gran=0, layer=0, mask=None, nl=0)
+    a.update(kw)
+    return lib.kv_rope_cache_axes(*a.values(), None, None)
+
+
+def _block_axes(lib, **kw):
+    a = dict(q=P, qs=1024, qo=2 * P, qos=1024, hq=8, k=P, ks=256, v=P, vs=256, n=4, axes=_pos(), cu=P, b=2, mq=4, rope=_rope(),
+             cache=_block(), tab=P, mb=4, ctx=P)
+    a.update(kw)
+    return lib.kv_block_cache_axes(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw", BAD_AXES)
+def test_axes_invalid(lib, kw):
+    assert _rope_axes(lib, axes=_pos(**kw)) == f.INVALID_ARG
+    assert _block_axes(lib, axes=_pos(**kw)) == f.INVALID_ARG
+
+
+def test_axes_other_refusals_and_empty_calls(lib):
+    assert _rope_axes(lib, slot=None) == f.INVALID_ARG and _rope_axes(lib, rope=_rope(rot=24)) == f.UNSUPPORTED
+    assert _block_axes(lib, rope=_rope(t=None, rot=0)) == f.INVALID_ARG      # positions without a rotation
+    assert _block_axes(lib, q=None, qo=None, hq=0, rope=_rope(t=None, rot=0)) == f.INVALID_ARG
+    assert _block_axes(lib, cache=_block(D=96)) == f.UNSUPPORTED
+    assert _rope_axes(lib, n=0) == f.OK and _block_axes(lib, n=0) == f.OK and _block_axes(lib, b=0) == f.OK
+
+
+def test_rope_axes_of_the_binding():
+    t = torch.zeros(9, 64)
+    assert f.Rope(t).pair_args == (None, 0)
+    assert f.Rope.sections(2, 0, 3) == [0, 0, 2, 2, 2]
+    r = f.Rope(t, axes=f.Rope.sections(12, 10, 10))
+    assert r.pair_args[1] == 32 and r.pair_axis.dtype == np.uint8
+    for bad in ([0] * 31, [0] * 33, [4] + [0] * 31, [-1] + [0] * 31, [0.5] * 32, [[0] * 32]):
+        with pytest.raises(ValueError, match="axes names"):
+            f.Rope(t, axes=bad)
+
+
+def _bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def test_compiled_binding_checks_of_axes(lib):
+    b = f.load_binding()
+    i64, t = torch.zeros(5, dtype=torch.int64), torch.zeros(9, 64)
+    pool, s = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.ones(1)
+    rope = f.Rope(t, axes=f.Rope.sections(12, 10, 10))
+    pos = torch.zeros(3, 5, dtype=torch.int64)
+    i32 = torch.zeros(3, dtype=torch.int32)
+    one = dict(q=_bf(5, 4, 64), k=_bf(5, 2, 64), v=_bf(5, 2, 64), pos=pos, slots=i64, cs=t, il=0, ax=rope.pair_args[0], n=rope.pair_args[1],
+               kc=pool, vc=pool, fmt=0, ks=s, vs=s, gran=0, layer=0, mask=None, nl=0, skip=0, qo=None, fault=None)
+    two = dict(k=_bf(5, 2, 64), v=_bf(5, 2, 64), cu=i32, mx=3, kc=pool, vc=pool, ks=torch.ones(3, 2), vs=torch.ones(3, 2),
+               tab=torch.zeros(2, 4, dtype=torch.int32), ctx=i32[:2], cs=t, il=0, ax=rope.pair_args[0], n=rope.pair_args[1], pos=pos, q=None,
+               qo=None, fault=None)
+    for fn, a in ((b.kv_rope_cache_axes, one), (b.kv_block_cache_axes, two)):
+        for match, change in [
+            ("positions is Long", dict(pos=i64)), (r"wanted Long \[axes, 5\]", dict(pos=pos[:, :4])), ("positions is Int", dict(pos=pos.int())),
+            ("consecutive rows", dict(pos=torch.zeros(5, 3, dtype=torch.int64).T)), ("its table has 32", dict(n=31)), ("not a tensor", dict(pos=None)),
+        ]:
+            with pytest.raises(ValueError, match=match):
+                fn(0, *dict(a, **change).values())
+    with pytest.raises(ValueError, match="without a rope"):
+        b.kv_block_cache_axes(0, *dict(two, cs=None, ax=None, n=0, pos=i64).values())
+    with pytest.raises(ValueError, match="takes positions"):
+        f.kv_block_cache(two["k"], two["v"], i32, 3, f.BlockCache(pool, pool, two["ks"], two["vs"]), two["tab"], two["ctx"], rope=rope)
