@@ -36,7 +36,7 @@ EXPORTS = (
     "fp8_decode_attn_num_splits", "fp8_decode_attn", "fkv_prefill_block_n", "fp8_prefill_attn",
     "fp8_decode_attn_noalloc", "fp8_decode_attn_split_blocks", "fkv_decode_block_n", "kv_quant_cache_clips",
     "fp8_decode_step", "fkv_set_decode_wait_limit_ns", "kv_rope_cache", "kv_block_cache",
-    "kv_rope_cache_axes", "kv_block_cache_axes",
+    "kv_rope_cache_axes", "kv_block_cache_axes", "kv_block_evict",
     "fp8_block_decode_attn_workspace_size", "fp8_block_decode_attn", "fp8_block_prefill_attn",
 )
 NOALLOC_WORKSPACE_BYTES = 16 << 20
@@ -137,6 +137,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.fp8_block_prefill_attn.restype = ctypes.c_int
     lib.fp8_block_prefill_attn.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f,
                                            c_i32, c_i32, c_vp, c_vp, c_vp]
+    lib.kv_block_evict.restype = ctypes.c_int
+    lib.kv_block_evict.argtypes = [_BlockCache, c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
+                                   c_vp, c_i32, c_vp, c_vp]
     if path is None:
         _lib = lib
     return lib
@@ -425,6 +428,14 @@ def _current(stream, index):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index))
 
 
+def _allocating(fn, on, stream):
+    """A context in which the device of the tensor `on` and the stream (None: that device's current one) are current."""
+    index = on.get_device()
+    if index < 0:
+        raise ValueError(f"{fn}: the tensors are not on a CUDA device")
+    return torch.cuda.device(index) if stream is None else _current(_stream(stream), index)
+
+
 def _call(fn, on, stream, *args):
     """fn of the compiled binding, with the device of the tensor `on` and the stream current (what the call
     allocates belongs to that stream); stream None: that device's current stream.  Returns its tensor."""
@@ -480,11 +491,8 @@ def fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_
 def block_decode_workspace(batch, num_q_heads, cache: BlockCache, stream=None):
     """A workspace of fp8_block_decode_attn, zero-filled on the stream (calls that may overlap on the GPU each
     need one)."""
-    index = cache.k_cache.get_device()
-    if index < 0:
-        raise ValueError("fp8_block_decode_attn: the tensors are not on a CUDA device")
     _, h, _, d = cache.k_cache.shape
-    with torch.cuda.device(index) if stream is None else _current(_stream(stream), index):
+    with _allocating("fp8_block_decode_attn", cache.k_cache, stream):
         n = fp8_block_decode_attn_workspace_size(batch, num_q_heads, h, d)
         return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k_cache.device)
 
@@ -504,3 +512,23 @@ def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_
     """Ragged chunks of queries (rows cu_seqlens_q[b] .. of q bf16 [total][Hq][D]) over a block-scaled cache."""
     return _call("fp8_block_prefill_attn", q, stream, q, cu_seqlens_q, max_q_len, cache.k_cache, cache.v_cache, cache.k_scale,
                  cache.v_scale, block_table, context_lens, softmax_scale, causal, window, out, fault)
+
+
+# ------------------------------------------------------------------ long and shared contexts
+
+def kv_block_evict(cache: BlockCache, block_table, context_lens, weights, budget, new_table, sink=0, recent=0, new_weights=None,
+                   new_lens=None, kept=None, fault=None, stream=None):
+    """Cut every sequence to min(T, budget) tokens per KV head: the first ``sink``, the last ``recent`` and, of the others,
+    those with the largest ``weights`` (float32 [batch][Hkv][>= T], equal ones by index), copied in order to the blocks
+    of ``new_table`` (none of them read by the call).  Returns (new_lens int32 [batch], kept int32 [batch][Hkv][budget]:
+    the kept tokens' old indices, then -1); their weights go to ``new_weights`` when given."""
+    dev = cache.k_cache.device
+    if new_lens is None or kept is None:
+        with _allocating("kv_block_evict", cache.k_cache, stream):
+            if new_lens is None:
+                new_lens = torch.empty(block_table.shape[0], dtype=torch.int32, device=dev)
+            if kept is None:
+                kept = torch.empty(block_table.shape[0], cache.k_cache.shape[1], budget, dtype=torch.int32, device=dev)
+    _call("kv_block_evict", cache.k_cache, stream, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
+          context_lens, weights, budget, sink, recent, new_table, new_weights, new_lens, kept, fault)
+    return new_lens, kept

@@ -709,4 +709,50 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+fkv_status kv_block_evict(fkv_block_cache cache, const int32_t* block_table, int32_t batch, int32_t max_blocks,
+                          const int32_t* context_lens, const float* weights, int32_t weights_len, int32_t budget,
+                          int32_t sink, int32_t recent, const int32_t* new_table, int32_t new_max_blocks, int32_t* new_lens,
+                          int32_t* kept, float* new_weights, int32_t new_weights_len, int32_t* fault, fkv_stream_t stream) {
+  if (batch < 0 || max_blocks <= 0 || weights_len < 0 || new_max_blocks < 0 || new_weights_len < 0) return FKV_INVALID_ARG;
+  if (budget < 1 || sink < 0 || recent < 0 || recent > budget || sink > budget - recent) return FKV_INVALID_ARG;
+  const fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (batch > 65535 || cache.num_kv_heads > 8192 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
+  const long long most = std::min({static_cast<long long>(budget), max_blocks * 16LL, static_cast<long long>(weights_len)});
+  if (most > new_max_blocks * 16LL || (new_weights && most > new_weights_len)) return FKV_INVALID_ARG;
+  // the kernels' grids
+  if (static_cast<long long>(batch) * cache.num_kv_heads * ((most + 15) / 16 + 8) > INT32_MAX) return FKV_UNSUPPORTED;
+  if (batch == 0) return FKV_OK;
+  if (!valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!block_table || !context_lens || !weights || !new_table || !new_lens || !kept || !aligned(block_table, 4) ||
+      !aligned(context_lens, 4) || !aligned(weights, 4) || !aligned(new_table, 4) || !aligned(new_lens, 4) ||
+      !aligned(kept, 4) || !aligned(new_weights, 4))
+    return FKV_INVALID_ARG;
+  fkv::EvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.kc = static_cast<uint8_t*>(cache.k_cache);
+  p.vc = static_cast<uint8_t*>(cache.v_cache);
+  p.ks = cache.k_scale;
+  p.vs = cache.v_scale;
+  p.B = batch;
+  p.H = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.new_max_blocks = new_max_blocks;
+  p.block_table = block_table;
+  p.ctx = context_lens;
+  p.weights = weights;
+  p.weights_len = weights_len;
+  p.new_weights_len = new_weights_len;
+  p.budget = budget;
+  p.sink = sink;
+  p.recent = recent;
+  p.new_table = new_table;
+  p.new_lens = new_lens;
+  p.kept = kept;
+  p.new_weights = new_weights;
+  p.fault = fault;
+  return from_cuda(fkv::launch_block_evict(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -332,6 +332,36 @@ PyObject* fp8_block_prefill_attn_(Args a) {
   return result(st, out);
 }
 
+// stream, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, weights, budget, sink, recent, new_table, new_weights,
+// new_lens, kept, fault
+PyObject* kv_block_evict_(Args a) {
+  void* stream = a.pointer();
+  const Tensor kc = a.tensor("k_cache");
+  --a.i;
+  if (kc.dim() != 4) refuse(a.fn, "k_cache is " + text(kc) + "; wanted [blocks][heads][16][head_dim]");
+  const at::Device dev = kc.device();
+  const fkv_block_cache c = block_cache(a, -1, kc.size(3), dev);
+  const Tensor table = a.tensor("block_table"), ctx = a.tensor("context_lens"), weights = a.tensor("weights");
+  const int32_t budget = a.i32(), sink = a.i32(), recent = a.i32();
+  const Tensor new_table = a.tensor("new_table"), new_weights = a.tensor("new_weights", true), new_lens = a.tensor("new_lens"),
+               kept = a.tensor("kept"), fault = a.tensor("fault", true);
+  a.done();
+  if (table.dim() != 2) refuse(a.fn, "block_table is " + text(table) + "; wanted [batch][blocks]");
+  if (new_table.dim() != 2) refuse(a.fn, "new_table is " + text(new_table) + "; wanted [batch][blocks]");
+  if (weights.dim() != 3) refuse(a.fn, "weights is " + text(weights) + "; wanted [batch][heads][tokens]");
+  if (new_weights.defined() && new_weights.dim() != 3) refuse(a.fn, "new_weights is " + text(new_weights) + "; wanted [batch][heads][tokens]");
+  const int64_t b = table.size(0), h = c.num_kv_heads, len = weights.size(2), new_len = new_weights.defined() ? new_weights.size(2) : 0;
+  const fkv_status st = kv_block_evict(
+      c, fits<int32_t>(a.fn, "block_table", table, at::kInt, table.sizes(), dev), small(a.fn, b), small(a.fn, table.size(1)),
+      fits<int32_t>(a.fn, "context_lens", ctx, at::kInt, {b}, dev), fits<float>(a.fn, "weights", weights, at::kFloat, {b, h, len}, dev),
+      small(a.fn, len), budget, sink, recent, fits<int32_t>(a.fn, "new_table", new_table, at::kInt, {b, new_table.size(1)}, dev),
+      small(a.fn, new_table.size(1)), fits<int32_t>(a.fn, "new_lens", new_lens, at::kInt, {b}, dev),
+      fits<int32_t>(a.fn, "kept", kept, at::kInt, {b, h, budget}, dev),
+      fits<float>(a.fn, "new_weights", new_weights, at::kFloat, {b, h, new_len}, dev), small(a.fn, new_len),
+      fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev), static_cast<fkv_stream_t>(stream));
+  return result(st, Tensor());
+}
+
 PyObject* kv_rope_cache_(Args a) { return rope_cache<false>(a); }
 PyObject* kv_rope_cache_axes_(Args a) { return rope_cache<true>(a); }
 PyObject* kv_block_cache_(Args a) { return block_cache_append<false>(a); }
@@ -357,13 +387,14 @@ FKV_ENTRY(kv_rope_cache)
 FKV_ENTRY(kv_block_cache)
 FKV_ENTRY(kv_rope_cache_axes)
 FKV_ENTRY(kv_block_cache_axes)
+FKV_ENTRY(kv_block_evict)
 FKV_ENTRY(fp8_block_decode_attn)
 FKV_ENTRY(fp8_block_prefill_attn)
 #undef FKV_ENTRY
 
 #define FKV_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name##_py)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FKV_METHOD(kv_rope_cache), FKV_METHOD(kv_block_cache), FKV_METHOD(kv_rope_cache_axes),
-                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(fp8_block_decode_attn),
+                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(kv_block_evict), FKV_METHOD(fp8_block_decode_attn),
                          FKV_METHOD(fp8_block_prefill_attn), {nullptr, nullptr, 0, nullptr}};
 #undef FKV_METHOD
 

@@ -28,6 +28,13 @@ FKV_DEV uint32_t f32x4_to_e4m3x4(float2 a, float2 b) {
   return r;
 }
 
+// The smallest power of two s >= 2^-126 with amax <= 448 s, from amax's bits: 448 = 1.75 * 2^8.
+FKV_DEV float pow2_scale(uint32_t amax_bits) {
+  const int e = static_cast<int>(amax_bits >> 23) - 127;
+  const int k = e - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return __uint_as_float(static_cast<uint32_t>(max(k, -126) + 127) << 23);
+}
+
 // A query row enters the products scaled by 2^-k, its largest magnitude (float32 bits `amax`, finite) in (224, 448], as
 // two e4m3 terms.
 FKV_DEV int query_exponent(uint32_t amax) {
@@ -181,6 +188,24 @@ struct BlockCacheParams {
 };
 
 cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s);
+
+struct EvictParams {
+  uint8_t *kc, *vc;
+  float *ks, *vs;                             // [num_blocks][H]
+  int B, H, num_blocks, max_blocks, new_max_blocks;
+  const int32_t* block_table;                 // [B][max_blocks]
+  const int32_t* ctx;                         // [B]
+  const float* weights;                       // [B][H][weights_len]
+  int weights_len, new_weights_len;
+  int budget, sink, recent;
+  const int32_t* new_table;                   // [B][new_max_blocks]
+  int32_t* new_lens;                          // [B]
+  int32_t* kept;                              // [B][H][budget]
+  float* new_weights;                         // [B][H][new_weights_len] or null
+  int32_t* fault;
+};
+
+cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStream_t s);
 
 struct BlockPrefillParams {
   const __nv_bfloat16* q;

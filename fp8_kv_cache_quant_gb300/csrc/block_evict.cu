@@ -1,0 +1,350 @@
+// Eviction from a block-scaled cache by accumulated attention weight: per (sequence, KV head) the
+// tokens that stay are found (evict_select_kernel), then copied to the sequence's new blocks with
+// scales of their own (evict_gather_kernel).
+//
+// Selection.  Of T weights the n = min(T, budget) largest stay, equal ones by ascending index; the first
+// `sink` and the last `recent` tokens count as larger than any weight.  Weights become 32-bit keys that order
+// like the numbers (NaN below everything), and the n-th largest key is found digit by digit, from the top, 11, 11 and 10
+// bits, with a histogram of the keys that share the digits found so far: three counts of T keys whatever the weights are.
+// A second walk in index order numbers the kept ones.
+// A unit (sequence, KV head) is a cluster of CTAs, each with a consecutive share of its keys in shared memory (so that
+// the weights are read from HBM once), whose histograms meet through distributed shared memory.
+//
+// Copy.  A warp per (new block, KV head): 16 kept tokens' K and V rows from anywhere, their largest finite
+// magnitude, the block's new scale as an append of the same values to an empty block would choose it, the codes brought to it.
+#include "block_common.cuh"
+
+namespace fkv {
+namespace {
+
+constexpr int kSelectThreads = 1024;
+constexpr int kBins = 2048;
+constexpr int kMaxResident = 49152;  // keys of a CTA held in shared memory, at most (192 KB)
+
+FKV_DEV uint32_t rank_in_cluster() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+FKV_DEV uint32_t ctas_of_cluster() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every CTA of the cluster: earlier writes of all are visible behind it.
+FKV_DEV void sync_cluster() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+FKV_DEV int peer_int(const int* p, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// A key that orders like the weight, NaN below all; tokens that always stay take the top one, which no weight has.
+constexpr uint32_t kSure = 0xFFFFFFFFu;
+FKV_DEV uint32_t key_of(float w) {
+  if (w != w) return 0u;
+  const uint32_t u = __float_as_uint(w + 0.f);  // (-0 is 0)
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct SelectShared {
+  int hist[3][kBins];
+  int warp_sum[32], warp_eq[32];
+  int digit, left;       // of the last histogram: the digit, and what is to be taken of it
+  int gt, eq;            // this CTA's keys above the threshold, and equal to it
+};
+
+__global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const EvictParams p, int resident_keys) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  SelectShared& sh = *reinterpret_cast<SelectShared*>(smem);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(SelectShared));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = static_cast<int>(ctas_of_cluster()), rank = static_cast<int>(rank_in_cluster());
+  for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int unit = blockIdx.x / C;
+  const int b = unit / p.H, h = unit - b * p.H;
+  const long long most = min(p.max_blocks * 16LL, static_cast<long long>(p.weights_len));
+  int T = p.ctx[b];
+  if (T < 0 || T > most) {
+    if (h == 0 && rank == 0 && tid == 0) raise_fault(p.fault, FKV_FAULT_CONTEXT);
+    T = T < 0 ? 0 : static_cast<int>(most);
+  }
+  const int n = min(T, p.budget);
+  if (h == 0 && rank == 0 && tid == 0) p.new_lens[b] = n;
+  int32_t* kept = p.kept + static_cast<size_t>(unit) * p.budget;
+  const float* weights = p.weights + static_cast<size_t>(unit) * p.weights_len;
+  float* moved = p.new_weights ? p.new_weights + static_cast<size_t>(unit) * p.new_weights_len : nullptr;
+  const int all = C * kSelectThreads, me = rank * kSelectThreads + tid;
+  for (int i = n + me; i < p.budget; i += all) kept[i] = -1;
+  if (T <= p.budget) {  // (the whole cluster)
+    for (int i = me; i < n; i += all) {
+      kept[i] = i;
+      if (moved) moved[i] = weights[i];
+    }
+    return;
+  }
+  // this CTA's keys [lo, hi), of which warp w walks [wlo, whi), 32 at a time
+  const int seg = ((T + C - 1) / C + 31) & ~31;
+  const int lo = min(rank * seg, T), hi = min(lo + seg, T);
+  const bool resident = seg <= resident_keys;
+  auto key_at = [&](int i) -> uint32_t {
+    if (i < p.sink || i >= T - p.recent) return kSure;
+    return key_of(weights[i]);
+  };
+  __syncthreads();
+  if (resident) {
+    for (int i = lo + tid; i < hi; i += kSelectThreads) {
+      const uint32_t k = key_at(i);
+      keys[i - lo] = k;
+      atomicAdd(&sh.hist[0][k >> 21], 1);
+    }
+  } else {
+    for (int i = lo + tid; i < hi; i += kSelectThreads) atomicAdd(&sh.hist[0][key_at(i) >> 21], 1);
+  }
+  auto get = [&](int i) -> uint32_t { return resident ? keys[i - lo] : key_at(i); };
+  int left = n;        // keys to take among those that share the digits found so far
+  uint32_t found = 0;  // these digits
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    if (pass > 0) {
+      for (int i = lo + tid; i < hi; i += kSelectThreads) {
+        const uint32_t k = get(i);
+        if (pass == 1 && k >> 21 == found) atomicAdd(&sh.hist[1][k >> 10 & 2047u], 1);
+        if (pass == 2 && k >> 10 == found) atomicAdd(&sh.hist[2][k & 1023u], 1);
+      }
+    }
+    if (C > 1) sync_cluster();
+    else __syncthreads();
+    // thread t: the t-th pair of bins from the top
+    const int hi_bin = kBins - 1 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    if (C > 1) {
+      for (int r = 0; r < C; ++r) {
+        c0 += peer_int(&sh.hist[pass][hi_bin], r);
+        c1 += peer_int(&sh.hist[pass][hi_bin - 1], r);
+      }
+    } else {
+      c0 = sh.hist[pass][hi_bin];
+      c1 = sh.hist[pass][hi_bin - 1];
+    }
+    int upto = c0 + c1;  // inclusive sums over the threads
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += x;
+    }
+    if (lane == 31) sh.warp_sum[warp] = upto;
+    __syncthreads();
+    int before = upto - c0 - c1;
+    {
+      const int x = lane < warp ? sh.warp_sum[lane] : 0;
+      before += __reduce_add_sync(0xffffffffu, x);
+    }
+    if (before < left && left <= before + c0) {
+      sh.digit = hi_bin;
+      sh.left = left - before;
+    } else if (before + c0 < left && left <= before + c0 + c1) {
+      sh.digit = hi_bin - 1;
+      sh.left = left - before - c0;
+    }
+    __syncthreads();
+    found = pass < 2 ? found << 11 | sh.digit : found << 10 | sh.digit;
+    left = sh.left;
+  }
+  // of the keys equal to the threshold `found` the first `left` stay
+  const int wseg = (((hi - lo + 31) / 32) + 31) & ~31;
+  const int wlo = min(lo + warp * wseg, hi), whi = min(wlo + wseg, hi);
+  int gt = 0, eq = 0;
+  for (int i0 = wlo; i0 < whi; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < whi ? get(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < whi && k > found));
+    eq += __popc(__ballot_sync(0xffffffffu, i < whi && k == found));
+  }
+  if (lane == 0) {
+    sh.warp_sum[warp] = gt;
+    sh.warp_eq[warp] = eq;
+  }
+  __syncthreads();
+  int gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0);
+  int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_eq[lane] : 0);
+  if (C > 1) {
+    if (tid == kSelectThreads - 1) {
+      sh.gt = gt_before + gt;
+      sh.eq = eq_before + eq;
+    }
+    sync_cluster();
+    for (int r = 0; r < rank; ++r) {
+      gt_before += peer_int(&sh.gt, r);
+      eq_before += peer_int(&sh.eq, r);
+    }
+  }
+  int at = gt_before + min(eq_before, left);
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = wlo; i0 < whi; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < whi ? get(i) : 0u;
+    const bool is_eq = i < whi && k == found;
+    const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
+    const bool keep = i < whi && (k > found || (is_eq && eq_before + __popc(eqs & below) < left));
+    const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
+    if (keep) {
+      const int to = at + __popc(keeps & below);
+      kept[to] = i;
+      if (moved) moved[to] = weights[i];
+    }
+    at += __popc(keeps);
+    eq_before += __popc(eqs);
+  }
+  if (C > 1) sync_cluster();  // no CTA leaves while another reads its shared memory
+}
+
+constexpr int kGatherThreads = 256;
+
+// 16 codes as float32 values times s (rounded to float32), four per word.
+FKV_DEV void values4(uint32_t w, float s, float (&x)[4]) {
+  uint32_t h01, h23;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"(static_cast<uint16_t>(w >> 16)));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h23));
+  x[0] = __fmul_rn(a.x, s);
+  x[1] = __fmul_rn(a.y, s);
+  x[2] = __fmul_rn(b.x, s);
+  x[3] = __fmul_rn(b.y, s);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictParams p, int blocks) {
+  constexpr int CPR = D / 16;          // 16-byte chunks of a row
+  constexpr int N = 16 * CPR / 32;     // chunks per lane of K, and of V
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long item = static_cast<long long>(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5);
+  const int h = static_cast<int>(item % p.H);
+  const long long rest = item / p.H;
+  const int blk = static_cast<int>(rest % blocks);
+  const int b = static_cast<int>(rest / blocks);
+  if (b >= p.B) return;
+  const int n = p.new_lens[b] - 16 * blk;  // rows of the block
+  if (n <= 0) return;
+  const int dst = p.new_table[static_cast<size_t>(b) * p.new_max_blocks + blk];
+  // lane r < 16: row r's place and scales
+  int src = 0, slot = 0;
+  float ks = 0.f, vs = 0.f;
+  if (lane < min(n, 16)) {
+    const int t = p.kept[(static_cast<size_t>(b) * p.H + h) * p.budget + 16 * blk + lane];
+    int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + (t >> 4)];
+    if (id < 0 || id >= p.num_blocks) {
+      raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+      id = 0;
+    }
+    src = id;
+    slot = t & 15;
+    const size_t at = static_cast<size_t>(id) * p.H + h;
+    ks = p.ks[at];
+    vs = p.vs[at];
+  }
+  if (dst < 0 || dst >= p.num_blocks) {
+    if (lane == 0) raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+    return;
+  }
+  uint4 k[N], v[N];
+  float sk[N], sv[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int c = lane + 32 * j, row = c / CPR;
+    const int id = __shfl_sync(0xffffffffu, src, row), s = __shfl_sync(0xffffffffu, slot, row);
+    sk[j] = __shfl_sync(0xffffffffu, ks, row);
+    sv[j] = __shfl_sync(0xffffffffu, vs, row);
+    k[j] = v[j] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < n) {
+      const size_t at = ((static_cast<size_t>(id) * p.H + h) * 16 + s) * CPR + c % CPR;
+      k[j] = reinterpret_cast<const uint4*>(p.kc)[at];
+      v[j] = reinterpret_cast<const uint4*>(p.vc)[at];
+    }
+  }
+  const size_t at = static_cast<size_t>(dst) * p.H + h;
+  auto store = [&](uint4 (&x)[N], const float (&s)[N], uint8_t* pool, float* scale) {
+    uint32_t amax = 0;  // bits of the largest finite magnitude
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y[4];
+        values4(w[i], s[j], y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+          if (m < 0x7F800000u) amax = max(amax, m);
+        }
+      }
+    }
+    amax = __reduce_max_sync(0xffffffffu, amax);
+    const float to = pow2_scale(amax);
+    const float inv = __frcp_rn(to);
+    if (lane == 0) scale[at] = to;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float y[4];
+        values4(w[i], s[j], y);
+        w[i] = f32x4_to_e4m3x4(make_float2(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv)),
+                               make_float2(__fmul_rn(y[2], inv), __fmul_rn(y[3], inv)));
+      }
+      const int c = lane + 32 * j;
+      if (c / CPR < n) reinterpret_cast<uint4*>(pool)[at * 16 * CPR + c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  };
+  store(k, sk, p.kc, p.ks);
+  store(v, sv, p.vc, p.vs);
+}
+
+}  // namespace
+
+cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStream_t s) {
+  const long long most = std::min(p.max_blocks * 16LL, static_cast<long long>(p.weights_len));
+  const long long units = static_cast<long long>(p.B) * p.H;
+  // clusters while SMs would idle and a CTA has more keys than its threads take at once
+  int C = 1;
+  while (C < 8 && 2 * C * units <= 2LL * num_sms && most / C > 4 * kSelectThreads) C *= 2;
+  const long long seg = ((most + C - 1) / C + 31) & ~31LL;
+  const int resident = static_cast<int>(std::min<long long>(seg, kMaxResident));
+  const size_t smem = sizeof(SelectShared) + 4 * static_cast<size_t>(resident);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sizeof(SelectShared) + 4 * static_cast<size_t>(kMaxResident)));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units * C));
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute a[2];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  a[1].id = cudaLaunchAttributeClusterDimension;
+  a[1].val.clusterDim.x = C;
+  a[1].val.clusterDim.y = a[1].val.clusterDim.z = 1;
+  cfg.attrs = a;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, resident);
+  if (e != cudaSuccess) return e;
+  const int blocks = static_cast<int>((std::min<long long>(most, p.budget) + 15) / 16);
+  if (blocks == 0) return cudaSuccess;
+  const long long items = units * blocks;
+  const unsigned grid = static_cast<unsigned>((items + kGatherThreads / 32 - 1) / (kGatherThreads / 32));
+  auto kern = D == 64 ? evict_gather_kernel<64> : D == 128 ? evict_gather_kernel<128> : evict_gather_kernel<256>;
+  return launch_dependent(kern, dim3(grid), dim3(kGatherThreads), 0, s, p, blocks);
+}
+
+}  // namespace fkv

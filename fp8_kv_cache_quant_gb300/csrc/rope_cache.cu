@@ -240,13 +240,6 @@ FKV_DEV uint32_t rescale4(uint32_t w, float r) {
          (static_cast<uint32_t>(f32x2_to_e4m3x2(__fmul_rn(b.x, r), __fmul_rn(b.y, r))) << 16);
 }
 
-// The smallest power of two s >= 2^-126 with amax <= 448 s, from amax's bits: 448 = 1.75 * 2^8.
-FKV_DEV float pow2_scale(uint32_t amax_bits) {
-  const int e = static_cast<int>(amax_bits >> 23) - 127;
-  const int k = e - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return __uint_as_float(static_cast<uint32_t>(max(k, -126) + 127) << 23);
-}
-
 // grid (pages of a sequence's new tokens, sequences, kv_parts + slices of the query rows).
 // CTAs z < kv_parts: K and V of one block, two (head_dim 256: four) warps per (KV head, K or V), which
 // share its 16 rows: the rows stay in registers between the maximum and the codes, so that each

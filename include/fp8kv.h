@@ -578,6 +578,40 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
                                   const int32_t* context_lens, float softmax_scale, int32_t causal,
                                   int32_t window, void* out, int32_t* fault, fkv_stream_t stream);
 
+/*
+ * kv_block_evict — cut the sequences of a block-scaled cache to the tokens that matter.
+ *
+ * Of sequence b's T_b = context_lens[b] tokens every KV head keeps n_b = min(T_b, budget): its first `sink`
+ * and its last `recent` tokens, and of the others those with the largest weights (equal weights: the lower index; a
+ * NaN is below every weight).  The kept tokens, in their order, become the tokens 0 .. n_b - 1 of the
+ * sequence in the blocks of new_table: heads keep different tokens, all the same number.  Keys keep the
+ * rotation that they were stored with, so later tokens are appended at positions that the caller
+ * names (kv_block_cache_axes).  A new block's K (and V) of a head are stored as kv_block_cache stores the
+ * values fl32(code * scale) in an empty block: the smallest power of two that holds their largest
+ * finite magnitude is the scale, so that a kept value changes only where it falls below a subnormal step.
+ *
+ *   cache         source and target; blocks that new_table's first ceil(n_b / 16) columns name are written, and must be
+ *                 different from one another and from every block that a sequence of the call reads.
+ *                 Sequences may share source blocks
+ *   block_table, max_blocks, context_lens  the sequences as they are
+ *   weights       device float32 [batch][num_kv_heads][weights_len], token t's at [b][g][t] (as
+ *                 fp8_block_attn_weights writes them)
+ *   budget        >= 1; sink, recent >= 0, sink + recent <= budget
+ *   new_table     device int32 [batch][new_max_blocks]
+ *   new_lens      device int32 [batch], written: n_b
+ *   kept          device int32 [batch][num_kv_heads][budget], written: the kept tokens' old indices, ascending, then -1
+ *   new_weights   device float32 [batch][num_kv_heads][new_weights_len] or NULL: the kept tokens'
+ *                 weights are written to it, the rest keeps its values; it must not overlap weights
+ * min(budget, 16 max_blocks, weights_len) must be at most 16 new_max_blocks and new_weights_len.  T_b outside
+ * [0, min(16 max_blocks, weights_len)] is clamped (FKV_FAULT_CONTEXT); a source block id out of range reads
+ * block 0, a target id out of range skips the block (FKV_FAULT_BLOCK_ID).  Slots behind n_b keep their bytes.
+ */
+fkv_status kv_block_evict(fkv_block_cache cache, const int32_t* block_table, int32_t batch, int32_t max_blocks,
+                          const int32_t* context_lens, const float* weights, int32_t weights_len,
+                          int32_t budget, int32_t sink, int32_t recent, const int32_t* new_table,
+                          int32_t new_max_blocks, int32_t* new_lens, int32_t* kept, float* new_weights,
+                          int32_t new_weights_len, int32_t* fault, fkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

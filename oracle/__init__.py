@@ -18,8 +18,9 @@ Modules and the passages they follow:
 
   blockcache the rotary position embedding and the block-scaled cache: append with
              power-of-two scales per block and KV head, and the plain softmax over it
+  longcontext  the attention weight that cached keys receive, and eviction by it
 
 Every function is pinned by tests in ``tests/test_oracle_*.py`` against closed forms,
 brute force, invariants or library routines; none is "parity unpinned".
 """
-from . import e4m3, kvcache, attention, blockcache  # noqa: F401
+from . import e4m3, kvcache, attention, blockcache, longcontext  # noqa: F401

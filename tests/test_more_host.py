@@ -117,3 +117,48 @@ def test_compiled_binding_checks_of_axes(lib):
         b.kv_block_cache_axes(0, *dict(two, cs=None, ax=None, n=0, pos=i64).values())
     with pytest.raises(ValueError, match="takes positions"):
         f.kv_block_cache(two["k"], two["v"], i32, 3, f.BlockCache(pool, pool, two["ks"], two["vs"]), two["tab"], two["ctx"], rope=rope)
+
+
+# ------------------------------------------------------------------ eviction
+
+def _evict(lib, **kw):
+    a = dict(cache=_block(), tab=P, b=2, mb=8, ctx=P, w=P, wl=128, budget=32, sink=4, recent=8, nt=P, nmb=2, nl=P, kept=P, nw=P, nwl=32)
+    a.update(kw)
+    return lib.kv_block_evict(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(b=-1), dict(mb=0), dict(wl=-1), dict(nmb=-1), dict(nwl=-1), dict(budget=0), dict(sink=-1), dict(recent=-1), dict(sink=25),
+    dict(recent=33), dict(recent=2 ** 31 - 1, sink=2 ** 31 - 1), dict(nmb=1), dict(nwl=31), dict(tab=None), dict(ctx=None), dict(w=None),
+    dict(nt=None), dict(nl=None), dict(kept=None), dict(tab=P + 2), dict(w=P + 1), dict(nw=P + 2), dict(kept=P + 3),
+    dict(cache=_block(k=None)), dict(cache=_block(vs=P + 2)), dict(cache=_block(nb=0)), dict(cache=_block(H=0)), dict(cache=_block(bs=0)),
+])
+def test_evict_invalid(lib, kw):
+    assert _evict(lib, **kw) == f.INVALID_ARG
+
+
+def test_evict_unsupported_and_empty(lib):
+    assert _evict(lib, cache=_block(D=96)) == f.UNSUPPORTED and _evict(lib, cache=_block(bs=32)) == f.UNSUPPORTED
+    assert _evict(lib, b=65536) == f.UNSUPPORTED and _evict(lib, mb=1 << 27) == f.UNSUPPORTED
+    assert _evict(lib, b=65535, cache=_block(H=8192)) == f.UNSUPPORTED
+    assert _evict(lib, b=0) == f.OK and _evict(lib, b=0, nw=None, nwl=0) == f.OK
+
+
+def test_compiled_binding_checks_of_evict(lib):
+    b = f.load_binding()
+    pool, sc, i32 = torch.zeros(9, 2, 16, 64, dtype=torch.uint8), torch.ones(9, 2), torch.zeros(2, dtype=torch.int32)
+    tab = torch.zeros(2, 4, dtype=torch.int32)
+    a = dict(kc=pool, vc=pool, ks=sc, vs=sc, tab=tab, ctx=i32, w=torch.zeros(2, 2, 64), budget=20, sink=0, recent=0, nt=tab[:, :2].contiguous(),
+             nw=torch.zeros(2, 2, 32), nl=i32, kept=torch.zeros(2, 2, 20, dtype=torch.int32), fault=None)
+    for match, change in [
+        ("k_cache is", dict(kc=pool[0])), ("v_scale", dict(vs=sc.T.contiguous())), ("block_table", dict(tab=tab[0])), ("context_lens", dict(ctx=i32[:1])),
+        ("weights is Double", dict(w=torch.zeros(2, 2, 64).double())), (r"weights is .* \[2, 3, 64\]", dict(w=torch.zeros(2, 3, 64))),
+        ("weights is .*not contiguous", dict(w=torch.zeros(2, 64, 2).transpose(1, 2))), ("weights is", dict(w=torch.zeros(4, 64))),
+        ("new_table", dict(nt=tab[:1])), ("new_table", dict(nt=tab[0])), ("new_weights", dict(nw=torch.zeros(1, 2, 32))), ("new_weights", dict(nw=torch.zeros(32))),
+        ("new_lens", dict(nl=i32.long())), ("kept", dict(kept=torch.zeros(2, 2, 19, dtype=torch.int32))), ("kept", dict(budget=-1)),
+        ("fault", dict(fault=i32)), ("32 bits", dict(sink=1 << 40)), ("not a tensor", dict(nl=None)),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            b.kv_block_evict(0, *dict(a, **change).values())
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        f.kv_block_evict(f.BlockCache(pool, pool, sc, sc), tab, i32, a["w"], 20, tab)
