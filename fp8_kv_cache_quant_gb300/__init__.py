@@ -37,6 +37,7 @@ EXPORTS = (
     "fp8_decode_attn_noalloc", "fp8_decode_attn_split_blocks", "fkv_decode_block_n", "kv_quant_cache_clips",
     "fp8_decode_step", "fkv_set_decode_wait_limit_ns", "kv_rope_cache", "kv_block_cache",
     "kv_rope_cache_axes", "kv_block_cache_axes", "kv_block_evict",
+    "fp8_block_attn_weights_workspace_size", "fp8_block_attn_weights",
     "fp8_block_decode_attn_workspace_size", "fp8_block_decode_attn", "fp8_block_prefill_attn",
 )
 NOALLOC_WORKSPACE_BYTES = 16 << 20
@@ -140,6 +141,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kv_block_evict.restype = ctypes.c_int
     lib.kv_block_evict.argtypes = [_BlockCache, c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
                                    c_vp, c_i32, c_vp, c_vp]
+    lib.fp8_block_attn_weights_workspace_size.restype = c_sz
+    lib.fp8_block_attn_weights_workspace_size.argtypes = [c_i32] * 7
+    lib.fp8_block_attn_weights.restype = ctypes.c_int
+    lib.fp8_block_attn_weights.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_f, c_f, c_vp,
+                                           c_i32, c_vp, c_sz, c_vp, c_vp]
     if path is None:
         _lib = lib
     return lib
@@ -515,6 +521,31 @@ def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_
 
 
 # ------------------------------------------------------------------ long and shared contexts
+
+def fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, max_blocks) -> int:
+    return int(load_library().fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                                                    head_dim, max_blocks))
+
+
+def attn_weights_workspace(batch, total_q, max_q_len, num_q_heads, cache: BlockCache, max_blocks, stream=None):
+    """A workspace of fp8_block_attn_weights (calls that may overlap on the GPU each need one)."""
+    _, h, _, d = cache.k_cache.shape
+    with _allocating("fp8_block_attn_weights", cache.k_cache, stream):
+        n = fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, h, d, max_blocks)
+        return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k_cache.device)
+
+
+def fp8_block_attn_weights(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_table, context_lens, weights, softmax_scale=0.0,
+                           decay=1.0, workspace=None, fault=None, stream=None):
+    """Add to ``weights`` (float32 [batch][Hkv][>= T]) the softmax weight that each key of a block-scaled cache receives from
+    the chunk's queries (the last tokens of their sequences; rows cu_seqlens_q[b] .. of q bf16 [total][Hq][D]), summed over the
+    queries and a group's heads: decay * before + new for older keys (decay 0: what was there is not read), new for the
+    chunk's own.  ``workspace``: of attn_weights_workspace (None: made for the call).  Returns weights."""
+    if workspace is None:
+        workspace = attn_weights_workspace(block_table.shape[0], q.shape[0], max_q_len, q.shape[1], cache, block_table.shape[1], stream)
+    return _call("fp8_block_attn_weights", q, stream, q, cu_seqlens_q, max_q_len, cache.k_cache, cache.v_cache, cache.k_scale,
+                 cache.v_scale, block_table, context_lens, weights, softmax_scale, decay, workspace, fault)
+
 
 def kv_block_evict(cache: BlockCache, block_table, context_lens, weights, budget, new_table, sink=0, recent=0, new_weights=None,
                    new_lens=None, kept=None, fault=None, stream=None):

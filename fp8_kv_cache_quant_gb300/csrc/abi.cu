@@ -709,6 +709,56 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
+                                             int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks) {
+  if (batch <= 0 || total_q <= 0 || max_q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks <= 0) return 0;
+  if (num_q_heads % num_kv_heads != 0 || !supported_head_dim(head_dim) || max_blocks > kMaxTableBlocks) return 0;
+  return fkv::block_weights_workspace(batch, total_q, std::min(max_q_len, total_q), num_q_heads, num_kv_heads, head_dim,
+                                      max_blocks * 16LL);
+}
+
+fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
+                                  int32_t num_q_heads, int32_t max_q_len, fkv_block_cache cache, const int32_t* block_table,
+                                  int32_t max_blocks, const int32_t* context_lens, float softmax_scale, float decay,
+                                  float* weights, int32_t weights_len, void* workspace, size_t workspace_bytes,
+                                  int32_t* fault, fkv_stream_t stream) {
+  if (total_q < 0 || batch < 0 || num_q_heads <= 0 || max_q_len < 0 || max_blocks <= 0 || weights_len < 0) return FKV_INVALID_ARG;
+  const fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale) || !std::isfinite(decay)) return FKV_INVALID_ARG;
+  if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
+  if (total_q == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
+  if (!q || !cu_seqlens_q || !block_table || !context_lens || !weights || !valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens_q, 4) || !aligned(weights, 4))
+    return FKV_INVALID_ARG;
+  const size_t need = fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, cache.num_kv_heads,
+                                                            cache.head_dim, max_blocks);
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FKV_INVALID_ARG;
+  fkv::BlockWeightsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
+  p.k_scale = cache.k_scale;
+  p.block_table = block_table;
+  p.ctx = context_lens;
+  p.cu = cu_seqlens_q;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.Hkv = cache.num_kv_heads;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.max_q_len = std::min(max_q_len, total_q);  // (longer ones have rows beyond total_q)
+  p.total_q = total_q;
+  p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
+  p.decay = decay;
+  p.weights = weights;
+  p.weights_len = weights_len;
+  p.lse = static_cast<float*>(workspace);
+  p.fault = fault;
+  return from_cuda(fkv::launch_block_weights(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 fkv_status kv_block_evict(fkv_block_cache cache, const int32_t* block_table, int32_t batch, int32_t max_blocks,
                           const int32_t* context_lens, const float* weights, int32_t weights_len, int32_t budget,
                           int32_t sink, int32_t recent, const int32_t* new_table, int32_t new_max_blocks, int32_t* new_lens,

@@ -332,6 +332,32 @@ PyObject* fp8_block_prefill_attn_(Args a) {
   return result(st, out);
 }
 
+// stream, q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, weights, softmax_scale,
+// decay, workspace, fault
+PyObject* fp8_block_attn_weights_(Args a) {
+  void* stream = a.pointer();
+  const Tensor q = three_dims(a, "q"), cu = a.tensor("cu_seqlens_q");
+  const int32_t max_q_len = a.i32();
+  const at::Device dev = q.device();
+  const fkv_block_cache c = block_cache(a, -1, q.size(2), dev);
+  const Tensor table = a.tensor("block_table"), ctx = a.tensor("context_lens"), weights = a.tensor("weights");
+  const float softmax_scale = a.real(), decay = a.real();
+  const Tensor workspace = a.tensor("workspace"), fault = a.tensor("fault", true);
+  a.done();
+  if (table.dim() != 2) refuse(a.fn, "block_table is " + text(table) + "; wanted [batch][blocks]");
+  if (weights.dim() != 3) refuse(a.fn, "weights is " + text(weights) + "; wanted [batch][heads][tokens]");
+  const int64_t b = table.size(0), len = weights.size(2);
+  if (workspace.device() != dev || !workspace.is_contiguous()) refuse(a.fn, "workspace is " + text(workspace) + "; wanted contiguous on " + dev.str());
+  const void* src = fits(a.fn, "q", q, at::kBFloat16, q.sizes(), dev);
+  const fkv_status st = fp8_block_attn_weights(
+      src, fits<int32_t>(a.fn, "cu_seqlens_q", cu, at::kInt, {b + 1}, dev), small(a.fn, q.size(0)), small(a.fn, b),
+      small(a.fn, q.size(1)), max_q_len, c, fits<int32_t>(a.fn, "block_table", table, at::kInt, table.sizes(), dev),
+      small(a.fn, table.size(1)), fits<int32_t>(a.fn, "context_lens", ctx, at::kInt, {b}, dev), softmax_scale, decay,
+      fits<float>(a.fn, "weights", weights, at::kFloat, {b, c.num_kv_heads, len}, dev), small(a.fn, len), workspace.data_ptr(),
+      workspace.nbytes(), fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev), static_cast<fkv_stream_t>(stream));
+  return result(st, weights);
+}
+
 // stream, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, weights, budget, sink, recent, new_table, new_weights,
 // new_lens, kept, fault
 PyObject* kv_block_evict_(Args a) {
@@ -388,13 +414,14 @@ FKV_ENTRY(kv_block_cache)
 FKV_ENTRY(kv_rope_cache_axes)
 FKV_ENTRY(kv_block_cache_axes)
 FKV_ENTRY(kv_block_evict)
+FKV_ENTRY(fp8_block_attn_weights)
 FKV_ENTRY(fp8_block_decode_attn)
 FKV_ENTRY(fp8_block_prefill_attn)
 #undef FKV_ENTRY
 
 #define FKV_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name##_py)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FKV_METHOD(kv_rope_cache), FKV_METHOD(kv_block_cache), FKV_METHOD(kv_rope_cache_axes),
-                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(kv_block_evict), FKV_METHOD(fp8_block_decode_attn),
+                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(kv_block_evict), FKV_METHOD(fp8_block_attn_weights), FKV_METHOD(fp8_block_decode_attn),
                          FKV_METHOD(fp8_block_prefill_attn), {nullptr, nullptr, 0, nullptr}};
 #undef FKV_METHOD
 

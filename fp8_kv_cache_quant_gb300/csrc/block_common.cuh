@@ -207,6 +207,25 @@ struct EvictParams {
 
 cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStream_t s);
 
+struct BlockWeightsParams {
+  const __nv_bfloat16* q;                     // [total_q][Hq][D]
+  const uint8_t* k_cache;
+  const float* k_scale;                       // [num_blocks][Hkv]
+  const int32_t* block_table;                 // [B][max_blocks]
+  const int32_t* ctx;                         // [B]
+  const int32_t* cu;                          // [B + 1]
+  int B, Hq, Hkv, num_blocks, max_blocks, max_q_len, total_q;
+  float sm_scale_log2;                        // softmax_scale * log2(e)
+  float decay;
+  float* weights;                             // [B][Hkv][weights_len]
+  int weights_len;
+  float* lse;                                 // [total_q][Hq], base 2
+  int32_t* fault;
+};
+
+size_t block_weights_workspace(int B, int total_q, int max_q_len, int Hq, int Hkv, int D, long long keys);
+cudaError_t launch_block_weights(const BlockWeightsParams& p, int D, int num_sms, cudaStream_t s);
+
 struct BlockPrefillParams {
   const __nv_bfloat16* q;
   const uint8_t *k_cache, *v_cache;

@@ -578,6 +578,42 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
                                   const int32_t* context_lens, float softmax_scale, int32_t causal,
                                   int32_t window, void* out, int32_t* fault, fkv_stream_t stream);
 
+/* Workspace bytes fp8_block_attn_weights needs for these sizes (same argument meaning as there); 0 for
+ * sizes it does not take. */
+size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int32_t max_q_len,
+                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                             int32_t max_blocks);
+
+/*
+ * fp8_block_attn_weights — the attention weight that each cached key receives.
+ *
+ * The queries are the last tokens of their sequences, as for the causal fp8_block_prefill_attn (one per
+ * sequence: a decode step).  With p_ij the softmax weight that row i gives key j of its KV head's keys 0 .. its own
+ * position, over the whole context, and w_j = sum over the chunk's queries and the heads of group g of p_ij:
+ *   weights[b][g][j] = decay * weights[b][g][j] + w_j   for keys older than the chunk (decay 0: w_j, what was
+ *                                                        there is not read),
+ *   weights[b][g][j] = w_j                               for the chunk's own keys.
+ * The query enters as it does in the attention over these pools; every sum is FP32, in an order that the sizes fix.
+ * A query row that holds a NaN or an infinity gives NaN weights to the keys it sees.
+ *
+ *   q, cu_seqlens_q, total_q, batch, num_q_heads, max_q_len  as for fp8_block_prefill_attn
+ *   cache         only K and its scales are read
+ *   block_table, max_blocks, context_lens, softmax_scale  as for fp8_block_prefill_attn
+ *   decay         finite; 1 adds up, 0 begins anew
+ *   weights       device float32 [batch][num_kv_heads][weights_len]; entries behind a sequence, and those of a
+ *                 sequence without queries, keep their values
+ *   workspace     device, >= fp8_block_attn_weights_workspace_size(...) bytes, 256-byte aligned, any contents; calls that may
+ *                 overlap on the GPU each need their own
+ * A sequence with Lq_b < 0, > max_q_len, > T_b or rows outside [0, total_q) is skipped and FKV_FAULT_QLEN
+ * raised; T_b outside [0, min(16 max_blocks, weights_len)] is clamped (FKV_FAULT_CONTEXT); a block id out of
+ * range reads block 0 (FKV_FAULT_BLOCK_ID).
+ */
+fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
+                                  int32_t num_q_heads, int32_t max_q_len, fkv_block_cache cache,
+                                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                  float softmax_scale, float decay, float* weights, int32_t weights_len,
+                                  void* workspace, size_t workspace_bytes, int32_t* fault, fkv_stream_t stream);
+
 /*
  * kv_block_evict — cut the sequences of a block-scaled cache to the tokens that matter.
  *

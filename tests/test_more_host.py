@@ -162,3 +162,50 @@ def test_compiled_binding_checks_of_evict(lib):
             b.kv_block_evict(0, *dict(a, **change).values())
     with pytest.raises(ValueError, match="not on a CUDA device"):
         f.kv_block_evict(f.BlockCache(pool, pool, sc, sc), tab, i32, a["w"], 20, tab)
+
+
+# ------------------------------------------------------------------ attention weights
+
+def _weights(lib, **kw):
+    a = dict(q=P, cu=P, tq=8, b=2, hq=8, mq=4, cache=_block(), tab=P, mb=8, ctx=P, sm=0.0, decay=1.0, w=P, wl=128, ws=P, wsb=1 << 30)
+    a.update(kw)
+    return lib.fp8_block_attn_weights(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(tq=-1), dict(b=-1), dict(hq=0), dict(hq=7), dict(mq=-1), dict(mb=0), dict(wl=-1), dict(sm=-1.0), dict(sm=float("inf")),
+    dict(sm=float("nan")), dict(decay=float("nan")), dict(decay=float("inf")), dict(q=None), dict(cu=None), dict(tab=None), dict(ctx=None),
+    dict(w=None), dict(ws=None), dict(q=P + 8), dict(cu=P + 2), dict(tab=P + 2), dict(ctx=P + 1), dict(w=P + 2), dict(ws=P + 128), dict(wsb=16),
+    dict(cache=_block(k=None)), dict(cache=_block(ks=None)), dict(cache=_block(nb=0)), dict(cache=_block(H=0)), dict(cache=_block(bs=0)),
+])
+def test_weights_invalid(lib, kw):
+    assert _weights(lib, **kw) == f.INVALID_ARG
+
+
+def test_weights_unsupported_empty_and_sizes(lib):
+    assert _weights(lib, cache=_block(D=96)) == f.UNSUPPORTED and _weights(lib, cache=_block(bs=32)) == f.UNSUPPORTED
+    assert _weights(lib, b=65536) == f.UNSUPPORTED and _weights(lib, mb=1 << 27) == f.UNSUPPORTED
+    assert _weights(lib, tq=0) == f.OK and _weights(lib, b=0) == f.OK and _weights(lib, mq=0) == f.OK
+    size = f.fp8_block_attn_weights_workspace_size
+    assert size(2, 8, 4, 8, 2, 128, 8) > 0 and size(2, 8, 99, 8, 2, 128, 8) == size(2, 8, 8, 8, 2, 128, 8)
+    for bad in ((0, 8, 4, 8, 2, 128, 8), (2, 0, 4, 8, 2, 128, 8), (2, 8, 0, 8, 2, 128, 8), (2, 8, 4, 7, 2, 128, 8), (2, 8, 4, 8, 2, 96, 8),
+                (2, 8, 4, 8, 2, 128, 0), (2, 8, 4, 8, 2, 128, 1 << 27)):
+        assert size(*bad) == 0
+
+
+def test_compiled_binding_checks_of_weights(lib):
+    b = f.load_binding()
+    pool, sc, i32 = torch.zeros(9, 2, 16, 64, dtype=torch.uint8), torch.ones(9, 2), torch.zeros(3, dtype=torch.int32)
+    tab = torch.zeros(2, 4, dtype=torch.int32)
+    a = dict(q=_bf(5, 4, 64), cu=i32, mx=3, kc=pool, vc=pool, ks=sc, vs=sc, tab=tab, ctx=i32[:2], w=torch.zeros(2, 2, 64), sm=0.0, decay=1.0,
+             ws=torch.zeros(1 << 16, dtype=torch.uint8), fault=None)
+    for match, change in [
+        ("q is Half", dict(q=_bf(5, 4, 64).half())), ("q is", dict(q=_bf(5, 256))), ("q is .*not contiguous", dict(q=_bf(4, 5, 64).transpose(0, 1))),
+        ("cu_seqlens_q", dict(cu=i32[:2])), ("k_cache", dict(q=_bf(5, 4, 128))), ("block_table", dict(tab=tab.long())), ("context_lens", dict(ctx=i32)),
+        ("weights is", dict(w=torch.zeros(2, 64))), ("weights is", dict(w=torch.zeros(2, 4, 64))), ("weights is Half", dict(w=torch.zeros(2, 2, 64).half())),
+        ("weights is .*not contiguous", dict(w=torch.zeros(2, 64, 2).transpose(1, 2))), ("workspace", dict(ws=torch.zeros(8, 8)[:, ::2])), ("fault", dict(fault=i32)),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            b.fp8_block_attn_weights(0, *dict(a, **change).values())
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        f.fp8_block_attn_weights(a["q"], i32, 3, f.BlockCache(pool, pool, sc, sc), tab, i32[:2], a["w"])
