@@ -545,7 +545,7 @@ def _run_own(s):
         f.kv_block_cache(s["k"], s["v"], s["cu"], s["max_new"], cache, s["table"], s["ctx"], rope=s["rope"], q=s["q"],
                          q_out=s["q_out"], positions=s["positions"])
     elif c["op"] == "shared":
-        return f.fp8_block_shared_decode_attn(s["q"], cache, s["table"], s["ctx"], s["starts"], s["shared"], s["max_group"],
+        return f.fp8_block_shared_decode_attn(s["q"], cache, s["table"], s["ctx"], s["starts"], s["shared"],
                                               window=c["window"], workspace=s["workspace"])
     elif c["op"] == "weights":
         return f.fp8_block_attn_weights(s["q"], s["cu"], s["max_new"], cache, s["table"], s["ctx"], s["weights"],
