@@ -37,6 +37,7 @@ EXPORTS = (
     "fp8_decode_attn_noalloc", "fp8_decode_attn_split_blocks", "fkv_decode_block_n", "kv_quant_cache_clips",
     "fp8_decode_step", "fkv_set_decode_wait_limit_ns", "kv_rope_cache", "kv_block_cache",
     "kv_rope_cache_axes", "kv_block_cache_axes", "kv_block_evict",
+    "fp8_block_shared_decode_attn_workspace_size", "fp8_block_shared_decode_attn",
     "fp8_block_attn_weights_workspace_size", "fp8_block_attn_weights",
     "fp8_block_decode_attn_workspace_size", "fp8_block_decode_attn", "fp8_block_prefill_attn",
 )
@@ -141,6 +142,11 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.kv_block_evict.restype = ctypes.c_int
     lib.kv_block_evict.argtypes = [_BlockCache, c_vp, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_i32, c_i32, c_vp, c_i32, c_vp, c_vp,
                                    c_vp, c_i32, c_vp, c_vp]
+    lib.fp8_block_shared_decode_attn_workspace_size.restype = c_sz
+    lib.fp8_block_shared_decode_attn_workspace_size.argtypes = [c_i32] * 5
+    lib.fp8_block_shared_decode_attn.restype = ctypes.c_int
+    lib.fp8_block_shared_decode_attn.argtypes = [c_vp, c_i32, c_i32, _BlockCache, c_vp, c_i32, c_vp, c_vp, c_vp, c_i32, c_f, c_i32, c_vp,
+                                                 c_vp, c_sz, c_vp, c_vp]
     lib.fp8_block_attn_weights_workspace_size.restype = c_sz
     lib.fp8_block_attn_weights_workspace_size.argtypes = [c_i32] * 7
     lib.fp8_block_attn_weights.restype = ctypes.c_int
@@ -521,6 +527,30 @@ def fp8_block_prefill_attn(q, cu_seqlens_q, max_q_len, cache: BlockCache, block_
 
 
 # ------------------------------------------------------------------ long and shared contexts
+
+def fp8_block_shared_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, num_groups) -> int:
+    return int(load_library().fp8_block_shared_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim, num_groups))
+
+
+def block_shared_workspace(batch, num_q_heads, cache: BlockCache, num_groups, stream=None):
+    """A workspace of fp8_block_shared_decode_attn, zero-filled on the stream (calls that may overlap on the GPU each
+    need one)."""
+    _, h, _, d = cache.k_cache.shape
+    with _allocating("fp8_block_shared_decode_attn", cache.k_cache, stream):
+        n = fp8_block_shared_decode_attn_workspace_size(batch, num_q_heads, h, d, num_groups)
+        return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k_cache.device)
+
+
+def fp8_block_shared_decode_attn(q, cache: BlockCache, block_table, context_lens, group_starts, shared_lens, softmax_scale=0.0,
+                                 window=0, out=None, workspace=None, fault=None, stream=None):
+    """fp8_block_decode_attn of a batch whose group i, sequences group_starts[i] .. group_starts[i + 1] - 1 (int32 [groups + 1]), has its
+    first shared_lens[i] tokens (int32 [groups]) in common: their keys and values are read and multiplied once per group.
+    ``workspace``: of block_shared_workspace (when None, one is made and cleared for the call: a loop keeps its own)."""
+    if workspace is None:
+        workspace = block_shared_workspace(q.shape[0], q.shape[1], cache, shared_lens.shape[0], stream)
+    return _call("fp8_block_shared_decode_attn", q, stream, q, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
+                 context_lens, group_starts, shared_lens, softmax_scale, window, out, workspace, fault)
+
 
 def fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, max_blocks) -> int:
     return int(load_library().fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, num_kv_heads,

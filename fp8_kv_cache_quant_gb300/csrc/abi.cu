@@ -709,6 +709,24 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
   return from_cuda(fkv::launch_block_prefill(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
+size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t num_groups) {
+  if (num_groups < 0) return 0;
+  return fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+}
+
+fkv_status fp8_block_shared_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
+                                        const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
+                                        const int32_t* group_starts, const int32_t* shared_lens, int32_t num_groups,
+                                        float softmax_scale, int32_t window, void* out, void* workspace,
+                                        size_t workspace_bytes, int32_t* fault, fkv_stream_t stream) {
+  if (num_groups < 0) return FKV_INVALID_ARG;
+  if (num_groups > 0 && (!group_starts || !shared_lens || !aligned(group_starts, 4) || !aligned(shared_lens, 4)))
+    return FKV_INVALID_ARG;
+  return fp8_block_decode_attn(q, batch, num_q_heads, cache, block_table, max_blocks, context_lens, softmax_scale, window, out,
+                               workspace, workspace_bytes, fault, stream);
+}
+
 size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,
                                              int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks) {
   if (batch <= 0 || total_q <= 0 || max_q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks <= 0) return 0;

@@ -332,6 +332,34 @@ PyObject* fp8_block_prefill_attn_(Args a) {
   return result(st, out);
 }
 
+// stream, q, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, group_starts, shared_lens, softmax_scale, window, out,
+// workspace, fault
+PyObject* fp8_block_shared_decode_attn_(Args a) {
+  void* stream = a.pointer();
+  const Tensor q = three_dims(a, "q");
+  const at::Device dev = q.device();
+  const fkv_block_cache c = block_cache(a, -1, q.size(2), dev);
+  const Tensor table = a.tensor("block_table"), ctx = a.tensor("context_lens"), starts = a.tensor("group_starts"), shared = a.tensor("shared_lens");
+  const float softmax_scale = a.real();
+  const int32_t window = a.i32();
+  Tensor out = a.tensor("out", true);
+  const Tensor workspace = a.tensor("workspace"), fault = a.tensor("fault", true);
+  a.done();
+  if (table.dim() != 2) refuse(a.fn, "block_table is " + text(table) + "; wanted [batch][blocks]");
+  if (shared.dim() != 1) refuse(a.fn, "shared_lens is " + text(shared) + "; wanted [groups]");
+  const int64_t b = table.size(0), hq = q.size(1), d = q.size(2), n = shared.size(0);
+  const void* src = fits(a.fn, "q", q, at::kBFloat16, {b, hq, d}, dev);
+  if (!out.defined()) out = at::empty({b, hq, d}, q.options());
+  if (workspace.device() != dev || !workspace.is_contiguous()) refuse(a.fn, "workspace is " + text(workspace) + "; wanted contiguous on " + dev.str());
+  const fkv_status st = fp8_block_shared_decode_attn(
+      src, small(a.fn, b), small(a.fn, hq), c, fits<int32_t>(a.fn, "block_table", table, at::kInt, table.sizes(), dev),
+      small(a.fn, table.size(1)), fits<int32_t>(a.fn, "context_lens", ctx, at::kInt, {b}, dev),
+      fits<int32_t>(a.fn, "group_starts", starts, at::kInt, {n + 1}, dev), fits<int32_t>(a.fn, "shared_lens", shared, at::kInt, {n}, dev),
+      small(a.fn, n), softmax_scale, window, fits(a.fn, "out", out, at::kBFloat16, {b, hq, d}, dev), workspace.data_ptr(),
+      workspace.nbytes(), fits<int32_t>(a.fn, "fault", fault, at::kInt, {1}, dev), static_cast<fkv_stream_t>(stream));
+  return result(st, out);
+}
+
 // stream, q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scale, v_scale, block_table, context_lens, weights, softmax_scale,
 // decay, workspace, fault
 PyObject* fp8_block_attn_weights_(Args a) {
@@ -414,6 +442,7 @@ FKV_ENTRY(kv_block_cache)
 FKV_ENTRY(kv_rope_cache_axes)
 FKV_ENTRY(kv_block_cache_axes)
 FKV_ENTRY(kv_block_evict)
+FKV_ENTRY(fp8_block_shared_decode_attn)
 FKV_ENTRY(fp8_block_attn_weights)
 FKV_ENTRY(fp8_block_decode_attn)
 FKV_ENTRY(fp8_block_prefill_attn)
@@ -421,7 +450,8 @@ FKV_ENTRY(fp8_block_prefill_attn)
 
 #define FKV_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name##_py)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FKV_METHOD(kv_rope_cache), FKV_METHOD(kv_block_cache), FKV_METHOD(kv_rope_cache_axes),
-                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(kv_block_evict), FKV_METHOD(fp8_block_attn_weights), FKV_METHOD(fp8_block_decode_attn),
+                         FKV_METHOD(kv_block_cache_axes), FKV_METHOD(kv_block_evict), FKV_METHOD(fp8_block_shared_decode_attn),
+                         FKV_METHOD(fp8_block_attn_weights), FKV_METHOD(fp8_block_decode_attn),
                          FKV_METHOD(fp8_block_prefill_attn), {nullptr, nullptr, 0, nullptr}};
 #undef FKV_METHOD
 

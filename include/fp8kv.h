@@ -578,6 +578,38 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
                                   const int32_t* context_lens, float softmax_scale, int32_t causal,
                                   int32_t window, void* out, int32_t* fault, fkv_stream_t stream);
 
+/* Workspace bytes fp8_block_shared_decode_attn needs for these sizes on the current device; 0 for
+ * sizes it does not take. */
+size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                                   int32_t head_dim, int32_t num_groups);
+
+/*
+ * fp8_block_shared_decode_attn — fp8_block_decode_attn for sequences that share their first tokens.
+ *
+ * Group i, sequences group_starts[i] .. group_starts[i + 1] - 1, has its first shared_lens[i] tokens in common:
+ * tokens that every member's row of block_table names, in the same blocks or in copies of them.  The
+ * result is that of fp8_block_decode_attn for the same arguments (to rounding), but the keys and values of the
+ * shared tokens are read, from the blocks that the group's first sequence names, and multiplied once for all
+ * members.  Sequences outside every group share nothing.  Groups whose sharing would not pay for itself (few bytes saved
+ * in the whole call) are attended like the others, over their own rows of block_table.
+ *
+ *   group_starts  device int32 [num_groups + 1], non-decreasing, within [0, batch]
+ *   shared_lens   device int32 [num_groups]; need not be multiples of 16, and a member may be
+ *                 shorter (it sees its own context_lens tokens)
+ *   num_groups    >= 0 (0: nothing is shared)
+ *   workspace     device, >= fp8_block_shared_decode_attn_workspace_size(...) bytes, 256-byte aligned, zero-filled
+ *                 before its first call; otherwise as for fp8_block_decode_attn
+ *   all others    as for fp8_block_decode_attn
+ * Group starts that decrease or leave [0, batch] raise FKV_FAULT_QLEN, a shared length outside [0, 16 max_blocks]
+ * FKV_FAULT_CONTEXT: the group then shares nothing (the starts of any: no group does).
+ */
+fkv_status fp8_block_shared_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
+                                        const int32_t* block_table, int32_t max_blocks,
+                                        const int32_t* context_lens, const int32_t* group_starts,
+                                        const int32_t* shared_lens, int32_t num_groups, float softmax_scale,
+                                        int32_t window, void* out, void* workspace, size_t workspace_bytes,
+                                        int32_t* fault, fkv_stream_t stream);
+
 /* Workspace bytes fp8_block_attn_weights needs for these sizes (same argument meaning as there); 0 for
  * sizes it does not take. */
 size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int32_t max_q_len,

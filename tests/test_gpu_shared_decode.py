@@ -1,0 +1,223 @@
+"""fp8_block_shared_decode_attn on the GPU against the float64 softmax of every sequence by itself.
+
+Tolerance of an output element, derived as for the attention over block-scaled pools: with p_j the softmax weights,
+P = sum_j p_j |v_j| and V the largest |v_j| of the sequence, P enters the products within 2^-8 (2^-8 P), scores are FP32 sums of
+exact products (2^-10 P), weights 2^-17 and more below a tile's largest may be off by a fixed step (2^-10 V), the output
+is rounded to bf16 (2^-8 |o|).  The join of the pieces is FP32.  The relative L2 distance is held to 2^-7."""
+import numpy as np
+import pytest
+import torch
+
+from helpers import rel_l2
+from oracle import blockcache
+
+f = pytest.importorskip("fp8_kv_cache_quant_gb300")
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+class Case:
+    """Groups of sequences behind shared tokens.  groups: (shared tokens, [own tokens of each member]); a negative number
+    of own tokens is a member shorter than the shared part.  `alone` sequences behind the last group share nothing."""
+
+    def __init__(self, groups, hq, h, d, seed=0, alone=(), spread=3, q_size=1.0, wide=0):
+        rng = np.random.default_rng(seed)
+        self.ctx, self.starts, self.shared, rows, nb = [], [0], [], [], 0
+
+        def blocks(n):
+            nonlocal nb
+            nb += n
+            return list(range(nb - n, nb))
+        copies = []
+        for p, mine in groups:
+            common = blocks(p // 16)
+            first = None
+            for m in mine:
+                t = max(0, p + m)
+                own = blocks((t + 15) // 16 - min(p, t) // 16)
+                rows.append(common[:min(p, t) // 16] + own)
+                if p % 16 and t >= p:
+                    if first is None:
+                        first = own[0]
+                    else:
+                        copies.append((first, own[0], p % 16))
+                self.ctx.append(t)
+            self.starts.append(len(self.ctx))
+            self.shared.append(p)
+        for t in alone:
+            rows.append(blocks((t + 15) // 16))
+            self.ctx.append(t)
+        nb += 2
+        perm = rng.permutation(nb).astype(np.int32)
+        self.table = np.full((len(rows), max(1, *(len(r) for r in rows)) + wide), -1, np.int32)
+        for b, r in enumerate(rows):
+            self.table[b, :len(r)] = perm[r]
+        self.pools, self.scales = [], []
+        for _ in range(2):
+            x = rng.standard_normal((nb, h, 16, d))
+            s = 2.0 ** rng.integers(-spread, spread + 1, (nb, h)) * 2.0 ** -7
+            p8 = torch.from_numpy((x * 128).astype(np.float32)).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+            s = s.astype(np.float32)
+            for a, c, n in copies:       # a copied block: the shared tokens' codes and their scale
+                p8[perm[c], :, :n], s[perm[c]] = p8[perm[a], :, :n], s[perm[a]]
+            for b, t in enumerate(self.ctx):
+                if t % 16 and not any(t < q for q in self._shared_of(b)):
+                    p8[self.table[b, t // 16], :, t % 16:] = rng.choice([0x7F, 0xFF, 0x7E, 3], p8[0, :, t % 16:].shape)
+            p8[perm[nb - 2:]] = 0x7F
+            self.pools.append(p8)
+            self.scales.append(s)
+        self.q = torch.from_numpy((rng.standard_normal((len(rows), hq, d)) * q_size).astype(np.float32)).to(torch.bfloat16)
+
+    def _shared_of(self, b):
+        return [p for i, p in enumerate(self.shared) if self.starts[i] <= b < self.starts[i + 1]]
+
+    def cache(self):
+        return f.BlockCache(*(torch.from_numpy(p).cuda() for p in self.pools), *(torch.from_numpy(s).cuda() for s in self.scales))
+
+    def run(self, **kw):
+        self.fault = torch.zeros(1, dtype=torch.int32, device="cuda")
+        return f.fp8_block_shared_decode_attn(self.q.cuda(), self.cache(), _i32(self.table), _i32(self.ctx), _i32(self.starts),
+                                              _i32(self.shared), fault=self.fault, **kw)
+
+    def check(self, got=None, **kw):
+        if got is None:
+            got = self.run(**kw)
+            assert int(self.fault) == 0
+        kw.pop("workspace", None)
+        a = (self.pools[0], self.pools[1], self.scales[0], self.scales[1], self.table, self.ctx, None)
+        q = self.q.float().numpy().astype(np.float64)
+        o, mag = blockcache.attend(q, *a, **kw), blockcache.p_bound(q, *a, **kw)
+        top = np.zeros(len(self.ctx))
+        for b, t in enumerate(self.ctx):
+            if t:
+                top[b] = max(np.abs(blockcache.sequence(self.pools[1], self.scales[1], self.table[b], t, g)).max() for g in range(self.pools[1].shape[1]))
+        tol = (2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -10 * top[:, None, None] + 2.0 ** -8 * np.abs(o)
+        got = got.float().cpu().numpy().astype(np.float64)
+        assert np.all(np.isfinite(got))
+        err = np.abs(got - o)
+        i = np.unravel_index(int(np.argmax(err - tol)), err.shape)
+        assert np.all(err <= tol), f"{err[i]:.3e} above {tol[i]:.3e} at {i} (T {self.ctx[i[0]]})"
+        assert rel_l2(got, o) <= 2.0 ** -7
+
+
+# 4 MB of shared keys and values saved is far above any rule's border here; the smallest cases are attended unshared
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
+def test_one_group(d, g):
+    if g * d > 2048:
+        pytest.skip("group and head_dim beyond the decode's limit")
+    Case([(6400, [1, 0, 17, 200, 3, 16, 40, 128])], 2 * g, 2, d, seed=d + g).check()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("groups,alone,hq,h", [
+    ([(5000, [5, 77]), (2049, [1] * 9), (3333, [600, 0, 30])], (300, 0, 17), 8, 2),
+    ([(4099, [1] * 70)], (), 8, 2), ([(100, [10, 10]), (9000, [40] * 5), (0, [33, 1]), (7, [9])], (5000,), 4, 1),
+    ([(8000, [3, -100, -7990, -8000, 50])], (), 8, 2), ([(16, [1, 2]), (16 * 400, [300] * 4)], (1,), 16, 8),
+])
+def test_groups(d, groups, alone, hq, h):
+    Case(groups, hq, h, d, seed=len(groups) + hq, alone=alone).check()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 50, 700, 6000])
+def test_windows(d, window):
+    Case([(6003, [1, 0, 60, 900, 5, 5]), (4000, [10, 2000, -30])], 8, 2, d, seed=window).check(window=window)
+
+
+def test_small_calls_and_many_groups():
+    Case([(1, [0, 0])], 2, 2, 64, seed=1).check()
+    Case([(33, [1, 2, 3, 4])], 8, 2, 128, seed=2).check()
+    Case([(320, [int(x) for x in range(1, 5)]) for _ in range(90)], 8, 4, 128, seed=3).check()
+    Case([(640, [1] * 2) for _ in range(80)], 32, 8, 64, seed=4).check()
+
+
+def test_one_long_prefix_of_one_head():
+    Case([(60000, [10, 1])], 2, 1, 64, seed=5).check()
+
+
+def test_scales_far_apart():
+    c = Case([(5000, [100, 20, 3, 9])], 8, 2, 128, seed=6, spread=0)
+    rng = np.random.default_rng(7)
+    for s in c.scales:
+        s *= (2.0 ** rng.integers(-40, 1, s.shape)).astype(np.float32)
+    c.scales[1][c.table[0, 3:9]] = 0.0
+    c.check()
+
+
+def test_all_shared_and_scale():
+    Case([(3000, [0] * 6)], 8, 2, 128, seed=8).check(softmax_scale=0.25)
+
+
+def test_no_groups():
+    c = Case([], 8, 2, 128, seed=9, alone=(100, 700, 0, 33))
+    c.check()
+    want = f.fp8_block_decode_attn(c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx))
+    assert torch.equal(c.run(), want)
+
+
+def test_bad_queries_keep_to_their_rows():
+    c = Case([(5000, [40, 3, 9, 70])], 8, 2, 128, seed=10)
+    want = c.run()
+    c.q[1, 5, 7] = float("nan")
+    c.q[2, 0, 1] = float("inf")
+    got = c.run()
+    assert bool(got[1, 5].isnan().all()) and bool(got[2, 0].isnan().all())
+    bad = torch.zeros(4, 8, dtype=torch.bool)
+    bad[1, 5] = bad[2, 0] = True
+    assert torch.equal(got[~bad], want[~bad])
+
+
+def test_bad_blocks_are_reported():
+    c = Case([(5000, [40, 3, 9])], 8, 2, 128, seed=12)
+    c.table[0, 7] = c.table[1, 7] = c.table[2, 7] = 1 << 29
+    c.pools[0][0], c.pools[1][0] = 0x10, 0x10
+    c.run()
+    assert int(c.fault) == f.FAULT_BLOCK_ID
+
+
+def test_one_workspace_for_calls_that_grow_and_shrink():
+    big, small = Case([(5000, [40] * 40)], 8, 2, 128, seed=13), Case([(4000, [3, 9]), (6000, [1, 1, 1])], 8, 2, 128, seed=14, alone=(50,))
+    ws = f.block_shared_workspace(40, 8, big.cache(), 2)
+    for c in (big, small, big, small, small):
+        c.check(workspace=ws)
+    one = big.run(workspace=ws)
+    assert torch.equal(one, big.run(workspace=ws)), "the same bits every time"
+    plain = f.fp8_block_decode_attn(small.q.cuda(), small.cache(), _i32(small.table), _i32(small.ctx), workspace=ws)
+    small.check(plain)
+    with pytest.raises(f.FkvError):
+        big.run(workspace=ws[:65536])
+
+
+def test_captured_and_replayed_with_other_groups_and_lengths():
+    c = Case([(5000, [40, 300, 9, 1]), (3000, [5, 6])], 8, 2, 128, seed=15)
+    cache, q, tab, ctx, starts, shared = c.cache(), c.q.cuda(), _i32(c.table), _i32(c.ctx), _i32(c.starts), _i32(c.shared)
+    ws, out = f.block_shared_workspace(6, 8, cache, 2), torch.empty_like(q)
+    f.fp8_block_shared_decode_attn(q, cache, tab, ctx, starts, shared, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        f.fp8_block_shared_decode_attn(q, cache, tab, ctx, starts, shared, out=out, workspace=ws)
+    g.replay()
+    c.check(out)
+    c.starts, c.shared, c.ctx = [0, 3, 3], [4990, 0], [5011, 5300, 5001, 5000, 3001, 2]
+    starts.copy_(_i32(c.starts)), shared.copy_(_i32(c.shared)), ctx.copy_(_i32(c.ctx))
+    out.zero_()
+    g.replay()
+    c.check(out)
+
+
+def test_on_another_stream_beside_another_call():
+    c, e = Case([(5000, [40, 300, 9, 1])], 8, 2, 128, seed=16), Case([(4000, [7, 8])], 8, 2, 128, seed=17)
+    s = torch.cuda.Stream()
+    a = (c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx), _i32(c.starts), _i32(c.shared))
+    b = (e.q.cuda(), e.cache(), _i32(e.table), _i32(e.ctx), _i32(e.starts), _i32(e.shared))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        x = f.fp8_block_shared_decode_attn(*a, stream=s)
+        y = f.fp8_block_shared_decode_attn(*b)
+    torch.cuda.synchronize()
+    c.check(x), e.check(y)

@@ -209,3 +209,45 @@ def test_compiled_binding_checks_of_weights(lib):
             b.fp8_block_attn_weights(0, *dict(a, **change).values())
     with pytest.raises(ValueError, match="not on a CUDA device"):
         f.fp8_block_attn_weights(a["q"], i32, 3, f.BlockCache(pool, pool, sc, sc), tab, i32[:2], a["w"])
+
+
+# ------------------------------------------------------------------ shared decode
+
+def _shared(lib, **kw):
+    a = dict(q=P, b=4, hq=8, cache=_block(), tab=P, mb=8, ctx=P, gs=P, sl=P, ng=2, sm=0.0, win=0, out=P, ws=P, wsb=1 << 30)
+    a.update(kw)
+    return lib.fp8_block_shared_decode_attn(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(b=-1), dict(hq=0), dict(hq=7), dict(mb=0), dict(ng=-1), dict(sm=-1.0), dict(sm=float("nan")), dict(win=-1), dict(q=None), dict(tab=None),
+    dict(ctx=None), dict(gs=None), dict(sl=None), dict(gs=P + 2), dict(sl=P + 1), dict(out=None), dict(out=P + 8), dict(ws=None), dict(ws=P + 128),
+    dict(wsb=1 << 16), dict(cache=_block(k=None)), dict(cache=_block(vs=None)), dict(cache=_block(nb=0)), dict(cache=_block(bs=0)),
+])
+def test_shared_invalid(lib, kw):
+    assert _shared(lib, **kw) == f.INVALID_ARG
+
+
+def test_shared_unsupported_empty_and_sizes(lib):
+    assert _shared(lib, cache=_block(D=96)) == f.UNSUPPORTED and _shared(lib, hq=6) == f.UNSUPPORTED and _shared(lib, b=65536) == f.UNSUPPORTED
+    assert _shared(lib, b=0) == f.OK and _shared(lib, b=0, ng=0, gs=None, sl=None) == f.OK
+    size = f.fp8_block_shared_decode_attn_workspace_size
+    assert size(4, 8, 2, 128, 2) >= f.fp8_block_decode_attn_workspace_size(4, 8, 2, 128) > 0
+    assert size(4, 8, 2, 128, -1) == 0 and size(0, 8, 2, 128, 1) == 0 and size(4, 7, 2, 128, 1) == 0 and size(4, 8, 2, 96, 1) == 0
+
+
+def test_compiled_binding_checks_of_shared(lib):
+    b = f.load_binding()
+    pool, sc, i32 = torch.zeros(9, 2, 16, 64, dtype=torch.uint8), torch.ones(9, 2), torch.zeros(3, dtype=torch.int32)
+    tab = torch.zeros(3, 4, dtype=torch.int32)
+    a = dict(q=_bf(3, 4, 64), kc=pool, vc=pool, ks=sc, vs=sc, tab=tab, ctx=i32, gs=i32, sl=i32[:2], sm=0.0, win=0, out=None,
+             ws=torch.zeros(1 << 16, dtype=torch.uint8), fault=None)
+    for match, change in [
+        ("q is Half", dict(q=_bf(3, 4, 64).half())), ("q is BFloat16", dict(q=_bf(2, 4, 64))), ("k_cache", dict(q=_bf(3, 4, 128))), ("block_table", dict(tab=tab[0])),
+        ("context_lens", dict(ctx=i32[:2])), ("group_starts", dict(gs=i32[:2])), ("group_starts is Long", dict(gs=i32.long())), ("shared_lens", dict(sl=tab)),
+        ("shared_lens is Long", dict(sl=i32[:2].long())), ("out is", dict(out=_bf(3, 4, 32))), ("workspace", dict(ws=torch.zeros(8, 8)[:, ::2])), ("fault", dict(fault=i32)),
+    ]:
+        with pytest.raises(ValueError, match=match):
+            b.fp8_block_shared_decode_attn(0, *dict(a, **change).values())
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        f.fp8_block_shared_decode_attn(a["q"], f.BlockCache(pool, pool, sc, sc), tab, i32, i32, i32[:2])
