@@ -164,6 +164,9 @@ bool valid_block_pools(const fkv_block_cache& c) {
 // Columns of a block table whose positions (and a tile more) the kernels count in 32 bits.
 constexpr int32_t kMaxTableBlocks = (1 << 27) - 64;
 
+// Rows (tokens times heads of a group) of an attention weights call that the kernels count in 32 bits, and their tiles' grid.
+constexpr long long kMaxWeightRows = 1LL << 30;
+
 // The block-scaled decode: CTAs resident at once, of which a unit (sequence, KV head) is given at
 // most 160 (the merge of its pieces grows with them: 0.05 us each, a tile of its own 1.5 us), and the
 // workspace: piece counters, the pieces' log-sum-exps and outputs.
@@ -731,8 +734,9 @@ size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int
                                              int32_t num_kv_heads, int32_t head_dim, int32_t max_blocks) {
   if (batch <= 0 || total_q <= 0 || max_q_len <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks <= 0) return 0;
   if (num_q_heads % num_kv_heads != 0 || !supported_head_dim(head_dim) || max_blocks > kMaxTableBlocks) return 0;
+  if (static_cast<long long>(total_q) * (num_q_heads / num_kv_heads) > kMaxWeightRows) return 0;
   return fkv::block_weights_workspace(batch, total_q, std::min(max_q_len, total_q), num_q_heads, num_kv_heads, head_dim,
-                                      max_blocks * 16LL);
+                                      max_blocks * 16LL, current_num_sms());
 }
 
 fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
@@ -746,6 +750,7 @@ fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, in
   if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
   if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale) || !std::isfinite(decay)) return FKV_INVALID_ARG;
   if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
+  if (static_cast<long long>(total_q) * (num_q_heads / cache.num_kv_heads) > kMaxWeightRows) return FKV_UNSUPPORTED;
   if (total_q == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
   if (!q || !cu_seqlens_q || !block_table || !context_lens || !weights || !valid_block_pools(cache)) return FKV_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens_q, 4) || !aligned(weights, 4))
@@ -772,9 +777,8 @@ fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, in
   p.decay = decay;
   p.weights = weights;
   p.weights_len = weights_len;
-  p.lse = static_cast<float*>(workspace);
   p.fault = fault;
-  return from_cuda(fkv::launch_block_weights(p, cache.head_dim, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(fkv::launch_block_weights(p, cache.head_dim, workspace, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 fkv_status kv_block_evict(fkv_block_cache cache, const int32_t* block_table, int32_t batch, int32_t max_blocks,

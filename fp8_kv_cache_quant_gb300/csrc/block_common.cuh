@@ -219,12 +219,20 @@ struct BlockWeightsParams {
   float decay;
   float* weights;                             // [B][Hkv][weights_len]
   int weights_len;
-  float* lse;                                 // [total_q][Hq], base 2
   int32_t* fault;
+  // the workspace's parts (block_weights.cu), set by the launch
+  int slots;                                  // CTAs of a launch, at most
+  int32_t* done;                              // [2][slots] pieces finished of the unit that CTA k begins, in either pass
+  float2* pieces;                             // [2 slots (+ units)][rows] maxima and sums
+  float* sums;                                // [2 slots][128]
+  float* rows;                                // [tiles][64]{c, c, -lse, -lse}
+  uint8_t* q_tiles;                           // [tiles] of both terms
+  int2* units;                                // [B][Hkv]{first CTA, pieces}
+  float* scores;                              // [B][Hkv][16 max_blocks][rows]
 };
 
-size_t block_weights_workspace(int B, int total_q, int max_q_len, int Hq, int Hkv, int D, long long keys);
-cudaError_t launch_block_weights(const BlockWeightsParams& p, int D, int num_sms, cudaStream_t s);
+size_t block_weights_workspace(int B, int total_q, int max_q_len, int Hq, int Hkv, int D, long long keys, int num_sms);
+cudaError_t launch_block_weights(BlockWeightsParams p, int D, void* workspace, int num_sms, cudaStream_t s);
 
 struct BlockPrefillParams {
   const __nv_bfloat16* q;

@@ -1,12 +1,32 @@
 // The attention weight that the cached keys of a block-scaled pool receive from a chunk of queries, summed over the
-// queries and the heads of a KV head's group: w_j = sum over rows r of 2^(x_rj - lse_r), x_rj = q_r . k_j * ks *
-// softmax_scale * log2(e), lse_r = log2 sum_j 2^(x_rj).
+// queries and the heads of a KV head's group, on tcgen05 tensor cores.
 //
-// One CTA per row finds lse_r; then a thread per key adds up its column, in row order.
+// Mathematics.  A row r is a (token, head of the group) pair, r = token * G + head; x_rj = q_r . k_j * ks_j * c, c =
+// softmax_scale log2(e), in base 2.  lse_r = log2 sum_j 2^(x_rj) over the keys that the row sees, and
+//   w_j = sum_r 2^(x_rj - lse_r).
+// No weight is final before every key of a row has been scored, so the keys are gone over twice.  Products are FP8: the
+// bf16 query as two e4m3 terms on its row's own power of two (split4_query), K as it lies in the cache, FP32 sums.
+//
+// Few rows (at most 16 per sequence and KV head: decode steps, drafts): one walk over K writes the scores, 16 to 64 bytes a key
+// where K has 64 to 256, and the rows' sums; a second kernel reads them back (from L2 as a rule) and adds up (score_kernel,
+// gather_kernel).
+// More rows: a score costs an exponential, which the GPU makes 16 of per clock and SM, in each of two passes, and writing it
+// down would cost more than making it again.  query_kernel lays the rows out in tiles of 128 as the products want
+// them; pass 0 takes rows as the MMA's M side (a thread owns a row, its maximum and sum stay in registers), pass 1 keys (a
+// thread owns a key, the sum over the rows stays in a register), so that neither needs a sum across threads in its loop.
+//
+// Work.  Lengths are known on the GPU alone.  The steps of a pass (a tile against a tile) of all units (sequence, KV head, row tile
+// or key tile) stand in a row, and every resident CTA takes the same number of them; a unit in several CTAs' ranges is joined by the
+// one that brings its last piece, in the order of the pieces, so that the same sizes give the same bits.
+// Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and products drain and returns.
 #include "block_common.cuh"
+#include "prefill_common.cuh"
+#include "tc.cuh"
 
 namespace fkv {
 namespace {
+
+constexpr float kHuge = 3e38f;  // minus this: the maximum of no scores
 
 // Sequence b's rows and keys; rows 0: nothing to do.
 struct WeightsSeq {
@@ -29,109 +49,1139 @@ FKV_DEV WeightsSeq weights_seq(const BlockWeightsParams& p, int b, bool report) 
   return s;
 }
 
-template <int D>
-FKV_DEV float score(const BlockWeightsParams& p, const __nv_bfloat16* q, int b, int g, int j) {
-  int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + (j >> 4)];
-  if (id < 0 || id >= p.num_blocks) {
-    raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
-    id = 0;
+// ---------------------------------------------------------------- the division of the work
+
+// What a kernel divides: kRows: row tiles against the key tiles that they see (pass 0); kKeys: key tiles against the row
+// tiles that see them (pass 1); kScores: all of a KV head's key tiles of KT keys as one unit.
+enum Kind { kRows, kKeys, kScores };
+
+template <Kind K, int KT>
+struct Units {
+  int G;
+  FKV_DEV int tiles(const WeightsSeq& s) const { return static_cast<int>((static_cast<long long>(s.rows) * G + 127) / 128); }
+  FKV_DEV int of(const WeightsSeq& s) const {  // units of a sequence and KV head
+    if (s.rows == 0) return 0;
+    return K == kRows ? tiles(s) : K == kKeys ? (s.T + 127) / 128 : 1;
   }
-  const size_t at = static_cast<size_t>(id) * p.Hkv + g;
-  const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k_cache + (at * 16 + (j & 15)) * D);
-  const uint2* qv = reinterpret_cast<const uint2*>(q);
-  float x = 0.f;
-  for (int i = 0; i < D / 4; ++i) {
-    const uint32_t w = k[i];
-    const uint2 y = qv[i];
-    uint32_t h01, h23;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h23) : "h"(static_cast<uint16_t>(w >> 16)));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h01)), c = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-    const float2 q0 = bf16x2_to_f2(y.x), q1 = bf16x2_to_f2(y.y);
-    x = fmaf(a.x, q0.x, x);
-    x = fmaf(a.y, q0.y, x);
-    x = fmaf(c.x, q1.x, x);
-    x = fmaf(c.y, q1.y, x);
+  // the first step's tile: 0, or the first row tile that sees key tile t
+  FKV_DEV int first(const WeightsSeq& s, int t) const {
+    if (K != kKeys) return 0;
+    const long long token = 128LL * t - (s.T - s.rows);
+    return token > 0 ? static_cast<int>(token * G / 128) : 0;
   }
-  return x * p.k_scale[at] * p.sm_scale_log2;
+  FKV_DEV int steps(const WeightsSeq& s, int t) const {
+    if (K == kScores) return (s.T + KT - 1) / KT;
+    if (K == kKeys) return tiles(s) - first(s, t);
+    const long long row = min(128LL * (t + 1), static_cast<long long>(s.rows) * G) - 1;  // the tile's last
+    return (s.T - s.rows + static_cast<int>(row / G)) / 128 + 1;
+  }
+};
+
+// A place in a CTA's range of steps.
+template <Kind K, int KT>
+struct Walk {
+  Units<K, KT> units;
+  int b, g, t, s;         // step s of unit t of (sequence b, KV head g)
+  int count, of;          // steps of the unit, units of (b, g)
+  WeightsSeq seq;
+  long long left;         // steps of the range from this one on
+  long long unit0;        // the place of the unit's first step
+  int piece;              // units begun before this one in the range
+
+  FKV_DEV bool begins() const { return fresh; }
+  FKV_DEV bool ends() const { return s + 1 == count || left == 1; }
+  FKV_DEV void advance(const BlockWeightsParams& p) {
+    fresh = false;
+    if (--left <= 0) return;
+    if (++s < count) return;
+    s = 0;
+    fresh = true;
+    ++piece;
+    unit0 += count;
+    if (++t == of) {
+      t = 0;
+      if (++g == p.Hkv) {
+        g = 0;
+        do {
+          seq = weights_seq(p, ++b, false);
+          of = units.of(seq);
+        } while (of == 0);
+      }
+    }
+    count = units.steps(seq, t);
+  }
+  bool fresh;             // this is the range's first step of the unit
+};
+
+// The range of CTA k of the grid: its first step, and W and N, the steps in all and the CTAs that have some.  Every lane of a
+// warp takes part.
+template <Kind K, int KT>
+FKV_DEV Walk<K, KT> first_step(const BlockWeightsParams& p, int k, long long& W, int& N, bool report) {
+  const int lane = threadIdx.x & 31;
+  Walk<K, KT> a;
+  a.units.G = p.Hq / p.Hkv;
+  a.b = a.g = a.t = a.s = a.count = a.of = a.piece = 0;
+  a.left = a.unit0 = 0;
+  a.fresh = true;
+  a.seq = WeightsSeq{0, 0, 0};
+  auto sum = [](long long x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+  };
+  // a sequence's steps for one KV head: by one lane where it has few units, by all of them where it may have many
+  const bool alone = K == kScores || p.max_q_len * static_cast<long long>(a.units.G) <= 512;
+  auto steps_of = [&](const WeightsSeq& s, int t0, int dt) -> long long {
+    if (s.rows == 0) return 0;
+    if constexpr (K == kKeys) {
+      // key tiles wholly before the chunk's first token are seen by every row tile, those behind by G fewer each
+      if (t0 != 0) return 0;
+      const int old = s.T - s.rows, nt = a.units.tiles(s), nk = a.units.of(s), t1 = min(old / 128 + 1, nk), n = nk - t1;
+      const long long G = a.units.G, skipped = G * (static_cast<long long>(t1) * n + static_cast<long long>(n) * (n - 1) / 2) - n * ((old * G + 127) / 128);
+      return static_cast<long long>(nt) * nk - skipped;
+    } else {
+      long long x = 0;
+      for (int t = t0; t < a.units.of(s); t += dt) x += a.units.steps(s, t);
+      return x;
+    }
+  };
+  const bool by_lane = alone || K == kKeys;
+  W = 0;
+  if (by_lane) {
+    for (int b0 = 0; b0 < p.B; b0 += 32) W += sum(b0 + lane < p.B ? steps_of(weights_seq(p, b0 + lane, report), 0, 1) : 0);
+  } else {
+    for (int b = 0; b < p.B; ++b) W += sum(steps_of(weights_seq(p, b, report && lane == 0), lane, 32));
+  }
+  W *= p.Hkv;
+  N = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
+  if (k >= N) return a;
+  const long long w0 = W * k / N;
+  a.left = W * (k + 1) / N - w0;
+  long long base = 0, mine = 0;  // places before sequence b, and one KV head's of it
+  bool found = false;
+  for (int b0 = 0; b0 < p.B && !found; b0 += by_lane ? 32 : 1) {
+    long long x = 0;
+    if (by_lane) x = b0 + lane < p.B ? steps_of(weights_seq(p, b0 + lane, false), 0, 1) : 0;
+    else x = sum(steps_of(weights_seq(p, b0, false), lane, 32));
+    long long upto = x;
+    if (by_lane) {
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += y;
+      }
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, base + upto * p.Hkv > w0);
+    if (past != 0) {
+      const int j = by_lane ? __ffs(past) - 1 : 0;
+      a.b = b0 + j;
+      mine = __shfl_sync(0xffffffffu, x, j);
+      base += (__shfl_sync(0xffffffffu, upto, j) - mine) * p.Hkv;
+      found = true;
+    } else {
+      base += __shfl_sync(0xffffffffu, upto, 31) * p.Hkv;
+    }
+  }
+  a.seq = weights_seq(p, a.b, false);
+  a.of = a.units.of(a.seq);
+  a.g = static_cast<int>((w0 - base) / mine);
+  long long rem = w0 - base - a.g * mine;
+  long long before = 0;  // steps of the units before t0
+  for (int t0 = 0; t0 < a.of; t0 += 32) {
+    const int n = t0 + lane < a.of ? a.units.steps(a.seq, t0 + lane) : 0;
+    long long upto = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, upto, off);
+      if (lane >= off) upto += y;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + upto > rem);
+    if (past != 0) {
+      const int j = __ffs(past) - 1;
+      a.t = t0 + j;
+      a.count = __shfl_sync(0xffffffffu, n, j);
+      const long long at = before + __shfl_sync(0xffffffffu, upto, j) - a.count;
+      a.s = static_cast<int>(rem - at);
+      a.unit0 = w0 - a.s;
+      break;
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return a;
 }
 
-constexpr int kThreads = 256;
+// The CTA whose range holds place w: the largest k with floor(W k / N) <= w.
+FKV_DEV int cta_of(long long w, long long W, int N) { return static_cast<int>(((w + 1) * N - 1) / W); }
 
-// grid (query rows and heads of a sequence, 1, sequences)
+// A unit's pieces lie at place 2 k0 + 1 (the CTA that begins it, whose last unit it is) and at 2 k of those behind it.
+FKV_DEV long long piece_place(int k, int k0) { return k == k0 ? 2LL * k + 1 : 2LL * k; }
+
+// Add 1 to a counter with release and acquire semantics at GPU scope.
+FKV_DEV int count_piece(int32_t* p) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+  return old;
+}
+
+// Index of row tile i of (b, g) among the tiles of the workspace.
+FKV_DEV size_t tile_index(const BlockWeightsParams& p, const WeightsSeq& s, int b, int g, int i) {
+  return (static_cast<size_t>(s.r0) * (p.Hq / p.Hkv) / 128 + b + i) * p.Hkv + g;
+}
+
+// The id of block `blk` of sequence b, reported and 0 where it is out of range.
+FKV_DEV int block_id(const BlockWeightsParams& p, int b, int blk) {
+  const int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
+  if (id >= 0 && id < p.num_blocks) return id;
+  raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+  return 0;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads) stats_kernel(const BlockWeightsParams p) {
-  __shared__ float m_s[kThreads / 32], l_s[kThreads / 32];
+struct Shape {
+  static constexpr int RB = D < 128 ? D : 128;   // bytes of one swizzled row
+  static constexpr int NSUB = D / RB;            // sub-tiles along head_dim
+  static constexpr int SWZ = RB == 128 ? 2 : 4;  // descriptor swizzle mode (128 B / 64 B)
+  static constexpr int SUB = 128 * RB;           // bytes of one 128-row sub-tile
+  static constexpr int TILE = 128 * D;           // bytes of 128 keys, or of a term of 128 query rows
+};
+
+// Bytes of a tile's parameters: (c, c, -lse, -lse) of two rows at a time.
+constexpr int kRowBytes = 128 * 8;
+
+// ---------------------------------------------------------------- query_kernel
+
+// The rows of every tile as two e4m3 terms in the products' layout, c of each; -lse of the rows that there are not is
+// -infinity, which makes their weights zero.  A CTA takes 16 rows of a tile, 8 threads each.
+template <int D>
+__global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) {
+  using S = Shape<D>;
   griddep_wait();
-  const int b = blockIdx.z;
-  const WeightsSeq s = weights_seq(p, b, blockIdx.x == 0 && threadIdx.x == 0);
-  const int t = blockIdx.x / p.Hq, h = blockIdx.x - t * p.Hq;
-  if (t >= s.rows) return;
-  const __nv_bfloat16* q = p.q + (static_cast<size_t>(s.r0 + t) * p.Hq + h) * D;
-  const int last = s.T - s.rows + t;
-  float m = -3e38f, l = 0.f;
-  for (int j = threadIdx.x; j <= last; j += kThreads) {
-    const float x = score<D>(p, q, b, h / (p.Hq / p.Hkv), j);
-    const float mx = fmaxf(m, x);
-    l = l * exp2f(m - mx) + exp2f(x - mx);
-    m = mx;
+  griddep_launch_dependents();
+  const int G = p.Hq / p.Hkv, lane = threadIdx.x & 31, g = blockIdx.y;
+  const int tile = blockIdx.x / 8, row0 = (blockIdx.x & 7) * 16;
+  if (blockIdx.x == 0 && g == 0)
+    for (int i = threadIdx.x; i < 2 * p.slots; i += 128) p.done[i] = 0;
+  // the last sequence whose tiles begin at or before this one
+  int b = -1;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const bool before = b0 + lane < p.B && static_cast<long long>(p.cu[b0 + lane]) * G / 128 + b0 + lane <= tile;
+    const unsigned m = __ballot_sync(0xffffffffu, before);
+    if (m == 0) break;
+    b = b0 + 31 - __clz(m);
   }
-  for (int off = 16; off > 0; off >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, off), l2 = __shfl_xor_sync(0xffffffffu, l, off), mx = fmaxf(m, m2);
-    l = l * exp2f(m - mx) + l2 * exp2f(m2 - mx);
-    m = mx;
+  if (b < 0) return;
+  const WeightsSeq s = weights_seq(p, b, false);
+  const long long R = static_cast<long long>(s.rows) * G;
+  const long long i = tile - (static_cast<long long>(s.r0) * G / 128 + b);
+  if (i < 0 || i * 128 >= R) return;
+  const int row = row0 + (threadIdx.x >> 3);
+  const long long r = i * 128 + row;
+  constexpr int NCH = (D / 16 + 7) / 8;  // 16-element chunks of a row per thread
+  uint32_t in[NCH][8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int cc = 0; cc < NCH; ++cc) {
+    const int ch = (threadIdx.x & 7) + 8 * cc;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
+    if (r < R && ch < D / 16) {
+      const long long token = r / G;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((s.r0 + token) * p.Hq + g * G + (r - token * G)) * D) + 2 * ch;
+      const uint4 x = src[0], y = src[1];
+      in[cc][0] = x.x; in[cc][1] = x.y; in[cc][2] = x.z; in[cc][3] = x.w;
+      in[cc][4] = y.x; in[cc][5] = y.y; in[cc][6] = y.z; in[cc][7] = y.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
   }
-  if ((threadIdx.x & 31) == 0) {
-    m_s[threadIdx.x >> 5] = m;
-    l_s[threadIdx.x >> 5] = l;
+#pragma unroll
+  for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  const int e = query_exponent(amax);  // q = q' 2^e
+  const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  const size_t at = tile_index(p, s, b, g, static_cast<int>(i));
+  if ((threadIdx.x & 7) == 0) {
+    // a row with a NaN or an infinity makes its scores NaN
+    float* out = p.rows + at * 256 + (row >> 1) * 4 + (row & 1);
+    out[0] = r >= R ? 0.f : amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+    if (r >= R) out[2] = -INFINITY;
+  }
+  uint8_t* dst = p.q_tiles + at * 2 * S::TILE;
+#pragma unroll
+  for (int cc = 0; cc < NCH; ++cc) {
+    const int c = (threadIdx.x & 7) + 8 * cc;
+    if (c >= D / 16) continue;
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
+      split4_query(make_float2(x0.x * down, x0.y * down), make_float2(x1.x * down, x1.y * down), hi[j], lo[j]);
+    }
+    const int byte = c * 16;
+    uint8_t* x = dst + (byte / S::RB) * S::SUB + swz(static_cast<uint32_t>(row * S::RB + byte % S::RB), S::RB);
+    *reinterpret_cast<uint4*>(x) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(x + S::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+// ---------------------------------------------------------------- the two passes over many rows
+
+template <int D, Kind K>
+struct PassCfg : Shape<D> {
+  using S = Shape<D>;
+  static constexpr int QT = 2 * S::TILE;                        // both terms of a row tile
+  static constexpr int STAY = K == kRows ? QT : S::TILE;        // the unit's own tile, two buffers
+  static constexpr int STREAM = K == kRows ? S::TILE : QT + kRowBytes;
+  static constexpr int NS = K == kRows && D == 64 ? 4 : 2;      // stages of the other one
+  static constexpr int CTAS = D <= 128 ? 2 : 1;                 // per SM: 256 columns of tensor memory each
+  static constexpr int SCN = 8;                                 // slots of K scales: the copies run at most NS + 2 tiles ahead
+  static constexpr int OFF_STAY = 0;
+  static constexpr int OFF_STREAM = OFF_STAY + 2 * STAY;
+  static constexpr int OFF_SC = OFF_STREAM + NS * STREAM;
+  static constexpr int OFF_BAR = OFF_SC + SCN * 8 * 4;
+  static constexpr int NBAR = 8 + 2 * NS + SCN + 1;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 64;
+  static constexpr uint32_t IDESC = idesc_e4m3_f32(128, 128, 0, 0);
+  static_assert(SCN > NS + 2, "a slot is rewritten only after its reader is done");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of the resident CTAs");
+};
+
+constexpr int kPassThreads = 320, kReaders = 8;  // warps 0-7 read the scores, 8 copies, 9 issues the products
+
+template <int D, Kind K>
+__global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
+    pass_kernel(const __grid_constant__ BlockWeightsParams p, const __grid_constant__ CUtensorMap tmk) {
+  using C = PassCfg<D, K>;
+  using Place = Walk<K, 128>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sStay = smem + C::OFF_STAY;
+  uint8_t* sStream = smem + C::OFF_STREAM;
+  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* y_full = bars + 0;    // [2] the tile of piece r in buffer r % 2
+  uint64_t* y_empty = bars + 2;   // [2]
+  uint64_t* s_full = bars + 4;    // [2] the scores of step u in buffer u % 2
+  uint64_t* s_free = bars + 6;    // [2]
+  uint64_t* x_full = bars + 8;    // [NS] the streamed tile of step u in stage u % NS
+  uint64_t* x_empty = x_full + C::NS;
+  uint64_t* sc_full = x_empty + C::NS;  // [SCN] K scales of step u in slot u % SCN
+  uint64_t* mma_done = sc_full + C::SCN;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* last_s = abort_s + 1;
+  volatile int* pend_s = abort_s + 2;  // [2] {pieces, first CTA, b, g, t} of the range's first and last unit, if they have several
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&y_full[i], 1);
+      mbar_init(&y_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kReaders);
+    }
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&x_full[i], 1);
+      mbar_init(&x_empty[i], K == kKeys ? 1 + kReaders : 1);  // (the rows' parameters are read by the readers)
+    }
+    for (int i = 0; i < C::SCN; ++i) mbar_init(&sc_full[i], 1);
+    mbar_init(mma_done, 1);
+    *abort_s = 0;
+    pend_s[0] = pend_s[5] = 0;
+    fence_mbar_init();
+  }
+  // The tensor memory is taken after the wait: before it, it could be what a CTA of the kernel before still needs.
+  griddep_wait();
+  if (warp == 9) {
+    tmem_alloc(tmem_slot, 256);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  long long W;
+  int N;
+  Place at = first_step<K, 128>(p, k, W, N, K == kRows && k == 0 && warp == 0);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  const int G = p.Hq / p.Hkv;
+  const long long n = at.left;  // steps of this CTA
+  int32_t* done = p.done + (K == kRows ? 0 : p.slots);
+
+  if (n == 0) {
+    // more CTAs than steps
+  } else if (warp < kReaders) {
+    // ============================================================ the scores' readers
+    // warp w: tensor memory lanes rb .. rb + 15, lanes l and l + 16 each half of their columns
+    const int hf = lane >> 4, rb = (warp & 3) * 32 + (warp >> 2) * 16, i = rb + (lane & 15);
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(rb) << 16);
+    bool ok = true;
+    float m = -kHuge, l = 0.f;              // pass 0: the row's maximum and sum (of this thread's columns)
+    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;  // pass 1: the key's sum
+    float mine = 0.f;                       // c of the row; ks of the key
+    int limit = 0;                          // keys that the row sees; the first row that sees the key
+    for (int u = 0; u < n; ++u) {
+      if (at.begins()) {
+        const int old = at.seq.T - at.seq.rows;
+        if constexpr (K == kRows) {
+          const long long r = 128LL * at.t + i;
+          const bool is_row = r < static_cast<long long>(at.seq.rows) * G;
+          limit = is_row ? old + static_cast<int>(r / G) + 1 : 0;
+          mine = is_row ? p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1)] : 0.f;
+          m = -kHuge;
+          l = 0.f;
+        } else {
+          const int key = 128 * at.t + i;
+          mine = key < at.seq.T ? p.k_scale[static_cast<size_t>(block_id(p, at.b, key >> 4)) * p.Hkv + at.g] : 0.f;
+          limit = static_cast<int>(min(max(static_cast<long long>(key) - old, 0LL) * G, static_cast<long long>(INT32_MAX)));
+          acc0 = acc1 = make_float2(0.f, 0.f);
+        }
+      }
+      if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+      const int sb = u & 1;
+      float cb[4];
+      if constexpr (K == kRows) {
+        if (!pf_wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1)) { ok = false; break; }
+        const float4 ks4 = *reinterpret_cast<const float4*>(sSc + (u % C::SCN) * 8 + 4 * hf);
+        // (plus 2^-126, so that a hidden score of -inf stays one where the product is zero)
+        constexpr float kLeast = 1.17549435e-38f;
+        cb[0] = fmaf(mine, ks4.x, kLeast);
+        cb[1] = fmaf(mine, ks4.y, kLeast);
+        cb[2] = fmaf(mine, ks4.z, kLeast);
+        cb[3] = fmaf(mine, ks4.w, kLeast);
+      }
+      if (!pf_wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
+      tc_fence_after();
+      const int st = u % C::NS;
+      // first column of this thread's half: its key, or its row
+      const int c0 = 128 * (K == kRows ? at.s : at.units.first(at.seq, at.t) + at.s) + 64 * hf;
+      const bool partly = K == kRows ? limit < c0 + 64 : limit > c0;
+      const bool any_partly = __any_sync(0xffffffffu, partly);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float v[32];
+        tmem_ld32_16x2<64>(lane_base + 128 * sb + 32 * c, v);
+        tmem_ld_wait();
+        if (c == 1) {
+          tc_fence_before();
+          mbar_arrive_warp(&s_free[sb]);
+        }
+        if constexpr (K == kRows) {
+          if (any_partly) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (c0 + 32 * c + j >= limit) v[j] = -INFINITY;
+          }
+          const float a = cb[2 * c], b2 = cb[2 * c + 1];
+          const float top = fmaxf(m, fmaxf(max_tree<16>(v) * a, max_tree<16>(v + 16) * b2));
+          float2 s0 = make_float2(l * ex2(m - top), 0.f), s1 = make_float2(0.f, 0.f);
+          m = top;
+          const float2 a2 = make_float2(a, a), bb = make_float2(b2, b2), t2 = make_float2(-top, -top);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), a2, t2), y = __ffma2_rn(make_float2(v[16 + j], v[17 + j]), bb, t2);
+            s0 = __fadd2_rn(s0, make_float2(ex2(x.x), ex2(x.y)));
+            s1 = __fadd2_rn(s1, make_float2(ex2(y.x), ex2(y.y)));
+          }
+          l = (s0.x + s0.y) + (s1.x + s1.y);
+        } else {
+          const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + 32 * hf + 16 * c;
+          const float2 ks = make_float2(mine, mine);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 r0 = rp[j / 2], r1 = rp[j / 2 + 1];
+            float2 x = __ffma2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), ks), make_float2(r0.x, r0.y), make_float2(r0.z, r0.w));
+            float2 y = __ffma2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), ks), make_float2(r1.x, r1.y), make_float2(r1.z, r1.w));
+            if (any_partly) {
+              const int r = c0 + 32 * c + j;
+              if (r < limit) x.x = -INFINITY;
+              if (r + 1 < limit) x.y = -INFINITY;
+              if (r + 2 < limit) y.x = -INFINITY;
+              if (r + 3 < limit) y.y = -INFINITY;
+            }
+            acc0 = __fadd2_rn(acc0, make_float2(ex2(x.x), ex2(x.y)));
+            acc1 = __fadd2_rn(acc1, make_float2(ex2(y.x), ex2(y.y)));
+          }
+        }
+      }
+      if constexpr (K == kKeys) mbar_arrive_warp(&x_empty[st]);
+      if (at.ends()) {
+        const int k0 = cta_of(at.unit0, W, N), ns = cta_of(at.unit0 + at.count - 1, W, N) - k0 + 1;
+        const long long place = piece_place(k, k0);
+        if constexpr (K == kRows) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, m, 16), l2 = __shfl_xor_sync(0xffffffffu, l, 16);
+          const float top = fmaxf(m, m2), sum = l * ex2(m - top) + l2 * ex2(m2 - top);
+          if (hf == 0) {
+            if (ns > 1) p.pieces[place * 128 + i] = make_float2(top, sum);
+            else if (limit > 0) p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(top + lg2(sum));
+          }
+        } else {
+          float sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int key = 128 * at.t + i;
+          if (hf == 0) {
+            if (ns > 1) {
+              p.sums[place * 128 + i] = sum;
+            } else if (key < at.seq.T) {
+              float* w = p.weights + (static_cast<size_t>(at.b) * p.Hkv + at.g) * p.weights_len + key;
+              *w = key < at.seq.T - at.seq.rows && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
+            }
+          }
+        }
+        if (ns > 1 && threadIdx.x == 0) {
+          volatile int* pend = pend_s + (k == k0 ? 5 : 0);
+          pend[0] = ns;
+          pend[1] = k0;
+          pend[2] = at.b;
+          pend[3] = at.g;
+          pend[4] = at.t;
+        }
+      }
+      at.advance(p);
+    }
+    tmem_ld_wait();  // no load left in flight on an early exit
+    if (!ok) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    }
+  } else if (warp == 8) {
+    // ============================================================ copies
+    int stay_pieces = 0;            // pieces whose tile was requested
+    long long used = 0;             // steps whose streamed tile was requested
+    size_t held[C::NS];             // pass 1: the row tile that a stage holds
+#pragma unroll
+    for (int s = 0; s < C::NS; ++s) held[s] = ~static_cast<size_t>(0);
+    // a tile of 128 keys: a block per lane, blocks behind the sequence left as they are (their keys are hidden)
+    auto copy_keys = [&](uint8_t* dst, const Place& a, int tile, int id, uint64_t* full) {
+      const int nblk = min(8, ((a.seq.T + 15) >> 4) - 8 * tile);
+      if (lane == 0) mbar_arrive_expect_tx(full, nblk * 16 * D);
+      __syncwarp();
+      if (lane < nblk) {
+#pragma unroll
+        for (int s = 0; s < C::NSUB; ++s) tma_load_4d(dst + s * C::SUB + lane * 16 * C::RB, &tmk, s * C::RB, 0, a.g, id, full);
+      }
+    };
+    auto id_of = [&](const Place& a, int tile) -> int {
+      const int blk = 8 * tile + lane;
+      return a.left > 0 && lane < 8 && blk < (a.seq.T + 15) >> 4 ? block_id(p, a.b, blk) : -1;
+    };
+    auto scale_of = [&](const Place& a, int id) -> float { return id >= 0 ? p.k_scale[static_cast<size_t>(id) * p.Hkv + a.g] : 0.f; };
+    Place nx = at;
+    int id = 0, id_next = 0;
+    float ks = 0.f;
+    if constexpr (K == kRows) {
+      id = id_of(at, at.s);
+      ks = scale_of(at, id);
+      nx.advance(p);
+      id_next = id_of(nx, nx.s);
+    }
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      if (abort_warp(abort_s)) break;
+      if (at.begins()) {
+        const int yb = at.piece & 1;
+        if (at.piece >= 2 && !pf_wait_warp(&y_empty[yb], ((at.piece >> 1) - 1) & 1)) { ok = false; break; }
+        if constexpr (K == kRows) {
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&y_full[yb], C::QT);
+            bulk_g2s(sStay + yb * C::STAY, p.q_tiles + tile_index(p, at.seq, at.b, at.g, at.t) * C::QT, C::QT, &y_full[yb]);
+          }
+          __syncwarp();
+        } else {
+          copy_keys(sStay + yb * C::STAY, at, at.t, id_of(at, at.t), &y_full[yb]);
+        }
+        stay_pieces = at.piece + 1;
+      }
+      const int st = u % C::NS;
+      if (u >= C::NS && !pf_wait_warp(&x_empty[st], (u / C::NS - 1) & 1)) { ok = false; break; }
+      uint8_t* dst = sStream + st * C::STREAM;
+      if constexpr (K == kRows) {
+        copy_keys(dst, at, at.s, max(id, 0), &x_full[st]);
+        if (lane < 8) sSc[(u % C::SCN) * 8 + lane] = ks;
+        mbar_arrive_warp(&sc_full[u % C::SCN]);
+        id = id_next;
+        ks = scale_of(nx, id);
+        at = nx;
+        nx.advance(p);
+        id_next = id_of(nx, nx.s);
+      } else {
+        const size_t tile = tile_index(p, at.seq, at.b, at.g, at.units.first(at.seq, at.t) + at.s);
+        bool same = false;
+#pragma unroll
+        for (int s = 0; s < C::NS; ++s) {
+          if (s != st) continue;
+          same = held[s] == tile;
+          held[s] = tile;
+        }
+        if (lane == 0) {
+          if (same) {
+            mbar_arrive(&x_full[st]);
+          } else {
+            mbar_arrive_expect_tx(&x_full[st], C::QT + kRowBytes);
+            bulk_g2s(dst, p.q_tiles + tile * C::QT, C::QT, &x_full[st]);
+            bulk_g2s(dst + C::QT, p.rows + tile * 256, kRowBytes, &x_full[st]);
+          }
+        }
+        __syncwarp();
+        at.advance(p);
+      }
+      used = u + 1;
+    }
+    if (!ok) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    }
+    // let every copy land before the CTA can exit
+    if (lane == 0) {
+      for (int s = 0; s < C::NS; ++s)
+        if (used > s) pf_wait(&x_full[s], ((used - 1 - s) / C::NS) & 1);
+      for (int s = 0; s < 2; ++s)
+        if (stay_pieces > s) pf_wait(&y_full[s], ((stay_pieces - 1 - s) / 2) & 1);
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ products
+    const uint64_t dY = smem_desc(smem_u32(sStay), 16, 8 * C::RB, C::SWZ), dX = smem_desc(smem_u32(sStream), 16, 8 * C::RB, C::SWZ);
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      if ((u & 7) == 7 && abort_warp(abort_s)) break;
+      const int yb = at.piece & 1, st = u % C::NS, sb = u & 1;
+      if (at.begins()) ok = pf_wait_warp(&y_full[yb], (at.piece >> 1) & 1);
+      if (ok) ok = pf_wait_warp(&x_full[st], (u / C::NS) & 1);
+      if (ok && u >= 2) ok = pf_wait_warp(&s_free[sb], ((u >> 1) - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const int byte = kk * 32;
+            const uint32_t off = (byte / C::RB) * C::SUB + (byte % C::RB);
+            const uint64_t y = desc_add(dY, yb * C::STAY + (K == kRows ? term * C::TILE : 0) + off);
+            const uint64_t x = desc_add(dX, st * C::STREAM + (K == kKeys ? term * C::TILE : 0) + off);
+            umma_f8(tmem + 128 * sb, y, x, C::IDESC, (term > 0 || kk > 0) ? 1u : 0u);
+          }
+        umma_commit(&s_full[sb]);
+        umma_commit(&x_empty[st]);
+        if (at.ends()) umma_commit(&y_empty[yb]);
+      }
+      __syncwarp();
+      at.advance(p);
+    }
+    if (!ok) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    }
+    if (lane == 0) {  // every product issued here completes before the tensor memory is released
+      umma_commit(mma_done);
+      pf_wait(mma_done, 0);
+    }
+    __syncwarp();
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kThreads / 32; ++i) {
-      const float mx = fmaxf(m, m_s[i]);
-      l = l * exp2f(m - mx) + l_s[i] * exp2f(m_s[i] - mx);
-      m = mx;
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
+  }
+  // the CTA that brings a unit's last piece joins them
+  for (int j = 0; j < 2; ++j) {
+    const int ns = pend_s[5 * j], k0 = pend_s[5 * j + 1], b = pend_s[5 * j + 2], g = pend_s[5 * j + 3], t = pend_s[5 * j + 4];
+    if (ns == 0) continue;
+    if (threadIdx.x == 0) *last_s = count_piece(&done[k0]) == ns - 1;
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (*last_s && i < 128) {
+      const WeightsSeq s = weights_seq(p, b, false);
+      if constexpr (K == kRows) {
+        float m = -kHuge, l = 0.f;
+        for (int x = 0; x < ns; ++x) {
+          const float2 y = __ldcg(p.pieces + piece_place(k0 + x, k0) * 128 + i);
+          const float top = fmaxf(m, y.x);
+          l = l * ex2(m - top) + y.y * ex2(y.x - top);
+          m = top;
+        }
+        if (128LL * t + i < static_cast<long long>(s.rows) * G) p.rows[tile_index(p, s, b, g, t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(m + lg2(l));
+      } else {
+        float sum = 0.f;
+        for (int x = 0; x < ns; ++x) sum += __ldcg(p.sums + piece_place(k0 + x, k0) * 128 + i);
+        const int key = 128 * t + i;
+        if (key < s.T) {
+          float* w = p.weights + (static_cast<size_t>(b) * p.Hkv + g) * p.weights_len + key;
+          *w = key < s.T - s.rows && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
+        }
+      }
     }
-    p.lse[static_cast<size_t>(s.r0 + t) * p.Hq + h] = m + log2f(l);
+    __syncthreads();
   }
 }
 
-// grid (tiles of keys, KV heads, sequences)
-template <int D>
-__global__ void __launch_bounds__(kThreads) sums_kernel(const BlockWeightsParams p) {
-  griddep_wait();
-  const int b = blockIdx.z, g = blockIdx.y, j = blockIdx.x * kThreads + threadIdx.x;
-  const WeightsSeq s = weights_seq(p, b, false);
-  if (s.rows == 0 || j >= s.T) return;
-  const int G = p.Hq / p.Hkv, old = s.T - s.rows;
-  float* w = p.weights + (static_cast<size_t>(b) * p.Hkv + g) * p.weights_len + j;
-  float sum = 0.f;
-  for (int t = max(0, j - old); t < s.rows; ++t)
-    for (int h = g * G; h < (g + 1) * G; ++h) {
-      const size_t row = static_cast<size_t>(s.r0 + t) * p.Hq + h;
-      sum += exp2f(score<D>(p, p.q + row * D, b, g, j) - p.lse[row]);
+// ---------------------------------------------------------------- few rows
+
+// RN: rows (4, 8 or 16) that a key's scores are kept for.
+template <int D, int RN>
+struct ScoreCfg : Shape<D> {
+  using S = Shape<D>;
+  static constexpr int LO = RN < 8 ? 8 : RN;                    // first row (column) of the query's second term
+  static constexpr int NP = 2 * LO;                             // the MMA's N
+  static constexpr int NHALF = D == 64 ? 2 : 1;                 // products of 128 keys per tile
+  static constexpr int BN = 128 * NHALF, TPB = BN / 16;         // keys and blocks of a tile
+  static constexpr int KSUB = BN * S::RB, KTILE = BN * D;
+  static constexpr int NS = D <= 128 ? 4 : 3;
+  static constexpr int CTAS = D <= 128 ? 3 : 2;
+  static constexpr int SCN = 8;
+  static constexpr int QSUB = NP * S::RB;
+  static constexpr int TM_COLS = 2 * NHALF * NP <= 32 ? 32 : 2 * NHALF * NP <= 64 ? 64 : 128;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = (OFF_Q + S::NSUB * QSUB + 1023) / 1024 * 1024;
+  static constexpr int OFF_SC = OFF_K + NS * KTILE;
+  static constexpr int OFF_C = OFF_SC + SCN * TPB * 4;          // c of the rows [16]
+  static constexpr int OFF_RED = OFF_C + 16 * 4;                // [4 warps][RN] float2
+  static constexpr int OFF_BAR = OFF_RED + 4 * RN * 8;
+  static constexpr int NBAR = 6 + 2 * NS + SCN;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM = OFF_MISC + 16;
+  static constexpr uint32_t IDESC = idesc_e4m3_f32(128, NP, 0, 0);
+  static_assert(SCN > NS + 2 && OFF_BAR % 8 == 0, "slots");
+  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of the resident CTAs");
+};
+
+constexpr int kScoreThreads = 192;  // warps 0-3 read the scores, 4 copies, 5 issues the products
+
+FKV_DEV void tmem_ld4(uint32_t addr, float* v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(addr));
+}
+
+// The scores of the rows of every (sequence, KV head) for its keys, [key][RN] in base 2 (-infinity where the row does not
+// see the key), and each piece's maxima and sums.  The products are taken transposed, S^T = K8 (hi | lo)^T: a thread owns a key, and
+// keeps its own running maximum and sum of every row, which meet at a piece's end.
+template <int D, int RN>
+__global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
+    score_kernel(const __grid_constant__ BlockWeightsParams p, const __grid_constant__ CUtensorMap tmk) {
+  using C = ScoreCfg<D, RN>;
+  using Place = Walk<kScores, C::BN>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);
+  float* sC = reinterpret_cast<float*>(smem + C::OFF_C);
+  float2* sRed = reinterpret_cast<float2*>(smem + C::OFF_RED);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars + 0;    // the query of piece r
+  uint64_t* s_full = bars + 1;    // [2]
+  uint64_t* s_free = bars + 3;    // [2]
+  uint64_t* mma_done = bars + 5;
+  uint64_t* k_full = bars + 6;
+  uint64_t* k_empty = k_full + C::NS;
+  uint64_t* sc_full = k_empty + C::NS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 4);
     }
-  *w = j < old && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
+    mbar_init(mma_done, 1);
+    for (int i = 0; i < C::NS; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+    }
+    for (int i = 0; i < C::SCN; ++i) mbar_init(&sc_full[i], 1);
+    *abort_s = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();  // (the tensor memory is taken after it, as in pass_kernel)
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, C::TM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  long long W;
+  int N;
+  Place at = first_step<kScores, C::BN>(p, k, W, N, k == 0 && warp == 0);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  const int G = p.Hq / p.Hkv;
+  const long long n = at.left;
+
+  if (n == 0) {
+    // more CTAs than tiles
+  } else if (warp < 4) {
+    // ============================================================ the scores' readers
+    const int i = threadIdx.x;  // key i (and 128 + i) of a tile
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    float m[RN], l[RN];
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      if (at.begins()) {
+        // ---- the piece's query: row r scaled to (224, 448], as two terms, 8 threads per row (the products with the
+        // last piece's query are done: their scores were read)
+        const int row = i >> 3, R = at.seq.rows * G;
+        constexpr int NCH = (D / 16 + 7) / 8;
+        uint32_t in[NCH][8];
+        uint32_t amax = 0;
+#pragma unroll
+        for (int cc = 0; cc < NCH; ++cc) {
+          const int ch = (i & 7) + 8 * cc;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
+          if (row < R && ch < D / 16) {
+            const int token = row / G;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<size_t>(at.seq.r0) + token) * p.Hq + at.g * G + (row - token * G)) * D) + 2 * ch;
+            const uint4 x = src[0], y = src[1];
+            in[cc][0] = x.x; in[cc][1] = x.y; in[cc][2] = x.z; in[cc][3] = x.w;
+            in[cc][4] = y.x; in[cc][5] = y.y; in[cc][6] = y.z; in[cc][7] = y.w;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
+        }
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+        const int e = query_exponent(amax);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        if ((i & 7) == 0)
+          sC[row] = amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int cc = 0; cc < NCH; ++cc) {
+          const int c = (i & 7) + 8 * cc;
+          if (c >= D / 16 || row >= C::LO) continue;
+          uint32_t wh[4], wl[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
+            split4_query(make_float2(x0.x * down, x0.y * down), make_float2(x1.x * down, x1.y * down), wh[j], wl[j]);
+          }
+          const int byte = c * 16;
+          uint8_t* sub = sQ + (byte / C::RB) * C::QSUB;
+          *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>(row * C::RB + byte % C::RB), C::RB)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+          *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>((C::LO + row) * C::RB + byte % C::RB), C::RB)) =
+              make_uint4(wl[0], wl[1], wl[2], wl[3]);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive_warp(q_full);
+        if (!wait_warp(q_full, at.piece & 1)) { ok = false; break; }  // every warp's rows and c are there
+#pragma unroll
+        for (int r = 0; r < RN; ++r) {
+          m[r] = -kHuge;
+          l[r] = 0.f;
+        }
+      }
+      if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+      const int sb = u & 1;
+      if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1) || !wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int hh = 0; hh < C::NHALF; ++hh) {
+        float v[2 * RN];
+        const uint32_t col = lane_base + (sb * C::NHALF + hh) * C::NP;
+        if constexpr (RN == 4) {
+          tmem_ld4(col, v);
+          tmem_ld4(col + C::LO, v + 4);
+        } else if constexpr (RN == 8) {
+          tmem_ld16(col, v);
+        } else {
+          tmem_ld32(col, v);
+        }
+        const float ks = sSc[(u % C::SCN) * C::TPB + 8 * hh + (i >> 4)];
+        const int key = C::BN * at.s + 128 * hh + i;
+        tmem_ld_wait();
+        if (hh + 1 == C::NHALF) {
+          tc_fence_before();
+          mbar_arrive_warp(&s_free[sb]);
+        }
+        // the first row that sees the key (none behind the sequence)
+        const int from = key < at.seq.T ? max(key - (at.seq.T - at.seq.rows), 0) * G : RN;
+#pragma unroll
+        for (int r = 0; r < RN; ++r) {
+          float x = (v[r] + v[RN + r]) * (sC[r] * ks);
+          if (r < from) x = -INFINITY;
+          v[r] = x;
+          // one exponential: of the smaller against the larger
+          const float e = ex2(-fabsf(x - m[r]));
+          l[r] = x > m[r] ? fmaf(l[r], e, 1.f) : l[r] + e;
+          m[r] = fmaxf(m[r], x);
+        }
+        if (key < at.seq.T) {
+          float4* dst = reinterpret_cast<float4*>(p.scores + ((static_cast<size_t>(at.b) * p.Hkv + at.g) * p.max_blocks * 16 + key) * RN);
+#pragma unroll
+          for (int r = 0; r < RN; r += 4) dst[r / 4] = make_float4(v[r], v[r + 1], v[r + 2], v[r + 3]);
+        }
+      }
+      if (at.ends()) {
+        const int k0 = cta_of(at.unit0, W, N), ns = cta_of(at.unit0 + at.count - 1, W, N) - k0 + 1;
+        if (i == 0 && k == k0) p.units[at.b * p.Hkv + at.g] = make_int2(k0, ns);
+#pragma unroll
+        for (int r = 0; r < RN; ++r) {
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m[r], off), l2 = __shfl_xor_sync(0xffffffffu, l[r], off), top = fmaxf(m[r], m2);
+            l[r] = l[r] * ex2(m[r] - top) + l2 * ex2(m2 - top);
+            m[r] = top;
+          }
+          if (lane == 0) sRed[warp * RN + r] = make_float2(m[r], l[r]);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (i < RN) {
+          float M = -kHuge, L = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const float2 y = sRed[w * RN + i];
+            const float top = fmaxf(M, y.x);
+            L = L * ex2(M - top) + y.y * ex2(y.x - top);
+            M = top;
+          }
+          // a unit that begins here lies at the odd place even if it ends here too
+          p.pieces[(k == k0 && ns == 1 ? 2LL * p.slots + static_cast<long long>(at.b) * p.Hkv + at.g : piece_place(k, k0)) * 16 + i] = make_float2(M, L);
+        }
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      }
+      at.advance(p);
+    }
+    tmem_ld_wait();
+    if (!ok) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    }
+  } else if (warp == 4) {
+    // ============================================================ K copies and scales (ids and scales read a tile ahead)
+    auto blocks_of = [&](const Place& a) { return a.left > 0 ? min(C::TPB, ((a.seq.T + 15) >> 4) - C::TPB * a.s) : 0; };
+    auto id_of = [&](const Place& a) -> int { return lane < blocks_of(a) ? block_id(p, a.b, C::TPB * a.s + lane) : -1; };
+    auto scale_of = [&](const Place& a, int id) -> float { return id >= 0 ? p.k_scale[static_cast<size_t>(id) * p.Hkv + a.g] : 0.f; };
+    int id = id_of(at);
+    float ks = scale_of(at, id);
+    Place nx = at;
+    nx.advance(p);
+    int id_next = id_of(nx);
+    long long used = 0;
+    for (int u = 0; u < n; ++u) {
+      if (abort_warp(abort_s)) break;
+      const int st = u % C::NS;
+      if (u >= C::NS && !wait_warp(&k_empty[st], (u / C::NS - 1) & 1)) {
+        if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+        *abort_s = 1;
+        break;
+      }
+      const int nblk = blocks_of(at);
+      if (lane == 0) mbar_arrive_expect_tx(&k_full[st], nblk * 16 * D);
+      __syncwarp();
+      if (lane < nblk) {
+#pragma unroll
+        for (int s = 0; s < C::NSUB; ++s) tma_load_4d(sK + st * C::KTILE + s * C::KSUB + lane * 16 * C::RB, &tmk, s * C::RB, 0, at.g, id, &k_full[st]);
+      }
+      used = u + 1;
+      if (lane < C::TPB) sSc[(u % C::SCN) * C::TPB + lane] = ks;
+      mbar_arrive_warp(&sc_full[u % C::SCN]);
+      id = id_next;
+      ks = scale_of(nx, id);
+      at = nx;
+      nx.advance(p);
+      id_next = id_of(nx);
+    }
+    if (lane == 0)
+      for (int s = 0; s < C::NS; ++s)
+        if (used > s) wait_ns(&k_full[s], ((used - 1 - s) / C::NS) & 1);
+    __syncwarp();
+  } else {
+    // ============================================================ products
+    const uint64_t dK = smem_desc(smem_u32(sK), 16, 8 * C::RB, C::SWZ), dQ = smem_desc(smem_u32(sQ), 16, 8 * C::RB, C::SWZ);
+    bool ok = true;
+    for (int u = 0; u < n; ++u) {
+      if ((u & 7) == 7 && abort_warp(abort_s)) break;
+      const int st = u % C::NS, sb = u & 1;
+      if (at.begins()) ok = wait_warp(q_full, at.piece & 1);
+      if (ok) ok = wait_warp(&k_full[st], (u / C::NS) & 1);
+      if (ok && u >= 2) ok = wait_warp(&s_free[sb], ((u >> 1) - 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int hh = 0; hh < C::NHALF; ++hh)
+#pragma unroll
+          for (int kk = 0; kk < D / 32; ++kk) {
+            const int byte = kk * 32;
+            umma_f8(tmem + (sb * C::NHALF + hh) * C::NP,
+                    desc_add(dK, st * C::KTILE + (byte / C::RB) * C::KSUB + hh * 128 * C::RB + byte % C::RB),
+                    desc_add(dQ, (byte / C::RB) * C::QSUB + byte % C::RB), C::IDESC, kk > 0 ? 1u : 0u);
+          }
+        umma_commit(&s_full[sb]);
+        umma_commit(&k_empty[st]);
+      }
+      __syncwarp();
+      at.advance(p);
+    }
+    if (!ok) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
+    }
+    if (lane == 0) {
+      umma_commit(mma_done);
+      wait_ns(mma_done, 0);
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == 5) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+}
+
+constexpr int kGatherThreads = 256, kGatherKeys = 4 * kGatherThreads;
+
+// w_j from the scores: grid (kGatherKeys keys each, KV heads, sequences).
+template <int RN>
+__global__ void __launch_bounds__(kGatherThreads) gather_kernel(const BlockWeightsParams p) {
+  __shared__ float lse_s[16];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.z, g = blockIdx.y, G = p.Hq / p.Hkv;
+  const WeightsSeq s = weights_seq(p, b, false);
+  if (s.rows == 0 || static_cast<long long>(blockIdx.x) * kGatherKeys >= s.T) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const size_t unit = static_cast<size_t>(b) * p.Hkv + g;
+  const int2 at = p.units[unit];
+  for (int r = warp; r < RN; r += kGatherThreads / 32) {
+    float m = -kHuge, l = 0.f;
+    for (int x = lane; x < at.y; x += 32) {
+      const float2 y = p.pieces[(at.y == 1 ? 2LL * p.slots + static_cast<long long>(unit) : piece_place(at.x + x, at.x)) * 16 + r];
+      const float top = fmaxf(m, y.x);
+      l = l * ex2(m - top) + y.y * ex2(y.x - top);
+      m = top;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float m2 = __shfl_xor_sync(0xffffffffu, m, off), l2 = __shfl_xor_sync(0xffffffffu, l, off), top = fmaxf(m, m2);
+      l = l * ex2(m - top) + l2 * ex2(m2 - top);
+      m = top;
+    }
+    if (lane == 0) lse_s[r] = r < s.rows * G ? m + lg2(l) : INFINITY;
+  }
+  __syncthreads();
+  float lse[RN];
+#pragma unroll
+  for (int r = 0; r < RN; ++r) lse[r] = lse_s[r];
+  const float4* scores = reinterpret_cast<const float4*>(p.scores + unit * p.max_blocks * 16 * RN);
+  float* weights = p.weights + unit * p.weights_len;
+#pragma unroll
+  for (int x = 0; x < kGatherKeys / kGatherThreads; ++x) {
+    const long long key = static_cast<long long>(blockIdx.x) * kGatherKeys + x * kGatherThreads + threadIdx.x;
+    if (key >= s.T) break;
+    float sum = 0.f;
+#pragma unroll
+    for (int r = 0; r < RN; r += 4) {
+      const float4 y = scores[key * (RN / 4) + r / 4];
+      const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum += v[j] == -INFINITY ? 0.f : ex2(v[j] - lse[r + j]);
+    }
+    weights[key] = key < s.T - s.rows && p.decay != 0.f ? fmaf(p.decay, weights[key], sum) : sum;
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+constexpr int kFewRows = 16;
+
+// Rows that a key's scores are kept for; 0: too many, pass by pass.
+int rows_kept(int max_q_len, int G) {
+  const long long R = static_cast<long long>(max_q_len) * G;
+  return R <= 4 ? 4 : R <= 8 ? 8 : R <= kFewRows ? 16 : 0;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+// The workspace's parts; returns its bytes.
+size_t lay_out(BlockWeightsParams* p, uint8_t* base, int B, int total_q, int max_q_len, int Hq, int Hkv, int D, long long keys, int slots) {
+  const int G = Hq / Hkv, RN = rows_kept(max_q_len, G);
+  size_t at = 0;
+  auto part = [&](size_t bytes) {
+    uint8_t* x = base ? base + at : nullptr;
+    at += up256(bytes);
+    return x;
+  };
+  const size_t units = static_cast<size_t>(B) * Hkv;
+  if (RN > 0) {
+    uint8_t* u = part(units * sizeof(int2));
+    uint8_t* pieces = part((2 * static_cast<size_t>(slots) + units) * 16 * sizeof(float2));
+    uint8_t* scores = part(units * keys * RN * sizeof(float));
+    if (p) {
+      p->units = reinterpret_cast<int2*>(u);
+      p->pieces = reinterpret_cast<float2*>(pieces);
+      p->scores = reinterpret_cast<float*>(scores);
+    }
+  } else {
+    const size_t tiles = (static_cast<size_t>(total_q) * G / 128 + B) * Hkv;
+    uint8_t* done = part(2 * static_cast<size_t>(slots) * sizeof(int32_t));
+    uint8_t* pieces = part(2 * static_cast<size_t>(slots) * 128 * sizeof(float2));
+    uint8_t* sums = part(2 * static_cast<size_t>(slots) * 128 * sizeof(float));
+    uint8_t* rows = part(tiles * kRowBytes);
+    uint8_t* q = part(tiles * 256 * D);
+    if (p) {
+      p->done = reinterpret_cast<int32_t*>(done);
+      p->pieces = reinterpret_cast<float2*>(pieces);
+      p->sums = reinterpret_cast<float*>(sums);
+      p->rows = reinterpret_cast<float*>(rows);
+      p->q_tiles = q;
+    }
+  }
+  return at;
+}
+
+template <typename Kernel>
+cudaError_t launch_tc(Kernel kern, int grid, int threads, int smem, const BlockWeightsParams& p, const CUtensorMap& tmk, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(grid), dim3(threads), smem, s, p, tmk);
+}
+
+template <int D, int RN>
+cudaError_t launch_few(const BlockWeightsParams& p, const CUtensorMap& tmk, int num_sms, cudaStream_t s) {
+  using C = ScoreCfg<D, RN>;
+  const cudaError_t e = launch_tc(score_kernel<D, RN>, C::CTAS * num_sms, kScoreThreads, C::SMEM, p, tmk, s);
+  if (e != cudaSuccess) return e;
+  const long long keys = std::min(p.max_blocks * 16LL, static_cast<long long>(p.weights_len));
+  return launch_dependent(gather_kernel<RN>, dim3(static_cast<unsigned>((keys + kGatherKeys - 1) / kGatherKeys), p.Hkv, p.B), dim3(kGatherThreads),
+                          0, s, p);
 }
 
 template <int D>
-cudaError_t launch_t(const BlockWeightsParams& p, cudaStream_t s) {
-  const cudaError_t e = launch_dependent(stats_kernel<D>, dim3(p.max_q_len * p.Hq, 1, p.B), dim3(kThreads), 0, s, p);
+cudaError_t launch_d(const BlockWeightsParams& p, int num_sms, cudaStream_t s) {
+  CUtensorMap tmk;
+  if (!make_pool_map(&tmk, const_cast<uint8_t*>(p.k_cache), D, p.Hkv, p.num_blocks, Shape<D>::RB)) return cudaErrorInvalidValue;
+  const int G = p.Hq / p.Hkv, RN = rows_kept(p.max_q_len, G);
+  if (RN == 4) return launch_few<D, 4>(p, tmk, num_sms, s);
+  if (RN == 8) return launch_few<D, 8>(p, tmk, num_sms, s);
+  if (RN == 16) return launch_few<D, 16>(p, tmk, num_sms, s);
+  const long long tiles = static_cast<long long>(p.total_q) * G / 128 + p.B;
+  if (tiles * 8 > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = launch_dependent(query_kernel<D>, dim3(static_cast<unsigned>(tiles * 8), p.Hkv), dim3(128), 0, s, p);
   if (e != cudaSuccess) return e;
-  const long long keys = std::min(p.max_blocks * 16LL, static_cast<long long>(p.weights_len));
-  return launch_dependent(sums_kernel<D>, dim3(static_cast<unsigned>((keys + kThreads - 1) / kThreads), p.Hkv, p.B), dim3(kThreads), 0, s, p);
+  e = launch_tc(pass_kernel<D, kRows>, PassCfg<D, kRows>::CTAS * num_sms, kPassThreads, PassCfg<D, kRows>::SMEM, p, tmk, s);
+  if (e != cudaSuccess) return e;
+  return launch_tc(pass_kernel<D, kKeys>, PassCfg<D, kKeys>::CTAS * num_sms, kPassThreads, PassCfg<D, kKeys>::SMEM, p, tmk, s);
 }
+
+// CTAs of a launch, at most.
+int slots_of(int num_sms) { return 3 * num_sms; }
 
 }  // namespace
 
-size_t block_weights_workspace(int B, int total_q, int max_q_len, int Hq, int Hkv, int D, long long keys) {
-  return 4 * static_cast<size_t>(total_q) * Hq;
+size_t block_weights_workspace(int B, int total_q, int max_q_len, int Hq, int Hkv, int D, long long keys, int num_sms) {
+  return lay_out(nullptr, nullptr, B, total_q, max_q_len, Hq, Hkv, D, keys, slots_of(num_sms));
 }
 
-cudaError_t launch_block_weights(const BlockWeightsParams& p, int D, int num_sms, cudaStream_t s) {
-  if (D == 64) return launch_t<64>(p, s);
-  if (D == 128) return launch_t<128>(p, s);
-  return launch_t<256>(p, s);
+cudaError_t launch_block_weights(BlockWeightsParams p, int D, void* workspace, int num_sms, cudaStream_t s) {
+  p.slots = slots_of(num_sms);
+  lay_out(&p, static_cast<uint8_t*>(workspace), p.B, p.total_q, p.max_q_len, p.Hq, p.Hkv, D, p.max_blocks * 16LL, p.slots);
+  if (D == 64) return launch_d<64>(p, num_sms, s);
+  if (D == 128) return launch_d<128>(p, num_sms, s);
+  return launch_d<256>(p, num_sms, s);
 }
 
 }  // namespace fkv

@@ -171,6 +171,18 @@ def test_bad_queries_keep_to_their_rows():
     assert torch.equal(got[~bad], want[~bad])
 
 
+def test_bad_groups_share_nothing_and_are_reported():
+    c = Case([(4000, [40, 3, 9]), (3000, [5, 6])], 8, 2, 128, seed=11)
+    for starts, shared, fault in (([0, 3, 2], [4000, 3000], f.FAULT_QLEN), ([-1, 3, 5], [4000, 3000], f.FAULT_QLEN), ([0, 3, 6], [4000, 3000], f.FAULT_QLEN),
+                                  ([0, 3, 5], [-1, 3000], f.FAULT_CONTEXT), ([0, 3, 5], [4000, 16 * c.table.shape[1] + 1], f.FAULT_CONTEXT)):
+        keep = c.starts, c.shared
+        c.starts, c.shared = starts, shared
+        got = c.run()
+        assert int(c.fault) == fault
+        c.starts, c.shared = keep
+        c.check(got)
+
+
 def test_bad_blocks_are_reported():
     c = Case([(5000, [40, 3, 9])], 8, 2, 128, seed=12)
     c.table[0, 7] = c.table[1, 7] = c.table[2, 7] = 1 << 29

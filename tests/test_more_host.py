@@ -185,6 +185,7 @@ def test_weights_invalid(lib, kw):
 def test_weights_unsupported_empty_and_sizes(lib):
     assert _weights(lib, cache=_block(D=96)) == f.UNSUPPORTED and _weights(lib, cache=_block(bs=32)) == f.UNSUPPORTED
     assert _weights(lib, b=65536) == f.UNSUPPORTED and _weights(lib, mb=1 << 27) == f.UNSUPPORTED
+    assert _weights(lib, tq=1 << 29, hq=6) == f.UNSUPPORTED
     assert _weights(lib, tq=0) == f.OK and _weights(lib, b=0) == f.OK and _weights(lib, mq=0) == f.OK
     size = f.fp8_block_attn_weights_workspace_size
     assert size(2, 8, 4, 8, 2, 128, 8) > 0 and size(2, 8, 99, 8, 2, 128, 8) == size(2, 8, 8, 8, 2, 128, 8)
