@@ -25,7 +25,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]
 SOURCES = ["abi.cu", "kv_quant_cache.cu", "decode_attn.cu", "decode_tc.cu", "prefill_attn.cu", "decode_noalloc.cu",
-           "rope_cache.cu", "block_prefill.cu", "block_decode.cu", "block_evict.cu", "block_weights.cu"]
+           "rope_cache.cu", "block_prefill.cu", "block_decode.cu", "block_evict.cu", "block_weights.cu", "block_shared.cu"]
 
 
 def _nvcc() -> str:

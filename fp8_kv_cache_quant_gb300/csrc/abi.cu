@@ -6,6 +6,7 @@
 #include <cstring>
 
 #include "block_common.cuh"
+#include "block_shared.cuh"
 
 namespace {
 
@@ -332,6 +333,66 @@ float base2_scale(float softmax_scale, int32_t head_dim) {
   return tau * 1.4426950408889634f;
 }
 
+// fp8_block_decode_attn, and with num_groups > 0 fp8_block_shared_decode_attn, whose plan and pieces lie behind the decode's own
+// workspace.
+fkv_status block_decode_entry(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache, const int32_t* block_table,
+                              int32_t max_blocks, const int32_t* context_lens, const int32_t* group_starts,
+                              const int32_t* shared_lens, int32_t num_groups, float softmax_scale, int32_t window, void* out,
+                              void* workspace, size_t workspace_bytes, int32_t* fault, fkv_stream_t stream) {
+  if (batch < 0 || num_q_heads <= 0 || max_blocks <= 0 || window < 0) return FKV_INVALID_ARG;
+  const fkv_status st = check_block_cache(cache);
+  if (st != FKV_OK) return st;
+  if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
+  const int G = num_q_heads / cache.num_kv_heads;
+  if (!supported_group(G, cache.head_dim)) return FKV_UNSUPPORTED;
+  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return FKV_INVALID_ARG;
+  if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
+  if (batch == 0) return FKV_OK;
+  if (!q || !out || !block_table || !context_lens || !valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4))
+    return FKV_INVALID_ARG;
+  const BlockDecodePlan plan = plan_block_decode(batch, num_q_heads, cache.num_kv_heads, cache.head_dim);
+  const size_t own_bytes = align256(plan.cnt_bytes + plan.lse_bytes + plan.o_bytes);
+  const size_t need = num_groups == 0 ? plan.cnt_bytes + plan.lse_bytes + plan.o_bytes
+                                      : own_bytes + fkv::block_shared_workspace(batch, num_q_heads, cache.num_kv_heads, cache.head_dim,
+                                                                                num_groups, current_num_sms());
+  if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FKV_INVALID_ARG;
+  fkv::BlockDecodeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
+  p.v_cache = static_cast<const uint8_t*>(cache.v_cache);
+  p.k_scale = cache.k_scale;
+  p.v_scale = cache.v_scale;
+  p.block_table = block_table;
+  p.ctx = context_lens;
+  p.B = batch;
+  p.Hq = num_q_heads;
+  p.Hkv = cache.num_kv_heads << plan.halves;
+  p.halves = plan.halves;
+  p.num_blocks = cache.num_blocks;
+  p.max_blocks = max_blocks;
+  p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
+  p.window = window;
+  uint8_t* at = static_cast<uint8_t*>(workspace);
+  p.done = reinterpret_cast<int32_t*>(at);
+  p.lse_part = reinterpret_cast<float*>(at + plan.cnt_bytes);
+  p.o_part = reinterpret_cast<float*>(at + plan.cnt_bytes + plan.lse_bytes);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.fault = fault;
+  p.stage_wait_ns = pipe_wait_ns();
+  // no more CTAs than there can be places (a unit's tiles and the blank one that leads them)
+  const long long blocks = window > 0 ? std::min<long long>(max_blocks, (window + 15LL) / 16 + 1) : max_blocks;
+  const int tpb = fkv::block_decode_tile_blocks(cache.head_dim);
+  const long long tiles = static_cast<long long>(batch) * p.Hkv * ((blocks + tpb - 1) / tpb + 1);
+  if (tiles > INT32_MAX) return FKV_UNSUPPORTED;  // the kernel counts them in 32 bits
+  const int ctas = static_cast<int>(std::min(plan.ctas, tiles));
+  if (num_groups > 0)
+    return from_cuda(fkv::launch_block_shared(p, cache.head_dim, ctas, group_starts, shared_lens, num_groups, at + own_bytes,
+                                              current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(fkv::launch_block_decode(p, cache.head_dim, ctas, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 namespace fkv {
@@ -621,52 +682,8 @@ fkv_status fp8_block_decode_attn(const void* q, int32_t batch, int32_t num_q_hea
                                  const int32_t* block_table, int32_t max_blocks, const int32_t* context_lens,
                                  float softmax_scale, int32_t window, void* out, void* workspace,
                                  size_t workspace_bytes, int32_t* fault, fkv_stream_t stream) {
-  if (batch < 0 || num_q_heads <= 0 || max_blocks <= 0 || window < 0) return FKV_INVALID_ARG;
-  const fkv_status st = check_block_cache(cache);
-  if (st != FKV_OK) return st;
-  if (num_q_heads % cache.num_kv_heads != 0) return FKV_INVALID_ARG;
-  const int G = num_q_heads / cache.num_kv_heads;
-  if (!supported_group(G, cache.head_dim)) return FKV_UNSUPPORTED;
-  if (!(softmax_scale >= 0.f) || std::isinf(softmax_scale)) return FKV_INVALID_ARG;
-  if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
-  if (batch == 0) return FKV_OK;
-  if (!q || !out || !block_table || !context_lens || !valid_block_pools(cache)) return FKV_INVALID_ARG;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4))
-    return FKV_INVALID_ARG;
-  const BlockDecodePlan plan = plan_block_decode(batch, num_q_heads, cache.num_kv_heads, cache.head_dim);
-  if (!workspace || !aligned(workspace, 256) || workspace_bytes < plan.cnt_bytes + plan.lse_bytes + plan.o_bytes)
-    return FKV_INVALID_ARG;
-  fkv::BlockDecodeParams p;
-  std::memset(&p, 0, sizeof(p));
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_cache = static_cast<const uint8_t*>(cache.k_cache);
-  p.v_cache = static_cast<const uint8_t*>(cache.v_cache);
-  p.k_scale = cache.k_scale;
-  p.v_scale = cache.v_scale;
-  p.block_table = block_table;
-  p.ctx = context_lens;
-  p.B = batch;
-  p.Hq = num_q_heads;
-  p.Hkv = cache.num_kv_heads << plan.halves;
-  p.halves = plan.halves;
-  p.num_blocks = cache.num_blocks;
-  p.max_blocks = max_blocks;
-  p.sm_scale_log2 = base2_scale(softmax_scale, cache.head_dim);
-  p.window = window;
-  uint8_t* at = static_cast<uint8_t*>(workspace);
-  p.done = reinterpret_cast<int32_t*>(at);
-  p.lse_part = reinterpret_cast<float*>(at + plan.cnt_bytes);
-  p.o_part = reinterpret_cast<float*>(at + plan.cnt_bytes + plan.lse_bytes);
-  p.out = static_cast<__nv_bfloat16*>(out);
-  p.fault = fault;
-  p.stage_wait_ns = pipe_wait_ns();
-  // no more CTAs than there can be places (a unit's tiles and the blank one that leads them)
-  const long long blocks = window > 0 ? std::min<long long>(max_blocks, (window + 15LL) / 16 + 1) : max_blocks;
-  const int tpb = fkv::block_decode_tile_blocks(cache.head_dim);
-  const long long tiles = static_cast<long long>(batch) * p.Hkv * ((blocks + tpb - 1) / tpb + 1);
-  if (tiles > INT32_MAX) return FKV_UNSUPPORTED;  // the kernel counts them in 32 bits
-  const int ctas = static_cast<int>(std::min(plan.ctas, tiles));
-  return from_cuda(fkv::launch_block_decode(p, cache.head_dim, ctas, reinterpret_cast<cudaStream_t>(stream)));
+  return block_decode_entry(q, batch, num_q_heads, cache, block_table, max_blocks, context_lens, nullptr, nullptr, 0, softmax_scale, window,
+                            out, workspace, workspace_bytes, fault, stream);
 }
 
 fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,
@@ -714,8 +731,9 @@ fkv_status fp8_block_prefill_attn(const void* q, const int32_t* cu_seqlens_q, in
 
 size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                                    int32_t head_dim, int32_t num_groups) {
-  if (num_groups < 0) return 0;
-  return fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+  const size_t own = fp8_block_decode_attn_workspace_size(batch, num_q_heads, num_kv_heads, head_dim);
+  if (num_groups <= 0 || own == 0) return num_groups < 0 ? 0 : own;
+  return align256(own) + fkv::block_shared_workspace(batch, num_q_heads, num_kv_heads, head_dim, num_groups, current_num_sms());
 }
 
 fkv_status fp8_block_shared_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
@@ -726,8 +744,8 @@ fkv_status fp8_block_shared_decode_attn(const void* q, int32_t batch, int32_t nu
   if (num_groups < 0) return FKV_INVALID_ARG;
   if (num_groups > 0 && (!group_starts || !shared_lens || !aligned(group_starts, 4) || !aligned(shared_lens, 4)))
     return FKV_INVALID_ARG;
-  return fp8_block_decode_attn(q, batch, num_q_heads, cache, block_table, max_blocks, context_lens, softmax_scale, window, out,
-                               workspace, workspace_bytes, fault, stream);
+  return block_decode_entry(q, batch, num_q_heads, cache, block_table, max_blocks, context_lens, group_starts, shared_lens, num_groups,
+                            softmax_scale, window, out, workspace, workspace_bytes, fault, stream);
 }
 
 size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int32_t max_q_len, int32_t num_q_heads,

@@ -269,6 +269,9 @@ struct BlockDecodeParams {
   __nv_bfloat16* out;                         // [B][Hq][D]
   int32_t* fault;
   uint64_t stage_wait_ns;                     // bound of the copies' wait for a free stage (the others': kPipeWaitNs)
+  // what sequences share (block_shared.cu)
+  const int4* shared;                         // [B]{shared keys, first piece's CTA, pieces per item, place in the group}
+  int2* units;                                // [B * Hkv]{first CTA, pieces}
 };
 
 // CTAs of the block-scaled decode that an SM holds, pool blocks of its tiles, and its launch on N CTAs.

@@ -590,12 +590,12 @@ size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_
  * tokens that every member's row of block_table names, in the same blocks or in copies of them.  The
  * result is that of fp8_block_decode_attn for the same arguments (to rounding), but the keys and values of the
  * shared tokens are read, from the blocks that the group's first sequence names, and multiplied once for all
- * members.  Sequences outside every group share nothing.  Groups whose sharing would not pay for itself (few bytes saved
- * in the whole call) are attended like the others, over their own rows of block_table.
+ * members.  What the first sequence's context does not reach is not shared, and a member whose context is shorter than the
+ * shared part is attended by itself, as are sequences outside every group, groups of one, and every group of a
+ * call in which sharing would not pay for itself (few bytes saved): over their own rows of block_table.
  *
  *   group_starts  device int32 [num_groups + 1], non-decreasing, within [0, batch]
- *   shared_lens   device int32 [num_groups]; need not be multiples of 16, and a member may be
- *                 shorter (it sees its own context_lens tokens)
+ *   shared_lens   device int32 [num_groups]; need not be multiples of 16
  *   num_groups    >= 0 (0: nothing is shared)
  *   workspace     device, >= fp8_block_shared_decode_attn_workspace_size(...) bytes, 256-byte aligned, zero-filled
  *                 before its first call; otherwise as for fp8_block_decode_attn
