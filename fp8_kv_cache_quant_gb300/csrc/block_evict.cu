@@ -35,11 +35,11 @@ FKV_DEV uint32_t ctas_of_cluster() {
 FKV_DEV void sync_cluster() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-FKV_DEV int peer_int(const int* p, uint32_t rank) {
+FKV_DEV int2 peer_int2(const int* p, uint32_t rank) {
   uint32_t a;
-  int v;
+  int2 v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
   return v;
 }
 
@@ -55,13 +55,15 @@ struct SelectShared {
   int hist[3][kBins];
   int warp_sum[32], warp_eq[32];
   int digit, left;       // of the last histogram: the digit, and what is to be taken of it
-  int gt, eq;            // this CTA's keys above the threshold, and equal to it
+  int gt_eq[2];          // this CTA's keys above the threshold, and equal to it
 };
+constexpr int kMaxCluster = 8;
+constexpr int kLoads = 8;  // weights that a thread has on their way
 
 __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const EvictParams p, int resident_keys) {
   extern __shared__ __align__(16) uint8_t smem[];
   SelectShared& sh = *reinterpret_cast<SelectShared*>(smem);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem + sizeof(SelectShared));
+  float* held = reinterpret_cast<float*>(smem + sizeof(SelectShared));  // this CTA's weights
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = static_cast<int>(ctas_of_cluster()), rank = static_cast<int>(rank_in_cluster());
   for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
@@ -93,21 +95,25 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
   const int seg = ((T + C - 1) / C + 31) & ~31;
   const int lo = min(rank * seg, T), hi = min(lo + seg, T);
   const bool resident = seg <= resident_keys;
-  auto key_at = [&](int i) -> uint32_t {
-    if (i < p.sink || i >= T - p.recent) return kSure;
-    return key_of(weights[i]);
-  };
+  auto key_of_token = [&](int i, float w) -> uint32_t { return i < p.sink || i >= T - p.recent ? kSure : key_of(w); };
   __syncthreads();
-  if (resident) {
-    for (int i = lo + tid; i < hi; i += kSelectThreads) {
-      const uint32_t k = key_at(i);
-      keys[i - lo] = k;
-      atomicAdd(&sh.hist[0][k >> 21], 1);
+  for (int i0 = lo + tid; i0 < hi; i0 += kLoads * kSelectThreads) {
+    float w[kLoads];
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = i0 + j * kSelectThreads;
+      w[j] = i < hi ? weights[i] : 0.f;
     }
-  } else {
-    for (int i = lo + tid; i < hi; i += kSelectThreads) atomicAdd(&sh.hist[0][key_at(i) >> 21], 1);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = i0 + j * kSelectThreads;
+      if (i >= hi) break;
+      if (resident) held[i - lo] = w[j];
+      atomicAdd(&sh.hist[0][key_of_token(i, w[j]) >> 21], 1);
+    }
   }
-  auto get = [&](int i) -> uint32_t { return resident ? keys[i - lo] : key_at(i); };
+  auto weight = [&](int i) -> float { return resident ? held[i - lo] : weights[i]; };
+  auto get = [&](int i) -> uint32_t { return key_of_token(i, weight(i)); };
   int left = n;        // keys to take among those that share the digits found so far
   uint32_t found = 0;  // these digits
 #pragma unroll
@@ -125,9 +131,12 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
     const int hi_bin = kBins - 1 - 2 * tid;
     int c0 = 0, c1 = 0;
     if (C > 1) {
-      for (int r = 0; r < C; ++r) {
-        c0 += peer_int(&sh.hist[pass][hi_bin], r);
-        c1 += peer_int(&sh.hist[pass][hi_bin - 1], r);
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        if (r >= C) break;
+        const int2 x = peer_int2(&sh.hist[pass][hi_bin - 1], r);
+        c0 += x.y;
+        c1 += x.x;
       }
     } else {
       c0 = sh.hist[pass][hi_bin];
@@ -176,20 +185,24 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
   int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_eq[lane] : 0);
   if (C > 1) {
     if (tid == kSelectThreads - 1) {
-      sh.gt = gt_before + gt;
-      sh.eq = eq_before + eq;
+      sh.gt_eq[0] = gt_before + gt;
+      sh.gt_eq[1] = eq_before + eq;
     }
     sync_cluster();
-    for (int r = 0; r < rank; ++r) {
-      gt_before += peer_int(&sh.gt, r);
-      eq_before += peer_int(&sh.eq, r);
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
+      if (r >= rank) break;
+      const int2 x = peer_int2(sh.gt_eq, r);
+      gt_before += x.x;
+      eq_before += x.y;
     }
   }
   int at = gt_before + min(eq_before, left);
   const uint32_t below = (1u << lane) - 1u;
   for (int i0 = wlo; i0 < whi; i0 += 32) {
     const int i = i0 + lane;
-    const uint32_t k = i < whi ? get(i) : 0u;
+    const float w = i < whi ? weight(i) : 0.f;
+    const uint32_t k = i < whi ? key_of_token(i, w) : 0u;
     const bool is_eq = i < whi && k == found;
     const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
     const bool keep = i < whi && (k > found || (is_eq && eq_before + __popc(eqs & below) < left));
@@ -197,7 +210,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
     if (keep) {
       const int to = at + __popc(keeps & below);
       kept[to] = i;
-      if (moved) moved[to] = weights[i];
+      if (moved) moved[to] = w;
     }
     at += __popc(keeps);
     eq_before += __popc(eqs);
@@ -207,7 +220,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
 
 constexpr int kGatherThreads = 256;
 
-// 16 codes as float32 values times s (rounded to float32), four per word.
+// Four codes as float32 values times s (rounded to float32).
 FKV_DEV void values4(uint32_t w, float s, float (&x)[4]) {
   uint32_t h01, h23;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h01) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
@@ -220,94 +233,165 @@ FKV_DEV void values4(uint32_t w, float s, float (&x)[4]) {
   x[3] = __fmul_rn(b.y, s);
 }
 
+// Four codes times r in binary16, as codes.
+FKV_DEV uint32_t scaled4(uint32_t w, __half2 r) {
+  uint32_t out;
+  asm("{\n\t.reg .b16 lo, hi;\n\t.reg .b32 a, b;\n\t"
+      "mov.b32 {lo, hi}, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 a, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, hi;\n\t"
+      "mul.rn.f16x2 a, a, %2;\n\t"
+      "mul.rn.f16x2 b, b, %2;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 lo, a;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hi, b;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(out)
+      : "r"(w), "r"(*reinterpret_cast<const uint32_t*>(&r)));
+  return out;
+}
+
+// The largest magnitude code of 16 (NaN, 0x7F, the largest of all).
+FKV_DEV uint32_t top_code(uint4 x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, __vmaxu2(w[i] & 0x007F007Fu, w[i] >> 8 & 0x007F007Fu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// Four values of the row's scale s as codes of the scale `to`, inv = 1 / to.
+FKV_DEV uint32_t recode4(uint32_t w, float s, float inv) {
+  float y[4];
+  values4(w, s, y);
+  return f32x4_to_e4m3x4(make_float2(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv)), make_float2(__fmul_rn(y[2], inv), __fmul_rn(y[3], inv)));
+}
+
+// Warps go from item to item (new block, KV head): while the rows of one are on their way, the table entries of the next and the kept
+// indices of the one behind it are read, so that an item costs one round trip to memory instead of four.
 template <int D>
-__global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictParams p, int blocks) {
+__global__ void __launch_bounds__(kGatherThreads, D <= 128 ? 4 : 2) evict_gather_kernel(const EvictParams p, int blocks) {
   constexpr int CPR = D / 16;          // 16-byte chunks of a row
   constexpr int N = 16 * CPR / 32;     // chunks per lane of K, and of V
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const long long item = static_cast<long long>(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5);
-  const int h = static_cast<int>(item % p.H);
-  const long long rest = item / p.H;
-  const int blk = static_cast<int>(rest % blocks);
-  const int b = static_cast<int>(rest / blocks);
-  if (b >= p.B) return;
-  const int n = p.new_lens[b] - 16 * blk;  // rows of the block
-  if (n <= 0) return;
-  const int dst = p.new_table[static_cast<size_t>(b) * p.new_max_blocks + blk];
-  // lane r < 16: row r's place and scales
-  int src = 0, slot = 0;
-  float ks = 0.f, vs = 0.f;
-  if (lane < min(n, 16)) {
-    const int t = p.kept[(static_cast<size_t>(b) * p.H + h) * p.budget + 16 * blk + lane];
-    int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + (t >> 4)];
-    if (id < 0 || id >= p.num_blocks) {
+  const long long items = static_cast<long long>(p.B) * p.H * blocks, step = static_cast<long long>(gridDim.x) * (kGatherThreads / 32);
+  struct Item {
+    int b, blk, h, n;     // n: rows of the block, 0: none
+  };
+  auto item_at = [&](long long x) -> Item {
+    Item t = {0, 0, 0, 0};
+    if (x >= items) return t;
+    t.h = static_cast<int>(x % p.H);
+    const long long rest = x / p.H;
+    t.blk = static_cast<int>(rest % blocks);
+    t.b = static_cast<int>(rest / blocks);
+    t.n = min(16, p.new_lens[t.b] - 16 * t.blk);
+    return t;
+  };
+  // lane r < 16: row r's old index, then its block (and the new block); -1: none
+  auto index_of = [&](const Item& t) -> int { return lane < t.n ? p.kept[(static_cast<size_t>(t.b) * p.H + t.h) * p.budget + 16 * t.blk + lane] : -1; };
+  auto block_of = [&](const Item& t, int i) -> int { return i >= 0 ? p.block_table[static_cast<size_t>(t.b) * p.max_blocks + (i >> 4)] : 0; };
+  auto target_of = [&](const Item& t) -> int { return t.n > 0 ? p.new_table[static_cast<size_t>(t.b) * p.new_max_blocks + t.blk] : 0; };
+  long long x = static_cast<long long>(blockIdx.x) * (kGatherThreads / 32) + (threadIdx.x >> 5);
+  Item now = item_at(x), next = item_at(x + step);
+  int i_now = index_of(now), i_next = index_of(next);
+  int id = block_of(now, i_now), dst = target_of(now);
+  for (; x < items; x += step) {
+    const Item t = now;
+    const int slot = i_now & 15, to = dst;
+    if (lane < t.n && (id < 0 || id >= p.num_blocks)) {
       raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
       id = 0;
     }
-    src = id;
-    slot = t & 15;
-    const size_t at = static_cast<size_t>(id) * p.H + h;
-    ks = p.ks[at];
-    vs = p.vs[at];
-  }
-  if (dst < 0 || dst >= p.num_blocks) {
-    if (lane == 0) raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
-    return;
-  }
-  uint4 k[N], v[N];
-  float sk[N], sv[N];
-#pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int c = lane + 32 * j, row = c / CPR;
-    const int id = __shfl_sync(0xffffffffu, src, row), s = __shfl_sync(0xffffffffu, slot, row);
-    sk[j] = __shfl_sync(0xffffffffu, ks, row);
-    sv[j] = __shfl_sync(0xffffffffu, vs, row);
-    k[j] = v[j] = make_uint4(0u, 0u, 0u, 0u);
-    if (row < n) {
-      const size_t at = ((static_cast<size_t>(id) * p.H + h) * 16 + s) * CPR + c % CPR;
-      k[j] = reinterpret_cast<const uint4*>(p.kc)[at];
-      v[j] = reinterpret_cast<const uint4*>(p.vc)[at];
+    const size_t src_row = static_cast<size_t>(id) * p.H + t.h;
+    float ks = 0.f, vs = 0.f;
+    if (lane < t.n) {
+      ks = p.ks[src_row];
+      vs = p.vs[src_row];
     }
-  }
-  const size_t at = static_cast<size_t>(dst) * p.H + h;
-  auto store = [&](uint4 (&x)[N], const float (&s)[N], uint8_t* pool, float* scale) {
-    uint32_t amax = 0;  // bits of the largest finite magnitude
+    uint4 k[N], v[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+      const int c = lane + 32 * j, row = c / CPR;
+      const int b = __shfl_sync(0xffffffffu, id, row), s = __shfl_sync(0xffffffffu, slot, row);
+      k[j] = v[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < t.n) {
+        const size_t at = ((static_cast<size_t>(b) * p.H + t.h) * 16 + s) * CPR + c % CPR;
+        k[j] = reinterpret_cast<const uint4*>(p.kc)[at];
+        v[j] = reinterpret_cast<const uint4*>(p.vc)[at];
+      }
+    }
+    now = next;
+    i_now = i_next;
+    next = item_at(x + 2 * step);
+    id = block_of(now, i_now);
+    dst = target_of(now);
+    i_next = index_of(next);
+    if (t.n <= 0) continue;
+    if (to < 0 || to >= p.num_blocks) {
+      if (lane == 0) raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+      continue;
+    }
+    const size_t at = static_cast<size_t>(to) * p.H + t.h;
+    auto store = [&](uint4 (&x4)[N], float scale_of_row, uint8_t* pool, float* scale) {
+      // Magnitudes order as their codes, so a chunk's largest is found among the codes.  Where a row holds a NaN, or a scale is
+      // no finite number that keeps its products finite, value by value: what is not finite does not count.
+      float s[N];
+      uint32_t amax = 0;  // bits of the largest finite magnitude
+      bool odd = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y[4];
-        values4(w[i], s[j], y);
+      for (int j = 0; j < N; ++j) {
+        s[j] = __shfl_sync(0xffffffffu, scale_of_row, (lane + 32 * j) / CPR);
+        const uint32_t top = top_code(x4[j]);
+        uint32_t h;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(top)));
+        const uint32_t m = __float_as_uint(__fmul_rn(__half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu))), s[j])) & 0x7FFFFFFFu;
+        odd = odd || top == 0x7Fu || m >= 0x7F800000u;
+        amax = max(amax, m);
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+        amax = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
-          if (m < 0x7F800000u) amax = max(amax, m);
+        for (int j = 0; j < N; ++j) {
+          const uint32_t w[4] = {x4[j].x, x4[j].y, x4[j].z, x4[j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y[4];
+            values4(w[i], s[j], y);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t m = __float_as_uint(y[e]) & 0x7FFFFFFFu;
+              if (m < 0x7F800000u) amax = max(amax, m);
+            }
+          }
         }
       }
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    const float to = pow2_scale(amax);
-    const float inv = __frcp_rn(to);
-    if (lane == 0) scale[at] = to;
+      amax = __reduce_max_sync(0xffffffffu, amax);
+      const float to_scale = pow2_scale(amax);
+      const float inv = __frcp_rn(to_scale);
+      if (lane == 0) scale[at] = to_scale;
+      // Scales that are powers of two: a code times r = s / to_scale is exact in binary16 from r = 2^-24 (below which every code ends at
+      // zero) to 2^15, save for what lies 2^-24 and below, where every code has long ended at zero.
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float y[4];
-        values4(w[i], s[j], y);
-        w[i] = f32x4_to_e4m3x4(make_float2(__fmul_rn(y[0], inv), __fmul_rn(y[1], inv)),
-                               make_float2(__fmul_rn(y[2], inv), __fmul_rn(y[3], inv)));
+      for (int j = 0; j < N; ++j) {
+        const int c = lane + 32 * j;
+        const uint32_t sb = __float_as_uint(s[j]);
+        const float r = s[j] * inv;
+        if (r != 1.f) {
+          if ((sb & 0x807FFFFFu) == 0u && sb != 0u && r <= 32768.f) {
+            const __half2 rh = __float2half2_rn(r);
+            x4[j] = make_uint4(scaled4(x4[j].x, rh), scaled4(x4[j].y, rh), scaled4(x4[j].z, rh), scaled4(x4[j].w, rh));
+          } else {
+            x4[j] = make_uint4(recode4(x4[j].x, s[j], inv), recode4(x4[j].y, s[j], inv), recode4(x4[j].z, s[j], inv), recode4(x4[j].w, s[j], inv));
+          }
+        }
+        if (c / CPR < t.n) reinterpret_cast<uint4*>(pool)[at * 16 * CPR + c] = x4[j];
       }
-      const int c = lane + 32 * j;
-      if (c / CPR < n) reinterpret_cast<uint4*>(pool)[at * 16 * CPR + c] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  };
-  store(k, sk, p.kc, p.ks);
-  store(v, sv, p.vc, p.vs);
+    };
+    store(k, ks, p.kc, p.ks);
+    store(v, vs, p.vc, p.vs);
+  }
 }
 
 }  // namespace
@@ -317,7 +401,7 @@ cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStr
   const long long units = static_cast<long long>(p.B) * p.H;
   // clusters while SMs would idle and a CTA has more keys than its threads take at once
   int C = 1;
-  while (C < 8 && 2 * C * units <= 2LL * num_sms && most / C > 4 * kSelectThreads) C *= 2;
+  while (C < kMaxCluster && 2 * C * units <= 2LL * num_sms && most / C > 4 * kSelectThreads) C *= 2;
   const long long seg = ((most + C - 1) / C + 31) & ~31LL;
   const int resident = static_cast<int>(std::min<long long>(seg, kMaxResident));
   const size_t smem = sizeof(SelectShared) + 4 * static_cast<size_t>(resident);
@@ -342,8 +426,12 @@ cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStr
   const int blocks = static_cast<int>((std::min<long long>(most, p.budget) + 15) / 16);
   if (blocks == 0) return cudaSuccess;
   const long long items = units * blocks;
-  const unsigned grid = static_cast<unsigned>((items + kGatherThreads / 32 - 1) / (kGatherThreads / 32));
   auto kern = D == 64 ? evict_gather_kernel<64> : D == 128 ? evict_gather_kernel<128> : evict_gather_kernel<256>;
+  int per_sm = 0;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kGatherThreads, 0);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(std::min<long long>((items + kGatherThreads / 32 - 1) / (kGatherThreads / 32),
+                                                                  static_cast<long long>(per_sm) * num_sms));
   return launch_dependent(kern, dim3(grid), dim3(kGatherThreads), 0, s, p, blocks);
 }
 
