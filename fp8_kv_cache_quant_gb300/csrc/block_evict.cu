@@ -401,7 +401,7 @@ cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStr
   const long long units = static_cast<long long>(p.B) * p.H;
   // clusters while SMs would idle and a CTA has more keys than its threads take at once
   int C = 1;
-  while (C < kMaxCluster && 2 * C * units <= 2LL * num_sms && most / C > 4 * kSelectThreads) C *= 2;
+  while (C < kMaxCluster && 2 * C * units <= num_sms && most / C > 2 * kSelectThreads) C *= 2;
   const long long seg = ((most + C - 1) / C + 31) & ~31LL;
   const int resident = static_cast<int>(std::min<long long>(seg, kMaxResident));
   const size_t smem = sizeof(SelectShared) + 4 * static_cast<size_t>(resident);

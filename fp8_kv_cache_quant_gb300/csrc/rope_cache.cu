@@ -138,19 +138,13 @@ constexpr int kRopeThreads = 256;
 // token's elements, slot and position are loaded before the current token is turned and stored, so
 // that a thread has 32 bytes in flight all the time.  Three CTAs per SM (four spill registers, five more):
 // 65,536 tokens of 32/8 heads at head_dim 128 take 255 us, 5.9 TB/s (280 and 321 us).
-// kPool: 0 e4m3, 1 e5m2, 2 bf16.  kAxes: positions of several axes.
-template <int D, int kPool, bool kAxes>
+// kPool: 0 e4m3, 1 e5m2, 2 bf16.
+template <int D, int kPool>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeCacheParams p, int t_step) {
   after_previous();
   constexpr int U = D / 16;
   const int per_token = (p.Hq + 2 * p.H) * U;
   const long long gid = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  bool mixed = false;  // a unit of this warp has pairs of different axes
-  if constexpr (kAxes) {
-    const int rem = static_cast<int>(gid % per_token), u = rem % U;
-    const uint32_t axes = rem / U < p.Hq + p.H && u < (p.rot >> 4) ? unit_axes(p.axes, u) : 0u;
-    mixed = __any_sync(0xffffffffu, axes != (axes & 3) * 0x5555u);
-  }
   if (gid >= static_cast<long long>(per_token) * t_step) return;
   const int t0 = static_cast<int>(gid / per_token), rem = static_cast<int>(gid - static_cast<long long>(t0) * per_token);
   const int row = rem / U, u = rem % U;
@@ -163,19 +157,14 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
   const __nv_bfloat16* src = (is_q ? p.q : is_v ? p.v : p.k) + h * D;
   uint8_t* pool = is_v ? p.vc : p.kc;
   const float inv = is_q || kPool == 2 ? 1.f : __frcp_rn((is_v ? p.vs : p.ks)[p.per_head ? h : 0]);
-  const uint32_t axes = kAxes && turned ? unit_axes(p.axes, u) : 0u;
   uint4 xa, xb;
-  long long slot, pos, more[3];  // more: of axes 1 .. 3
+  long long slot, pos;
   auto fetch = [&](long long t) {
     const uint4* x = reinterpret_cast<const uint4*>(src + t * stride);
     xa = x[ca];
     xb = x[cb];
     slot = p.slots[t];
     pos = p.positions[t];
-    if constexpr (kAxes) {
-#pragma unroll
-      for (int x = 0; x < 3; ++x) more[x] = x + 1 < p.axes.count ? p.positions[(x + 1) * p.axes.stride + t] : 0;
-    }
   };
   if (t0 < p.n_tokens) fetch(t0);
   for (long long t = t0; t < p.n_tokens; t += t_step) {
@@ -183,27 +172,13 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
     unpack8(xa, a);
     unpack8(xb, b);
     const long long s = slot, x = pos;
-    bool in_table = x >= 0 && x < p.max_pos;
-    int at_axis[4] = {static_cast<int>(x), 0, 0, 0};
-    if constexpr (kAxes) {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        in_table = in_table && more[i] >= 0 && more[i] < p.max_pos;
-        at_axis[i + 1] = static_cast<int>(more[i]);
-      }
-    }
     if (t + t_step < p.n_tokens) fetch(t + t_step);
     if (s < 0) continue;
-    if (s >= p.capacity || !in_table) {
+    if (s >= p.capacity || x < 0 || x >= p.max_pos) {
       if (rem == 0) raise_fault(p.fault, s >= p.capacity ? FKV_FAULT_SLOT : FKV_FAULT_POSITION);
       continue;
     }
-    if constexpr (kAxes) {
-      if (turned && mixed) turn_unit_axes(a, b, p.cos_sin, at_axis, axes, p.rot, u, p.interleaved);
-      else if (turned) turn_unit(a, b, p.cos_sin + static_cast<long long>(pick(at_axis, axes & 3)) * p.rot, p.rot, u, p.interleaved);
-    } else {
-      if (turned) turn_unit(a, b, p.cos_sin + x * p.rot, p.rot, u, p.interleaved);
-    }
+    if (turned) turn_unit(a, b, p.cos_sin + x * p.rot, p.rot, u, p.interleaved);
     if (is_q) {
       uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * D);
       dst[ca] = pack8_bf16(a);
@@ -217,6 +192,90 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
       } else {
         reinterpret_cast<uint2*>(pool)[at + ca] = pack8_fp8<kPool == 1>(a, inv);
         reinterpret_cast<uint2*>(pool)[at + cb] = pack8_fp8<kPool == 1>(b, inv);
+      }
+    }
+  }
+}
+
+// The same with positions of several axes.  Thread = one unit of four heads of a kind (query, K, V) of one token, heads a quarter of their
+// number apart, which are turned by the same table entries: a unit with pairs of several axes reads its sixteen one by one, a
+// quarter of the loads of a thread per head.  9,001 tokens of 64/8 heads at head_dim 64, axes in turns, bf16 pool: 33 us, 5.6 TB/s, as
+// with one axis (39 a thread per head; 41 with four CTAs per SM, whose 64 registers spill).
+template <int D, int kPool>
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_axes_kernel(const RopeCacheParams p) {
+  after_previous();
+  constexpr int U = D / 16;
+  const int Qq = (p.Hq + 3) / 4, Qk = (p.H + 3) / 4, per_token = (Qq + 2 * Qk) * U;
+  const long long gid = static_cast<long long>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const long long t = gid / per_token;
+  const int rem = static_cast<int>(gid - t * per_token), quad = rem / U, u = rem % U;
+  const bool is_q = quad < Qq, is_v = quad >= Qq + Qk;
+  const int heads = is_q ? p.Hq : p.H, Q = is_q ? Qq : Qk, h0 = is_q ? quad : is_v ? quad - Qq - Qk : quad - Qq;
+  const bool turned = !is_v && u < (p.rot >> 4);
+  const uint32_t axes = turned ? unit_axes(p.axes, u) : 0u;
+  const bool mixed = __any_sync(0xffffffffu, axes != (axes & 3) * 0x5555u);
+  if (t >= p.n_tokens) return;
+  const long long s = p.slots[t];
+  long long at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) at[i] = i < p.axes.count ? p.positions[i * p.axes.stride + t] : 0;
+  int ca, cb;
+  unit_chunks(u, is_v ? 0 : p.rot, p.interleaved, ca, cb);
+  const __nv_bfloat16* src = (is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride);
+  uint4 xa[4], xb[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (h0 + j * Q < heads) {
+      const uint4* x = reinterpret_cast<const uint4*>(src + (h0 + j * Q) * D);
+      xa[j] = x[ca];
+      xb[j] = x[cb];
+    }
+  }
+  bool in_table = true;
+  int pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    in_table = in_table && at[i] >= 0 && at[i] < p.max_pos;
+    pos[i] = static_cast<int>(at[i]);
+  }
+  if (s < 0) return;
+  if (s >= p.capacity || !in_table) {
+    if (rem == 0) raise_fault(p.fault, s >= p.capacity ? FKV_FAULT_SLOT : FKV_FAULT_POSITION);
+    return;
+  }
+  float cs[8], sn[8];
+  if (turned) {
+    if (mixed) {
+      load_entries(p.cos_sin, pos, axes, p.rot, u, cs, sn);
+    } else {
+      const float* row = p.cos_sin + static_cast<long long>(pick(pos, axes & 3)) * p.rot + 8 * u;
+      load8(row, cs);
+      load8(row + p.rot / 2, sn);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int h = h0 + j * Q;
+    if (h >= heads) break;
+    float a[8], b[8];
+    unpack8(xa[j], a);
+    unpack8(xb[j], b);
+    if (turned) turn8(a, b, cs, sn, p.interleaved);
+    if (is_q) {
+      uint4* dst = reinterpret_cast<uint4*>(p.q_out + t * p.q_out_stride + h * D);
+      dst[ca] = pack8_bf16(a);
+      dst[cb] = pack8_bf16(b);
+    } else {
+      uint8_t* pool = is_v ? p.vc : p.kc;
+      // chunk index of the row's first 8 elements in the pool
+      const long long row = ((((s >> 4) * p.H + h) << 4) + (s & 15)) * (D >> 3);
+      if constexpr (kPool == 2) {
+        reinterpret_cast<uint4*>(pool)[row + ca] = pack8_bf16(a);
+        reinterpret_cast<uint4*>(pool)[row + cb] = pack8_bf16(b);
+      } else {
+        const float inv = __frcp_rn((is_v ? p.vs : p.ks)[p.per_head ? h : 0]);
+        reinterpret_cast<uint2*>(pool)[row + ca] = pack8_fp8<kPool == 1>(a, inv);
+        reinterpret_cast<uint2*>(pool)[row + cb] = pack8_fp8<kPool == 1>(b, inv);
       }
     }
   }
@@ -484,22 +543,29 @@ __global__ void __launch_bounds__(kBlockThreads, D <= 128 ? 4 : 3) block_cache_k
   }
 }
 
-template <int D, bool kAxes>
+template <int D>
 cudaError_t launch_rope(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
+  if (p.axes.count > 1) {
+    const long long units = (static_cast<long long>((p.Hq + 3) / 4) + 2 * ((p.H + 3) / 4)) * (D / 16) * p.n_tokens;
+    const long long blocks = (units + kRopeThreads - 1) / kRopeThreads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    auto kern = pool == 2 ? rope_cache_axes_kernel<D, 2> : pool == 1 ? rope_cache_axes_kernel<D, 1> : rope_cache_axes_kernel<D, 0>;
+    return launch_dependent(kern, dim3(static_cast<unsigned>(blocks)), dim3(kRopeThreads), 0, s, p);
+  }
   const long long per_token = static_cast<long long>(p.Hq + 2 * p.H) * (D / 16);
   // as many tokens at once as three CTAs per SM hold
   const long long t_step = std::min<long long>(p.n_tokens, std::max<long long>(1, 3LL * num_sms * kRopeThreads / per_token));
   const unsigned blocks = static_cast<unsigned>((per_token * t_step + kRopeThreads - 1) / kRopeThreads);
-  auto kern = pool == 2 ? rope_cache_kernel<D, 2, kAxes> : pool == 1 ? rope_cache_kernel<D, 1, kAxes> : rope_cache_kernel<D, 0, kAxes>;
+  auto kern = pool == 2 ? rope_cache_kernel<D, 2> : pool == 1 ? rope_cache_kernel<D, 1> : rope_cache_kernel<D, 0>;
   return launch_dependent(kern, dim3(blocks), dim3(kRopeThreads), 0, s, p, static_cast<int>(t_step));
 }
 
 }  // namespace
 
 cudaError_t launch_rope_cache(const RopeCacheParams& p, int pool, int num_sms, cudaStream_t s) {
-  auto launch = p.axes.count > 1 ? (p.D == 64 ? launch_rope<64, true> : p.D == 128 ? launch_rope<128, true> : launch_rope<256, true>)
-                                 : (p.D == 64 ? launch_rope<64, false> : p.D == 128 ? launch_rope<128, false> : launch_rope<256, false>);
-  return launch(p, pool, num_sms, s);
+  if (p.D == 64) return launch_rope<64>(p, pool, num_sms, s);
+  if (p.D == 128) return launch_rope<128>(p, pool, num_sms, s);
+  return launch_rope<256>(p, pool, num_sms, s);
 }
 
 cudaError_t launch_block_cache(const BlockCacheParams& p, int D, cudaStream_t s) {
