@@ -224,7 +224,7 @@ struct BlockWeightsParams {
   int slots;                                  // CTAs of a launch, at most
   int32_t* done;                              // [2][slots] pieces finished of the unit that CTA k begins, in either pass
   float2* pieces;                             // [2 slots (+ units)][rows] maxima and sums
-  float* sums;                                // [2 slots][128]
+  float* sums;                                // [2 slots][256]
   float* rows;                                // [tiles][64]{c, c, -lse, -lse}
   uint8_t* q_tiles;                           // [tiles] of both terms
   int2* units;                                // [B][Hkv]{first CTA, pieces}

@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kBins = 2048;
-constexpr int kMaxResident = 49152;  // keys of a CTA held in shared memory, at most (192 KB)
+constexpr int kMaxResident = 45056;  // keys of a CTA held in shared memory, at most (176 KB)
 
 FKV_DEV uint32_t rank_in_cluster() {
   uint32_t r;
@@ -32,8 +32,16 @@ FKV_DEV uint32_t ctas_of_cluster() {
   return r;
 }
 // Every thread of every CTA of the cluster: earlier writes of all are visible behind it.
+FKV_DEV void arrive_cluster() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+FKV_DEV void wait_cluster() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 FKV_DEV void sync_cluster() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  arrive_cluster();
+  wait_cluster();
+}
+FKV_DEV void peer_add(int* p, uint32_t rank, int v) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 FKV_DEV int2 peer_int2(const int* p, uint32_t rank) {
   uint32_t a;
@@ -52,7 +60,8 @@ FKV_DEV uint32_t key_of(float w) {
 }
 
 struct SelectShared {
-  int hist[3][kBins];
+  int hist[3][kBins];    // this CTA's keys
+  int total[3][kBins];   // the cluster's
   int warp_sum[32], warp_eq[32];
   int digit, left;       // of the last histogram: the digit, and what is to be taken of it
   int gt_eq[2];          // this CTA's keys above the threshold, and equal to it
@@ -66,7 +75,8 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
   float* held = reinterpret_cast<float*>(smem + sizeof(SelectShared));  // this CTA's weights
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = static_cast<int>(ctas_of_cluster()), rank = static_cast<int>(rank_in_cluster());
-  for (int i = tid; i < 3 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
+  for (int i = tid; i < 6 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
+  if (C > 1) arrive_cluster();  // (waited for before the first access to another CTA)
   griddep_wait();
   griddep_launch_dependents();
   const int unit = blockIdx.x / C;
@@ -85,6 +95,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
   const int all = C * kSelectThreads, me = rank * kSelectThreads + tid;
   for (int i = n + me; i < p.budget; i += all) kept[i] = -1;
   if (T <= p.budget) {  // (the whole cluster)
+    if (C > 1) wait_cluster();
     for (int i = me; i < n; i += all) {
       kept[i] = i;
       if (moved) moved[i] = weights[i];
@@ -125,22 +136,20 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
         if (pass == 2 && k >> 10 == found) atomicAdd(&sh.hist[2][k & 1023u], 1);
       }
     }
-    if (C > 1) sync_cluster();
-    else __syncthreads();
-    // thread t: the t-th pair of bins from the top
+    __syncthreads();
+    // thread t: the t-th pair of bins from the top.  Few bins are taken (a key's exponent and first digits: tens of them), so every CTA adds
+    // its own to all CTAs' totals rather than reading eight histograms through.
     const int hi_bin = kBins - 1 - 2 * tid;
-    int c0 = 0, c1 = 0;
+    int c0 = sh.hist[pass][hi_bin], c1 = sh.hist[pass][hi_bin - 1];
     if (C > 1) {
-#pragma unroll
-      for (int r = 0; r < kMaxCluster; ++r) {
-        if (r >= C) break;
-        const int2 x = peer_int2(&sh.hist[pass][hi_bin - 1], r);
-        c0 += x.y;
-        c1 += x.x;
+      if (pass == 0) wait_cluster();
+      for (int r = 0; r < C; ++r) {
+        if (c0 != 0) peer_add(&sh.total[pass][hi_bin], r, c0);
+        if (c1 != 0) peer_add(&sh.total[pass][hi_bin - 1], r, c1);
       }
-    } else {
-      c0 = sh.hist[pass][hi_bin];
-      c1 = sh.hist[pass][hi_bin - 1];
+      sync_cluster();
+      c0 = sh.total[pass][hi_bin];
+      c1 = sh.total[pass][hi_bin - 1];
     }
     int upto = c0 + c1;  // inclusive sums over the threads
 #pragma unroll
@@ -196,6 +205,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
       gt_before += x.x;
       eq_before += x.y;
     }
+    arrive_cluster();  // (the last access to another CTA)
   }
   int at = gt_before + min(eq_before, left);
   const uint32_t below = (1u << lane) - 1u;
@@ -215,7 +225,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
     at += __popc(keeps);
     eq_before += __popc(eqs);
   }
-  if (C > 1) sync_cluster();  // no CTA leaves while another reads its shared memory
+  if (C > 1) wait_cluster();  // no CTA leaves while another reads its shared memory
 }
 
 constexpr int kGatherThreads = 256;

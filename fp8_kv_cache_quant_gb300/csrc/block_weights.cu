@@ -51,8 +51,8 @@ FKV_DEV WeightsSeq weights_seq(const BlockWeightsParams& p, int b, bool report) 
 
 // ---------------------------------------------------------------- the division of the work
 
-// What a kernel divides: kRows: row tiles against the key tiles that they see (pass 0); kKeys: key tiles against the row
-// tiles that see them (pass 1); kScores: all of a KV head's key tiles of KT keys as one unit.
+// What a kernel divides: kRows: row tiles against the key tiles (of 128) that they see (pass 0); kKeys: key tiles of KT keys against
+// the row tiles that see them (pass 1); kScores: all of a KV head's key tiles of KT keys as one unit.
 enum Kind { kRows, kKeys, kScores };
 
 template <Kind K, int KT>
@@ -61,12 +61,12 @@ struct Units {
   FKV_DEV int tiles(const WeightsSeq& s) const { return static_cast<int>((static_cast<long long>(s.rows) * G + 127) / 128); }
   FKV_DEV int of(const WeightsSeq& s) const {  // units of a sequence and KV head
     if (s.rows == 0) return 0;
-    return K == kRows ? tiles(s) : K == kKeys ? (s.T + 127) / 128 : 1;
+    return K == kRows ? tiles(s) : K == kKeys ? (s.T + KT - 1) / KT : 1;
   }
   // the first step's tile: 0, or the first row tile that sees key tile t
   FKV_DEV int first(const WeightsSeq& s, int t) const {
     if (K != kKeys) return 0;
-    const long long token = 128LL * t - (s.T - s.rows);
+    const long long token = static_cast<long long>(KT) * t - (s.T - s.rows);
     return token > 0 ? static_cast<int>(token * G / 128) : 0;
   }
   FKV_DEV int steps(const WeightsSeq& s, int t) const {
@@ -134,10 +134,11 @@ FKV_DEV Walk<K, KT> first_step(const BlockWeightsParams& p, int k, long long& W,
   auto steps_of = [&](const WeightsSeq& s, int t0, int dt) -> long long {
     if (s.rows == 0) return 0;
     if constexpr (K == kKeys) {
-      // key tiles wholly before the chunk's first token are seen by every row tile, those behind by G fewer each
+      // key tiles that begin before the chunk or with it are seen by every row tile, those behind by KT / 128 G fewer each
       if (t0 != 0) return 0;
-      const int old = s.T - s.rows, nt = a.units.tiles(s), nk = a.units.of(s), t1 = min(old / 128 + 1, nk), n = nk - t1;
-      const long long G = a.units.G, skipped = G * (static_cast<long long>(t1) * n + static_cast<long long>(n) * (n - 1) / 2) - n * ((old * G + 127) / 128);
+      const int old = s.T - s.rows, nt = a.units.tiles(s), nk = a.units.of(s), t1 = min(old / KT + 1, nk), n = nk - t1;
+      const long long G = a.units.G;
+      const long long skipped = KT / 128 * G * (static_cast<long long>(t1) * n + static_cast<long long>(n) * (n - 1) / 2) - n * ((old * G + 127) / 128);
       return static_cast<long long>(nt) * nk - skipped;
     } else {
       long long x = 0;
@@ -228,13 +229,75 @@ FKV_DEV size_t tile_index(const BlockWeightsParams& p, const WeightsSeq& s, int 
   return (static_cast<size_t>(s.r0) * (p.Hq / p.Hkv) / 128 + b + i) * p.Hkv + g;
 }
 
-// The id of block `blk` of sequence b, reported and 0 where it is out of range.
-FKV_DEV int block_id(const BlockWeightsParams& p, int b, int blk) {
-  const int id = p.block_table[static_cast<size_t>(b) * p.max_blocks + blk];
-  if (id >= 0 && id < p.num_blocks) return id;
-  raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
-  return 0;
-}
+// The block ids and K scales of the key tiles that a range of steps goes through, for the warp that copies them: as many tiles as a warp
+// has lanes for their blocks (a batch) are read at once, the ids two batches and the scales one ahead.  Tile by tile and one ahead, a step
+// took a round trip to memory, 1.0 us, whatever else it did.
+template <Kind K, int KT>
+struct KeyFeed {
+  static constexpr int TB = KT / 16, BATCH = 32 / TB;
+  struct Read {
+    int id, g;
+    bool in;
+  };
+  Walk<K, KT> ahead;    // the place whose tile this lane reads next
+  Read now, next, last;
+  float ks, ks_next;
+  int taken;
+
+  // the place of the key tile behind a's: the next step's, or (kKeys) the next unit's
+  static FKV_DEV void to_next_keys(Walk<K, KT>& a, const BlockWeightsParams& p) {
+    if (K == kKeys) {
+      const int skip = static_cast<int>(min(static_cast<long long>(a.count - a.s), a.left)) - 1;
+      a.left -= skip;
+      a.s += skip;
+    }
+    a.advance(p);
+  }
+  static FKV_DEV int tile_of(const Walk<K, KT>& a) { return K == kKeys ? a.t : a.s; }
+  static FKV_DEV int blocks_of(const Walk<K, KT>& a) { return min(TB, ((a.seq.T + 15) >> 4) - TB * tile_of(a)); }
+  FKV_DEV Read read(const BlockWeightsParams& p) {
+    const int j = (threadIdx.x & 31) % TB;
+    Read x = {0, ahead.g, ahead.left > 0 && j < blocks_of(ahead)};
+    if (x.in) x.id = p.block_table[static_cast<size_t>(ahead.b) * p.max_blocks + TB * tile_of(ahead) + j];
+#pragma unroll 1
+    for (int i = 0; i < BATCH; ++i) to_next_keys(ahead, p);
+    return x;
+  }
+  // an id out of range reads block 0 and is reported
+  static FKV_DEV float scale_of(Read& x, const BlockWeightsParams& p) {
+    if (!x.in) return 0.f;
+    if (x.id < 0 || x.id >= p.num_blocks) {
+      raise_fault(p.fault, FKV_FAULT_BLOCK_ID);
+      x.id = 0;
+    }
+    return p.k_scale[static_cast<size_t>(x.id) * p.Hkv + x.g];
+  }
+  FKV_DEV void begin(const Walk<K, KT>& at, const BlockWeightsParams& p) {
+    ahead = at;
+    for (int i = 0; i < (threadIdx.x & 31) / TB; ++i) to_next_keys(ahead, p);
+    now = read(p);
+    next = read(p);
+    ks = scale_of(now, p);
+    last = read(p);
+    ks_next = scale_of(next, p);
+    taken = 0;
+  }
+  // the next tile's: lane j < TB has block j's
+  FKV_DEV void take(const BlockWeightsParams& p, int& id, float& scale) {
+    const int j = taken % BATCH;
+    if (taken > 0 && j == 0) {
+      now = next;
+      ks = ks_next;
+      next = last;
+      ks_next = scale_of(next, p);
+      last = read(p);
+    }
+    const int from = TB * j + (threadIdx.x & 31) % TB;
+    id = __shfl_sync(0xffffffffu, now.id, from);
+    scale = __shfl_sync(0xffffffffu, ks, from);
+    ++taken;
+  }
+};
 
 template <int D>
 struct Shape {
@@ -325,47 +388,61 @@ __global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) 
 
 // ---------------------------------------------------------------- the two passes over many rows
 
+// The unit's own tile stays (pass 0: 128 rows, both terms; pass 1: 256 keys, two products of 128), the others stream past it.  One CTA per
+// SM.  Sixteen warps read the scores, a quarter of the columns each: a thread has one row's scores for 32 keys, or two keys' for 32 rows
+// (whose c and lse it reads from shared memory once for both: one key per thread was bound by that, 2,000 cycles per 256 keys and 128
+// rows).  The loops are rolled as far as the arithmetic allows: the warps that copy and issue run their code once per step and fetch
+// it anew when the readers' is too long.
 template <int D, Kind K>
 struct PassCfg : Shape<D> {
   using S = Shape<D>;
+  static constexpr int KT = K == kRows ? 128 : 256;             // keys of a unit or step
+  static constexpr int NT = KT / 128;                           // products per step
   static constexpr int QT = 2 * S::TILE;                        // both terms of a row tile
-  static constexpr int STAY = K == kRows ? QT : S::TILE;        // the unit's own tile, two buffers
+  static constexpr int STAY = K == kRows ? QT : 2 * S::TILE;
   static constexpr int STREAM = K == kRows ? S::TILE : QT + kRowBytes;
-  static constexpr int NS = K == kRows && D == 64 ? 4 : 2;      // stages of the other one
-  static constexpr int CTAS = D <= 128 ? 2 : 1;                 // per SM: 256 columns of tensor memory each
-  static constexpr int SCN = 8;                                 // slots of K scales: the copies run at most NS + 2 tiles ahead
+  static constexpr int NY = K == kRows ? 2 : D == 256 ? 1 : 3;  // buffers of the one, stages of the other
+  static constexpr int NS = K == kRows ? (D == 256 ? 2 : 8) : (D == 256 ? 2 : 3);
+  static constexpr int SBUF = 4 / NT;                           // buffers of a step's scores, 128 NT columns each
+  static constexpr int READERS = 16, THREADS = 32 * (READERS + 2);
+  // K scales in slots: of step u (pass 0; the copies run at most NS + SBUF steps ahead), or of piece r (pass 1: NY ahead of the
+  // products, which are SBUF steps ahead of the readers)
+  static constexpr int SCN = K == kRows ? 16 : 8;
+  static constexpr int SCF = KT / 16;
   static constexpr int OFF_STAY = 0;
-  static constexpr int OFF_STREAM = OFF_STAY + 2 * STAY;
+  static constexpr int OFF_STREAM = OFF_STAY + NY * STAY;
   static constexpr int OFF_SC = OFF_STREAM + NS * STREAM;
-  static constexpr int OFF_BAR = OFF_SC + SCN * 8 * 4;
-  static constexpr int NBAR = 8 + 2 * NS + SCN + 1;
+  static constexpr int OFF_JOIN = OFF_SC + SCN * SCF * 4;       // the column quarters' results [4][128] float2, [4][256] float
+  static constexpr int OFF_BAR = OFF_JOIN + 4 * 128 * 8;
+  static constexpr int NBAR = 2 * NY + 2 * SBUF + 2 * NS + SCN + 3;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 64;
   static constexpr uint32_t IDESC = idesc_e4m3_f32(128, 128, 0, 0);
-  static_assert(SCN > NS + 2, "a slot is rewritten only after its reader is done");
-  static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory of the resident CTAs");
+  static_assert(SCN > (K == kRows ? NS + SBUF : NY + SBUF + 1) && OFF_BAR % 8 == 0, "a slot is rewritten only after its readers are done");
+  static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-constexpr int kPassThreads = 320, kReaders = 8;  // warps 0-7 read the scores, 8 copies, 9 issues the products
-
+// Warps 0 .. 15 read the scores, 16 copies, 17 issues the products.
 template <int D, Kind K>
-__global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
+__global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     pass_kernel(const __grid_constant__ BlockWeightsParams p, const __grid_constant__ CUtensorMap tmk) {
   using C = PassCfg<D, K>;
-  using Place = Walk<K, 128>;
+  using Place = Walk<K, C::KT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sStay = smem + C::OFF_STAY;
   uint8_t* sStream = smem + C::OFF_STREAM;
   float* sSc = reinterpret_cast<float*>(smem + C::OFF_SC);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* y_full = bars + 0;    // [2] the tile of piece r in buffer r % 2
-  uint64_t* y_empty = bars + 2;   // [2]
-  uint64_t* s_full = bars + 4;    // [2] the scores of step u in buffer u % 2
-  uint64_t* s_free = bars + 6;    // [2]
-  uint64_t* x_full = bars + 8;    // [NS] the streamed tile of step u in stage u % NS
+  uint64_t* y_full = bars;              // [NY] the tile of piece r in buffer r % NY
+  uint64_t* y_empty = y_full + C::NY;
+  uint64_t* s_full = y_empty + C::NY;   // [SBUF] the scores of step u in buffer u % SBUF
+  uint64_t* s_free = s_full + C::SBUF;
+  uint64_t* x_full = s_free + C::SBUF;  // [NS] the streamed tile of step u in stage u % NS
   uint64_t* x_empty = x_full + C::NS;
-  uint64_t* sc_full = x_empty + C::NS;  // [SCN] K scales of step u in slot u % SCN
+  uint64_t* sc_full = x_empty + C::NS;  // [SCN]
   uint64_t* mma_done = sc_full + C::SCN;
+  uint64_t* j_full = mma_done + 1;      // the column quarters' results of piece r ...
+  uint64_t* j_free = mma_done + 2;      // ... and taken
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* last_s = abort_s + 1;
@@ -373,167 +450,205 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < C::NY; ++i) {
       mbar_init(&y_full[i], 1);
       mbar_init(&y_empty[i], 1);
+    }
+    for (int i = 0; i < C::SBUF; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], kReaders);
+      mbar_init(&s_free[i], C::READERS);
     }
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(&x_full[i], 1);
-      mbar_init(&x_empty[i], K == kKeys ? 1 + kReaders : 1);  // (the rows' parameters are read by the readers)
+      mbar_init(&x_empty[i], K == kKeys ? 1 + C::READERS : 1);  // (the rows' parameters are read by the readers)
     }
     for (int i = 0; i < C::SCN; ++i) mbar_init(&sc_full[i], 1);
     mbar_init(mma_done, 1);
+    mbar_init(j_full, C::READERS);
+    mbar_init(j_free, K == kRows ? 4 : 8);
     *abort_s = 0;
     pend_s[0] = pend_s[5] = 0;
     fence_mbar_init();
   }
-  // The tensor memory is taken after the wait: before it, it could be what a CTA of the kernel before still needs.
+  // The tensor memory, all of an SM's, is taken after the wait: before it, it could be what a CTA of the kernel before still needs.
   griddep_wait();
-  if (warp == 9) {
-    tmem_alloc(tmem_slot, 256);
+  if (warp == C::READERS + 1) {
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
     tc_fence_before();
   }
   long long W;
   int N;
-  Place at = first_step<K, 128>(p, k, W, N, K == kRows && k == 0 && warp == 0);
+  Place at = first_step<K, C::KT>(p, k, W, N, K == kRows && k == 0 && warp == 0);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
   const int G = p.Hq / p.Hkv;
-  const long long n = at.left;  // steps of this CTA
+  const int n = static_cast<int>(at.left);  // steps of this CTA
   int32_t* done = p.done + (K == kRows ? 0 : p.slots);
 
   if (n == 0) {
     // more CTAs than steps
-  } else if (warp < kReaders) {
+  } else if (warp < C::READERS) {
     // ============================================================ the scores' readers
-    // warp w: tensor memory lanes rb .. rb + 15, lanes l and l + 16 each half of their columns
-    const int hf = lane >> 4, rb = (warp & 3) * 32 + (warp >> 2) * 16, i = rb + (lane & 15);
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>(rb) << 16);
+    // tensor memory lane i, columns 32 part .. + 31 of every product
+    const int part = warp >> 2, i = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * part;
     bool ok = true;
-    float m = -kHuge, l = 0.f;              // pass 0: the row's maximum and sum (of this thread's columns)
-    float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;  // pass 1: the key's sum
-    float mine = 0.f;                       // c of the row; ks of the key
-    int limit = 0;                          // keys that the row sees; the first row that sees the key
+    // pass 0: the row's sum l of 2^(x - m) (of this thread's columns).  m need not be the maximum, only near enough that no sum
+    // overflows: it is the largest score of the first columns, and moves when a sum of 32 reaches 2^60.
+    float m = -kHuge, l = 0.f;
+    float2 acc[C::NT];                      // pass 1: the keys' sums
+    float mine[C::NT];                      // c of the row; ks of the keys
+    int limit[C::NT];                       // keys that the row sees; the first row that sees the key
+    bool whole = false;                     // the unit begins in this CTA
     for (int u = 0; u < n; ++u) {
       if (at.begins()) {
         const int old = at.seq.T - at.seq.rows;
+        whole = at.s == 0;
         if constexpr (K == kRows) {
           const long long r = 128LL * at.t + i;
           const bool is_row = r < static_cast<long long>(at.seq.rows) * G;
-          limit = is_row ? old + static_cast<int>(r / G) + 1 : 0;
-          mine = is_row ? p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1)] : 0.f;
+          limit[0] = is_row ? old + static_cast<int>(r / G) + 1 : 0;
+          mine[0] = is_row ? p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1)] : 0.f;
           m = -kHuge;
           l = 0.f;
         } else {
-          const int key = 128 * at.t + i;
-          mine = key < at.seq.T ? p.k_scale[static_cast<size_t>(block_id(p, at.b, key >> 4)) * p.Hkv + at.g] : 0.f;
-          limit = static_cast<int>(min(max(static_cast<long long>(key) - old, 0LL) * G, static_cast<long long>(INT32_MAX)));
-          acc0 = acc1 = make_float2(0.f, 0.f);
+          if (!wait_warp(&sc_full[at.piece % C::SCN], (at.piece / C::SCN) & 1)) { ok = false; break; }
+#pragma unroll
+          for (int h = 0; h < C::NT; ++h) {
+            const int key = C::KT * at.t + 128 * h + i;
+            mine[h] = sSc[(at.piece % C::SCN) * C::SCF + 8 * h + (i >> 4)];
+            limit[h] = static_cast<int>(min(max(static_cast<long long>(key) - old, 0LL) * G, static_cast<long long>(INT32_MAX)));
+            acc[h] = make_float2(0.f, 0.f);
+          }
         }
       }
       if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
-      const int sb = u & 1;
-      float cb[4];
+      const int sb = u % C::SBUF, st = u % C::NS;
+      // this thread's first column: its key, or its row
+      const int c0 = 128 * (K == kRows ? at.s : at.units.first(at.seq, at.t) + at.s) + 32 * part;
       if constexpr (K == kRows) {
-        if (!pf_wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1)) { ok = false; break; }
-        const float4 ks4 = *reinterpret_cast<const float4*>(sSc + (u % C::SCN) * 8 + 4 * hf);
+        if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1) || !wait_warp(&s_full[sb], (u / C::SBUF) & 1)) { ok = false; break; }
+        const float2 ks2 = *reinterpret_cast<const float2*>(sSc + (u % C::SCN) * C::SCF + 2 * part);
+        tc_fence_after();
+        float v[32];
+        tmem_ld32(lane_base + 128 * sb, v);
+        tmem_ld_wait();
+        tc_fence_before();
+        mbar_arrive_warp(&s_free[sb]);
+        if (__any_sync(0xffffffffu, limit[0] < c0 + 32)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (c0 + j >= limit[0]) v[j] = -INFINITY;
+        }
         // (plus 2^-126, so that a hidden score of -inf stays one where the product is zero)
         constexpr float kLeast = 1.17549435e-38f;
-        cb[0] = fmaf(mine, ks4.x, kLeast);
-        cb[1] = fmaf(mine, ks4.y, kLeast);
-        cb[2] = fmaf(mine, ks4.z, kLeast);
-        cb[3] = fmaf(mine, ks4.w, kLeast);
-      }
-      if (!pf_wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
-      tc_fence_after();
-      const int st = u % C::NS;
-      // first column of this thread's half: its key, or its row
-      const int c0 = 128 * (K == kRows ? at.s : at.units.first(at.seq, at.t) + at.s) + 64 * hf;
-      const bool partly = K == kRows ? limit < c0 + 64 : limit > c0;
-      const bool any_partly = __any_sync(0xffffffffu, partly);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float v[32];
-        tmem_ld32_16x2<64>(lane_base + 128 * sb + 32 * c, v);
-        tmem_ld_wait();
-        if (c == 1) {
-          tc_fence_before();
-          mbar_arrive_warp(&s_free[sb]);
-        }
-        if constexpr (K == kRows) {
-          if (any_partly) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (c0 + 32 * c + j >= limit) v[j] = -INFINITY;
-          }
-          const float a = cb[2 * c], b2 = cb[2 * c + 1];
-          const float top = fmaxf(m, fmaxf(max_tree<16>(v) * a, max_tree<16>(v + 16) * b2));
-          float2 s0 = make_float2(l * ex2(m - top), 0.f), s1 = make_float2(0.f, 0.f);
-          m = top;
-          const float2 a2 = make_float2(a, a), bb = make_float2(b2, b2), t2 = make_float2(-top, -top);
+        const float a = fmaf(mine[0], ks2.x, kLeast), b2 = fmaf(mine[0], ks2.y, kLeast);
+        // the sum against m; a sum of 2^60 and above, or NaN, moves its row's m to the maximum and is made again (the rows of which
+        // it is not true stay as they are)
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          const float2 a2 = make_float2(a, a), bb = make_float2(b2, b2), t2 = make_float2(-m, -m);
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), a2, t2), y = __ffma2_rn(make_float2(v[16 + j], v[17 + j]), bb, t2);
             s0 = __fadd2_rn(s0, make_float2(ex2(x.x), ex2(x.y)));
             s1 = __fadd2_rn(s1, make_float2(ex2(y.x), ex2(y.y)));
           }
-          l = (s0.x + s0.y) + (s1.x + s1.y);
-        } else {
-          const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + 32 * hf + 16 * c;
-          const float2 ks = make_float2(mine, mine);
+          s0 = __fadd2_rn(s0, s1);
+          const float sum = s0.x + s0.y;
+          const bool over = !again && !(sum < 1.152921504606847e18f);
+          if (!__any_sync(0xffffffffu, over)) {
+            l += sum;
+            break;
+          }
+          const float top = over ? fmaxf(m, fmaxf(max_tree<16>(v) * a, max_tree<16>(v + 16) * b2)) : m;
+          l *= ex2(m - top);
+          m = top;
+        }
+      } else {
+        const bool any_partly = __any_sync(0xffffffffu, limit[0] > c0 || limit[C::NT - 1] > c0);
+        if (!wait_warp(&s_full[sb], (u / C::SBUF) & 1)) { ok = false; break; }
+        tc_fence_after();
+        const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + 16 * part;
+#pragma unroll 1
+        for (int c = 0; c < 32; c += 16) {
+          float v[C::NT][16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            const float4 r0 = rp[j / 2], r1 = rp[j / 2 + 1];
-            float2 x = __ffma2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), ks), make_float2(r0.x, r0.y), make_float2(r0.z, r0.w));
-            float2 y = __ffma2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), ks), make_float2(r1.x, r1.y), make_float2(r1.z, r1.w));
-            if (any_partly) {
-              const int r = c0 + 32 * c + j;
-              if (r < limit) x.x = -INFINITY;
-              if (r + 1 < limit) x.y = -INFINITY;
-              if (r + 2 < limit) y.x = -INFINITY;
-              if (r + 3 < limit) y.y = -INFINITY;
+          for (int h = 0; h < C::NT; ++h) tmem_ld16(lane_base + 128 * (C::NT * sb + h) + c, v[h]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float4 r = rp[(c + j) / 2];
+#pragma unroll
+            for (int h = 0; h < C::NT; ++h) {
+              float2 x = __ffma2_rn(__fmul2_rn(make_float2(v[h][j], v[h][j + 1]), make_float2(mine[h], mine[h])), make_float2(r.x, r.y), make_float2(r.z, r.w));
+              float2 e = make_float2(ex2(x.x), ex2(x.y));
+              if (any_partly) {  // (a hidden score has no weight, whatever its row's sum is)
+                if (c0 + c + j < limit[h]) e.x = 0.f;
+                if (c0 + c + j + 1 < limit[h]) e.y = 0.f;
+              }
+              acc[h] = __fadd2_rn(acc[h], e);
             }
-            acc0 = __fadd2_rn(acc0, make_float2(ex2(x.x), ex2(x.y)));
-            acc1 = __fadd2_rn(acc1, make_float2(ex2(y.x), ex2(y.y)));
           }
         }
+        tc_fence_before();
+        mbar_arrive_warp(&s_free[sb]);
+        mbar_arrive_warp(&x_empty[st]);
       }
-      if constexpr (K == kKeys) mbar_arrive_warp(&x_empty[st]);
       if (at.ends()) {
-        const int k0 = cta_of(at.unit0, W, N), ns = cta_of(at.unit0 + at.count - 1, W, N) - k0 + 1;
-        const long long place = piece_place(k, k0);
+        // ---- the column quarters of the piece meet in shared memory
+        float2* row_join = reinterpret_cast<float2*>(smem + C::OFF_JOIN);
+        float* key_join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
+        if (at.piece > 0 && !wait_warp(j_free, (at.piece - 1) & 1)) { ok = false; break; }
         if constexpr (K == kRows) {
-          const float m2 = __shfl_xor_sync(0xffffffffu, m, 16), l2 = __shfl_xor_sync(0xffffffffu, l, 16);
-          const float top = fmaxf(m, m2), sum = l * ex2(m - top) + l2 * ex2(m2 - top);
-          if (hf == 0) {
-            if (ns > 1) p.pieces[place * 128 + i] = make_float2(top, sum);
-            else if (limit > 0) p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(top + lg2(sum));
-          }
+          row_join[part * 128 + i] = make_float2(m, l);
         } else {
-          float sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-          const int key = 128 * at.t + i;
-          if (hf == 0) {
+#pragma unroll
+          for (int h = 0; h < C::NT; ++h) key_join[part * 256 + 128 * h + i] = acc[h].x + acc[h].y;
+        }
+        mbar_arrive_warp(j_full);
+        if (warp < (K == kRows ? 4 : 8)) {
+          if (!wait_warp(j_full, at.piece & 1)) { ok = false; break; }
+          int k0 = k, ns = 1;
+          if (!whole || at.s + 1 != at.count) {
+            k0 = cta_of(at.unit0, W, N);
+            ns = cta_of(at.unit0 + at.count - 1, W, N) - k0 + 1;
+          }
+          const long long place = piece_place(k, k0);
+          if constexpr (K == kRows) {
+            float top = -kHuge, sum = 0.f;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float2 y = row_join[x * 128 + i];
+              const float mx = fmaxf(top, y.x);
+              sum = sum * ex2(top - mx) + y.y * ex2(y.x - mx);
+              top = mx;
+            }
+            if (ns > 1) p.pieces[place * 128 + i] = make_float2(top, sum);
+            else if (limit[0] > 0) p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(top + lg2(sum));
+          } else {
+            const int j = threadIdx.x, key = C::KT * at.t + j;
+            const float sum = (key_join[j] + key_join[256 + j]) + (key_join[512 + j] + key_join[768 + j]);
             if (ns > 1) {
-              p.sums[place * 128 + i] = sum;
+              p.sums[place * C::KT + j] = sum;
             } else if (key < at.seq.T) {
               float* w = p.weights + (static_cast<size_t>(at.b) * p.Hkv + at.g) * p.weights_len + key;
               *w = key < at.seq.T - at.seq.rows && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
             }
           }
-        }
-        if (ns > 1 && threadIdx.x == 0) {
-          volatile int* pend = pend_s + (k == k0 ? 5 : 0);
-          pend[0] = ns;
-          pend[1] = k0;
-          pend[2] = at.b;
-          pend[3] = at.g;
-          pend[4] = at.t;
+          mbar_arrive_warp(j_free);
+          if (ns > 1 && threadIdx.x == 0) {
+            volatile int* pend = pend_s + (k == k0 ? 5 : 0);
+            pend[0] = ns;
+            pend[1] = k0;
+            pend[2] = at.b;
+            pend[3] = at.g;
+            pend[4] = at.t;
+          }
         }
       }
       at.advance(p);
@@ -543,43 +658,39 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
-  } else if (warp == 8) {
+  } else if (warp == C::READERS) {
     // ============================================================ copies
+    using Feed = KeyFeed<K, C::KT>;
     int stay_pieces = 0;            // pieces whose tile was requested
-    long long used = 0;             // steps whose streamed tile was requested
+    int used = 0;                   // steps whose streamed tile was requested
     size_t held[C::NS];             // pass 1: the row tile that a stage holds
 #pragma unroll
     for (int s = 0; s < C::NS; ++s) held[s] = ~static_cast<size_t>(0);
-    // a tile of 128 keys: a block per lane, blocks behind the sequence left as they are (their keys are hidden)
-    auto copy_keys = [&](uint8_t* dst, const Place& a, int tile, int id, uint64_t* full) {
-      const int nblk = min(8, ((a.seq.T + 15) >> 4) - 8 * tile);
+    Feed feed;
+    feed.begin(at, p);
+    // The keys of `at` (a block per lane; blocks behind the sequence are left as they are: their keys are hidden, or their sums not
+    // stored) and their scales.
+    auto copy_keys = [&](uint8_t* dst, uint64_t* full, int slot) {
+      int id;
+      float ks;
+      feed.take(p, id, ks);
+      const int nblk = Feed::blocks_of(at);
       if (lane == 0) mbar_arrive_expect_tx(full, nblk * 16 * D);
       __syncwarp();
       if (lane < nblk) {
 #pragma unroll
-        for (int s = 0; s < C::NSUB; ++s) tma_load_4d(dst + s * C::SUB + lane * 16 * C::RB, &tmk, s * C::RB, 0, a.g, id, full);
+        for (int s = 0; s < C::NSUB; ++s)
+          tma_load_4d(dst + (lane >> 3) * C::TILE + s * C::SUB + (lane & 7) * 16 * C::RB, &tmk, s * C::RB, 0, at.g, id, full);
       }
+      if (lane < Feed::TB) sSc[slot * C::SCF + lane] = ks;
+      mbar_arrive_warp(&sc_full[slot]);
     };
-    auto id_of = [&](const Place& a, int tile) -> int {
-      const int blk = 8 * tile + lane;
-      return a.left > 0 && lane < 8 && blk < (a.seq.T + 15) >> 4 ? block_id(p, a.b, blk) : -1;
-    };
-    auto scale_of = [&](const Place& a, int id) -> float { return id >= 0 ? p.k_scale[static_cast<size_t>(id) * p.Hkv + a.g] : 0.f; };
-    Place nx = at;
-    int id = 0, id_next = 0;
-    float ks = 0.f;
-    if constexpr (K == kRows) {
-      id = id_of(at, at.s);
-      ks = scale_of(at, id);
-      nx.advance(p);
-      id_next = id_of(nx, nx.s);
-    }
     bool ok = true;
     for (int u = 0; u < n; ++u) {
       if (abort_warp(abort_s)) break;
       if (at.begins()) {
-        const int yb = at.piece & 1;
-        if (at.piece >= 2 && !pf_wait_warp(&y_empty[yb], ((at.piece >> 1) - 1) & 1)) { ok = false; break; }
+        const int yb = at.piece % C::NY;
+        if (at.piece >= C::NY && !wait_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1)) { ok = false; break; }
         if constexpr (K == kRows) {
           if (lane == 0) {
             mbar_arrive_expect_tx(&y_full[yb], C::QT);
@@ -587,22 +698,15 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
           }
           __syncwarp();
         } else {
-          copy_keys(sStay + yb * C::STAY, at, at.t, id_of(at, at.t), &y_full[yb]);
+          copy_keys(sStay + yb * C::STAY, &y_full[yb], at.piece % C::SCN);
         }
         stay_pieces = at.piece + 1;
       }
       const int st = u % C::NS;
-      if (u >= C::NS && !pf_wait_warp(&x_empty[st], (u / C::NS - 1) & 1)) { ok = false; break; }
+      if (u >= C::NS && !wait_warp(&x_empty[st], (u / C::NS - 1) & 1)) { ok = false; break; }
       uint8_t* dst = sStream + st * C::STREAM;
       if constexpr (K == kRows) {
-        copy_keys(dst, at, at.s, max(id, 0), &x_full[st]);
-        if (lane < 8) sSc[(u % C::SCN) * 8 + lane] = ks;
-        mbar_arrive_warp(&sc_full[u % C::SCN]);
-        id = id_next;
-        ks = scale_of(nx, id);
-        at = nx;
-        nx.advance(p);
-        id_next = id_of(nx, nx.s);
+        copy_keys(dst, &x_full[st], u % C::SCN);
       } else {
         const size_t tile = tile_index(p, at.seq, at.b, at.g, at.units.first(at.seq, at.t) + at.s);
         bool same = false;
@@ -622,8 +726,8 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
           }
         }
         __syncwarp();
-        at.advance(p);
       }
+      at.advance(p);
       used = u + 1;
     }
     if (!ok) {
@@ -633,9 +737,9 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
     // let every copy land before the CTA can exit
     if (lane == 0) {
       for (int s = 0; s < C::NS; ++s)
-        if (used > s) pf_wait(&x_full[s], ((used - 1 - s) / C::NS) & 1);
-      for (int s = 0; s < 2; ++s)
-        if (stay_pieces > s) pf_wait(&y_full[s], ((stay_pieces - 1 - s) / 2) & 1);
+        if (used > s) wait_ns(&x_full[s], ((used - 1 - s) / C::NS) & 1);
+      for (int s = 0; s < C::NY; ++s)
+        if (stay_pieces > s) wait_ns(&y_full[s], ((stay_pieces - 1 - s) / C::NY) & 1);
     }
     __syncwarp();
   } else {
@@ -644,26 +748,28 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
     bool ok = true;
     for (int u = 0; u < n; ++u) {
       if ((u & 7) == 7 && abort_warp(abort_s)) break;
-      const int yb = at.piece & 1, st = u % C::NS, sb = u & 1;
-      if (at.begins()) ok = pf_wait_warp(&y_full[yb], (at.piece >> 1) & 1);
-      if (ok) ok = pf_wait_warp(&x_full[st], (u / C::NS) & 1);
-      if (ok && u >= 2) ok = pf_wait_warp(&s_free[sb], ((u >> 1) - 1) & 1);
+      const int yb = at.piece % C::NY, st = u % C::NS, sb = u % C::SBUF;
+      if (at.begins()) ok = wait_warp(&y_full[yb], (at.piece / C::NY) & 1);
+      if (ok) ok = wait_warp(&x_full[st], (u / C::NS) & 1);
+      if (ok && u >= C::SBUF) ok = wait_warp(&s_free[sb], (u / C::SBUF - 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
+      const bool ends = at.ends();
+      if (elect_one()) {
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+        for (int h = 0; h < C::NT; ++h)
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            const int byte = kk * 32;
-            const uint32_t off = (byte / C::RB) * C::SUB + (byte % C::RB);
-            const uint64_t y = desc_add(dY, yb * C::STAY + (K == kRows ? term * C::TILE : 0) + off);
-            const uint64_t x = desc_add(dX, st * C::STREAM + (K == kKeys ? term * C::TILE : 0) + off);
-            umma_f8(tmem + 128 * sb, y, x, C::IDESC, (term > 0 || kk > 0) ? 1u : 0u);
-          }
+          for (int term = 0; term < 2; ++term)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk) {
+              const int byte = kk * 32;
+              const uint32_t off = (byte / C::RB) * C::SUB + (byte % C::RB);
+              umma_f8(tmem + 128 * (C::NT * sb + h), desc_add(dY, yb * C::STAY + (K == kRows ? term : h) * C::TILE + off),
+                      desc_add(dX, st * C::STREAM + (K == kKeys ? term : 0) * C::TILE + off), C::IDESC, (term > 0 || kk > 0) ? 1u : 0u);
+            }
         umma_commit(&s_full[sb]);
         umma_commit(&x_empty[st]);
-        if (at.ends()) umma_commit(&y_empty[yb]);
+        if (ends) umma_commit(&y_empty[yb]);
       }
       __syncwarp();
       at.advance(p);
@@ -672,28 +778,28 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
-    if (lane == 0) {  // every product issued here completes before the tensor memory is released
-      umma_commit(mma_done);
-      pf_wait(mma_done, 0);
-    }
+    if (elect_one()) umma_commit(mma_done);  // every product issued here completes before the tensor memory is released
     __syncwarp();
+    wait_warp(mma_done, 0);
   }
   __syncthreads();
-  if (warp == 9) {
+  if (warp == C::READERS + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
   // the CTA that brings a unit's last piece joins them
+#pragma unroll 1
   for (int j = 0; j < 2; ++j) {
     const int ns = pend_s[5 * j], k0 = pend_s[5 * j + 1], b = pend_s[5 * j + 2], g = pend_s[5 * j + 3], t = pend_s[5 * j + 4];
     if (ns == 0) continue;
     if (threadIdx.x == 0) *last_s = count_piece(&done[k0]) == ns - 1;
     __syncthreads();
     const int i = threadIdx.x;
-    if (*last_s && i < 128) {
+    if (*last_s && i < (K == kRows ? 128 : C::KT)) {
       const WeightsSeq s = weights_seq(p, b, false);
       if constexpr (K == kRows) {
         float m = -kHuge, l = 0.f;
+#pragma unroll 4
         for (int x = 0; x < ns; ++x) {
           const float2 y = __ldcg(p.pieces + piece_place(k0 + x, k0) * 128 + i);
           const float top = fmaxf(m, y.x);
@@ -703,8 +809,9 @@ __global__ void __launch_bounds__(kPassThreads, (PassCfg<D, K>::CTAS))
         if (128LL * t + i < static_cast<long long>(s.rows) * G) p.rows[tile_index(p, s, b, g, t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(m + lg2(l));
       } else {
         float sum = 0.f;
-        for (int x = 0; x < ns; ++x) sum += __ldcg(p.sums + piece_place(k0 + x, k0) * 128 + i);
-        const int key = 128 * t + i;
+#pragma unroll 4
+        for (int x = 0; x < ns; ++x) sum += __ldcg(p.sums + piece_place(k0 + x, k0) * C::KT + i);
+        const int key = C::KT * t + i;
         if (key < s.T) {
           float* w = p.weights + (static_cast<size_t>(b) * p.Hkv + g) * p.weights_len + key;
           *w = key < s.T - s.rows && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
@@ -949,15 +1056,10 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
       *abort_s = 1;
     }
   } else if (warp == 4) {
-    // ============================================================ K copies and scales (ids and scales read a tile ahead)
-    auto blocks_of = [&](const Place& a) { return a.left > 0 ? min(C::TPB, ((a.seq.T + 15) >> 4) - C::TPB * a.s) : 0; };
-    auto id_of = [&](const Place& a) -> int { return lane < blocks_of(a) ? block_id(p, a.b, C::TPB * a.s + lane) : -1; };
-    auto scale_of = [&](const Place& a, int id) -> float { return id >= 0 ? p.k_scale[static_cast<size_t>(id) * p.Hkv + a.g] : 0.f; };
-    int id = id_of(at);
-    float ks = scale_of(at, id);
-    Place nx = at;
-    nx.advance(p);
-    int id_next = id_of(nx);
+    // ============================================================ K copies and scales
+    using Feed = KeyFeed<kScores, C::BN>;
+    Feed feed;
+    feed.begin(at, p);
     long long used = 0;
     for (int u = 0; u < n; ++u) {
       if (abort_warp(abort_s)) break;
@@ -967,7 +1069,10 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
         *abort_s = 1;
         break;
       }
-      const int nblk = blocks_of(at);
+      int id;
+      float ks;
+      feed.take(p, id, ks);
+      const int nblk = Feed::blocks_of(at);
       if (lane == 0) mbar_arrive_expect_tx(&k_full[st], nblk * 16 * D);
       __syncwarp();
       if (lane < nblk) {
@@ -977,11 +1082,7 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
       used = u + 1;
       if (lane < C::TPB) sSc[(u % C::SCN) * C::TPB + lane] = ks;
       mbar_arrive_warp(&sc_full[u % C::SCN]);
-      id = id_next;
-      ks = scale_of(nx, id);
-      at = nx;
-      nx.advance(p);
-      id_next = id_of(nx);
+      at.advance(p);
     }
     if (lane == 0)
       for (int s = 0; s < C::NS; ++s)
@@ -999,7 +1100,7 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
       if (ok && u >= 2) ok = wait_warp(&s_free[sb], ((u >> 1) - 1) & 1);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int hh = 0; hh < C::NHALF; ++hh)
 #pragma unroll
@@ -1019,11 +1120,9 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
-    if (lane == 0) {
-      umma_commit(mma_done);
-      wait_ns(mma_done, 0);
-    }
+    if (elect_one()) umma_commit(mma_done);
     __syncwarp();
+    wait_warp(mma_done, 0);
   }
   __syncthreads();
   if (warp == 5) {
@@ -1119,7 +1218,7 @@ size_t lay_out(BlockWeightsParams* p, uint8_t* base, int B, int total_q, int max
     const size_t tiles = (static_cast<size_t>(total_q) * G / 128 + B) * Hkv;
     uint8_t* done = part(2 * static_cast<size_t>(slots) * sizeof(int32_t));
     uint8_t* pieces = part(2 * static_cast<size_t>(slots) * 128 * sizeof(float2));
-    uint8_t* sums = part(2 * static_cast<size_t>(slots) * 128 * sizeof(float));
+    uint8_t* sums = part(2 * static_cast<size_t>(slots) * 256 * sizeof(float));
     uint8_t* rows = part(tiles * kRowBytes);
     uint8_t* q = part(tiles * 256 * D);
     if (p) {
@@ -1162,9 +1261,9 @@ cudaError_t launch_d(const BlockWeightsParams& p, int num_sms, cudaStream_t s) {
   if (tiles * 8 > INT32_MAX) return cudaErrorInvalidValue;
   cudaError_t e = launch_dependent(query_kernel<D>, dim3(static_cast<unsigned>(tiles * 8), p.Hkv), dim3(128), 0, s, p);
   if (e != cudaSuccess) return e;
-  e = launch_tc(pass_kernel<D, kRows>, PassCfg<D, kRows>::CTAS * num_sms, kPassThreads, PassCfg<D, kRows>::SMEM, p, tmk, s);
+  e = launch_tc(pass_kernel<D, kRows>, num_sms, PassCfg<D, kRows>::THREADS, PassCfg<D, kRows>::SMEM, p, tmk, s);
   if (e != cudaSuccess) return e;
-  return launch_tc(pass_kernel<D, kKeys>, PassCfg<D, kKeys>::CTAS * num_sms, kPassThreads, PassCfg<D, kKeys>::SMEM, p, tmk, s);
+  return launch_tc(pass_kernel<D, kKeys>, num_sms, PassCfg<D, kKeys>::THREADS, PassCfg<D, kKeys>::SMEM, p, tmk, s);
 }
 
 // CTAs of a launch, at most.

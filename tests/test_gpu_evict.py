@@ -77,7 +77,7 @@ def test_evict_clusters(ctx, budget, h):
 
 
 def test_evict_more_keys_than_shared_memory_holds():
-    """400,001 tokens of one head: eight CTAs hold 49,152 keys each, the walk goes over global memory."""
+    """400,001 tokens of one head: eight CTAs hold 45,056 keys each, the walk goes over global memory."""
     Case([400001], 700, 4, 100, 1, 64, seed=9).check()
 
 
