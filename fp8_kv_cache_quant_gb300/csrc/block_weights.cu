@@ -55,161 +55,154 @@ FKV_DEV WeightsSeq weights_seq(const BlockWeightsParams& p, int b, bool report) 
 // the row tiles that see them (pass 1); kScores: all of a KV head's key tiles of KT keys as one unit.
 enum Kind { kRows, kKeys, kScores };
 
-template <Kind K, int KT>
-struct Units {
-  int G;
-  FKV_DEV int tiles(const WeightsSeq& s) const { return static_cast<int>((static_cast<long long>(s.rows) * G + 127) / 128); }
-  FKV_DEV int of(const WeightsSeq& s) const {  // units of a sequence and KV head
-    if (s.rows == 0) return 0;
-    return K == kRows ? tiles(s) : K == kKeys ? (s.T + KT - 1) / KT : 1;
-  }
-  // the first step's tile: 0, or the first row tile that sees key tile t
-  FKV_DEV int first(const WeightsSeq& s, int t) const {
-    if (K != kKeys) return 0;
-    const long long token = static_cast<long long>(KT) * t - (s.T - s.rows);
-    return token > 0 ? static_cast<int>(token * G / 128) : 0;
-  }
-  FKV_DEV int steps(const WeightsSeq& s, int t) const {
-    if (K == kScores) return (s.T + KT - 1) / KT;
-    if (K == kKeys) return tiles(s) - first(s, t);
-    const long long row = min(128LL * (t + 1), static_cast<long long>(s.rows) * G) - 1;  // the tile's last
-    return (s.T - s.rows + static_cast<int>(row / G)) / 128 + 1;
-  }
-};
-
-// A place in a CTA's range of steps.
+// A piece: the steps of a unit that a CTA takes.  (Rows and keys of a sequence are below 2^31, rows times G at most 2^30.)
 template <Kind K, int KT>
 struct Walk {
-  Units<K, KT> units;
-  int b, g, t, s;         // step s of unit t of (sequence b, KV head g)
-  int count, of;          // steps of the unit, units of (b, g)
-  WeightsSeq seq;
-  long long left;         // steps of the range from this one on
+  int G;
+  int b, g, t, of;        // unit t of the `of` of (sequence b, KV head g)
+  int r0, rows, T;        // the sequence
+  int s, n, count;        // steps s .. s + n - 1 of its count; n 0: behind the range
+  int left;               // steps of the range behind this piece
+  int piece;              // pieces before this one
   long long unit0;        // the place of the unit's first step
-  int piece;              // units begun before this one in the range
 
-  FKV_DEV bool begins() const { return fresh; }
-  FKV_DEV bool ends() const { return s + 1 == count || left == 1; }
-  FKV_DEV void advance(const BlockWeightsParams& p) {
-    fresh = false;
-    if (--left <= 0) return;
-    if (++s < count) return;
-    s = 0;
-    fresh = true;
+  FKV_DEV void set(const WeightsSeq& q) {
+    r0 = q.r0;
+    rows = q.rows;
+    T = q.T;
+    of = rows == 0 ? 0 : K == kRows ? tiles() : K == kKeys ? (T + KT - 1) / KT : 1;
+  }
+  FKV_DEV int old() const { return T - rows; }
+  FKV_DEV int tiles() const { return (rows * G + 127) / 128; }
+  // the first step's tile: 0, or the first row tile that sees key tile x
+  FKV_DEV int first(int x) const { return K == kKeys ? max(KT * x - old(), 0) * G / 128 : 0; }
+  FKV_DEV int first() const { return first(t); }
+  FKV_DEV int steps(int x) const {
+    if (K == kScores) return (T + KT - 1) / KT;
+    if (K == kKeys) return tiles() - first(x);
+    return (old() + (min(128 * (x + 1), rows * G) - 1) / G) / 128 + 1;
+  }
+  FKV_DEV bool whole() const { return n == count; }
+  FKV_DEV void next(const BlockWeightsParams& p) {
+    n = 0;
+    if (left == 0) return;
     ++piece;
     unit0 += count;
     if (++t == of) {
       t = 0;
       if (++g == p.Hkv) {
         g = 0;
-        do {
-          seq = weights_seq(p, ++b, false);
-          of = units.of(seq);
-        } while (of == 0);
+        do set(weights_seq(p, ++b, false));
+        while (of == 0);
       }
     }
-    count = units.steps(seq, t);
+    count = steps(t);
+    s = 0;
+    n = min(count, left);
+    left -= n;
   }
-  bool fresh;             // this is the range's first step of the unit
 };
 
-// The range of CTA k of the grid: its first step, and W and N, the steps in all and the CTAs that have some.  Every lane of a
-// warp takes part.
+// The range of CTA k of the grid: its first piece, and W and N, the steps in all and the CTAs that have some.  By one warp.
 template <Kind K, int KT>
-FKV_DEV Walk<K, KT> first_step(const BlockWeightsParams& p, int k, long long& W, int& N, bool report) {
+FKV_DEV Walk<K, KT> first_piece(const BlockWeightsParams& p, int k, long long& W, int& N, bool report) {
   const int lane = threadIdx.x & 31;
   Walk<K, KT> a;
-  a.units.G = p.Hq / p.Hkv;
-  a.b = a.g = a.t = a.s = a.count = a.of = a.piece = 0;
-  a.left = a.unit0 = 0;
-  a.fresh = true;
-  a.seq = WeightsSeq{0, 0, 0};
+  a.G = p.Hq / p.Hkv;
+  a.b = a.g = a.t = a.s = a.n = a.count = a.left = a.piece = 0;
+  a.unit0 = 0;
+  a.set(WeightsSeq{0, 0, 0});
   auto sum = [](long long x) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x;
   };
+  auto upto = [&](long long x) {  // inclusive sums over the lanes
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    return x;
+  };
   // a sequence's steps for one KV head: by one lane where it has few units, by all of them where it may have many
-  const bool alone = K == kScores || p.max_q_len * static_cast<long long>(a.units.G) <= 512;
-  auto steps_of = [&](const WeightsSeq& s, int t0, int dt) -> long long {
-    if (s.rows == 0) return 0;
-    if constexpr (K == kKeys) {
+  const bool by_lane = K != kRows || p.max_q_len * static_cast<long long>(a.G) <= 512;
+  auto steps_of = [&](int b, bool rep) -> long long {
+    Walk<K, KT> c = a;
+    c.set(weights_seq(p, b, rep));
+    if (c.of == 0) return 0;
+    if constexpr (K == kScores) {
+      return c.steps(0);
+    } else if constexpr (K == kKeys) {
       // key tiles that begin before the chunk or with it are seen by every row tile, those behind by KT / 128 G fewer each
-      if (t0 != 0) return 0;
-      const int old = s.T - s.rows, nt = a.units.tiles(s), nk = a.units.of(s), t1 = min(old / KT + 1, nk), n = nk - t1;
-      const long long G = a.units.G;
-      const long long skipped = KT / 128 * G * (static_cast<long long>(t1) * n + static_cast<long long>(n) * (n - 1) / 2) - n * ((old * G + 127) / 128);
+      const int nt = c.tiles(), nk = c.of, t1 = min(c.old() / KT + 1, nk), n = nk - t1;
+      const long long G = c.G;
+      const long long skipped = KT / 128 * G * (static_cast<long long>(t1) * n + static_cast<long long>(n) * (n - 1) / 2) - n * ((c.old() * G + 127) / 128);
       return static_cast<long long>(nt) * nk - skipped;
     } else {
       long long x = 0;
-      for (int t = t0; t < a.units.of(s); t += dt) x += a.units.steps(s, t);
-      return x;
+      for (int t = by_lane ? 0 : lane; t < c.of; t += by_lane ? 1 : 32) x += c.steps(t);
+      return by_lane ? x : sum(x);
     }
   };
-  const bool by_lane = alone || K == kKeys;
-  W = 0;
-  if (by_lane) {
-    for (int b0 = 0; b0 < p.B; b0 += 32) W += sum(b0 + lane < p.B ? steps_of(weights_seq(p, b0 + lane, report), 0, 1) : 0);
-  } else {
-    for (int b = 0; b < p.B; ++b) W += sum(steps_of(weights_seq(p, b, report && lane == 0), lane, 32));
-  }
+  const int db = by_lane ? 32 : 1;
+  auto of_lane = [&](int b0, bool rep) -> long long {
+    const int b = by_lane ? b0 + lane : b0;
+    return b < p.B ? steps_of(b, rep && (by_lane || lane == 0)) : 0;
+  };
+  const long long first32 = of_lane(0, report);
+  W = by_lane ? sum(first32) : first32;
+  for (int b0 = db; b0 < p.B; b0 += db) W += by_lane ? sum(of_lane(b0, report)) : of_lane(b0, report);
   W *= p.Hkv;
   N = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
   if (k >= N) return a;
-  const long long w0 = W * k / N;
-  a.left = W * (k + 1) / N - w0;
+  const bool small = W < (1LL << 31) / N;
+  const long long w0 = small ? static_cast<uint32_t>(W) * k / static_cast<uint32_t>(N) : W * k / N;
+  const long long w1 = small ? static_cast<uint32_t>(W) * (k + 1) / static_cast<uint32_t>(N) : W * (k + 1) / N;
   long long base = 0, mine = 0;  // places before sequence b, and one KV head's of it
-  bool found = false;
-  for (int b0 = 0; b0 < p.B && !found; b0 += by_lane ? 32 : 1) {
-    long long x = 0;
-    if (by_lane) x = b0 + lane < p.B ? steps_of(weights_seq(p, b0 + lane, false), 0, 1) : 0;
-    else x = sum(steps_of(weights_seq(p, b0, false), lane, 32));
-    long long upto = x;
-    if (by_lane) {
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += y;
-      }
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, base + upto * p.Hkv > w0);
+  for (int b0 = 0;; b0 += db) {
+    const long long x = b0 == 0 ? first32 : of_lane(b0, false), y = by_lane ? upto(x) : x;
+    const unsigned past = __ballot_sync(0xffffffffu, base + y * p.Hkv > w0);
     if (past != 0) {
       const int j = by_lane ? __ffs(past) - 1 : 0;
       a.b = b0 + j;
       mine = __shfl_sync(0xffffffffu, x, j);
-      base += (__shfl_sync(0xffffffffu, upto, j) - mine) * p.Hkv;
-      found = true;
-    } else {
-      base += __shfl_sync(0xffffffffu, upto, 31) * p.Hkv;
+      base += (__shfl_sync(0xffffffffu, y, j) - mine) * p.Hkv;
+      break;
     }
+    base += __shfl_sync(0xffffffffu, y, 31) * p.Hkv;
   }
-  a.seq = weights_seq(p, a.b, false);
-  a.of = a.units.of(a.seq);
-  a.g = static_cast<int>((w0 - base) / mine);
-  long long rem = w0 - base - a.g * mine;
+  a.set(weights_seq(p, a.b, false));
+  const long long in = w0 - base;
+  a.g = small ? static_cast<int>(static_cast<uint32_t>(in) / static_cast<uint32_t>(mine)) : static_cast<int>(in / mine);
+  const long long rem = in - a.g * mine;
   long long before = 0;  // steps of the units before t0
   for (int t0 = 0; t0 < a.of; t0 += 32) {
-    const int n = t0 + lane < a.of ? a.units.steps(a.seq, t0 + lane) : 0;
-    long long upto = n;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += y;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + upto > rem);
+    const int n = t0 + lane < a.of ? a.steps(t0 + lane) : 0;
+    const long long y = before + upto(n);
+    const unsigned past = __ballot_sync(0xffffffffu, y > rem);
     if (past != 0) {
       const int j = __ffs(past) - 1;
       a.t = t0 + j;
       a.count = __shfl_sync(0xffffffffu, n, j);
-      const long long at = before + __shfl_sync(0xffffffffu, upto, j) - a.count;
-      a.s = static_cast<int>(rem - at);
-      a.unit0 = w0 - a.s;
+      a.s = static_cast<int>(rem - (__shfl_sync(0xffffffffu, y, j) - a.count));
       break;
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    before = __shfl_sync(0xffffffffu, y, 31);
   }
+  a.unit0 = w0 - a.s;
+  a.n = static_cast<int>(min(static_cast<long long>(a.count - a.s), w1 - w0));
+  a.left = static_cast<int>(w1 - w0 - a.n);
   return a;
 }
+
+// The division as the CTA's warps share it.
+template <Kind K, int KT>
+struct Division {
+  Walk<K, KT> first;
+  long long W;
+  int N;
+};
 
 // The CTA whose range holds place w: the largest k with floor(W k / N) <= w.
 FKV_DEV int cta_of(long long w, long long W, int N) { return static_cast<int>(((w + 1) * N - 1) / W); }
@@ -224,9 +217,9 @@ FKV_DEV int count_piece(int32_t* p) {
   return old;
 }
 
-// Index of row tile i of (b, g) among the tiles of the workspace.
-FKV_DEV size_t tile_index(const BlockWeightsParams& p, const WeightsSeq& s, int b, int g, int i) {
-  return (static_cast<size_t>(s.r0) * (p.Hq / p.Hkv) / 128 + b + i) * p.Hkv + g;
+// Index of row tile i of (b, g) among the tiles of the workspace, r0 the sequence's first row.
+FKV_DEV size_t tile_index(const BlockWeightsParams& p, int r0, int b, int g, int i) {
+  return (static_cast<size_t>(r0) * (p.Hq / p.Hkv) / 128 + b + i) * p.Hkv + g;
 }
 
 // The block ids and K scales of the key tiles that a range of steps goes through, for the warp that copies them: as many tiles as a warp
@@ -239,28 +232,31 @@ struct KeyFeed {
     int id, g;
     bool in;
   };
-  Walk<K, KT> ahead;    // the place whose tile this lane reads next
+  Walk<K, KT> ahead;    // the piece, and which of its steps, whose tile this lane reads next
+  int step;
   Read now, next, last;
   float ks, ks_next;
   int taken;
 
-  // the place of the key tile behind a's: the next step's, or (kKeys) the next unit's
-  static FKV_DEV void to_next_keys(Walk<K, KT>& a, const BlockWeightsParams& p) {
+  static FKV_DEV int blocks_of(const Walk<K, KT>& a, int tile) { return min(TB, ((a.T + 15) >> 4) - TB * tile); }
+  FKV_DEV void skip(const BlockWeightsParams& p, int x) {  // x key tiles on
     if (K == kKeys) {
-      const int skip = static_cast<int>(min(static_cast<long long>(a.count - a.s), a.left)) - 1;
-      a.left -= skip;
-      a.s += skip;
-    }
-    a.advance(p);
-  }
-  static FKV_DEV int tile_of(const Walk<K, KT>& a) { return K == kKeys ? a.t : a.s; }
-  static FKV_DEV int blocks_of(const Walk<K, KT>& a) { return min(TB, ((a.seq.T + 15) >> 4) - TB * tile_of(a)); }
-  FKV_DEV Read read(const BlockWeightsParams& p) {
-    const int j = (threadIdx.x & 31) % TB;
-    Read x = {0, ahead.g, ahead.left > 0 && j < blocks_of(ahead)};
-    if (x.in) x.id = p.block_table[static_cast<size_t>(ahead.b) * p.max_blocks + TB * tile_of(ahead) + j];
 #pragma unroll 1
-    for (int i = 0; i < BATCH; ++i) to_next_keys(ahead, p);
+      for (; x > 0 && ahead.n > 0; --x) ahead.next(p);
+    } else {
+      step += x;
+#pragma unroll 1
+      while (ahead.n > 0 && step >= ahead.n) {
+        step -= ahead.n;
+        ahead.next(p);
+      }
+    }
+  }
+  FKV_DEV Read read(const BlockWeightsParams& p) {
+    const int j = (threadIdx.x & 31) % TB, tile = K == kKeys ? ahead.t : ahead.s + step;
+    Read x = {0, ahead.g, ahead.n > 0 && j < blocks_of(ahead, tile)};
+    if (x.in) x.id = p.block_table[static_cast<size_t>(ahead.b) * p.max_blocks + TB * tile + j];
+    skip(p, BATCH);
     return x;
   }
   // an id out of range reads block 0 and is reported
@@ -274,7 +270,8 @@ struct KeyFeed {
   }
   FKV_DEV void begin(const Walk<K, KT>& at, const BlockWeightsParams& p) {
     ahead = at;
-    for (int i = 0; i < (threadIdx.x & 31) / TB; ++i) to_next_keys(ahead, p);
+    step = 0;
+    skip(p, (threadIdx.x & 31) / TB);
     now = read(p);
     next = read(p);
     ks = scale_of(now, p);
@@ -361,7 +358,7 @@ __global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) 
   for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
   const int e = query_exponent(amax);  // q = q' 2^e
   const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  const size_t at = tile_index(p, s, b, g, static_cast<int>(i));
+  const size_t at = tile_index(p, s.r0, b, g, static_cast<int>(i));
   if ((threadIdx.x & 7) == 0) {
     // a row with a NaN or an infinity makes its scores NaN
     float* out = p.rows + at * 256 + (row >> 1) * 4 + (row & 1);
@@ -389,10 +386,10 @@ __global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) 
 // ---------------------------------------------------------------- the two passes over many rows
 
 // The unit's own tile stays (pass 0: 128 rows, both terms; pass 1: 256 keys, two products of 128), the others stream past it.  One CTA per
-// SM.  Sixteen warps read the scores, a quarter of the columns each: a thread has one row's scores for 32 keys, or two keys' for 32 rows
-// (whose c and lse it reads from shared memory once for both: one key per thread was bound by that, 2,000 cycles per 256 keys and 128
-// rows).  The loops are rolled as far as the arithmetic allows: the warps that copy and issue run their code once per step and fetch
-// it anew when the readers' is too long.
+// SM.  Sixteen warps read the scores: in pass 0 eight of them every other step, a thread one row's scores for 64 keys; in pass 1 all of them
+// every step, a thread two keys' for 32 rows (whose c and lse it reads from shared memory once for both: one key per thread was bound by
+// that, 2,000 cycles per 256 keys and 128 rows).  A wait that need not wait takes 100 to 200 cycles, a step's products 540 (head_dim
+// 128), so the readers wait as seldom as they can, and two warps issue the products of the steps in turn.
 template <int D, Kind K>
 struct PassCfg : Shape<D> {
   using S = Shape<D>;
@@ -404,25 +401,26 @@ struct PassCfg : Shape<D> {
   static constexpr int NY = K == kRows ? 2 : D == 256 ? 1 : 3;  // buffers of the one, stages of the other
   static constexpr int NS = K == kRows ? (D == 256 ? 2 : 8) : (D == 256 ? 2 : 3);
   static constexpr int SBUF = 4 / NT;                           // buffers of a step's scores, 128 NT columns each
-  static constexpr int READERS = 16, THREADS = 32 * (READERS + 2);
-  // K scales in slots: of step u (pass 0; the copies run at most NS + SBUF steps ahead), or of piece r (pass 1: NY ahead of the
-  // products, which are SBUF steps ahead of the readers)
-  static constexpr int SCN = K == kRows ? 16 : 8;
-  static constexpr int SCF = KT / 16;
+  static constexpr int READERS = 16, THREADS = 32 * (READERS + 3);
+  // K scales in slots: of steps 4 b .. 4 b + 3 (pass 0; the copies run at most NS + SBUF steps ahead), or of piece r (pass 1: NY ahead of
+  // the products, which are SBUF steps ahead of the readers)
+  static constexpr int SCN = 8, SCB = K == kRows ? 4 : 1;
+  static constexpr int SCF = K == kRows ? 32 : 16;
   static constexpr int OFF_STAY = 0;
   static constexpr int OFF_STREAM = OFF_STAY + NY * STAY;
   static constexpr int OFF_SC = OFF_STREAM + NS * STREAM;
-  static constexpr int OFF_JOIN = OFF_SC + SCN * SCF * 4;       // the column quarters' results [4][128] float2, [4][256] float
-  static constexpr int OFF_BAR = OFF_JOIN + 4 * 128 * 8;
-  static constexpr int NBAR = 2 * NY + 2 * SBUF + 2 * NS + SCN + 3;
+  static constexpr int JOIN = 4 * 128 * 8;                      // the column parts' results [4][128] float2, [4][256] float, twice
+  static constexpr int OFF_JOIN = OFF_SC + SCN * SCF * 4;
+  static constexpr int OFF_BAR = OFF_JOIN + 2 * JOIN;
+  static constexpr int NBAR = 2 * NY + 2 * SBUF + 2 * NS + SCN + 6;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 64;
   static constexpr uint32_t IDESC = idesc_e4m3_f32(128, 128, 0, 0);
-  static_assert(SCN > (K == kRows ? NS + SBUF : NY + SBUF + 1) && OFF_BAR % 8 == 0, "a slot is rewritten only after its readers are done");
+  static_assert(SCN * SCB > (K == kRows ? NS + SBUF + SCB : NY + SBUF + 1) && OFF_BAR % 8 == 0, "a slot is rewritten only after its readers are done");
   static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// Warps 0 .. 15 read the scores, 16 copies, 17 issues the products.
+// Warps 0 .. 15 read the scores, 16 copies, 17 and 18 issue the products.
 template <int D, Kind K>
 __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     pass_kernel(const __grid_constant__ BlockWeightsParams p, const __grid_constant__ CUtensorMap tmk) {
@@ -440,9 +438,9 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
   uint64_t* x_full = s_free + C::SBUF;  // [NS] the streamed tile of step u in stage u % NS
   uint64_t* x_empty = x_full + C::NS;
   uint64_t* sc_full = x_empty + C::NS;  // [SCN]
-  uint64_t* mma_done = sc_full + C::SCN;
-  uint64_t* j_full = mma_done + 1;      // the column quarters' results of piece r ...
-  uint64_t* j_free = mma_done + 2;      // ... and taken
+  uint64_t* mma_done = sc_full + C::SCN;  // [2]
+  uint64_t* j_full = mma_done + 2;      // [2] the column parts' results of piece r in buffer r % 2 ...
+  uint64_t* j_free = j_full + 2;        // [2] ... and taken
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   volatile int* last_s = abort_s + 1;
@@ -452,20 +450,22 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::NY; ++i) {
       mbar_init(&y_full[i], 1);
-      mbar_init(&y_empty[i], 1);
+      mbar_init(&y_empty[i], 2);  // (both issuing warps)
     }
     for (int i = 0; i < C::SBUF; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], C::READERS);
+      mbar_init(&s_free[i], K == kRows ? C::READERS / 2 : C::READERS);
     }
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(&x_full[i], 1);
       mbar_init(&x_empty[i], K == kKeys ? 1 + C::READERS : 1);  // (the rows' parameters are read by the readers)
     }
     for (int i = 0; i < C::SCN; ++i) mbar_init(&sc_full[i], 1);
-    mbar_init(mma_done, 1);
-    mbar_init(j_full, C::READERS);
-    mbar_init(j_free, K == kRows ? 4 : 8);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&mma_done[i], 1);
+      mbar_init(&j_full[i], C::READERS);
+      mbar_init(&j_free[i], K == kRows ? 4 : 8);
+    }
     *abort_s = 0;
     pend_s[0] = pend_s[5] = 0;
     fence_mbar_init();
@@ -477,181 +477,198 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     tmem_relinquish();
     tc_fence_before();
   }
-  long long W;
-  int N;
-  Place at = first_step<K, C::KT>(p, k, W, N, K == kRows && k == 0 && warp == 0);
+  __shared__ Division<K, C::KT> division;
+  if (warp == 0) {
+    Division<K, C::KT> d;
+    d.first = first_piece<K, C::KT>(p, k, d.W, d.N, K == kRows && k == 0);
+    if (lane == 0) division = d;
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
-  const int G = p.Hq / p.Hkv;
-  const int n = static_cast<int>(at.left);  // steps of this CTA
   int32_t* done = p.done + (K == kRows ? 0 : p.slots);
+  Place at = division.first;
+  int u = 0;  // steps so far
 
-  if (n == 0) {
-    // more CTAs than steps
-  } else if (warp < C::READERS) {
+  if (warp < C::READERS) {
     // ============================================================ the scores' readers
-    // tensor memory lane i, columns 32 part .. + 31 of every product
+    // tensor memory lane i; pass 0: part >> 1 the steps' parity, columns 64 (part & 1) .. + 63; pass 1: columns 32 part .. + 31
     const int part = warp >> 2, i = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 32 * part;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (K == kRows ? 64 * (part & 1) : 32 * part);
     bool ok = true;
-    // pass 0: the row's sum l of 2^(x - m) (of this thread's columns).  m need not be the maximum, only near enough that no sum
-    // overflows: it is the largest score of the first columns, and moves when a sum of 32 reaches 2^60.
-    float m = -kHuge, l = 0.f;
-    float2 acc[C::NT];                      // pass 1: the keys' sums
-    float mine[C::NT];                      // c of the row; ks of the keys
-    int limit[C::NT];                       // keys that the row sees; the first row that sees the key
-    bool whole = false;                     // the unit begins in this CTA
-    for (int u = 0; u < n; ++u) {
-      if (at.begins()) {
-        const int old = at.seq.T - at.seq.rows;
-        whole = at.s == 0;
-        if constexpr (K == kRows) {
-          const long long r = 128LL * at.t + i;
-          const bool is_row = r < static_cast<long long>(at.seq.rows) * G;
-          limit[0] = is_row ? old + static_cast<int>(r / G) + 1 : 0;
-          mine[0] = is_row ? p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1)] : 0.f;
-          m = -kHuge;
-          l = 0.f;
-        } else {
-          if (!wait_warp(&sc_full[at.piece % C::SCN], (at.piece / C::SCN) & 1)) { ok = false; break; }
+    while (ok && at.n > 0) {
+      // pass 0: the row's sum l of 2^(x - m) (of this thread's columns).  m need not be the maximum, only near enough that no sum
+      // overflows: it is the largest score of the first columns, and moves when a sum of 32 reaches 2^60.
+      float m = -kHuge, l = 0.f;
+      float2 acc[C::NT];                      // pass 1: the keys' sums
+      float mine[C::NT];                      // c of the row; ks of the keys
+      int limit[C::NT];                       // keys that the row sees; the first row that sees the key
+      if constexpr (K == kRows) {
+        const int r = 128 * at.t + i;
+        const bool is_row = r < at.rows * at.G;
+        limit[0] = is_row ? at.old() + r / at.G + 1 : 0;
+        mine[0] = is_row ? p.rows[tile_index(p, at.r0, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1)] : 0.f;
+      } else {
+        if (!wait_warp(&sc_full[at.piece % C::SCN], (at.piece / C::SCN) & 1)) ok = false;
 #pragma unroll
-          for (int h = 0; h < C::NT; ++h) {
-            const int key = C::KT * at.t + 128 * h + i;
-            mine[h] = sSc[(at.piece % C::SCN) * C::SCF + 8 * h + (i >> 4)];
-            limit[h] = static_cast<int>(min(max(static_cast<long long>(key) - old, 0LL) * G, static_cast<long long>(INT32_MAX)));
-            acc[h] = make_float2(0.f, 0.f);
-          }
+        for (int h = 0; h < C::NT; ++h) {
+          mine[h] = sSc[(at.piece % C::SCN) * C::SCF + 8 * h + (i >> 4)];
+          limit[h] = max(C::KT * at.t + 128 * h + i - at.old(), 0) * at.G;
+          acc[h] = make_float2(0.f, 0.f);
         }
       }
-      if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
-      const int sb = u % C::SBUF, st = u % C::NS;
-      // this thread's first column: its key, or its row
-      const int c0 = 128 * (K == kRows ? at.s : at.units.first(at.seq, at.t) + at.s) + 32 * part;
+      const int end = u + at.n;
       if constexpr (K == kRows) {
-        if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1) || !wait_warp(&s_full[sb], (u / C::SBUF) & 1)) { ok = false; break; }
-        const float2 ks2 = *reinterpret_cast<const float2*>(sSc + (u % C::SCN) * C::SCF + 2 * part);
-        tc_fence_after();
-        float v[32];
-        tmem_ld32(lane_base + 128 * sb, v);
-        tmem_ld_wait();
-        tc_fence_before();
-        mbar_arrive_warp(&s_free[sb]);
-        if (__any_sync(0xffffffffu, limit[0] < c0 + 32)) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c0 + j >= limit[0]) v[j] = -INFINITY;
-        }
-        // (plus 2^-126, so that a hidden score of -inf stays one where the product is zero)
-        constexpr float kLeast = 1.17549435e-38f;
-        const float a = fmaf(mine[0], ks2.x, kLeast), b2 = fmaf(mine[0], ks2.y, kLeast);
-        // the sum against m; a sum of 2^60 and above, or NaN, moves its row's m to the maximum and is made again (the rows of which
-        // it is not true stay as they are)
+        int c0 = 128 * (at.s + ((u ^ (part >> 1)) & 1)) + 64 * (part & 1);  // this thread's first key in its first step
+        for (int v0 = u + ((u ^ (part >> 1)) & 1); ok && v0 < end; v0 += 2, c0 += 256) {
+          const int sb = v0 % C::SBUF;
+          if ((v0 & 6) == 6 && abort_warp(abort_s)) { ok = false; break; }
+          if (!wait_warp(&sc_full[(v0 / C::SCB) % C::SCN], (v0 / (C::SCB * C::SCN)) & 1) || !wait_warp(&s_full[sb], (v0 / C::SBUF) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const bool any_partly = __any_sync(0xffffffffu, limit[0] < c0 + 64);
+          const float* ks = sSc + ((v0 / C::SCB) % C::SCN) * C::SCF + 8 * (v0 % C::SCB) + 4 * (part & 1);
 #pragma unroll 1
-        for (bool again = false;; again = true) {
-          const float2 a2 = make_float2(a, a), bb = make_float2(b2, b2), t2 = make_float2(-m, -m);
-          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          for (int c = 0; c < 64; c += 32) {
+            float v[32];
+            tmem_ld32(lane_base + 128 * sb + c, v);
+            const float2 ks2 = *reinterpret_cast<const float2*>(ks + c / 16);
+            tmem_ld_wait();
+            if (c == 32) {
+              tc_fence_before();
+              mbar_arrive_warp(&s_free[sb]);
+            }
+            if (any_partly) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), a2, t2), y = __ffma2_rn(make_float2(v[16 + j], v[17 + j]), bb, t2);
-            s0 = __fadd2_rn(s0, make_float2(ex2(x.x), ex2(x.y)));
-            s1 = __fadd2_rn(s1, make_float2(ex2(y.x), ex2(y.y)));
+              for (int j = 0; j < 32; ++j)
+                if (c0 + c + j >= limit[0]) v[j] = -INFINITY;
+            }
+            // (plus 2^-126, so that a hidden score of -inf stays one where the product is zero)
+            constexpr float kLeast = 1.17549435e-38f;
+            const float a = fmaf(mine[0], ks2.x, kLeast), b2 = fmaf(mine[0], ks2.y, kLeast);
+            // the sum against m; a sum of 2^60 and above, or NaN, moves its row's m to the maximum and is made again (the rows of
+            // which it is not true stay as they are)
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+              const float2 a2 = make_float2(a, a), bb = make_float2(b2, b2), t2 = make_float2(-m, -m);
+              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                const float2 x = __ffma2_rn(make_float2(v[j], v[j + 1]), a2, t2), y = __ffma2_rn(make_float2(v[16 + j], v[17 + j]), bb, t2);
+                s0 = __fadd2_rn(s0, make_float2(ex2(x.x), ex2(x.y)));
+                s1 = __fadd2_rn(s1, make_float2(ex2(y.x), ex2(y.y)));
+              }
+              s0 = __fadd2_rn(s0, s1);
+              const float sum = s0.x + s0.y;
+              const bool over = !again && !(sum < 1.152921504606847e18f);
+              if (!__any_sync(0xffffffffu, over)) {
+                l += sum;
+                break;
+              }
+              const float top = over ? fmaxf(m, fmaxf(max_tree<16>(v) * a, max_tree<16>(v + 16) * b2)) : m;
+              l *= ex2(m - top);
+              m = top;
+            }
           }
-          s0 = __fadd2_rn(s0, s1);
-          const float sum = s0.x + s0.y;
-          const bool over = !again && !(sum < 1.152921504606847e18f);
-          if (!__any_sync(0xffffffffu, over)) {
-            l += sum;
-            break;
-          }
-          const float top = over ? fmaxf(m, fmaxf(max_tree<16>(v) * a, max_tree<16>(v + 16) * b2)) : m;
-          l *= ex2(m - top);
-          m = top;
         }
       } else {
-        const bool any_partly = __any_sync(0xffffffffu, limit[0] > c0 || limit[C::NT - 1] > c0);
-        if (!wait_warp(&s_full[sb], (u / C::SBUF) & 1)) { ok = false; break; }
-        tc_fence_after();
-        const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + 16 * part;
+        int c0 = 128 * (at.first() + at.s) + 32 * part;  // this thread's first row
+        for (int v0 = u; ok && v0 < end; ++v0, c0 += 128) {
+          const int sb = v0 % C::SBUF, st = v0 % C::NS;
+          if ((v0 & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+          const bool any_partly = __any_sync(0xffffffffu, limit[0] > c0 || limit[C::NT - 1] > c0);
+          if (!wait_warp(&s_full[sb], (v0 / C::SBUF) & 1)) { ok = false; break; }
+          tc_fence_after();
+          const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + 16 * part;
 #pragma unroll 1
-        for (int c = 0; c < 32; c += 16) {
-          float v[C::NT][16];
+          for (int c = 0; c < 32; c += 16) {
+            float v[C::NT][16];
 #pragma unroll
-          for (int h = 0; h < C::NT; ++h) tmem_ld16(lane_base + 128 * (C::NT * sb + h) + c, v[h]);
-          tmem_ld_wait();
+            for (int h = 0; h < C::NT; ++h) tmem_ld16(lane_base + 128 * (C::NT * sb + h) + c, v[h]);
+            tmem_ld_wait();
+            if (c == 16) {
+              tc_fence_before();
+              mbar_arrive_warp(&s_free[sb]);
+            }
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float4 r = rp[(c + j) / 2];
+            for (int j = 0; j < 16; j += 2) {
+              const float4 r = rp[(c + j) / 2];
 #pragma unroll
-            for (int h = 0; h < C::NT; ++h) {
-              float2 x = __ffma2_rn(__fmul2_rn(make_float2(v[h][j], v[h][j + 1]), make_float2(mine[h], mine[h])), make_float2(r.x, r.y), make_float2(r.z, r.w));
-              float2 e = make_float2(ex2(x.x), ex2(x.y));
-              if (any_partly) {  // (a hidden score has no weight, whatever its row's sum is)
-                if (c0 + c + j < limit[h]) e.x = 0.f;
-                if (c0 + c + j + 1 < limit[h]) e.y = 0.f;
+              for (int h = 0; h < C::NT; ++h) {
+                const float2 x = __ffma2_rn(__fmul2_rn(make_float2(v[h][j], v[h][j + 1]), make_float2(mine[h], mine[h])), make_float2(r.x, r.y), make_float2(r.z, r.w));
+                v[h][j] = ex2(x.x);
+                v[h][j + 1] = ex2(x.y);
               }
-              acc[h] = __fadd2_rn(acc[h], e);
             }
+            if (any_partly) {  // (a hidden score has no weight, whatever its row's sum is)
+#pragma unroll
+              for (int h = 0; h < C::NT; ++h)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  if (c0 + c + j < limit[h]) v[h][j] = 0.f;
+            }
+#pragma unroll
+            for (int h = 0; h < C::NT; ++h)
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) acc[h] = __fadd2_rn(acc[h], make_float2(v[h][j], v[h][j + 1]));
           }
+          mbar_arrive_warp(&x_empty[st]);
         }
-        tc_fence_before();
-        mbar_arrive_warp(&s_free[sb]);
-        mbar_arrive_warp(&x_empty[st]);
       }
-      if (at.ends()) {
-        // ---- the column quarters of the piece meet in shared memory
-        float2* row_join = reinterpret_cast<float2*>(smem + C::OFF_JOIN);
-        float* key_join = reinterpret_cast<float*>(smem + C::OFF_JOIN);
-        if (at.piece > 0 && !wait_warp(j_free, (at.piece - 1) & 1)) { ok = false; break; }
+      u = end;
+      if (!ok) break;
+      // ---- the column parts of the piece meet in shared memory
+      const int jb = at.piece & 1;
+      float2* row_join = reinterpret_cast<float2*>(smem + C::OFF_JOIN + jb * C::JOIN);
+      float* key_join = reinterpret_cast<float*>(row_join);
+      if (at.piece > 1 && !wait_warp(&j_free[jb], ((at.piece >> 1) - 1) & 1)) { ok = false; break; }
+      if constexpr (K == kRows) {
+        row_join[part * 128 + i] = make_float2(m, l);
+      } else {
+#pragma unroll
+        for (int h = 0; h < C::NT; ++h) key_join[part * 256 + 128 * h + i] = acc[h].x + acc[h].y;
+      }
+      mbar_arrive_warp(&j_full[jb]);
+      if (warp < (K == kRows ? 4 : 8)) {
+        if (!wait_warp(&j_full[jb], (at.piece >> 1) & 1)) { ok = false; break; }
+        int k0 = k, ns = 1;
+        if (!at.whole()) {
+          k0 = cta_of(at.unit0, division.W, division.N);
+          ns = cta_of(at.unit0 + at.count - 1, division.W, division.N) - k0 + 1;
+        }
+        const long long place = piece_place(k, k0);
         if constexpr (K == kRows) {
-          row_join[part * 128 + i] = make_float2(m, l);
+          float top = -kHuge, sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float2 y = row_join[x * 128 + i];
+            const float mx = fmaxf(top, y.x);
+            sum = sum * ex2(top - mx) + y.y * ex2(y.x - mx);
+            top = mx;
+          }
+          if (ns > 1) p.pieces[place * 128 + i] = make_float2(top, sum);
+          else if (limit[0] > 0) p.rows[tile_index(p, at.r0, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(top + lg2(sum));
         } else {
-#pragma unroll
-          for (int h = 0; h < C::NT; ++h) key_join[part * 256 + 128 * h + i] = acc[h].x + acc[h].y;
+          const int j = threadIdx.x, key = C::KT * at.t + j;
+          const float sum = (key_join[j] + key_join[256 + j]) + (key_join[512 + j] + key_join[768 + j]);
+          if (ns > 1) {
+            p.sums[place * C::KT + j] = sum;
+          } else if (key < at.T) {
+            float* w = p.weights + (static_cast<size_t>(at.b) * p.Hkv + at.g) * p.weights_len + key;
+            *w = key < at.old() && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
+          }
         }
-        mbar_arrive_warp(j_full);
-        if (warp < (K == kRows ? 4 : 8)) {
-          if (!wait_warp(j_full, at.piece & 1)) { ok = false; break; }
-          int k0 = k, ns = 1;
-          if (!whole || at.s + 1 != at.count) {
-            k0 = cta_of(at.unit0, W, N);
-            ns = cta_of(at.unit0 + at.count - 1, W, N) - k0 + 1;
-          }
-          const long long place = piece_place(k, k0);
-          if constexpr (K == kRows) {
-            float top = -kHuge, sum = 0.f;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float2 y = row_join[x * 128 + i];
-              const float mx = fmaxf(top, y.x);
-              sum = sum * ex2(top - mx) + y.y * ex2(y.x - mx);
-              top = mx;
-            }
-            if (ns > 1) p.pieces[place * 128 + i] = make_float2(top, sum);
-            else if (limit[0] > 0) p.rows[tile_index(p, at.seq, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(top + lg2(sum));
-          } else {
-            const int j = threadIdx.x, key = C::KT * at.t + j;
-            const float sum = (key_join[j] + key_join[256 + j]) + (key_join[512 + j] + key_join[768 + j]);
-            if (ns > 1) {
-              p.sums[place * C::KT + j] = sum;
-            } else if (key < at.seq.T) {
-              float* w = p.weights + (static_cast<size_t>(at.b) * p.Hkv + at.g) * p.weights_len + key;
-              *w = key < at.seq.T - at.seq.rows && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
-            }
-          }
-          mbar_arrive_warp(j_free);
-          if (ns > 1 && threadIdx.x == 0) {
-            volatile int* pend = pend_s + (k == k0 ? 5 : 0);
-            pend[0] = ns;
-            pend[1] = k0;
-            pend[2] = at.b;
-            pend[3] = at.g;
-            pend[4] = at.t;
-          }
+        mbar_arrive_warp(&j_free[jb]);
+        if (ns > 1 && threadIdx.x == 0) {
+          volatile int* pend = pend_s + (k == k0 ? 5 : 0);
+          pend[0] = ns;
+          pend[1] = k0;
+          pend[2] = at.b;
+          pend[3] = at.g;
+          pend[4] = at.t;
         }
       }
-      at.advance(p);
+      at.next(p);
     }
     tmem_ld_wait();  // no load left in flight on an early exit
     if (!ok) {
@@ -662,19 +679,18 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     // ============================================================ copies
     using Feed = KeyFeed<K, C::KT>;
     int stay_pieces = 0;            // pieces whose tile was requested
-    int used = 0;                   // steps whose streamed tile was requested
     size_t held[C::NS];             // pass 1: the row tile that a stage holds
 #pragma unroll
     for (int s = 0; s < C::NS; ++s) held[s] = ~static_cast<size_t>(0);
     Feed feed;
-    feed.begin(at, p);
-    // The keys of `at` (a block per lane; blocks behind the sequence are left as they are: their keys are hidden, or their sums not
-    // stored) and their scales.
-    auto copy_keys = [&](uint8_t* dst, uint64_t* full, int slot) {
+    if (at.n > 0) feed.begin(at, p);
+    // The keys of tile `tile` (a block per lane; blocks behind the sequence are left as they are: their keys are hidden, or their sums
+    // not stored) and their scales.
+    auto copy_keys = [&](uint8_t* dst, uint64_t* full, int tile, int x) {  // x: the step (pass 0) or piece
       int id;
       float ks;
       feed.take(p, id, ks);
-      const int nblk = Feed::blocks_of(at);
+      const int nblk = Feed::blocks_of(at, tile);
       if (lane == 0) mbar_arrive_expect_tx(full, nblk * 16 * D);
       __syncwarp();
       if (lane < nblk) {
@@ -682,105 +698,116 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
         for (int s = 0; s < C::NSUB; ++s)
           tma_load_4d(dst + (lane >> 3) * C::TILE + s * C::SUB + (lane & 7) * 16 * C::RB, &tmk, s * C::RB, 0, at.g, id, full);
       }
-      if (lane < Feed::TB) sSc[slot * C::SCF + lane] = ks;
-      mbar_arrive_warp(&sc_full[slot]);
+      if (x % C::SCB == 0) {
+        const int slot = (x / C::SCB) % C::SCN;
+        if (K == kRows) sSc[slot * C::SCF + lane] = feed.ks;  // (a batch: the scales of four steps)
+        else if (lane < Feed::TB) sSc[slot * C::SCF + lane] = ks;
+        mbar_arrive_warp(&sc_full[slot]);
+      }
     };
     bool ok = true;
-    for (int u = 0; u < n; ++u) {
-      if (abort_warp(abort_s)) break;
-      if (at.begins()) {
-        const int yb = at.piece % C::NY;
-        if (at.piece >= C::NY && !wait_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1)) { ok = false; break; }
-        if constexpr (K == kRows) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&y_full[yb], C::QT);
-            bulk_g2s(sStay + yb * C::STAY, p.q_tiles + tile_index(p, at.seq, at.b, at.g, at.t) * C::QT, C::QT, &y_full[yb]);
-          }
-          __syncwarp();
-        } else {
-          copy_keys(sStay + yb * C::STAY, &y_full[yb], at.piece % C::SCN);
-        }
-        stay_pieces = at.piece + 1;
-      }
-      const int st = u % C::NS;
-      if (u >= C::NS && !wait_warp(&x_empty[st], (u / C::NS - 1) & 1)) { ok = false; break; }
-      uint8_t* dst = sStream + st * C::STREAM;
+    while (ok && at.n > 0) {
+      const int yb = at.piece % C::NY;
+      if (at.piece >= C::NY && !wait_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1)) { ok = false; break; }
+      size_t tile = tile_index(p, at.r0, at.b, at.g, K == kRows ? at.t : at.first() + at.s);
       if constexpr (K == kRows) {
-        copy_keys(dst, &x_full[st], u % C::SCN);
-      } else {
-        const size_t tile = tile_index(p, at.seq, at.b, at.g, at.units.first(at.seq, at.t) + at.s);
-        bool same = false;
-#pragma unroll
-        for (int s = 0; s < C::NS; ++s) {
-          if (s != st) continue;
-          same = held[s] == tile;
-          held[s] = tile;
-        }
         if (lane == 0) {
-          if (same) {
-            mbar_arrive(&x_full[st]);
-          } else {
-            mbar_arrive_expect_tx(&x_full[st], C::QT + kRowBytes);
-            bulk_g2s(dst, p.q_tiles + tile * C::QT, C::QT, &x_full[st]);
-            bulk_g2s(dst + C::QT, p.rows + tile * 256, kRowBytes, &x_full[st]);
-          }
+          mbar_arrive_expect_tx(&y_full[yb], C::QT);
+          bulk_g2s(sStay + yb * C::STAY, p.q_tiles + tile * C::QT, C::QT, &y_full[yb]);
         }
         __syncwarp();
+      } else {
+        copy_keys(sStay + yb * C::STAY, &y_full[yb], at.t, at.piece);
       }
-      at.advance(p);
-      used = u + 1;
+      stay_pieces = at.piece + 1;
+      const int end = u + at.n;
+      for (int x = 0; u < end; ++u, ++x, tile += p.Hkv) {
+        if (abort_warp(abort_s)) { ok = false; break; }
+        const int st = u % C::NS;
+        if (u >= C::NS && !wait_warp(&x_empty[st], (u / C::NS - 1) & 1)) { ok = false; break; }
+        uint8_t* dst = sStream + st * C::STREAM;
+        if constexpr (K == kRows) {
+          copy_keys(dst, &x_full[st], at.s + x, u);
+        } else {
+          bool same = false;
+#pragma unroll
+          for (int s = 0; s < C::NS; ++s) {
+            if (s != st) continue;
+            same = held[s] == tile;
+            held[s] = tile;
+          }
+          if (lane == 0) {
+            if (same) {
+              mbar_arrive(&x_full[st]);
+            } else {
+              mbar_arrive_expect_tx(&x_full[st], C::QT + kRowBytes);
+              bulk_g2s(dst, p.q_tiles + tile * C::QT, C::QT, &x_full[st]);
+              bulk_g2s(dst + C::QT, p.rows + tile * 256, kRowBytes, &x_full[st]);
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (ok) at.next(p);
     }
     if (!ok) {
-      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      if (lane == 0 && *abort_s == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
     // let every copy land before the CTA can exit
     if (lane == 0) {
       for (int s = 0; s < C::NS; ++s)
-        if (used > s) wait_ns(&x_full[s], ((used - 1 - s) / C::NS) & 1);
+        if (u > s) wait_ns(&x_full[s], ((u - 1 - s) / C::NS) & 1);
       for (int s = 0; s < C::NY; ++s)
         if (stay_pieces > s) wait_ns(&y_full[s], ((stay_pieces - 1 - s) / C::NY) & 1);
     }
     __syncwarp();
   } else {
     // ============================================================ products
+    // Warp w the steps of its parity.  A piece's tile is free when both warps' products with it are done.
+    const int w = warp - C::READERS - 1;
     const uint64_t dY = smem_desc(smem_u32(sStay), 16, 8 * C::RB, C::SWZ), dX = smem_desc(smem_u32(sStream), 16, 8 * C::RB, C::SWZ);
     bool ok = true;
-    for (int u = 0; u < n; ++u) {
-      if ((u & 7) == 7 && abort_warp(abort_s)) break;
-      const int yb = at.piece % C::NY, st = u % C::NS, sb = u % C::SBUF;
-      if (at.begins()) ok = wait_warp(&y_full[yb], (at.piece / C::NY) & 1);
-      if (ok) ok = wait_warp(&x_full[st], (u / C::NS) & 1);
-      if (ok && u >= C::SBUF) ok = wait_warp(&s_free[sb], (u / C::SBUF - 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      const bool ends = at.ends();
-      if (elect_one()) {
+    while (ok && at.n > 0) {
+      const int yb = at.piece % C::NY, end = u + at.n;
+      ok = wait_warp(&y_full[yb], (at.piece / C::NY) & 1);
+      for (int v0 = u + ((u ^ w) & 1); ok && v0 < end; v0 += 2) {
+        if ((v0 & 6) == 6 && abort_warp(abort_s)) { ok = false; break; }
+        const int st = v0 % C::NS, sb = v0 % C::SBUF;
+        ok = wait_warp(&x_full[st], (v0 / C::NS) & 1);
+        if (ok && v0 >= C::SBUF) ok = wait_warp(&s_free[sb], (v0 / C::SBUF - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int h = 0; h < C::NT; ++h)
+          for (int h = 0; h < C::NT; ++h)
 #pragma unroll
-          for (int term = 0; term < 2; ++term)
+            for (int term = 0; term < 2; ++term)
 #pragma unroll
-            for (int kk = 0; kk < D / 32; ++kk) {
-              const int byte = kk * 32;
-              const uint32_t off = (byte / C::RB) * C::SUB + (byte % C::RB);
-              umma_f8(tmem + 128 * (C::NT * sb + h), desc_add(dY, yb * C::STAY + (K == kRows ? term : h) * C::TILE + off),
-                      desc_add(dX, st * C::STREAM + (K == kKeys ? term : 0) * C::TILE + off), C::IDESC, (term > 0 || kk > 0) ? 1u : 0u);
-            }
-        umma_commit(&s_full[sb]);
-        umma_commit(&x_empty[st]);
-        if (ends) umma_commit(&y_empty[yb]);
+              for (int kk = 0; kk < D / 32; ++kk) {
+                const int byte = kk * 32;
+                const uint32_t off = (byte / C::RB) * C::SUB + (byte % C::RB);
+                umma_f8(tmem + 128 * (C::NT * sb + h), desc_add(dY, yb * C::STAY + (K == kRows ? term : h) * C::TILE + off),
+                        desc_add(dX, st * C::STREAM + (K == kKeys ? term : 0) * C::TILE + off), C::IDESC, (term > 0 || kk > 0) ? 1u : 0u);
+              }
+          umma_commit(&s_full[sb]);
+          umma_commit(&x_empty[st]);
+        }
+        __syncwarp();
       }
+      u = end;
+      if (!ok) break;
+      if (elect_one()) umma_commit(&y_empty[yb]);
       __syncwarp();
-      at.advance(p);
+      at.next(p);
     }
     if (!ok) {
-      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      if (lane == 0 && *abort_s == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
-    if (elect_one()) umma_commit(mma_done);  // every product issued here completes before the tensor memory is released
+    if (elect_one()) umma_commit(&mma_done[w]);  // every product issued here completes before the tensor memory is released
     __syncwarp();
-    wait_warp(mma_done, 0);
+    wait_warp(&mma_done[w], 0);
   }
   __syncthreads();
   if (warp == C::READERS + 1) {
@@ -806,7 +833,7 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
           l = l * ex2(m - top) + y.y * ex2(y.x - top);
           m = top;
         }
-        if (128LL * t + i < static_cast<long long>(s.rows) * G) p.rows[tile_index(p, s, b, g, t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(m + lg2(l));
+        if (128 * t + i < s.rows * (p.Hq / p.Hkv)) p.rows[tile_index(p, s.r0, b, g, t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(m + lg2(l));
       } else {
         float sum = 0.f;
 #pragma unroll 4
@@ -842,9 +869,9 @@ struct ScoreCfg : Shape<D> {
   static constexpr int OFF_K = (OFF_Q + S::NSUB * QSUB + 1023) / 1024 * 1024;
   static constexpr int OFF_SC = OFF_K + NS * KTILE;
   static constexpr int OFF_C = OFF_SC + SCN * TPB * 4;          // c of the rows [16]
-  static constexpr int OFF_RED = OFF_C + 16 * 4;                // [4 warps][RN] float2
-  static constexpr int OFF_BAR = OFF_RED + 4 * RN * 8;
-  static constexpr int NBAR = 6 + 2 * NS + SCN;
+  static constexpr int OFF_RED = OFF_C + 16 * 4;                // [2][4 warps][RN] float2
+  static constexpr int OFF_BAR = OFF_RED + 2 * 4 * RN * 8;
+  static constexpr int NBAR = 7 + 2 * NS + SCN;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_MISC + 16;
   static constexpr uint32_t IDESC = idesc_e4m3_f32(128, NP, 0, 0);
@@ -879,7 +906,8 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
   uint64_t* s_full = bars + 1;    // [2]
   uint64_t* s_free = bars + 3;    // [2]
   uint64_t* mma_done = bars + 5;
-  uint64_t* k_full = bars + 6;
+  uint64_t* r_full = bars + 6;    // the warps' results of piece r
+  uint64_t* k_full = bars + 7;
   uint64_t* k_empty = k_full + C::NS;
   uint64_t* sc_full = k_empty + C::NS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -888,6 +916,7 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, k = blockIdx.x;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 4);
+    mbar_init(r_full, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], 4);
@@ -907,148 +936,158 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
     tmem_relinquish();
     tc_fence_before();
   }
-  long long W;
-  int N;
-  Place at = first_step<kScores, C::BN>(p, k, W, N, k == 0 && warp == 0);
+  __shared__ Division<kScores, C::BN> division;
+  if (warp == 0) {
+    Division<kScores, C::BN> d;
+    d.first = first_piece<kScores, C::BN>(p, k, d.W, d.N, k == 0);
+    if (lane == 0) division = d;
+  }
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
-  const int G = p.Hq / p.Hkv;
-  const long long n = at.left;
+  Place at = division.first;
+  const int G = at.G;
+  int u = 0;  // steps so far
 
-  if (n == 0) {
-    // more CTAs than tiles
-  } else if (warp < 4) {
+  if (warp < 4) {
     // ============================================================ the scores' readers
     const int i = threadIdx.x;  // key i (and 128 + i) of a tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float m[RN], l[RN];
     bool ok = true;
-    for (int u = 0; u < n; ++u) {
-      if (at.begins()) {
-        // ---- the piece's query: row r scaled to (224, 448], as two terms, 8 threads per row (the products with the
-        // last piece's query are done: their scores were read)
-        const int row = i >> 3, R = at.seq.rows * G;
-        constexpr int NCH = (D / 16 + 7) / 8;
-        uint32_t in[NCH][8];
-        uint32_t amax = 0;
+    while (ok && at.n > 0) {
+      // ---- the piece's query: row r scaled to (224, 448], as two terms, 8 threads per row (the products with the
+      // last piece's query are done: their scores were read)
+      const int row = i >> 3, R = at.rows * G;
+      constexpr int NCH = (D / 16 + 7) / 8;
+      uint32_t in[NCH][8];
+      uint32_t amax = 0;
 #pragma unroll
-        for (int cc = 0; cc < NCH; ++cc) {
-          const int ch = (i & 7) + 8 * cc;
+      for (int cc = 0; cc < NCH; ++cc) {
+        const int ch = (i & 7) + 8 * cc;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
-          if (row < R && ch < D / 16) {
-            const int token = row / G;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<size_t>(at.seq.r0) + token) * p.Hq + at.g * G + (row - token * G)) * D) + 2 * ch;
-            const uint4 x = src[0], y = src[1];
-            in[cc][0] = x.x; in[cc][1] = x.y; in[cc][2] = x.z; in[cc][3] = x.w;
-            in[cc][4] = y.x; in[cc][5] = y.y; in[cc][6] = y.z; in[cc][7] = y.w;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
+        for (int j = 0; j < 8; ++j) in[cc][j] = 0u;
+        if (row < R && ch < D / 16) {
+          const int token = row / G;
+          const uint4* src = reinterpret_cast<const uint4*>(p.q + ((static_cast<size_t>(at.r0) + token) * p.Hq + at.g * G + (row - token * G)) * D) + 2 * ch;
+          const uint4 x = src[0], y = src[1];
+          in[cc][0] = x.x; in[cc][1] = x.y; in[cc][2] = x.z; in[cc][3] = x.w;
+          in[cc][4] = y.x; in[cc][5] = y.y; in[cc][6] = y.z; in[cc][7] = y.w;
         }
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-        const int e = query_exponent(amax);
-        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        if ((i & 7) == 0)
-          sC[row] = amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __uint_as_float(0x7FC00000u);
+        for (int j = 0; j < 8; ++j) amax = max(amax, max((in[cc][j] << 16) & 0x7FFF0000u, in[cc][j] & 0x7FFF0000u));
+      }
 #pragma unroll
-        for (int cc = 0; cc < NCH; ++cc) {
-          const int c = (i & 7) + 8 * cc;
-          if (c >= D / 16 || row >= C::LO) continue;
-          uint32_t wh[4], wl[4];
+      for (int off = 1; off < 8; off <<= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      const int e = query_exponent(amax);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      if ((i & 7) == 0)
+        sC[row] = amax < 0x7F800000u ? p.sm_scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23) : __uint_as_float(0x7FC00000u);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
-            split4_query(make_float2(x0.x * down, x0.y * down), make_float2(x1.x * down, x1.y * down), wh[j], wl[j]);
-          }
-          const int byte = c * 16;
-          uint8_t* sub = sQ + (byte / C::RB) * C::QSUB;
-          *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>(row * C::RB + byte % C::RB), C::RB)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-          *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>((C::LO + row) * C::RB + byte % C::RB), C::RB)) =
-              make_uint4(wl[0], wl[1], wl[2], wl[3]);
+      for (int cc = 0; cc < NCH; ++cc) {
+        const int c = (i & 7) + 8 * cc;
+        if (c >= D / 16 || row >= C::LO) continue;
+        uint32_t wh[4], wl[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x0 = bf16x2_to_f2(in[cc][2 * j]), x1 = bf16x2_to_f2(in[cc][2 * j + 1]);
+          split4_query(make_float2(x0.x * down, x0.y * down), make_float2(x1.x * down, x1.y * down), wh[j], wl[j]);
         }
-        fence_proxy_async_smem();
-        mbar_arrive_warp(q_full);
-        if (!wait_warp(q_full, at.piece & 1)) { ok = false; break; }  // every warp's rows and c are there
+        const int byte = c * 16;
+        uint8_t* sub = sQ + (byte / C::RB) * C::QSUB;
+        *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>(row * C::RB + byte % C::RB), C::RB)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+        *reinterpret_cast<uint4*>(sub + swz(static_cast<uint32_t>((C::LO + row) * C::RB + byte % C::RB), C::RB)) =
+            make_uint4(wl[0], wl[1], wl[2], wl[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive_warp(q_full);
+      if (!wait_warp(q_full, at.piece & 1)) { ok = false; break; }  // every warp's rows and c are there
 #pragma unroll
-        for (int r = 0; r < RN; ++r) {
-          m[r] = -kHuge;
-          l[r] = 0.f;
+      for (int r = 0; r < RN; ++r) {
+        m[r] = -kHuge;
+        l[r] = 0.f;
+      }
+      const int end = u + at.n;
+      for (int x0 = 0; ok && u < end; ++u, ++x0) {
+        if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+        const int sb = u & 1;
+        if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1) || !wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int hh = 0; hh < C::NHALF; ++hh) {
+          float v[2 * RN];
+          const uint32_t col = lane_base + (sb * C::NHALF + hh) * C::NP;
+          if constexpr (RN == 4) {
+            tmem_ld4(col, v);
+            tmem_ld4(col + C::LO, v + 4);
+          } else if constexpr (RN == 8) {
+            tmem_ld16(col, v);
+          } else {
+            tmem_ld32(col, v);
+          }
+          const float ks = sSc[(u % C::SCN) * C::TPB + 8 * hh + (i >> 4)];
+          const int key = C::BN * (at.s + x0) + 128 * hh + i;
+          tmem_ld_wait();
+          if (hh + 1 == C::NHALF) {
+            tc_fence_before();
+            mbar_arrive_warp(&s_free[sb]);
+          }
+          // the first row that sees the key (none behind the sequence)
+          const int from = key < at.T ? max(key - (at.T - at.rows), 0) * G : RN;
+#pragma unroll
+          for (int r = 0; r < RN; ++r) {
+            float x = (v[r] + v[RN + r]) * (sC[r] * ks);
+            if (r < from) x = -INFINITY;
+            v[r] = x;
+            // one exponential: of the smaller against the larger
+            const float e = ex2(-fabsf(x - m[r]));
+            l[r] = x > m[r] ? fmaf(l[r], e, 1.f) : l[r] + e;
+            m[r] = fmaxf(m[r], x);
+          }
+          if (key < at.T) {
+            float4* dst = reinterpret_cast<float4*>(p.scores + ((static_cast<size_t>(at.b) * p.Hkv + at.g) * p.max_blocks * 16 + key) * RN);
+#pragma unroll
+            for (int r = 0; r < RN; r += 4) dst[r / 4] = make_float4(v[r], v[r + 1], v[r + 2], v[r + 3]);
+          }
         }
       }
-      if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
-      const int sb = u & 1;
-      if (!wait_warp(&sc_full[u % C::SCN], (u / C::SCN) & 1) || !wait_warp(&s_full[sb], (u >> 1) & 1)) { ok = false; break; }
-      tc_fence_after();
+      if (!ok) break;
+      // ---- the warps' maxima and sums meet in shared memory; behind this barrier no warp reads the piece's query constants
+      float2* red = sRed + (at.piece & 1) * 4 * RN;
 #pragma unroll
-      for (int hh = 0; hh < C::NHALF; ++hh) {
-        float v[2 * RN];
-        const uint32_t col = lane_base + (sb * C::NHALF + hh) * C::NP;
-        if constexpr (RN == 4) {
-          tmem_ld4(col, v);
-          tmem_ld4(col + C::LO, v + 4);
-        } else if constexpr (RN == 8) {
-          tmem_ld16(col, v);
-        } else {
-          tmem_ld32(col, v);
-        }
-        const float ks = sSc[(u % C::SCN) * C::TPB + 8 * hh + (i >> 4)];
-        const int key = C::BN * at.s + 128 * hh + i;
-        tmem_ld_wait();
-        if (hh + 1 == C::NHALF) {
-          tc_fence_before();
-          mbar_arrive_warp(&s_free[sb]);
-        }
-        // the first row that sees the key (none behind the sequence)
-        const int from = key < at.seq.T ? max(key - (at.seq.T - at.seq.rows), 0) * G : RN;
+      for (int r = 0; r < RN; ++r) {
 #pragma unroll
-        for (int r = 0; r < RN; ++r) {
-          float x = (v[r] + v[RN + r]) * (sC[r] * ks);
-          if (r < from) x = -INFINITY;
-          v[r] = x;
-          // one exponential: of the smaller against the larger
-          const float e = ex2(-fabsf(x - m[r]));
-          l[r] = x > m[r] ? fmaf(l[r], e, 1.f) : l[r] + e;
-          m[r] = fmaxf(m[r], x);
+        for (int off = 16; off > 0; off >>= 1) {
+          const float m2 = __shfl_xor_sync(0xffffffffu, m[r], off), l2 = __shfl_xor_sync(0xffffffffu, l[r], off), top = fmaxf(m[r], m2);
+          l[r] = l[r] * ex2(m[r] - top) + l2 * ex2(m2 - top);
+          m[r] = top;
         }
-        if (key < at.seq.T) {
-          float4* dst = reinterpret_cast<float4*>(p.scores + ((static_cast<size_t>(at.b) * p.Hkv + at.g) * p.max_blocks * 16 + key) * RN);
-#pragma unroll
-          for (int r = 0; r < RN; r += 4) dst[r / 4] = make_float4(v[r], v[r + 1], v[r + 2], v[r + 3]);
-        }
+        if (lane == 0) red[warp * RN + r] = make_float2(m[r], l[r]);
       }
-      if (at.ends()) {
-        const int k0 = cta_of(at.unit0, W, N), ns = cta_of(at.unit0 + at.count - 1, W, N) - k0 + 1;
-        if (i == 0 && k == k0) p.units[at.b * p.Hkv + at.g] = make_int2(k0, ns);
-#pragma unroll
-        for (int r = 0; r < RN; ++r) {
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) {
-            const float m2 = __shfl_xor_sync(0xffffffffu, m[r], off), l2 = __shfl_xor_sync(0xffffffffu, l[r], off), top = fmaxf(m[r], m2);
-            l[r] = l[r] * ex2(m[r] - top) + l2 * ex2(m2 - top);
-            m[r] = top;
-          }
-          if (lane == 0) sRed[warp * RN + r] = make_float2(m[r], l[r]);
+      mbar_arrive_warp(r_full);
+      if (!wait_warp(r_full, at.piece & 1)) { ok = false; break; }
+      if (warp == 0) {
+        int k0 = k, ns = 1;
+        if (!at.whole()) {
+          k0 = cta_of(at.unit0, division.W, division.N);
+          ns = cta_of(at.unit0 + at.count - 1, division.W, division.N) - k0 + 1;
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (i < RN) {
+        if (lane == 0 && k == k0) p.units[at.b * p.Hkv + at.g] = make_int2(k0, ns);
+        if (lane < RN) {
           float M = -kHuge, L = 0.f;
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            const float2 y = sRed[w * RN + i];
+            const float2 y = red[w * RN + lane];
             const float top = fmaxf(M, y.x);
             L = L * ex2(M - top) + y.y * ex2(y.x - top);
             M = top;
           }
-          // a unit that begins here lies at the odd place even if it ends here too
-          p.pieces[(k == k0 && ns == 1 ? 2LL * p.slots + static_cast<long long>(at.b) * p.Hkv + at.g : piece_place(k, k0)) * 16 + i] = make_float2(M, L);
+          // (a unit in one piece has a place of its own: a CTA may have many)
+          p.pieces[(ns == 1 ? 2LL * p.slots + static_cast<long long>(at.b) * p.Hkv + at.g : piece_place(k, k0)) * 16 + lane] = make_float2(M, L);
         }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
       }
-      at.advance(p);
+      at.next(p);
     }
     tmem_ld_wait();
     if (!ok) {
@@ -1059,65 +1098,67 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
     // ============================================================ K copies and scales
     using Feed = KeyFeed<kScores, C::BN>;
     Feed feed;
-    feed.begin(at, p);
-    long long used = 0;
-    for (int u = 0; u < n; ++u) {
-      if (abort_warp(abort_s)) break;
-      const int st = u % C::NS;
-      if (u >= C::NS && !wait_warp(&k_empty[st], (u / C::NS - 1) & 1)) {
-        if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
-        *abort_s = 1;
-        break;
-      }
-      int id;
-      float ks;
-      feed.take(p, id, ks);
-      const int nblk = Feed::blocks_of(at);
-      if (lane == 0) mbar_arrive_expect_tx(&k_full[st], nblk * 16 * D);
-      __syncwarp();
-      if (lane < nblk) {
+    if (at.n > 0) feed.begin(at, p);
+    bool ok = true;
+    for (; ok && at.n > 0; at.next(p)) {
+      const int end = u + at.n;
+      for (int x = 0; u < end; ++u, ++x) {
+        const int st = u % C::NS;
+        if (abort_warp(abort_s) || (u >= C::NS && !wait_warp(&k_empty[st], (u / C::NS - 1) & 1))) { ok = false; break; }
+        int id;
+        float ks;
+        feed.take(p, id, ks);
+        const int nblk = Feed::blocks_of(at, at.s + x);
+        if (lane == 0) mbar_arrive_expect_tx(&k_full[st], nblk * 16 * D);
+        __syncwarp();
+        if (lane < nblk) {
 #pragma unroll
-        for (int s = 0; s < C::NSUB; ++s) tma_load_4d(sK + st * C::KTILE + s * C::KSUB + lane * 16 * C::RB, &tmk, s * C::RB, 0, at.g, id, &k_full[st]);
+          for (int s = 0; s < C::NSUB; ++s) tma_load_4d(sK + st * C::KTILE + s * C::KSUB + lane * 16 * C::RB, &tmk, s * C::RB, 0, at.g, id, &k_full[st]);
+        }
+        if (lane < C::TPB) sSc[(u % C::SCN) * C::TPB + lane] = ks;
+        mbar_arrive_warp(&sc_full[u % C::SCN]);
       }
-      used = u + 1;
-      if (lane < C::TPB) sSc[(u % C::SCN) * C::TPB + lane] = ks;
-      mbar_arrive_warp(&sc_full[u % C::SCN]);
-      at.advance(p);
+    }
+    if (!ok) {
+      if (lane == 0 && *abort_s == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      *abort_s = 1;
     }
     if (lane == 0)
       for (int s = 0; s < C::NS; ++s)
-        if (used > s) wait_ns(&k_full[s], ((used - 1 - s) / C::NS) & 1);
+        if (u > s) wait_ns(&k_full[s], ((u - 1 - s) / C::NS) & 1);
     __syncwarp();
   } else {
     // ============================================================ products
     const uint64_t dK = smem_desc(smem_u32(sK), 16, 8 * C::RB, C::SWZ), dQ = smem_desc(smem_u32(sQ), 16, 8 * C::RB, C::SWZ);
     bool ok = true;
-    for (int u = 0; u < n; ++u) {
-      if ((u & 7) == 7 && abort_warp(abort_s)) break;
-      const int st = u % C::NS, sb = u & 1;
-      if (at.begins()) ok = wait_warp(q_full, at.piece & 1);
-      if (ok) ok = wait_warp(&k_full[st], (u / C::NS) & 1);
-      if (ok && u >= 2) ok = wait_warp(&s_free[sb], ((u >> 1) - 1) & 1);
-      if (!ok) break;
-      tc_fence_after();
-      if (elect_one()) {
+    for (; ok && at.n > 0; at.next(p)) {
+      const int end = u + at.n;
+      ok = wait_warp(q_full, at.piece & 1);
+      for (; ok && u < end; ++u) {
+        if ((u & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+        const int st = u % C::NS, sb = u & 1;
+        ok = wait_warp(&k_full[st], (u / C::NS) & 1);
+        if (ok && u >= 2) ok = wait_warp(&s_free[sb], ((u >> 1) - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int hh = 0; hh < C::NHALF; ++hh)
+          for (int hh = 0; hh < C::NHALF; ++hh)
 #pragma unroll
-          for (int kk = 0; kk < D / 32; ++kk) {
-            const int byte = kk * 32;
-            umma_f8(tmem + (sb * C::NHALF + hh) * C::NP,
-                    desc_add(dK, st * C::KTILE + (byte / C::RB) * C::KSUB + hh * 128 * C::RB + byte % C::RB),
-                    desc_add(dQ, (byte / C::RB) * C::QSUB + byte % C::RB), C::IDESC, kk > 0 ? 1u : 0u);
-          }
-        umma_commit(&s_full[sb]);
-        umma_commit(&k_empty[st]);
+            for (int kk = 0; kk < D / 32; ++kk) {
+              const int byte = kk * 32;
+              umma_f8(tmem + (sb * C::NHALF + hh) * C::NP,
+                      desc_add(dK, st * C::KTILE + (byte / C::RB) * C::KSUB + hh * 128 * C::RB + byte % C::RB),
+                      desc_add(dQ, (byte / C::RB) * C::QSUB + byte % C::RB), C::IDESC, kk > 0 ? 1u : 0u);
+            }
+          umma_commit(&s_full[sb]);
+          umma_commit(&k_empty[st]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      at.advance(p);
     }
     if (!ok) {
-      if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
+      if (lane == 0 && *abort_s == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
     }
     if (elect_one()) umma_commit(mma_done);
