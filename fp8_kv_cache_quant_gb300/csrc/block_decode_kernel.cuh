@@ -49,7 +49,8 @@
 // products drain and returns (its pieces are then undefined, its units still counted).
 //
 // SHARED: the decode of what sequences do not share (block_shared.cu): keys from p.shared[b].x on, and a unit of a sequence
-// that shares is not merged here: its pieces, the first one's place and their number in p.units, are left for the join.
+// that shares is not merged here: its pieces, the first one's place and their number in p.units, are left for the join.  It starts
+// on the SMs that the kernel before it, the shared part's, leaves, without waiting for the others.
 #pragma once
 #include <type_traits>
 
@@ -426,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     tmem_relinquish();
     tc_fence_before();
   }
-  griddep_wait();
+  // SHARED: nothing that the kernel before this one writes is read here, and when it let this one start, the kernels before it were done.
+  if constexpr (!SHARED) griddep_wait();
   int N, w0, W;
   Place at = first_tile<TPB, SHARED>(p, k, N, w0, W, k == 0 && warp == 0);
   const int n = at.left;  // tiles of this CTA
@@ -1042,6 +1044,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     }
     __syncthreads();
   }
+  if constexpr (SHARED) griddep_wait();  // (what waits for this kernel waits for the one before it too)
 }
 
 }  // namespace

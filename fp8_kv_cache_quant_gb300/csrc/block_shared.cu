@@ -18,7 +18,7 @@ namespace {
 constexpr long long kLeastSaved = 1;
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
-constexpr int kGroupsHeld = 512;  // groups whose numbers the plan keeps in shared memory
+constexpr int kGroupsHeld = 512;  // groups that the plan keeps in shared memory
 
 FKV_DEV int context_of(const SharedParams& p, int b) { return min(max(p.ctx[b], 0), static_cast<int>(min(p.max_blocks * 16LL, static_cast<long long>(INT32_MAX)))); }
 
@@ -28,86 +28,87 @@ FKV_DEV long long warp_sum(long long x) {
   return x;
 }
 
+FKV_DEV int tiles_of(const SharedGroup& g) { return (g.keys + 127) / 128 - g.lo / 128; }
+FKV_DEV int items_of(const SharedParams& p, const SharedGroup& g) { return (g.members + p.tok - 1) / p.tok * p.Hkv; }  // (row tile, KV head)
+
+// One CTA; what bounds it are its round trips to L2 (the groups' borders, their first members' contexts, the contexts of all).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p) {
-  __shared__ long long sum_s[kPlanWarps];
-  __shared__ int items_s[kGroupsHeld], tiles_s[kGroupsHeld], most_s[kPlanWarps], cut_s[3], base_s;
+  __shared__ SharedGroup held_s[kGroupsHeld];
+  __shared__ long long sum_s[3][kPlanWarps];
+  __shared__ int most_s[kPlanWarps], cut_s[3], base_s;
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto block_sum = [&](long long x) {
-    x = warp_sum(x);
-    __syncthreads();
-    if (lane == 0) sum_s[warp] = x;
-    __syncthreads();
-    x = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w) x += sum_s[w];
-    return x;
-  };
-  bool bad = false;
-  for (int i = tid; i < p.num_groups; i += kPlanThreads) {
-    const int a = p.starts[i], e = p.starts[i + 1];
-    bad = bad || a < 0 || e < a || e > p.B;
-  }
-  bad = __syncthreads_or(bad);
-  if (bad && tid == 0) raise_fault(p.fault, FKV_FAULT_QLEN);
-  // the groups: members, shared keys (as many as the first member has), items (row tile, KV head), key tiles
+  auto group = [&](int i) { return i < kGroupsHeld ? held_s[i] : p.groups[i]; };
+  // the groups: members, shared keys (as many as the first member has); what they save, their items and steps (item, key tile)
   long long saved = 0, items = 0, steps = 0;
   int most = 0;
+  bool bad = false;
   for (int i = tid; i < p.num_groups; i += kPlanThreads) {
     SharedGroup g = {};
-    int n_items = 0, tiles = 0;
-    if (!bad) {
-      g.first = p.starts[i];
-      g.members = p.starts[i + 1] - g.first;
-      g.keys = p.lens[i];
+    const int e = p.starts[i + 1];
+    g.first = p.starts[i];
+    g.keys = p.lens[i];
+    if (g.first < 0 || e < g.first || e > p.B) {
+      bad = true;
+      g.first = g.keys = 0;
+    } else {
+      g.members = e - g.first;
       if (g.keys < 0 || g.keys > p.max_blocks * 16LL) {
         raise_fault(p.fault, FKV_FAULT_CONTEXT);
         g.keys = 0;
       }
       g.keys = g.members >= 2 ? min(g.keys, context_of(p, g.first)) : 0;
-      if (g.keys > 0) {
-        g.lo = p.window > 0 ? max(0, g.keys - p.window) : 0;
-        tiles = (g.keys + 127) / 128 - g.lo / 128;
-        n_items = (g.members + p.tok - 1) / p.tok * p.Hkv;
-        saved += static_cast<long long>(g.members - 1) * (g.keys - g.lo);
-        items += n_items;
-        steps += static_cast<long long>(n_items) * tiles;
-        most = max(most, tiles);
-      }
     }
-    p.groups[i] = g;
-    if (i < kGroupsHeld) {
-      items_s[i] = n_items;
-      tiles_s[i] = tiles;
+    if (g.keys > 0) {
+      g.lo = p.window > 0 ? max(0, g.keys - p.window) : 0;
+      const int tiles = tiles_of(g), n = items_of(p, g);
+      saved += static_cast<long long>(g.members - 1) * (g.keys - g.lo);
+      items += n;
+      steps += static_cast<long long>(n) * tiles;
+      most = max(most, tiles);
     }
+    (i < kGroupsHeld ? held_s[i] : p.groups[i]) = g;
   }
-  saved = block_sum(saved);
-  items = block_sum(items);
-  steps = block_sum(steps);
+  saved = warp_sum(saved);
+  items = warp_sum(items);
+  steps = warp_sum(steps);
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) most_s[warp] = most;
-  __syncthreads();
-  most = 0;
+  if (lane == 0) {
+    sum_s[0][warp] = saved;
+    sum_s[1][warp] = items;
+    sum_s[2][warp] = steps;
+    most_s[warp] = most;
+  }
+  if (tid == 0) base_s = 0;
+  bad = __syncthreads_or(bad);
+  if (bad && tid == 0) raise_fault(p.fault, FKV_FAULT_QLEN);
+  saved = items = steps = most = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanWarps; ++w) most = max(most, most_s[w]);
-  const bool share = saved * p.Hkv * 2 * p.D >= kLeastSaved;
-  // How many key tiles a piece has: the fewest whose pieces fit the SMs once (or twice, or three times: cut_s), by as many tries
-  // as a warp has lanes; a wave costs about three tiles besides its own.  More items than that are not cut.
+  for (int w = 0; w < kPlanWarps; ++w) {
+    saved += sum_s[0][w];
+    items += sum_s[1][w];
+    steps += sum_s[2][w];
+    most = max(most, most_s[w]);
+  }
+  const bool share = !bad && saved * p.Hkv * 2 * p.D >= kLeastSaved;
+  // How many key tiles a piece has: the fewest whose pieces fit the SMs once (or, where the grid has room for it, twice, or three
+  // times: cut_s), by as many tries as a warp has lanes; a wave costs about three tiles besides its own.  More items than that are
+  // not cut.
   if (share && warp < 3) {
     const long long room = static_cast<long long>(warp + 1) * p.num_sms;
     int c = 0;
-    if (items <= room && p.num_groups <= kGroupsHeld) {
+    if (items <= room && room <= p.most_pieces && p.num_groups <= kGroupsHeld) {
       const long long least = (steps + room - 1) / room;
       const int mine = static_cast<int>(least + least * lane / 12 + (least < 12 ? lane : 0));
       long long pieces = 0;
-      for (int i = 0; i < p.num_groups; ++i) pieces += items_s[i] == 0 ? 0 : static_cast<long long>(items_s[i]) * ((tiles_s[i] + mine - 1) / mine);
+      for (int i = 0; i < p.num_groups; ++i)
+        if (held_s[i].keys > 0) pieces += static_cast<long long>(items_of(p, held_s[i])) * ((tiles_of(held_s[i]) + mine - 1) / mine);
       const unsigned fits = __ballot_sync(0xffffffffu, pieces <= room);
       if (fits != 0) c = __shfl_sync(0xffffffffu, mine, __ffs(fits) - 1);
     }
     if (lane == 0) cut_s[warp] = c;
   }
-  if (tid == 0) base_s = 0;
   __syncthreads();
   int cut = max(most, 1);
   if (share) {
@@ -127,12 +128,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
     SharedGroup g = {};
     int pieces = 0;
     if (i < p.num_groups) {
-      g = p.groups[i];
+      g = group(i);
       if (!share) g.keys = 0;
       if (g.keys > 0) {
-        const int tiles = (g.keys + 127) / 128 - g.lo / 128;
-        g.shares = (tiles + cut - 1) / cut;
-        pieces = (g.members + p.tok - 1) / p.tok * p.Hkv * g.shares;
+        g.shares = (tiles_of(g) + cut - 1) / cut;
+        pieces = items_of(p, g) * g.shares;
       }
     }
     int upto = pieces;
@@ -146,7 +146,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
     int before = base_s;
     for (int w = 0; w < warp; ++w) before += most_s[w];
     g.base = before + upto - pieces;
-    if (i < p.num_groups) p.groups[i] = g;
+    if (i < p.num_groups) {
+      p.groups[i] = g;
+      if (i < kGroupsHeld) held_s[i] = g;
+    }
     __syncthreads();
     if (tid == kPlanThreads - 1) base_s = before + upto;
     __syncthreads();
@@ -154,16 +157,17 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
   if (tid == 0) *p.pieces = base_s;
   // the sequences: in which group, if it shares (a member shorter than the shared part does not)
   for (int b = tid; b < p.B; b += kPlanThreads) {
-    int lo = 0, hi = share && !bad ? p.num_groups : 0;  // groups before lo begin at or before b, those from hi on behind it
+    const int T = context_of(p, b);
+    int lo = 0, hi = share ? p.num_groups : 0;  // groups before lo begin at or before b, those from hi on behind it
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (p.starts[mid] <= b) lo = mid + 1;
+      if (group(mid).first <= b) lo = mid + 1;
       else hi = mid;
     }
     int4 out = make_int4(0, 0, 0, 0);
     if (lo > 0) {
-      const SharedGroup g = p.groups[lo - 1];
-      if (b < g.first + g.members && g.keys > 0 && context_of(p, b) >= g.keys) out = make_int4(g.keys, g.base, g.shares, b - g.first);
+      const SharedGroup g = group(lo - 1);
+      if (b < g.first + g.members && g.keys > 0 && T >= g.keys) out = make_int4(g.keys, g.base, g.shares, b - g.first);
     }
     p.info[b] = out;
   }
@@ -196,77 +200,94 @@ __global__ void __launch_bounds__(512, 1)
   attend_tile<D, WIN, kPieces>(p, tmk, tmv, g.first, g.members, g.keys, tile, at - item * g.shares, g.shares, piece);
 }
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 512;
 
-// CTA per (sequence, unit of the decode): a thread takes four columns of a head at a time, heads next to one another (as they lie
-// in the prefix's pieces).
+// CTA per (sequence, unit of the decode): a thread takes four columns of a head, heads next to one another (as they lie in the prefix's
+// pieces), and every PARTS-th piece, eight of them on their way at a time; the threads' maxima, sums and columns are put together in
+// shared memory.  What bounds it are its round trips to L2 (the sequence's numbers, its pieces, once or twice).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const SharedParams p, int units, int G) {
-  __shared__ float top_s[16], inv_s[16];
+  constexpr int U = 8;
+  __shared__ float top_s[kJoinThreads], sum_s[kJoinThreads];
+  __shared__ float4 o_s[kJoinThreads];
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x / units, u = blockIdx.x - b * units;
   const int4 info = p.info[b];
   if (info.x == 0) return;
-  const int T = context_of(p, b);
-  int2 own = make_int2(0, 0);
-  if (T > info.x) own = p.units[blockIdx.x];
+  int2 own = p.units[blockIdx.x];
+  if (context_of(p, b) <= info.x) own = make_int2(0, 0);  // (not written)
   const float* own_lse = p.lse_part + (static_cast<long long>(own.x) + blockIdx.x) * G;
   const float4* own_o = reinterpret_cast<const float4*>(p.o_part + (static_cast<long long>(own.x) + blockIdx.x) * G * D);
+  const int quads = G * D / 4, parts = kJoinThreads / quads;  // (quads: a power of two from 16 to 512)
+  const int part = threadIdx.x / quads, q = threadIdx.x - part * quads, d4 = q / G, h = q - d4 * G;
   // head h of the unit among the rows of the prefix's pieces: the first one's CTA, and the row
-  const int group = p.Hq / p.Hkv, tile = info.w / p.tok, row0 = (info.w - tile * p.tok) * group;
-  auto place = [&](int h, int& row) {
-    const int head = u * G + h, g = head / group;
-    row = row0 + head - g * group;
-    return info.y + (tile * p.Hkv + g) * info.z;
-  };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = info.z + own.y;
-  for (int h = warp; h < G; h += kJoinThreads / 32) {
-    int row;
-    const int k0 = place(h, row);
-    auto lse = [&](int i) { return i < info.z ? p.piece_lse[static_cast<size_t>(k0 + i) * 128 + row] : own_lse[static_cast<size_t>(i - info.z) * G + h]; };
-    float top = -kHuge;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, lse(i));
+  const int group = p.Hq / p.Hkv, tile = info.w / p.tok, head = u * G + h, g = head / group;
+  const int row = (info.w - tile * p.tok) * group + head - g * group, k0 = info.y + (tile * p.Hkv + g) * info.z;
+  float top = -kHuge, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = part; i0 < info.z + own.y; i0 += U * parts) {
+    float lse[U];
+    float4 x[U];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float sum = 0.f;
-    for (int i = lane; i < n; i += 32) sum += ex2(lse(i) - top);
+    for (int v = 0; v < U; ++v) {
+      const int i = i0 + v * parts, j = i - info.z;
+      lse[v] = -INFINITY;
+      x[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (j < 0) {
+        lse[v] = p.piece_lse[static_cast<size_t>(k0 + i) * 128 + row];
+        x[v] = p.piece_o[(static_cast<size_t>(k0 + i) * (D / 4) + d4) * 128 + row];
+      } else if (j < own.y) {
+        lse[v] = own_lse[static_cast<size_t>(j) * G + h];
+        x[v] = own_o[(static_cast<size_t>(j) * G + h) * (D / 4) + d4];
+      }
+    }
+    float m = top;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    if (lane == 0) {
-      top_s[h] = top;
-      inv_s[h] = 1.f / sum;
+    for (int v = 0; v < U; ++v) m = fmaxf(m, lse[v]);
+    const float a = ex2(top - m);  // (of -kHuge: 1 or 0)
+    top = m;
+    sum *= a;
+    o.x *= a, o.y *= a, o.z *= a, o.w *= a;
+#pragma unroll
+    for (int v = 0; v < U; ++v) {
+      const float w = ex2(lse[v] - m);  // (a piece of NaN has lse +infinity: NaN)
+      sum += w;
+      o.x = fmaf(w, x[v].x, o.x);
+      o.y = fmaf(w, x[v].y, o.y);
+      o.z = fmaf(w, x[v].z, o.z);
+      o.w = fmaf(w, x[v].w, o.w);
     }
   }
+  top_s[threadIdx.x] = top;
+  sum_s[threadIdx.x] = sum;
+  o_s[threadIdx.x] = o;
   __syncthreads();
-  for (int q = threadIdx.x; q < G * D / 4; q += kJoinThreads) {
-    const int d4 = q / G, h = q - d4 * G;
-    int row;
-    const int k0 = place(h, row);
-    const float top = top_s[h];
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](float w, float4 x) {
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
-    };
-#pragma unroll 4
-    for (int i = 0; i < info.z; ++i)
-      add(ex2(p.piece_lse[static_cast<size_t>(k0 + i) * 128 + row] - top), p.piece_o[(static_cast<size_t>(k0 + i) * (D / 4) + d4) * 128 + row]);
-#pragma unroll 4
-    for (int i = 0; i < own.y; ++i) add(ex2(own_lse[static_cast<size_t>(i) * G + h] - top), own_o[(static_cast<size_t>(i) * G + h) * (D / 4) + d4]);
-    const float inv = inv_s[h];
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + (static_cast<size_t>(b) * p.Hq + u * G + h) * D + 4 * d4);
-    dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  if (part > 0) return;
+  for (int i = 1; i < parts; ++i) top = fmaxf(top, top_s[i * quads + q]);
+  sum = 0.f;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < parts; ++i) {
+    const int at = i * quads + q;
+    const float w = ex2(top_s[at] - top);
+    sum = fmaf(w, sum_s[at], sum);
+    o.x = fmaf(w, o_s[at].x, o.x);
+    o.y = fmaf(w, o_s[at].y, o.y);
+    o.z = fmaf(w, o_s[at].z, o.z);
+    o.w = fmaf(w, o_s[at].w, o.w);
   }
+  const float inv = 1.f / sum;
+  __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(p.out + (static_cast<size_t>(b) * p.Hq + head) * D + 4 * d4);
+  dst[0] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  dst[1] = __floats2bfloat162_rn(o.z * inv, o.w * inv);
 }
 
-// CTAs of the prefix kernel, at most: three for every SM, or one for every item (groups of two and more).
+// CTAs of the prefix kernel.  Items (groups of two and more have them), at most; where an SM can have two each, the SMs, and otherwise
+// three for every SM or one for every item.
 long long prefix_ctas(int B, int Hq, int Hkv, int num_groups, int num_sms) {
   const int tok = 128 / (Hq / Hkv);
-  return std::max<long long>(3LL * num_sms, static_cast<long long>(Hkv) * (B / tok + std::min(num_groups, B / 2)));
+  const long long items = static_cast<long long>(Hkv) * (B / tok + std::min(num_groups, B / 2));
+  return 2 * items <= num_sms ? num_sms : std::max<long long>(3LL * num_sms, items);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -364,6 +385,9 @@ size_t block_shared_workspace(int B, int Hq, int Hkv, int D, int num_groups, int
 
 cudaError_t launch_block_shared(BlockDecodeParams dp, int D, int ctas, const int32_t* starts, const int32_t* lens, int num_groups, void* workspace,
                                 int num_sms, cudaStream_t s) {
+  // (keys that a group can save, whatever the groups are)
+  const long long keys = std::min(dp.max_blocks * 16LL, dp.window > 0 ? static_cast<long long>(dp.window) : INT64_MAX);
+  if ((dp.B - 1) * keys * (dp.Hkv >> dp.halves) * 2 * D < kLeastSaved) return launch_block_decode(dp, D, ctas, s);
   SharedParams sp = {};
   sp.B = dp.B;
   sp.Hq = dp.Hq;
@@ -383,6 +407,7 @@ cudaError_t launch_block_shared(BlockDecodeParams dp, int D, int ctas, const int
   sp.o_part = dp.o_part;
   const long long prefix = prefix_ctas(dp.B, sp.Hq, sp.Hkv, num_groups, num_sms);
   if (prefix > INT32_MAX) return cudaErrorInvalidValue;
+  sp.most_pieces = static_cast<int>(prefix);
   lay_out(&sp, static_cast<uint8_t*>(workspace), dp.B, sp.Hq, sp.Hkv, D, num_groups, prefix);
   dp.shared = sp.info;
   dp.units = sp.units;

@@ -14,6 +14,7 @@ struct SharedGroup {
 struct SharedParams {
   int B, Hq, Hkv, D, max_blocks, window, num_groups, num_sms;
   int tok;                                    // members of a row tile
+  int most_pieces;
   const int32_t* ctx;                         // [B]
   const int32_t* starts;                      // [num_groups + 1]
   const int32_t* lens;                        // [num_groups]
