@@ -113,6 +113,7 @@ constexpr int kThreads = 320;
 // Keys of sequence b: [lo, T), blocks [blk0, blk_end), n tiles of TPB blocks from blk0.
 struct Seq {
   int T, lo, n;
+  bool shares;  // SHARED: the sequence's keys before lo are another kernel's
 };
 
 template <int TPB, bool SHARED>
@@ -124,7 +125,12 @@ FKV_DEV Seq seq_of(const BlockDecodeParams& p, int b, bool report) {
     s.T = s.T < 0 ? 0 : p.max_blocks * 16;
   }
   s.lo = p.window > 0 ? max(0, s.T - p.window) : 0;
-  if constexpr (SHARED) s.lo = min(max(s.lo, p.shared[b].x), s.T);
+  s.shares = false;
+  if constexpr (SHARED) {
+    const int keys = p.shared[b].x;
+    s.shares = keys > 0;
+    s.lo = min(max(s.lo, keys), s.T);
+  }
   s.n = (((s.T + 15) >> 4) - (s.lo >> 4) + TPB - 1) / TPB;
   if constexpr (SHARED) s.n = s.lo < s.T ? s.n : 0;
   return s;
@@ -160,7 +166,7 @@ template <int TPB, bool SHARED>
 FKV_DEV Cursor<TPB, SHARED> first_tile(const BlockDecodeParams& p, int k, int& N, int& w0, int& W, bool report) {
   const int lane = threadIdx.x & 31;
   auto places = [](int n) { return n > 0 ? n + 1 : 0; };
-  auto seq = [&](int b0, bool rep) { return b0 + lane < p.B ? seq_of<TPB, SHARED>(p, b0 + lane, rep) : Seq{0, 0, 0}; };
+  auto seq = [&](int b0, bool rep) { return b0 + lane < p.B ? seq_of<TPB, SHARED>(p, b0 + lane, rep) : Seq{0, 0, 0, false}; };
   const Seq s0 = seq(0, report);
   int total = __reduce_add_sync(0xffffffffu, places(s0.n));
   for (int b0 = 32; b0 < p.B; b0 += 32) total += __reduce_add_sync(0xffffffffu, places(seq(b0, report).n));
@@ -168,7 +174,7 @@ FKV_DEV Cursor<TPB, SHARED> first_tile(const BlockDecodeParams& p, int k, int& N
   N = min(static_cast<int>(gridDim.x), W);
   Cursor<TPB, SHARED> c;
   c.left = c.b = c.g = c.t = c.piece = 0;
-  c.s = Seq{0, 0, 0};
+  c.s = Seq{0, 0, 0, false};
   w0 = 0;
   if (k >= N) return c;
   const int each = W / N, rest = W - each * N;  // floor(k W / N) = k each + floor(k rest / N)
@@ -190,6 +196,7 @@ FKV_DEV Cursor<TPB, SHARED> first_tile(const BlockDecodeParams& p, int k, int& N
       c.s.T = __shfl_sync(0xffffffffu, s.T, j);
       c.s.lo = __shfl_sync(0xffffffffu, s.lo, j);
       c.s.n = __shfl_sync(0xffffffffu, s.n, j);
+      c.s.shares = SHARED && __shfl_sync(0xffffffffu, s.shares, j);
       const int rem = w0 - base - __shfl_sync(0xffffffffu, before - places(s.n), j) * p.Hkv;
       c.g = rem / (c.s.n + 1);
       c.t = rem - c.g * (c.s.n + 1) - 1;
@@ -494,10 +501,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   // sequences without keys: zero rows, spread over the CTAs
   if (warp >= 4 && warp < 8)
     for (int b = k; b < p.B; b += gridDim.x) {
-      if (seq_of<TPB, SHARED>(p, b, false).n != 0) continue;
-      if constexpr (SHARED) {
-        if (p.shared[b].x > 0) continue;  // (the join writes it)
-      }
+      const Seq s = seq_of<TPB, SHARED>(p, b, false);
+      if (s.n != 0 || s.shares) continue;  // (what is shared, the join writes)
       for (int x = threadIdx.x - 128; x < p.Hq * D / 8; x += 128)
         reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.Hq * D)[x] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -793,11 +798,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         const int unit = at.b * p.Hkv + at.g;
         const int u0 = w - at.t;  // the place of the unit's first tile
         const int k0 = cta_of(u0, W, N), ns = cta_of(u0 + at.s.n - 1, W, N) - k0 + 1;
-        bool shares = false;
-        if constexpr (SHARED) {
-          shares = p.shared[at.b].x > 0;
-          if (shares && i == 0 && k == k0) p.units[unit] = make_int2(k0, ns);
-        }
+        const bool shares = SHARED && at.s.shares;
+        if (shares && i == 0 && k == k0) p.units[unit] = make_int2(k0, ns);
         if (ok) ok = wait_warp(&l_full[r & 1], (r >> 1) & 1);
         if (ok) {
           const long long row = static_cast<long long>(k) + unit;
@@ -849,24 +851,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   } else if (warp == 8) {
     // ============================================================ K copies and scales
     // K(u) into stage u % NS once the S^T of tile u - NS has read it, the first NS with their V at
-    // once; the scales of tile u into their slot.
-    int id = 0;
-    {
-      Place c = at;
-#pragma unroll
-      for (int j = 0; j < C::NS; ++j) {
-        if (j >= n0) break;
-        const int x = checked(ids[j]);
-        if (j == 0) id = x;
-        copy_tile(&tmk, sK + j * C::KTILE, c, x, &k_full[j]);
-        if (lane > 0 && lane < 4) mbar_arrive(&v_full[j]);  // (a phase has four arrivals)
-        copy_tile(&tmv, sV + j * C::KTILE, c, x, &v_full[j]);
-        c.advance(p);
-      }
-    }
-    Place nx = at;
-    nx.advance(p);
-    int id_next = block_id(nx);
+    // once; the scales of tile u into their slot.  (A warp's copies go out one after another, 100 cycles each: the first tile's scales
+    // come before the copies of the tiles behind it.)
     float ks_n = 0.f, vs_n = 0.f;
     auto read_scales = [&](const Place& c, int j) {
       ks_n = vs_n = 0.f;
@@ -876,9 +862,19 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         vs_n = p.v_scale[x];
       }
     };
+    auto copy_first = [&](const Place& c, int x, int st) {  // K and V
+      copy_tile(&tmk, sK + st * C::KTILE, c, x, &k_full[st]);
+      if (lane > 0 && lane < 4) mbar_arrive(&v_full[st]);  // (a phase has four arrivals)
+      copy_tile(&tmv, sV + st * C::KTILE, c, x, &v_full[st]);
+    };
+    int id = checked(ids[0]);
     read_scales(at, id);
+    copy_first(at, id, 0);
+    int used = 1;  // tiles whose K copy was issued
+    Place nx = at;
+    nx.advance(p);
+    int id_next = ids[1];
     ScaleRange range;
-    int used = 0;  // tiles whose K copy was issued
     for (int u = 0; u < n; ++u) {
       if (abort_warp(abort_s)) break;
       const float ks = ks_n, vs = vs_n;
@@ -897,8 +893,8 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
           break;
         }
         copy_tile(&tmk, sK + st * C::KTILE, here, id_u, &k_full[st]);
+        used = u + 1;
       }
-      used = u + 1;
       if (here.t == 0) range = ScaleRange();  // another piece
       const BlockScale sc = block_scales(range, vs, lane < here.blocks());
       float* slot = sc_s + (u % C::SCN) * C::SCF;
@@ -913,13 +909,22 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         slot[3 * TPB + 2] = sc.change;
       }
       mbar_arrive_warp(&sc_full[u % C::SCN]);
+      if (u == 0) {
+        Place c = at;
+#pragma unroll
+        for (int j = 1; j < C::NS; ++j) {
+          if (j >= n0) break;
+          copy_first(c, j == 1 ? id : checked(ids[j]), j);
+          if (j + 1 < C::NS) c.advance(p);
+        }
+        used = n0;
+      }
     }
     // let every copy issued here land before the CTA can exit
     if (lane == 0) {
-      used = max(used, n0);
       for (int s = 0; s < C::NS; ++s)
         if (used > s) wait_ns(&k_full[s], ((used - 1 - s) / C::NS) & 1);
-      for (int s = 0; s < n0; ++s)
+      for (int s = 0; s < min(used, n0); ++s)
         if (*abort_s) wait_ns(&v_full[s], 0);
     }
     __syncwarp();

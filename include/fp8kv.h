@@ -601,7 +601,8 @@ size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_
  *                 before its first call; otherwise as for fp8_block_decode_attn
  *   all others    as for fp8_block_decode_attn
  * Group starts that decrease or leave [0, batch] raise FKV_FAULT_QLEN, a shared length outside [0, 16 max_blocks]
- * FKV_FAULT_CONTEXT: the group then shares nothing (the starts of any: no group does).
+ * FKV_FAULT_CONTEXT: the group then shares nothing (the starts of any: no group does).  Where batch, max_blocks and
+ * window alone say that no groups can pay for sharing, the call is fp8_block_decode_attn and does not look at them.
  */
 fkv_status fp8_block_shared_decode_attn(const void* q, int32_t batch, int32_t num_q_heads, fkv_block_cache cache,
                                         const int32_t* block_table, int32_t max_blocks,

@@ -3,7 +3,10 @@
 Tolerance of an output element, derived as for the attention over block-scaled pools: with p_j the softmax weights,
 P = sum_j p_j |v_j| and V the largest |v_j| of the sequence, P enters the products within 2^-8 (2^-8 P), scores are FP32 sums of
 exact products (2^-10 P), weights 2^-17 and more below a tile's largest may be off by a fixed step (2^-10 V), the output
-is rounded to bf16 (2^-8 |o|).  The join of the pieces is FP32.  The relative L2 distance is held to 2^-7."""
+is rounded to bf16 (2^-8 |o|).  The join of the pieces is FP32.  The relative L2 distance is held to 2^-7.
+
+Sharing begins where it saves 64 to 112 MB of keys and values (by head_dim): a case's first group has as many members more, each with a
+few tokens of its own, as take it beyond that (`fill`), unless the case is about calls that are too small for it."""
 import numpy as np
 import pytest
 import torch
@@ -23,8 +26,15 @@ class Case:
     """Groups of sequences behind shared tokens.  groups: (shared tokens, [own tokens of each member]); a negative number
     of own tokens is a member shorter than the shared part.  `alone` sequences behind the last group share nothing."""
 
-    def __init__(self, groups, hq, h, d, seed=0, alone=(), spread=3, q_size=1.0, wide=0):
+    def __init__(self, groups, hq, h, d, seed=0, alone=(), spread=3, q_size=1.0, wide=0, fill=True, window=0):
         rng = np.random.default_rng(seed)
+        if fill:
+            # members beyond what the rule asks for, 4 MB a key tile counted for pieces of up to five
+            seen = [min(p, window or p) for p, _ in groups]
+            least = (48 + d // 4 + 5 * min(d, 128) // 16) << 20
+            have = sum((len(m) - 1) * n for n, (_, m) in zip(seen, groups)) * h * 2 * d
+            more = max(0, -(-(least - have) // (seen[0] * h * 2 * d)))
+            groups = [(groups[0][0], list(groups[0][1]) + [1 + i % 37 for i in range(more)])] + list(groups[1:])
         self.ctx, self.starts, self.shared, rows, nb = [], [0], [], [], 0
 
         def blocks(n):
@@ -82,19 +92,47 @@ class Case:
         return f.fp8_block_shared_decode_attn(self.q.cuda(), self.cache(), _i32(self.table), _i32(self.ctx), _i32(self.starts),
                                               _i32(self.shared), fault=self.fault, **kw)
 
+    def exact(self, softmax_scale=0.0, window=0, device="cuda"):
+        """(softmax(q K^T) V, softmax(q K^T) |V|, the largest |V|) of every sequence by itself in float64, the shared tokens of a
+        group from the blocks that its first sequence names."""
+        batch, hq, d = self.q.shape
+        h = self.pools[0].shape[1]
+        scale = softmax_scale or d ** -0.5
+        pool = [torch.from_numpy(p).to(device).view(torch.float8_e4m3fn) for p in self.pools]
+        step = [torch.from_numpy(s).to(device).double() for s in self.scales]
+        o, mag, top = (torch.zeros(batch, hq, n, dtype=torch.float64, device=device) for n in (d, d, 1))
+        for b, t in enumerate(self.ctx):
+            if t == 0:
+                continue
+            lo = max(0, t - window) if window else 0
+            spans = [(b, lo, t)]
+            for i, n in enumerate(self.shared):
+                n = min(n, self.ctx[self.starts[i]]) if self.starts[i] < self.starts[i + 1] else 0
+                if self.starts[i] <= b < self.starts[i + 1] and t >= n > lo:
+                    spans = [(self.starts[i], lo, n), (b, n, t)]
+
+            def tokens(p, s):
+                x = []
+                for row, a, e in spans:
+                    ids = torch.from_numpy(self.table[row, a // 16:(e + 15) // 16].astype(np.int64)).to(device)
+                    y = p.view(torch.uint8)[ids].view(torch.float8_e4m3fn).double() * s[ids][:, :, None, None]
+                    x.append(y.transpose(1, 2).reshape(-1, h, d)[a % 16:e - a // 16 * 16])
+                return torch.cat(x)
+            k, v = (tokens(p, s) for p, s in zip(pool, step))
+            q = self.q[b].to(device).double().view(h, hq // h, d)
+            w = torch.softmax(torch.einsum("hgd,thd->hgt", q, k) * scale, -1)
+            for dst, x in ((o, v), (mag, v.abs())):
+                dst[b] = torch.einsum("hgt,thd->hgd", w, x).reshape(hq, d)
+            top[b] = v.abs().amax()
+        return (x.cpu().numpy() for x in (o, mag, top))
+
     def check(self, got=None, **kw):
         if got is None:
             got = self.run(**kw)
             assert int(self.fault) == 0
         kw.pop("workspace", None)
-        a = (self.pools[0], self.pools[1], self.scales[0], self.scales[1], self.table, self.ctx, None)
-        q = self.q.float().numpy().astype(np.float64)
-        o, mag = blockcache.attend(q, *a, **kw), blockcache.p_bound(q, *a, **kw)
-        top = np.zeros(len(self.ctx))
-        for b, t in enumerate(self.ctx):
-            if t:
-                top[b] = max(np.abs(blockcache.sequence(self.pools[1], self.scales[1], self.table[b], t, g)).max() for g in range(self.pools[1].shape[1]))
-        tol = (2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -10 * top[:, None, None] + 2.0 ** -8 * np.abs(o)
+        o, mag, top = self.exact(**kw)
+        tol = (2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -10 * top + 2.0 ** -8 * np.abs(o)
         got = got.float().cpu().numpy().astype(np.float64)
         assert np.all(np.isfinite(got))
         err = np.abs(got - o)
@@ -103,7 +141,16 @@ class Case:
         assert rel_l2(got, o) <= 2.0 ** -7
 
 
-# 4 MB of shared keys and values saved is far above any rule's border here; the smallest cases are attended unshared
+def test_the_oracle_here_is_the_other_tests_one():
+    c = Case([(500, [1, 30, 3]), (33, [4, 5])], 8, 2, 64, alone=(0, 70), fill=False)
+    a = (c.pools[0], c.pools[1], c.scales[0], c.scales[1], c.table, c.ctx, None)
+    q = c.q.float().numpy().astype(np.float64)
+    for kw in ({}, {"window": 100}, {"softmax_scale": 0.3}):
+        o, mag, _ = c.exact(**kw)
+        np.testing.assert_allclose(o, blockcache.attend(q, *a, **kw), rtol=1e-9, atol=1e-12)
+        np.testing.assert_allclose(mag, blockcache.p_bound(q, *a, **kw), rtol=1e-9, atol=1e-12)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("g", [1, 2, 4, 8, 16])
 def test_one_group(d, g):
@@ -125,14 +172,36 @@ def test_groups(d, groups, alone, hq, h):
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("window", [1, 50, 700, 6000])
 def test_windows(d, window):
-    Case([(6003, [1, 0, 60, 900, 5, 5]), (4000, [10, 2000, -30])], 8, 2, d, seed=window).check(window=window)
+    # (a window of 1 or 50 saves too little to be worth sharing)
+    Case([(6003, [1, 0, 60, 900, 5, 5]), (4000, [10, 2000, -30])], 16, 8, d, seed=window, fill=window > 50, window=window).check(window=window)
 
 
-def test_small_calls_and_many_groups():
-    Case([(1, [0, 0])], 2, 2, 64, seed=1).check()
-    Case([(33, [1, 2, 3, 4])], 8, 2, 128, seed=2).check()
-    Case([(320, [int(x) for x in range(1, 5)]) for _ in range(90)], 8, 4, 128, seed=3).check()
-    Case([(640, [1] * 2) for _ in range(80)], 32, 8, 64, seed=4).check()
+@pytest.mark.parametrize("groups,hq,h,d", [
+    ([(1, [0, 0])], 2, 2, 64), ([(33, [1, 2, 3, 4])], 8, 2, 128), ([(2048, [1, 50, 100, 150])], 32, 8, 128),
+    ([(2048, [5, 6]), (700, [1, 1, 1]), (0, [16]), (30, [0, 0])], 16, 8, 64),
+])
+def test_calls_too_small_to_share(groups, hq, h, d):
+    c = Case(groups, hq, h, d, seed=len(groups), fill=False)
+    c.check()
+    assert torch.equal(c.run(), f.fp8_block_decode_attn(c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx)))
+
+
+@pytest.mark.parametrize("groups,hq,h,d", [
+    # a wide table and a batch large enough that only the lengths, on the GPU, tell that sharing does not pay
+    ([(160, [1, 2, 3]), (40, [5, 6])], 16, 8, 64), ([(0, [400, 900, 16]), (700, [0, 1])], 8, 8, 128),
+])
+def test_lengths_too_short_to_share(groups, hq, h, d):
+    c = Case(groups, hq, h, d, seed=2, fill=False, wide=2048)
+    c.check()
+    assert torch.equal(c.run(), f.fp8_block_decode_attn(c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx)))
+
+
+@pytest.mark.parametrize("groups,hq,h,d", [
+    ([(320, [int(x) for x in range(1, 5)]) for _ in range(110)], 8, 4, 128), ([(1280, [1] * 2) for _ in range(80)], 32, 8, 64),
+    ([(96, [0, 1, 2]) for _ in range(600)], 8, 8, 64),
+])
+def test_many_groups(groups, hq, h, d):
+    Case(groups, hq, h, d, seed=3).check()
 
 
 def test_one_long_prefix_of_one_head():
@@ -153,7 +222,7 @@ def test_all_shared_and_scale():
 
 
 def test_no_groups():
-    c = Case([], 8, 2, 128, seed=9, alone=(100, 700, 0, 33))
+    c = Case([], 8, 2, 128, seed=9, alone=(100, 700, 0, 33), fill=False)
     c.check()
     want = f.fp8_block_decode_attn(c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx))
     assert torch.equal(c.run(), want)
@@ -166,26 +235,27 @@ def test_bad_queries_keep_to_their_rows():
     c.q[2, 0, 1] = float("inf")
     got = c.run()
     assert bool(got[1, 5].isnan().all()) and bool(got[2, 0].isnan().all())
-    bad = torch.zeros(4, 8, dtype=torch.bool)
+    bad = torch.zeros(len(c.ctx), 8, dtype=torch.bool)
     bad[1, 5] = bad[2, 0] = True
     assert torch.equal(got[~bad], want[~bad])
 
 
 def test_bad_groups_share_nothing_and_are_reported():
     c = Case([(4000, [40, 3, 9]), (3000, [5, 6])], 8, 2, 128, seed=11)
-    for starts, shared, fault in (([0, 3, 2], [4000, 3000], f.FAULT_QLEN), ([-1, 3, 5], [4000, 3000], f.FAULT_QLEN), ([0, 3, 6], [4000, 3000], f.FAULT_QLEN),
-                                  ([0, 3, 5], [-1, 3000], f.FAULT_CONTEXT), ([0, 3, 5], [4000, 16 * c.table.shape[1] + 1], f.FAULT_CONTEXT)):
-        keep = c.starts, c.shared
+    n = c.starts[1]
+    plain = f.fp8_block_decode_attn(c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx))
+    assert not torch.equal(c.run(), plain), "the unspoiled call shares"
+    for starts, shared, fault in (([0, n, n - 1], [4000, 3000], f.FAULT_QLEN), ([-1, n, n + 2], [4000, 3000], f.FAULT_QLEN),
+                                  ([0, n, n + 3], [4000, 3000], f.FAULT_QLEN), ([0, n, n + 2], [-1, 3000], f.FAULT_CONTEXT),
+                                  ([0, n, n + 2], [16 * c.table.shape[1] + 1, 3000], f.FAULT_CONTEXT)):
         c.starts, c.shared = starts, shared
-        got = c.run()
+        assert torch.equal(c.run(), plain)
         assert int(c.fault) == fault
-        c.starts, c.shared = keep
-        c.check(got)
 
 
 def test_bad_blocks_are_reported():
     c = Case([(5000, [40, 3, 9])], 8, 2, 128, seed=12)
-    c.table[0, 7] = c.table[1, 7] = c.table[2, 7] = 1 << 29
+    c.table[:, 7] = 1 << 29
     c.pools[0][0], c.pools[1][0] = 0x10, 0x10
     c.run()
     assert int(c.fault) == f.FAULT_BLOCK_ID
@@ -193,7 +263,7 @@ def test_bad_blocks_are_reported():
 
 def test_one_workspace_for_calls_that_grow_and_shrink():
     big, small = Case([(5000, [40] * 40)], 8, 2, 128, seed=13), Case([(4000, [3, 9]), (6000, [1, 1, 1])], 8, 2, 128, seed=14, alone=(50,))
-    ws = f.block_shared_workspace(40, 8, big.cache(), 2)
+    ws = f.block_shared_workspace(max(len(big.ctx), len(small.ctx)), 8, big.cache(), 2)
     for c in (big, small, big, small, small):
         c.check(workspace=ws)
     one = big.run(workspace=ws)
@@ -207,7 +277,8 @@ def test_one_workspace_for_calls_that_grow_and_shrink():
 def test_captured_and_replayed_with_other_groups_and_lengths():
     c = Case([(5000, [40, 300, 9, 1]), (3000, [5, 6])], 8, 2, 128, seed=15)
     cache, q, tab, ctx, starts, shared = c.cache(), c.q.cuda(), _i32(c.table), _i32(c.ctx), _i32(c.starts), _i32(c.shared)
-    ws, out = f.block_shared_workspace(6, 8, cache, 2), torch.empty_like(q)
+    n = c.starts[1]
+    ws, out = f.block_shared_workspace(n + 2, 8, cache, 2), torch.empty_like(q)
     f.fp8_block_shared_decode_attn(q, cache, tab, ctx, starts, shared, out=out, workspace=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
@@ -215,7 +286,7 @@ def test_captured_and_replayed_with_other_groups_and_lengths():
         f.fp8_block_shared_decode_attn(q, cache, tab, ctx, starts, shared, out=out, workspace=ws)
     g.replay()
     c.check(out)
-    c.starts, c.shared, c.ctx = [0, 3, 3], [4990, 0], [5011, 5300, 5001, 5000, 3001, 2]
+    c.starts, c.shared, c.ctx = [0, n - 1, n - 1], [4990, 0], [5011, 5300, 5001, 5000] + c.ctx[4:n] + [3001, 2]
     starts.copy_(_i32(c.starts)), shared.copy_(_i32(c.shared)), ctx.copy_(_i32(c.ctx))
     out.zero_()
     g.replay()
