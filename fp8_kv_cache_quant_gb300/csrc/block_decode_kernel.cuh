@@ -851,8 +851,9 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
   } else if (warp == 8) {
     // ============================================================ K copies and scales
     // K(u) into stage u % NS once the S^T of tile u - NS has read it, the first NS with their V at
-    // once; the scales of tile u into their slot.  (A warp's copies go out one after another, 100 cycles each: the first tile's scales
-    // come before the copies of the tiles behind it.)
+    // once; the scales of tile u into their slot.  (A warp's copies go out one after another, 100 cycles each.  SHARED, short ranges
+    // mostly: the first tile's scales come before the copies of the tiles behind it, the first P after 8,270 cycles instead of 13,580;
+    // longer ranges gain nothing.)
     float ks_n = 0.f, vs_n = 0.f;
     auto read_scales = [&](const Place& c, int j) {
       ks_n = vs_n = 0.f;
@@ -873,6 +874,16 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     int used = 1;  // tiles whose K copy was issued
     Place nx = at;
     nx.advance(p);
+    auto copy_next_ones = [&](Place c) {
+#pragma unroll
+      for (int j = 1; j < C::NS; ++j) {
+        if (j >= n0) break;
+        copy_first(c, checked(ids[j]), j);
+        if (j + 1 < C::NS) c.advance(p);
+      }
+      used = n0;
+    };
+    if constexpr (!SHARED) copy_next_ones(nx);
     int id_next = ids[1];
     ScaleRange range;
     for (int u = 0; u < n; ++u) {
@@ -909,16 +920,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
         slot[3 * TPB + 2] = sc.change;
       }
       mbar_arrive_warp(&sc_full[u % C::SCN]);
-      if (u == 0) {
-        Place c = at;
-#pragma unroll
-        for (int j = 1; j < C::NS; ++j) {
-          if (j >= n0) break;
-          copy_first(c, j == 1 ? id : checked(ids[j]), j);
-          if (j + 1 < C::NS) c.advance(p);
-        }
-        used = n0;
-      }
+      if (SHARED && u == 0) copy_next_ones(at);
     }
     // let every copy issued here land before the CTA can exit
     if (lane == 0) {
