@@ -595,7 +595,8 @@ size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_
  * call in which sharing would not pay for itself (few bytes saved): over their own rows of block_table.
  *
  *   group_starts  device int32 [num_groups + 1], non-decreasing, within [0, batch]
- *   shared_lens   device int32 [num_groups]; need not be multiples of 16
+ *   shared_lens   device int32 [num_groups]; need not be multiples of 16 (but an append requantises the block that it
+ *                 goes on in: behind appends to copies of a half-full block, only the blocks before it are in common)
  *   num_groups    >= 0 (0: nothing is shared)
  *   workspace     device, >= fp8_block_shared_decode_attn_workspace_size(...) bytes, 256-byte aligned, zero-filled
  *                 before its first call; otherwise as for fp8_block_decode_attn

@@ -26,12 +26,12 @@ class Case:
     """Groups of sequences behind shared tokens.  groups: (shared tokens, [own tokens of each member]); a negative number
     of own tokens is a member shorter than the shared part.  `alone` sequences behind the last group share nothing."""
 
-    def __init__(self, groups, hq, h, d, seed=0, alone=(), spread=3, q_size=1.0, wide=0, fill=True, window=0):
+    def __init__(self, groups, hq, h, d, seed=0, alone=(), spread=3, q_size=1.0, wide=0, fill=True, window=0, tiles=5):
         rng = np.random.default_rng(seed)
         if fill:
-            # members beyond what the rule asks for, 4 MB a key tile counted for pieces of up to five
+            # members beyond what the rule asks for with pieces of up to `tiles` key tiles
             seen = [min(p, window or p) for p, _ in groups]
-            least = (48 + d // 4 + 5 * min(d, 128) // 16) << 20
+            least = (48 + d // 4 + tiles * min(d, 128) // 16) << 20
             have = sum((len(m) - 1) * n for n, (_, m) in zip(seen, groups)) * h * 2 * d
             more = max(0, -(-(least - have) // (seen[0] * h * 2 * d)))
             groups = [(groups[0][0], list(groups[0][1]) + [1 + i % 37 for i in range(more)])] + list(groups[1:])
@@ -304,3 +304,30 @@ def test_on_another_stream_beside_another_call():
         y = f.fp8_block_shared_decode_attn(*b)
     torch.cuda.synchronize()
     c.check(x), e.check(y)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_wait_that_runs_out(d):
+    """The copies' wait for a free stage given less time than the pipeline takes: reported, and the next call is sound."""
+    c = Case([(100000, [100, 300])], 8, 1, d, seed=18, tiles=8)      # (782 key tiles of one KV head: six in a piece)
+    cache, q, tab, ctx, starts, shared = c.cache(), c.q.cuda(), _i32(c.table), _i32(c.ctx), _i32(c.starts), _i32(c.shared)
+    ws, fault, lib = f.block_shared_workspace(len(c.ctx), q.shape[1], cache, 1), _i32([0]), f.load_library()
+
+    def call():
+        return f.fp8_block_shared_decode_attn(q, cache, tab, ctx, starts, shared, workspace=ws, fault=fault)
+    ref = call()
+    torch.cuda.synchronize()
+    assert int(fault) == 0
+    assert not torch.equal(ref, f.fp8_block_decode_attn(q, cache, tab, ctx)), "the call shares"
+    lib.fkv_set_decode_wait_limit_ns(1)
+    try:
+        for _ in range(2):
+            call()
+        torch.cuda.synchronize()
+    finally:
+        lib.fkv_set_decode_wait_limit_ns(0)
+    assert int(fault) == f.FAULT_TIMEOUT
+    fault.zero_()
+    for _ in range(2):
+        assert torch.equal(call(), ref)
+    assert int(fault) == 0
