@@ -6,12 +6,19 @@
 // `sink` and the last `recent` tokens count as larger than any weight.  Weights become 32-bit keys that order
 // like the numbers (NaN below everything), and the n-th largest key is found digit by digit, from the top, 11, 11 and 10
 // bits, with a histogram of the keys that share the digits found so far: three counts of T keys whatever the weights are.
-// A second walk in index order numbers the kept ones.
+// A last walk in index order numbers the kept ones.
 // A unit (sequence, KV head) is a cluster of CTAs, each with a consecutive share of its keys in shared memory (so that
-// the weights are read from HBM once), whose histograms meet through distributed shared memory.
+// the weights are read from HBM once), whose histograms meet through distributed shared memory.  Of every 32 keys two words
+// say which are above the digits found so far, and which share them: the walks behind the first look at the latter alone.
+//
+// What bounds it: 32 keys and fewer a thread, so its chain of walks, barriers and round trips through distributed shared memory.  8 heads
+// of 8 sequences of 16k-24k tokens (two CTAs a unit) 16 us, of one of 131,072 (eight) 20, kept to 4,096 and 32,768; reading the weights
+// alone takes 1.
 //
 // Copy.  A warp per (new block, KV head): 16 kept tokens' K and V rows from anywhere, their largest finite
 // magnitude, the block's new scale as an append of the same values to an empty block would choose it, the codes brought to it.
+#include <type_traits>
+
 #include "block_common.cuh"
 
 namespace fkv {
@@ -19,7 +26,7 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kBins = 2048;
-constexpr int kMaxResident = 45056;  // keys of a CTA held in shared memory, at most (176 KB)
+constexpr int kMaxResident = 40960;  // keys of a CTA held in shared memory, at most (160 KB, and 10 KB of masks)
 
 FKV_DEV uint32_t rank_in_cluster() {
   uint32_t r;
@@ -61,10 +68,11 @@ FKV_DEV uint32_t key_of(float w) {
 
 struct SelectShared {
   int hist[3][kBins];    // this CTA's keys
-  int total[3][kBins];   // the cluster's
+  int total[3][kBins];   // the cluster's, of the bins that are this CTA's to sum
   int warp_sum[32], warp_eq[32];
   int digit, left;       // of the last histogram: the digit, and what is to be taken of it
   int gt_eq[2];          // this CTA's keys above the threshold, and equal to it
+  uint2 masks[kMaxResident / 32];  // of 32 keys each
 };
 constexpr int kMaxCluster = 8;
 constexpr int kLoads = 8;  // weights that a thread has on their way
@@ -72,7 +80,7 @@ constexpr int kLoads = 8;  // weights that a thread has on their way
 __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const EvictParams p, int resident_keys) {
   extern __shared__ __align__(16) uint8_t smem[];
   SelectShared& sh = *reinterpret_cast<SelectShared*>(smem);
-  float* held = reinterpret_cast<float*>(smem + sizeof(SelectShared));  // this CTA's weights
+  uint32_t* held = reinterpret_cast<uint32_t*>(smem + sizeof(SelectShared));  // this CTA's keys
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int C = static_cast<int>(ctas_of_cluster()), rank = static_cast<int>(rank_in_cluster());
   for (int i = tid; i < 6 * kBins; i += kSelectThreads) (&sh.hist[0][0])[i] = 0;
@@ -102,7 +110,7 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
     }
     return;
   }
-  // this CTA's keys [lo, hi), of which warp w walks [wlo, whi), 32 at a time
+  // this CTA's keys [lo, hi)
   const int seg = ((T + C - 1) / C + 31) & ~31;
   const int lo = min(rank * seg, T), hi = min(lo + seg, T);
   const bool resident = seg <= resident_keys;
@@ -119,37 +127,87 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
     for (int j = 0; j < kLoads; ++j) {
       const int i = i0 + j * kSelectThreads;
       if (i >= hi) break;
-      if (resident) held[i - lo] = w[j];
-      atomicAdd(&sh.hist[0][key_of_token(i, w[j]) >> 21], 1);
+      const uint32_t k = key_of_token(i, w[j]);
+      if (resident) held[i - lo] = k;
+      atomicAdd(&sh.hist[0][k >> 21], 1);
     }
   }
-  auto weight = [&](int i) -> float { return resident ? held[i - lo] : weights[i]; };
-  auto get = [&](int i) -> uint32_t { return key_of_token(i, weight(i)); };
+  // warp w walks the keys [wlo, whi), 32 at a time
+  const int wseg = (((hi - lo + 31) / 32) + 31) & ~31;
+  const int wlo = min(lo + warp * wseg, hi), whi = min(wlo + wseg, hi);
+  // Of every 32 keys (i0 ...) those whose digits from bit `shift` up are above `found`, and those that have them, to act(i0, masks, the
+  // lane's key where it is one of the latter).  Behind the first walk, words without any of the latter are passed over, `all` aside.
+  auto walk = [&](auto first, auto all, int shift, uint32_t found, auto act) {
+    if (!resident) {
+      for (int i0 = wlo; i0 < whi; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = i < whi ? key_of_token(i, weights[i]) : 0u, d = k >> shift;
+        act(i0, make_uint2(__ballot_sync(0xffffffffu, i < whi && d > found), __ballot_sync(0xffffffffu, i < whi && d == found)), k);
+      }
+      return;
+    }
+    const uint32_t* keys = held + (wlo - lo) + lane;
+    uint2* masks = sh.masks + ((wlo - lo) >> 5);
+    const int words = (whi - wlo + 31) >> 5, rest = whi - wlo - lane;  // keys of this lane at 0, 32, ... below rest
+    if constexpr (decltype(first)::value) {
+#pragma unroll 4
+      for (int x = 0; x < words; ++x) {
+        const bool in = 32 * x < rest;
+        const uint32_t k = in ? keys[32 * x] : 0u, d = k >> shift;
+        const uint2 m = make_uint2(__ballot_sync(0xffffffffu, in && d > found), __ballot_sync(0xffffffffu, in && d == found));
+        if (lane == 0) masks[x] = m;
+        act(wlo + 32 * x, m, k);
+      }
+    } else {
+      for (int x0 = 0; x0 < words; x0 += 32) {  // a word per lane
+        uint2 mine = x0 + lane < words ? masks[x0 + lane] : make_uint2(0u, 0u);
+        for (unsigned some = __ballot_sync(0xffffffffu, mine.y != 0); some != 0; some &= some - 1) {
+          const int at = __ffs(some) - 1, x = x0 + at;
+          const uint32_t y = __shfl_sync(0xffffffffu, mine.y, at);
+          const bool in = y >> lane & 1u;
+          const uint32_t k = in ? keys[32 * x] : 0u, d = k >> shift;
+          uint2 m = make_uint2(__ballot_sync(0xffffffffu, in && d > found), __ballot_sync(0xffffffffu, in && d == found));
+          if (lane == at) mine = make_uint2(mine.x | m.x, m.y);
+          if constexpr (!decltype(all)::value) act(wlo + 32 * x, m, k);
+        }
+        if constexpr (decltype(all)::value) act(x0, mine, 0u);
+        if (x0 + lane < words) masks[x0 + lane] = mine;
+      }
+    }
+    __syncwarp();
+  };
   int left = n;        // keys to take among those that share the digits found so far
   uint32_t found = 0;  // these digits
 #pragma unroll
   for (int pass = 0; pass < 3; ++pass) {
     if (pass > 0) {
-      for (int i = lo + tid; i < hi; i += kSelectThreads) {
-        const uint32_t k = get(i);
-        if (pass == 1 && k >> 21 == found) atomicAdd(&sh.hist[1][k >> 10 & 2047u], 1);
-        if (pass == 2 && k >> 10 == found) atomicAdd(&sh.hist[2][k & 1023u], 1);
-      }
+      if (pass == 1)
+        walk(std::true_type(), std::false_type(), 21, found, [&](int, uint2 m, uint32_t k) {
+          if (m.y >> lane & 1u) atomicAdd(&sh.hist[1][k >> 10 & 2047u], 1);
+        });
+      else
+        walk(std::false_type(), std::false_type(), 10, found, [&](int, uint2 m, uint32_t k) {
+          if (m.y >> lane & 1u) atomicAdd(&sh.hist[2][k & 1023u], 1);
+        });
     }
     __syncthreads();
-    // thread t: the t-th pair of bins from the top.  Few bins are taken (a key's exponent and first digits: tens of them), so every CTA adds
-    // its own to all CTAs' totals rather than reading eight histograms through.
+    // thread t: the t-th pair of bins from the top.  Where few bins are taken (a key's exponent and first digits, and what is left in the
+    // end) every CTA adds its own to all CTAs' totals; in between, where most are, pair x is summed in CTA x % C alone and read there
+    // (131k keys of a unit, cycles added to all and to one: 3,900 and 5,000, 15,000 and 5,400, 3,600 and 6,100).
     const int hi_bin = kBins - 1 - 2 * tid;
     int c0 = sh.hist[pass][hi_bin], c1 = sh.hist[pass][hi_bin - 1];
     if (C > 1) {
       if (pass == 0) wait_cluster();
-      for (int r = 0; r < C; ++r) {
+      const int owner = tid & (C - 1);
+      for (int r = pass == 1 ? owner : 0; r <= (pass == 1 ? owner : C - 1); ++r) {
         if (c0 != 0) peer_add(&sh.total[pass][hi_bin], r, c0);
         if (c1 != 0) peer_add(&sh.total[pass][hi_bin - 1], r, c1);
       }
       sync_cluster();
-      c0 = sh.total[pass][hi_bin];
-      c1 = sh.total[pass][hi_bin - 1];
+      int2 x = *reinterpret_cast<const int2*>(&sh.total[pass][hi_bin - 1]);
+      if (pass == 1) x = peer_int2(&sh.total[pass][hi_bin - 1], owner);
+      c0 = x.y;
+      c1 = x.x;
     }
     int upto = c0 + c1;  // inclusive sums over the threads
 #pragma unroll
@@ -176,54 +234,98 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
     left = sh.left;
   }
   // of the keys equal to the threshold `found` the first `left` stay
-  const int wseg = (((hi - lo + 31) / 32) + 31) & ~31;
-  const int wlo = min(lo + warp * wseg, hi), whi = min(wlo + wseg, hi);
   int gt = 0, eq = 0;
-  for (int i0 = wlo; i0 < whi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < whi ? get(i) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < whi && k > found));
-    eq += __popc(__ballot_sync(0xffffffffu, i < whi && k == found));
+  walk(std::false_type(), std::true_type(), 0, found, [&](int, uint2 m, uint32_t) {  // (resident: a word per lane)
+    gt += __popc(m.x);
+    eq += __popc(m.y);
+  });
+  if (resident) {
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
   }
   if (lane == 0) {
     sh.warp_sum[warp] = gt;
     sh.warp_eq[warp] = eq;
   }
   __syncthreads();
-  int gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0);
-  int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_eq[lane] : 0);
+  // above and equal: in the warps before this one, in the CTA, and in the CTAs before it
+  int gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_sum[lane] : 0), eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_eq[lane] : 0);
+  const int gt_cta = __reduce_add_sync(0xffffffffu, sh.warp_sum[lane]), eq_cta = __reduce_add_sync(0xffffffffu, sh.warp_eq[lane]);
+  int gt_peers = 0, eq_peers = 0;
   if (C > 1) {
-    if (tid == kSelectThreads - 1) {
-      sh.gt_eq[0] = gt_before + gt;
-      sh.gt_eq[1] = eq_before + eq;
+    if (tid == 0) {
+      sh.gt_eq[0] = gt_cta;
+      sh.gt_eq[1] = eq_cta;
     }
     sync_cluster();
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r) {
       if (r >= rank) break;
       const int2 x = peer_int2(sh.gt_eq, r);
-      gt_before += x.x;
-      eq_before += x.y;
+      gt_peers += x.x;
+      eq_peers += x.y;
     }
     arrive_cluster();  // (the last access to another CTA)
   }
-  int at = gt_before + min(eq_before, left);
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = wlo; i0 < whi; i0 += 32) {
-    const int i = i0 + lane;
-    const float w = i < whi ? weight(i) : 0.f;
-    const uint32_t k = i < whi ? key_of_token(i, w) : 0u;
-    const bool is_eq = i < whi && k == found;
-    const uint32_t eqs = __ballot_sync(0xffffffffu, is_eq);
-    const bool keep = i < whi && (k > found || (is_eq && eq_before + __popc(eqs & below) < left));
-    const uint32_t keeps = __ballot_sync(0xffffffffu, keep);
-    if (keep) {
-      const int to = at + __popc(keeps & below);
-      kept[to] = i;
-      if (moved) moved[to] = w;
+  eq_before += eq_peers;
+  const int base = gt_peers + min(eq_peers, left);  // this CTA's first place
+  int at = gt_peers + gt_before + min(eq_before, left);
+  if (resident && wseg >= 256) {
+    // the tokens that stay into a list over the keys, a word per lane, and from there in order: 4,800 cycles for 16,384 keys of a CTA
+    // (straight from the masks, stores of a few lanes each: 9,000; for 1,536 keys 1,500 against 3,700, most lanes without a word)
+    int* list = reinterpret_cast<int*>(held);
+    const int words = (whi - wlo + 31) >> 5;
+    for (int x0 = 0; x0 < words; x0 += 32) {
+      const uint2 m = x0 + lane < words ? sh.masks[((wlo - lo) >> 5) + x0 + lane] : make_uint2(0u, 0u);
+      int eq_to = __popc(m.y);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, eq_to, off);
+        if (lane >= off) eq_to += x;
+      }
+      uint32_t y = m.y;
+      for (int over = min(eq_before + eq_to - left, __popc(y)); over > 0; --over) y &= ~(0x80000000u >> __clz(y));
+      uint32_t keeps = m.x | y;
+      int to = __popc(keeps);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, to, off);
+        if (lane >= off) to += x;
+      }
+      const int sum = __shfl_sync(0xffffffffu, to, 31);
+      to += at - base - __popc(keeps);
+      for (; keeps != 0; keeps &= keeps - 1) list[to++] = wlo + 32 * (x0 + lane) + __ffs(keeps) - 1;
+      at += sum;
+      eq_before += __shfl_sync(0xffffffffu, eq_to, 31);
     }
-    at += __popc(keeps);
-    eq_before += __popc(eqs);
+    __syncthreads();
+    const int count = gt_cta + min(eq_peers + eq_cta, left) - min(eq_peers, left);
+#pragma unroll 4
+    for (int j = tid; j < count; j += kSelectThreads) {
+      const int i = list[j];
+      kept[base + j] = i;
+      if (moved) moved[base + j] = weights[i];
+    }
+  } else {
+    const uint32_t below = (1u << lane) - 1u;
+    auto put = [&](int i0, uint2 m) {
+      uint32_t keeps = m.x | m.y;
+      if (eq_before + __popc(m.y) > left)
+        keeps = __ballot_sync(0xffffffffu, m.x >> lane & 1u || (m.y >> lane & 1u && eq_before + __popc(m.y & below) < left));
+      if (keeps >> lane & 1u) {
+        const int i = i0 + lane, to = at + __popc(keeps & below);
+        kept[to] = i;
+        if (moved) moved[to] = weights[i];
+      }
+      at += __popc(keeps);
+      eq_before += __popc(m.y);
+    };
+    if (resident) {
+#pragma unroll 4
+      for (int i0 = wlo; i0 < whi; i0 += 32) put(i0, sh.masks[(i0 - lo) >> 5]);
+    } else {
+      walk(std::false_type(), std::false_type(), 0, found, [&](int i0, uint2 m, uint32_t) { put(i0, m); });
+    }
   }
   if (C > 1) wait_cluster();  // no CTA leaves while another reads its shared memory
 }

@@ -24,7 +24,7 @@ __host__ __device__ constexpr long long least_saved(int D, int tiles) {
 }
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
-constexpr int kGroupsHeld = 512;  // groups that the plan keeps in shared memory
+constexpr int kGroupsHeld = 512, kLensHeld = 1024;  // groups and sequences whose numbers the plan keeps in shared memory
 
 FKV_DEV int context_of(const SharedParams& p, int b) { return min(max(p.ctx[b], 0), static_cast<int>(min(p.max_blocks * 16LL, static_cast<long long>(INT32_MAX)))); }
 
@@ -37,14 +37,19 @@ FKV_DEV long long warp_sum(long long x) {
 FKV_DEV int tiles_of(const SharedGroup& g) { return (g.keys + 127) / 128 - g.lo / 128; }
 FKV_DEV int items_of(const SharedParams& p, const SharedGroup& g) { return (g.members + p.tok - 1) / p.tok * p.Hkv; }  // (row tile, KV head)
 
-// One CTA; what bounds it are its round trips to L2 (the groups' borders, their first members' contexts, the contexts of all).
+// One CTA; what bounds it are its round trips to L2 (all numbers of the first 256 groups and sequences in one of them).
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p) {
   __shared__ SharedGroup held_s[kGroupsHeld];
   __shared__ long long sum_s[3][kPlanWarps];
-  __shared__ int most_s[kPlanWarps], cut_s[3], base_s;
+  __shared__ int lens_s[kLensHeld], most_s[kPlanWarps], cut_s[3], base_s;
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const bool first_in = tid < p.num_groups;
+  const int first_a = first_in ? p.starts[tid] : 0, first_e = first_in ? p.starts[tid + 1] : 0, first_n = first_in ? p.lens[tid] : 0;
+  for (int b = tid; b < min(p.B, kLensHeld); b += kPlanThreads) lens_s[b] = context_of(p, b);
+  __syncthreads();
+  auto context = [&](int b) { return b < kLensHeld ? lens_s[b] : context_of(p, b); };
   auto group = [&](int i) { return i < kGroupsHeld ? held_s[i] : p.groups[i]; };
   // the groups: members, shared keys (as many as the first member has); what they save, their items and steps (item, key tile)
   long long saved = 0, items = 0, steps = 0;
@@ -52,9 +57,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
   bool bad = false;
   for (int i = tid; i < p.num_groups; i += kPlanThreads) {
     SharedGroup g = {};
-    const int e = p.starts[i + 1];
-    g.first = p.starts[i];
-    g.keys = p.lens[i];
+    const int e = i < kPlanThreads ? first_e : p.starts[i + 1];
+    g.first = i < kPlanThreads ? first_a : p.starts[i];
+    g.keys = i < kPlanThreads ? first_n : p.lens[i];
     if (g.first < 0 || e < g.first || e > p.B) {
       bad = true;
       g.first = g.keys = 0;
@@ -64,7 +69,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
         raise_fault(p.fault, FKV_FAULT_CONTEXT);
         g.keys = 0;
       }
-      g.keys = g.members >= 2 ? min(g.keys, context_of(p, g.first)) : 0;
+      g.keys = g.members >= 2 ? min(g.keys, context(g.first)) : 0;
     }
     if (g.keys > 0) {
       g.lo = p.window > 0 ? max(0, g.keys - p.window) : 0;
@@ -165,7 +170,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
   if (tid == 0) *p.pieces = base_s;
   // the sequences: in which group, if it shares (a member shorter than the shared part does not)
   for (int b = tid; b < p.B; b += kPlanThreads) {
-    const int T = context_of(p, b);
+    const int T = context(b);
     int lo = 0, hi = share ? p.num_groups : 0;  // groups before lo begin at or before b, those from hi on behind it
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;

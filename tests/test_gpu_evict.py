@@ -71,13 +71,13 @@ def test_evict(d, ctx, budget, sink, recent, h):
     Case(ctx, budget, sink, recent, h, d, seed=len(ctx) + budget).check()
 
 
-@pytest.mark.parametrize("ctx,budget,h", [([5000, 12345], 1000, 1), ([40001], 20000, 2), ([30000, 100, 8193], 8192, 3)])
+@pytest.mark.parametrize("ctx,budget,h", [([5000, 12345], 1000, 1), ([40001], 20000, 2), ([30000, 100, 8193], 8192, 3), ([90001, 66000], 30000, 1)])
 def test_evict_clusters(ctx, budget, h):
     Case(ctx, budget, 4, 100, h, 64, seed=budget, wide=3).check()
 
 
 def test_evict_more_keys_than_shared_memory_holds():
-    """400,001 tokens of one head: eight CTAs hold 45,056 keys each, the walk goes over global memory."""
+    """400,001 tokens of one head: eight CTAs hold 40,960 keys each, the walk goes over global memory."""
     Case([400001], 700, 4, 100, 1, 64, seed=9).check()
 
 
@@ -98,7 +98,7 @@ def _close(rng, shape):
 
 
 @pytest.mark.parametrize("weights", [_ties, _same, _special, _close])
-@pytest.mark.parametrize("ctx,budget", [([100, 4097], 50), ([20000], 4001)])
+@pytest.mark.parametrize("ctx,budget", [([100, 4097], 50), ([20000], 4001), ([80003], 5001)])
 def test_evict_equal_and_special_weights(weights, ctx, budget):
     Case(ctx, budget, 2, 5, 2, 64, seed=budget, weights=weights).check()
 
