@@ -1174,7 +1174,8 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
 
 constexpr int kGatherThreads = 256, kGatherKeys = 4 * kGatherThreads;
 
-// w_j from the scores: grid (kGatherKeys keys each, KV heads, sequences).
+// w_j from the scores: grid (kGatherKeys keys each, KV heads, sequences).  A thread's scores and weights are on their way while the rows'
+// sums, a chain of round trips, are put together.
 template <int RN>
 __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const BlockWeightsParams p) {
   __shared__ float lse_s[16];
@@ -1186,6 +1187,19 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const BlockWeigh
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t unit = static_cast<size_t>(b) * p.Hkv + g;
   const int2 at = p.units[unit];
+  constexpr int KEYS = kGatherKeys / kGatherThreads;
+  const float4* scores = reinterpret_cast<const float4*>(p.scores + unit * p.max_blocks * 16 * RN);
+  float* weights = p.weights + unit * p.weights_len;
+  const long long key0 = static_cast<long long>(blockIdx.x) * kGatherKeys + threadIdx.x;
+  float4 y[KEYS][RN / 4];
+  float old[KEYS];
+#pragma unroll
+  for (int x = 0; x < KEYS; ++x) {
+    const long long key = key0 + x * kGatherThreads;
+#pragma unroll
+    for (int r = 0; r < RN / 4; ++r) y[x][r] = key < s.T ? scores[key * (RN / 4) + r] : make_float4(0.f, 0.f, 0.f, 0.f);
+    old[x] = key < s.T - s.rows && p.decay != 0.f ? weights[key] : 0.f;
+  }
   for (int r = warp; r < RN; r += kGatherThreads / 32) {
     float m = -kHuge, l = 0.f;
     for (int x = lane; x < at.y; x += 32) {
@@ -1206,21 +1220,18 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const BlockWeigh
   float lse[RN];
 #pragma unroll
   for (int r = 0; r < RN; ++r) lse[r] = lse_s[r];
-  const float4* scores = reinterpret_cast<const float4*>(p.scores + unit * p.max_blocks * 16 * RN);
-  float* weights = p.weights + unit * p.weights_len;
 #pragma unroll
-  for (int x = 0; x < kGatherKeys / kGatherThreads; ++x) {
-    const long long key = static_cast<long long>(blockIdx.x) * kGatherKeys + x * kGatherThreads + threadIdx.x;
+  for (int x = 0; x < KEYS; ++x) {
+    const long long key = key0 + x * kGatherThreads;
     if (key >= s.T) break;
     float sum = 0.f;
 #pragma unroll
-    for (int r = 0; r < RN; r += 4) {
-      const float4 y = scores[key * (RN / 4) + r / 4];
-      const float v[4] = {y.x, y.y, y.z, y.w};
+    for (int r = 0; r < RN / 4; ++r) {
+      const float v[4] = {y[x][r].x, y[x][r].y, y[x][r].z, y[x][r].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum += v[j] == -INFINITY ? 0.f : ex2(v[j] - lse[r + j]);
+      for (int j = 0; j < 4; ++j) sum += v[j] == -INFINITY ? 0.f : ex2(v[j] - lse[4 * r + j]);
     }
-    weights[key] = key < s.T - s.rows && p.decay != 0.f ? fmaf(p.decay, weights[key], sum) : sum;
+    weights[key] = key < s.T - s.rows && p.decay != 0.f ? fmaf(p.decay, old[x], sum) : sum;
   }
 }
 
