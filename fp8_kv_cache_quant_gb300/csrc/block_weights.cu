@@ -470,8 +470,8 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     pend_s[0] = pend_s[5] = 0;
     fence_mbar_init();
   }
-  // The tensor memory, all of an SM's, is taken after the wait: before it, it could be what a CTA of the kernel before still needs.
-  griddep_wait();
+  // The kernel before this one lets it start when itself has waited for what came before: the sequences, the block table and the scales
+  // are there, and only it holds tensor memory, all of which it has.  What it writes is waited for further down.
   if (warp == C::READERS + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -486,10 +486,13 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_launch_dependents();
   int32_t* done = p.done + (K == kRows ? 0 : p.slots);
   Place at = division.first;
   int u = 0;  // steps so far
+  KeyFeed<K, C::KT> feed;
+  if (warp == C::READERS && at.n > 0) feed.begin(at, p);
+  griddep_wait();
+  griddep_launch_dependents();
 
   if (warp < C::READERS) {
     // ============================================================ the scores' readers
@@ -682,8 +685,6 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     size_t held[C::NS];             // pass 1: the row tile that a stage holds
 #pragma unroll
     for (int s = 0; s < C::NS; ++s) held[s] = ~static_cast<size_t>(0);
-    Feed feed;
-    if (at.n > 0) feed.begin(at, p);
     // The keys of tile `tile` (a block per lane; blocks behind the sequence are left as they are: their keys are hidden, or their sums
     // not stored) and their scales.
     auto copy_keys = [&](uint8_t* dst, uint64_t* full, int tile, int x) {  // x: the step (pass 0) or piece
