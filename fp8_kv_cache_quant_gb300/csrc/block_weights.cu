@@ -386,9 +386,11 @@ __global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) 
 // ---------------------------------------------------------------- the two passes over many rows
 
 // The unit's own tile stays (pass 0: 128 rows, both terms; pass 1: 256 keys, two products of 128), the others stream past it.  One CTA per
-// SM.  Sixteen warps read the scores: in pass 0 eight of them every other step, a thread one row's scores for 64 keys; in pass 1 all of them
-// every step, a thread two keys' for 32 rows (whose c and lse it reads from shared memory once for both: one key per thread was bound by
-// that, 2,000 cycles per 256 keys and 128 rows).  A wait that need not wait takes 100 to 200 cycles, a step's products 540 (head_dim
+// SM.  Sixteen warps read the scores: in pass 0 a thread one row's for 64 keys, in pass 1 two keys' for 64 rows (whose c and lse it reads
+// from shared memory once for both: one key per thread was bound by that, 2,000 cycles per 256 keys and 128 rows).  Eight of them take
+// every other step, so that a piece's end, a chain of barriers, is passed by eight while the others compute (128 rows a
+// unit, head_dim 128: 53.1 us a call with turns in pass 0 alone, 51.3 with both); in pass 1 at head_dim 256, whose products set the pace and wait for the scores' two buffers,
+// all sixteen take every step, 32 rows a thread (a prompt of 4,001 tokens, 8/1 heads: 91 us against 97).  A wait that need not wait takes 100 to 200 cycles, a step's products 540 (head_dim
 // 128), so the readers wait as seldom as they can, and two warps issue the products of the steps in turn.
 template <int D, Kind K>
 struct PassCfg : Shape<D> {
@@ -402,6 +404,8 @@ struct PassCfg : Shape<D> {
   static constexpr int NS = K == kRows ? (D == 256 ? 2 : 8) : (D == 256 ? 2 : 3);
   static constexpr int SBUF = 4 / NT;                           // buffers of a step's scores, 128 NT columns each
   static constexpr int READERS = 16, THREADS = 32 * (READERS + 3);
+  static constexpr bool TURNS = K == kRows || D <= 128;         // eight readers every other step
+  static constexpr int COLS = TURNS ? 64 : 32;                  // columns of a reader
   // K scales in slots: of steps 4 b .. 4 b + 3 (pass 0; the copies run at most NS + SBUF steps ahead), or of piece r (pass 1: NY ahead of
   // the products, which are SBUF steps ahead of the readers)
   static constexpr int SCN = 8, SCB = K == kRows ? 4 : 1;
@@ -454,11 +458,11 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     }
     for (int i = 0; i < C::SBUF; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], K == kRows ? C::READERS / 2 : C::READERS);
+      mbar_init(&s_free[i], C::TURNS ? C::READERS / 2 : C::READERS);
     }
     for (int i = 0; i < C::NS; ++i) {
       mbar_init(&x_full[i], 1);
-      mbar_init(&x_empty[i], K == kKeys ? 1 + C::READERS : 1);  // (the rows' parameters are read by the readers)
+      mbar_init(&x_empty[i], K == kKeys ? 1 + (C::TURNS ? C::READERS / 2 : C::READERS) : 1);  // (the rows' parameters are read by the readers)
     }
     for (int i = 0; i < C::SCN; ++i) mbar_init(&sc_full[i], 1);
     for (int i = 0; i < 2; ++i) {
@@ -496,11 +500,17 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
 
   if (warp < C::READERS) {
     // ============================================================ the scores' readers
-    // tensor memory lane i; pass 0: part >> 1 the steps' parity, columns 64 (part & 1) .. + 63; pass 1: columns 32 part .. + 31
+    // tensor memory lane i, columns c_part .. + COLS - 1; taking turns, part >> 1 the steps' parity
     const int part = warp >> 2, i = (warp & 3) * 32 + lane;
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (K == kRows ? 64 * (part & 1) : 32 * part);
+    const int c_part = C::TURNS ? 64 * (part & 1) : 32 * part;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + c_part;
     bool ok = true;
     while (ok && at.n > 0) {
+      if (K == kKeys && C::TURNS && at.n == 1 && (u & 1) != part >> 1) {  // the other eight warps' alone
+        ++u;
+        at.next(p);
+        continue;
+      }
       // pass 0: the row's sum l of 2^(x - m) (of this thread's columns).  m need not be the maximum, only near enough that no sum
       // overflows: it is the largest score of the first columns, and moves when a sum of 32 reaches 2^60.
       float m = -kHuge, l = 0.f;
@@ -575,21 +585,22 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
           }
         }
       } else {
-        int c0 = 128 * (at.first() + at.s) + 32 * part;  // this thread's first row
-        for (int v0 = u; ok && v0 < end; ++v0, c0 += 128) {
+        const int off = C::TURNS ? (u ^ (part >> 1)) & 1 : 0;
+        int c0 = 128 * (at.first() + at.s + off) + c_part;  // this thread's first row
+        for (int v0 = u + off; ok && v0 < end; v0 += C::TURNS ? 2 : 1, c0 += C::TURNS ? 256 : 128) {
           const int sb = v0 % C::SBUF, st = v0 % C::NS;
-          if ((v0 & 7) == 7 && abort_warp(abort_s)) { ok = false; break; }
+          if ((v0 & 6) == 6 && abort_warp(abort_s)) { ok = false; break; }
           const bool any_partly = __any_sync(0xffffffffu, limit[0] > c0 || limit[C::NT - 1] > c0);
           if (!wait_warp(&s_full[sb], (v0 / C::SBUF) & 1)) { ok = false; break; }
           tc_fence_after();
-          const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + 16 * part;
+          const float4* rp = reinterpret_cast<const float4*>(sStream + st * C::STREAM + C::QT) + c_part / 2;
 #pragma unroll 1
-          for (int c = 0; c < 32; c += 16) {
+          for (int c = 0; c < C::COLS; c += 16) {
             float v[C::NT][16];
 #pragma unroll
             for (int h = 0; h < C::NT; ++h) tmem_ld16(lane_base + 128 * (C::NT * sb + h) + c, v[h]);
             tmem_ld_wait();
-            if (c == 16) {
+            if (c == C::COLS - 16) {
               tc_fence_before();
               mbar_arrive_warp(&s_free[sb]);
             }
@@ -620,7 +631,8 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
       }
       u = end;
       if (!ok) break;
-      // ---- the column parts of the piece meet in shared memory
+      // ---- the column parts of the piece meet in shared memory (pass 1, a piece of one step: those of eight warps, which arrive twice)
+      const bool alone = K == kKeys && C::TURNS && at.n == 1;
       const int jb = at.piece & 1;
       float2* row_join = reinterpret_cast<float2*>(smem + C::OFF_JOIN + jb * C::JOIN);
       float* key_join = reinterpret_cast<float*>(row_join);
@@ -632,7 +644,8 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
         for (int h = 0; h < C::NT; ++h) key_join[part * 256 + 128 * h + i] = acc[h].x + acc[h].y;
       }
       mbar_arrive_warp(&j_full[jb]);
-      if (warp < (K == kRows ? 4 : 8)) {
+      if (alone) mbar_arrive_warp(&j_full[jb]);
+      if (K == kRows ? warp < 4 : ((C::TURNS ? end - 1 : 0) & 1) == part >> 1) {
         if (!wait_warp(&j_full[jb], (at.piece >> 1) & 1)) { ok = false; break; }
         int k0 = k, ns = 1;
         if (!at.whole()) {
@@ -652,8 +665,10 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
           if (ns > 1) p.pieces[place * 128 + i] = make_float2(top, sum);
           else if (limit[0] > 0) p.rows[tile_index(p, at.r0, at.b, at.g, at.t) * 256 + (i >> 1) * 4 + (i & 1) + 2] = -(top + lg2(sum));
         } else {
-          const int j = threadIdx.x, key = C::KT * at.t + j;
-          const float sum = (key_join[j] + key_join[256 + j]) + (key_join[512 + j] + key_join[768 + j]);
+          const int j = threadIdx.x & 255, key = C::KT * at.t + j;
+          const float* mine_join = key_join + 512 * (part >> 1) + j;
+          float sum = mine_join[0] + mine_join[256];
+          if (!alone) sum = part >> 1 ? (key_join[j] + key_join[256 + j]) + sum : sum + (key_join[512 + j] + key_join[768 + j]);
           if (ns > 1) {
             p.sums[place * C::KT + j] = sum;
           } else if (key < at.T) {
@@ -662,7 +677,7 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
           }
         }
         mbar_arrive_warp(&j_free[jb]);
-        if (ns > 1 && threadIdx.x == 0) {
+        if (ns > 1 && threadIdx.x == (K == kRows ? 0 : 256 * (part >> 1))) {
           volatile int* pend = pend_s + (k == k0 ? 5 : 0);
           pend[0] = ns;
           pend[1] = k0;
