@@ -4,8 +4,10 @@ Argument marshalling only (part of it compiled, csrc/binding.cpp): every step of
 computation runs in the library's CUDA kernels.  Tensors are torch CUDA tensors (used for device memory and streams); the
 C entry points receive their raw pointers.  The binding has the C ABI's names:
 ``kv_quant_cache``, ``fp8_decode_attn``, ``fp8_prefill_attn`` and the size queries; the rotary
-cache writes ``kv_rope_cache`` and ``kv_block_cache``; ``fp8_block_decode_attn`` and
-``fp8_block_prefill_attn`` over block-scaled pools.
+cache writes ``kv_rope_cache`` and ``kv_block_cache`` (positions of one axis or several);
+``fp8_block_decode_attn``, ``fp8_block_shared_decode_attn`` (sequences that share their first
+tokens) and ``fp8_block_prefill_attn`` over block-scaled pools; ``fp8_block_attn_weights``, what
+cached keys receive of the attention, and ``kv_block_evict``, which keeps the heaviest.
 
 The library must have been built (``python -m fp8_kv_cache_quant_gb300.build`` or
 ``__graft_entry__.build()``); importing the binding does not load it, calling an
@@ -589,7 +591,7 @@ def kv_block_evict(cache: BlockCache, block_table, context_lens, weights, budget
             if new_lens is None:
                 new_lens = torch.empty(block_table.shape[0], dtype=torch.int32, device=dev)
             if kept is None:
-                kept = torch.empty(block_table.shape[0], cache.k_cache.shape[1], budget, dtype=torch.int32, device=dev)
+                kept = torch.empty(block_table.shape[0], cache.k_cache.shape[1], max(budget, 0), dtype=torch.int32, device=dev)
     _call("kv_block_evict", cache.k_cache, stream, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale, block_table,
           context_lens, weights, budget, sink, recent, new_table, new_weights, new_lens, kept, fault)
     return new_lens, kept

@@ -1,6 +1,6 @@
 // The compiled part of the Python binding: argument checks and the calls of the entry points whose
-// small calls are bound by the host (the rotary cache writes and the attention over block-scaled
-// caches).  A decode step makes these calls once per layer, and their kernels run for a few
+// small calls are bound by the host (the rotary cache writes, and the attention over block-scaled
+// caches with its weights and the eviction).  A decode step makes these calls once per layer, and their kernels run for a few
 // microseconds; checking a dozen tensors' types, shapes and devices takes Python ten.
 //
 // Every function takes the raw stream, then its arguments in order (None for an absent tensor),

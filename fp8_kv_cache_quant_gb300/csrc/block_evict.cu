@@ -17,6 +17,7 @@
 //
 // Copy.  A warp per (new block, KV head): 16 kept tokens' K and V rows from anywhere, their largest finite
 // magnitude, the block's new scale as an append of the same values to an empty block would choose it, the codes brought to it.
+#include <atomic>
 #include <type_traits>
 
 #include "block_common.cuh"
@@ -539,9 +540,14 @@ cudaError_t launch_block_evict(const EvictParams& p, int D, int num_sms, cudaStr
   if (blocks == 0) return cudaSuccess;
   const long long items = units * blocks;
   auto kern = D == 64 ? evict_gather_kernel<64> : D == 128 ? evict_gather_kernel<128> : evict_gather_kernel<256>;
-  int per_sm = 0;
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kGatherThreads, 0);
-  if (e != cudaSuccess) return e;
+  static std::atomic<int> known[3];  // CTAs of each that an SM holds, asked once
+  std::atomic<int>& k = known[D == 64 ? 0 : D == 128 ? 1 : 2];
+  int per_sm = k.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kGatherThreads, 0);
+    if (e != cudaSuccess) return e;
+    k.store(per_sm, std::memory_order_relaxed);
+  }
   const unsigned grid = static_cast<unsigned>(std::min<long long>((items + kGatherThreads / 32 - 1) / (kGatherThreads / 32),
                                                                   static_cast<long long>(per_sm) * num_sms));
   return launch_dependent(kern, dim3(grid), dim3(kGatherThreads), 0, s, p, blocks);

@@ -7,6 +7,13 @@
 //                  tile of block_attend.cuh, whose result goes to the workspace as (o, lse);
 //   block_decode_kernel<.., true>  what every sequence has of its own, and sequences that share nothing;
 //   join_kernel    per (sequence, KV head) o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over both kinds of pieces.
+//
+// What bounds it.  32 sequences of 16 to 1,024 tokens behind 32,768 shared ones, 32/8 heads of 128: 51 us (271 read one by one), in a
+// chain: plan 3, prefix 26 (14 key tiles a CTA at 1.4 us, the softmax's instructions, as in the prefill), their own tokens 15
+// (its fixed 12 of ramp, last pieces and merge) and join 5.  The four kernels meet in the stream; only the third begins before the
+// second has ended.
+#include <atomic>
+
 #include "block_attend.cuh"
 #include "block_decode_kernel.cuh"
 #include "block_shared.cuh"
@@ -344,10 +351,14 @@ cudaError_t launch_prefix(const BlockPrefillParams& p, const SharedParams& sp, c
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
   // the warpgroups' register budgets add up to the launch's 128 per thread (a kernel built with fewer would wait forever)
-  cudaFuncAttributes a;
-  e = cudaFuncGetAttributes(&a, kern);
-  if (e != cudaSuccess) return e;
-  if (a.numRegs != C::REG_LAUNCH) return cudaErrorInvalidKernelImage;
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes a;
+    e = cudaFuncGetAttributes(&a, kern);
+    if (e != cudaSuccess) return e;
+    regs.store(a.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != C::REG_LAUNCH) return cudaErrorInvalidKernelImage;
   return launch_dependent(kern, dim3(ctas), dim3(C::THREADS), C::SMEM, s, p, sp, tmk, tmv);
 }
 

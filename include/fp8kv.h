@@ -36,11 +36,12 @@
  *             (block, KV head) has its own float32 scale for K and one for V: no scale is
  *             calibrated, the append (kv_block_cache) finds it from the block's tokens.
  *
- * Launches.  The decode kernels, the rotary and block-scaled cache writes and the block-scaled
- * prefill are launched with programmatic stream serialisation: such a kernel may
- * be scheduled while the kernel before it in the stream finishes, and a decode kernel sets up
- * its barriers and tensor memory then, but it reads and writes no global memory until that
- * kernel has completed, so the stream's ordering is kept.
+ * Launches.  The decode kernels, the rotary and block-scaled cache writes, the block-scaled
+ * prefill, the eviction and the attention weights are launched with programmatic stream serialisation:
+ * such a kernel may be scheduled while the kernel before it in the stream finishes, and a decode kernel
+ * sets up its barriers and tensor memory then, but a call's first kernel reads and writes no global memory
+ * until that kernel has completed, and no later call's until all of this call's have, so the stream's
+ * ordering is kept.
  *
  * Errors.  Argument checks run on the host before anything is enqueued and return
  * FKV_INVALID_ARG or FKV_UNSUPPORTED; a failed launch returns FKV_CUDA_ERROR.  Data
