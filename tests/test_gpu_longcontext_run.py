@@ -216,3 +216,75 @@ def test_many_answers_from_one_thinned_prompt():
     alone = f.fp8_block_decode_attn(turned1, s.cache, d_forks, _i32(ctx), fault=fault)
     s.attended(alone, turned1, forks, ctx)
     assert not torch.equal(out, alone), "the shared part is attended by itself"
+
+
+def test_calls_right_behind_one_another():
+    """Kernels start while those before them end: the calls of a program, each fed by the one before, give the bits that they give
+    with the GPU idle in between."""
+    rng = np.random.default_rng(3)
+    lens, members, budget = [3000, 700, 1500], 100, 2000
+    blocks = [(t + 15) // 16 for t in lens]
+    nb = sum(blocks) + (members + 2) * 4 + 3 * 125
+    ids = rng.permutation(nb).astype(np.int32)
+    table = np.full((3, max(blocks)), -1, np.int32)
+    at = 0
+    for b, n in enumerate(blocks):
+        table[b, :n] = ids[at:at + n]
+        at += n
+    new_table = ids[at:at + 3 * 125].reshape(3, 125)
+    at += 3 * 125
+    forks = np.full((members, 125 + 2), -1, np.int32)     # 100 sequences behind what the first one keeps, two blocks each of their own
+    forks[:, :125] = new_table[0]
+    forks[:, 125:] = ids[at:at + 2 * members].reshape(members, 2)
+    n = sum(lens)
+    cu = np.concatenate(([0], np.cumsum(lens)))
+    pools = [torch.from_numpy((rng.integers(0, 256, (nb, H, 16, D)) & 0x7B).astype(np.uint8)).cuda() for _ in range(2)]
+    scales = [torch.full((nb, H), 2.0 ** -9, device="cuda") for _ in range(2)]
+    q, k, v = _bf16(rng, n, HQ, D), _bf16(rng, n, H, D), _bf16(rng, n, H, D)
+    q1, k1, v1 = _bf16(rng, members, HQ, D), _bf16(rng, members, H, D), _bf16(rng, members, H, D)
+    rope = f.Rope(f.Rope.table(ROWS, D), axes=f.Rope.sections(24, 20, 20))
+    pos, pos1 = (torch.from_numpy(rng.integers(0, ROWS, (3, m))).cuda() for m in (n, members))
+    d = dict(cu=_i32(cu), table=_i32(table), lens=_i32(lens), new_table=_i32(new_table), forks=_i32(forks), starts=_i32([0, members]),
+             shared=_i32([budget]), cu1=_i32(np.arange(members + 1)))
+    last = torch.cat([torch.arange(e - 40, e) for e in cu[1:]]).cuda()
+
+    def run(wait):
+        cache = f.BlockCache(*(x.clone() for x in pools + scales))
+        weights, moved = (torch.zeros(3, H, m * 16, device="cuda") for m in (table.shape[1], 125))
+        per_fork = torch.zeros(members, H, 127 * 16, device="cuda")
+        fault = _i32([0])
+        ws = (f.block_shared_workspace(members, HQ, cache, 1), f.attn_weights_workspace(3, 120, 40, HQ, cache, table.shape[1]),
+              f.block_decode_workspace(members, HQ, cache), f.attn_weights_workspace(members, members, 1, HQ, cache, forks.shape[1]))
+        turned1, out1, out2 = (torch.empty_like(q1) for _ in range(3))
+        fork_lens = torch.full((members,), budget, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        turned = f.kv_block_cache(k, v, d["cu"], max(lens), cache, d["table"], d["lens"], rope=rope, q=q, positions=pos, fault=fault)
+        wait()
+        out = f.fp8_block_prefill_attn(turned, d["cu"], max(lens), cache, d["table"], d["lens"], fault=fault)
+        wait()
+        f.fp8_block_attn_weights(turned, d["cu"], max(lens), cache, d["table"], d["lens"], weights, decay=0.0, fault=fault)
+        wait()
+        f.fp8_block_attn_weights(turned[last], _i32([0, 40, 80, 120]), 40, cache, d["table"], d["lens"], weights, decay=0.5, workspace=ws[1], fault=fault)
+        wait()
+        new_lens, kept = f.kv_block_evict(cache, d["table"], d["lens"], weights, budget, d["new_table"], sink=4, recent=64, new_weights=moved, fault=fault)
+        wait()
+        for _ in range(3):
+            fork_lens += 1
+            f.kv_block_cache(k1, v1, d["cu1"], 1, cache, d["forks"], fork_lens, rope=rope, q=q1, q_out=turned1, positions=pos1, fault=fault)
+            wait()
+            f.fp8_block_shared_decode_attn(turned1, cache, d["forks"], fork_lens, d["starts"], d["shared"], out=out1, workspace=ws[0], fault=fault)
+            wait()
+            f.fp8_block_attn_weights(out1, d["cu1"], 1, cache, d["forks"], fork_lens, per_fork, workspace=ws[3], fault=fault)
+            wait()
+            f.fp8_block_decode_attn(out1, cache, d["forks"], fork_lens, out=out2, workspace=ws[2], fault=fault)
+            wait()
+            f.fp8_block_shared_decode_attn(out2, cache, d["forks"], fork_lens, d["starts"], d["shared"], out=out1, workspace=ws[0], fault=fault)
+            wait()
+        torch.cuda.synchronize()
+        assert int(fault) == 0
+        return [out, weights, moved, new_lens, kept, out1, out2, per_fork, cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale]
+    want = run(torch.cuda.synchronize)
+    assert all(bool(x.float().isfinite().all()) for x in want[:8])
+    for _ in range(8):
+        for x, y in zip(run(lambda: None), want):
+            assert torch.equal(x, y)
