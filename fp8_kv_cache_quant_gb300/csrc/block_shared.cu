@@ -26,8 +26,8 @@ namespace {
 // 8,192 tokens (saved 117 MB, 4 tiles) 25.8 and 28.0, behind 4,096 (59 MB, 2) 23.0 and 20.2; 4 behind 32,768 (201 MB, 14) 33.4 and
 // 42.9, behind 16,384 (101 MB, 7) 27.0 and 26.0; 64/8 heads of 64: 8 behind 16,384 (117 MB, 7) 28.4 and 37.4, 4 (50 MB) 27.6 and
 // 24.8; 16/8 heads of 256: 4 behind 16,384 (201 MB, 7) 36.9 and 46.0, 8,192 (101 MB, 4) 30.8 and 27.6.
-__host__ __device__ constexpr long long least_saved(int D, int tiles) {
-  return (48LL + D / 4 << 20) + (static_cast<long long>(D < 128 ? D : 128) << 16) * tiles;
+__host__ __device__ constexpr bool sharing_pays(long long tokens, int Hkv, int D, int tiles) {  // (tokens, times heads, may pass 64 bits)
+  return static_cast<double>(tokens) * 2 * Hkv * D >= static_cast<double>((48LL + D / 4 << 20) + (static_cast<long long>(D < 128 ? D : 128) << 16) * tiles);
 }
 
 constexpr int kPlanThreads = 256, kPlanWarps = kPlanThreads / 32;
@@ -109,8 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
     steps += sum_s[2][w];
     most = max(most, most_s[w]);
   }
-  saved *= p.Hkv * 2 * p.D;
-  bool share = !bad && saved >= least_saved(p.D, 1);
+  bool share = !bad && sharing_pays(saved, p.Hkv, p.D, 1);
   // How many key tiles a piece has: the fewest whose pieces fit the SMs once (or, where the grid has room for it, twice, or three
   // times: cut_s), by as many tries as a warp has lanes; a wave costs about three tiles besides its own.  More items than that are
   // not cut.
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
         cut = cut_s[m];
       }
     }
-    share = saved >= least_saved(p.D, cut);
+    share = sharing_pays(saved, p.Hkv, p.D, cut);
   }
   // the pieces' places, group after group
   for (int i0 = 0; i0 < p.num_groups; i0 += kPlanThreads) {
@@ -411,7 +410,7 @@ cudaError_t launch_block_shared(BlockDecodeParams dp, int D, int ctas, const int
                                 int num_sms, cudaStream_t s) {
   // (keys that a group can save, whatever the groups are)
   const long long keys = std::min(dp.max_blocks * 16LL, dp.window > 0 ? static_cast<long long>(dp.window) : INT64_MAX);
-  if ((dp.B - 1) * keys * (dp.Hkv >> dp.halves) * 2 * D < least_saved(D, 1)) return launch_block_decode(dp, D, ctas, s);
+  if (!sharing_pays((dp.B - 1) * keys, dp.Hkv >> dp.halves, D, 1)) return launch_block_decode(dp, D, ctas, s);
   SharedParams sp = {};
   sp.B = dp.B;
   sp.Hq = dp.Hq;
