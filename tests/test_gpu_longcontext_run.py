@@ -288,3 +288,40 @@ def test_calls_right_behind_one_another():
     for _ in range(8):
         for x, y in zip(run(lambda: None), want):
             assert torch.equal(x, y)
+
+
+def test_blocks_behind_four_gigabytes():
+    """The same contents in a small pool and at the end of one of 4.5 GB: the same bits of every call."""
+    rng = np.random.default_rng(4)
+    lens, budget, nb, far = [2300, 40, 700], 600, 400, 1_100_000
+    ids, at = rng.permutation(nb).astype(np.int32), 0
+    table, new_table = np.full((3, 150), -1, np.int32), np.full((3, 40), -1, np.int32)
+    for b, t in enumerate(lens):
+        n, m = (t + 15) // 16, (min(t, budget) + 15) // 16
+        table[b, :n], new_table[b, :m] = ids[at:at + n], ids[at + n:at + n + m]
+        at += n + m
+    members = 90                              # of one group behind the first sequence's first 2,288 tokens
+    forks = np.tile(table[0, :144], (members, 1))
+    n, cu = sum(lens), np.concatenate(([0], np.cumsum(lens)))
+    pools = [torch.from_numpy((rng.integers(0, 256, (nb, H, 16, D)) & 0x7B).astype(np.uint8)).cuda() for _ in range(2)]
+    q, k, v, q1 = _bf16(rng, n, HQ, D), _bf16(rng, n, H, D), _bf16(rng, n, H, D), _bf16(rng, members, HQ, D)
+    rope = f.Rope(f.Rope.table(ROWS, D), axes=f.Rope.sections(24, 20, 20))
+    pos = torch.from_numpy(rng.integers(0, ROWS, (3, n))).cuda()
+
+    def run(blocks):
+        off = blocks - nb
+        cache = f.BlockCache(*(torch.zeros(blocks, H, 16, D, dtype=torch.uint8, device="cuda") for _ in range(2)),
+                             *(torch.ones(blocks, H, device="cuda") for _ in range(2)))
+        for x, y in zip((cache.k_cache, cache.v_cache), pools):
+            x[off:] = y
+        t, nt, fk = (_i32(np.where(x < 0, x, x + off)) for x in (table, new_table, forks))
+        fault, weights, ctx, moved = _i32([0]), torch.zeros(3, H, 2400, device="cuda"), _i32(lens), torch.zeros(3, H, 640, device="cuda")
+        turned = f.kv_block_cache(k, v, _i32(cu), max(lens), cache, t, ctx, rope=rope, q=q, positions=pos, fault=fault)
+        f.fp8_block_attn_weights(turned, _i32(cu), max(lens), cache, t, ctx, weights, decay=0.0, fault=fault)
+        f.fp8_block_attn_weights(turned[:3].contiguous(), _i32([0, 1, 2, 3]), 1, cache, t, ctx, weights, fault=fault)
+        out = f.fp8_block_shared_decode_attn(q1, cache, fk, _i32([2300] * members), _i32([0, members]), _i32([2288]), fault=fault)
+        kept = f.kv_block_evict(cache, t, ctx, weights, budget, nt, sink=4, recent=64, new_weights=moved, fault=fault)
+        assert int(fault) == 0
+        return [turned, weights, out, moved, *kept, *(x[off:].clone() for x in (cache.k_cache, cache.v_cache, cache.k_scale, cache.v_scale))]
+    for x, y in zip(run(nb), run(far)):
+        assert torch.equal(x, y)
