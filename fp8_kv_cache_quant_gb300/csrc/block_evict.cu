@@ -69,7 +69,7 @@ FKV_DEV uint32_t key_of(float w) {
 
 struct SelectShared {
   int hist[3][kBins];    // this CTA's keys
-  int total[3][kBins];   // the cluster's, of the bins that are this CTA's to sum
+  int total[3][kBins];   // the cluster's (of the second digit: of the pairs of bins that are this CTA's to sum)
   int warp_sum[32], warp_eq[32];
   int digit, left;       // of the last histogram: the digit, and what is to be taken of it
   int gt_eq[2];          // this CTA's keys above the threshold, and equal to it
