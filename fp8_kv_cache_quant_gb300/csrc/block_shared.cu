@@ -45,6 +45,8 @@ FKV_DEV int tiles_of(const SharedGroup& g) { return (g.keys + 127) / 128 - g.lo 
 FKV_DEV int items_of(const SharedParams& p, const SharedGroup& g) { return (g.members + p.tok - 1) / p.tok * p.Hkv; }  // (row tile, KV head)
 
 // One CTA; what bounds it are its round trips to L2 (all numbers of the first 256 groups and sequences in one of them).
+// With a window the shared part is what the shortest sharing member sees of the shared keys, as it sees them: what lies before its window is
+// before every member's, where the blocks may be gone, and a longer member's row may have lost blocks that it still names.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p) {
   __shared__ SharedGroup held_s[kGroupsHeld];
   __shared__ long long sum_s[3][kPlanWarps];
@@ -58,10 +60,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
   __syncthreads();
   auto context = [&](int b) { return b < kLensHeld ? lens_s[b] : context_of(p, b); };
   auto group = [&](int i) { return i < kGroupsHeld ? held_s[i] : p.groups[i]; };
+  // the group that b is in, or would be by the groups' starts alone: the last that begins at or before it (-1: none)
+  auto group_of = [&](int b) {
+    int lo = 0, hi = p.num_groups;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (group(mid).first <= b) lo = mid + 1;
+      else hi = mid;
+    }
+    return lo - 1;
+  };
   // the groups: members, shared keys (as many as the first member has); what they save, their items and steps (item, key tile)
   long long saved = 0, items = 0, steps = 0;
   int most = 0;
   bool bad = false;
+  auto counted = [&](const SharedGroup& g) {
+    if (g.keys <= 0) return;
+    const int tiles = tiles_of(g), n = items_of(p, g);
+    saved += static_cast<long long>(g.members - 1) * (g.keys - g.lo);
+    items += n;
+    steps += static_cast<long long>(n) * tiles;
+    most = max(most, tiles);
+  };
   for (int i = tid; i < p.num_groups; i += kPlanThreads) {
     SharedGroup g = {};
     const int e = i < kPlanThreads ? first_e : p.starts[i + 1];
@@ -78,15 +98,30 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
       }
       g.keys = g.members >= 2 ? min(g.keys, context(g.first)) : 0;
     }
-    if (g.keys > 0) {
-      g.lo = p.window > 0 ? max(0, g.keys - p.window) : 0;
-      const int tiles = tiles_of(g), n = items_of(p, g);
-      saved += static_cast<long long>(g.members - 1) * (g.keys - g.lo);
-      items += n;
-      steps += static_cast<long long>(n) * tiles;
-      most = max(most, tiles);
-    }
+    g.row = g.first;
+    if (p.window == 0) counted(g);
     (i < kGroupsHeld ? held_s[i] : p.groups[i]) = g;
+    if (p.window > 0) p.least[i] = ~0ull;
+  }
+  if (p.window > 0) {
+    __syncthreads();
+    for (int b = tid; b < p.B; b += kPlanThreads) {
+      const int i = group_of(b), T = context(b);
+      if (i < 0) continue;
+      const SharedGroup g = group(i);
+      if (b < g.first + g.members && g.keys > 0 && T >= g.keys) atomicMin(&p.least[i], static_cast<unsigned long long>(T) << 32 | static_cast<unsigned>(b));
+    }
+    __syncthreads();
+    for (int i = tid; i < p.num_groups; i += kPlanThreads) {
+      SharedGroup g = group(i);
+      const unsigned long long least = __ldcg(&p.least[i]);
+      const int T = static_cast<int>(least >> 32);  // (-1: no member shares)
+      g.lo = max(0, T - p.window);
+      g.row = static_cast<int>(least & 0xFFFFFFFFu);
+      if (T < 0 || g.lo >= g.keys) g.keys = 0;
+      counted(g);
+      (i < kGroupsHeld ? held_s[i] : p.groups[i]) = g;
+    }
   }
   saved = warp_sum(saved);
   items = warp_sum(items);
@@ -176,16 +211,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const SharedParams p
   if (tid == 0) *p.pieces = base_s;
   // the sequences: in which group, if it shares (a member shorter than the shared part does not)
   for (int b = tid; b < p.B; b += kPlanThreads) {
-    const int T = context(b);
-    int lo = 0, hi = share ? p.num_groups : 0;  // groups before lo begin at or before b, those from hi on behind it
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (group(mid).first <= b) lo = mid + 1;
-      else hi = mid;
-    }
+    const int T = context(b), i = share ? group_of(b) : -1;
     int4 out = make_int4(0, 0, 0, 0);
-    if (lo > 0) {
-      const SharedGroup g = group(lo - 1);
+    if (i >= 0) {
+      const SharedGroup g = group(i);
       if (b < g.first + g.members && g.keys > 0 && T >= g.keys) out = make_int4(g.keys, g.base, g.shares, b - g.first);
     }
     p.info[b] = out;
@@ -212,7 +241,7 @@ __global__ void __launch_bounds__(512, 1)
   const int at = k - g.base, item = at / g.shares, tile = item / sp.Hkv;
   Piece piece;
   piece.g = item - tile * sp.Hkv;
-  piece.table_row = g.first;
+  piece.table_row = g.row;
   piece.kv_lo = g.lo;
   piece.o = sp.piece_o + static_cast<size_t>(k) * (D / 4) * 128;
   piece.lse = sp.piece_lse + static_cast<size_t>(k) * 128;
@@ -319,6 +348,7 @@ size_t lay_out(SharedParams* p, uint8_t* base, int B, int Hq, int Hkv, int D, in
     return x;
   };
   uint8_t* groups = part(static_cast<size_t>(num_groups) * sizeof(SharedGroup));
+  uint8_t* least = part(static_cast<size_t>(num_groups) * sizeof(unsigned long long));
   uint8_t* pieces = part(sizeof(int));
   uint8_t* info = part(static_cast<size_t>(B) * sizeof(int4));
   uint8_t* units = part(static_cast<size_t>(B) * Hkv * 2 * sizeof(int2));
@@ -326,6 +356,7 @@ size_t lay_out(SharedParams* p, uint8_t* base, int B, int Hq, int Hkv, int D, in
   uint8_t* o = part(static_cast<size_t>(ctas) * 128 * D * sizeof(float));
   if (p) {
     p->groups = reinterpret_cast<SharedGroup*>(groups);
+    p->least = reinterpret_cast<unsigned long long*>(least);
     p->pieces = reinterpret_cast<int*>(pieces);
     p->info = reinterpret_cast<int4*>(info);
     p->units = reinterpret_cast<int2*>(units);

@@ -7,8 +7,9 @@ namespace fkv {
 // A group of sequences, as planned on the GPU.
 struct SharedGroup {
   int first, members;
-  int keys, lo;        // shared keys (0: it shares nothing), the first that any member may see
+  int keys, lo;        // shared keys (0: it shares nothing), the first that any sharing member sees
   int base, shares;    // place of its first piece, pieces that each (row tile, KV head)'s keys are cut into
+  int row;             // the sequence whose blocks are read
 };
 
 struct SharedParams {
@@ -23,6 +24,7 @@ struct SharedParams {
   const float *lse_part, *o_part;             // of the decode's own pieces
   // the workspace's parts
   SharedGroup* groups;
+  unsigned long long* least;                  // [num_groups] of the sharing members the shortest: context, then the sequence
   int* pieces;                                // their number
   int4* info;                                 // [B], see BlockDecodeParams::shared
   int2* units;

@@ -591,7 +591,8 @@ size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_
  * tokens that every member's row of block_table names, in the same blocks or in copies of them.  The
  * result is that of fp8_block_decode_attn for the same arguments (to rounding), but the keys and values of the
  * shared tokens are read, from the blocks that the group's first sequence names, and multiplied once for all
- * members.  What the first sequence's context does not reach is not shared, and a member whose context is shorter than the
+ * members.  With a window they are read from the blocks of the shortest member that has them all, and from where its window
+ * begins: what lies before every member's window is not looked at.  What the first sequence's context does not reach is not shared, and a member whose context is shorter than the
  * shared part is attended by itself, as are sequences outside every group, groups of one, and every group of a
  * call in which sharing would not pay for itself (few bytes saved): over their own rows of block_table.
  *

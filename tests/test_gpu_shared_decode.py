@@ -331,3 +331,43 @@ def test_wait_that_runs_out(d):
     for _ in range(2):
         assert torch.equal(call(), ref)
     assert int(fault) == 0
+
+
+def _within(got, o, mag, top):
+    """The tolerance above, against an `exact` that was taken before the case was spoiled."""
+    got = got.float().cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(got)), f"not finite: sequences {np.unique(np.nonzero(~np.isfinite(got))[0]).tolist()}"
+    assert np.all(np.abs(got - o) <= (2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -10 * top + 2.0 ** -8 * np.abs(o))
+    assert rel_l2(got, o) <= 2.0 ** -7
+
+
+@pytest.mark.parametrize("d,members", [(64, 45), (128, 28), (256, 24)])
+@pytest.mark.parametrize("longest", [0, -1])
+def test_windows_over_evicted_blocks(d, members, longest):
+    """What lies before every member's window is gone: blocks taken out of the table, their slots NaN codes.  The group's
+    first sequence is the longest one, whose row has lost blocks that others still see, or the last is."""
+    w, p = 3000, 4003
+    own = [45 + 7 * i for i in range(members)]
+    own.insert(0 if longest == 0 else members, 900)
+    c = Case([(p, own)], 16, 8, d, seed=d, fill=False)
+    exact = list(c.exact(window=w))
+    plain = f.fp8_block_decode_attn(c.q.cuda(), c.cache(), _i32(c.table), _i32(c.ctx), window=w)
+    least = min(c.ctx) - w
+    assert least % 16 and least > p - w
+    row = c.table[int(np.argmin(c.ctx))]
+    for pool in c.pools:
+        pool[row[:least // 16]] = 0x7F
+        pool[row[least // 16], :, :least % 16] = 0x7F
+    for b, t in enumerate(c.ctx):
+        c.table[b, :(t - w) // 16] = -1
+    got = c.run(window=w)
+    _within(got, *exact)
+    assert int(c.fault) == 0
+    assert not torch.equal(got, plain), "the call shares"
+
+
+@pytest.mark.parametrize("own", [[2999, 2998], [3000, 3500, 4000], [1, 3100]])
+def test_windows_that_hardly_reach_the_shared_tokens(own):
+    """Members whose windows begin at, behind or just before the end of the shared tokens, beside a group that shares."""
+    w = 3000
+    Case([(5000, own), (4000, [40 + i for i in range(30)])], 16, 8, 128, seed=len(own), fill=False).check(window=w)
