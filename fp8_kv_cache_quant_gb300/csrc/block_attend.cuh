@@ -290,7 +290,8 @@ FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, co
     // keys [lo_row, lim_row) visible
     int lim_row = (!PIECES && p.causal && row_ok) ? min(T, pos + 1) : T, lo_row = (!PIECES && WIN && row_ok) ? max(0, pos - p.window + 1) : 0;
     if constexpr (PIECES) {
-      const int ctx = row_ok ? p.ctx[r0 + q0 + it] : T;
+      // (a context beyond the table is that of the whole table, as for the keys of its own)
+      const int ctx = row_ok ? static_cast<int>(min(static_cast<long long>(p.ctx[r0 + q0 + it]), p.max_blocks * 16LL)) : T;
       if (ctx < T) lim_row = 0;
       if (WIN) lo_row = max(0, ctx - p.window);
     }

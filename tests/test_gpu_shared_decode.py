@@ -371,3 +371,17 @@ def test_windows_that_hardly_reach_the_shared_tokens(own):
     """Members whose windows begin at, behind or just before the end of the shared tokens, beside a group that shares."""
     w = 3000
     Case([(5000, own), (4000, [40 + i for i in range(30)])], 16, 8, 128, seed=len(own), fill=False).check(window=w)
+
+
+@pytest.mark.parametrize("window", [0, 3000])
+def test_a_context_beyond_the_table(window):
+    """Reported and clamped to the table, for the shared part's windows too."""
+    c = Case([(4000, [880] + [30 + 5 * i for i in range(28)])], 16, 8, 128, seed=19, fill=False)
+    assert c.ctx[0] == 16 * c.table.shape[1] == max(c.ctx)
+    exact = list(c.exact(window=window))
+    within = c.run(window=window)
+    c.ctx[0] += 700
+    got = c.run(window=window)
+    assert int(c.fault) == f.FAULT_CONTEXT
+    _within(got, *exact)
+    assert torch.equal(got, within)
