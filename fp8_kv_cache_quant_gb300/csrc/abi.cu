@@ -796,6 +796,7 @@ fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, in
   p.weights = weights;
   p.weights_len = weights_len;
   p.fault = fault;
+  p.stage_wait_ns = pipe_wait_ns();
   return from_cuda(fkv::launch_block_weights(p, cache.head_dim, workspace, current_num_sms(), reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -220,6 +220,7 @@ struct BlockWeightsParams {
   float* weights;                             // [B][Hkv][weights_len]
   int weights_len;
   int32_t* fault;
+  uint64_t stage_wait_ns;                     // bound of the copies' wait for a free stage (the others': kPipeWaitNs)
   // the workspace's parts (block_weights.cu), set by the launch
   int slots;                                  // CTAs of a launch, at most
   int32_t* done;                              // [2][slots] pieces finished of the unit that CTA k begins, in either pass

@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
       const int end = u + at.n;
       for (int x = 0; u < end; ++u, ++x) {
         const int st = u % C::NS;
-        if (abort_warp(abort_s) || (u >= C::NS && !wait_warp(&k_empty[st], (u / C::NS - 1) & 1))) { ok = false; break; }
+        if (abort_warp(abort_s) || (u >= C::NS && !wait_warp(&k_empty[st], (u / C::NS - 1) & 1, p.stage_wait_ns))) { ok = false; break; }
         int id;
         float ks;
         feed.take(p, id, ks);
@@ -1208,7 +1208,10 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const BlockWeigh
   if (s.rows == 0 || static_cast<long long>(blockIdx.x) * kGatherKeys >= s.T) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t unit = static_cast<size_t>(b) * p.Hkv + g;
-  const int2 at = p.units[unit];
+  // (a CTA whose wait ran out leaves the workspace's old bytes: the weights then are anything, the reads stay in the pieces)
+  int2 at = p.units[unit];
+  at.x = min(max(at.x, 0), p.slots - 1);
+  at.y = min(max(at.y, 1), p.slots - at.x);
   constexpr int KEYS = kGatherKeys / kGatherThreads;
   const float4* scores = reinterpret_cast<const float4*>(p.scores + unit * p.max_blocks * 16 * RN);
   float* weights = p.weights + unit * p.weights_len;

@@ -14,6 +14,7 @@ import pytest
 import torch
 
 from oracle import blockcache, longcontext
+from test_gpu_block_timeout import _runs_out
 
 f = pytest.importorskip("fp8_kv_cache_quant_gb300")
 pytestmark = pytest.mark.gpu
@@ -221,3 +222,30 @@ def test_on_another_stream():
     got = f.fp8_block_attn_weights(*args, stream=s)
     s.synchronize()
     assert np.array_equal(got.cpu().numpy().astype(np.float64), want)
+
+
+def _large_pool(sequences, tokens, d):
+    """A pool larger than the L2 cache, so that copies wait for memory: 64 x 8,000 tokens are 262 MB of keys."""
+    h, per = 512 // d, -(-tokens // 16)
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    k = torch.randint(0, 256, (sequences * per, h, 16, d), dtype=torch.uint8, device="cuda", generator=gen) & 0xBB
+    s = torch.full((sequences * per, h), 2.0 ** -5, device="cuda")
+    table = torch.randperm(sequences * per, device="cuda", generator=gen).to(torch.int32).view(sequences, per)
+    return h, f.BlockCache(k, k, s, s), table
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("g", [4, 7, 16])
+def test_wait_that_runs_out_few_rows(d, g):
+    """The copies' wait for a free stage given less time than the pipeline takes, in a workspace of any bytes: reported, and the next
+    call is sound."""
+    h, cache, table = _large_pool(64, 8000, d)
+    q = torch.randn(64, g * h, d, generator=torch.Generator().manual_seed(g)).to(torch.bfloat16).cuda()
+    lens, cu = _i32([8000 - 9 * b for b in range(64)]), _i32(range(65))
+    ws = f.attn_weights_workspace(64, 64, 1, g * h, cache, table.shape[1])
+
+    def call(fault):
+        w = torch.zeros(64, h, 8000, device="cuda")
+        ws.fill_(0x7F)
+        return f.fp8_block_attn_weights(q, cu, 1, cache, table, lens, w, decay=0.0, workspace=ws, fault=fault)
+    _runs_out(call)
