@@ -730,7 +730,7 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     bool ok = true;
     while (ok && at.n > 0) {
       const int yb = at.piece % C::NY;
-      if (at.piece >= C::NY && !wait_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1)) { ok = false; break; }
+      if (at.piece >= C::NY && !wait_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1, p.stage_wait_ns)) { ok = false; break; }
       size_t tile = tile_index(p, at.r0, at.b, at.g, K == kRows ? at.t : at.first() + at.s);
       if constexpr (K == kRows) {
         if (lane == 0) {
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
       for (int x = 0; u < end; ++u, ++x, tile += p.Hkv) {
         if (abort_warp(abort_s)) { ok = false; break; }
         const int st = u % C::NS;
-        if (u >= C::NS && !wait_warp(&x_empty[st], (u / C::NS - 1) & 1)) { ok = false; break; }
+        if (u >= C::NS && !wait_warp(&x_empty[st], (u / C::NS - 1) & 1, p.stage_wait_ns)) { ok = false; break; }
         uint8_t* dst = sStream + st * C::STREAM;
         if constexpr (K == kRows) {
           copy_keys(dst, &x_full[st], at.s + x, u);

@@ -249,3 +249,20 @@ def test_wait_that_runs_out_few_rows(d, g):
         ws.fill_(0x7F)
         return f.fp8_block_attn_weights(q, cu, 1, cache, table, lens, w, decay=0.0, workspace=ws, fault=fault)
     _runs_out(call)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sequences,tokens,g,new", [(4, 3000, 16, 160), (64, 8000, 7, 33), (1024, 100, 2, 9)])
+def test_wait_that_runs_out_many_rows(d, sequences, tokens, g, new):
+    """The same for the two passes over many rows: row tiles that stream past the keys, long contexts, and many short ones, whose
+    pieces follow one another faster than their tiles are done with (either pass stops there)."""
+    h, cache, table = _large_pool(sequences, tokens, d)
+    q = torch.randn(sequences * new, g * h, d, generator=torch.Generator().manual_seed(g)).to(torch.bfloat16).cuda()
+    lens, cu = _i32([tokens] * sequences), _i32(np.arange(sequences + 1) * new)
+    ws = f.attn_weights_workspace(sequences, sequences * new, new, g * h, cache, table.shape[1])
+
+    def call(fault):
+        w = torch.zeros(sequences, h, tokens, device="cuda")
+        ws.fill_(0x7F)
+        return f.fp8_block_attn_weights(q, cu, new, cache, table, lens, w, decay=0.0, workspace=ws, fault=fault)
+    _runs_out(call)
