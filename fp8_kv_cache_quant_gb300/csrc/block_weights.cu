@@ -34,14 +34,17 @@ namespace {
 
 constexpr float kHuge = 3e38f;  // minus this: the maximum of no scores
 
-// Sequence b's rows and keys; rows 0: nothing to do.
+// Sequence b's rows and keys; rows 0: nothing to do.  back: the starts decrease behind it.
 struct WeightsSeq {
   int r0, rows, T;
+  bool back;
+  FKV_DEV int end() const { return rows > 0 ? r0 + rows : 0; }
 };
 FKV_DEV WeightsSeq weights_seq(const BlockWeightsParams& p, int b, bool report) {
   WeightsSeq s;
   s.r0 = p.cu[b];
   s.rows = p.cu[b + 1] - s.r0;
+  s.back = s.rows < 0;
   s.T = p.ctx[b];
   const long long most = min(p.max_blocks * 16LL, static_cast<long long>(p.weights_len));
   if (s.T < 0 || s.T > most) {
@@ -62,6 +65,8 @@ FKV_DEV WeightsSeq weights_seq(const BlockWeightsParams& p, int b, bool report) 
 enum Kind { kRows, kKeys, kScores };
 
 // A piece: the steps of a unit that a CTA takes.  (Rows and keys of a sequence are below 2^31, rows times G at most 2^30.)
+// The row tiles have their places in the workspace by the sequences' first rows (tile_index).  Where the starts decrease, a sequence
+// whose rows do not lie behind those of all earlier ones would share places with them, and is left out (kRows, kKeys).
 template <Kind K, int KT>
 struct Walk {
   int G;
@@ -70,6 +75,7 @@ struct Walk {
   int s, n, count;        // steps s .. s + n - 1 of its count; n 0: behind the range
   int left;               // steps of the range behind this piece
   int piece;              // pieces before this one
+  int top;                // the rows of sequences up to this one end at or before it (0 where the starts do not decrease)
   long long unit0;        // the place of the unit's first step
 
   FKV_DEV void set(const WeightsSeq& q) {
@@ -98,8 +104,15 @@ struct Walk {
       t = 0;
       if (++g == p.Hkv) {
         g = 0;
-        do set(weights_seq(p, ++b, false));
-        while (of == 0);
+        do {
+          WeightsSeq q = weights_seq(p, ++b, false);
+          if constexpr (K != kScores) {
+            const int end = q.end();
+            if (q.r0 < top) q.rows = 0;
+            top = max(top, end);
+          }
+          set(q);
+        } while (of == 0);
       }
     }
     count = steps(t);
@@ -115,9 +128,9 @@ FKV_DEV Walk<K, KT> first_piece(const BlockWeightsParams& p, int k, long long& W
   const int lane = threadIdx.x & 31;
   Walk<K, KT> a;
   a.G = p.Hq / p.Hkv;
-  a.b = a.g = a.t = a.s = a.n = a.count = a.left = a.piece = 0;
+  a.b = a.g = a.t = a.s = a.n = a.count = a.left = a.piece = a.top = 0;
   a.unit0 = 0;
-  a.set(WeightsSeq{0, 0, 0});
+  a.set(WeightsSeq{0, 0, 0, false});
   auto sum = [](long long x) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
@@ -133,9 +146,9 @@ FKV_DEV Walk<K, KT> first_piece(const BlockWeightsParams& p, int k, long long& W
   };
   // a sequence's steps for one KV head: by one lane where it has few units, by all of them where it may have many
   const bool by_lane = K != kRows || p.max_q_len * static_cast<long long>(a.G) <= 512;
-  auto steps_of = [&](int b, bool rep) -> long long {
+  auto steps_of = [&](const WeightsSeq& q) -> long long {
     Walk<K, KT> c = a;
-    c.set(weights_seq(p, b, rep));
+    c.set(q);
     if (c.of == 0) return 0;
     if constexpr (K == kScores) {
       return c.steps(0);
@@ -152,13 +165,46 @@ FKV_DEV Walk<K, KT> first_piece(const BlockWeightsParams& p, int k, long long& W
     }
   };
   const int db = by_lane ? 32 : 1;
-  auto of_lane = [&](int b0, bool rep) -> long long {
+  auto seq_at = [&](int b0, bool rep) {
     const int b = by_lane ? b0 + lane : b0;
-    return b < p.B ? steps_of(b, rep && (by_lane || lane == 0)) : 0;
+    return b < p.B ? weights_seq(p, b, rep && (by_lane || lane == 0)) : WeightsSeq{0, 0, 0, false};
   };
-  const long long first32 = of_lane(0, report);
-  W = by_lane ? sum(first32) : first32;
-  for (int b0 = db; b0 < p.B; b0 += db) W += by_lane ? sum(of_lane(b0, report)) : of_lane(b0, report);
+  // where the starts decrease: the sequence left out if it does not lie behind those before it, whose rows end at top
+  bool back = false;
+  int top = 0;
+  auto check = [&](WeightsSeq& q) {  // returns where the rows up to this lane's sequence end
+    if (!by_lane) {
+      const int end = q.end();
+      if (q.r0 < top) q.rows = 0;
+      return top = max(top, end);
+    }
+    int end = max(top, q.end());
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, end, off);
+      if (lane >= off) end = max(end, y);
+    }
+    const int before = __shfl_up_sync(0xffffffffu, end, 1);
+    if (q.r0 < (lane > 0 ? before : top)) q.rows = 0;
+    top = __shfl_sync(0xffffffffu, end, 31);
+    return end;
+  };
+  long long first32 = 0;
+#pragma unroll 1
+  for (int go = 0; go < 2; ++go) {
+    bool decrease = false;
+    W = 0;
+    for (int b0 = 0; b0 < p.B; b0 += db) {
+      WeightsSeq q = seq_at(b0, report && go == 0);
+      decrease = decrease || q.back;
+      if (back) check(q);
+      const long long x = steps_of(q);
+      if (b0 == 0) first32 = x;
+      W += by_lane ? sum(x) : x;
+    }
+    if (K == kScores || go > 0 || !__any_sync(0xffffffffu, decrease)) break;
+    back = true;
+  }
   W *= p.Hkv;
   N = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
   if (k >= N) return a;
@@ -166,12 +212,21 @@ FKV_DEV Walk<K, KT> first_piece(const BlockWeightsParams& p, int k, long long& W
   const long long w0 = small ? static_cast<uint32_t>(W) * k / static_cast<uint32_t>(N) : W * k / N;
   const long long w1 = small ? static_cast<uint32_t>(W) * (k + 1) / static_cast<uint32_t>(N) : W * (k + 1) / N;
   long long base = 0, mine = 0;  // places before sequence b, and one KV head's of it
+  top = 0;
   for (int b0 = 0;; b0 += db) {
-    const long long x = b0 == 0 ? first32 : of_lane(b0, false), y = by_lane ? upto(x) : x;
+    long long x = first32;
+    int end = 0;
+    if (back || b0 > 0) {
+      WeightsSeq q = seq_at(b0, false);
+      if (back) end = check(q);
+      x = steps_of(q);
+    }
+    const long long y = by_lane ? upto(x) : x;
     const unsigned past = __ballot_sync(0xffffffffu, base + y * p.Hkv > w0);
     if (past != 0) {
       const int j = by_lane ? __ffs(past) - 1 : 0;
       a.b = b0 + j;
+      a.top = __shfl_sync(0xffffffffu, end, j);
       mine = __shfl_sync(0xffffffffu, x, j);
       base += (__shfl_sync(0xffffffffu, y, j) - mine) * p.Hkv;
       break;
@@ -327,19 +382,26 @@ __global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) 
   const int tile = blockIdx.x / 8, row0 = (blockIdx.x & 7) * 16;
   if (blockIdx.x == 0 && g == 0)
     for (int i = threadIdx.x; i < 2 * p.slots; i += 128) p.done[i] = 0;
-  // the last sequence whose tiles begin at or before this one
+  // the first sequence that has this tile
+  WeightsSeq s = {0, 0, 0, false};
   int b = -1;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const bool before = b0 + lane < p.B && static_cast<long long>(p.cu[b0 + lane]) * G / 128 + b0 + lane <= tile;
-    const unsigned m = __ballot_sync(0xffffffffu, before);
-    if (m == 0) break;
-    b = b0 + 31 - __clz(m);
+    if (b0 + lane < p.B) s = weights_seq(p, b0 + lane, false);
+    else s.rows = 0;
+    const long long i = tile - (static_cast<long long>(s.r0) * G / 128 + b0 + lane);
+    const unsigned has = __ballot_sync(0xffffffffu, i >= 0 && i * 128 < static_cast<long long>(s.rows) * G);
+    if (has != 0) {
+      const int j = __ffs(has) - 1;
+      b = b0 + j;
+      s.r0 = __shfl_sync(0xffffffffu, s.r0, j);
+      s.rows = __shfl_sync(0xffffffffu, s.rows, j);
+      break;
+    }
+    if (__any_sync(0xffffffffu, s.rows > 0 && i < 0)) break;  // (those behind it that are not left out begin behind it)
   }
   if (b < 0) return;
-  const WeightsSeq s = weights_seq(p, b, false);
   const long long R = static_cast<long long>(s.rows) * G;
   const long long i = tile - (static_cast<long long>(s.r0) * G / 128 + b);
-  if (i < 0 || i * 128 >= R) return;
   const int row = row0 + (threadIdx.x >> 3);
   const long long r = i * 128 + row;
   constexpr int NCH = (D / 16 + 7) / 8;  // 16-element chunks of a row per thread

@@ -641,7 +641,8 @@ size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int
  *   workspace     device, >= fp8_block_attn_weights_workspace_size(...) bytes, 256-byte aligned, any contents; calls that may
  *                 overlap on the GPU each need their own
  * A sequence with Lq_b < 0, > max_q_len, > T_b or rows outside [0, total_q) is skipped and FKV_FAULT_QLEN
- * raised; T_b outside [0, min(16 max_blocks, weights_len)] is clamped (FKV_FAULT_CONTEXT); a block id out of
+ * raised (where Lq_b < 0 lets later rows begin before those of an earlier sequence end, the later sequence may be
+ * skipped too); T_b outside [0, min(16 max_blocks, weights_len)] is clamped (FKV_FAULT_CONTEXT); a block id out of
  * range reads block 0 (FKV_FAULT_BLOCK_ID).
  */
 fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, int32_t total_q, int32_t batch,

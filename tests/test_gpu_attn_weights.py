@@ -266,3 +266,33 @@ def test_wait_that_runs_out_many_rows(d, sequences, tokens, g, new):
         ws.fill_(0x7F)
         return f.fp8_block_attn_weights(q, cu, new, cache, table, lens, w, decay=0.0, workspace=ws, fault=fault)
     _runs_out(call)
+
+
+@pytest.mark.parametrize("cu", [[0, 200, 50, 100], [100, 200, 50, 100], [0, 1000, 150, 200], [0, 130, 20, 200]])
+def test_starts_that_decrease(cu):
+    """A sequence's weights do not depend on what a bad one does to the starts behind it: whose rows lie behind those of all earlier
+    sequences (of those that are sound by themselves) get their weights, the others keep what was there."""
+    c = Case([300, 260, 400], [200, 0, 0], 16, 4, 64, seed=20)
+    c.cu, rows = cu, [(cu[b], cu[b + 1] - cu[b]) for b in range(3)]
+    got = c.run(0.0)
+    assert int(c.fault) == f.FAULT_QLEN
+    end = 0
+    for b, (r, n) in enumerate(rows):
+        sound = 0 < n <= 200 and r + n <= 200 and n <= c.ctx[b]
+        if sound and r >= end:
+            want = longcontext.softmax_weights(c.q[r:r + n].float().numpy().astype(np.float64), c.k, c.k_scale, c.table[b:b + 1], c.ctx[b:b + 1], [0, n])[0]
+            assert np.linalg.norm(got[b, :, :c.ctx[b]] - want) <= 2.0 ** -16 * np.linalg.norm(want), f"sequence {b}"
+        else:
+            assert np.array_equal(got[b], c.before[b].astype(np.float64)), f"sequence {b}"
+        end = max(end, r + n) if sound else end
+
+
+@pytest.mark.parametrize("cu,max_q", [([0, 3, 1, 2], 3)])
+def test_starts_that_decrease_few_rows(cu, max_q):
+    c = Case([300, 260, 400], [3, 0, 0], 16, 4, 64, seed=21)
+    c.cu = cu
+    got = c.run(0.0)
+    assert int(c.fault) == f.FAULT_QLEN
+    want = longcontext.softmax_weights(c.q[:3].float().numpy().astype(np.float64), c.k, c.k_scale, c.table[:1], c.ctx[:1], [0, 3])[0]
+    assert np.linalg.norm(got[0, :, :300] - want) <= 2.0 ** -16 * np.linalg.norm(want)
+    assert np.array_equal(got[1], c.before[1].astype(np.float64))
