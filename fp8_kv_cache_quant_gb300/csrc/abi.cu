@@ -770,7 +770,8 @@ fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, in
   if (batch > 65535 || num_q_heads > 65535 || max_blocks > kMaxTableBlocks) return FKV_UNSUPPORTED;
   if (static_cast<long long>(total_q) * (num_q_heads / cache.num_kv_heads) > kMaxWeightRows) return FKV_UNSUPPORTED;
   if (total_q == 0 || batch == 0 || max_q_len == 0) return FKV_OK;
-  if (!q || !cu_seqlens_q || !block_table || !context_lens || !weights || !valid_block_pools(cache)) return FKV_INVALID_ARG;
+  if (!q || !cu_seqlens_q || !block_table || !context_lens || (!weights && weights_len > 0) || !valid_block_pools(cache))
+    return FKV_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(block_table, 4) || !aligned(context_lens, 4) || !aligned(cu_seqlens_q, 4) || !aligned(weights, 4))
     return FKV_INVALID_ARG;
   const size_t need = fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, cache.num_kv_heads,
@@ -815,7 +816,7 @@ fkv_status kv_block_evict(fkv_block_cache cache, const int32_t* block_table, int
   if (static_cast<long long>(batch) * cache.num_kv_heads * ((most + 15) / 16 + 8) > INT32_MAX) return FKV_UNSUPPORTED;
   if (batch == 0) return FKV_OK;
   if (!valid_block_pools(cache)) return FKV_INVALID_ARG;
-  if (!block_table || !context_lens || !weights || !new_table || !new_lens || !kept || !aligned(block_table, 4) ||
+  if (!block_table || !context_lens || (!weights && weights_len > 0) || (!new_table && new_max_blocks > 0) || !new_lens || !kept || !aligned(block_table, 4) ||
       !aligned(context_lens, 4) || !aligned(weights, 4) || !aligned(new_table, 4) || !aligned(new_lens, 4) ||
       !aligned(kept, 4) || !aligned(new_weights, 4))
     return FKV_INVALID_ARG;

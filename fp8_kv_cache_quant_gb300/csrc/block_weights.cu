@@ -1384,6 +1384,7 @@ cudaError_t launch_few(const BlockWeightsParams& p, const CUtensorMap& tmk, int 
   const cudaError_t e = launch_tc(score_kernel<D, RN>, C::CTAS * num_sms, kScoreThreads, C::SMEM, p, tmk, s);
   if (e != cudaSuccess) return e;
   const long long keys = std::min(p.max_blocks * 16LL, static_cast<long long>(p.weights_len));
+  if (keys == 0) return cudaSuccess;  // (no weights: the sequences were reported)
   return launch_dependent(gather_kernel<RN>, dim3(static_cast<unsigned>((keys + kGatherKeys - 1) / kGatherKeys), p.Hkv, p.B), dim3(kGatherThreads),
                           0, s, p);
 }

@@ -637,7 +637,7 @@ size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int
  *   block_table, max_blocks, context_lens, softmax_scale  as for fp8_block_prefill_attn
  *   decay         finite; 1 adds up, 0 begins anew
  *   weights       device float32 [batch][num_kv_heads][weights_len]; entries behind a sequence, and those of a
- *                 sequence without queries, keep their values
+ *                 sequence without queries, keep their values.  NULL where weights_len is 0
  *   workspace     device, >= fp8_block_attn_weights_workspace_size(...) bytes, 256-byte aligned, any contents; calls that may
  *                 overlap on the GPU each need their own
  * A sequence with Lq_b < 0, > max_q_len, > T_b or rows outside [0, total_q) is skipped and FKV_FAULT_QLEN
@@ -668,9 +668,9 @@ fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, in
  *                 Sequences may share source blocks
  *   block_table, max_blocks, context_lens  the sequences as they are
  *   weights       device float32 [batch][num_kv_heads][weights_len], token t's at [b][g][t] (as
- *                 fp8_block_attn_weights writes them)
+ *                 fp8_block_attn_weights writes them).  NULL where weights_len is 0
  *   budget        >= 1; sink, recent >= 0, sink + recent <= budget
- *   new_table     device int32 [batch][new_max_blocks]
+ *   new_table     device int32 [batch][new_max_blocks].  NULL where new_max_blocks is 0
  *   new_lens      device int32 [batch], written: n_b
  *   kept          device int32 [batch][num_kv_heads][budget], written: the kept tokens' old indices, ascending, then -1
  *   new_weights   device float32 [batch][num_kv_heads][new_weights_len] or NULL: the kept tokens'

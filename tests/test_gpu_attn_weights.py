@@ -296,3 +296,12 @@ def test_starts_that_decrease_few_rows(cu, max_q):
     want = longcontext.softmax_weights(c.q[:3].float().numpy().astype(np.float64), c.k, c.k_scale, c.table[:1], c.ctx[:1], [0, 3])[0]
     assert np.linalg.norm(got[0, :, :300] - want) <= 2.0 ** -16 * np.linalg.norm(want)
     assert np.array_equal(got[1], c.before[1].astype(np.float64))
+
+
+@pytest.mark.parametrize("new", [[1, 1], [40, 20]])
+def test_weights_of_no_tokens(new):
+    """weights_len 0: every context is clamped to 0, and a query without keys is skipped."""
+    c = Case([100, 60], new, 4, 2, 64, seed=22)
+    c.before = c.before[:, :, :0]
+    c.run(1.0)
+    assert int(c.fault) == f.FAULT_CONTEXT | f.FAULT_QLEN

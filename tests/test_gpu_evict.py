@@ -161,3 +161,13 @@ def test_evict_on_another_stream():
     s.synchronize()
     want = longcontext.kept_tokens(c.weights[0, 1], 3000, 128, 4, 16)
     assert np.array_equal(kept[0, 1].cpu().numpy(), want)
+
+
+def test_evict_without_weights_keeps_nothing():
+    """weights_len 0: every context is clamped to 0."""
+    c = Case([60, 40], 20, 0, 0, 2, 64, seed=13)
+    c.weights, c.new_table = c.weights[:, :, :0], c.new_table[:, :0]
+    lens, kept = c.run()
+    assert int(c.fault) == f.FAULT_CONTEXT
+    assert lens.tolist() == [0, 0] and bool((kept == -1).all())
+    assert np.array_equal(c.cache.k_cache.cpu().numpy(), c.pools[0]) and np.array_equal(c.cache.v_scale.cpu().numpy(), c.scales[1])

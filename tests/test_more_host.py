@@ -252,3 +252,10 @@ def test_compiled_binding_checks_of_shared(lib):
             b.fp8_block_shared_decode_attn(0, *dict(a, **change).values())
     with pytest.raises(ValueError, match="not on a CUDA device"):
         f.fp8_block_shared_decode_attn(a["q"], f.BlockCache(pool, pool, sc, sc), tab, i32, i32, i32[:2])
+
+
+def test_no_weights_at_all(lib):
+    """Null where there are none: refused for another reason only."""
+    assert _weights(lib, w=None, wl=0, ws=None) == f.INVALID_ARG and _weights(lib, w=None, wl=0, b=0) == f.OK
+    assert _weights(lib, w=None, wl=1) == f.INVALID_ARG
+    assert _evict(lib, w=None, wl=1) == f.INVALID_ARG and _evict(lib, nt=None, nmb=1, wl=16) == f.INVALID_ARG
