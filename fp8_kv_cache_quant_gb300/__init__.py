@@ -379,14 +379,22 @@ class Rope:
     interleaved: bool = False
     axes: Optional[Sequence[int]] = None
 
-    def __post_init__(self):
-        self.pair_axis, self.pair_args = None, (None, 0)   # bytes kept alive here, and what the calls take
-        if self.axes is not None:
-            x = np.asarray(self.axes)
-            if x.ndim != 1 or 2 * x.size != self.cos_sin.shape[1] or x.dtype.kind not in "iu" or x.min() < 0 or x.max() > 3:
-                raise ValueError(f"Rope: axes names an axis from 0 to 3 for each of the {self.cos_sin.shape[1] // 2} pairs")
-            self.pair_axis = np.ascontiguousarray(x, np.uint8)
-            self.pair_args = (self.pair_axis.ctypes.data, self.pair_axis.size)
+    def __setattr__(self, name, value):
+        if name == "axes":
+            pairs = None            # the axes as the calls take them, one byte a pair
+            if value is not None:
+                x = np.asarray(value)
+                if x.ndim != 1 or 2 * x.size != self.cos_sin.shape[1] or x.dtype.kind not in "iu" or x.min() < 0 or x.max() > 3:
+                    raise ValueError(f"Rope: axes names an axis from 0 to 3 for each of the {self.cos_sin.shape[1] // 2} pairs")
+                pairs = np.ascontiguousarray(x, np.uint8)
+                value = tuple(x.tolist())   # (changed by assigning others)
+            object.__setattr__(self, "pair_axis", pairs)
+        object.__setattr__(self, name, value)
+
+    @property
+    def pair_args(self):
+        """The address of pair_axis' bytes, this rope's own (a copy has others), and their number."""
+        return (None, 0) if self.pair_axis is None else (self.pair_axis.ctypes.data, self.pair_axis.size)
 
     @staticmethod
     def sections(*pairs):

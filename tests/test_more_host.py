@@ -1,6 +1,7 @@
 """What the operators for long and shared contexts refuse on the host (no GPU needed): the C entry points before
 anything is enqueued, and the binding."""
 import ctypes
+import dataclasses
 import os
 
 import numpy as np
@@ -259,3 +260,33 @@ def test_no_weights_at_all(lib):
     assert _weights(lib, w=None, wl=0, ws=None) == f.INVALID_ARG and _weights(lib, w=None, wl=0, b=0) == f.OK
     assert _weights(lib, w=None, wl=1) == f.INVALID_ARG
     assert _evict(lib, w=None, wl=1) == f.INVALID_ARG and _evict(lib, nt=None, nmb=1, wl=16) == f.INVALID_ARG
+
+
+def test_copies_of_a_rope_with_axes():
+    """The library reads a copy's axes from the copy's own memory, also in another process and behind the original."""
+    import copy
+    import pickle
+    axes = f.Rope.sections(12, 10, 10)
+    r = f.Rope(torch.zeros(9, 64), axes=axes)
+    for make in (copy.deepcopy, copy.copy, lambda x: pickle.loads(pickle.dumps(x)), lambda x: dataclasses.replace(x, interleaved=True)):
+        c = make(f.Rope(r.cos_sin, axes=axes))      # (the original is gone)
+        at, n = c.pair_args
+        assert at == c.pair_axis.ctypes.data and n == 32
+        assert list((ctypes.c_uint8 * n).from_address(at)) == axes == list(c.axes)
+
+
+def test_axes_assigned_later():
+    r = f.Rope(torch.zeros(9, 64))
+    assert r.pair_args == (None, 0)
+    r.axes = [0, 1] * 16
+    at, n = r.pair_args
+    assert list((ctypes.c_uint8 * n).from_address(at)) == [0, 1] * 16
+    with pytest.raises(ValueError, match="axes names"):
+        r.axes = [0] * 31
+    assert r.pair_axis.tolist() == list(r.axes) == [0, 1] * 16
+    r.axes = None
+    assert r.pair_axis is None and r.pair_args == (None, 0)
+    given = [2] * 32
+    r.axes = given
+    given[0] = 0
+    assert list(r.axes) == [2] * 32 == r.pair_axis.tolist()
