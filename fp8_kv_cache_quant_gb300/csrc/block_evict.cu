@@ -102,11 +102,12 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
   const float* weights = p.weights + static_cast<size_t>(unit) * p.weights_len;
   float* moved = p.new_weights ? p.new_weights + static_cast<size_t>(unit) * p.new_weights_len : nullptr;
   const int all = C * kSelectThreads, me = rank * kSelectThreads + tid;
-  for (int i = n + me; i < p.budget; i += all) kept[i] = -1;
+  // (budgets and contexts go up to 2^31 - 1 and 2^31 - 1024: a step of all threads behind them passes 32 bits)
+  for (long long i = n + static_cast<long long>(me); i < p.budget; i += all) kept[i] = -1;
   if (T <= p.budget) {  // (the whole cluster)
     if (C > 1) wait_cluster();
-    for (int i = me; i < n; i += all) {
-      kept[i] = i;
+    for (long long i = me; i < n; i += all) {
+      kept[i] = static_cast<int>(i);
       if (moved) moved[i] = weights[i];
     }
     return;
@@ -117,17 +118,15 @@ __global__ void __launch_bounds__(kSelectThreads, 1) evict_select_kernel(const E
   const bool resident = seg <= resident_keys;
   auto key_of_token = [&](int i, float w) -> uint32_t { return i < p.sink || i >= T - p.recent ? kSure : key_of(w); };
   __syncthreads();
-  for (int i0 = lo + tid; i0 < hi; i0 += kLoads * kSelectThreads) {
+  for (int left0 = hi - lo - tid; left0 > 0; left0 -= kLoads * kSelectThreads) {  // (keys from this thread's next on)
+    const int i0 = hi - left0;
     float w[kLoads];
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const int i = i0 + j * kSelectThreads;
-      w[j] = i < hi ? weights[i] : 0.f;
-    }
+    for (int j = 0; j < kLoads; ++j) w[j] = j * kSelectThreads < left0 ? weights[i0 + j * kSelectThreads] : 0.f;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
+      if (j * kSelectThreads >= left0) break;
       const int i = i0 + j * kSelectThreads;
-      if (i >= hi) break;
       const uint32_t k = key_of_token(i, w[j]);
       if (resident) held[i - lo] = k;
       atomicAdd(&sh.hist[0][k >> 21], 1);

@@ -171,3 +171,39 @@ def test_evict_without_weights_keeps_nothing():
     assert int(c.fault) == f.FAULT_CONTEXT
     assert lens.tolist() == [0, 0] and bool((kept == -1).all())
     assert np.array_equal(c.cache.k_cache.cpu().numpy(), c.pools[0]) and np.array_equal(c.cache.v_scale.cpu().numpy(), c.scales[1])
+
+
+def _counting(tokens, columns):
+    """One sequence of one head over a pool of two blocks, which its whole table names in turn."""
+    pool = torch.arange(16, dtype=torch.uint8, device="cuda")[None, None, :, None].expand(8, 1, 16, 64).contiguous()
+    cache = f.BlockCache(pool.clone(), pool.clone(), torch.ones(8, 1, device="cuda"), torch.ones(8, 1, device="cuda"))
+    table = (torch.arange(columns, device="cuda") % 2).to(torch.int32)[None]
+    return cache, table, torch.tensor([tokens], dtype=torch.int32, device="cuda")
+
+
+def _tokens(cache, block):
+    """What the block's tokens hold (a kept value moves to a new scale)."""
+    return (cache.k_cache[block, 0, :, 0].view(torch.float8_e4m3fn).float() * cache.k_scale[block, 0]).tolist()
+
+
+def test_evict_the_largest_budget():
+    """A budget without a limit, whose last entries' indices a step of all threads carries beyond 32 bits."""
+    cache, table, ctx = _counting(40, 3)
+    new = torch.tensor([[2, 3, 4]], dtype=torch.int32, device="cuda")
+    lens, kept = f.kv_block_evict(cache, table, ctx, torch.zeros(1, 1, 48, device="cuda"), 2 ** 31 - 1, new)
+    assert lens.tolist() == [40] and kept.shape[2] == 2 ** 31 - 1
+    assert kept[0, 0, :40].tolist() == list(range(40))
+    assert all(int(x.max()) == -1 == int(x.min()) for x in kept[0, 0, 40:].split(1 << 28))
+    assert _tokens(cache, 2) == _tokens(cache, 0) == _tokens(cache, 3) and _tokens(cache, 4)[:8] == _tokens(cache, 0)[:8]
+
+
+def test_evict_the_longest_context():
+    """As many tokens as a table can name, most of them of equal weight."""
+    columns = (1 << 27) - 64
+    tokens = 16 * columns
+    cache, table, ctx = _counting(tokens, columns)
+    weights = torch.zeros(1, 1, tokens, device="cuda")
+    weights[0, 0, [5, 2 ** 30 + 7, tokens - 1]] = torch.tensor([1.0, 3.0, 2.0], device="cuda")
+    lens, kept = f.kv_block_evict(cache, table, ctx, weights, 16, torch.tensor([[2]], dtype=torch.int32, device="cuda"))
+    assert lens.tolist() == [16] and kept[0, 0].tolist() == [*range(14), 2 ** 30 + 7, tokens - 1]
+    assert _tokens(cache, 2) == [_tokens(cache, 0)[x % 16] for x in kept[0, 0].tolist()]
