@@ -14,6 +14,12 @@ using fkv::DecodeParams;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether arrays of that many 4-byte elements have one in common.
+bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * bn && y < x + 4 * an;
+}
+
 int current_num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -819,6 +825,11 @@ fkv_status kv_block_evict(fkv_block_cache cache, const int32_t* block_table, int
   if (!block_table || !context_lens || (!weights && weights_len > 0) || (!new_table && new_max_blocks > 0) || !new_lens || !kept || !aligned(block_table, 4) ||
       !aligned(context_lens, 4) || !aligned(weights, 4) || !aligned(new_table, 4) || !aligned(new_lens, 4) ||
       !aligned(kept, 4) || !aligned(new_weights, 4))
+    return FKV_INVALID_ARG;
+  // a sequence's heads read its length, and their weights, in any order
+  const uint64_t units = static_cast<uint64_t>(batch) * cache.num_kv_heads;
+  if (overlap(new_lens, batch, context_lens, batch) ||
+      (new_weights && overlap(new_weights, units * new_weights_len, weights, units * weights_len)))
     return FKV_INVALID_ARG;
   fkv::EvictParams p;
   std::memset(&p, 0, sizeof(p));

@@ -671,10 +671,10 @@ fkv_status fp8_block_attn_weights(const void* q, const int32_t* cu_seqlens_q, in
  *                 fp8_block_attn_weights writes them).  NULL where weights_len is 0
  *   budget        >= 1; sink, recent >= 0, sink + recent <= budget
  *   new_table     device int32 [batch][new_max_blocks].  NULL where new_max_blocks is 0
- *   new_lens      device int32 [batch], written: n_b
+ *   new_lens      device int32 [batch], written: n_b; it must not overlap context_lens (FKV_INVALID_ARG)
  *   kept          device int32 [batch][num_kv_heads][budget], written: the kept tokens' old indices, ascending, then -1
  *   new_weights   device float32 [batch][num_kv_heads][new_weights_len] or NULL: the kept tokens'
- *                 weights are written to it, the rest keeps its values; it must not overlap weights
+ *                 weights are written to it, the rest keeps its values; it must not overlap weights (FKV_INVALID_ARG)
  * min(budget, 16 max_blocks, weights_len) must be at most 16 new_max_blocks and new_weights_len.  T_b outside
  * [0, min(16 max_blocks, weights_len)] is clamped (FKV_FAULT_CONTEXT); a source block id out of range reads
  * block 0, a target id out of range skips the block (FKV_FAULT_BLOCK_ID).  Slots behind n_b keep their bytes.

@@ -207,3 +207,17 @@ def test_evict_the_longest_context():
     lens, kept = f.kv_block_evict(cache, table, ctx, weights, 16, torch.tensor([[2]], dtype=torch.int32, device="cuda"))
     assert lens.tolist() == [16] and kept[0, 0].tolist() == [*range(14), 2 ** 30 + 7, tokens - 1]
     assert _tokens(cache, 2) == [_tokens(cache, 0)[x % 16] for x in kept[0, 0].tolist()]
+
+
+def test_evict_results_beside_its_input():
+    """Lengths and weights right behind the input's in one allocation."""
+    pool, sc = torch.zeros(9, 1, 16, 64, dtype=torch.uint8, device="cuda"), torch.ones(9, 1, device="cuda")
+    lens, w = torch.tensor([40, 40, 0, 0], dtype=torch.int32, device="cuda"), torch.arange(2 * 48 + 2 * 20, device="cuda").float()
+    tab = torch.tensor([[0, 1, 2], [1, 2, 0]], dtype=torch.int32, device="cuda")
+    new = torch.tensor([[3, 4], [5, 6]], dtype=torch.int32, device="cuda")
+    moved = w[96:].view(2, 1, 20)
+    got, kept = f.kv_block_evict(f.BlockCache(pool, pool, sc, sc), tab, lens[:2], w[:96].view(2, 1, 48), 20, new, new_weights=moved, new_lens=lens[2:])
+    assert lens.tolist() == [40, 40, 20, 20] and kept[1, 0].tolist() == list(range(20, 40))
+    assert moved[1, 0].tolist() == list(range(48 + 20, 48 + 40))
+    with pytest.raises(f.FkvError):
+        f.kv_block_evict(f.BlockCache(pool, pool, sc, sc), tab, lens[:2], w[:96].view(2, 1, 48), 20, new, new_lens=lens[:2])

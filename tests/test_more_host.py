@@ -290,3 +290,14 @@ def test_axes_assigned_later():
     r.axes = given
     given[0] = 0
     assert list(r.axes) == [2] * 32 == r.pair_axis.tolist()
+
+
+def test_evict_results_over_its_own_input(lib):
+    """New lengths over the lengths, moved weights over the weights: heads read them at any time."""
+    far = 1 << 30
+    ok = dict(ctx=P, nl=P + far, w=P + 2 * far, nw=P + 3 * far, kept=P + 4 * far)
+    refused = [dict(nl=P), dict(nl=P + 4), dict(nl=P - 4), dict(nw=P + 2 * far), dict(nw=P + 2 * far + 4 * (2 * 2 * 128 - 1)),
+               dict(nw=P + 2 * far - 4 * (2 * 2 * 32 - 1))]
+    for kw in refused:
+        assert _evict(lib, **{**ok, **kw}) == f.INVALID_ARG
+    assert _evict(lib, **{**ok, "b": 0}) == f.OK
