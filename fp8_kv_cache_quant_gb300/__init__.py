@@ -381,20 +381,26 @@ class Rope:
 
     def __setattr__(self, name, value):
         if name == "axes":
-            pairs = None            # the axes as the calls take them, one byte a pair
+            pairs = None
             if value is not None:
                 x = np.asarray(value)
                 if x.ndim != 1 or 2 * x.size != self.cos_sin.shape[1] or x.dtype.kind not in "iu" or x.min() < 0 or x.max() > 3:
                     raise ValueError(f"Rope: axes names an axis from 0 to 3 for each of the {self.cos_sin.shape[1] // 2} pairs")
                 pairs = np.ascontiguousarray(x, np.uint8)
                 value = tuple(x.tolist())   # (changed by assigning others)
-            object.__setattr__(self, "pair_axis", pairs)
+            self.pair_axis = pairs
+        elif name == "pair_axis":
+            # what the calls take: the address of this rope's own bytes (asking for it takes a microsecond) and their number
+            object.__setattr__(self, "pair_args", (None, 0) if value is None else (value.ctypes.data, value.size))
         object.__setattr__(self, name, value)
 
-    @property
-    def pair_args(self):
-        """The address of pair_axis' bytes, this rope's own (a copy has others), and their number."""
-        return (None, 0) if self.pair_axis is None else (self.pair_axis.ctypes.data, self.pair_axis.size)
+    # A copy, also in another process, has bytes and an address of its own.
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("pair_axis", "pair_args")}
+
+    def __setstate__(self, state):
+        for k, v in state.items():
+            setattr(self, k, v)
 
     @staticmethod
     def sections(*pairs):
