@@ -49,8 +49,7 @@
 // products drain and returns (its pieces are then undefined, its units still counted).
 //
 // SHARED: the decode of what sequences do not share (block_shared.cu): keys from p.shared[b].x on, and a unit of a sequence
-// that shares is not merged here: its pieces, the first one's place and their number in p.units, are left for the join.  It starts
-// on the SMs that the kernel before it, the shared part's, leaves, without waiting for the others.
+// that shares is not merged here: its pieces, the first one's place and their number in p.units, are left for the join.
 #pragma once
 #include <type_traits>
 
@@ -434,8 +433,9 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     tmem_relinquish();
     tc_fence_before();
   }
-  // SHARED: nothing that the kernel before this one writes is read here, and when it let this one start, the kernels before it were done.
-  if constexpr (!SHARED) griddep_wait();
+  // (SHARED too: the kernel before this one is the shared part's, whose results are not read here, but only behind this wait is what the plan
+  // before it wrote sure to be visible)
+  griddep_wait();
   int N, w0, W;
   Place at = first_tile<TPB, SHARED>(p, k, N, w0, W, k == 0 && warp == 0);
   const int n = at.left;  // tiles of this CTA
@@ -1051,7 +1051,6 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
     }
     __syncthreads();
   }
-  if constexpr (SHARED) griddep_wait();  // (what waits for this kernel waits for the one before it too)
 }
 
 }  // namespace

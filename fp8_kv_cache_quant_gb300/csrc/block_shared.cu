@@ -10,8 +10,7 @@
 //
 // What bounds it.  32 sequences of 16 to 1,024 tokens behind 32,768 shared ones, 32/8 heads of 128: 51 us (271 read one by one), in a
 // chain: plan 3, prefix 26 (14 key tiles a CTA at 1.4 us, the softmax's instructions, as in the prefill), their own tokens 15
-// (its fixed 12 of ramp, last pieces and merge) and join 5.  The four kernels meet in the stream; only the third begins before the
-// second has ended.
+// (its fixed 12 of ramp, last pieces and merge) and join 5.  The four kernels follow one another in the stream.
 #include <atomic>
 
 #include "block_attend.cuh"

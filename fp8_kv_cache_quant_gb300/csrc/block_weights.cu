@@ -542,13 +542,15 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     pend_s[0] = pend_s[5] = 0;
     fence_mbar_init();
   }
-  // The kernel before this one lets it start when itself has waited for what came before: the sequences, the block table and the scales
-  // are there, and only it holds tensor memory, all of which it has.  What it writes is waited for further down.
+  // The kernel before this one lets it start when itself has waited for what came before, so that only it holds tensor memory, all of
+  // which it has.  Everything else is read behind the wait for it, the sequences and the table too, which are older: only what is behind
+  // a kernel's own wait is sure to be visible to it.
   if (warp == C::READERS + 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
     tc_fence_before();
   }
+  griddep_wait();
   __shared__ Division<K, C::KT> division;
   if (warp == 0) {
     Division<K, C::KT> d;
@@ -563,7 +565,6 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
   int u = 0;  // steps so far
   KeyFeed<K, C::KT> feed;
   if (warp == C::READERS && at.n > 0) feed.begin(at, p);
-  griddep_wait();
   griddep_launch_dependents();
 
   if (warp < C::READERS) {

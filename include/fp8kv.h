@@ -39,9 +39,8 @@
  * Launches.  The decode kernels, the rotary and block-scaled cache writes, the block-scaled
  * prefill, the eviction and the attention weights are launched with programmatic stream serialisation:
  * such a kernel may be scheduled while the kernel before it in the stream finishes, and a decode kernel
- * sets up its barriers and tensor memory then, but a call's first kernel reads and writes no global memory
- * until that kernel has completed, and no later call's until all of this call's have, so the stream's
- * ordering is kept.
+ * sets up its barriers and tensor memory then, but no kernel reads or writes global memory
+ * until the one before it in the stream, of this call or another, has completed, so the stream's ordering is kept.
  *
  * Errors.  Argument checks run on the host before anything is enqueued and return
  * FKV_INVALID_ARG or FKV_UNSUPPORTED; a failed launch returns FKV_CUDA_ERROR.  Data
