@@ -1040,6 +1040,16 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
     const int i = threadIdx.x;  // key i (and 128 + i) of a tile
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
     float m[RN], l[RN];
+    // the piece's unit: its first CTA and its pieces, which that CTA writes down
+    auto put_unit = [&]() {
+      int2 unit = make_int2(k, 1);
+      if (!at.whole()) {
+        unit.x = cta_of(at.unit0, division.W, division.N);
+        unit.y = cta_of(at.unit0 + at.count - 1, division.W, division.N) - unit.x + 1;
+      }
+      if (lane == 0 && k == unit.x) p.units[at.b * p.Hkv + at.g] = unit;
+      return unit;
+    };
     bool ok = true;
     while (ok && at.n > 0) {
       // ---- the piece's query: row r scaled to (224, 448], as two terms, 8 threads per row (the products with the
@@ -1153,12 +1163,8 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
       mbar_arrive_warp(r_full);
       if (!wait_warp(r_full, at.piece & 1)) { ok = false; break; }
       if (warp == 0) {
-        int k0 = k, ns = 1;
-        if (!at.whole()) {
-          k0 = cta_of(at.unit0, division.W, division.N);
-          ns = cta_of(at.unit0 + at.count - 1, division.W, division.N) - k0 + 1;
-        }
-        if (lane == 0 && k == k0) p.units[at.b * p.Hkv + at.g] = make_int2(k0, ns);
+        const int2 unit = put_unit();
+        const int k0 = unit.x, ns = unit.y;
         if (lane < RN) {
           float M = -kHuge, L = 0.f;
 #pragma unroll
@@ -1178,6 +1184,9 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
     if (!ok) {
       if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
       *abort_s = 1;
+      // what the gather finds its pieces by is there all the same (what they hold is then anything)
+      if (warp == 0)
+        for (; at.n > 0; at.next(p)) put_unit();
     }
   } else if (warp == 4) {
     // ============================================================ K copies and scales
@@ -1271,10 +1280,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_kernel(const BlockWeigh
   if (s.rows == 0 || static_cast<long long>(blockIdx.x) * kGatherKeys >= s.T) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t unit = static_cast<size_t>(b) * p.Hkv + g;
-  // (a CTA whose wait ran out leaves the workspace's old bytes: the weights then are anything, the reads stay in the pieces)
-  int2 at = p.units[unit];
-  at.x = min(max(at.x, 0), p.slots - 1);
-  at.y = min(max(at.y, 1), p.slots - at.x);
+  const int2 at = p.units[unit];
   constexpr int KEYS = kGatherKeys / kGatherThreads;
   const float4* scores = reinterpret_cast<const float4*>(p.scores + unit * p.max_blocks * 16 * RN);
   float* weights = p.weights + unit * p.weights_len;
