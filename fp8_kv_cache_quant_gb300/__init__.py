@@ -574,7 +574,8 @@ def fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads
 
 
 def attn_weights_workspace(batch, total_q, max_q_len, num_q_heads, cache: BlockCache, max_blocks, stream=None):
-    """A workspace of fp8_block_attn_weights (calls that may overlap on the GPU each need one)."""
+    """A workspace of fp8_block_attn_weights (calls that may overlap on the GPU each need one).  For few queries (at most 16 rows of
+    a KV head and sequence) it grows with the table's width, ``max_blocks``: see include/fp8kv.h."""
     _, h, _, d = cache.k_cache.shape
     with _allocating("fp8_block_attn_weights", cache.k_cache, stream):
         n = fp8_block_attn_weights_workspace_size(batch, total_q, max_q_len, num_q_heads, h, d, max_blocks)

@@ -8,9 +8,9 @@
 //   block_decode_kernel<.., true>  what every sequence has of its own, and sequences that share nothing;
 //   join_kernel    per (sequence, KV head) o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M) over both kinds of pieces.
 //
-// What bounds it.  32 sequences of 16 to 1,024 tokens behind 32,768 shared ones, 32/8 heads of 128: 51 us (271 read one by one), in a
-// chain: plan 3, prefix 26 (14 key tiles a CTA at 1.4 us, the softmax's instructions, as in the prefill), their own tokens 15
-// (its fixed 12 of ramp, last pieces and merge) and join 5.  The four kernels follow one another in the stream.
+// What bounds it.  32 sequences of 16 to 1,024 tokens behind 32,768 shared ones, 32/8 heads of 128: 54 us (271 read one by one), in a
+// chain: plan 3, prefix 26 (14 key tiles a CTA at 1.4 us, the softmax's instructions, as in the prefill), their own tokens 18
+// (its fixed 15 of ramp, last pieces and merge) and join 6.  The four kernels follow one another in the stream.
 #include <atomic>
 
 #include "block_attend.cuh"
@@ -22,9 +22,9 @@ namespace {
 
 // Bytes of keys and values that sharing has to save: it costs more launches, the pieces' way through memory and, per key tile that a
 // CTA takes in turn, 0.8 to 1.5 us, where the decode by itself reads 6 TB/s.  us shared and not, 32/8 heads of 128: 8 sequences behind
-// 8,192 tokens (saved 117 MB, 4 tiles) 25.8 and 28.0, behind 4,096 (59 MB, 2) 23.0 and 20.2; 4 behind 32,768 (201 MB, 14) 33.4 and
-// 42.9, behind 16,384 (101 MB, 7) 27.0 and 26.0; 64/8 heads of 64: 8 behind 16,384 (117 MB, 7) 28.4 and 37.4, 4 (50 MB) 27.6 and
-// 24.8; 16/8 heads of 256: 4 behind 16,384 (201 MB, 7) 36.9 and 46.0, 8,192 (101 MB, 4) 30.8 and 27.6.
+// 8,192 tokens (saved 117 MB, 4 tiles) 26.0 and 27.0, behind 4,096 (59 MB, 2) 23.3 and 18.2; 4 behind 32,768 (201 MB, 14) 37.7 and
+// 42.2, behind 16,384 (101 MB, 7) 29.2 and 25.8; 64/8 heads of 64: 8 behind 16,384 (117 MB, 7) 28.9 and 37.5, 4 (50 MB) 28.7 and
+// 24.8; 16/8 heads of 256: 4 behind 16,384 (201 MB, 7) 41.5 and 46.6, 8,192 (101 MB, 4) 33.5 and 28.7.
 __host__ __device__ constexpr bool sharing_pays(long long tokens, int Hkv, int D, int tiles) {  // (tokens, times heads, may pass 64 bits)
   return static_cast<double>(tokens) * 2 * Hkv * D >= static_cast<double>((48LL + D / 4 << 20) + (static_cast<long long>(D < 128 ? D : 128) << 16) * tiles);
 }

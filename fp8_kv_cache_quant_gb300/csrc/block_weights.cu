@@ -22,8 +22,8 @@
 // What bounds it.  Few rows: K's bytes, and the scores' way through L2: 8 sequences of 16k-24k tokens, 32/8 heads of 128, 44 us (163 MB
 // of K; 34 us score_kernel and 10 gather_kernel one by one, cold).  More rows: a step of pass 0 (128 rows against 128 keys) takes 1,150
 // cycles, its products 540 and its exponentials 512, and a piece's end and beginning in pass 1 as much as its 256 keys; 32 queries of
-// four sequences of 7k-16k, 32/8 heads of 128, 51 us, of which each pass needs 4 to find its work and its first tiles; a whole prompt of
-// 4,001 tokens, 8/1 heads of 256, 91 us, where the products and the copies of the rows' tiles (64 KB each) set the pace.
+// four sequences of 7k-16k, 32/8 heads of 128, 54 us, of which each pass needs 5 to find its work and its first tiles; a whole prompt of
+// 4,001 tokens, 8/1 heads of 256, 95 us, where the products and the copies of the rows' tiles (64 KB each) set the pace.
 // Every wait is bounded in time; a timeout records FKV_FAULT_TIMEOUT, lets the CTA's copies and products drain and returns.
 #include "block_common.cuh"
 #include "prefill_common.cuh"
@@ -457,8 +457,8 @@ __global__ void __launch_bounds__(128) query_kernel(const BlockWeightsParams p) 
 // SM.  Sixteen warps read the scores: in pass 0 a thread one row's for 64 keys, in pass 1 two keys' for 64 rows (whose c and lse it reads
 // from shared memory once for both: one key per thread was bound by that, 2,000 cycles per 256 keys and 128 rows).  Eight of them take
 // every other step, so that a piece's end, a chain of barriers, is passed by eight while the others compute (128 rows a
-// unit, head_dim 128: 53.1 us a call with turns in pass 0 alone, 51.3 with both); in pass 1 at head_dim 256, whose products set the pace and wait for the scores' two buffers,
-// all sixteen take every step, 32 rows a thread (a prompt of 4,001 tokens, 8/1 heads: 91 us against 97).  A wait that need not wait takes 100 to 200 cycles, a step's products 540 (head_dim
+// unit, head_dim 128: 53.1 us a call with turns in pass 0 alone, 51.3 with both, then); in pass 1 at head_dim 256, whose products set the pace and wait for the scores' two buffers,
+// all sixteen take every step, 32 rows a thread (a prompt of 4,001 tokens, 8/1 heads: 91 us against 97 then).  A wait that need not wait takes 100 to 200 cycles, a step's products 540 (head_dim
 // 128), so the readers wait as seldom as they can, and two warps issue the products of the steps in turn.
 template <int D, Kind K>
 struct PassCfg : Shape<D> {

@@ -199,8 +199,8 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_kernel(const RopeC
 
 // The same with positions of several axes.  Thread = one unit of four heads of a kind (query, K, V) of one token, heads a quarter of their
 // number apart, which are turned by the same table entries: a unit with pairs of several axes reads its sixteen one by one, a
-// quarter of the loads of a thread per head.  9,001 tokens of 64/8 heads at head_dim 64, axes in turns, bf16 pool: 33 us, 5.6 TB/s, as
-// with one axis (39 a thread per head; 41 with four CTAs per SM, whose 64 registers spill).
+// quarter of the loads of a thread per head.  9,001 tokens of 64/8 heads at head_dim 64, axes in turns, e4m3 or e5m2 pool: 35 us, 5.1
+// TB/s; bf16 pool: 33 us, 5.6 TB/s, as with one axis (39 a thread per head; 41 with four CTAs per SM, whose 64 registers spill).
 template <int D, int kPool>
 __global__ void __launch_bounds__(kRopeThreads, 3) rope_cache_axes_kernel(const RopeCacheParams p) {
   after_previous();

@@ -591,7 +591,8 @@ size_t fp8_block_shared_decode_attn_workspace_size(int32_t batch, int32_t num_q_
  * result is that of fp8_block_decode_attn for the same arguments (to rounding), but the keys and values of the
  * shared tokens are read, from the blocks that the group's first sequence names, and multiplied once for all
  * members.  With a window they are read from the blocks of the shortest member that has them all, and from where its window
- * begins: what lies before every member's window is not looked at.  What the first sequence's context does not reach is not shared, and a member whose context is shorter than the
+ * begins: what lies before every member's window is not looked at.  (A NaN among the values that the shortest sees makes all
+ * members NaN that are attended with it, also those whose window it has left.)  What the first sequence's context does not reach is not shared, and a member whose context is shorter than the
  * shared part is attended by itself, as are sequences outside every group, groups of one, and every group of a
  * call in which sharing would not pay for itself (few bytes saved): over their own rows of block_table.
  *
@@ -614,7 +615,9 @@ fkv_status fp8_block_shared_decode_attn(const void* q, int32_t batch, int32_t nu
                                         int32_t* fault, fkv_stream_t stream);
 
 /* Workspace bytes fp8_block_attn_weights needs for these sizes (same argument meaning as there); 0 for
- * sizes it does not take. */
+ * sizes it does not take.  With max_q_len (num_q_heads / num_kv_heads) <= 16 rows it holds a score for every row (4, 8 or
+ * 16), KV head and token of the table's width, whatever the contexts are: 256 sequences of 8 KV heads over a table of 131,072 tokens
+ * take 4.3 GB at 4 rows and 17 GB at 16, so a table as wide as the contexts of the call serves best. */
 size_t fp8_block_attn_weights_workspace_size(int32_t batch, int32_t total_q, int32_t max_q_len,
                                              int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                              int32_t max_blocks);
