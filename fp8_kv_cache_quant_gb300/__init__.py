@@ -368,35 +368,44 @@ def fp8_prefill_attn(q, cu_seqlens_q, max_q_len, cache: LayerCache, block_table,
 
 # ------------------------------------------------------------------ rotary cache writes, block-scaled cache
 
+class _PairAxes:
+    """Rope.axes: checked when assigned, and kept as the calls take them besides."""
+
+    def __get__(self, rope, cls=None):
+        return None if rope is None else rope._axes
+
+    def __set__(self, rope, axes):
+        if axes is None:
+            if rope._axes is not None:
+                del rope._axes, rope.pair_axis, rope.pair_args      # (the class has those of no axes)
+            return
+        x, n = np.asarray(axes), rope.cos_sin.shape[1]
+        if x.ndim != 1 or 2 * x.size != n or x.dtype.kind not in "iu" or x.min() < 0 or x.max() > 3:
+            raise ValueError(f"Rope: axes names an axis from 0 to 3 for each of the {n // 2} pairs")
+        rope._axes = tuple(x.tolist())      # (changed by assigning others)
+        rope.pair_axis = np.ascontiguousarray(x, np.uint8)
+        rope.pair_args = (rope.pair_axis.ctypes.data, rope.pair_axis.size)
+
+
 @dataclasses.dataclass
 class Rope:
     """A rotary position embedding: ``cos_sin`` float32 [max_positions][rot_dim], row p holding
     rot_dim / 2 cosines, then rot_dim / 2 sines; ``interleaved`` pairs neighbours (2 i, 2 i + 1)
     instead of the halves (i, i + rot_dim / 2).  ``axes``: for positions of several axes (time, height, width),
-    the axis, 0 to 3, of each of the rot_dim / 2 pairs; positions are then int64 [axes][n]."""
+    the axis, 0 to 3, of each of the rot_dim / 2 pairs; positions are then int64 [axes][n].
+    pair_axis holds them as bytes, pair_args these bytes' address and number."""
 
     cos_sin: torch.Tensor
     interleaved: bool = False
-    axes: Optional[Sequence[int]] = None
+    axes: Optional[Sequence[int]] = _PairAxes()
 
-    def __setattr__(self, name, value):
-        if name == "axes":
-            pairs = None
-            if value is not None:
-                x = np.asarray(value)
-                if x.ndim != 1 or 2 * x.size != self.cos_sin.shape[1] or x.dtype.kind not in "iu" or x.min() < 0 or x.max() > 3:
-                    raise ValueError(f"Rope: axes names an axis from 0 to 3 for each of the {self.cos_sin.shape[1] // 2} pairs")
-                pairs = np.ascontiguousarray(x, np.uint8)
-                value = tuple(x.tolist())   # (changed by assigning others)
-            self.pair_axis = pairs
-        elif name == "pair_axis":
-            # what the calls take: the address of this rope's own bytes (asking for it takes a microsecond) and their number
-            object.__setattr__(self, "pair_args", (None, 0) if value is None else (value.ctypes.data, value.size))
-        object.__setattr__(self, name, value)
+    _axes = pair_axis = None
+    pair_args = (None, 0)
 
     # A copy, also in another process, has bytes and an address of its own.
     def __getstate__(self):
-        return {k: v for k, v in self.__dict__.items() if k not in ("pair_axis", "pair_args")}
+        own = ("_axes", "pair_axis", "pair_args")
+        return {**{k: v for k, v in self.__dict__.items() if k not in own}, "axes": self.axes}
 
     def __setstate__(self, state):
         for k, v in state.items():
