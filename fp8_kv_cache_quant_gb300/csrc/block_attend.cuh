@@ -587,7 +587,7 @@ FKV_DEV void attend_tile(const BlockPrefillParams& p, const CUtensorMap& tmk, co
         id_next = block_id(t + 2);
         const int st = t % C::NS, use = t / C::NS;
         bool ok = true;
-        if (lane == 0 && use > 0) ok = wait_stage<true>(&empty[st], (use - 1) & 1, p.stage_wait_ns, hurried(p.stage_wait_ns));
+        if (lane == 0 && use > 0) ok = pf_wait(&empty[st], (use - 1) & 1, p.stage_wait_ns);
         if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
           if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
           *abort_s = 1;

@@ -898,7 +898,7 @@ __global__ void __launch_bounds__(kThreads, (BlockDecodeCfg<D, G>::CTAS))
       id_next = block_id(nx);
       const int st = u % C::NS, use = u / C::NS;
       if (u >= n0) {
-        if (!wait_stage_warp(&k_empty[st], (use - 1) & 1, p.stage_wait_ns, hurried(p.stage_wait_ns))) {
+        if (!wait_stage_warp(&k_empty[st], (use - 1) & 1, p.stage_wait_ns)) {
           if (lane == 0) raise_fault(p.fault, FKV_FAULT_TIMEOUT);
           *abort_s = 1;
           break;

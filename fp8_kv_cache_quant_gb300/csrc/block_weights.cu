@@ -766,7 +766,6 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     // ============================================================ copies
     using Feed = KeyFeed<K, C::KT>;
     int stay_pieces = 0;            // pieces whose tile was requested
-    const bool in_a_hurry = hurried(p.stage_wait_ns);
     size_t held[C::NS];             // pass 1: the row tile that a stage holds
 #pragma unroll
     for (int s = 0; s < C::NS; ++s) held[s] = ~static_cast<size_t>(0);
@@ -794,7 +793,7 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
     bool ok = true;
     while (ok && at.n > 0) {
       const int yb = at.piece % C::NY;
-      if (at.piece >= C::NY && !wait_stage_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1, p.stage_wait_ns, in_a_hurry)) { ok = false; break; }
+      if (at.piece >= C::NY && !wait_warp(&y_empty[yb], (at.piece / C::NY - 1) & 1, p.stage_wait_ns)) { ok = false; break; }
       size_t tile = tile_index(p, at.r0, at.b, at.g, K == kRows ? at.t : at.first() + at.s);
       if constexpr (K == kRows) {
         if (lane == 0) {
@@ -810,7 +809,7 @@ __global__ void __launch_bounds__((PassCfg<D, K>::THREADS), 1)
       for (int x = 0; u < end; ++u, ++x, tile += p.Hkv) {
         if (abort_warp(abort_s)) { ok = false; break; }
         const int st = u % C::NS;
-        if (u >= C::NS && !wait_stage_warp(&x_empty[st], (u / C::NS - 1) & 1, p.stage_wait_ns, in_a_hurry)) { ok = false; break; }
+        if (u >= C::NS && !wait_warp(&x_empty[st], (u / C::NS - 1) & 1, p.stage_wait_ns)) { ok = false; break; }
         uint8_t* dst = sStream + st * C::STREAM;
         if constexpr (K == kRows) {
           copy_keys(dst, &x_full[st], at.s + x, u);
@@ -1194,13 +1193,12 @@ __global__ void __launch_bounds__(kScoreThreads, (ScoreCfg<D, RN>::CTAS))
     using Feed = KeyFeed<kScores, C::BN>;
     Feed feed;
     if (at.n > 0) feed.begin(at, p);
-    const bool in_a_hurry = hurried(p.stage_wait_ns);
     bool ok = true;
     for (; ok && at.n > 0; at.next(p)) {
       const int end = u + at.n;
       for (int x = 0; u < end; ++u, ++x) {
         const int st = u % C::NS;
-        if (abort_warp(abort_s) || (u >= C::NS && !wait_stage_warp(&k_empty[st], (u / C::NS - 1) & 1, p.stage_wait_ns, in_a_hurry))) { ok = false; break; }
+        if (abort_warp(abort_s) || (u >= C::NS && !wait_warp(&k_empty[st], (u / C::NS - 1) & 1, p.stage_wait_ns))) { ok = false; break; }
         int id;
         float ks;
         feed.take(p, id, ks);

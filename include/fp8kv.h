@@ -169,7 +169,7 @@ int32_t fkv_version(void);
  * its tensor memory and returns; the output of such a launch is undefined (the split
  * merge reads whatever the workspace held).  For the launches of fp8_block_decode_attn,
  * fp8_block_prefill_attn, fp8_block_shared_decode_attn and fp8_block_attn_weights it bounds the wait of
- * the copies for a stage that the products have read (1 ns: no such wait is satisfied): they stop there,
+ * the copies for a stage that the products have read (fp8_block_decode_attn, 1 ns: none is satisfied): they stop there,
  * and the rest of such a CTA (one with more tiles than stages) runs into its own bounds of 200 ms.  Not for production use.
  */
 void fkv_set_decode_wait_limit_ns(unsigned long long ns);
